@@ -482,6 +482,155 @@ tpgemm_status tpgemm_vcopy_roundtrip(void* dst, const void* src, size_t buffer_b
                                      const tpgemm_vcopy_desc* d, int ctas, int64_t cta_stride,
                                      void* smem_out, void* stream);
 
+/*
+ * ------------------------------------------------------------------------
+ * The operators around the multiply: the linear layer with its epilogue, its
+ * gradients, the root-mean-square norm and its gradients. (Not on the pages:
+ * what a network computes right before and right after the multiply.)
+ *
+ * Matrices here are row-major with unit column stride and a row stride in
+ * elements (0 = dense, else at least the columns), so slices of wider buffers
+ * can be given. Pointers are aligned to their element; rows that start on
+ * 16-byte boundaries run fastest. Sizes may be any, zero included. All calls are asynchronous on
+ * `stream`, allocate nothing, keep no pointer, and may be captured into a
+ * CUDA graph. An output may not share bytes with an input or another output,
+ * except where in-place use is named below. Inputs' infinities and NaN
+ * propagate as in the formulas.
+ */
+typedef enum {
+    TPGEMM_ELEM_F16 = 0,  /* the first four codes are tpgemm_dtype's */
+    TPGEMM_ELEM_BF16 = 1,
+    TPGEMM_ELEM_E4M3 = 2,
+    TPGEMM_ELEM_E5M2 = 3,
+    TPGEMM_ELEM_F32 = 8   /* IEEE binary32 */
+} tpgemm_elem;
+
+typedef enum {
+    TPGEMM_ACT_NONE = 0,
+    TPGEMM_ACT_RELU = 1,
+    TPGEMM_ACT_SILU = 2,     /* z / (1 + exp(-z)) */
+    TPGEMM_ACT_GELU = 3,     /* z (1 + erf(z / sqrt 2)) / 2 */
+    TPGEMM_ACT_GELU_TANH = 4 /* z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2 */
+} tpgemm_act;
+
+/*
+ * The linear layer:
+ *   Z[m, n] = scale_a[m] scale_w[n] sum_k A[m, k] W[n, k] + bias[n]
+ *   Y[m, n] = act(Z[m, n]) + R[m, n].
+ * A is [M, K] and W [N, K], both of `dtype` (f16, bf16, e4m3 or e5m2). Y, Z, R
+ * and bias are of `out` (f16, bf16 or f32). Sums are 32-bit and each output is
+ * rounded once; Y is computed from the unrounded Z.
+ */
+typedef struct {
+    int64_t M, N, K;                 /* each below 2^30 */
+    int64_t lda, ldw, ldr, ldy, ldz; /* row strides of A, W, R, Y, Z */
+    tpgemm_elem dtype, out;
+    tpgemm_act act;
+} tpgemm_linear_desc;
+
+/* Z, R and bias may be NULL (not stored; zero). scale_a [M] and scale_w [N]
+ * (float32) may each be NULL (one) and need 8-bit operands. Y may be R itself (same
+ * address and row stride). workspace: device memory of at least
+ * tpgemm_linear_workspace_bytes bytes, 256-byte aligned (NULL when that is 0),
+ * not shared with an operand, untouched until the work has run. */
+tpgemm_status tpgemm_linear(void* Y, void* Z, const void* A, const void* W, const float* scale_a,
+                            const float* scale_w, const void* bias, const void* R,
+                            const tpgemm_linear_desc* d, void* workspace, size_t workspace_bytes,
+                            void* stream);
+
+/* Bytes of workspace tpgemm_linear needs: 0 unless more than 16 rows of A are
+ * multiplied and A's or W's rows do not start on 16-byte boundaries; those
+ * operands are then copied to rows that do. The addresses matter by their
+ * alignment only. 0 for a description that tpgemm_linear rejects. */
+size_t tpgemm_linear_workspace_bytes(const void* A, const void* W, const tpgemm_linear_desc* d);
+
+/*
+ * Gradients of the linear layer without scales:
+ *   dZ = dY act'(Z),  dA = dZ W,  dW = dZ^T A,  dbias[n] = sum_m dZ[m, n]
+ * (the gradient of R is dY). dY and Z are [M, N], A [M, K], W [N, K] and dA
+ * [M, K], all of `dtype` (f16 or bf16); dW [N, K] and dbias [N] of `grad` (f16,
+ * bf16 or f32). Z is not read for TPGEMM_ACT_NONE (it may be NULL). dA, dW and
+ * dbias may each be NULL when not wanted. The products read dZ rounded to
+ * `dtype`; dbias sums it unrounded.
+ */
+typedef struct {
+    int64_t M, N, K;
+    int64_t lddy, ldz, lda, ldw, ldda, lddw; /* row strides */
+    tpgemm_elem dtype, grad;
+    tpgemm_act act;
+} tpgemm_linear_grad_desc;
+
+tpgemm_status tpgemm_linear_backward(void* dA, void* dW, void* dbias, const void* dY,
+                                     const void* A, const void* W, const void* Z,
+                                     const tpgemm_linear_grad_desc* d, void* workspace,
+                                     size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace tpgemm_linear_backward needs (dZ, the bias gradient's
+ * partial sums, copies of operands whose rows do not start on 16-byte
+ * boundaries). 0 for a description that it rejects. */
+size_t tpgemm_linear_backward_workspace_bytes(const void* dY, const void* A, const void* W,
+                                              const tpgemm_linear_grad_desc* d);
+
+/*
+ * Root-mean-square norm of each row, after the residual's addition:
+ *   H = X + R,  rstd[i] = 1 / sqrt(mean_j H[i, j]^2 + eps),
+ *   Y[i, j] = H[i, j] rstd[i] gamma[j].
+ * X, R and H are of `x` (f16, bf16 or f32), gamma [cols] of `gamma` (`x` or
+ * f32). Y is of `y`: f16, bf16 or f32 with TPGEMM_SCALE_NONE, or e4m3 / e5m2 as
+ * Y / scale with
+ *   TPGEMM_SCALE_ROW: scale float32 [rows], max(max_j |Y| / t, 2^-126), t the
+ *     type's largest value (448 / 57344): the scale_a of tpgemm_linear;
+ *   TPGEMM_SCALE_MX: scale E8M0 bytes [rows][ceil(cols / 32)], 2^(e - 127) with
+ *     e - 127 = floor(log2 max |Y|) - (8 / 15) over each 32 columns, at least
+ *     -127: the SFA of tpgemm_gemm_mx (dense Y). Larger values saturate.
+ * A row (block) with an infinity or a NaN gets a NaN scale. Sums, H before its
+ * rounding, and Y before its rounding are 32-bit.
+ */
+typedef enum {
+    TPGEMM_SCALE_NONE = 0,
+    TPGEMM_SCALE_ROW = 1,
+    TPGEMM_SCALE_MX = 2
+} tpgemm_scale_mode;
+
+typedef struct {
+    int64_t rows, cols;          /* rows >= 0, cols >= 1, each below 2^30 */
+    int64_t ldx, ldr, ldh, ldy;  /* row strides */
+    tpgemm_elem x, gamma, y;
+    tpgemm_scale_mode scale;
+    float eps;
+} tpgemm_rmsnorm_desc;
+
+/* R may be NULL (zero); H and rstd [rows] may be NULL (not stored). H may be X
+ * or R itself (same address and row stride), and Y may be X or R itself when
+ * they have one type and H is NULL. */
+tpgemm_status tpgemm_rmsnorm(void* Y, void* H, void* scale, float* rstd, const void* X,
+                             const void* R, const void* gamma, const tpgemm_rmsnorm_desc* d,
+                             void* stream);
+
+/*
+ * Gradients of the norm, n = H rstd, w = dY gamma:
+ *   dX[i, j] = rstd[i] (w[i, j] - n[i, j] mean_j(w n)) + dH[i, j]
+ *   dgamma[j] = sum_i dY[i, j] n[i, j].
+ * dX is the gradient of X and of R. dY, H, dH and dX are of `x`; dgamma [cols]
+ * of `grad` (f16, bf16 or f32). dH (the gradient that reaches H past the norm)
+ * may be NULL; dX and dgamma may each be NULL when not wanted. dX may be dY, H
+ * or dH itself (same address and row stride).
+ */
+typedef struct {
+    int64_t rows, cols;
+    int64_t lddy, ldh, lddh, lddx; /* row strides */
+    tpgemm_elem x, gamma, grad;
+} tpgemm_rmsnorm_grad_desc;
+
+tpgemm_status tpgemm_rmsnorm_backward(void* dX, void* dgamma, const void* dY, const void* H,
+                                      const float* rstd, const void* gamma, const void* dH,
+                                      const tpgemm_rmsnorm_grad_desc* d, void* workspace,
+                                      size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace tpgemm_rmsnorm_backward needs for dgamma's partial sums
+ * (0 when dgamma is not wanted), 256-byte aligned. */
+size_t tpgemm_rmsnorm_backward_workspace_bytes(int64_t rows, int64_t cols);
+
 /* Static English name of a status. Never NULL. */
 const char* tpgemm_status_string(tpgemm_status s);
 

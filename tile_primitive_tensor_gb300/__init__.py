@@ -15,6 +15,7 @@ import ctypes
 import os
 import re
 import threading
+import typing
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_lib", "libtpgemm.so")
@@ -69,6 +70,49 @@ TPGEMM_CP_LANES_QUADRANTS = 1
 TPGEMM_CP_LANES_PAIRS_02_13 = 2
 TPGEMM_CP_LANES_PAIRS_01_23 = 3
 TPGEMM_CP_LANES_ALL_QUADS = 4
+
+
+# tpgemm_elem (the first four codes are tpgemm_dtype's)
+TPGEMM_ELEM_F16 = 0
+TPGEMM_ELEM_BF16 = 1
+TPGEMM_ELEM_E4M3 = 2
+TPGEMM_ELEM_E5M2 = 3
+TPGEMM_ELEM_F32 = 8
+# tpgemm_act
+TPGEMM_ACT_NONE = 0
+TPGEMM_ACT_RELU = 1
+TPGEMM_ACT_SILU = 2
+TPGEMM_ACT_GELU = 3
+TPGEMM_ACT_GELU_TANH = 4
+# tpgemm_scale_mode
+TPGEMM_SCALE_NONE = 0
+TPGEMM_SCALE_ROW = 1
+TPGEMM_SCALE_MX = 2
+
+
+class LinearDesc(ctypes.Structure):
+    """tpgemm_linear_desc: sizes, row strides, types and activation of a linear layer."""
+    _fields_ = [(n, ctypes.c_int64) for n in ("M", "N", "K", "lda", "ldw", "ldr", "ldy", "ldz")] + \
+        [(n, ctypes.c_int) for n in ("dtype", "out", "act")]
+
+
+class LinearGradDesc(ctypes.Structure):
+    """tpgemm_linear_grad_desc: as LinearDesc, for the gradients."""
+    _fields_ = [(n, ctypes.c_int64)
+                for n in ("M", "N", "K", "lddy", "ldz", "lda", "ldw", "ldda", "lddw")] + \
+        [(n, ctypes.c_int) for n in ("dtype", "grad", "act")]
+
+
+class RmsNormDesc(ctypes.Structure):
+    """tpgemm_rmsnorm_desc: sizes, row strides, types, scale mode and eps of a norm."""
+    _fields_ = [(n, ctypes.c_int64) for n in ("rows", "cols", "ldx", "ldr", "ldh", "ldy")] + \
+        [(n, ctypes.c_int) for n in ("x", "gamma", "y", "scale")] + [("eps", ctypes.c_float)]
+
+
+class RmsNormGradDesc(ctypes.Structure):
+    """tpgemm_rmsnorm_grad_desc: as RmsNormDesc, for the gradients."""
+    _fields_ = [(n, ctypes.c_int64) for n in ("rows", "cols", "lddy", "ldh", "lddh", "lddx")] + \
+        [(n, ctypes.c_int) for n in ("x", "gamma", "grad")]
 
 
 class CpDesc(ctypes.Structure):
@@ -137,6 +181,21 @@ def _open(path):
     lib.tpgemm_gemm_mx.restype = ci
     lib.tpgemm_gemm_mx_workspace_bytes.argtypes = [i64, i64, i64]
     lib.tpgemm_gemm_mx_workspace_bytes.restype = sz
+    lib.tpgemm_linear.argtypes = [vp] * 8 + [ctypes.POINTER(LinearDesc), vp, sz, vp]
+    lib.tpgemm_linear.restype = ci
+    lib.tpgemm_linear_workspace_bytes.argtypes = [vp, vp, ctypes.POINTER(LinearDesc)]
+    lib.tpgemm_linear_workspace_bytes.restype = sz
+    lib.tpgemm_linear_backward.argtypes = [vp] * 7 + [ctypes.POINTER(LinearGradDesc), vp, sz, vp]
+    lib.tpgemm_linear_backward.restype = ci
+    lib.tpgemm_linear_backward_workspace_bytes.argtypes = [vp, vp, vp,
+                                                           ctypes.POINTER(LinearGradDesc)]
+    lib.tpgemm_linear_backward_workspace_bytes.restype = sz
+    lib.tpgemm_rmsnorm.argtypes = [vp] * 7 + [ctypes.POINTER(RmsNormDesc), vp]
+    lib.tpgemm_rmsnorm.restype = ci
+    lib.tpgemm_rmsnorm_backward.argtypes = [vp] * 7 + [ctypes.POINTER(RmsNormGradDesc), vp, sz, vp]
+    lib.tpgemm_rmsnorm_backward.restype = ci
+    lib.tpgemm_rmsnorm_backward_workspace_bytes.argtypes = [i64, i64]
+    lib.tpgemm_rmsnorm_backward_workspace_bytes.restype = sz
     lib.tpgemm_version.argtypes = []
     lib.tpgemm_version.restype = ctypes.c_char_p
     lib.tpgemm_cp_parse_shape.argtypes = [ctypes.c_char_p, ctypes.POINTER(ci)]
@@ -472,3 +531,285 @@ def gemm(A, B, C=None, *, beta=None, transA=False, transB=False, out=None, strea
     check(tpgemm_gemm_path(out, A, B, C if beta else C, M, N, K, transA, transB,
                            dtype_code(A.dtype), beta, stream, path))
     return out
+
+
+# ------------------------------------------------ the operators around the multiply
+def tpgemm_linear(Y, Z, A, W, scale_a, scale_w, bias, R, desc: LinearDesc, workspace=None,
+                  workspace_bytes=0, stream=None) -> int:
+    """Enqueue Y = act(scale_a scale_w A.W^T + bias) + R; returns the tpgemm_status code."""
+    return int(_load().tpgemm_linear(_ptr(Y), _ptr(Z), _ptr(A), _ptr(W), _ptr(scale_a),
+                                     _ptr(scale_w), _ptr(bias), _ptr(R), ctypes.byref(desc),
+                                     _ptr(workspace), int(workspace_bytes), _stream(stream)))
+
+
+def tpgemm_linear_workspace_bytes(A, W, desc: LinearDesc) -> int:
+    return int(_load().tpgemm_linear_workspace_bytes(_ptr(A), _ptr(W), ctypes.byref(desc)))
+
+
+def tpgemm_linear_backward(dA, dW, dbias, dY, A, W, Z, desc: LinearGradDesc, workspace=None,
+                           workspace_bytes=0, stream=None) -> int:
+    """Enqueue the gradients of a linear layer; returns the tpgemm_status code."""
+    return int(_load().tpgemm_linear_backward(_ptr(dA), _ptr(dW), _ptr(dbias), _ptr(dY), _ptr(A),
+                                              _ptr(W), _ptr(Z), ctypes.byref(desc),
+                                              _ptr(workspace), int(workspace_bytes),
+                                              _stream(stream)))
+
+
+def tpgemm_linear_backward_workspace_bytes(dY, A, W, desc: LinearGradDesc) -> int:
+    return int(_load().tpgemm_linear_backward_workspace_bytes(_ptr(dY), _ptr(A), _ptr(W),
+                                                              ctypes.byref(desc)))
+
+
+def tpgemm_rmsnorm(Y, H, scale, rstd, X, R, gamma, desc: RmsNormDesc, stream=None) -> int:
+    """Enqueue a root-mean-square norm; returns the tpgemm_status code."""
+    return int(_load().tpgemm_rmsnorm(_ptr(Y), _ptr(H), _ptr(scale), _ptr(rstd), _ptr(X), _ptr(R),
+                                      _ptr(gamma), ctypes.byref(desc), _stream(stream)))
+
+
+def tpgemm_rmsnorm_backward(dX, dgamma, dY, H, rstd, gamma, dH, desc: RmsNormGradDesc,
+                            workspace=None, workspace_bytes=0, stream=None) -> int:
+    """Enqueue the gradients of a root-mean-square norm; returns the tpgemm_status code."""
+    return int(_load().tpgemm_rmsnorm_backward(_ptr(dX), _ptr(dgamma), _ptr(dY), _ptr(H),
+                                               _ptr(rstd), _ptr(gamma), _ptr(dH),
+                                               ctypes.byref(desc), _ptr(workspace),
+                                               int(workspace_bytes), _stream(stream)))
+
+
+def tpgemm_rmsnorm_backward_workspace_bytes(rows, cols) -> int:
+    return int(_load().tpgemm_rmsnorm_backward_workspace_bytes(int(rows), int(cols)))
+
+
+_ACTS = {"none": TPGEMM_ACT_NONE, "relu": TPGEMM_ACT_RELU, "silu": TPGEMM_ACT_SILU,
+         "gelu": TPGEMM_ACT_GELU, "gelu_tanh": TPGEMM_ACT_GELU_TANH}
+_SCALES = {None: TPGEMM_SCALE_NONE, "row": TPGEMM_SCALE_ROW, "mx": TPGEMM_SCALE_MX}
+_ELEMS = {}
+
+
+def elem_code(torch_dtype) -> int:
+    """The tpgemm_elem code of a torch dtype."""
+    if not _ELEMS:
+        import torch
+        _ELEMS.update({torch.float16: TPGEMM_ELEM_F16, torch.bfloat16: TPGEMM_ELEM_BF16,
+                       torch.float8_e4m3fn: TPGEMM_ELEM_E4M3, torch.float8_e5m2: TPGEMM_ELEM_E5M2,
+                       torch.float32: TPGEMM_ELEM_F32})
+    code = _ELEMS.get(torch_dtype)
+    if code is None:
+        raise TypeError(f"unsupported element type {torch_dtype}")
+    return code
+
+
+def _act_code(act) -> int:
+    if act in _ACTS:
+        return _ACTS[act]
+    raise ValueError(f"act must be one of {', '.join(_ACTS)}, got {act!r}")
+
+
+def _matrix(name, t, rows, cols, dtype, device) -> int:
+    """Checks a [rows, cols] argument of unit column stride; returns its row stride."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not {device}")
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+        raise ValueError(f"{name} must be [{rows}, {cols}], got {list(t.shape)}")
+    s0, s1 = t.stride()
+    if cols > 1 and s1 != 1:
+        raise ValueError(f"{name} must have unit column stride, got {s1}")
+    if rows <= 1 or cols == 0:
+        return cols
+    if s0 < cols:
+        raise ValueError(f"{name}: row stride {s0} is less than its {cols} columns")
+    return s0
+
+
+def _vector(name, t, n, dtype, device) -> None:
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not {device}")
+    if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be a dense vector of {n}")
+
+
+def _scratch(torch, workspace, need, device):
+    """(workspace, its bytes): the caller's, or one from torch (None when none is needed)."""
+    if workspace is None:
+        if need == 0:
+            return None, 0
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    elif workspace.device != device:
+        raise ValueError(f"workspace is on {workspace.device}, not {device}")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def _cuda(name, t):
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.device
+
+
+def linear(A, W, bias=None, residual=None, *, act="none", scale_a=None, scale_w=None,
+           out_dtype=None, out=None, pre=None, workspace=None, stream=None):
+    """Y = act(scale_a[m] scale_w[n] A.W^T + bias) + residual on CUDA tensors; returns Y.
+
+    A [M, K] and W [N, K] are both float16, bfloat16, float8_e4m3fn or float8_e5m2; Y, bias [N],
+    residual [M, N] and ``pre`` [M, N] (given to receive the value before the activation) are of
+    out_dtype (float16, bfloat16 or float32; by default A's 16-bit type, or bfloat16). The float32
+    scales, per row of A and of W, are for the 8-bit types. act: none, relu, silu, gelu or
+    gelu_tanh. Matrices may be row-strided; ``out`` may be the residual itself. The workspace, if
+    one is needed (tpgemm_linear_workspace_bytes), is allocated here with torch unless given."""
+    import torch
+    dev = _cuda("A", A)
+    M, K = A.shape
+    N = W.shape[0]
+    dt = A.dtype
+    desc = LinearDesc(M, N, K, _matrix("A", A, M, K, dt, dev), _matrix("W", W, N, K, dt, dev))
+    if out is not None:
+        out_dtype = out.dtype if out_dtype is None else out_dtype
+    elif out_dtype is None:
+        out_dtype = dt if dt.itemsize == 2 else torch.bfloat16
+    if out is None:
+        out = torch.empty((M, N), dtype=out_dtype, device=dev)
+    desc.ldy = _matrix("out", out, M, N, out_dtype, dev)
+    desc.dtype = elem_code(dt)
+    desc.out = elem_code(out_dtype)
+    desc.act = _act_code(act)
+    if residual is not None:
+        desc.ldr = _matrix("residual", residual, M, N, out_dtype, dev)
+    if pre is not None:
+        desc.ldz = _matrix("pre", pre, M, N, out_dtype, dev)
+    if bias is not None:
+        _vector("bias", bias, N, out_dtype, dev)
+    if scale_a is not None:
+        _vector("scale_a", scale_a, M, torch.float32, dev)
+    if scale_w is not None:
+        _vector("scale_w", scale_w, N, torch.float32, dev)
+    need = tpgemm_linear_workspace_bytes(A, W, desc) if workspace is None else 0
+    workspace, size = _scratch(torch, workspace, need, dev)
+    with torch.cuda.device(dev):
+        check(tpgemm_linear(out, pre, A, W, scale_a, scale_w, bias, residual, desc, workspace,
+                            size, stream))
+    return out
+
+
+def linear_backward(dY, A, W, pre=None, *, act="none", grad_dtype=None, need=(True, True, True),
+                    workspace=None, stream=None):
+    """(dA, dW, dbias) of Y = act(A.W^T + bias) + residual, given dY [M, N] (the residual's own
+    gradient) and ``pre``, the value before the activation (not needed for act="none").
+
+    dY, A, W, pre and dA are all float16 or all bfloat16; dW and dbias are of grad_dtype (float32,
+    float16 or bfloat16; by default A's type). ``need`` says which of the three are wanted; the
+    others are None."""
+    import torch
+    dev = _cuda("A", A)
+    M, K = A.shape
+    N = W.shape[0]
+    dt = A.dtype
+    grad_dtype = dt if grad_dtype is None else grad_dtype
+    code = _act_code(act)
+    desc = LinearGradDesc(M, N, K, _matrix("dY", dY, M, N, dt, dev), 0,
+                          _matrix("A", A, M, K, dt, dev), _matrix("W", W, N, K, dt, dev), K, K,
+                          elem_code(dt), elem_code(grad_dtype), code)
+    if code != TPGEMM_ACT_NONE:
+        if pre is None:
+            raise ValueError(f"act={act!r} needs pre, the value before the activation")
+        desc.ldz = _matrix("pre", pre, M, N, dt, dev)
+    else:
+        pre = None
+    dA = torch.empty((M, K), dtype=dt, device=dev) if need[0] else None
+    dW = torch.empty((N, K), dtype=grad_dtype, device=dev) if need[1] else None
+    dbias = torch.empty(N, dtype=grad_dtype, device=dev) if need[2] else None
+    size = tpgemm_linear_backward_workspace_bytes(dY, A, W, desc) if workspace is None else 0
+    workspace, size = _scratch(torch, workspace, size, dev)
+    with torch.cuda.device(dev):
+        check(tpgemm_linear_backward(dA, dW, dbias, dY, A, W, pre, desc, workspace, size, stream))
+    return dA, dW, dbias
+
+
+class RmsNorm(typing.NamedTuple):
+    """What rmsnorm returns; what was not asked for is None."""
+    y: object
+    h: object      # x + residual
+    scale: object  # float32 [rows] ("row") or uint8 [rows, ceil(cols / 32)] E8M0 ("mx")
+    rstd: object   # float32 [rows]
+
+
+def rmsnorm(x, weight, residual=None, *, eps=1e-6, quant=None, out_dtype=None, need_rstd=False,
+            out=None, out_h=None, stream=None):
+    """Root-mean-square norm of the rows of h = x + residual: y = h / sqrt(mean(h^2) + eps) weight.
+
+    x, residual and h [rows, cols] are float16, bfloat16 or float32; weight [cols] is of x's type
+    or float32. y is of out_dtype: a float type (by default x's), or with quant="row" (one float32
+    scale per row, linear's scale_a) or quant="mx" (one E8M0 scale per 32 columns, gemm_mx's SFA)
+    float8_e4m3fn (the default) or float8_e5m2, holding y / scale. h is returned with a residual
+    only; it may be written in place (out_h = x or residual)."""
+    import torch
+    dev = _cuda("x", x)
+    rows, cols = x.shape
+    dt = x.dtype
+    if quant not in _SCALES:
+        raise ValueError(f"quant must be None, 'row' or 'mx', got {quant!r}")
+    if out_dtype is None:
+        out_dtype = out.dtype if out is not None else (dt if quant is None else torch.float8_e4m3fn)
+    if weight.dtype is not dt and weight.dtype is not torch.float32:
+        raise TypeError(f"weight must be {dt} or float32, got {weight.dtype}")
+    _vector("weight", weight, cols, weight.dtype, dev)
+    if out is None:
+        out = torch.empty((rows, cols), dtype=out_dtype, device=dev)
+    desc = RmsNormDesc(rows, cols, _matrix("x", x, rows, cols, dt, dev), 0, 0,
+                       _matrix("out", out, rows, cols, out_dtype, dev), elem_code(dt),
+                       elem_code(weight.dtype), elem_code(out_dtype), _SCALES[quant], eps)
+    h = scale = rstd = None
+    if residual is not None:
+        desc.ldr = _matrix("residual", residual, rows, cols, dt, dev)
+        h = torch.empty((rows, cols), dtype=dt, device=dev) if out_h is None else out_h
+        desc.ldh = _matrix("out_h", h, rows, cols, dt, dev)
+    elif out_h is not None:
+        raise ValueError("out_h needs a residual (h is x without one)")
+    if quant == "row":
+        scale = torch.empty(rows, dtype=torch.float32, device=dev)
+    elif quant == "mx":
+        scale = torch.empty((rows, (cols + 31) // 32), dtype=torch.uint8, device=dev)
+    if need_rstd:
+        rstd = torch.empty(rows, dtype=torch.float32, device=dev)
+    with torch.cuda.device(dev):
+        check(tpgemm_rmsnorm(out, h, scale, rstd, x, residual, weight, desc, stream))
+    return RmsNorm(out, h, scale, rstd)
+
+
+def rmsnorm_backward(dy, h, rstd, weight, dh=None, *, grad_dtype=None, need=(True, True), out=None,
+                     workspace=None, stream=None):
+    """(dx, dweight) of a root-mean-square norm, given dy, the normalised rows' h and rstd, and the
+    gradient dh that reaches h past the norm (or None). dx is the gradient of x and of residual.
+
+    dy, h, dh and dx [rows, cols] are of one type (float16, bfloat16 or float32), dweight of
+    grad_dtype (by default weight's). ``need`` says which are wanted; ``out`` may be dy, h or dh."""
+    import torch
+    dev = _cuda("dy", dy)
+    rows, cols = dy.shape
+    dt = dy.dtype
+    grad_dtype = weight.dtype if grad_dtype is None else grad_dtype
+    if weight.dtype is not dt and weight.dtype is not torch.float32:
+        raise TypeError(f"weight must be {dt} or float32, got {weight.dtype}")
+    _vector("weight", weight, cols, weight.dtype, dev)
+    _vector("rstd", rstd, rows, torch.float32, dev)
+    desc = RmsNormGradDesc(rows, cols, _matrix("dy", dy, rows, cols, dt, dev),
+                           _matrix("h", h, rows, cols, dt, dev), 0, 0, elem_code(dt),
+                           elem_code(weight.dtype), elem_code(grad_dtype))
+    if dh is not None:
+        desc.lddh = _matrix("dh", dh, rows, cols, dt, dev)
+    dx = dweight = None
+    if need[0]:
+        dx = torch.empty((rows, cols), dtype=dt, device=dev) if out is None else out
+        desc.lddx = _matrix("out", dx, rows, cols, dt, dev)
+    size = 0
+    if need[1]:
+        dweight = torch.empty(cols, dtype=grad_dtype, device=dev)
+        size = tpgemm_rmsnorm_backward_workspace_bytes(rows, cols) if workspace is None else 0
+    workspace, size = _scratch(torch, workspace, size, dev)
+    with torch.cuda.device(dev):
+        check(tpgemm_rmsnorm_backward(dx, dweight, dy, h, rstd, weight, dh, desc, workspace, size,
+                                      stream))
+    return dx, dweight

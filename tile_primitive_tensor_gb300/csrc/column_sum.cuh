@@ -1,0 +1,44 @@
+// out[n] = sum over strips s of partial[s][n], in the strips' order, rounded once.
+#pragma once
+
+#include "elem.cuh"
+
+namespace tpg {
+namespace {
+
+template <typename O>
+__global__ void __launch_bounds__(256) column_sum_kernel(const float* partial, int strips,
+                                                         int64_t cols, O* out) {
+    __shared__ float s[8][33];
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int64_t n = int64_t(blockIdx.x) * 32 + lane;
+    float v = 0.f;
+    if (n < cols)
+        for (int i = w; i < strips; i += 8) v += partial[int64_t(i) * cols + n];
+    s[w][lane] = v;
+    __syncthreads();
+    if (w == 0 && n < cols) {
+        float t = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) t += s[i][lane];
+        out[n] = from_f32<O>(t);
+    }
+}
+
+inline cudaError_t launch_column_sum(const float* partial, int strips, int64_t cols, void* out,
+                                     int elem, cudaStream_t stream) {
+    const int64_t blocks = (cols + 31) / 32;
+    if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+    const unsigned g = unsigned(blocks);
+    if (elem == TPGEMM_ELEM_F16)
+        column_sum_kernel<<<g, 256, 0, stream>>>(partial, strips, cols, static_cast<__half*>(out));
+    else if (elem == TPGEMM_ELEM_BF16)
+        column_sum_kernel<<<g, 256, 0, stream>>>(partial, strips, cols,
+                                                 static_cast<__nv_bfloat16*>(out));
+    else
+        column_sum_kernel<<<g, 256, 0, stream>>>(partial, strips, cols, static_cast<float*>(out));
+    return cudaGetLastError();
+}
+
+}  // namespace
+}  // namespace tpg

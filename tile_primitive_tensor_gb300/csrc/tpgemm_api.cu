@@ -22,6 +22,7 @@
 #include <mutex>
 #include <string>
 
+#include "ops_internal.h"
 #include "ptx.cuh"
 #include "tpgemm.h"
 #include "tpgemm_internal.h"
@@ -1340,6 +1341,29 @@ tpgemm_status run_host(float* Dh, const void* Ah, const void* Bh, const float* C
 
 namespace tpg {
 void set_error_detail(const char* text) { g_detail = text ? text : ""; }
+
+tpgemm_status fail_with(tpgemm_status s, const char* fmt, ...) {
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof(buf), fmt, ap);
+    va_end(ap);
+    g_detail = buf;
+    return s;
+}
+
+tpgemm_status require_device(int* sms) {
+    DeviceInfo dev;
+    const tpgemm_status s = device_info(&dev);
+    if (s != TPGEMM_OK) return s;
+    if (!(dev.major == 10 && dev.minor == 3))
+        return fail(TPGEMM_ERR_ARCH, "device is compute capability %d.%d; this build targets sm_103a",
+                    dev.major, dev.minor);
+    *sms = dev.sms;
+    return TPGEMM_OK;
+}
+
+tpgemm_status tensor_map_encoder(PFN_cuTensorMapEncodeTiled_v12000* fn) { return get_encoder(fn); }
 
 uint64_t wait_timeout_ns() {
     long long ms = tuning().wait_ms;
