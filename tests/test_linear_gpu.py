@@ -351,3 +351,47 @@ def test_python_refusals():
     for kind, call in cases:
         with pytest.raises(kind):
             call()
+
+
+# Each kernel at sizes the planner would give to another, and the choices it makes within one.
+@pytest.mark.parametrize("path", ["tile", "split"])
+@pytest.mark.parametrize("M,N,K", [(1, 8, 16), (17, 16, 16), (129, 64, 264), (256, 256, 512),
+                                   (300, 304, 304), (130, 1000, 72), (1000, 24, 24), (520, 776, 1032)])
+def test_each_kernel(path, M, N, K, tune):
+    tune.setenv("TPGEMM_LINEAR_PATH", path)
+    for dtype in (BF16, E4M3):
+        check_linear(M, N, K, dtype, act="silu", pre=True, seed=M + N + K)
+    check_backward(M, N, K, F16, "gelu", F32, seed=M)
+    tune.delenv("TPGEMM_LINEAR_PATH")
+
+
+@pytest.mark.parametrize("bn", range(32, 257, 32))
+def test_tile_widths(bn, tune):
+    tune.setenv("TPGEMM_LINEAR_PATH", "tile")
+    tune.setenv("TPGEMM_LINEAR_BN", str(bn))
+    check_linear(400, 520, 200, F16, act="gelu", seed=bn)
+    check_linear(400, 520, 208, E4M3, act="gelu", seed=bn)
+    check_backward(400, 200, 136, BF16, "none", BF16, seed=bn)
+    tune.delenv("TPGEMM_LINEAR_PATH")
+    tune.delenv("TPGEMM_LINEAR_BN")
+
+
+@pytest.mark.parametrize("split", range(1, 9))
+@pytest.mark.parametrize("bp", [64, 80, 96, 112, 128])
+def test_splits_and_tile_rows(split, bp, tune):
+    tune.setenv("TPGEMM_LINEAR_PATH", "split")
+    tune.setenv("TPGEMM_LINEAR_SPLIT", str(split))
+    tune.setenv("TPGEMM_LINEAR_BP", str(bp))
+    check_linear(40, 520, 1032, F16, act="gelu", pre=True, seed=bp)
+    check_linear(300, 136, 1040, E4M3, act="gelu", seed=bp)
+    if bp % 64 == 0:
+        check_backward(24, 200, 328, BF16, "none", BF16, seed=bp)
+        check_backward(520, 200, 136, BF16, "none", F32, seed=bp)
+    for name in ("PATH", "SPLIT", "BP"):
+        tune.delenv("TPGEMM_LINEAR_" + name)
+
+
+def test_many_tiles_per_pair():
+    # Several tiles to a pair of CTAs: both accumulators in turn, ragged on every side.
+    check_linear(4100, 5000, 264, BF16, act="relu", pre=True, seed=1)
+    check_linear(6000, 3000, 144, E5M2, act="none", seed=2)

@@ -1,0 +1,205 @@
+// Planning of the linear layer's product on the tcgen05 kernels: which kernel,
+// orientation, tile and split, the tensor maps, and the launch.
+#include <algorithm>
+#include <mutex>
+
+#include "linear_tc.h"
+#include "ptx.cuh"
+#include "tpgemm_internal.h"
+
+namespace tpg {
+namespace {
+
+constexpr int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// CTA pairs that fit the device at once (all tile kernels hold the same shared
+// memory and threads), asked once per device.
+tpgemm_status max_pairs(const TcLinear& p, int* pairs) {
+    static std::mutex m;
+    static int cache[64] = {};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < 0 || dev >= 64) return fail_with(TPGEMM_ERR_ARCH, "device index %d unsupported", dev);
+    std::lock_guard<std::mutex> lock(m);
+    if (!cache[dev]) {
+        const cudaError_t e = tc_linear_max_pairs(p, &cache[dev]);
+        if (e != cudaSuccess || cache[dev] <= 0) {
+            cache[dev] = 0;
+            return fail_with(TPGEMM_ERR_LAUNCH, "cluster occupancy query failed: %s",
+                             cudaGetErrorString(e));
+        }
+    }
+    *pairs = cache[dev];
+    return TPGEMM_OK;
+}
+
+// Bytes one SM takes in per nanosecond when a stage's operands come from L2 (53
+// to 56 bytes per clock measured on the multiply), the pair's time for one
+// 128-byte-wide K stage at the tensor rate, and what a launch costs around its
+// K loop, all in ns.
+constexpr double kSmBytes = 105.0;
+constexpr double kStageNs = 340.0;  // 256 x 256 x (64 of 16 bits)
+
+struct Choice {
+    double ns = 1e30;
+    int pair = 0, swap = 0, bn = 0, bp = 128, split = 1;
+};
+
+}  // namespace
+
+bool tma_rows(const Operand& o, int64_t rows, int64_t K, int dtype) {
+    const int64_t lines = o.mn ? K : rows;
+    return reinterpret_cast<uintptr_t>(o.p) % 16 == 0 &&
+           (lines <= 1 || (o.ld * elem_size(dtype)) % 16 == 0);
+}
+
+namespace {
+
+tpgemm_status encode(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* map, const Operand& o,
+                     int64_t rows, int64_t K, int dtype, int box_rows) {
+    const int es = elem_size(dtype);
+    const CUtensorMapDataType t = es == 1                      ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                  : dtype == TPGEMM_ELEM_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                              : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    const uint64_t inner = uint64_t(o.mn ? rows : K), outer = uint64_t(o.mn ? K : rows);
+    cuuint64_t dims[2] = {inner, outer};
+    // (A single line's pitch is never used, but has to be a multiple of 16.)
+    cuuint64_t pitch[1] = {outer > 1 ? uint64_t(o.ld) * es : (inner * es + 15) / 16 * 16};
+    cuuint32_t box[2] = {cuuint32_t(128 / es), cuuint32_t(o.mn ? 64 : box_rows)};
+    cuuint32_t one[2] = {1, 1};
+    const CUresult r = enc(map, t, 2, const_cast<void*>(o.p), dims, pitch, box, one,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS)
+        return fail_with(TPGEMM_ERR_LAUNCH, "cuTensorMapEncodeTiled failed with CUresult %d", int(r));
+    return TPGEMM_OK;
+}
+
+bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+// Whether eight neighbouring outputs can be moved with 16-byte accesses.
+bool vector_epilogue(const Epilogue& e) {
+    const int es = elem_size(e.out);
+    auto rows16 = [&](const void* p, int64_t ld) { return !p || (aligned16(p) && (ld * es) % 16 == 0); };
+    return rows16(e.Y, e.ldy) && rows16(e.Z, e.ldz) && rows16(e.R, e.ldr) && aligned16(e.bias) &&
+           aligned16(e.sw);
+}
+
+// Time of the tile kernel: waves of 256 x bn tiles over the pairs, each K stage
+// at the tensor rate or at what an SM can take in.
+Choice plan_tile(const LinearOp& op, int64_t kb, int pairs, int bn_forced) {
+    Choice best;
+    for (int bn = 256; bn >= 32; bn -= 32) {
+        if (bn_forced > 0 && bn != bn_forced) continue;
+        const int64_t tiles = ceil_div(op.M, 256) * ceil_div(op.N, bn);
+        const double stage = std::max(kStageNs * bn / 256, (128 + bn / 2) * 128 / kSmBytes);
+        const double ns = 6000 + double(ceil_div(tiles, pairs)) * (double(kb) * stage + 500);
+        if (ns < best.ns) {
+            best.ns = ns;
+            best.pair = 1;
+            best.swap = 0;
+            best.bn = bn;
+        }
+    }
+    return best;
+}
+
+// Time of the split kernel: tiles x split CTAs over the SMs, each taking in its
+// share of the operands; joining costs more with every CTA of a cluster.
+Choice plan_split(const LinearOp& op, int64_t kb, int sms, const LinearTuning& t) {
+    Choice best;
+    // The output's longer side along the lanes.
+    const bool swap = op.N >= op.M;
+    const int64_t Mp = swap ? op.N : op.M, Nq = swap ? op.M : op.N;
+    const bool p_mn = swap ? op.b.mn : op.a.mn;
+    const int bn = Nq >= 256 ? 256 : int(ceil_div(Nq, 16) * 16);
+    for (int bp = 128; bp >= 64; bp -= 16) {
+        if (p_mn && bp % 64) continue;
+        if (t.bp > 0 && bp != t.bp) continue;
+        for (int split = 1; split <= 8 && split <= kb; ++split) {
+            if (t.split > 0 && split != std::min<int64_t>(t.split, kb)) continue;
+            const int64_t ctas = ceil_div(Mp, bp) * ceil_div(Nq, bn) * split;
+            const double bytes = double(bp + bn) * 128;
+            const double ns = 5000 + 250 * split + double(ceil_div(ctas, sms)) *
+                              (double(ceil_div(kb, split)) * bytes / kSmBytes + 1000);
+            if (ns < best.ns) {
+                best.ns = ns;
+                best.swap = swap;
+                best.bn = bn;
+                best.bp = bp;
+                best.split = split;
+            }
+        }
+    }
+    return best;
+}
+
+}  // namespace
+
+tpgemm_status run_linear_tc(const LinearOp& op, int sms, cudaStream_t stream) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc;
+    tpgemm_status s = tensor_map_encoder(&enc);
+    if (s != TPGEMM_OK) return s;
+    const LinearTuning t = linear_tuning();
+    TcLinear p{};
+    p.e = op.e;
+    p.fp8 = elem_size(op.dtype) == 1;
+    p.bk = p.fp8 ? 128 : 64;
+    p.k_blocks = int(ceil_div(op.K, p.bk));
+    p.timeout_ns = wait_timeout_ns();
+    p.vec = vector_epilogue(op.e);
+    const Choice split = plan_split(op, p.k_blocks, sms, t);
+    Choice c = plan_tile(op, p.k_blocks, sms / 2, t.bn);
+    if (t.path == kLinearSplit || (t.path != kLinearTile && split.ns < c.ns)) c = split;
+    if (c.bn == 0) return fail_with(TPGEMM_ERR_PATH, "the planner overrides leave no plan");
+    p.pair = c.pair;
+    p.swap = c.swap;
+    p.bn = c.bn;
+    p.bp = c.bp;
+    p.split = c.split;
+    const Operand& P = p.swap ? op.b : op.a;
+    const Operand& Q = p.swap ? op.a : op.b;
+    p.Mp = p.swap ? op.N : op.M;
+    p.Nq = p.swap ? op.M : op.N;
+    p.p_mn = P.mn;
+    p.q_mn = Q.mn;
+    p.idesc = idesc_f16_f32(op.dtype == TPGEMM_ELEM_BF16 || op.dtype == TPGEMM_ELEM_E5M2, P.mn != 0,
+                            Q.mn != 0, p.pair ? 256 : 128, p.bn);
+    const int q_rows = p.pair ? p.bn / 2 : p.bn;
+    p.p_bytes = 16384;
+    p.q_bytes = p.q_mn ? uint32_t((q_rows + 63) / 64) * 8192u : uint32_t(q_rows) * 128u;
+    const int64_t tiles_p = ceil_div(p.Mp, p.pair ? 256 : p.bp), tiles_q = ceil_div(p.Nq, p.bn);
+    if (tiles_p * tiles_q * p.split > 0x7fffffff)
+        return fail_with(TPGEMM_ERR_SHAPE, "too many tiles");
+    p.tiles_p = int(tiles_p);
+    p.tiles_q = int(tiles_q);
+    p.tiles = int(tiles_p * tiles_q);
+    const size_t budget = size_t(kTcMaxSmem) - 1024 - 512;
+    int grid;
+    if (p.pair) {
+        p.stages = int(std::min<size_t>(8, budget / (p.p_bytes + p.q_bytes)));
+        p.group = 8;
+        int pairs = 0;
+        s = max_pairs(p, &pairs);
+        if (s != TPGEMM_OK) return s;
+        grid = 2 * std::min(p.tiles, pairs);
+    } else {
+        p.stages = int(std::min<size_t>(12, budget / (p.p_bytes + p.q_bytes)));
+        p.ring_bytes = uint32_t(p.stages) * (p.p_bytes + p.q_bytes);
+        p.ring_bytes = std::max(p.ring_bytes, uint32_t(p.bn) * 129u * 4u);
+        p.tmem_cols = 32;
+        while (p.tmem_cols < 32 * ((p.bn + 31) / 32)) p.tmem_cols *= 2;
+        grid = p.tiles * p.split;
+    }
+    CUtensorMap mapP, mapQ;
+    s = encode(enc, &mapP, P, p.Mp, op.K, op.dtype, p.pair ? 128 : p.bp);
+    if (s != TPGEMM_OK) return s;
+    s = encode(enc, &mapQ, Q, p.Nq, op.K, op.dtype, q_rows);
+    if (s != TPGEMM_OK) return s;
+    const cudaError_t e = launch_tc_linear(mapP, mapQ, p, grid, stream);
+    if (e != cudaSuccess)
+        return fail_with(TPGEMM_ERR_LAUNCH, "tcgen05 linear kernel launch: %s", cudaGetErrorString(e));
+    return TPGEMM_OK;
+}
+
+}  // namespace tpg

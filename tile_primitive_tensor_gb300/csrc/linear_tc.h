@@ -1,0 +1,37 @@
+// The tcgen05 kernels of the linear layer: their parameters and launch.
+#pragma once
+
+#include "ops_internal.h"
+
+namespace tpg {
+
+struct TcLinear {
+    Epilogue e;
+    int64_t Mp, Nq;        // rows of P and of Q
+    uint64_t timeout_ns;   // bound of every wait
+    int tiles_p, tiles_q;  // tiles along P (tile kernel: of a pair's 256 rows) and Q
+    int tiles;             // tile kernel: their number
+    int k_blocks, bk;      // 128-byte-wide K stages, and K elements of each
+    int bp, bn;            // P rows of a split tile; Q rows of a tile
+    int p_mn, q_mn;        // operand stored along its rows
+    int stages;            // depth of the TMA ring
+    uint32_t p_bytes, q_bytes;  // shared bytes of one stage's operands (of one CTA)
+    uint32_t ring_bytes;   // split kernel: shared bytes of ring and partial sums
+    uint32_t idesc;
+    int tmem_cols;         // split kernel
+    int split;             // split kernel: CTAs of a cluster, each a share of K
+    int group;             // tile kernel: P tiles of a raster run
+    int swap;              // P holds the output's columns
+    int pair;              // tile kernel (1) or split kernel (0)
+    int fp8;
+    int vec;               // 16-byte aligned rows of Y, Z, R (and dense bias, scale_w)
+};
+
+size_t tc_linear_smem(const TcLinear& p);
+cudaError_t launch_tc_linear(const CUtensorMap& mapP, const CUtensorMap& mapQ, const TcLinear& p,
+                             int grid, cudaStream_t stream);
+// CTA pairs of the tile kernel that fit the device at once.
+cudaError_t tc_linear_max_pairs(const TcLinear& p, int* pairs);
+cudaError_t linear_read_and_clear_status(int* status);
+
+}  // namespace tpg

@@ -131,7 +131,10 @@ tpgemm_status check_act(int act) {
     } while (0)
 
 // One product on the kernel that suits it.
-tpgemm_status run_product(const tpg::LinearOp& op, cudaStream_t st) {
+tpgemm_status run_product(const tpg::LinearOp& op, int sms, cudaStream_t st) {
+    if (op.K > 0 && tpg::tma_rows(op.a, op.M, op.K, op.dtype) &&
+        tpg::tma_rows(op.b, op.N, op.K, op.dtype))
+        return tpg::run_linear_tc(op, sms, st);
     return launched(tpg::launch_linear_simple(op, st), "linear kernel launch");
 }
 
@@ -233,7 +236,7 @@ tpgemm_status tpgemm_linear(void* Y, void* Z, const void* A, const void* W, cons
     tpg::LinearOp op{M, N, K, d->dtype, {A, in[0].ld, 0}, {W, in[1].ld, 0},
                      {Y, Z, R, bias, scale_a, scale_w, out[0].ld, out[1].ld, in[2].ld, d->act,
                       d->out}};
-    return run_product(op, static_cast<cudaStream_t>(stream));
+    return run_product(op, sms, static_cast<cudaStream_t>(stream));
 }
 
 size_t tpgemm_linear_backward_workspace_bytes(const void* dY, const void* A, const void* W,
@@ -306,13 +309,13 @@ tpgemm_status tpgemm_linear_backward(void* dA, void* dW, void* dbias, const void
         tpg::LinearOp op{M, K, N, d->dtype, {dz, lddz, 0}, {W, in[2].ld, 1},
                          {dA, nullptr, nullptr, nullptr, nullptr, nullptr, out[0].ld, 0, 0,
                           TPGEMM_ACT_NONE, d->dtype}};
-        TPG_TRY(run_product(op, st));
+        TPG_TRY(run_product(op, sms, st));
     }
     if (dW) {  // [N, K] = dZ^T . A: along the rows of both
         tpg::LinearOp op{N, K, M, d->dtype, {dz, lddz, 1}, {A, in[1].ld, 1},
                          {dW, nullptr, nullptr, nullptr, nullptr, nullptr, out[1].ld, 0, 0,
                           TPGEMM_ACT_NONE, d->grad}};
-        TPG_TRY(run_product(op, st));
+        TPG_TRY(run_product(op, sms, st));
     }
     return TPGEMM_OK;
 }

@@ -20,6 +20,14 @@ tpgemm_status fail_with(tpgemm_status s, const char* fmt, ...);
 tpgemm_status require_device(int* sms);
 tpgemm_status tensor_map_encoder(PFN_cuTensorMapEncodeTiled_v12000* fn);
 
+// Planner overrides of the linear layer's product (TPGEMM_LINEAR_PATH, _BN, _BP,
+// _SPLIT; -1: not set), from the snapshot that tpgemm_reload_tuning renews.
+enum { kLinearTile = 0, kLinearSplit = 1, kLinearFew = 2 };
+struct LinearTuning {
+    int path, bn, bp, split;
+};
+LinearTuning linear_tuning();
+
 inline int elem_size(int elem) {
     return elem == TPGEMM_ELEM_F32 ? 4 : (elem == TPGEMM_ELEM_F16 || elem == TPGEMM_ELEM_BF16) ? 2 : 1;
 }
@@ -57,6 +65,11 @@ struct LinearOp {
 };
 
 cudaError_t launch_linear_simple(const LinearOp& op, cudaStream_t stream);
+
+// The product on the tcgen05 kernels (linear_plan.cu); its operands' rows start
+// on 16-byte boundaries (tma_rows). K >= 1.
+tpgemm_status run_linear_tc(const LinearOp& op, int sms, cudaStream_t stream);
+bool tma_rows(const Operand& o, int64_t rows, int64_t K, int dtype);
 
 // ---- gradients of the linear layer's epilogue ----
 // dZ = dY act'(Z) (dZ is not written when act is none) and per-strip column

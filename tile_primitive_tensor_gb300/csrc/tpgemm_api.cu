@@ -22,6 +22,7 @@
 #include <mutex>
 #include <string>
 
+#include "linear_tc.h"
 #include "ops_internal.h"
 #include "ptx.cuh"
 #include "tpgemm.h"
@@ -95,6 +96,7 @@ struct Tuning {
     int krotate = -1, max_clusters = -1, pair = -1, producers = -1, sk = -1, stages = -1;
     int tail = -1, host_blocks = -1, l2_p = -1, l2_q = -1, l2_cd = -1, snake = -1, krev = -1;
     int epi_help = -1, host_edge = -1;
+    int linear_path = -1, linear_bn = -1, linear_bp = -1, linear_split = -1;
     int debug_plant = -1;  // debug builds only
     int orient = 0;  // 1 "swap", 2 "normal"
     long long wait_ms = -1;
@@ -126,6 +128,14 @@ Tuning read_tuning() {
     geti("TPGEMM_TC_L2_Q", &t.l2_q);
     geti("TPGEMM_TC_L2_CD", &t.l2_cd);
     geti("TPGEMM_TC_SNAKE", &t.snake);
+    geti("TPGEMM_LINEAR_BN", &t.linear_bn);
+    geti("TPGEMM_LINEAR_BP", &t.linear_bp);
+    geti("TPGEMM_LINEAR_SPLIT", &t.linear_split);
+    if (const char* f = getenv("TPGEMM_LINEAR_PATH")) {
+        if (!strcmp(f, "tile")) t.linear_path = tpg::kLinearTile;
+        if (!strcmp(f, "split")) t.linear_path = tpg::kLinearSplit;
+        if (!strcmp(f, "few")) t.linear_path = tpg::kLinearFew;
+    }
     if (const char* f = getenv("TPGEMM_TC_ORIENT")) {
         if (!strcmp(f, "swap")) t.orient = 1;
         if (!strcmp(f, "normal")) t.orient = 2;
@@ -1363,6 +1373,11 @@ tpgemm_status require_device(int* sms) {
     return TPGEMM_OK;
 }
 
+LinearTuning linear_tuning() {
+    const Tuning& t = tuning();
+    return {t.linear_path, t.linear_bn, t.linear_bp, t.linear_split};
+}
+
 tpgemm_status tensor_map_encoder(PFN_cuTensorMapEncodeTiled_v12000* fn) { return get_encoder(fn); }
 
 uint64_t wait_timeout_ns() {
@@ -1470,6 +1485,8 @@ tpgemm_status tpgemm_last_device_error(void) {
     int st = 0, st_cp = 0, site = 0;
     e = tpg::tc_read_and_clear_device_status(&st, &site);
     if (e == cudaSuccess) e = tpg::cp_read_and_clear_device_status(&st_cp);
+    int st_linear = 0;
+    if (e == cudaSuccess) e = tpg::linear_read_and_clear_status(&st_linear);
     if (e != cudaSuccess)
         return fail(TPGEMM_ERR_LAUNCH, "reading device status: %s", cudaGetErrorString(e));
     if (st == tpg::kStatusTimeout)
@@ -1483,6 +1500,8 @@ tpgemm_status tpgemm_last_device_error(void) {
                     "a debug bounds check failed at site %d (%s); the access was skipped", site,
                     kSites[site >= 0 && site <= 7 ? site : 0]);
     }
+    if (st_linear == tpg::kStatusTimeout)
+        return fail(TPGEMM_ERR_TIMEOUT, "a linear-layer kernel wait exceeded its bound");
     if (st_cp == tpg::kStatusTimeout)
         return fail(TPGEMM_ERR_TIMEOUT, "a tensor-memory copy kernel wait exceeded its bound");
     return TPGEMM_OK;
