@@ -395,3 +395,12 @@ def test_many_tiles_per_pair():
     # Several tiles to a pair of CTAs: both accumulators in turn, ragged on every side.
     check_linear(4100, 5000, 264, BF16, act="relu", pre=True, seed=1)
     check_linear(6000, 3000, 144, E5M2, act="none", seed=2)
+
+
+@pytest.mark.parametrize("split", [1, 2, 4, 8])
+@pytest.mark.parametrize("M,N,K", [(1, 24, 3001), (8, 40, 128), (9, 17, 2000), (16, 1000, 520)])
+def test_few_tokens_splits(split, M, N, K, tune):
+    tune.setenv("TPGEMM_LINEAR_SPLIT", str(split))
+    for dtype in (F16, BF16, E4M3, E5M2):
+        check_linear(M, N, K, dtype, act="silu", pre=True, seed=split)
+    tune.delenv("TPGEMM_LINEAR_SPLIT")

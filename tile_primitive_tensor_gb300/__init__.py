@@ -610,10 +610,10 @@ def _matrix(name, t, rows, cols, dtype, device) -> int:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, not {device}")
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+    if t.shape != (rows, cols):
         raise ValueError(f"{name} must be [{rows}, {cols}], got {list(t.shape)}")
     s0, s1 = t.stride()
-    if cols > 1 and s1 != 1:
+    if s1 != 1 and cols > 1:
         raise ValueError(f"{name} must have unit column stride, got {s1}")
     if rows <= 1 or cols == 0:
         return cols
@@ -627,7 +627,7 @@ def _vector(name, t, n, dtype, device) -> None:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, not {device}")
-    if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+    if t.shape != (n,) or (n > 1 and t.stride(0) != 1):
         raise ValueError(f"{name} must be a dense vector of {n}")
 
 
@@ -650,6 +650,19 @@ def _cuda(name, t):
     return t.device
 
 
+def _enqueue(torch, device, stream, call):
+    """Runs call(stream) with `device` current and raises if it is refused. The default stream
+    is the device's current one, read through its raw handle: building torch's stream object
+    costs 2.9 us of a 10 us call."""
+    index = device.index
+    if index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            check(call(_stream(stream)))
+    else:
+        check(call(torch._C._cuda_getCurrentRawStream(index) if stream is None
+                   else _stream(stream)))
+
+
 def linear(A, W, bias=None, residual=None, *, act="none", scale_a=None, scale_w=None,
            out_dtype=None, out=None, pre=None, workspace=None, stream=None):
     """Y = act(scale_a[m] scale_w[n] A.W^T + bias) + residual on CUDA tensors; returns Y.
@@ -661,36 +674,41 @@ def linear(A, W, bias=None, residual=None, *, act="none", scale_a=None, scale_w=
     gelu_tanh. Matrices may be row-strided; ``out`` may be the residual itself. The workspace, if
     one is needed (tpgemm_linear_workspace_bytes), is allocated here with torch unless given."""
     import torch
+    lib = _lib or _load()
     dev = _cuda("A", A)
     M, K = A.shape
     N = W.shape[0]
     dt = A.dtype
-    desc = LinearDesc(M, N, K, _matrix("A", A, M, K, dt, dev), _matrix("W", W, N, K, dt, dev))
-    if out is not None:
-        out_dtype = out.dtype if out_dtype is None else out_dtype
-    elif out_dtype is None:
-        out_dtype = dt if dt.itemsize == 2 else torch.bfloat16
+    lda = _matrix("A", A, M, K, dt, dev)
+    ldw = _matrix("W", W, N, K, dt, dev)
+    if out_dtype is None:
+        out_dtype = out.dtype if out is not None else (dt if dt.itemsize == 2 else torch.bfloat16)
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype, device=dev)
-    desc.ldy = _matrix("out", out, M, N, out_dtype, dev)
-    desc.dtype = elem_code(dt)
-    desc.out = elem_code(out_dtype)
-    desc.act = _act_code(act)
+        out, ldy = torch.empty((M, N), dtype=out_dtype, device=dev), N
+    else:
+        ldy = _matrix("out", out, M, N, out_dtype, dev)
+    ldr = ldz = 0
     if residual is not None:
-        desc.ldr = _matrix("residual", residual, M, N, out_dtype, dev)
+        ldr = _matrix("residual", residual, M, N, out_dtype, dev)
     if pre is not None:
-        desc.ldz = _matrix("pre", pre, M, N, out_dtype, dev)
+        ldz = _matrix("pre", pre, M, N, out_dtype, dev)
     if bias is not None:
         _vector("bias", bias, N, out_dtype, dev)
     if scale_a is not None:
         _vector("scale_a", scale_a, M, torch.float32, dev)
     if scale_w is not None:
         _vector("scale_w", scale_w, N, torch.float32, dev)
-    need = tpgemm_linear_workspace_bytes(A, W, desc) if workspace is None else 0
+    desc = LinearDesc(M, N, K, lda, ldw, ldr, ldy, ldz, elem_code(dt), elem_code(out_dtype),
+                      _act_code(act))
+    ref = ctypes.byref(desc)
+    pa, pw = A.data_ptr(), W.data_ptr()
+    need = 0
+    if workspace is None:
+        need = lib.tpgemm_linear_workspace_bytes(pa, pw, ref)
     workspace, size = _scratch(torch, workspace, need, dev)
-    with torch.cuda.device(dev):
-        check(tpgemm_linear(out, pre, A, W, scale_a, scale_w, bias, residual, desc, workspace,
-                            size, stream))
+    _enqueue(torch, dev, stream, lambda st: lib.tpgemm_linear(
+        out.data_ptr(), _ptr(pre), pa, pw, _ptr(scale_a), _ptr(scale_w), _ptr(bias),
+        _ptr(residual), ref, _ptr(workspace), size, st))
     return out
 
 
@@ -703,28 +721,34 @@ def linear_backward(dY, A, W, pre=None, *, act="none", grad_dtype=None, need=(Tr
     float16 or bfloat16; by default A's type). ``need`` says which of the three are wanted; the
     others are None."""
     import torch
+    lib = _lib or _load()
     dev = _cuda("A", A)
     M, K = A.shape
     N = W.shape[0]
     dt = A.dtype
     grad_dtype = dt if grad_dtype is None else grad_dtype
     code = _act_code(act)
-    desc = LinearGradDesc(M, N, K, _matrix("dY", dY, M, N, dt, dev), 0,
-                          _matrix("A", A, M, K, dt, dev), _matrix("W", W, N, K, dt, dev), K, K,
-                          elem_code(dt), elem_code(grad_dtype), code)
+    ldz = 0
     if code != TPGEMM_ACT_NONE:
         if pre is None:
             raise ValueError(f"act={act!r} needs pre, the value before the activation")
-        desc.ldz = _matrix("pre", pre, M, N, dt, dev)
+        ldz = _matrix("pre", pre, M, N, dt, dev)
     else:
         pre = None
+    desc = LinearGradDesc(M, N, K, _matrix("dY", dY, M, N, dt, dev), ldz,
+                          _matrix("A", A, M, K, dt, dev), _matrix("W", W, N, K, dt, dev), K, K,
+                          elem_code(dt), elem_code(grad_dtype), code)
     dA = torch.empty((M, K), dtype=dt, device=dev) if need[0] else None
     dW = torch.empty((N, K), dtype=grad_dtype, device=dev) if need[1] else None
     dbias = torch.empty(N, dtype=grad_dtype, device=dev) if need[2] else None
-    size = tpgemm_linear_backward_workspace_bytes(dY, A, W, desc) if workspace is None else 0
+    ref = ctypes.byref(desc)
+    py, pa, pw = dY.data_ptr(), A.data_ptr(), W.data_ptr()
+    size = 0
+    if workspace is None:
+        size = lib.tpgemm_linear_backward_workspace_bytes(py, pa, pw, ref)
     workspace, size = _scratch(torch, workspace, size, dev)
-    with torch.cuda.device(dev):
-        check(tpgemm_linear_backward(dA, dW, dbias, dY, A, W, pre, desc, workspace, size, stream))
+    _enqueue(torch, dev, stream, lambda st: lib.tpgemm_linear_backward(
+        _ptr(dA), _ptr(dW), _ptr(dbias), py, pa, pw, _ptr(pre), ref, _ptr(workspace), size, st))
     return dA, dW, dbias
 
 
@@ -746,6 +770,7 @@ def rmsnorm(x, weight, residual=None, *, eps=1e-6, quant=None, out_dtype=None, n
     float8_e4m3fn (the default) or float8_e5m2, holding y / scale. h is returned with a residual
     only; it may be written in place (out_h = x or residual)."""
     import torch
+    lib = _lib or _load()
     dev = _cuda("x", x)
     rows, cols = x.shape
     dt = x.dtype
@@ -756,16 +781,19 @@ def rmsnorm(x, weight, residual=None, *, eps=1e-6, quant=None, out_dtype=None, n
     if weight.dtype is not dt and weight.dtype is not torch.float32:
         raise TypeError(f"weight must be {dt} or float32, got {weight.dtype}")
     _vector("weight", weight, cols, weight.dtype, dev)
+    ldx = _matrix("x", x, rows, cols, dt, dev)
     if out is None:
-        out = torch.empty((rows, cols), dtype=out_dtype, device=dev)
-    desc = RmsNormDesc(rows, cols, _matrix("x", x, rows, cols, dt, dev), 0, 0,
-                       _matrix("out", out, rows, cols, out_dtype, dev), elem_code(dt),
-                       elem_code(weight.dtype), elem_code(out_dtype), _SCALES[quant], eps)
+        out, ldy = torch.empty((rows, cols), dtype=out_dtype, device=dev), cols
+    else:
+        ldy = _matrix("out", out, rows, cols, out_dtype, dev)
     h = scale = rstd = None
+    ldr = ldh = 0
     if residual is not None:
-        desc.ldr = _matrix("residual", residual, rows, cols, dt, dev)
-        h = torch.empty((rows, cols), dtype=dt, device=dev) if out_h is None else out_h
-        desc.ldh = _matrix("out_h", h, rows, cols, dt, dev)
+        ldr = _matrix("residual", residual, rows, cols, dt, dev)
+        if out_h is None:
+            h, ldh = torch.empty((rows, cols), dtype=dt, device=dev), cols
+        else:
+            h, ldh = out_h, _matrix("out_h", out_h, rows, cols, dt, dev)
     elif out_h is not None:
         raise ValueError("out_h needs a residual (h is x without one)")
     if quant == "row":
@@ -774,8 +802,11 @@ def rmsnorm(x, weight, residual=None, *, eps=1e-6, quant=None, out_dtype=None, n
         scale = torch.empty((rows, (cols + 31) // 32), dtype=torch.uint8, device=dev)
     if need_rstd:
         rstd = torch.empty(rows, dtype=torch.float32, device=dev)
-    with torch.cuda.device(dev):
-        check(tpgemm_rmsnorm(out, h, scale, rstd, x, residual, weight, desc, stream))
+    desc = RmsNormDesc(rows, cols, ldx, ldr, ldh, ldy, elem_code(dt), elem_code(weight.dtype),
+                       elem_code(out_dtype), _SCALES[quant], eps)
+    _enqueue(torch, dev, stream, lambda st: lib.tpgemm_rmsnorm(
+        out.data_ptr(), _ptr(h), _ptr(scale), _ptr(rstd), x.data_ptr(), _ptr(residual),
+        weight.data_ptr(), ctypes.byref(desc), st))
     return RmsNorm(out, h, scale, rstd)
 
 
@@ -787,6 +818,7 @@ def rmsnorm_backward(dy, h, rstd, weight, dh=None, *, grad_dtype=None, need=(Tru
     dy, h, dh and dx [rows, cols] are of one type (float16, bfloat16 or float32), dweight of
     grad_dtype (by default weight's). ``need`` says which are wanted; ``out`` may be dy, h or dh."""
     import torch
+    lib = _lib or _load()
     dev = _cuda("dy", dy)
     rows, cols = dy.shape
     dt = dy.dtype
@@ -795,21 +827,23 @@ def rmsnorm_backward(dy, h, rstd, weight, dh=None, *, grad_dtype=None, need=(Tru
         raise TypeError(f"weight must be {dt} or float32, got {weight.dtype}")
     _vector("weight", weight, cols, weight.dtype, dev)
     _vector("rstd", rstd, rows, torch.float32, dev)
-    desc = RmsNormGradDesc(rows, cols, _matrix("dy", dy, rows, cols, dt, dev),
-                           _matrix("h", h, rows, cols, dt, dev), 0, 0, elem_code(dt),
-                           elem_code(weight.dtype), elem_code(grad_dtype))
-    if dh is not None:
-        desc.lddh = _matrix("dh", dh, rows, cols, dt, dev)
+    lddh = 0 if dh is None else _matrix("dh", dh, rows, cols, dt, dev)
     dx = dweight = None
+    lddx = size = 0
     if need[0]:
-        dx = torch.empty((rows, cols), dtype=dt, device=dev) if out is None else out
-        desc.lddx = _matrix("out", dx, rows, cols, dt, dev)
-    size = 0
+        if out is None:
+            dx, lddx = torch.empty((rows, cols), dtype=dt, device=dev), cols
+        else:
+            dx, lddx = out, _matrix("out", out, rows, cols, dt, dev)
+    desc = RmsNormGradDesc(rows, cols, _matrix("dy", dy, rows, cols, dt, dev),
+                           _matrix("h", h, rows, cols, dt, dev), lddh, lddx, elem_code(dt),
+                           elem_code(weight.dtype), elem_code(grad_dtype))
     if need[1]:
         dweight = torch.empty(cols, dtype=grad_dtype, device=dev)
-        size = tpgemm_rmsnorm_backward_workspace_bytes(rows, cols) if workspace is None else 0
+        if workspace is None:
+            size = lib.tpgemm_rmsnorm_backward_workspace_bytes(rows, cols)
     workspace, size = _scratch(torch, workspace, size, dev)
-    with torch.cuda.device(dev):
-        check(tpgemm_rmsnorm_backward(dx, dweight, dy, h, rstd, weight, dh, desc, workspace, size,
-                                      stream))
+    _enqueue(torch, dev, stream, lambda st: lib.tpgemm_rmsnorm_backward(
+        _ptr(dx), _ptr(dweight), dy.data_ptr(), h.data_ptr(), rstd.data_ptr(), weight.data_ptr(),
+        _ptr(dh), ctypes.byref(desc), _ptr(workspace), size, st))
     return dx, dweight

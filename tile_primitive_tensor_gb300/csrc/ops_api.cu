@@ -132,6 +132,9 @@ tpgemm_status check_act(int act) {
 
 // One product on the kernel that suits it.
 tpgemm_status run_product(const tpg::LinearOp& op, int sms, cudaStream_t st) {
+    const int path = tpg::linear_tuning().path;
+    if (tpg::linear_few_takes(op) && (path < 0 || path == tpg::kLinearFew || op.K == 0))
+        return launched(tpg::launch_linear_few(op, sms, st), "linear kernel launch");
     if (op.K > 0 && tpg::tma_rows(op.a, op.M, op.K, op.dtype) &&
         tpg::tma_rows(op.b, op.N, op.K, op.dtype))
         return tpg::run_linear_tc(op, sms, st);

@@ -69,6 +69,13 @@ cudaError_t launch_linear_simple(const LinearOp& op, cudaStream_t stream);
 // The product on the tcgen05 kernels (linear_plan.cu); its operands' rows start
 // on 16-byte boundaries (tma_rows). K >= 1.
 tpgemm_status run_linear_tc(const LinearOp& op, int sms, cudaStream_t stream);
+
+// The product for few rows of A (linear_few.cu), operands K-contiguous, any
+// alignment, any K.
+constexpr int kFewTokens = 16;
+bool linear_few_takes(const LinearOp& op);
+cudaError_t launch_linear_few(const LinearOp& op, int sms, cudaStream_t stream);
+
 bool tma_rows(const Operand& o, int64_t rows, int64_t K, int dtype);
 
 // ---- gradients of the linear layer's epilogue ----

@@ -14,34 +14,28 @@
 //
 // Gradients, with n = h rstd and w = dy gamma:
 //   dx = rstd (w - n mean(w n)) + dh,   dgamma = sum over rows of dy n.
+//
+// All of it is bound by memory. A row is read once into registers by a team of
+// threads (a warp for narrow rows, else a block), eight neighbouring columns to
+// a thread at a time so that each load moves 16 bytes, reduced, and written
+// from the registers. Rows wider than a team's registers (16384 columns) are
+// read twice, the second time from L2.
 #include "column_sum.cuh"
-#include "elem.cuh"
+#include "launch.cuh"
+#include "ptx.cuh"
+#include "vec8.cuh"
 
 namespace tpg {
 namespace {
 
-constexpr int kThreads = 256;
-
-__device__ __forceinline__ float load_as(const void* p, int elem, int64_t i) {
-    if (elem == TPGEMM_ELEM_F16) return to_f32(static_cast<const __half*>(p)[i]);
-    if (elem == TPGEMM_ELEM_BF16) return to_f32(static_cast<const __nv_bfloat16*>(p)[i]);
-    return static_cast<const float*>(p)[i];
-}
-
-__device__ __forceinline__ void store_as(void* p, int elem, int64_t i, float v) {
-    switch (elem) {
-        case TPGEMM_ELEM_F16: static_cast<__half*>(p)[i] = from_f32<__half>(v); break;
-        case TPGEMM_ELEM_BF16: static_cast<__nv_bfloat16*>(p)[i] = from_f32<__nv_bfloat16>(v); break;
-        case TPGEMM_ELEM_E4M3: static_cast<e4m3*>(p)[i] = from_f32<e4m3>(v); break;
-        case TPGEMM_ELEM_E5M2: static_cast<e5m2*>(p)[i] = from_f32<e5m2>(v); break;
-        default: static_cast<float*>(p)[i] = v; break;
-    }
-}
+constexpr int kMaxTeam = 1024;               // threads of a row
+constexpr int kMaxHeld = kMaxTeam * 8 * 2;   // columns a team holds in registers
+constexpr int kWarpRows = 8;                 // rows of a block when a row is a warp's
 
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
-// Largest |value| of a set as the 32-bit pattern: an integer maximum, so that
-// infinities and NaN (the largest patterns) are kept.
+// Scale of a row whose largest |value| has the given 32-bit pattern. Maxima are
+// taken of the patterns, so that infinities and NaN (the largest ones) are kept.
 __device__ __forceinline__ float row_scale(uint32_t amax, int elem) {
     const float top = elem == TPGEMM_ELEM_E4M3 ? 448.f : 57344.f;
     if (amax >= 0x7f800000u) return __uint_as_float(0x7fffffffu);
@@ -59,128 +53,458 @@ __device__ __forceinline__ uint32_t mx_scale(uint32_t amax, int elem, float& inv
     return uint32_t(e + 127);
 }
 
-// Sum of a and maximum of b over the block, in every thread.
-__device__ __forceinline__ void block_sum_max(float& a, uint32_t& b) {
-    __shared__ float sa[32];
-    __shared__ uint32_t sb[32];
+// A thread's eight columns of group i of a row that `team` threads share:
+// neighbouring ones when rows are aligned, else team columns apart, so that
+// either way a warp's accesses are contiguous.
+template <bool VEC>
+struct Cols {
+    int64_t first;  // of the eight
+    int step, n;    // distance between them, and how many lie in the row
+    __device__ __forceinline__ Cols(int64_t i, int t, int team, int64_t cols) {
+        const int64_t base = i * 8 * team;
+        first = VEC ? base + 8 * t : base + t;
+        step = VEC ? 1 : team;
+        const int64_t left = cols - first;
+        n = left <= 0 ? 0 : VEC ? (left < 8 ? int(left) : 8)
+                                : int(min(int64_t(8), (left + team - 1) / team));
+    }
+};
+
+template <typename T, bool VEC>
+__device__ __forceinline__ void load_cols(const void* base, int64_t row, const Cols<VEC>& c,
+                                          float (&f)[8]) {
+    if constexpr (VEC) {
+        // (Aligned rows are whole groups of eight.)
+        if (c.n == 8) {
+            load8<T>(base, row + c.first, true, 8, f);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j] = 0.f;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            f[j] = j < c.n ? to_f32(static_cast<const T*>(base)[row + c.first + int64_t(j) * c.step]) : 0.f;
+    }
+}
+
+template <typename T, bool VEC>
+__device__ __forceinline__ void store_cols(void* base, int64_t row, const Cols<VEC>& c,
+                                           const float (&f)[8]) {
+    if constexpr (VEC) {
+        if (c.n == 8) {
+            if constexpr (sizeof(T) == 1)
+                *reinterpret_cast<uint2*>(static_cast<T*>(base) + row + c.first) =
+                    pack8_fp8(f, std::is_same<T, e4m3>::value ? __NV_E4M3 : __NV_E5M2);
+            else
+                store8<T>(base, row + c.first, true, 8, f);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (j < c.n)
+                static_cast<T*>(base)[row + c.first + int64_t(j) * c.step] = from_f32<T>(f[j]);
+    }
+}
+
+template <typename XT, bool VEC>
+__device__ __forceinline__ void load_gamma(const void* gamma, int elem, const Cols<VEC>& c,
+                                           float (&f)[8]) {
+    if (elem == TPGEMM_ELEM_F32)
+        load_cols<float, VEC>(gamma, 0, c, f);
+    else
+        load_cols<XT, VEC>(gamma, 0, c, f);
+}
+
+// Sum of a and maximum of b over a warp, or over the block through `s`.
+template <bool WARP>
+__device__ __forceinline__ void team_sum_max(float& a, uint32_t& b, float2* s) {
+#pragma unroll
     for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
     b = __reduce_max_sync(0xffffffffu, b);
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, nw = blockDim.x >> 5;
-    __syncthreads();
-    if (lane == 0) {
-        sa[w] = a;
-        sb[w] = b;
-    }
-    __syncthreads();
-    a = 0.f;
-    b = 0u;
-    for (int i = 0; i < nw; ++i) {
-        a += sa[i];
-        b = max(b, sb[i]);
+    if constexpr (!WARP) {
+        const int nw = blockDim.x >> 5, lane = threadIdx.x & 31;
+        if (lane == 0) s[threadIdx.x >> 5] = make_float2(a, __uint_as_float(b));
+        __syncthreads();
+        const float2 v = lane < nw ? s[lane] : make_float2(0.f, 0.f);
+        a = v.x;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+        b = __reduce_max_sync(0xffffffffu, __float_as_uint(v.y));
     }
 }
 
-// One row per block, any width: a first pass over the row for its sum of
-// squares (and largest |h gamma|), a second that reads it again and writes.
-__global__ void __launch_bounds__(kThreads) rmsnorm_wide_kernel(RmsNormOp op) {
-    const int64_t row = blockIdx.x;
-    const int64_t xo = row * op.ldx, ro = row * op.ldr, ho = row * op.ldh, yo = row * op.ldy;
-    auto h_at = [&](int64_t c) {
-        float h = load_as(op.X, op.x, xo + c);
-        if (op.R) h += load_as(op.R, op.x, ro + c);
-        return h;
-    };
+// Stores one group of y (scaled for an 8-bit output) and, for MX, its scales.
+template <bool VEC>
+__device__ __forceinline__ void store_y(const RmsNormOp& op, int64_t row, const Cols<VEC>& c,
+                                        float (&y)[8], float inv) {
+    if (op.mode == TPGEMM_SCALE_MX) {
+        uint8_t* scale = static_cast<uint8_t*>(op.scale) + row * ((op.cols + 31) / 32);
+        if constexpr (VEC) {  // four lanes hold 32 neighbouring columns
+            uint32_t amax = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) amax = max(amax, abs_bits(y[j]));
+            amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+            amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+            const uint32_t code = mx_scale(amax, op.y, inv);
+            if ((threadIdx.x & 3) == 0 && c.n > 0) scale[c.first / 32] = uint8_t(code);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[j] *= inv;
+        } else {  // the warp holds 32 neighbouring columns of each j
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const uint32_t code =
+                    mx_scale(__reduce_max_sync(0xffffffffu, abs_bits(y[j])), op.y, inv);
+                if ((threadIdx.x & 31) == 0 && j < c.n)
+                    scale[(c.first + int64_t(j) * c.step) / 32] = uint8_t(code);
+                y[j] *= inv;
+            }
+        }
+    } else if (op.mode == TPGEMM_SCALE_ROW) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] *= inv;
+    }
+    const int64_t at = row * op.ldy;
+    switch (op.y) {
+        case TPGEMM_ELEM_F16: store_cols<__half, VEC>(op.Y, at, c, y); break;
+        case TPGEMM_ELEM_BF16: store_cols<__nv_bfloat16, VEC>(op.Y, at, c, y); break;
+        case TPGEMM_ELEM_E4M3: store_cols<e4m3, VEC>(op.Y, at, c, y); break;
+        case TPGEMM_ELEM_E5M2: store_cols<e5m2, VEC>(op.Y, at, c, y); break;
+        default: store_cols<float, VEC>(op.Y, at, c, y); break;
+    }
+}
+
+// h of one group: x + r.
+template <typename XT, bool VEC>
+__device__ __forceinline__ void load_h(const RmsNormOp& op, int64_t row, const Cols<VEC>& c,
+                                       float (&h)[8]) {
+    load_cols<XT, VEC>(op.X, row * op.ldx, c, h);
+    if (op.R) {
+        float r[8];
+        load_cols<XT, VEC>(op.R, row * op.ldr, c, r);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) h[j] += r[j];
+    }
+}
+
+// V groups of eight columns to a thread; WARP: a row to a warp, else to a
+// block; V == 0: rows of any width, read twice by a block.
+template <typename XT, int V, bool VEC, bool WARP>
+__global__ void __launch_bounds__(WARP ? 32 * kWarpRows : kMaxTeam) rmsnorm_kernel(const __grid_constant__ RmsNormOp op) {
+    __shared__ float2 s[32];
+    constexpr bool kWide = V == 0;
+    constexpr int kHeld = kWide ? 1 : V;
+    const int team = WARP ? 32 : int(blockDim.x);
+    const int t = WARP ? int(threadIdx.x & 31) : int(threadIdx.x);
+    const int64_t row = WARP ? int64_t(blockIdx.x) * kWarpRows + (threadIdx.x >> 5) : int64_t(blockIdx.x);
+    grid_launch_dependents();
+    grid_dependency_wait();
+    if (WARP && row >= op.rows) return;
+    const bool row_mode = op.mode == TPGEMM_SCALE_ROW;
+    const int64_t groups = kWide ? (op.cols + 8 * team - 1) / (8 * team) : V;
+    float h[kHeld][8], g[kHeld][8];
     float ss = 0.f;
     uint32_t amax = 0;
-    for (int64_t c = threadIdx.x; c < op.cols; c += kThreads) {
-        const float h = h_at(c);
-        ss += h * h;
-        if (op.mode == TPGEMM_SCALE_ROW) amax = max(amax, abs_bits(h * load_as(op.gamma, op.g, c)));
+    if constexpr (!kWide) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) load_h<XT, VEC>(op, row, Cols<VEC>(i, t, team, op.cols), h[i]);
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            load_gamma<XT, VEC>(op.gamma, op.g, Cols<VEC>(i, t, team, op.cols), g[i]);
     }
-    block_sum_max(ss, amax);
+    auto add = [&](const float (&hv)[8], const float (&gv)[8]) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            ss += hv[j] * hv[j];
+            if (row_mode) amax = max(amax, abs_bits(hv[j] * gv[j]));
+        }
+    };
+    if constexpr (kWide) {
+        for (int64_t i = 0; i < groups; ++i) {
+            const Cols<VEC> c(i, t, team, op.cols);
+            load_h<XT, VEC>(op, row, c, h[0]);
+            if (row_mode) load_gamma<XT, VEC>(op.gamma, op.g, c, g[0]);
+            add(h[0], g[0]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) add(h[i], g[i]);
+    }
+    team_sum_max<WARP>(ss, amax, s);
     const float rstd = 1.f / sqrtf(ss / float(op.cols) + op.eps);
-    if (threadIdx.x == 0 && op.rstd) op.rstd[row] = rstd;
+    if (t == 0 && op.rstd) op.rstd[row] = rstd;
     float inv = 1.f;
-    if (op.mode == TPGEMM_SCALE_ROW) {
+    if (row_mode) {
         const float scale = row_scale(abs_bits(rstd * __uint_as_float(amax)), op.y);
-        if (threadIdx.x == 0) static_cast<float*>(op.scale)[row] = scale;
+        if (t == 0) static_cast<float*>(op.scale)[row] = scale;
         inv = 1.f / scale;
     }
-    const int64_t blocks = (op.cols + 31) / 32;
-    for (int64_t c0 = 0; c0 < op.cols; c0 += kThreads) {
-        const int64_t c = c0 + threadIdx.x;
-        float y = 0.f;
-        if (c < op.cols) {
-            const float h = h_at(c);
-            if (op.H) store_as(op.H, op.x, ho + c, h);
-            y = h * rstd * load_as(op.gamma, op.g, c);
+    auto finish = [&](const Cols<VEC>& c, const float (&hv)[8], const float (&gv)[8]) {
+        if (op.H) store_cols<XT, VEC>(op.H, row * op.ldh, c, hv);
+        float y[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] = hv[j] * rstd * gv[j];
+        store_y<VEC>(op, row, c, y, inv);
+    };
+    if constexpr (kWide) {
+        for (int64_t i = 0; i < groups; ++i) {
+            const Cols<VEC> c(i, t, team, op.cols);
+            load_h<XT, VEC>(op, row, c, h[0]);
+            load_gamma<XT, VEC>(op.gamma, op.g, c, g[0]);
+            finish(c, h[0], g[0]);
         }
-        if (op.mode == TPGEMM_SCALE_MX) {  // a warp holds one block of 32 columns
-            const uint32_t code = mx_scale(__reduce_max_sync(0xffffffffu, abs_bits(y)), op.y, inv);
-            if ((threadIdx.x & 31) == 0 && c < op.cols)
-                static_cast<uint8_t*>(op.scale)[row * blocks + c / 32] = uint8_t(code);
-        }
-        if (c < op.cols) store_as(op.Y, op.y, yo + c, op.mode == TPGEMM_SCALE_NONE ? y : y * inv);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) finish(Cols<VEC>(i, t, team, op.cols), h[i], g[i]);
     }
 }
 
-__global__ void __launch_bounds__(kThreads) rmsnorm_grad_wide_kernel(RmsNormGradOp op) {
+// ---------------------------------------------------------------- gradients
+// Blocks walk the rows grid-stride, a team (a warp or the block) to a row, and
+// keep the columns' sums of dgamma in registers; partial[block] gets the
+// block's. Rows wider than a team's registers take the two kernels after this.
+template <typename XT, int V, bool VEC, bool WARP, int MAXT = 512>
+__global__ void __launch_bounds__(WARP ? 32 * kWarpRows : MAXT) rmsnorm_grad_kernel(const __grid_constant__ RmsNormGradOp op) {
+    __shared__ float2 s[2][32];
+    __shared__ float sum[WARP ? 8 * 32 * 8 * V : 1];
+    const int team = WARP ? 32 : int(blockDim.x);
+    const int t = WARP ? int(threadIdx.x & 31) : int(threadIdx.x);
+    const int64_t teams = WARP ? kWarpRows : 1;
+    grid_launch_dependents();
+    grid_dependency_wait();
+    float g[V][8], acc[V][8];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const Cols<VEC> c(i, t, team, op.cols);
+        if (op.dX) load_gamma<XT, VEC>(op.gamma, op.g, c, g[i]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[i][j] = 0.f;
+    }
+    int turn = 0;
+    for (int64_t row = int64_t(blockIdx.x) * teams + (WARP ? threadIdx.x >> 5 : 0); row < op.rows;
+         row += int64_t(gridDim.x) * teams, turn ^= 1) {
+        float dy[V][8], n[V][8];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const Cols<VEC> c(i, t, team, op.cols);
+            load_cols<XT, VEC>(op.dY, row * op.lddy, c, dy[i]);
+            load_cols<XT, VEC>(op.H, row * op.ldh, c, n[i]);
+        }
+        const float rstd = op.rstd[row];
+        float dot = 0.f;
+        uint32_t unused = 0;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                n[i][j] *= rstd;
+                acc[i][j] += dy[i][j] * n[i][j];
+                if (op.dX) {
+                    dy[i][j] *= g[i][j];
+                    dot += dy[i][j] * n[i][j];
+                }
+            }
+        if (!op.dX) continue;
+        team_sum_max<WARP>(dot, unused, s[turn]);
+        dot /= float(op.cols);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const Cols<VEC> c(i, t, team, op.cols);
+            float d[8];
+            if (op.dH) {
+                load_cols<XT, VEC>(op.dH, row * op.lddh, c, d);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) d[j] = 0.f;
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) d[j] += rstd * (dy[i][j] - n[i][j] * dot);
+            store_cols<XT, VEC>(op.dX, row * op.lddx, c, d);
+        }
+    }
+    if (!op.dgamma) return;
+    float* out = op.partial + int64_t(blockIdx.x) * op.cols;
+    if constexpr (WARP) {
+        const int w = threadIdx.x >> 5;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sum[((w * V + i) * 8 + j) * 32 + t] = acc[i][j];
+        __syncthreads();
+        // The warps' sums in order; warp w finishes the groups w, w + 8, ...
+        for (int k = w; k < V * 8; k += kWarpRows) {
+            float v = 0.f;
+#pragma unroll
+            for (int r = 0; r < kWarpRows; ++r) v += sum[(r * V * 8 + k) * 32 + t];
+            const Cols<VEC> c(k / 8, t, team, op.cols);
+            if (k % 8 < c.n) out[c.first + int64_t(k % 8) * c.step] = v;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) store_cols<float, VEC>(op.partial, int64_t(blockIdx.x) * op.cols,
+                                                           Cols<VEC>(i, t, team, op.cols), acc[i]);
+    }
+}
+
+template <typename XT>
+__device__ __forceinline__ float gamma_at(const RmsNormGradOp& op, int64_t c) {
+    return op.g == TPGEMM_ELEM_F32 ? static_cast<const float*>(op.gamma)[c]
+                                   : to_f32(static_cast<const XT*>(op.gamma)[c]);
+}
+
+constexpr int kWideThreads = 512;
+
+template <typename XT>
+__global__ void __launch_bounds__(kWideThreads) rmsnorm_grad_wide_kernel(const RmsNormGradOp op) {
+    __shared__ float2 s[32];
     const int64_t row = blockIdx.x;
-    const int64_t yo = row * op.lddy, ho = row * op.ldh, do_ = row * op.lddh, xo = row * op.lddx;
+    const XT* dy = static_cast<const XT*>(op.dY) + row * op.lddy;
+    const XT* h = static_cast<const XT*>(op.H) + row * op.ldh;
     const float rstd = op.rstd[row];
     float dot = 0.f;
     uint32_t unused = 0;
-    for (int64_t c = threadIdx.x; c < op.cols; c += kThreads)
-        dot += load_as(op.dY, op.x, yo + c) * load_as(op.gamma, op.g, c) *
-               (load_as(op.H, op.x, ho + c) * rstd);
-    block_sum_max(dot, unused);
+    for (int64_t c = threadIdx.x; c < op.cols; c += kWideThreads)
+        dot += to_f32(dy[c]) * gamma_at<XT>(op, c) * (to_f32(h[c]) * rstd);
+    team_sum_max<false>(dot, unused, s);
     dot /= float(op.cols);
-    for (int64_t c = threadIdx.x; c < op.cols; c += kThreads) {
-        const float n = load_as(op.H, op.x, ho + c) * rstd;
-        float d = rstd * (load_as(op.dY, op.x, yo + c) * load_as(op.gamma, op.g, c) - n * dot);
-        if (op.dH) d += load_as(op.dH, op.x, do_ + c);
-        store_as(op.dX, op.x, xo + c, d);
+    for (int64_t c = threadIdx.x; c < op.cols; c += kWideThreads) {
+        float d = rstd * (to_f32(dy[c]) * gamma_at<XT>(op, c) - to_f32(h[c]) * rstd * dot);
+        if (op.dH) d += to_f32(static_cast<const XT*>(op.dH)[row * op.lddh + c]);
+        static_cast<XT*>(op.dX)[row * op.lddx + c] = from_f32<XT>(d);
     }
 }
 
 // partial[strip][c] = sum over the strip's rows of dy h rstd.
-__global__ void __launch_bounds__(kThreads) rmsnorm_dgamma_kernel(RmsNormGradOp op, int strips) {
-    const int64_t c = int64_t(blockIdx.x) * kThreads + threadIdx.x;
+template <typename XT>
+__global__ void __launch_bounds__(256) rmsnorm_dgamma_kernel(const RmsNormGradOp op, int strips) {
+    const int64_t c = int64_t(blockIdx.x) * 256 + threadIdx.x;
     const int64_t begin = op.rows * blockIdx.y / strips, end = op.rows * (blockIdx.y + 1) / strips;
     if (c >= op.cols) return;
     float v = 0.f;
     for (int64_t r = begin; r < end; ++r)
-        v += load_as(op.dY, op.x, r * op.lddy + c) * (load_as(op.H, op.x, r * op.ldh + c) * op.rstd[r]);
+        v += to_f32(static_cast<const XT*>(op.dY)[r * op.lddy + c]) *
+             (to_f32(static_cast<const XT*>(op.H)[r * op.ldh + c]) * op.rstd[r]);
     op.partial[int64_t(blockIdx.y) * op.cols + c] = v;
+}
+
+// How a row is spread: threads of a team (a warp's rows come kWarpRows to a
+// block), groups of eight columns to a thread (0: wider than the registers).
+struct Spread {
+    int team, v;
+    bool warp;
+    int threads() const { return warp ? 32 * kWarpRows : team; }
+    int rows() const { return warp ? kWarpRows : 1; }
+};
+
+// Up to 512 columns a warp holds the row. Wider rows take one group to a thread
+// while that leaves the team at 512 threads or fewer, then two.
+Spread spread_of(int64_t rows, int64_t cols) {
+    const int64_t groups = (cols + 7) / 8;
+    if (groups <= 64) return {32, groups <= 32 ? 1 : 2, true};
+    if (cols > kMaxHeld) return {kMaxTeam, 0, false};
+    const bool one = groups <= 512 || (groups <= kMaxTeam && rows <= 152);
+    const int64_t per = one ? groups : (groups + 1) / 2;
+    return {int((per + 31) / 32 * 32), one ? 1 : 2, false};
+}
+
+bool rows_aligned(const void* p, int64_t ld, int64_t rows, int elem, int bytes) {
+    return !p || (reinterpret_cast<uintptr_t>(p) % bytes == 0 &&
+                  (rows <= 1 || (ld * elem_size(elem)) % bytes == 0));
+}
+
+template <typename XT, bool VEC>
+cudaError_t launch_norm(const RmsNormOp& op, cudaStream_t stream) {
+    const Spread s = spread_of(op.rows, op.cols);
+    const int64_t blocks = (op.rows + s.rows() - 1) / s.rows();
+    if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+    const dim3 grid{unsigned(blocks)}, block{unsigned(s.threads())};
+    auto fn = s.warp ? (s.v == 1 ? rmsnorm_kernel<XT, 1, VEC, true> : rmsnorm_kernel<XT, 2, VEC, true>)
+              : s.v == 0 ? rmsnorm_kernel<XT, 0, VEC, false>
+              : s.v == 1 ? rmsnorm_kernel<XT, 1, VEC, false>
+                         : rmsnorm_kernel<XT, 2, VEC, false>;
+    return launch_dependent(fn, grid, block, 0, stream, op);
+}
+
+template <typename XT>
+cudaError_t launch_norm_typed(const RmsNormOp& op, cudaStream_t stream) {
+    const bool vec = op.cols % 8 == 0 && rows_aligned(op.X, op.ldx, op.rows, op.x, 16) &&
+                     rows_aligned(op.R, op.ldr, op.rows, op.x, 16) &&
+                     rows_aligned(op.H, op.ldh, op.rows, op.x, 16) &&
+                     rows_aligned(op.Y, op.ldy, op.rows, op.y, elem_size(op.y) == 1 ? 8 : 16) &&
+                     rows_aligned(op.gamma, 0, 1, op.g, 16);
+    return vec ? launch_norm<XT, true>(op, stream) : launch_norm<XT, false>(op, stream);
+}
+
+// Blocks of the register kernel: enough to fill the GPU's threads, at most one
+// to a team's worth of rows.
+int grad_blocks(int64_t rows, const Spread& s) {
+    const int64_t most = (rows + s.rows() - 1) / s.rows();
+    const int64_t fill = 152 * (s.threads() <= 256 ? 4 : s.threads() <= 512 ? 2 : 1);
+    return int(most < fill ? (most < 1 ? 1 : most) : fill);
+}
+
+int wide_strips(int64_t rows) {
+    const int64_t most = (rows + 15) / 16;
+    return int(most < 1 ? 1 : (most < 64 ? most : 64));
+}
+
+// (Teams of more than 512 threads have 64 registers to a thread: a variant of
+// its own, so that the others are not held to that.)
+template <typename XT, bool VEC>
+void (*pick_grad(const Spread& s))(const RmsNormGradOp) {
+    if (s.warp) return s.v == 1 ? rmsnorm_grad_kernel<XT, 1, VEC, true> : rmsnorm_grad_kernel<XT, 2, VEC, true>;
+    if (s.team <= 512) return s.v == 1 ? rmsnorm_grad_kernel<XT, 1, VEC, false> : rmsnorm_grad_kernel<XT, 2, VEC, false>;
+    return s.v == 1 ? rmsnorm_grad_kernel<XT, 1, VEC, false, kMaxTeam> : rmsnorm_grad_kernel<XT, 2, VEC, false, kMaxTeam>;
+}
+
+template <typename XT>
+cudaError_t launch_grad_typed(const RmsNormGradOp& op, cudaStream_t stream) {
+    const Spread s = spread_of(op.rows, op.cols);
+    const int strips = rmsnorm_grad_strips(op.rows, op.cols);
+    cudaError_t e = cudaSuccess;
+    if (s.v == 0) {
+        // dgamma first: dX may be written over dY or H.
+        if (op.dgamma) {
+            const dim3 grid(unsigned((op.cols + 255) / 256), static_cast<unsigned>(strips));
+            rmsnorm_dgamma_kernel<XT><<<grid, 256, 0, stream>>>(op, strips);
+            e = cudaGetLastError();
+        }
+        if (e == cudaSuccess && op.dX) {
+            rmsnorm_grad_wide_kernel<XT><<<unsigned(op.rows), kWideThreads, 0, stream>>>(op);
+            e = cudaGetLastError();
+        }
+    } else {
+        const bool vec = op.cols % 8 == 0 && rows_aligned(op.dY, op.lddy, op.rows, op.x, 16) &&
+                         rows_aligned(op.H, op.ldh, op.rows, op.x, 16) &&
+                         rows_aligned(op.dH, op.lddh, op.rows, op.x, 16) &&
+                         rows_aligned(op.dX, op.lddx, op.rows, op.x, 16) &&
+                         rows_aligned(op.gamma, 0, 1, op.g, 16);
+        const dim3 grid{unsigned(strips)}, block{unsigned(s.threads())};
+        e = launch_dependent(vec ? pick_grad<XT, true>(s) : pick_grad<XT, false>(s), grid, block, 0,
+                             stream, op);
+    }
+    if (e != cudaSuccess || !op.dgamma) return e;
+    return launch_column_sum(op.partial, strips, op.cols, op.dgamma, op.grad, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_rmsnorm(const RmsNormOp& op, cudaStream_t stream) {
-    if (op.rows > 0x7fffffff) return cudaErrorInvalidValue;
-    rmsnorm_wide_kernel<<<unsigned(op.rows), kThreads, 0, stream>>>(op);
-    return cudaGetLastError();
+    if (op.x == TPGEMM_ELEM_F16) return launch_norm_typed<__half>(op, stream);
+    if (op.x == TPGEMM_ELEM_BF16) return launch_norm_typed<__nv_bfloat16>(op, stream);
+    return launch_norm_typed<float>(op, stream);
 }
 
 int rmsnorm_grad_strips(int64_t rows, int64_t cols) {
-    const int64_t most = (rows + 15) / 16;
-    return int(most < 1 ? 1 : (most < 152 ? most : 152));
+    const Spread s = spread_of(rows, cols);
+    return s.v == 0 ? wide_strips(rows) : grad_blocks(rows, s);
 }
 
 cudaError_t launch_rmsnorm_grad(const RmsNormGradOp& op, cudaStream_t stream) {
     if (op.rows > 0x7fffffff) return cudaErrorInvalidValue;
-    // dgamma first: dX may be written over dY or H.
-    if (op.dgamma) {
-        const int strips = rmsnorm_grad_strips(op.rows, op.cols);
-        const dim3 grid(unsigned((op.cols + kThreads - 1) / kThreads), static_cast<unsigned>(strips));
-        rmsnorm_dgamma_kernel<<<grid, kThreads, 0, stream>>>(op, strips);
-        cudaError_t e = cudaGetLastError();
-        if (e == cudaSuccess)
-            e = launch_column_sum(op.partial, strips, op.cols, op.dgamma, op.grad, stream);
-        if (e != cudaSuccess) return e;
-    }
-    if (op.dX && op.rows > 0) rmsnorm_grad_wide_kernel<<<unsigned(op.rows), kThreads, 0, stream>>>(op);
-    return cudaGetLastError();
+    if (op.x == TPGEMM_ELEM_F16) return launch_grad_typed<__half>(op, stream);
+    if (op.x == TPGEMM_ELEM_BF16) return launch_grad_typed<__nv_bfloat16>(op, stream);
+    return launch_grad_typed<float>(op, stream);
 }
 
 }  // namespace tpg
