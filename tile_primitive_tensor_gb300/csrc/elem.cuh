@@ -31,17 +31,33 @@ __device__ __forceinline__ T from_f32(float v) {
         return T(v);  // 8 bits: round to nearest even, saturating
 }
 
-// act(z). The exponentials are the hardware's (relative error near 2^-21, far
-// below a 16-bit output's rounding and about 8 ulp of a 32-bit one's).
+// The normal distribution's tail past |z|, given e = exp(-z^2 / 2): erfc(|z| /
+// sqrt 2) / 2 by the rational approximation 7.1.26 of Abramowitz and Stegun's
+// Handbook of Mathematical Functions (absolute error of erf below 1.5e-7; and
+// no cancellation for negative z). One branch-free evaluation for all lanes:
+// erff takes two paths that a warp has to go through both.
+__device__ __forceinline__ float normal_tail(float z, float e) {
+    const float t = __fdividef(1.f, 1.f + 0.3275911f * 0.70710678118654752f * fabsf(z));
+    const float s = t * (0.254829592f +
+                         t * (-0.284496736f + t * (1.421413741f + t * (-1.453152027f + t * 1.061405429f))));
+    return 0.5f * s * e;
+}
+
+// act(z). The exponentials and divisions are the hardware's (relative error near
+// 2^-21, far below a 16-bit output's rounding and about 8 ulp of a 32-bit
+// one's; a quotient by 2^126 or more is 0).
 template <int ACT>
 __device__ __forceinline__ float act_fwd(float z) {
     if constexpr (ACT == TPGEMM_ACT_RELU) return z > 0.f ? z : (z != z ? z : 0.f);
-    if constexpr (ACT == TPGEMM_ACT_SILU) return z / (1.f + __expf(-z));
-    if constexpr (ACT == TPGEMM_ACT_GELU) return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
+    if constexpr (ACT == TPGEMM_ACT_SILU) return __fdividef(z, 1.f + __expf(-z));
+    if constexpr (ACT == TPGEMM_ACT_GELU) {
+        const float q = normal_tail(z, __expf(-0.5f * z * z));
+        return z * (z > 0.f ? 1.f - q : q);
+    }
     if constexpr (ACT == TPGEMM_ACT_GELU_TANH) {
         // (1 + tanh u) / 2 = 1 / (1 + exp(-2 u)), u = sqrt(2/pi) (z + 0.044715 z^3)
         const float u2 = 1.5957691216057308f * (z + 0.044715f * z * z * z);
-        return z / (1.f + __expf(-u2));
+        return __fdividef(z, 1.f + __expf(-u2));
     }
     return z;
 }
@@ -51,16 +67,18 @@ template <int ACT>
 __device__ __forceinline__ float act_bwd(float z) {
     if constexpr (ACT == TPGEMM_ACT_RELU) return z > 0.f ? 1.f : 0.f;
     if constexpr (ACT == TPGEMM_ACT_SILU) {
-        const float s = 1.f / (1.f + __expf(-z));
+        const float s = __fdividef(1.f, 1.f + __expf(-z));
         return s * (1.f + z * (1.f - s));
     }
-    if constexpr (ACT == TPGEMM_ACT_GELU)
-        return 0.5f * (1.f + erff(z * 0.70710678118654752f)) +
-               z * 0.3989422804014327f * __expf(-0.5f * z * z);
+    if constexpr (ACT == TPGEMM_ACT_GELU) {
+        const float e = __expf(-0.5f * z * z);
+        const float q = normal_tail(z, e);
+        return (z > 0.f ? 1.f - q : q) + z * 0.3989422804014327f * e;
+    }
     if constexpr (ACT == TPGEMM_ACT_GELU_TANH) {
         const float z2 = z * z;
         const float u2 = 1.5957691216057308f * (z + 0.044715f * z * z2);
-        const float s = 1.f / (1.f + __expf(-u2));
+        const float s = __fdividef(1.f, 1.f + __expf(-u2));
         // d(z s)/dz with ds/dz = s (1 - s) d(2u)/dz
         return s + z * s * (1.f - s) * 1.5957691216057308f * (1.f + 0.134145f * z2);
     }

@@ -12,24 +12,26 @@ namespace {
 
 constexpr int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// CTA pairs that fit the device at once (all tile kernels hold the same shared
-// memory and threads), asked once per device.
-tpgemm_status max_pairs(const TcLinear& p, int* pairs) {
+// Clusters of the tile kernel that fit the device at once (all variants hold
+// the same threads and nearly all shared memory), asked once per device and
+// cluster size.
+tpgemm_status max_clusters(const TcLinear& p, int* clusters) {
     static std::mutex m;
-    static int cache[64] = {};
+    static int cache[64][2] = {};
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev < 0 || dev >= 64) return fail_with(TPGEMM_ERR_ARCH, "device index %d unsupported", dev);
     std::lock_guard<std::mutex> lock(m);
-    if (!cache[dev]) {
-        const cudaError_t e = tc_linear_max_pairs(p, &cache[dev]);
-        if (e != cudaSuccess || cache[dev] <= 0) {
-            cache[dev] = 0;
+    int& n = cache[dev][p.share ? 1 : 0];
+    if (!n) {
+        const cudaError_t e = tc_linear_max_clusters(p, &n);
+        if (e != cudaSuccess || n <= 0) {
+            n = 0;
             return fail_with(TPGEMM_ERR_LAUNCH, "cluster occupancy query failed: %s",
                              cudaGetErrorString(e));
         }
     }
-    *pairs = cache[dev];
+    *clusters = n;
     return TPGEMM_OK;
 }
 
@@ -42,7 +44,7 @@ constexpr double kStageNs = 340.0;  // 256 x 256 x (64 of 16 bits)
 
 struct Choice {
     double ns = 1e30;
-    int pair = 0, swap = 0, bn = 0, bp = 128, split = 1;
+    int pair = 0, swap = 0, bn = 0, bp = 128, split = 1, share = 0;
 };
 
 }  // namespace
@@ -55,6 +57,7 @@ bool tma_rows(const Operand& o, int64_t rows, int64_t K, int dtype) {
 
 namespace {
 
+// box_rows: rows of a K-contiguous box; K rows of a box along the operand's rows.
 tpgemm_status encode(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* map, const Operand& o,
                      int64_t rows, int64_t K, int dtype, int box_rows) {
     const int es = elem_size(dtype);
@@ -65,7 +68,7 @@ tpgemm_status encode(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* map, co
     cuuint64_t dims[2] = {inner, outer};
     // (A single line's pitch is never used, but has to be a multiple of 16.)
     cuuint64_t pitch[1] = {outer > 1 ? uint64_t(o.ld) * es : (inner * es + 15) / 16 * 16};
-    cuuint32_t box[2] = {cuuint32_t(128 / es), cuuint32_t(o.mn ? 64 : box_rows)};
+    cuuint32_t box[2] = {cuuint32_t(128 / es), cuuint32_t(box_rows)};
     cuuint32_t one[2] = {1, 1};
     const CUresult r = enc(map, t, 2, const_cast<void*>(o.p), dims, pitch, box, one,
                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -75,30 +78,58 @@ tpgemm_status encode(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* map, co
     return TPGEMM_OK;
 }
 
-bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
-
-// Whether eight neighbouring outputs can be moved with 16-byte accesses.
-bool vector_epilogue(const Epilogue& e) {
-    const int es = elem_size(e.out);
-    auto rows16 = [&](const void* p, int64_t ld) { return !p || (aligned16(p) && (ld * es) % 16 == 0); };
-    return rows16(e.Y, e.ldy) && rows16(e.Z, e.ldz) && rows16(e.R, e.ldr) && aligned16(e.bias) &&
-           aligned16(e.sw);
+// Y, Z or R: 32 x 32 boxes, staged in shared memory with the swizzle of their
+// 64- or 128-byte rows.
+tpgemm_status encode_out(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* map, const void* base,
+                         int64_t M, int64_t N, int64_t ld, int elem) {
+    const int es = elem_size(elem);
+    const CUtensorMapDataType t = es == 4                    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                  : elem == TPGEMM_ELEM_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                             : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    cuuint64_t dims[2] = {uint64_t(N), uint64_t(M)};
+    cuuint64_t pitch[1] = {M > 1 ? uint64_t(ld) * es : (uint64_t(N) * es + 15) / 16 * 16};
+    cuuint32_t box[2] = {32, 32}, one[2] = {1, 1};
+    const CUresult r = enc(map, t, 2, const_cast<void*>(base), dims, pitch, box, one,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           es == 4 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS)
+        return fail_with(TPGEMM_ERR_LAUNCH, "cuTensorMapEncodeTiled failed with CUresult %d", int(r));
+    return TPGEMM_OK;
 }
 
-// Time of the tile kernel: waves of 256 x bn tiles over the pairs, each K stage
-// at the tensor rate or at what an SM can take in.
-Choice plan_tile(const LinearOp& op, int64_t kb, int pairs, int bn_forced) {
+bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+// Whether every row of Y, Z and R starts on a 16-byte boundary.
+bool tma_outputs(const Epilogue& e, int64_t M) {
+    const int es = elem_size(e.out);
+    auto rows16 = [&](const void* p, int64_t ld) {
+        return !p || (aligned16(p) && (M <= 1 || (ld * es) % 16 == 0));
+    };
+    return rows16(e.Y, e.ldy) && rows16(e.Z, e.ldz) && rows16(e.R, e.ldr);
+}
+
+// Time of the tile kernel: waves of a cluster's tiles, each K stage at the
+// tensor rate or at what an SM can take in.
+Choice plan_tile(const LinearOp& op, int64_t kb, int sms, const LinearTuning& t) {
     Choice best;
-    for (int bn = 256; bn >= 32; bn -= 32) {
-        if (bn_forced > 0 && bn != bn_forced) continue;
-        const int64_t tiles = ceil_div(op.M, 256) * ceil_div(op.N, bn);
-        const double stage = std::max(kStageNs * bn / 256, (128 + bn / 2) * 128 / kSmBytes);
-        const double ns = 6000 + double(ceil_div(tiles, pairs)) * (double(kb) * stage + 500);
-        if (ns < best.ns) {
-            best.ns = ns;
-            best.pair = 1;
-            best.swap = 0;
-            best.bn = bn;
+    for (int share = kShareNone; share <= kShareP; ++share) {
+        if (t.share >= 0 && share != t.share) continue;
+        for (int bn = 256; bn >= 32; bn -= 32) {
+            if (t.bn > 0 && bn != t.bn) continue;
+            const int64_t tiles = ceil_div(op.M, share == kShareQ ? 512 : 256) *
+                                  ceil_div(op.N, share == kShareP ? 2 * bn : bn);
+            const int clusters = share ? sms / 4 : sms / 2;
+            const int rows = (share == kShareP ? 64 : 128) + bn / (share == kShareQ ? 4 : 2);
+            const double stage = std::max(kStageNs * bn / 256, rows * 128 / kSmBytes);
+            const double ns = 6000 + double(ceil_div(tiles, clusters)) * (double(kb) * stage + 500);
+            if (ns < best.ns) {
+                best.ns = ns;
+                best.pair = 1;
+                best.swap = 0;
+                best.bn = bn;
+                best.share = share;
+            }
         }
     }
     return best;
@@ -147,9 +178,9 @@ tpgemm_status run_linear_tc(const LinearOp& op, int sms, cudaStream_t stream) {
     p.bk = p.fp8 ? 128 : 64;
     p.k_blocks = int(ceil_div(op.K, p.bk));
     p.timeout_ns = wait_timeout_ns();
-    p.vec = vector_epilogue(op.e);
+    p.vec = aligned16(op.e.bias) && aligned16(op.e.sw);
     const Choice split = plan_split(op, p.k_blocks, sms, t);
-    Choice c = plan_tile(op, p.k_blocks, sms / 2, t.bn);
+    Choice c = plan_tile(op, p.k_blocks, sms, t);
     if (t.path == kLinearSplit || (t.path != kLinearTile && split.ns < c.ns)) c = split;
     if (c.bn == 0) return fail_with(TPGEMM_ERR_PATH, "the planner overrides leave no plan");
     p.pair = c.pair;
@@ -157,6 +188,8 @@ tpgemm_status run_linear_tc(const LinearOp& op, int sms, cudaStream_t stream) {
     p.bn = c.bn;
     p.bp = c.bp;
     p.split = c.split;
+    p.share = c.share;
+    p.tma_out = p.pair && tma_outputs(op.e, op.M);
     const Operand& P = p.swap ? op.b : op.a;
     const Operand& Q = p.swap ? op.a : op.b;
     p.Mp = p.swap ? op.N : op.M;
@@ -168,8 +201,9 @@ tpgemm_status run_linear_tc(const LinearOp& op, int sms, cudaStream_t stream) {
     const int q_rows = p.pair ? p.bn / 2 : p.bn;
     p.p_bytes = 16384;
     p.q_bytes = p.q_mn ? uint32_t((q_rows + 63) / 64) * 8192u : uint32_t(q_rows) * 128u;
-    const int64_t tiles_p = ceil_div(p.Mp, p.pair ? 256 : p.bp), tiles_q = ceil_div(p.Nq, p.bn);
-    if (tiles_p * tiles_q * p.split > 0x7fffffff)
+    const int64_t tiles_p = ceil_div(p.Mp, !p.pair ? p.bp : p.share == kShareQ ? 512 : 256);
+    const int64_t tiles_q = ceil_div(p.Nq, p.share == kShareP ? 2 * p.bn : p.bn);
+    if (tiles_p * tiles_q * p.split > 0x1fffffff)
         return fail_with(TPGEMM_ERR_SHAPE, "too many tiles");
     p.tiles_p = int(tiles_p);
     p.tiles_q = int(tiles_q);
@@ -177,12 +211,12 @@ tpgemm_status run_linear_tc(const LinearOp& op, int sms, cudaStream_t stream) {
     const size_t budget = size_t(kTcMaxSmem) - 1024 - 512;
     int grid;
     if (p.pair) {
-        p.stages = int(std::min<size_t>(8, budget / (p.p_bytes + p.q_bytes)));
-        p.group = 8;
-        int pairs = 0;
-        s = max_pairs(p, &pairs);
+        p.stages = int(std::min<size_t>(8, (budget - kTileStagingBytes) / (p.p_bytes + p.q_bytes)));
+        p.group = p.share == kShareQ ? 4 : 8;
+        int clusters = 0;
+        s = max_clusters(p, &clusters);
         if (s != TPGEMM_OK) return s;
-        grid = 2 * std::min(p.tiles, pairs);
+        grid = (p.share ? 4 : 2) * std::min(p.tiles, clusters);
     } else {
         p.stages = int(std::min<size_t>(12, budget / (p.p_bytes + p.q_bytes)));
         p.ring_bytes = uint32_t(p.stages) * (p.p_bytes + p.q_bytes);
@@ -191,12 +225,22 @@ tpgemm_status run_linear_tc(const LinearOp& op, int sms, cudaStream_t stream) {
         while (p.tmem_cols < 32 * ((p.bn + 31) / 32)) p.tmem_cols *= 2;
         grid = p.tiles * p.split;
     }
-    CUtensorMap mapP, mapQ;
-    s = encode(enc, &mapP, P, p.Mp, op.K, op.dtype, p.pair ? 128 : p.bp);
+    TcLinearMaps maps;
+    s = encode(enc, &maps.P, P, p.Mp, op.K, op.dtype,
+               P.mn ? 64 : !p.pair ? p.bp : p.share == kShareP ? 64 : 128);
     if (s != TPGEMM_OK) return s;
-    s = encode(enc, &mapQ, Q, p.Nq, op.K, op.dtype, q_rows);
+    s = encode(enc, &maps.Q, Q, p.Nq, op.K, op.dtype,
+               Q.mn ? (p.share == kShareQ ? 32 : 64) : p.share == kShareQ ? q_rows / 2 : q_rows);
     if (s != TPGEMM_OK) return s;
-    const cudaError_t e = launch_tc_linear(mapP, mapQ, p, grid, stream);
+    maps.Y = maps.Z = maps.R = maps.P;
+    if (p.tma_out) {
+        const Epilogue& o = op.e;
+        s = encode_out(enc, &maps.Y, o.Y, op.M, op.N, o.ldy, o.out);
+        if (s == TPGEMM_OK && o.Z) s = encode_out(enc, &maps.Z, o.Z, op.M, op.N, o.ldz, o.out);
+        if (s == TPGEMM_OK && o.R) s = encode_out(enc, &maps.R, o.R, op.M, op.N, o.ldr, o.out);
+        if (s != TPGEMM_OK) return s;
+    }
+    const cudaError_t e = launch_tc_linear(maps, p, grid, stream);
     if (e != cudaSuccess)
         return fail_with(TPGEMM_ERR_LAUNCH, "tcgen05 linear kernel launch: %s", cudaGetErrorString(e));
     return TPGEMM_OK;

@@ -47,6 +47,19 @@ __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, vol
     }
 }
 
+// CTA-pair TMA load into the same place of every CTA of the cluster in `mask`
+// (bit: rank); the bytes of each complete on the barrier at `bar`'s place in
+// the even CTA of that one's pair (bar is given in an even CTA).
+__device__ __forceinline__ void tma_load_2d_pair_multicast(void* dst, const CUtensorMap* map, uint32_t bar,
+                                                           int32_t x, int32_t y, uint16_t mask,
+                                                           uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        ".multicast::cluster.L2::cache_hint [%0], [%1, {%3, %4}], [%2], %5, %6;" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "h"(mask), "l"(policy)
+        : "memory");
+}
+
 // Four MMAs: one 128-byte-wide stage of K. dP / dQ: descriptor templates, the
 // stage's operand addresses and the address step of one MMA's K.
 template <bool PAIR, bool FP8>
@@ -76,10 +89,11 @@ __device__ __forceinline__ uint64_t operand_desc(int mn) {
 __device__ __forceinline__ uint32_t operand_step(int mn) { return mn ? 2048u : 32u; }
 
 // ---------------------------------------------------------------- epilogues
-__device__ __forceinline__ void act8(int act, float (&x)[8]) {
+template <int N>
+__device__ __forceinline__ void act_n(int act, float (&x)[N]) {
     with_act(act, [&](auto a) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = act_fwd<decltype(a)::value>(x[i]);
+        for (int i = 0; i < N; ++i) x[i] = act_fwd<decltype(a)::value>(x[i]);
     });
 }
 
@@ -105,7 +119,7 @@ __device__ __forceinline__ void epilogue_row8(const Epilogue& e, bool vec, int64
         for (int i = 0; i < 8; ++i) x[i] += t[i];
     }
     if (e.Z) store8<T>(e.Z, m * e.ldz + n, vec, cnt, x);
-    act8(e.act, x);
+    act_n(e.act, x);
     if (e.R) {
         load8<T>(e.R, m * e.ldr + n, vec, cnt, t);
 #pragma unroll
@@ -114,35 +128,91 @@ __device__ __forceinline__ void epilogue_row8(const Epilogue& e, bool vec, int64
     store8<T>(e.Y, m * e.ldy + n, vec, cnt, x);
 }
 
-// Up to 8 consecutive rows m.. of output column n, a column to a lane.
+// 32 columns of an output row, staged for a TMA store: a lane's row of the
+// warp's 32 x 32 tile, its 16-byte units placed by the store's swizzle (64
+// bytes to a row of 16-bit outputs, 128 to one of 32-bit ones).
 template <typename T>
-__device__ __forceinline__ void epilogue_col8(const Epilogue& e, int64_t m, int64_t M, int64_t n,
-                                              float sw, float bias, float (&x)[8]) {
+__device__ __forceinline__ uint4* staged_unit(uint8_t* buf, int lane, int u) {
+    if constexpr (sizeof(T) == 4)
+        return reinterpret_cast<uint4*>(buf + lane * 128) + (u ^ (lane & 7));
+    else
+        return reinterpret_cast<uint4*>(buf + lane * 64) + (u ^ ((lane >> 1) & 3));
+}
+
+template <typename T>
+__device__ __forceinline__ void stage_row32(uint8_t* buf, int lane, const float (&x)[32]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        if (e.sa && m + i < M) x[i] *= e.sa[m + i];
-        x[i] = x[i] * sw + bias;
-        if (e.Z && m + i < M) static_cast<T*>(e.Z)[(m + i) * e.ldz + n] = from_f32<T>(x[i]);
+    for (int g = 0; g < 4; ++g) {
+        float f[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = x[8 * g + i];
+        if constexpr (sizeof(T) == 4) {
+            *staged_unit<T>(buf, lane, 2 * g) = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]),
+                                                           __float_as_uint(f[2]), __float_as_uint(f[3]));
+            *staged_unit<T>(buf, lane, 2 * g + 1) = make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]),
+                                                               __float_as_uint(f[6]), __float_as_uint(f[7]));
+        } else {
+            *staged_unit<T>(buf, lane, g) = pack8<T>(f);
+        }
     }
-    act8(e.act, x);
+}
+
+template <typename T>
+__device__ __forceinline__ void add_staged32(uint8_t* buf, int lane, float (&x)[32]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        if (m + i >= M) continue;
-        if (e.R) x[i] += to_f32(static_cast<const T*>(e.R)[(m + i) * e.ldr + n]);
-        static_cast<T*>(e.Y)[(m + i) * e.ldy + n] = from_f32<T>(x[i]);
+    for (int g = 0; g < 4; ++g) {
+        float f[8];
+        if constexpr (sizeof(T) == 4) {
+            const uint4 a = *staged_unit<T>(buf, lane, 2 * g), b = *staged_unit<T>(buf, lane, 2 * g + 1);
+            f[0] = __uint_as_float(a.x); f[1] = __uint_as_float(a.y);
+            f[2] = __uint_as_float(a.z); f[3] = __uint_as_float(a.w);
+            f[4] = __uint_as_float(b.x); f[5] = __uint_as_float(b.y);
+            f[6] = __uint_as_float(b.z); f[7] = __uint_as_float(b.w);
+        } else {
+            unpack8<T>(*staged_unit<T>(buf, lane, g), f);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[8 * g + i] += f[i];
+    }
+}
+
+// x += / *= 32 consecutive elements at base[n], the same ones for every lane.
+template <typename T, bool MUL>
+__device__ __forceinline__ void apply_columns(const void* base, int64_t n, int64_t N, bool vec,
+                                              float (&x)[32]) {
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+        float f[8];
+        const int64_t left = N - (n + 8 * g);
+        load8<T>(base, n + 8 * g, vec && left >= 8, left < 8 ? int(left) : 8, f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[8 * g + i] = MUL ? x[8 * g + i] * f[i] : x[8 * g + i] + f[i];
     }
 }
 
 // ------------------------------------------------------------- tile kernel
 // 12 warps: 0 and 2 issue the TMA fills (every other one each), 1 the MMAs (of
-// the pair's even CTA) and owns tensor memory, 4..11 run the epilogue, two
-// warps to a lane quadrant taking alternate 32-column chunks.
+// a pair's even CTA) and owns tensor memory, 4..11 run the epilogue, two warps
+// to a lane quadrant taking alternate 32-column chunks.
+//
+// A cluster is one pair, or two pairs that share an operand tile: with
+// kShareQ they hold neighbouring P tiles and one Q tile, with kShareP one P
+// tile and neighbouring Q tiles. Each of the four CTAs then loads half of what
+// it needs of the shared tile and multicasts it to itself and to the CTA of
+// the other pair that needs the same half.
+//
+// Outputs whose rows start on 16-byte boundaries leave through a staging tile
+// and TMA stores; the residual comes in the same way, ahead of its use. Stores
+// straight from registers, 16 bytes to each of 32 rows, occupy the load/store
+// path for 32 cycles an instruction; they serve the other outputs.
 constexpr int kTileThreads = 384;
 constexpr int kTileEpiWarps = 8;
+constexpr int kStaging = 4096;  // staging bytes of an epilogue warp
 
 struct TileSmem {
     uint8_t* stages;
-    uint64_t *full, *empty, *acc_full, *acc_empty, *drain;
+    uint8_t* staging;
+    uint64_t *full, *empty, *acc_full, *acc_empty, *drain, *rbar;
     uint32_t* tmem_base;
     volatile int* abort;
 };
@@ -151,13 +221,15 @@ __device__ __forceinline__ TileSmem carve_tile(uint8_t* raw, const TcLinear& p) 
     TileSmem s;
     uint8_t* b = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     s.stages = b;
-    uint64_t* bars = reinterpret_cast<uint64_t*>(b + size_t(p.stages) * (p.p_bytes + p.q_bytes));
+    s.staging = b + size_t(p.stages) * (p.p_bytes + p.q_bytes);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(s.staging + kTileEpiWarps * kStaging);
     s.full = bars;
     s.empty = bars + p.stages;
     s.acc_full = bars + 2 * p.stages;
     s.acc_empty = s.acc_full + 2;
     s.drain = s.acc_empty + 2;
-    s.tmem_base = reinterpret_cast<uint32_t*>(s.drain + 1);
+    s.rbar = s.drain + 1;  // [epilogue warps][2] residual fills
+    s.tmem_base = reinterpret_cast<uint32_t*>(s.rbar + 2 * kTileEpiWarps);
     s.abort = reinterpret_cast<volatile int*>(s.tmem_base + 1);
     return s;
 }
@@ -175,29 +247,46 @@ __device__ __forceinline__ void tile_at(int T, const TcLinear& p, int& tp, int& 
     if (g & 1) tq = p.tiles_q - 1 - tq;
 }
 
-template <typename T, bool SWAP>
+__device__ __forceinline__ void load_box(void* dst, const CUtensorMap* map, uint32_t bar, int x, int y,
+                                         uint64_t pol, uint32_t mask) {
+    if (mask)
+        tma_load_2d_pair_multicast(dst, map, bar, x, y, uint16_t(mask), pol);
+    else
+        tma_load_2d_pair_hint(dst, map, bar, x, y, pol);
+}
+
+template <typename T>
 __global__ void __launch_bounds__(kTileThreads, 1)
     linear_tile_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_constant__ CUtensorMap mapQ,
-                       const __grid_constant__ TcLinear p) {
+                       const __grid_constant__ CUtensorMap mapY, const __grid_constant__ CUtensorMap mapZ,
+                       const __grid_constant__ CUtensorMap mapR, const __grid_constant__ TcLinear p) {
     extern __shared__ uint8_t smem_raw[];
     const TileSmem s = carve_tile(smem_raw, p);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = int(cluster_ctarank());
-    const int cid = blockIdx.x >> 1, ncl = gridDim.x >> 1;
+    const int csize = p.share ? 4 : 2;
+    const int pair = rank >> 1, half_id = rank & 1, leader = rank & ~1;
+    const int cid = blockIdx.x / csize, ncl = gridDim.x / csize;
     const uint32_t stage_bytes = p.p_bytes + p.q_bytes;
     const uint64_t tmo = p.timeout_ns;
     if (warp == 0 && lane == 0) {
         prefetch_tensormap(&mapP);
         prefetch_tensormap(&mapQ);
+        if (p.tma_out) {
+            prefetch_tensormap(&mapY);
+            if (p.e.Z) prefetch_tensormap(&mapZ);
+            if (p.e.R) prefetch_tensormap(&mapR);
+        }
         for (int i = 0; i < p.stages; ++i) {
             mbar_init(&s.full[i], 1);
-            mbar_init(&s.empty[i], 1);
+            mbar_init(&s.empty[i], p.share ? 2 : 1);  // every pair that reads the stage's fills
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s.acc_full[i], 1);
             mbar_init(&s.acc_empty[i], 2 * kTileEpiWarps);  // both CTAs' epilogue warps
         }
         mbar_init(s.drain, 1);
+        for (int i = 0; i < 2 * kTileEpiWarps; ++i) mbar_init(&s.rbar[i], 1);
         *s.abort = 0;
         fence_mbarrier_init();
     }
@@ -211,22 +300,27 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     grid_launch_dependents();
     const uint32_t tmem = *s.tmem_base;
     uint32_t issued_any = 0, issued_parity = 0;  // a producer's last fill of each stage
+    uint32_t rphase = 0, rpend = 0;  // residual fills: next parity, and in flight (bit: buffer)
 
     const int prod = warp == 0 ? 0 : (warp == 2 ? 1 : -1);
     if (prod >= 0 && lane == 0) {
         grid_dependency_wait();
         const uint64_t pol = l2_policy(2);  // panels are read again by later tiles
-        const int q_rows = p.bn / 2;
+        const int q_rows = p.bn / 2;        // of this CTA's half
         const int q_atoms = (q_rows + 63) / 64;
         const uint32_t tx = 2u * (p.p_bytes + (p.q_mn ? uint32_t(q_atoms) * kAtom : uint32_t(q_rows) * 128u));
+        const uint32_t both = 5u << half_id;  // the CTAs of both pairs that hold this half
+        const uint32_t mask_p = p.share == kShareP ? both : 0u, mask_q = p.share == kShareQ ? both : 0u;
         int stage = 0, turn = 0;
         uint32_t phase = 0;
         bool ok = true;
         for (int t = cid; ok && t < p.tiles; t += ncl) {
             int tp, tq;
             tile_at(t, p, tp, tq);
-            const int p0 = (2 * tp + rank) * 128;
-            const int q0 = tq * p.bn + rank * q_rows;
+            if (p.share == kShareQ) tp = 2 * tp + pair;
+            if (p.share == kShareP) tq = 2 * tq + pair;
+            const int p0 = (2 * tp + half_id) * 128;
+            const int q0 = tq * p.bn + half_id * q_rows;
             for (int kb = 0; kb < p.k_blocks; ++kb, turn ^= 1) {
                 if (turn == prod) {
                     if (!wait_bounded(&s.empty[stage], phase ^ 1u, s.abort, tmo)) {
@@ -236,19 +330,24 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     uint8_t* sp = s.stages + size_t(stage) * stage_bytes;
                     uint8_t* sq = sp + p.p_bytes;
                     const int k0 = kb * p.bk;
-                    const uint32_t fb = mapa_shared(smem_u32(&s.full[stage]), 0);
-                    if (rank == 0) mbar_arrive_expect_tx(&s.full[stage], tx);
-                    if (p.p_mn) {
-                        tma_load_2d_pair_hint(sp, &mapP, fb, p0, k0, pol);
-                        tma_load_2d_pair_hint(sp + kAtom, &mapP, fb, p0 + 64, k0, pol);
+                    const uint32_t fb = mapa_shared(smem_u32(&s.full[stage]), uint32_t(leader));
+                    if (half_id == 0) mbar_arrive_expect_tx(&s.full[stage], tx);
+                    if (mask_p) {  // 64 of the 128 rows
+                        load_box(sp + pair * kAtom, &mapP, fb, p.p_mn ? p0 + 64 * pair : k0,
+                                 p.p_mn ? k0 : p0 + 64 * pair, pol, mask_p);
+                    } else if (p.p_mn) {
+                        load_box(sp, &mapP, fb, p0, k0, pol, 0);
+                        load_box(sp + kAtom, &mapP, fb, p0 + 64, k0, pol, 0);
                     } else {
-                        tma_load_2d_pair_hint(sp, &mapP, fb, k0, p0, pol);
+                        load_box(sp, &mapP, fb, k0, p0, pol, 0);
                     }
-                    if (p.q_mn) {
+                    if (p.q_mn) {  // (shared: half of the K rows of each atom)
+                        const int kh = mask_q ? 32 * pair : 0;
                         for (int a = 0; a < q_atoms; ++a)
-                            tma_load_2d_pair_hint(sq + a * kAtom, &mapQ, fb, q0 + 64 * a, k0, pol);
+                            load_box(sq + a * kAtom + kh * 128, &mapQ, fb, q0 + 64 * a, k0 + kh, pol, mask_q);
                     } else {
-                        tma_load_2d_pair_hint(sq, &mapQ, fb, k0, q0, pol);
+                        const int rh = mask_q ? (q_rows / 2) * pair : 0;
+                        load_box(sq + rh * 128, &mapQ, fb, k0, q0 + rh, pol, mask_q);
                     }
                     issued_any |= 1u << stage;
                     issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
@@ -260,12 +359,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             }
         }
     }
-    if (warp == 1 && lane == 0 && rank == 0) {
+    if (warp == 1 && lane == 0 && half_id == 0) {
         const uint64_t dP = operand_desc(p.p_mn), dQ = operand_desc(p.q_mn);
         const uint32_t step_p = operand_step(p.p_mn), step_q = operand_step(p.q_mn);
         const uint32_t base = smem_u32(s.stages), p_bytes = p.p_bytes, idesc = p.idesc;
         const int nstages = p.stages, nk = p.k_blocks;
         const bool fp8 = p.fp8 != 0;
+        const uint16_t mine = uint16_t(3u << leader), readers = p.share ? uint16_t(15) : mine;
         int stage = 0, it = 0;
         uint32_t phase = 0;
         bool ok = true;
@@ -285,75 +385,170 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     issue_stage<true, true>(acc, dP, dQ, ap, ap + p_bytes, step_p, step_q, idesc, kb == 0);
                 else
                     issue_stage<true, false>(acc, dP, dQ, ap, ap + p_bytes, step_p, step_q, idesc, kb == 0);
-                tc_commit_pair_multicast(&s.empty[stage], 3);
+                tc_commit_pair_multicast(&s.empty[stage], readers);
                 if (++stage == nstages) {
                     stage = 0;
                     phase ^= 1u;
                 }
             }
-            if (ok) tc_commit_pair_multicast(&s.acc_full[b], 3);
+            if (ok) tc_commit_pair_multicast(&s.acc_full[b], mine);
         }
         tc_commit_pair(s.drain);
         wait_bounded(s.drain, 0, s.abort, tmo, true);
     }
     if (warp >= 4) {
         grid_dependency_wait();
-        const int quad = warp & 3, half = (warp - 4) >> 2;
+        const int ew = warp - 4, quad = warp & 3, half = ew >> 2;
         const uint32_t lanes = uint32_t(quad * 32) << 16;
-        const int chunks = p.bn / 32;
+        uint8_t* const staging = s.staging + ew * kStaging;
+        uint64_t* const rbar = s.rbar + 2 * ew;
+        constexpr int kBuf = 1024 * int(sizeof(T));           // one 32 x 32 tile
+        constexpr int kBufs = kStaging / kBuf;                // 2, or 1 of 32-bit outputs
+        const bool tma = p.tma_out != 0;
+        const bool staged_z = tma && p.e.Z;
+        const bool staged_r = tma && p.e.R && !p.e.Z;         // (with Z the buffers are taken)
+        const uint64_t pol = l2_policy(1);                    // outputs pass through once
         int it = 0;
         for (int t = cid; t < p.tiles; t += ncl, ++it) {
             int tp, tq;
             tile_at(t, p, tp, tq);
-            const int64_t pr = int64_t(2 * tp + rank) * 128 + quad * 32 + lane;
+            if (p.share == kShareQ) tp = 2 * tp + pair;
+            if (p.share == kShareP) tq = 2 * tq + pair;
+            const int64_t m0 = int64_t(2 * tp + half_id) * 128 + quad * 32, m = m0 + lane;
             const int64_t q0 = int64_t(tq) * p.bn;
             const int b = it & 1;
+            const bool live = m < p.Mp;
+            // This warp's chunks: columns c = 32 half, + 64, ... below limit.
+            const int limit = m0 < p.Mp ? int(max(int64_t(0), min(int64_t(p.bn), p.Nq - q0))) : 0;
+            auto fetch_r = [&](int c, int buf) {  // lane 0; the buffer's last store has been read
+                mbar_arrive_expect_tx(&rbar[buf], kBuf);
+                tma_load_2d_hint(staging + buf * kBuf, &mapR, &rbar[buf], int(q0) + c, int(m0), pol);
+            };
+            if (staged_r) {
+                if (lane == 0) bulk_wait_group_read<0>();
+                for (int j = 0; j < kBufs; ++j)
+                    if (32 * half + 64 * j < limit) {
+                        if (lane == 0) fetch_r(32 * half + 64 * j, j);
+                        rpend |= 1u << j;
+                    }
+                __syncwarp();
+            }
+            const float sa = live && p.e.sa ? p.e.sa[m] : 1.f;
             bool ok = wait_bounded(&s.acc_full[b], (it >> 1) & 1, s.abort, tmo);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tc_fence_after_sync();
-            const bool live = pr < p.Mp;
-            // Swapped: this lane's output column; normal: its output row.
-            const float sa = !SWAP && live && p.e.sa ? p.e.sa[pr] : 1.f;
-            const float sw = SWAP && live && p.e.sw ? p.e.sw[pr] : 1.f;
-            const float bias = SWAP && live && p.e.bias ? to_f32(static_cast<const T*>(p.e.bias)[pr]) : 0.f;
-            const int limit = int(min(int64_t(p.bn), p.Nq - q0));  // columns in the matrix
             const uint32_t acc = tmem + lanes + uint32_t(b * 256);
-            // 32-column chunks half, half + 2, ...
-            for (int c = 32 * half; c < limit; c += 64) {
-                uint32_t r[32];
-                tmem_ld_32x32b_x32(acc + uint32_t(c), r);
-                tmem_ld_wait(r);
-                if (live) {
+            int j = 0;
+            for (int c = 32 * half; c < limit; c += 64, j ^= kBufs - 1) {
+                float x[32];
+                {
+                    uint32_t r[32];
+                    tmem_ld_32x32b_x32(acc + uint32_t(c), r);
+                    tmem_ld_wait(r);
 #pragma unroll
-                    for (int g = 0; g < 4; ++g) {
-                        float x[8];
+                    for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(r[i]);
+                }
+                if (!tma) {
+                    if (live) {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(r[8 * g + i]);
-                        if constexpr (SWAP)
-                            epilogue_col8<T>(p.e, q0 + c + 8 * g, p.Nq, pr, sw, bias, x);
-                        else
-                            epilogue_row8<T>(p.e, p.vec, pr, q0 + c + 8 * g, p.Nq, sa, x);
+                        for (int g = 0; g < 4; ++g) {
+                            float y[8];
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) y[i] = x[8 * g + i];
+                            epilogue_row8<T>(p.e, false, m, q0 + c + 8 * g, p.Nq, sa, y);
+                        }
                     }
+                    __syncwarp();
+                    continue;
+                }
+                const int64_t n = q0 + c;
+                if (p.e.sa) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) x[i] *= sa;
+                }
+                if (p.e.sw) apply_columns<float, true>(p.e.sw, n, p.Nq, p.vec, x);
+                if (p.e.bias) apply_columns<T, false>(p.e.bias, n, p.Nq, p.vec, x);
+                uint8_t* buf = staging + j * kBuf;
+                if (staged_z) {
+                    // Two 16-bit buffers: Z's and Y's; one 32-bit buffer in turn.
+                    if (lane == 0) {
+                        if (kBufs == 2) bulk_wait_group_read<1>();
+                        else bulk_wait_group_read<0>();
+                    }
+                    __syncwarp();
+                    stage_row32<T>(staging, lane, x);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        tma_store_2d_hint(&mapZ, staging, int(n), int(m0), pol);
+                        bulk_commit_group();
+                    }
+                    buf = staging + (kBufs - 1) * kBuf;
+                }
+                act_n(p.e.act, x);
+                if (staged_r) {
+                    bool rok = wait_bounded(&rbar[j], (rphase >> j) & 1u, s.abort, tmo);
+                    ok = __all_sync(0xffffffffu, rok);
+                    if (!ok) break;
+                    rphase ^= 1u << j;
+                    rpend &= ~(1u << j);
+                    add_staged32<T>(buf, lane, x);
+                } else {
+                    if (p.e.R && live) {
+#pragma unroll
+                        for (int g = 0; g < 4; ++g) {
+                            float f[8];
+                            const int64_t left = p.Nq - (n + 8 * g);
+                            load8<T>(p.e.R, m * p.e.ldr + n + 8 * g, left >= 8, left < 8 ? int(left) : 8, f);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) x[8 * g + i] += f[i];
+                        }
+                    }
+                    // The buffer's last store has been read (with Z: all but Z's).
+                    if (lane == 0) {
+                        if (kBufs == 2) bulk_wait_group_read<1>();
+                        else bulk_wait_group_read<0>();
+                    }
+                    __syncwarp();
+                }
+                stage_row32<T>(buf, lane, x);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    tma_store_2d_hint(&mapY, buf, int(n), int(m0), pol);
+                    bulk_commit_group();
+                }
+                if (staged_r && c + 64 * kBufs < limit) {
+                    if (lane == 0) {
+                        bulk_wait_group_read<0>();
+                        fetch_r(c + 64 * kBufs, j);
+                    }
+                    rpend |= 1u << j;
                 }
                 __syncwarp();
             }
             tc_fence_before_sync();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&s.acc_empty[b]), 0));
+            if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&s.acc_empty[b]), uint32_t(leader)));
+            if (!ok) break;
         }
+        if (lane == 0) bulk_wait_group_read<0>();
+        if (*s.abort)
+            for (int j = 0; j < 2; ++j)
+                if (rpend & (1u << j)) wait_bounded(&rbar[j], (rphase >> j) & 1u, s.abort, tmo, true);
     }
     tc_fence_before_sync();
     __syncthreads();
     if (*s.abort) {
         // Both CTAs' fills complete on the even CTA's barriers.
-        if (prod >= 0 && lane == 0 && rank == 0)
+        if (prod >= 0 && lane == 0 && half_id == 0)
             for (int i = 0; i < p.stages; ++i)
                 if (issued_any & (1u << i))
                     wait_bounded(&s.full[i], (issued_parity >> i) & 1u, s.abort, tmo, true);
         __syncthreads();
     }
-    cluster_sync();  // no CTA leaves while its peer may still reach its barriers
+    cluster_sync();  // no CTA leaves while a peer may still reach its barriers
     if (warp == 1) {
         __syncwarp();
         tc_fence_after_sync();
@@ -542,41 +737,59 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
     }
 }
 
-using TcFn = void (*)(CUtensorMap, CUtensorMap, TcLinear);
+using TileFn = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, TcLinear);
+using SplitFn = void (*)(CUtensorMap, CUtensorMap, TcLinear);
+
+TileFn pick_tile(const TcLinear& p) {
+    return p.e.out == TPGEMM_ELEM_F16    ? linear_tile_kernel<__half>
+           : p.e.out == TPGEMM_ELEM_BF16 ? linear_tile_kernel<__nv_bfloat16>
+                                         : linear_tile_kernel<float>;
+}
 
 template <typename T>
-TcFn pick_typed(const TcLinear& p) {
-    if (p.pair) return p.swap ? linear_tile_kernel<T, true> : linear_tile_kernel<T, false>;
+SplitFn pick_split_typed(const TcLinear& p) {
     return p.swap ? linear_split_kernel<T, true> : linear_split_kernel<T, false>;
 }
 
-TcFn pick(const TcLinear& p) {
-    if (p.e.out == TPGEMM_ELEM_F16) return pick_typed<__half>(p);
-    if (p.e.out == TPGEMM_ELEM_BF16) return pick_typed<__nv_bfloat16>(p);
-    return pick_typed<float>(p);
+SplitFn pick_split(const TcLinear& p) {
+    return p.e.out == TPGEMM_ELEM_F16    ? pick_split_typed<__half>(p)
+           : p.e.out == TPGEMM_ELEM_BF16 ? pick_split_typed<__nv_bfloat16>(p)
+                                         : pick_split_typed<float>(p);
+}
+
+int cluster_of(const TcLinear& p) { return p.pair ? (p.share ? 4 : 2) : p.split; }
+
+void set_cluster(cudaLaunchAttribute& a, int n) {
+    a.id = cudaLaunchAttributeClusterDimension;
+    a.val.clusterDim.x = unsigned(n);
+    a.val.clusterDim.y = 1;
+    a.val.clusterDim.z = 1;
 }
 
 }  // namespace
 
 size_t tc_linear_smem(const TcLinear& p) {
-    const size_t ring = p.pair ? size_t(p.stages) * (p.p_bytes + p.q_bytes) : size_t(p.ring_bytes);
-    return 1024 + ring + 8 * (2 * size_t(p.stages) + 5) + 16;
+    if (p.pair)
+        return 1024 + size_t(p.stages) * (p.p_bytes + p.q_bytes) + kTileEpiWarps * kStaging +
+               8 * (2 * size_t(p.stages) + 5 + 2 * kTileEpiWarps) + 16;
+    return 1024 + size_t(p.ring_bytes) + 8 * (2 * size_t(p.stages) + 1) + 16;
 }
 
-cudaError_t launch_tc_linear(const CUtensorMap& mapP, const CUtensorMap& mapQ, const TcLinear& p,
-                             int grid, cudaStream_t stream) {
-    const int cluster = p.pair ? 2 : p.split;
-    if (p.stages < 2 || p.stages > 32 || grid % cluster != 0 || p.bn % 16 != 0 || p.bn > 256 ||
+cudaError_t launch_tc_linear(const TcLinearMaps& maps, const TcLinear& p, int grid, cudaStream_t stream) {
+    const int cluster = cluster_of(p);
+    if (p.stages < 2 || p.stages > 32 || cluster < 1 || cluster > 8 || grid % cluster != 0 ||
+        p.bn % 16 != 0 || p.bn > 256 ||
         (p.pair && (p.bn % 32 != 0 || p.group < 1)) ||
-        (!p.pair && (p.bp > 128 || p.bp % 16 != 0 || p.split < 1 || p.split > 8 ||
-                     p.split > p.k_blocks ||
+        (!p.pair && (p.bp > 128 || p.bp % 16 != 0 || p.split > p.k_blocks ||
                      size_t(p.bn) * kPad * 4 > p.ring_bytes ||
                      size_t(p.stages) * (p.p_bytes + p.q_bytes) > p.ring_bytes)))
         return cudaErrorInvalidValue;
     const size_t smem = tc_linear_smem(p);
     if (smem > size_t(kTcMaxSmem)) return cudaErrorInvalidConfiguration;
-    const TcFn fn = pick(p);
-    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcMaxSmem);
+    const TileFn tile = pick_tile(p);
+    const SplitFn split = pick_split(p);
+    cudaError_t e = p.pair ? cudaFuncSetAttribute(tile, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcMaxSmem)
+                           : cudaFuncSetAttribute(split, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcMaxSmem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(grid));
@@ -586,31 +799,26 @@ cudaError_t launch_tc_linear(const CUtensorMap& mapP, const CUtensorMap& mapQ, c
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = unsigned(cluster);
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
+    set_cluster(attr[1], cluster);
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, fn, mapP, mapQ, p);
+    if (p.pair) return cudaLaunchKernelEx(&cfg, tile, maps.P, maps.Q, maps.Y, maps.Z, maps.R, p);
+    return cudaLaunchKernelEx(&cfg, split, maps.P, maps.Q, p);
 }
 
-cudaError_t tc_linear_max_pairs(const TcLinear& p, int* pairs) {
-    const TcFn fn = pick(p);
+cudaError_t tc_linear_max_clusters(const TcLinear& p, int* clusters) {
+    const TileFn fn = pick_tile(p);
     cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcMaxSmem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2);
+    cfg.gridDim = dim3(unsigned(cluster_of(p)));
     cfg.blockDim = dim3(kTileThreads);
     cfg.dynamicSmemBytes = tc_linear_smem(p);
     cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
+    set_cluster(attr[0], cluster_of(p));
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaOccupancyMaxActiveClusters(pairs, fn, &cfg);
+    return cudaOccupancyMaxActiveClusters(clusters, fn, &cfg);
 }
 
 cudaError_t linear_read_and_clear_status(int* status) {

@@ -9,7 +9,7 @@ struct TcLinear {
     Epilogue e;
     int64_t Mp, Nq;        // rows of P and of Q
     uint64_t timeout_ns;   // bound of every wait
-    int tiles_p, tiles_q;  // tiles along P (tile kernel: of a pair's 256 rows) and Q
+    int tiles_p, tiles_q;  // a cluster's tiles along P and Q
     int tiles;             // tile kernel: their number
     int k_blocks, bk;      // 128-byte-wide K stages, and K elements of each
     int bp, bn;            // P rows of a split tile; Q rows of a tile
@@ -20,18 +20,26 @@ struct TcLinear {
     uint32_t idesc;
     int tmem_cols;         // split kernel
     int split;             // split kernel: CTAs of a cluster, each a share of K
-    int group;             // tile kernel: P tiles of a raster run
+    int group;             // tile kernel: P tiles (of a cluster) in a raster run
+    int share;             // tile kernel: what a cluster's two pairs share (0: one pair)
+    int tma_out;           // tile kernel: Y, Z and R move by TMA (rows on 16-byte boundaries)
     int swap;              // P holds the output's columns
     int pair;              // tile kernel (1) or split kernel (0)
     int fp8;
-    int vec;               // 16-byte aligned rows of Y, Z, R (and dense bias, scale_w)
+    int vec;               // bias and scale_w start on 16-byte boundaries
+};
+enum { kShareNone = 0, kShareQ = 1, kShareP = 2 };
+
+struct TcLinearMaps {
+    CUtensorMap P, Q;     // operands
+    CUtensorMap Y, Z, R;  // tile kernel with tma_out: 32 x 32 boxes
 };
 
 size_t tc_linear_smem(const TcLinear& p);
-cudaError_t launch_tc_linear(const CUtensorMap& mapP, const CUtensorMap& mapQ, const TcLinear& p,
-                             int grid, cudaStream_t stream);
-// CTA pairs of the tile kernel that fit the device at once.
-cudaError_t tc_linear_max_pairs(const TcLinear& p, int* pairs);
+cudaError_t launch_tc_linear(const TcLinearMaps& maps, const TcLinear& p, int grid, cudaStream_t stream);
+// Clusters of the tile kernel that fit the device at once.
+cudaError_t tc_linear_max_clusters(const TcLinear& p, int* clusters);
+constexpr size_t kTileStagingBytes = 8 * 4096;  // of the epilogue's warps
 cudaError_t linear_read_and_clear_status(int* status);
 
 }  // namespace tpg
