@@ -60,33 +60,79 @@ __device__ __forceinline__ void tma_load_2d_pair_multicast(void* dst, const CUte
         : "memory");
 }
 
-// Four MMAs: one 128-byte-wide stage of K. dP / dQ: descriptor templates, the
-// stage's operand addresses and the address step of one MMA's K.
-template <bool PAIR, bool FP8>
-__device__ __forceinline__ void issue_stage(uint32_t acc, uint64_t dP, uint64_t dQ, uint32_t ap,
-                                            uint32_t aq, uint32_t step_p, uint32_t step_q,
-                                            uint32_t idesc, bool first) {
-#pragma unroll
-    for (int kk = 0; kk < 4; ++kk) {
-        const uint64_t a = smem_desc_with_addr(dP, ap + kk * step_p);
-        const uint64_t b = smem_desc_with_addr(dQ, aq + kk * step_q);
-        const uint32_t more = !first || kk != 0;
-        if constexpr (PAIR) {
-            if constexpr (FP8) tc_mma_f8_pair(acc, a, b, idesc, more);
-            else tc_mma_f16_pair(acc, a, b, idesc, more);
-        } else {
-            if constexpr (FP8) tc_mma_f8(acc, a, b, idesc, more);
-            else tc_mma_f16(acc, a, b, idesc, more);
-        }
+// Four MMAs, one 128-byte-wide stage of K, and their commit to `bar`, issued by
+// one thread that the warp elects. The whole warp runs this, convergent, with
+// the same values: descriptors, addresses and flags then live in uniform
+// registers, where the MMA takes them from. (Under a one-lane branch each MMA's
+// operands are moved there one by one, which cost about 135 cycles an MMA, more
+// than the 128 it computes for at 256 x 256: 4096^3 bf16 88 us against 74.)
+// a, b: descriptors of the stage's operands; step_a, step_b: their step for one
+// MMA's K. mask: the CTAs whose barrier the commit reaches (pair form).
+#define TPG_STAGE_ASM(KIND, CG, COMMIT)                                                   \
+    asm volatile(                                                                         \
+        "{\n\t.reg .pred e, p, t;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"                \
+        "elect.sync _|e, 0xffffffff;\n\t"                                                 \
+        "setp.ne.b32 p, %6, 0;\n\t"                                                       \
+        "setp.eq.b32 t, 0, 0;\n\t"                                                        \
+        "add.u64 a1, %1, %3;\n\tadd.u64 b1, %2, %4;\n\t"                                  \
+        "add.u64 a2, a1, %3;\n\tadd.u64 b2, b1, %4;\n\t"                                  \
+        "add.u64 a3, a2, %3;\n\tadd.u64 b3, b2, %4;\n\t"                                  \
+        "@e tcgen05.mma.cta_group::" CG ".kind::" KIND " [%0], %1, %2, %5, p;\n\t"        \
+        "@e tcgen05.mma.cta_group::" CG ".kind::" KIND " [%0], a1, b1, %5, t;\n\t"        \
+        "@e tcgen05.mma.cta_group::" CG ".kind::" KIND " [%0], a2, b2, %5, t;\n\t"        \
+        "@e tcgen05.mma.cta_group::" CG ".kind::" KIND " [%0], a3, b3, %5, t;\n\t"        \
+        "@e " COMMIT "\n\t}" ::"r"(acc),                                                  \
+        "l"(a), "l"(b), "l"(step_a), "l"(step_b), "r"(idesc), "r"(more), "r"(bar), "h"(mask) \
+        : "memory")
+
+template <bool PAIR>
+__device__ __forceinline__ void issue_stage(bool fp8, uint32_t acc, uint64_t a, uint64_t b,
+                                            uint64_t step_a, uint64_t step_b, uint32_t idesc,
+                                            uint32_t more, uint32_t bar, uint16_t mask) {
+    if constexpr (PAIR) {
+        if (fp8)
+            TPG_STAGE_ASM("f8f6f4", "2",
+                          "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster"
+                          ".multicast::cluster.b64 [%7], %8;");
+        else
+            TPG_STAGE_ASM("f16", "2",
+                          "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster"
+                          ".multicast::cluster.b64 [%7], %8;");
+    } else {
+        if (fp8)
+            TPG_STAGE_ASM("f8f6f4", "1",
+                          "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%7];");
+        else
+            TPG_STAGE_ASM("f16", "1",
+                          "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%7];");
     }
+}
+#undef TPG_STAGE_ASM
+
+// Commits of the elected thread's MMAs (the whole warp, convergent).
+__device__ __forceinline__ void commit_elected(uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+            smem_u32(bar))
+        : "memory");
+}
+
+__device__ __forceinline__ void commit_elected_pair(uint64_t* bar, uint16_t mask) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+        " [%0], %1;\n\t}" ::"r"(smem_u32(bar)),
+        "h"(mask)
+        : "memory");
 }
 
 __device__ __forceinline__ uint64_t operand_desc(int mn) {
     return mn ? smem_desc_sw128_template(kAtom, 1024) : smem_desc_sw128_template(16, 1024);
 }
-// Address step of one MMA's K (32 bytes of a K-contiguous row; 16 rows of 128
-// bytes of an operand stored along its rows).
-__device__ __forceinline__ uint32_t operand_step(int mn) { return mn ? 2048u : 32u; }
+// Descriptor step (16-byte units) of one MMA's K: 32 bytes of a K-contiguous
+// row; 16 rows of 128 bytes of an operand stored along its rows.
+__device__ __forceinline__ uint64_t operand_step(int mn) { return mn ? 128u : 2u; }
 
 // ---------------------------------------------------------------- epilogues
 template <int N>
@@ -359,10 +405,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             }
         }
     }
-    if (warp == 1 && lane == 0 && half_id == 0) {
-        const uint64_t dP = operand_desc(p.p_mn), dQ = operand_desc(p.q_mn);
-        const uint32_t step_p = operand_step(p.p_mn), step_q = operand_step(p.q_mn);
-        const uint32_t base = smem_u32(s.stages), p_bytes = p.p_bytes, idesc = p.idesc;
+    if (warp == 1 && half_id == 0) {
+        const uint64_t dP = smem_desc_with_addr(operand_desc(p.p_mn), smem_u32(s.stages));
+        const uint64_t dQ = smem_desc_with_addr(operand_desc(p.q_mn), smem_u32(s.stages) + p.p_bytes);
+        const uint64_t step_p = operand_step(p.p_mn), step_q = operand_step(p.q_mn);
+        const uint32_t idesc = p.idesc, stage_units = stage_bytes >> 4;
+        const uint32_t empty0 = smem_u32(s.empty);
         const int nstages = p.stages, nk = p.k_blocks;
         const bool fp8 = p.fp8 != 0;
         const uint16_t mine = uint16_t(3u << leader), readers = p.share ? uint16_t(15) : mine;
@@ -371,29 +419,27 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         bool ok = true;
         for (int t = cid; ok && t < p.tiles; t += ncl, ++it) {
             const int b = it & 1;
-            if (!wait_bounded(&s.acc_empty[b], ((it >> 1) & 1) ^ 1u, s.abort, tmo)) break;
+            if (!__all_sync(0xffffffffu, wait_bounded(&s.acc_empty[b], ((it >> 1) & 1) ^ 1u, s.abort, tmo)))
+                break;
             tc_fence_after_sync();
             const uint32_t acc = tmem + uint32_t(b) * 256u;
             for (int kb = 0; kb < nk; ++kb) {
-                if (!wait_bounded(&s.full[stage], phase, s.abort, tmo)) {
+                if (!__all_sync(0xffffffffu, wait_bounded(&s.full[stage], phase, s.abort, tmo))) {
                     ok = false;
                     break;
                 }
                 tc_fence_after_sync();
-                const uint32_t ap = base + uint32_t(stage) * stage_bytes;
-                if (fp8)
-                    issue_stage<true, true>(acc, dP, dQ, ap, ap + p_bytes, step_p, step_q, idesc, kb == 0);
-                else
-                    issue_stage<true, false>(acc, dP, dQ, ap, ap + p_bytes, step_p, step_q, idesc, kb == 0);
-                tc_commit_pair_multicast(&s.empty[stage], readers);
+                const uint64_t off = uint64_t(uint32_t(stage) * stage_units);
+                issue_stage<true>(fp8, acc, dP + off, dQ + off, step_p, step_q, idesc, kb != 0,
+                                  empty0 + 8u * uint32_t(stage), readers);
                 if (++stage == nstages) {
                     stage = 0;
                     phase ^= 1u;
                 }
             }
-            if (ok) tc_commit_pair_multicast(&s.acc_full[b], mine);
+            if (ok) commit_elected_pair(&s.acc_full[b], mine);
         }
-        tc_commit_pair(s.drain);
+        commit_elected_pair(s.drain, uint16_t(1u << rank));
         wait_bounded(s.drain, 0, s.abort, tmo, true);
     }
     if (warp >= 4) {
@@ -655,30 +701,29 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
                 phase ^= 1u;
             }
         }
-    } else if (warp == 1 && lane == 0) {
-        const uint64_t dP = operand_desc(p.p_mn), dQ = operand_desc(p.q_mn);
-        const uint32_t step_p = operand_step(p.p_mn), step_q = operand_step(p.q_mn);
-        const uint32_t base = smem_u32(s.stages), p_bytes = p.p_bytes, idesc = p.idesc;
+    } else if (warp == 1) {
+        const uint64_t dP = smem_desc_with_addr(operand_desc(p.p_mn), smem_u32(s.stages));
+        const uint64_t dQ = smem_desc_with_addr(operand_desc(p.q_mn), smem_u32(s.stages) + p.p_bytes);
+        const uint64_t step_p = operand_step(p.p_mn), step_q = operand_step(p.q_mn);
+        const uint32_t idesc = p.idesc, stage_units = stage_bytes >> 4;
+        const uint32_t empty0 = smem_u32(s.empty);
         const int nstages = p.stages;
         const bool fp8 = p.fp8 != 0;
         int stage = 0;
         uint32_t phase = 0;
         for (int kb = kb0; kb < kb1; ++kb) {
-            if (!wait_bounded(&s.full[stage], phase, s.abort, tmo)) break;
+            if (!__all_sync(0xffffffffu, wait_bounded(&s.full[stage], phase, s.abort, tmo))) break;
             tc_fence_after_sync();
-            const uint32_t ap = base + uint32_t(stage) * stage_bytes;
-            if (fp8)
-                issue_stage<false, true>(tmem, dP, dQ, ap, ap + p_bytes, step_p, step_q, idesc, kb == kb0);
-            else
-                issue_stage<false, false>(tmem, dP, dQ, ap, ap + p_bytes, step_p, step_q, idesc, kb == kb0);
-            tc_commit(&s.empty[stage]);
+            const uint64_t off = uint64_t(uint32_t(stage) * stage_units);
+            issue_stage<false>(fp8, tmem, dP + off, dQ + off, step_p, step_q, idesc, kb != kb0,
+                               empty0 + 8u * uint32_t(stage), 0);
             if (++stage == nstages) {
                 stage = 0;
                 phase ^= 1u;
             }
         }
         // Complete once every MMA issued is (also after a wait gave up).
-        tc_commit(s.acc_full);
+        commit_elected(s.acc_full);
     }
     __syncwarp();
     // Every warp waits for the MMAs before it may read tensor memory, reuse the
