@@ -208,7 +208,7 @@ tpgemm_status run_linear_tc(const LinearOp& op, int sms, cudaStream_t stream) {
     p.tiles_p = int(tiles_p);
     p.tiles_q = int(tiles_q);
     p.tiles = int(tiles_p * tiles_q);
-    const size_t budget = size_t(kTcMaxSmem) - 1024 - 512;
+    const size_t budget = size_t(kTcMaxSmem) - 512;  // (barriers)
     int grid;
     if (p.pair) {
         p.stages = int(std::min<size_t>(8, (budget - kTileStagingBytes) / (p.p_bytes + p.q_bytes)));

@@ -139,7 +139,8 @@ template <int N>
 __device__ __forceinline__ void act_n(int act, float (&x)[N]) {
     with_act(act, [&](auto a) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) x[i] = act_fwd<decltype(a)::value>(x[i]);
+        for (int i = 0; i < N; i += 2)
+            split(act_fwd<decltype(a)::value>(f2(x[i], x[i + 1])), x[i], x[i + 1]);
     });
 }
 
@@ -222,17 +223,14 @@ __device__ __forceinline__ void add_staged32(uint8_t* buf, int lane, float (&x)[
     }
 }
 
-// x += / *= 32 consecutive elements at base[n], the same ones for every lane.
-template <typename T, bool MUL>
-__device__ __forceinline__ void apply_columns(const void* base, int64_t n, int64_t N, bool vec,
-                                              float (&x)[32]) {
+// x += / *= the 32 values that the lanes hold, one to a column.
+template <bool MUL>
+__device__ __forceinline__ void apply_columns(float v, float (&x)[32]) {
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-        float f[8];
-        const int64_t left = N - (n + 8 * g);
-        load8<T>(base, n + 8 * g, vec && left >= 8, left < 8 ? int(left) : 8, f);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[8 * g + i] = MUL ? x[8 * g + i] * f[i] : x[8 * g + i] + f[i];
+    for (int i = 0; i < 32; i += 2) {
+        const F2 a = f2(x[i], x[i + 1]);
+        const F2 c = f2(__shfl_sync(0xffffffffu, v, i), __shfl_sync(0xffffffffu, v, i + 1));
+        split(MUL ? mul(a, c) : add(a, c), x[i], x[i + 1]);
     }
 }
 
@@ -254,10 +252,12 @@ __device__ __forceinline__ void apply_columns(const void* base, int64_t n, int64
 constexpr int kTileThreads = 384;
 constexpr int kTileEpiWarps = 8;
 constexpr int kStaging = 4096;  // staging bytes of an epilogue warp
+constexpr int kBiasBytes = 256;
 
 struct TileSmem {
     uint8_t* stages;
     uint8_t* staging;
+    uint8_t* bias;  // [epilogue warps][128] 16-bit bias of the warp's columns
     uint64_t *full, *empty, *acc_full, *acc_empty, *drain, *rbar;
     uint32_t* tmem_base;
     volatile int* abort;
@@ -265,10 +265,11 @@ struct TileSmem {
 
 __device__ __forceinline__ TileSmem carve_tile(uint8_t* raw, const TcLinear& p) {
     TileSmem s;
-    uint8_t* b = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* b = raw;  // 1024-byte aligned
     s.stages = b;
     s.staging = b + size_t(p.stages) * (p.p_bytes + p.q_bytes);
-    uint64_t* bars = reinterpret_cast<uint64_t*>(s.staging + kTileEpiWarps * kStaging);
+    s.bias = s.staging + kTileEpiWarps * kStaging;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(s.bias + kTileEpiWarps * kBiasBytes);
     s.full = bars;
     s.empty = bars + p.stages;
     s.acc_full = bars + 2 * p.stages;
@@ -306,7 +307,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     linear_tile_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_constant__ CUtensorMap mapQ,
                        const __grid_constant__ CUtensorMap mapY, const __grid_constant__ CUtensorMap mapZ,
                        const __grid_constant__ CUtensorMap mapR, const __grid_constant__ TcLinear p) {
-    extern __shared__ uint8_t smem_raw[];
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
     const TileSmem s = carve_tile(smem_raw, p);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = int(cluster_ctarank());
@@ -480,6 +481,32 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 __syncwarp();
             }
             const float sa = live && p.e.sa ? p.e.sa[m] : 1.f;
+            // While the MMAs run: a 16-bit bias of the warp's columns into shared
+            // memory, from where every lane reads all of it; a 32-bit bias and
+            // the columns' scales into a register of the column's lane, a chunk
+            // ahead, to be passed round by shuffles.
+            constexpr bool kBiasSmem = sizeof(T) == 2;
+            T* const bias_s = reinterpret_cast<T*>(s.bias + ew * kBiasBytes);
+            float bias_c = 0.f, sw_c = 1.f;
+            auto fetch_columns = [&](int c) {
+                const int64_t n = q0 + c + lane;
+                if (c < limit && n < p.Nq) {
+                    if (!kBiasSmem && p.e.bias) bias_c = to_f32(static_cast<const T*>(p.e.bias)[n]);
+                    if (p.e.sw) sw_c = p.e.sw[n];
+                }
+            };
+            if (tma) {
+                if (kBiasSmem && p.e.bias) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int64_t n = q0 + 32 * half + 64 * i + lane;
+                        if (32 * half + 64 * i < limit && n < p.Nq)
+                            bias_s[32 * i + lane] = static_cast<const T*>(p.e.bias)[n];
+                    }
+                    __syncwarp();
+                }
+                fetch_columns(32 * half);
+            }
             bool ok = wait_bounded(&s.acc_full[b], (it >> 1) & 1, s.abort, tmo);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
@@ -509,12 +536,30 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     continue;
                 }
                 const int64_t n = q0 + c;
+                const float bias_n = bias_c, sw_n = sw_c;
+                fetch_columns(c + 64);
                 if (p.e.sa) {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) x[i] *= sa;
+                    for (int i = 0; i < 32; i += 2)
+                        split(mul(f2(x[i], x[i + 1]), f2(sa)), x[i], x[i + 1]);
                 }
-                if (p.e.sw) apply_columns<float, true>(p.e.sw, n, p.Nq, p.vec, x);
-                if (p.e.bias) apply_columns<T, false>(p.e.bias, n, p.Nq, p.vec, x);
+                if (p.e.sw) apply_columns<true>(sw_n, x);
+                if (p.e.bias) {
+                    if constexpr (kBiasSmem) {
+                        const uint4* v = reinterpret_cast<const uint4*>(bias_s + c / 64 * 32);
+#pragma unroll
+                        for (int g = 0; g < 4; ++g) {
+                            float f[8];
+                            unpack8<T>(v[g], f);
+#pragma unroll
+                            for (int i = 0; i < 8; i += 2)
+                                split(add(f2(x[8 * g + i], x[8 * g + i + 1]), f2(f[i], f[i + 1])),
+                                      x[8 * g + i], x[8 * g + i + 1]);
+                        }
+                    } else {
+                        apply_columns<false>(bias_n, x);
+                    }
+                }
                 uint8_t* buf = staging + j * kBuf;
                 if (staged_z) {
                     // Two 16-bit buffers: Z's and Y's; one 32-bit buffer in turn.
@@ -615,7 +660,7 @@ struct SplitSmem {
 
 __device__ __forceinline__ SplitSmem carve_split(uint8_t* raw, const TcLinear& p) {
     SplitSmem s;
-    uint8_t* b = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* b = raw;  // 1024-byte aligned
     s.stages = b;
     uint64_t* bars = reinterpret_cast<uint64_t*>(b + p.ring_bytes);
     s.full = bars;
@@ -636,7 +681,7 @@ template <typename T, bool SWAP>
 __global__ void __launch_bounds__(kSplitThreads, 1)
     linear_split_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_constant__ CUtensorMap mapQ,
                         const __grid_constant__ TcLinear p) {
-    extern __shared__ uint8_t smem_raw[];
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
     const SplitSmem s = carve_split(smem_raw, p);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = int(cluster_ctarank());
@@ -815,9 +860,9 @@ void set_cluster(cudaLaunchAttribute& a, int n) {
 
 size_t tc_linear_smem(const TcLinear& p) {
     if (p.pair)
-        return 1024 + size_t(p.stages) * (p.p_bytes + p.q_bytes) + kTileEpiWarps * kStaging +
+        return size_t(p.stages) * (p.p_bytes + p.q_bytes) + kTileEpiWarps * (kStaging + kBiasBytes) +
                8 * (2 * size_t(p.stages) + 5 + 2 * kTileEpiWarps) + 16;
-    return 1024 + size_t(p.ring_bytes) + 8 * (2 * size_t(p.stages) + 1) + 16;
+    return size_t(p.ring_bytes) + 8 * (2 * size_t(p.stages) + 1) + 16;
 }
 
 cudaError_t launch_tc_linear(const TcLinearMaps& maps, const TcLinear& p, int grid, cudaStream_t stream) {

@@ -39,7 +39,7 @@ size_t tc_linear_smem(const TcLinear& p);
 cudaError_t launch_tc_linear(const TcLinearMaps& maps, const TcLinear& p, int grid, cudaStream_t stream);
 // Clusters of the tile kernel that fit the device at once.
 cudaError_t tc_linear_max_clusters(const TcLinear& p, int* clusters);
-constexpr size_t kTileStagingBytes = 8 * 4096;  // of the epilogue's warps
+constexpr size_t kTileStagingBytes = 8 * (4096 + 256);  // of the epilogue's warps
 cudaError_t linear_read_and_clear_status(int* status);
 
 }  // namespace tpg
