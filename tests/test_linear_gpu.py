@@ -365,17 +365,15 @@ def test_each_kernel(path, M, N, K, tune):
     tune.delenv("TPGEMM_LINEAR_PATH")
 
 
-@pytest.mark.parametrize("share", [0, 1, 2])  # a cluster's pairs share nothing, Q or P
 @pytest.mark.parametrize("bn", range(32, 257, 32))
-def test_tile_widths(bn, share, tune):
+def test_tile_widths(bn, tune):
     tune.setenv("TPGEMM_LINEAR_PATH", "tile")
-    tune.setenv("TPGEMM_LINEAR_SHARE", str(share))
     tune.setenv("TPGEMM_LINEAR_BN", str(bn))
     check_linear(1100, 1300, 520, BF16, act="silu", pre=bn % 64 == 0, seed=bn)
     check_linear(400, 520, 200, F16, act="gelu", seed=bn)
     check_linear(400, 520, 208, E4M3, act="gelu", seed=bn)
     check_backward(400, 200, 136, BF16, "none", BF16, seed=bn)
-    for name in ("PATH", "SHARE", "BN"):
+    for name in ("PATH", "BN"):
         tune.delenv("TPGEMM_LINEAR_" + name)
 
 

@@ -12,17 +12,17 @@ namespace {
 
 constexpr int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Clusters of the tile kernel that fit the device at once (all variants hold
-// the same threads and nearly all shared memory), asked once per device and
-// cluster size.
+// Clusters of the kernel that fit the device at once, asked once per device,
+// cluster size and shared-memory size (clusters are placed within groups of
+// SMs, so they can be fewer than the SMs divided by their size).
 tpgemm_status max_clusters(const TcLinear& p, int* clusters) {
     static std::mutex m;
-    static int cache[64][2] = {};
+    static int cache[64][3][9] = {};
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev < 0 || dev >= 64) return fail_with(TPGEMM_ERR_ARCH, "device index %d unsupported", dev);
     std::lock_guard<std::mutex> lock(m);
-    int& n = cache[dev][p.share ? 1 : 0];
+    int& n = cache[dev][p.pair ? 0 : p.half_sm ? 1 : 2][p.pair ? 2 : p.split];
     if (!n) {
         const cudaError_t e = tc_linear_max_clusters(p, &n);
         if (e != cudaSuccess || n <= 0) {
@@ -35,16 +35,16 @@ tpgemm_status max_clusters(const TcLinear& p, int* clusters) {
     return TPGEMM_OK;
 }
 
-// Bytes one SM takes in per nanosecond when a stage's operands come from L2 (53
-// to 56 bytes per clock measured on the multiply), the pair's time for one
-// 128-byte-wide K stage at the tensor rate, and what a launch costs around its
-// K loop, all in ns.
-constexpr double kSmBytes = 105.0;
-constexpr double kStageNs = 340.0;  // 256 x 256 x (64 of 16 bits)
+// Times in ns at the clocks that products run at here (1.85 GHz): an SM takes
+// in 64 bytes a clock, and a 128-row MMA of 16 x 16-bit K takes bn / 2 clocks,
+// at least 45 (its P operand; measured in isolation). Memory delivers about
+// 6 kB a ns to all SMs together.
+constexpr double kClock = 1.85;
+constexpr double kMemory = 6000;
 
 struct Choice {
     double ns = 1e30;
-    int pair = 0, swap = 0, bn = 0, bp = 128, split = 1, share = 0;
+    int pair = 0, swap = 0, bn = 0, bp = 128, split = 1, half_sm = 0;
 };
 
 }  // namespace
@@ -109,60 +109,69 @@ bool tma_outputs(const Epilogue& e, int64_t M) {
     return rows16(e.Y, e.ldy) && rows16(e.Z, e.ldz) && rows16(e.R, e.ldr);
 }
 
-// Time of the tile kernel: waves of a cluster's tiles, each K stage at the
-// tensor rate or at what an SM can take in.
+// Time of the tile kernel: waves of 256 x bn tiles, each K stage bound by what
+// an SM takes in (128 + bn / 2 rows of 128 bytes; 7 % over that measured), which
+// at bn = 256 is the tensor rate too; and the last epilogue.
 Choice plan_tile(const LinearOp& op, int64_t kb, int sms, const LinearTuning& t) {
     Choice best;
-    for (int share = kShareNone; share <= kShareP; ++share) {
-        if (t.share >= 0 && share != t.share) continue;
-        for (int bn = 256; bn >= 32; bn -= 32) {
-            if (t.bn > 0 && bn != t.bn) continue;
-            const int64_t tiles = ceil_div(op.M, share == kShareQ ? 512 : 256) *
-                                  ceil_div(op.N, share == kShareP ? 2 * bn : bn);
-            const int clusters = share ? sms / 4 : sms / 2;
-            const int rows = (share == kShareP ? 64 : 128) + bn / (share == kShareQ ? 4 : 2);
-            const double stage = std::max(kStageNs * bn / 256, rows * 128 / kSmBytes);
-            const double ns = 6000 + double(ceil_div(tiles, clusters)) * (double(kb) * stage + 500);
-            if (ns < best.ns) {
-                best.ns = ns;
-                best.pair = 1;
-                best.swap = 0;
-                best.bn = bn;
-                best.share = share;
-            }
+    for (int bn = 256; bn >= 32; bn -= 32) {
+        if (t.bn > 0 && bn != t.bn) continue;
+        const int64_t tiles = ceil_div(op.M, 256) * ceil_div(op.N, bn);
+        const double stage = (256 + bn) * (bn == 256 ? 1.01 : 1.07) / kClock;
+        const double ns = 3500 + bn * 12 + double(ceil_div(tiles, sms / 2)) * (double(kb) * stage + 200);
+        if (ns < best.ns) {
+            best.ns = ns;
+            best.pair = 1;
+            best.bn = bn;
         }
     }
     return best;
 }
 
-// Time of the split kernel: tiles x split CTAs over the SMs, each taking in its
-// share of the operands; joining costs more with every CTA of a cluster.
-Choice plan_split(const LinearOp& op, int64_t kb, int sms, const LinearTuning& t) {
-    Choice best;
+// Time of the split kernel: tiles x split CTAs, each taking in its share of the
+// operands, no faster than memory delivers them; then the join.
+tpgemm_status plan_split(const LinearOp& op, int64_t kb, int sms, const LinearTuning& t, Choice* best) {
     // The output's longer side along the lanes.
     const bool swap = op.N >= op.M;
     const int64_t Mp = swap ? op.N : op.M, Nq = swap ? op.M : op.N;
     const bool p_mn = swap ? op.b.mn : op.a.mn;
-    const int bn = Nq >= 256 ? 256 : int(ceil_div(Nq, 16) * 16);
-    for (int bp = 128; bp >= 64; bp -= 16) {
-        if (p_mn && bp % 64) continue;
-        if (t.bp > 0 && bp != t.bp) continue;
-        for (int split = 1; split <= 8 && split <= kb; ++split) {
-            if (t.split > 0 && split != std::min<int64_t>(t.split, kb)) continue;
-            const int64_t ctas = ceil_div(Mp, bp) * ceil_div(Nq, bn) * split;
-            const double bytes = double(bp + bn) * 128;
-            const double ns = 5000 + 250 * split + double(ceil_div(ctas, sms)) *
-                              (double(ceil_div(kb, split)) * bytes / kSmBytes + 1000);
-            if (ns < best.ns) {
-                best.ns = ns;
-                best.swap = swap;
-                best.bn = bn;
-                best.bp = bp;
-                best.split = split;
+    const int64_t es = elem_size(op.dtype);
+    const double memory = double((op.M + op.N) * op.K * es + 2 * op.M * op.N) / kMemory;
+    // Q in tiles of equal width, 256 at most.
+    const int64_t tiles_q = ceil_div(Nq, 256);
+    TcLinear p{};
+    p.swap = swap;
+    p.bn = int(ceil_div(ceil_div(Nq, tiles_q), 16) * 16);
+    p.e.out = op.e.out;
+    for (p.bp = 128; p.bp >= 64; p.bp -= 16) {
+        if (p_mn && p.bp % 64) continue;
+        if (t.bp > 0 && p.bp != t.bp) continue;
+        // Two blocks to an SM where the partial sums and three stages fit half of it.
+        const size_t stage = size_t(p.bp + p.bn) * 128 + 16384;  // (atoms and unused rows)
+        p.half_sm = std::max(split_partial_bytes(p), 3 * stage) + 512 <= kSplitHalfSmem;
+        for (p.split = 1; p.split <= 8 && p.split <= kb; ++p.split) {
+            if (t.split > 0 && p.split != std::min<int64_t>(t.split, kb)) continue;
+            const int64_t ctas = ceil_div(Mp, p.bp) * tiles_q * p.split;
+            int fit = 0;
+            const tpgemm_status s = max_clusters(p, &fit);
+            if (s != TPGEMM_OK) return s;
+            const int64_t rounds = ceil_div(ctas, int64_t(fit) * p.split);
+            const int64_t each = rounds > 1 ? rounds * (p.half_sm ? 2 : 1) : ceil_div(ctas, sms);
+            const double clocks = std::max(2.0 * (p.bp + p.bn), 4.0 * std::max(45, p.bn / 2));
+            const double join = (p.split > 1 ? 900 + 60 * p.split : 0) + p.bp * p.bn * 4 / 40 / kClock;
+            const double ns = 3000 + std::max(double(each * ceil_div(kb, p.split)) * clocks / kClock, memory) +
+                              double(rounds) * join;
+            if (ns < best->ns) {
+                best->ns = ns;
+                best->swap = swap;
+                best->bn = p.bn;
+                best->bp = p.bp;
+                best->split = p.split;
+                best->half_sm = p.half_sm;
             }
         }
     }
-    return best;
+    return TPGEMM_OK;
 }
 
 }  // namespace
@@ -178,8 +187,9 @@ tpgemm_status run_linear_tc(const LinearOp& op, int sms, cudaStream_t stream) {
     p.bk = p.fp8 ? 128 : 64;
     p.k_blocks = int(ceil_div(op.K, p.bk));
     p.timeout_ns = wait_timeout_ns();
-    p.vec = aligned16(op.e.bias) && aligned16(op.e.sw);
-    const Choice split = plan_split(op, p.k_blocks, sms, t);
+    Choice split;
+    s = plan_split(op, p.k_blocks, sms, t, &split);
+    if (s != TPGEMM_OK) return s;
     Choice c = plan_tile(op, p.k_blocks, sms, t);
     if (t.path == kLinearSplit || (t.path != kLinearTile && split.ns < c.ns)) c = split;
     if (c.bn == 0) return fail_with(TPGEMM_ERR_PATH, "the planner overrides leave no plan");
@@ -188,8 +198,9 @@ tpgemm_status run_linear_tc(const LinearOp& op, int sms, cudaStream_t stream) {
     p.bn = c.bn;
     p.bp = c.bp;
     p.split = c.split;
-    p.share = c.share;
+    p.half_sm = c.half_sm;
     p.tma_out = p.pair && tma_outputs(op.e, op.M);
+    p.vec = !p.pair && tma_outputs(op.e, op.M) && aligned16(op.e.bias) && aligned16(op.e.sw);
     const Operand& P = p.swap ? op.b : op.a;
     const Operand& Q = p.swap ? op.a : op.b;
     p.Mp = p.swap ? op.N : op.M;
@@ -201,8 +212,8 @@ tpgemm_status run_linear_tc(const LinearOp& op, int sms, cudaStream_t stream) {
     const int q_rows = p.pair ? p.bn / 2 : p.bn;
     p.p_bytes = 16384;
     p.q_bytes = p.q_mn ? uint32_t((q_rows + 63) / 64) * 8192u : uint32_t(q_rows) * 128u;
-    const int64_t tiles_p = ceil_div(p.Mp, !p.pair ? p.bp : p.share == kShareQ ? 512 : 256);
-    const int64_t tiles_q = ceil_div(p.Nq, p.share == kShareP ? 2 * p.bn : p.bn);
+    const int64_t tiles_p = ceil_div(p.Mp, p.pair ? 256 : p.bp);
+    const int64_t tiles_q = ceil_div(p.Nq, p.bn);
     if (tiles_p * tiles_q * p.split > 0x1fffffff)
         return fail_with(TPGEMM_ERR_SHAPE, "too many tiles");
     p.tiles_p = int(tiles_p);
@@ -212,25 +223,26 @@ tpgemm_status run_linear_tc(const LinearOp& op, int sms, cudaStream_t stream) {
     int grid;
     if (p.pair) {
         p.stages = int(std::min<size_t>(8, (budget - kTileStagingBytes) / (p.p_bytes + p.q_bytes)));
-        p.group = p.share == kShareQ ? 4 : 8;
+        p.group = 8;
         int clusters = 0;
         s = max_clusters(p, &clusters);
         if (s != TPGEMM_OK) return s;
-        grid = (p.share ? 4 : 2) * std::min(p.tiles, clusters);
+        grid = 2 * std::min(p.tiles, clusters);
     } else {
-        p.stages = int(std::min<size_t>(12, budget / (p.p_bytes + p.q_bytes)));
-        p.ring_bytes = uint32_t(p.stages) * (p.p_bytes + p.q_bytes);
-        p.ring_bytes = std::max(p.ring_bytes, uint32_t(p.bn) * 129u * 4u);
+        const size_t have = p.half_sm ? kSplitHalfSmem - 512 : budget;
+        p.stages = int(std::min<size_t>(12, have / (p.p_bytes + p.q_bytes)));
+        p.ring_bytes = std::max(uint32_t(p.stages) * (p.p_bytes + p.q_bytes),
+                                uint32_t((split_partial_bytes(p) + 1023) / 1024 * 1024));
         p.tmem_cols = 32;
         while (p.tmem_cols < 32 * ((p.bn + 31) / 32)) p.tmem_cols *= 2;
         grid = p.tiles * p.split;
     }
     TcLinearMaps maps;
     s = encode(enc, &maps.P, P, p.Mp, op.K, op.dtype,
-               P.mn ? 64 : !p.pair ? p.bp : p.share == kShareP ? 64 : 128);
+               P.mn ? 64 : p.pair ? 128 : p.bp);
     if (s != TPGEMM_OK) return s;
     s = encode(enc, &maps.Q, Q, p.Nq, op.K, op.dtype,
-               Q.mn ? (p.share == kShareQ ? 32 : 64) : p.share == kShareQ ? q_rows / 2 : q_rows);
+               Q.mn ? 64 : q_rows);
     if (s != TPGEMM_OK) return s;
     maps.Y = maps.Z = maps.R = maps.P;
     if (p.tma_out) {

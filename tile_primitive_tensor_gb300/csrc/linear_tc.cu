@@ -47,19 +47,6 @@ __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, vol
     }
 }
 
-// CTA-pair TMA load into the same place of every CTA of the cluster in `mask`
-// (bit: rank); the bytes of each complete on the barrier at `bar`'s place in
-// the even CTA of that one's pair (bar is given in an even CTA).
-__device__ __forceinline__ void tma_load_2d_pair_multicast(void* dst, const CUtensorMap* map, uint32_t bar,
-                                                           int32_t x, int32_t y, uint16_t mask,
-                                                           uint64_t policy) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-        ".multicast::cluster.L2::cache_hint [%0], [%1, {%3, %4}], [%2], %5, %6;" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "h"(mask), "l"(policy)
-        : "memory");
-}
-
 // Four MMAs, one 128-byte-wide stage of K, and their commit to `bar`, issued by
 // one thread that the warp elects. The whole warp runs this, convergent, with
 // the same values: descriptors, addresses and flags then live in uniform
@@ -239,11 +226,11 @@ __device__ __forceinline__ void apply_columns(float v, float (&x)[32]) {
 // a pair's even CTA) and owns tensor memory, 4..11 run the epilogue, two warps
 // to a lane quadrant taking alternate 32-column chunks.
 //
-// A cluster is one pair, or two pairs that share an operand tile: with
-// kShareQ they hold neighbouring P tiles and one Q tile, with kShareP one P
-// tile and neighbouring Q tiles. Each of the four CTAs then loads half of what
-// it needs of the shared tile and multicasts it to itself and to the CTA of
-// the other pair that needs the same half.
+// A stage brings 128 P rows and bn / 2 Q rows of 128 bytes into each SM, which
+// takes in 64 bytes a clock: 256 + bn clocks, against 2 bn at the tensor rate.
+// So bn = 256 is where both meet (515 measured), and narrower tiles are bound
+// by delivery (413 at 128). Two pairs sharing a tile by TMA multicast measured
+// no faster: they save reads of L2, not what arrives at an SM.
 //
 // Outputs whose rows start on 16-byte boundaries leave through a staging tile
 // and TMA stores; the residual comes in the same way, ahead of its use. Stores
@@ -294,14 +281,6 @@ __device__ __forceinline__ void tile_at(int T, const TcLinear& p, int& tp, int& 
     if (g & 1) tq = p.tiles_q - 1 - tq;
 }
 
-__device__ __forceinline__ void load_box(void* dst, const CUtensorMap* map, uint32_t bar, int x, int y,
-                                         uint64_t pol, uint32_t mask) {
-    if (mask)
-        tma_load_2d_pair_multicast(dst, map, bar, x, y, uint16_t(mask), pol);
-    else
-        tma_load_2d_pair_hint(dst, map, bar, x, y, pol);
-}
-
 template <typename T>
 __global__ void __launch_bounds__(kTileThreads, 1)
     linear_tile_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_constant__ CUtensorMap mapQ,
@@ -311,9 +290,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const TileSmem s = carve_tile(smem_raw, p);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = int(cluster_ctarank());
-    const int csize = p.share ? 4 : 2;
-    const int pair = rank >> 1, half_id = rank & 1, leader = rank & ~1;
-    const int cid = blockIdx.x / csize, ncl = gridDim.x / csize;
+    const int cid = blockIdx.x / 2, ncl = gridDim.x / 2;
     const uint32_t stage_bytes = p.p_bytes + p.q_bytes;
     const uint64_t tmo = p.timeout_ns;
     if (warp == 0 && lane == 0) {
@@ -326,7 +303,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
         for (int i = 0; i < p.stages; ++i) {
             mbar_init(&s.full[i], 1);
-            mbar_init(&s.empty[i], p.share ? 2 : 1);  // every pair that reads the stage's fills
+            mbar_init(&s.empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s.acc_full[i], 1);
@@ -356,18 +333,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const int q_rows = p.bn / 2;        // of this CTA's half
         const int q_atoms = (q_rows + 63) / 64;
         const uint32_t tx = 2u * (p.p_bytes + (p.q_mn ? uint32_t(q_atoms) * kAtom : uint32_t(q_rows) * 128u));
-        const uint32_t both = 5u << half_id;  // the CTAs of both pairs that hold this half
-        const uint32_t mask_p = p.share == kShareP ? both : 0u, mask_q = p.share == kShareQ ? both : 0u;
         int stage = 0, turn = 0;
         uint32_t phase = 0;
         bool ok = true;
         for (int t = cid; ok && t < p.tiles; t += ncl) {
             int tp, tq;
             tile_at(t, p, tp, tq);
-            if (p.share == kShareQ) tp = 2 * tp + pair;
-            if (p.share == kShareP) tq = 2 * tq + pair;
-            const int p0 = (2 * tp + half_id) * 128;
-            const int q0 = tq * p.bn + half_id * q_rows;
+            const int p0 = (2 * tp + rank) * 128;
+            const int q0 = tq * p.bn + rank * q_rows;
             for (int kb = 0; kb < p.k_blocks; ++kb, turn ^= 1) {
                 if (turn == prod) {
                     if (!wait_bounded(&s.empty[stage], phase ^ 1u, s.abort, tmo)) {
@@ -377,24 +350,20 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     uint8_t* sp = s.stages + size_t(stage) * stage_bytes;
                     uint8_t* sq = sp + p.p_bytes;
                     const int k0 = kb * p.bk;
-                    const uint32_t fb = mapa_shared(smem_u32(&s.full[stage]), uint32_t(leader));
-                    if (half_id == 0) mbar_arrive_expect_tx(&s.full[stage], tx);
-                    if (mask_p) {  // 64 of the 128 rows
-                        load_box(sp + pair * kAtom, &mapP, fb, p.p_mn ? p0 + 64 * pair : k0,
-                                 p.p_mn ? k0 : p0 + 64 * pair, pol, mask_p);
-                    } else if (p.p_mn) {
-                        load_box(sp, &mapP, fb, p0, k0, pol, 0);
-                        load_box(sp + kAtom, &mapP, fb, p0 + 64, k0, pol, 0);
+                    // Both CTAs' fills complete on the even one's barrier.
+                    const uint32_t fb = mapa_shared(smem_u32(&s.full[stage]), 0);
+                    if (rank == 0) mbar_arrive_expect_tx(&s.full[stage], tx);
+                    if (p.p_mn) {
+                        tma_load_2d_pair_hint(sp, &mapP, fb, p0, k0, pol);
+                        tma_load_2d_pair_hint(sp + kAtom, &mapP, fb, p0 + 64, k0, pol);
                     } else {
-                        load_box(sp, &mapP, fb, k0, p0, pol, 0);
+                        tma_load_2d_pair_hint(sp, &mapP, fb, k0, p0, pol);
                     }
-                    if (p.q_mn) {  // (shared: half of the K rows of each atom)
-                        const int kh = mask_q ? 32 * pair : 0;
+                    if (p.q_mn) {
                         for (int a = 0; a < q_atoms; ++a)
-                            load_box(sq + a * kAtom + kh * 128, &mapQ, fb, q0 + 64 * a, k0 + kh, pol, mask_q);
+                            tma_load_2d_pair_hint(sq + a * kAtom, &mapQ, fb, q0 + 64 * a, k0, pol);
                     } else {
-                        const int rh = mask_q ? (q_rows / 2) * pair : 0;
-                        load_box(sq + rh * 128, &mapQ, fb, k0, q0 + rh, pol, mask_q);
+                        tma_load_2d_pair_hint(sq, &mapQ, fb, k0, q0, pol);
                     }
                     issued_any |= 1u << stage;
                     issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
@@ -406,7 +375,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             }
         }
     }
-    if (warp == 1 && half_id == 0) {
+    if (warp == 1 && rank == 0) {
         const uint64_t dP = smem_desc_with_addr(operand_desc(p.p_mn), smem_u32(s.stages));
         const uint64_t dQ = smem_desc_with_addr(operand_desc(p.q_mn), smem_u32(s.stages) + p.p_bytes);
         const uint64_t step_p = operand_step(p.p_mn), step_q = operand_step(p.q_mn);
@@ -414,7 +383,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const uint32_t empty0 = smem_u32(s.empty);
         const int nstages = p.stages, nk = p.k_blocks;
         const bool fp8 = p.fp8 != 0;
-        const uint16_t mine = uint16_t(3u << leader), readers = p.share ? uint16_t(15) : mine;
         int stage = 0, it = 0;
         uint32_t phase = 0;
         bool ok = true;
@@ -432,15 +400,15 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 tc_fence_after_sync();
                 const uint64_t off = uint64_t(uint32_t(stage) * stage_units);
                 issue_stage<true>(fp8, acc, dP + off, dQ + off, step_p, step_q, idesc, kb != 0,
-                                  empty0 + 8u * uint32_t(stage), readers);
+                                  empty0 + 8u * uint32_t(stage), 3);
                 if (++stage == nstages) {
                     stage = 0;
                     phase ^= 1u;
                 }
             }
-            if (ok) commit_elected_pair(&s.acc_full[b], mine);
+            if (ok) commit_elected_pair(&s.acc_full[b], 3);
         }
-        commit_elected_pair(s.drain, uint16_t(1u << rank));
+        commit_elected_pair(s.drain, 1);
         wait_bounded(s.drain, 0, s.abort, tmo, true);
     }
     if (warp >= 4) {
@@ -459,9 +427,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         for (int t = cid; t < p.tiles; t += ncl, ++it) {
             int tp, tq;
             tile_at(t, p, tp, tq);
-            if (p.share == kShareQ) tp = 2 * tp + pair;
-            if (p.share == kShareP) tq = 2 * tq + pair;
-            const int64_t m0 = int64_t(2 * tp + half_id) * 128 + quad * 32, m = m0 + lane;
+            const int64_t m0 = int64_t(2 * tp + rank) * 128 + quad * 32, m = m0 + lane;
             const int64_t q0 = int64_t(tq) * p.bn;
             const int b = it & 1;
             const bool live = m < p.Mp;
@@ -621,7 +587,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             }
             tc_fence_before_sync();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&s.acc_empty[b]), uint32_t(leader)));
+            if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&s.acc_empty[b]), 0u));
             if (!ok) break;
         }
         if (lane == 0) bulk_wait_group_read<0>();
@@ -633,7 +599,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     __syncthreads();
     if (*s.abort) {
         // Both CTAs' fills complete on the even CTA's barriers.
-        if (prod >= 0 && lane == 0 && half_id == 0)
+        if (prod >= 0 && lane == 0 && rank == 0)
             for (int i = 0; i < p.stages; ++i)
                 if (issued_any & (1u << i))
                     wait_bounded(&s.full[i], (issued_parity >> i) & 1u, s.abort, tmo, true);
@@ -648,11 +614,19 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 }
 
 // ------------------------------------------------------------ split kernel
+// 8 warps: 0 issues the TMA fills, 1 the MMAs and owns tensor memory, and all
+// of them join and write the tile. A block that stays within half of an SM's
+// shared memory shares the SM with another one, whose fills run under this
+// one's set-up and joining.
+//
+// Each CTA leaves its partial sums in shared memory (in the stages, which are
+// idle by then), lines along the output's contiguous direction; after a cluster
+// barrier every CTA adds up and writes its share of the lines, 16 bytes of
+// partial sums of each rank at a time, always in rank order.
 constexpr int kSplitThreads = 256;
-constexpr int kPad = 129;  // words between a column's and the next one's 128 lanes
 
 struct SplitSmem {
-    uint8_t* stages;  // then the partial sums, [bn][kPad] f32
+    uint8_t* stages;  // then the partial sums
     uint64_t *full, *empty, *acc_full;
     uint32_t* tmem_base;
     volatile int* abort;
@@ -660,9 +634,8 @@ struct SplitSmem {
 
 __device__ __forceinline__ SplitSmem carve_split(uint8_t* raw, const TcLinear& p) {
     SplitSmem s;
-    uint8_t* b = raw;  // 1024-byte aligned
-    s.stages = b;
-    uint64_t* bars = reinterpret_cast<uint64_t*>(b + p.ring_bytes);
+    s.stages = raw;  // 1024-byte aligned
+    uint64_t* bars = reinterpret_cast<uint64_t*>(raw + p.ring_bytes);
     s.full = bars;
     s.empty = bars + p.stages;
     s.acc_full = bars + 2 * p.stages;
@@ -671,14 +644,85 @@ __device__ __forceinline__ SplitSmem carve_split(uint8_t* raw, const TcLinear& p
     return s;
 }
 
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
     return v;
 }
 
+// Four neighbouring outputs n.. of row m (cnt of them in the matrix; vec: all
+// four, and every pointer's address there a multiple of four elements).
+template <typename T>
+__device__ __forceinline__ void load4(const void* base, int64_t at, bool vec, int cnt, float (&f)[4]) {
+    const T* p = static_cast<const T*>(base) + at;
+    if (vec) {
+        if constexpr (sizeof(T) == 4) {
+            const float4 v = *reinterpret_cast<const float4*>(p);
+            f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
+        } else {
+            const uint2 v = *reinterpret_cast<const uint2*>(p);
+            float g[8];
+            unpack8<T>(make_uint4(v.x, v.y, 0, 0), g);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[i] = g[i];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = i < cnt ? to_f32(p[i]) : 0.f;
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ void store4(void* base, int64_t at, bool vec, int cnt, const float (&f)[4]) {
+    T* p = static_cast<T*>(base) + at;
+    if (vec) {
+        if constexpr (sizeof(T) == 4) {
+            *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+        } else {
+            const float g[8] = {f[0], f[1], f[2], f[3], 0.f, 0.f, 0.f, 0.f};
+            const uint4 v = pack8<T>(g);
+            *reinterpret_cast<uint2*>(p) = make_uint2(v.x, v.y);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < cnt) p[i] = from_f32<T>(f[i]);
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ void epilogue_row4(const Epilogue& e, bool vec, int64_t m, int64_t n,
+                                              int cnt, float (&x)[4]) {
+    float t[4];
+    vec = vec && cnt == 4;
+    const float sa = e.sa ? e.sa[m] : 1.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] *= sa;
+    if (e.sw) {
+        load4<float>(e.sw, n, vec, cnt, t);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] *= t[i];
+    }
+    if (e.bias) {
+        load4<T>(e.bias, n, vec, cnt, t);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] += t[i];
+    }
+    if (e.Z) store4<T>(e.Z, m * e.ldz + n, vec, cnt, x);
+    act_n(e.act, x);
+    if (e.R) {
+        load4<T>(e.R, m * e.ldr + n, vec, cnt, t);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] += t[i];
+    }
+    store4<T>(e.Y, m * e.ldy + n, vec, cnt, x);
+}
+
 template <typename T, bool SWAP>
-__global__ void __launch_bounds__(kSplitThreads, 1)
+__global__ void __launch_bounds__(kSplitThreads, 2)
     linear_split_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_constant__ CUtensorMap mapQ,
                         const __grid_constant__ TcLinear p) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -714,11 +758,21 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
     const uint32_t tmem = *s.tmem_base;
     uint32_t issued_any = 0, issued_parity = 0;
     if (warp == 0 && lane == 0) {
-        grid_dependency_wait();
         const uint64_t pol_p = l2_policy(p.tiles_q == 1 ? 1 : 2), pol_q = l2_policy(2);
         const int q_atoms = (p.bn + 63) / 64, p_atoms = (p.bp + 63) / 64;
         const uint32_t tx = (p.p_mn ? uint32_t(p_atoms) * kAtom : uint32_t(p.bp) * 128u) +
                             (p.q_mn ? uint32_t(q_atoms) * kAtom : uint32_t(p.bn) * 128u);
+        // Ask L2 for the first stages' boxes before waiting for the previous
+        // grid: its writes land in L2 too, so no line there is ever stale.
+        for (int kb = kb0; kb < kb1 && kb < kb0 + p.stages; ++kb) {
+            const int k0 = kb * p.bk;
+            if (p.p_mn) {
+                for (int a = 0; a < p_atoms; ++a) tma_prefetch_2d(&mapP, p0 + 64 * a, k0);
+            } else {
+                tma_prefetch_2d(&mapP, k0, p0);
+            }
+        }
+        grid_dependency_wait();
         int stage = 0;
         uint32_t phase = 0;
         for (int kb = kb0; kb < kb1; ++kb) {
@@ -777,16 +831,28 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
     ok = __all_sync(0xffffffffu, ok);
     tc_fence_after_sync();
     float* part = reinterpret_cast<float*>(s.stages);
+    // Lines of the output's contiguous direction: of bp (swapped) or bn values,
+    // four words more apart.
+    const int len = SWAP ? 128 : p.bn, lines = SWAP ? p.bn : p.bp, pitch = len + 4;
     if (ok && !*s.abort) {
-        const int quad = warp & 3;
+        const int quad = warp & 3, pl = quad * 32 + lane;
         for (int c = warp >> 2; 32 * c < p.bn; c += 2) {
             uint32_t r[32];
             tmem_ld_32x32b_x32(tmem + (uint32_t(quad * 32) << 16) + uint32_t(32 * c), r);
             tmem_ld_wait(r);
+            if constexpr (SWAP) {  // a lane is a place in each of 32 lines
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-                if (32 * c + i < p.bn)
-                    part[(32 * c + i) * kPad + quad * 32 + lane] = __uint_as_float(r[i]);
+                for (int i = 0; i < 32; ++i)
+                    if (32 * c + i < p.bn) part[(32 * c + i) * pitch + pl] = __uint_as_float(r[i]);
+            } else if (pl < p.bp) {  // a lane is a line
+#pragma unroll
+                for (int i = 0; i < 32; i += 4)
+                    if (32 * c + i < p.bn)
+                        *reinterpret_cast<float4*>(part + pl * pitch + 32 * c + i) =
+                            make_float4(__uint_as_float(r[i]), __uint_as_float(r[i + 1]),
+                                        __uint_as_float(r[i + 2]), __uint_as_float(r[i + 3]));
+            }
+            __syncwarp();
         }
     }
     tc_fence_before_sync();
@@ -794,26 +860,32 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
     cluster_sync();
     grid_dependency_wait();
     if (!*s.abort) {
-        // This CTA's share of the tile: every split-th run of 32 outputs along
-        // the output's rows' contiguous direction. Ranks are added in order.
         const uint32_t mine = smem_u32(part);
-        const int runs_in = SWAP ? (p.bp + 31) / 32 : (p.bn + 31) / 32;  // runs along that direction
-        const int lines = SWAP ? p.bn : p.bp;
-        with_act(p.e.act, [&](auto act) {
-            constexpr int ACT = decltype(act)::value;
-            for (int i = warp * p.split + rank; i < runs_in * lines; i += p.split * (kSplitThreads / 32)) {
-                const int along = 32 * (i % runs_in) + lane, line = i / runs_in;
-                const int pl = SWAP ? along : line, ql = SWAP ? line : along;
-                if (pl >= p.bp || ql >= p.bn || p0 + pl >= p.Mp || q0 + ql >= p.Nq) continue;
-                const uint32_t at = mine + 4u * uint32_t(ql * kPad + pl);
-                float x = 0.f;
-                for (int r = 0; r < p.split; ++r) x += ld_cluster_f32(mapa_shared(at, uint32_t(r)));
-                if constexpr (SWAP)
-                    epilogue_one<T, ACT>(p.e, q0 + ql, p0 + pl, x);
-                else
-                    epilogue_one<T, ACT>(p.e, p0 + pl, q0 + ql, x);
-            }
-        });
+        const int units = (SWAP ? p.bp : p.bn) / 4;  // of four values in a line
+        const int64_t M = SWAP ? p.Nq : p.Mp, N = SWAP ? p.Mp : p.Nq;
+        const int64_t m0 = SWAP ? q0 : p0, n0 = SWAP ? p0 : q0;
+        for (int u = rank * kSplitThreads + int(threadIdx.x); u < units * lines;
+             u += p.split * kSplitThreads) {
+            const int line = u / units, at = 4 * (u - line * units);
+            const int64_t m = m0 + line, n = n0 + at;
+            if (m >= M || n >= N) continue;
+            const uint32_t addr = mine + 4u * uint32_t(line * pitch + at);
+            float4 v[8];
+#pragma unroll
+            for (int r = 0; r < 8; ++r)
+                if (r < p.split) v[r] = ld_cluster_f32x4(mapa_shared(addr, uint32_t(r)));
+            float x[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+#pragma unroll
+            for (int r = 1; r < 8; ++r)
+                if (r < p.split) {
+                    x[0] += v[r].x;
+                    x[1] += v[r].y;
+                    x[2] += v[r].z;
+                    x[3] += v[r].w;
+                }
+            const int64_t left = N - n;
+            epilogue_row4<T>(p.e, p.vec != 0, m, n, left < 4 ? int(left) : 4, x);
+        }
     }
     if (*s.abort && warp == 0 && lane == 0)
         for (int i = 0; i < p.stages; ++i)
@@ -847,7 +919,7 @@ SplitFn pick_split(const TcLinear& p) {
                                          : pick_split_typed<float>(p);
 }
 
-int cluster_of(const TcLinear& p) { return p.pair ? (p.share ? 4 : 2) : p.split; }
+int cluster_of(const TcLinear& p) { return p.pair ? 2 : p.split; }
 
 void set_cluster(cudaLaunchAttribute& a, int n) {
     a.id = cudaLaunchAttributeClusterDimension;
@@ -862,17 +934,17 @@ size_t tc_linear_smem(const TcLinear& p) {
     if (p.pair)
         return size_t(p.stages) * (p.p_bytes + p.q_bytes) + kTileEpiWarps * (kStaging + kBiasBytes) +
                8 * (2 * size_t(p.stages) + 5 + 2 * kTileEpiWarps) + 16;
-    return size_t(p.ring_bytes) + 8 * (2 * size_t(p.stages) + 1) + 16;
+    return p.half_sm ? kSplitHalfSmem : size_t(kTcMaxSmem);
 }
 
 cudaError_t launch_tc_linear(const TcLinearMaps& maps, const TcLinear& p, int grid, cudaStream_t stream) {
     const int cluster = cluster_of(p);
+    const size_t ring = size_t(p.stages) * (p.p_bytes + p.q_bytes);
     if (p.stages < 2 || p.stages > 32 || cluster < 1 || cluster > 8 || grid % cluster != 0 ||
-        p.bn % 16 != 0 || p.bn > 256 ||
-        (p.pair && (p.bn % 32 != 0 || p.group < 1)) ||
-        (!p.pair && (p.bp > 128 || p.bp % 16 != 0 || p.split > p.k_blocks ||
-                     size_t(p.bn) * kPad * 4 > p.ring_bytes ||
-                     size_t(p.stages) * (p.p_bytes + p.q_bytes) > p.ring_bytes)))
+        p.bn % 16 != 0 || p.bn > 256 || (p.pair && (p.bn % 32 != 0 || p.group < 1)) ||
+        (!p.pair && (p.bp > 128 || p.bp % 16 != 0 || p.split > p.k_blocks || ring > p.ring_bytes ||
+                     split_partial_bytes(p) > p.ring_bytes ||
+                     p.ring_bytes + 8 * (2 * size_t(p.stages) + 1) + 16 > tc_linear_smem(p))))
         return cudaErrorInvalidValue;
     const size_t smem = tc_linear_smem(p);
     if (smem > size_t(kTcMaxSmem)) return cudaErrorInvalidConfiguration;
@@ -897,12 +969,13 @@ cudaError_t launch_tc_linear(const TcLinearMaps& maps, const TcLinear& p, int gr
 }
 
 cudaError_t tc_linear_max_clusters(const TcLinear& p, int* clusters) {
-    const TileFn fn = pick_tile(p);
+    const void* fn = p.pair ? reinterpret_cast<const void*>(pick_tile(p))
+                            : reinterpret_cast<const void*>(pick_split(p));
     cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcMaxSmem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(cluster_of(p)));
-    cfg.blockDim = dim3(kTileThreads);
+    cfg.blockDim = dim3(p.pair ? kTileThreads : kSplitThreads);
     cfg.dynamicSmemBytes = tc_linear_smem(p);
     cudaLaunchAttribute attr[1];
     set_cluster(attr[0], cluster_of(p));

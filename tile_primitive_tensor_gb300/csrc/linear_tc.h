@@ -20,15 +20,14 @@ struct TcLinear {
     uint32_t idesc;
     int tmem_cols;         // split kernel
     int split;             // split kernel: CTAs of a cluster, each a share of K
-    int group;             // tile kernel: P tiles (of a cluster) in a raster run
-    int share;             // tile kernel: what a cluster's two pairs share (0: one pair)
+    int group;             // tile kernel: P tiles in a raster run
+    int half_sm;           // split kernel: half of an SM's shared memory, two blocks to an SM
     int tma_out;           // tile kernel: Y, Z and R move by TMA (rows on 16-byte boundaries)
     int swap;              // P holds the output's columns
     int pair;              // tile kernel (1) or split kernel (0)
     int fp8;
-    int vec;               // bias and scale_w start on 16-byte boundaries
+    int vec;               // split kernel: four outputs move as one access
 };
-enum { kShareNone = 0, kShareQ = 1, kShareP = 2 };
 
 struct TcLinearMaps {
     CUtensorMap P, Q;     // operands
@@ -37,8 +36,14 @@ struct TcLinearMaps {
 
 size_t tc_linear_smem(const TcLinear& p);
 cudaError_t launch_tc_linear(const TcLinearMaps& maps, const TcLinear& p, int grid, cudaStream_t stream);
-// Clusters of the tile kernel that fit the device at once.
+// Clusters of the kernel that fit the device at once.
 cudaError_t tc_linear_max_clusters(const TcLinear& p, int* clusters);
+// Shared memory of a split block that leaves room for another on its SM.
+constexpr size_t kSplitHalfSmem = 112 * 1024;
+// Shared bytes of a split tile's partial sums.
+inline size_t split_partial_bytes(const TcLinear& p) {
+    return p.swap ? size_t(p.bn) * (128 + 4) * 4 : size_t(p.bp) * (p.bn + 4) * 4;
+}
 constexpr size_t kTileStagingBytes = 8 * (4096 + 256);  // of the epilogue's warps
 cudaError_t linear_read_and_clear_status(int* status);
 

@@ -21,10 +21,10 @@ tpgemm_status require_device(int* sms);
 tpgemm_status tensor_map_encoder(PFN_cuTensorMapEncodeTiled_v12000* fn);
 
 // Planner overrides of the linear layer's product (TPGEMM_LINEAR_PATH, _BN, _BP,
-// _SPLIT, _SHARE; -1: not set), from the snapshot that tpgemm_reload_tuning renews.
+// _SPLIT; -1: not set), from the snapshot that tpgemm_reload_tuning renews.
 enum { kLinearTile = 0, kLinearSplit = 1, kLinearFew = 2 };
 struct LinearTuning {
-    int path, bn, bp, split, share;
+    int path, bn, bp, split;
 };
 LinearTuning linear_tuning();
 

@@ -97,7 +97,6 @@ struct Tuning {
     int tail = -1, host_blocks = -1, l2_p = -1, l2_q = -1, l2_cd = -1, snake = -1, krev = -1;
     int epi_help = -1, host_edge = -1;
     int linear_path = -1, linear_bn = -1, linear_bp = -1, linear_split = -1;
-    int linear_share = -1;
     int debug_plant = -1;  // debug builds only
     int orient = 0;  // 1 "swap", 2 "normal"
     long long wait_ms = -1;
@@ -132,7 +131,6 @@ Tuning read_tuning() {
     geti("TPGEMM_LINEAR_BN", &t.linear_bn);
     geti("TPGEMM_LINEAR_BP", &t.linear_bp);
     geti("TPGEMM_LINEAR_SPLIT", &t.linear_split);
-    geti("TPGEMM_LINEAR_SHARE", &t.linear_share);
     if (const char* f = getenv("TPGEMM_LINEAR_PATH")) {
         if (!strcmp(f, "tile")) t.linear_path = tpg::kLinearTile;
         if (!strcmp(f, "split")) t.linear_path = tpg::kLinearSplit;
@@ -1377,7 +1375,7 @@ tpgemm_status require_device(int* sms) {
 
 LinearTuning linear_tuning() {
     const Tuning& t = tuning();
-    return {t.linear_path, t.linear_bn, t.linear_bp, t.linear_split, t.linear_share};
+    return {t.linear_path, t.linear_bn, t.linear_bp, t.linear_split};
 }
 
 tpgemm_status tensor_map_encoder(PFN_cuTensorMapEncodeTiled_v12000* fn) { return get_encoder(fn); }
