@@ -149,8 +149,11 @@ tpgemm_status plan_split(const LinearOp& op, int64_t kb, int sms, const LinearTu
         // Two blocks to an SM where the partial sums and three stages fit half of it.
         const size_t stage = size_t(p.bp + p.bn) * 128 + 16384;  // (atoms and unused rows)
         p.half_sm = std::max(split_partial_bytes(p), 3 * stage) + 512 <= kSplitHalfSmem;
-        for (p.split = 1; p.split <= 8 && p.split <= kb; ++p.split) {
-            if (t.split > 0 && p.split != std::min<int64_t>(t.split, kb)) continue;
+        // Clusters of other sizes than these leave SMs of a group without a place.
+        const int forced = t.split == 2 || t.split == 4 || t.split == 8 || t.split == 1 ? t.split : 0;
+        for (p.split = 1; p.split <= 8 && p.split <= kb; p.split *= 2) {
+            if (forced && p.split != forced && p.split * 2 <= kb && p.split < forced) continue;
+            if (forced && p.split > forced) break;
             const int64_t ctas = ceil_div(Mp, p.bp) * tiles_q * p.split;
             int fit = 0;
             const tpgemm_status s = max_clusters(p, &fit);
@@ -158,8 +161,13 @@ tpgemm_status plan_split(const LinearOp& op, int64_t kb, int sms, const LinearTu
             const int64_t rounds = ceil_div(ctas, int64_t(fit) * p.split);
             const int64_t each = rounds > 1 ? rounds * (p.half_sm ? 2 : 1) : ceil_div(ctas, sms);
             const double clocks = std::max(2.0 * (p.bp + p.bn), 4.0 * std::max(45, p.bn / 2));
+            const double share = double(ceil_div(kb, p.split));
+            // A CTA's stages in flight come back after about 1.5 us under load.
+            const double alone = double(rounds) * share * (p.bp + p.bn) * 128 * 1500 /
+                                 double(p.half_sm ? kSplitHalfSmem : size_t(kTcMaxSmem));
+            const double busy = double(each) * share * clocks / kClock;
             const double join = (p.split > 1 ? 900 + 60 * p.split : 0) + p.bp * p.bn * 4 / 40 / kClock;
-            const double ns = 3000 + std::max(double(each * ceil_div(kb, p.split)) * clocks / kClock, memory) +
+            const double ns = 3000 + std::max(std::max(busy, alone), memory) +
                               double(rounds) * join;
             if (ns < best->ns) {
                 best->ns = ns;
@@ -224,6 +232,8 @@ tpgemm_status run_linear_tc(const LinearOp& op, int sms, cudaStream_t stream) {
     if (p.pair) {
         p.stages = int(std::min<size_t>(8, (budget - kTileStagingBytes) / (p.p_bytes + p.q_bytes)));
         p.group = 8;
+        // Few tiles along one side: the CTAs at work all read the same panels.
+        p.k_rotate = p.tiles_p == 1 || p.tiles_q == 1;
         int clusters = 0;
         s = max_clusters(p, &clusters);
         if (s != TPGEMM_OK) return s;

@@ -30,7 +30,7 @@ __device__ int g_linear_status;  // 0 = ok, kStatusTimeout after an expired wait
 
 namespace {
 
-constexpr int kAtom = 8192;  // an operand stored along its rows: 64 K x 64 rows of 16 bits
+constexpr uint32_t kAtom = 8192;  // an operand stored along its rows: 64 K x 64 rows of 16 bits
 
 __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, volatile int* abort,
                                              uint64_t timeout_ns, bool drain = false) {
@@ -95,6 +95,57 @@ __device__ __forceinline__ void issue_stage(bool fp8, uint32_t acc, uint64_t a, 
     }
 }
 #undef TPG_STAGE_ASM
+
+// TMA loads and their byte counts, issued likewise by the elected thread of a
+// convergent warp: a fill of two boxes from under a one-lane branch held its
+// thread for 400 clocks, most of the 512 that a 256 x 256 stage computes for.
+__device__ __forceinline__ void expect_elected(uint32_t bar, uint32_t bytes) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar),
+        "r"(bytes)
+        : "memory");
+}
+
+template <bool PAIR>
+__device__ __forceinline__ void load_elected(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t x,
+                                             int32_t y, uint64_t policy) {
+    if constexpr (PAIR)
+        asm volatile(
+            "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+            "@e cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+            ".L2::cache_hint [%0], [%1, {%3, %4}], [%2], %5;\n\t}" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "l"(policy)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+            "@e cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
+            ".L2::cache_hint [%0], [%1, {%3, %4}], [%2], %5;\n\t}" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "l"(policy)
+            : "memory");
+}
+
+__device__ __forceinline__ void prefetch_elected(const CUtensorMap* map, int32_t x, int32_t y) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];\n\t}" ::"l"(
+            reinterpret_cast<uint64_t>(map)),
+        "r"(x), "r"(y)
+        : "memory");
+}
+
+// One operand's box or boxes of a stage: `rows` rows from r0 on, K from k0 on.
+template <bool PAIR>
+__device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* map, uint32_t bar, int mn,
+                                             int atoms, int r0, int k0, uint64_t policy) {
+    if (mn) {
+        for (int a = 0; a < atoms; ++a)
+            load_elected<PAIR>(dst + uint32_t(a) * kAtom, map, bar, r0 + 64 * a, k0, policy);
+    } else {
+        load_elected<PAIR>(dst, map, bar, k0, r0, policy);
+    }
+}
 
 // Commits of the elected thread's MMAs (the whole warp, convergent).
 __device__ __forceinline__ void commit_elected(uint64_t* bar) {
@@ -327,12 +378,15 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     uint32_t rphase = 0, rpend = 0;  // residual fills: next parity, and in flight (bit: buffer)
 
     const int prod = warp == 0 ? 0 : (warp == 2 ? 1 : -1);
-    if (prod >= 0 && lane == 0) {
+    if (prod >= 0) {
         grid_dependency_wait();
         const uint64_t pol = l2_policy(2);  // panels are read again by later tiles
         const int q_rows = p.bn / 2;        // of this CTA's half
         const int q_atoms = (q_rows + 63) / 64;
         const uint32_t tx = 2u * (p.p_bytes + (p.q_mn ? uint32_t(q_atoms) * kAtom : uint32_t(q_rows) * 128u));
+        const uint32_t stages0 = smem_u32(s.stages), full0 = smem_u32(s.full);
+        const uint32_t lead0 = mapa_shared(full0, 0);  // both CTAs' fills complete on the even one's
+        const int nstages = p.stages, nk = p.k_blocks;
         int stage = 0, turn = 0;
         uint32_t phase = 0;
         bool ok = true;
@@ -341,34 +395,23 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             tile_at(t, p, tp, tq);
             const int p0 = (2 * tp + rank) * 128;
             const int q0 = tq * p.bn + rank * q_rows;
-            for (int kb = 0; kb < p.k_blocks; ++kb, turn ^= 1) {
+            int kb = p.k_rotate ? int(int64_t(t) * nk / p.tiles) : 0;
+            for (int i = 0; i < nk; ++i, turn ^= 1, kb = kb + 1 == nk ? 0 : kb + 1) {
                 if (turn == prod) {
-                    if (!wait_bounded(&s.empty[stage], phase ^ 1u, s.abort, tmo)) {
+                    if (!__all_sync(0xffffffffu, wait_bounded(&s.empty[stage], phase ^ 1u, s.abort, tmo))) {
                         ok = false;
                         break;
                     }
-                    uint8_t* sp = s.stages + size_t(stage) * stage_bytes;
-                    uint8_t* sq = sp + p.p_bytes;
+                    const uint32_t sp = stages0 + uint32_t(stage) * stage_bytes;
+                    const uint32_t lead = lead0 + 8u * uint32_t(stage);
                     const int k0 = kb * p.bk;
-                    // Both CTAs' fills complete on the even one's barrier.
-                    const uint32_t fb = mapa_shared(smem_u32(&s.full[stage]), 0);
-                    if (rank == 0) mbar_arrive_expect_tx(&s.full[stage], tx);
-                    if (p.p_mn) {
-                        tma_load_2d_pair_hint(sp, &mapP, fb, p0, k0, pol);
-                        tma_load_2d_pair_hint(sp + kAtom, &mapP, fb, p0 + 64, k0, pol);
-                    } else {
-                        tma_load_2d_pair_hint(sp, &mapP, fb, k0, p0, pol);
-                    }
-                    if (p.q_mn) {
-                        for (int a = 0; a < q_atoms; ++a)
-                            tma_load_2d_pair_hint(sq + a * kAtom, &mapQ, fb, q0 + 64 * a, k0, pol);
-                    } else {
-                        tma_load_2d_pair_hint(sq, &mapQ, fb, k0, q0, pol);
-                    }
+                    if (rank == 0) expect_elected(full0 + 8u * uint32_t(stage), tx);
+                    load_operand<true>(sp, &mapP, lead, p.p_mn, 2, p0, k0, pol);
+                    load_operand<true>(sp + p.p_bytes, &mapQ, lead, p.q_mn, q_atoms, q0, k0, pol);
                     issued_any |= 1u << stage;
                     issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
                 }
-                if (++stage == p.stages) {
+                if (++stage == nstages) {
                     stage = 0;
                     phase ^= 1u;
                 }
@@ -693,32 +736,71 @@ __device__ __forceinline__ void store4(void* base, int64_t at, bool vec, int cnt
     }
 }
 
-template <typename T>
-__device__ __forceinline__ void epilogue_row4(const Epilogue& e, bool vec, int64_t m, int64_t n,
-                                              int cnt, float (&x)[4]) {
-    float t[4];
-    vec = vec && cnt == 4;
-    const float sa = e.sa ? e.sa[m] : 1.f;
+// This CTA's share of the tile's `rows` lines of `cols` values: a line to a warp
+// at a time, four values to a lane, kAhead lines' sums in flight. Bias and
+// column scales are the same for all lines and loaded once.
+template <typename T, int SPLIT>
+__device__ __forceinline__ void join_lines(const TcLinear& p, const float* part, int pitch, int rank,
+                                           int rows, int cols, int64_t m0, int64_t n0) {
+    constexpr int kAhead = SPLIT == 8 ? 2 : 4;
+    constexpr int kWarps = kSplitThreads / 32 * SPLIT;  // of the cluster
+    const Epilogue& e = p.e;
+    const int first = rank * (kSplitThreads / 32) + int(threadIdx.x >> 5);
+    for (int at = 4 * int(threadIdx.x & 31); at < cols; at += 128) {
+        const int cnt = min(4, cols - at);
+        const bool vec = p.vec && cnt == 4;
+        const int64_t n = n0 + at;
+        float bias[4] = {}, sw[4] = {1.f, 1.f, 1.f, 1.f};
+        if (e.bias) load4<T>(e.bias, n, vec, cnt, bias);
+        if (e.sw) load4<float>(e.sw, n, vec, cnt, sw);
+        for (int line = first; line < rows; line += kWarps * kAhead) {
+            float x[kAhead][4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] *= sa;
-    if (e.sw) {
-        load4<float>(e.sw, n, vec, cnt, t);
+            for (int j = 0; j < kAhead; ++j) {
+                // (Past the last line: the last one again, not written.)
+                const float* own = part + min(line + j * kWarps, rows - 1) * pitch + at;
+                float4 v[SPLIT];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] *= t[i];
+                for (int r = 0; r < SPLIT; ++r)
+                    v[r] = SPLIT == 1 ? *reinterpret_cast<const float4*>(own)
+                                      : ld_cluster_f32x4(mapa_shared(smem_u32(own), uint32_t(r)));
+                x[j][0] = v[0].x;
+                x[j][1] = v[0].y;
+                x[j][2] = v[0].z;
+                x[j][3] = v[0].w;
+#pragma unroll
+                for (int r = 1; r < SPLIT; ++r) {
+                    x[j][0] += v[r].x;
+                    x[j][1] += v[r].y;
+                    x[j][2] += v[r].z;
+                    x[j][3] += v[r].w;
+                }
+            }
+            float res[kAhead][4];
+            if (e.R) {
+#pragma unroll
+                for (int j = 0; j < kAhead; ++j) {
+                    const int64_t m = m0 + min(line + j * kWarps, rows - 1);
+                    load4<T>(e.R, m * e.ldr + n, vec, cnt, res[j]);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                if (line + j * kWarps >= rows) break;
+                const int64_t m = m0 + line + j * kWarps;
+                const float sa = e.sa ? e.sa[m] : 1.f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[j][i] = fmaf(x[j][i], sa * sw[i], bias[i]);
+                if (e.Z) store4<T>(e.Z, m * e.ldz + n, vec, cnt, x[j]);
+                act_n(e.act, x[j]);
+                if (e.R) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[j][i] += res[j][i];
+                }
+                store4<T>(e.Y, m * e.ldy + n, vec, cnt, x[j]);
+            }
+        }
     }
-    if (e.bias) {
-        load4<T>(e.bias, n, vec, cnt, t);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] += t[i];
-    }
-    if (e.Z) store4<T>(e.Z, m * e.ldz + n, vec, cnt, x);
-    act_n(e.act, x);
-    if (e.R) {
-        load4<T>(e.R, m * e.ldr + n, vec, cnt, t);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] += t[i];
-    }
-    store4<T>(e.Y, m * e.ldy + n, vec, cnt, x);
 }
 
 template <typename T, bool SWAP>
@@ -734,6 +816,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
     const int p0 = tp * p.bp, q0 = tq * p.bn;
     const int kb0 = int(int64_t(p.k_blocks) * rank / p.split);
     const int kb1 = int(int64_t(p.k_blocks) * (rank + 1) / p.split);
+    const int nk = kb1 - kb0;
     const uint32_t stage_bytes = p.p_bytes + p.q_bytes;
     const uint64_t tmo = p.timeout_ns;
     if (warp == 0 && lane == 0) {
@@ -757,45 +840,36 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
     grid_launch_dependents();
     const uint32_t tmem = *s.tmem_base;
     uint32_t issued_any = 0, issued_parity = 0;
-    if (warp == 0 && lane == 0) {
+    if (warp == 0) {
         const uint64_t pol_p = l2_policy(p.tiles_q == 1 ? 1 : 2), pol_q = l2_policy(2);
         const int q_atoms = (p.bn + 63) / 64, p_atoms = (p.bp + 63) / 64;
         const uint32_t tx = (p.p_mn ? uint32_t(p_atoms) * kAtom : uint32_t(p.bp) * 128u) +
                             (p.q_mn ? uint32_t(q_atoms) * kAtom : uint32_t(p.bn) * 128u);
+        const uint32_t stages0 = smem_u32(s.stages), full0 = smem_u32(s.full);
+        const int nstages = p.stages;
         // Ask L2 for the first stages' boxes before waiting for the previous
         // grid: its writes land in L2 too, so no line there is ever stale.
-        for (int kb = kb0; kb < kb1 && kb < kb0 + p.stages; ++kb) {
-            const int k0 = kb * p.bk;
+        for (int i = 0; i < nk && i < nstages; ++i) {
+            const int k0 = (kb0 + i) * p.bk;
             if (p.p_mn) {
-                for (int a = 0; a < p_atoms; ++a) tma_prefetch_2d(&mapP, p0 + 64 * a, k0);
+                for (int a = 0; a < p_atoms; ++a) prefetch_elected(&mapP, p0 + 64 * a, k0);
             } else {
-                tma_prefetch_2d(&mapP, k0, p0);
+                prefetch_elected(&mapP, k0, p0);
             }
         }
         grid_dependency_wait();
         int stage = 0;
         uint32_t phase = 0;
         for (int kb = kb0; kb < kb1; ++kb) {
-            if (!wait_bounded(&s.empty[stage], phase ^ 1u, s.abort, tmo)) break;
-            uint8_t* sp = s.stages + size_t(stage) * stage_bytes;
-            uint8_t* sq = sp + p.p_bytes;
+            if (!__all_sync(0xffffffffu, wait_bounded(&s.empty[stage], phase ^ 1u, s.abort, tmo))) break;
+            const uint32_t sp = stages0 + uint32_t(stage) * stage_bytes, bar = full0 + 8u * uint32_t(stage);
             const int k0 = kb * p.bk;
-            mbar_arrive_expect_tx(&s.full[stage], tx);
-            if (p.p_mn) {
-                for (int a = 0; a < p_atoms; ++a)
-                    tma_load_2d_hint(sp + a * kAtom, &mapP, &s.full[stage], p0 + 64 * a, k0, pol_p);
-            } else {
-                tma_load_2d_hint(sp, &mapP, &s.full[stage], k0, p0, pol_p);
-            }
-            if (p.q_mn) {
-                for (int a = 0; a < q_atoms; ++a)
-                    tma_load_2d_hint(sq + a * kAtom, &mapQ, &s.full[stage], q0 + 64 * a, k0, pol_q);
-            } else {
-                tma_load_2d_hint(sq, &mapQ, &s.full[stage], k0, q0, pol_q);
-            }
+            expect_elected(bar, tx);
+            load_operand<false>(sp, &mapP, bar, p.p_mn, p_atoms, p0, k0, pol_p);
+            load_operand<false>(sp + p.p_bytes, &mapQ, bar, p.q_mn, q_atoms, q0, k0, pol_q);
             issued_any |= 1u << stage;
             issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
-            if (++stage == p.stages) {
+            if (++stage == nstages) {
                 stage = 0;
                 phase ^= 1u;
             }
@@ -810,11 +884,11 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
         const bool fp8 = p.fp8 != 0;
         int stage = 0;
         uint32_t phase = 0;
-        for (int kb = kb0; kb < kb1; ++kb) {
+        for (int i = 0; i < nk; ++i) {
             if (!__all_sync(0xffffffffu, wait_bounded(&s.full[stage], phase, s.abort, tmo))) break;
             tc_fence_after_sync();
             const uint64_t off = uint64_t(uint32_t(stage) * stage_units);
-            issue_stage<false>(fp8, tmem, dP + off, dQ + off, step_p, step_q, idesc, kb != kb0,
+            issue_stage<false>(fp8, tmem, dP + off, dQ + off, step_p, step_q, idesc, i != 0,
                                empty0 + 8u * uint32_t(stage), 0);
             if (++stage == nstages) {
                 stage = 0;
@@ -857,34 +931,19 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
     }
     tc_fence_before_sync();
     __syncwarp();
-    cluster_sync();
+    if (p.split > 1) cluster_sync();
+    else __syncthreads();
     grid_dependency_wait();
     if (!*s.abort) {
-        const uint32_t mine = smem_u32(part);
-        const int units = (SWAP ? p.bp : p.bn) / 4;  // of four values in a line
         const int64_t M = SWAP ? p.Nq : p.Mp, N = SWAP ? p.Mp : p.Nq;
         const int64_t m0 = SWAP ? q0 : p0, n0 = SWAP ? p0 : q0;
-        for (int u = rank * kSplitThreads + int(threadIdx.x); u < units * lines;
-             u += p.split * kSplitThreads) {
-            const int line = u / units, at = 4 * (u - line * units);
-            const int64_t m = m0 + line, n = n0 + at;
-            if (m >= M || n >= N) continue;
-            const uint32_t addr = mine + 4u * uint32_t(line * pitch + at);
-            float4 v[8];
-#pragma unroll
-            for (int r = 0; r < 8; ++r)
-                if (r < p.split) v[r] = ld_cluster_f32x4(mapa_shared(addr, uint32_t(r)));
-            float x[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
-#pragma unroll
-            for (int r = 1; r < 8; ++r)
-                if (r < p.split) {
-                    x[0] += v[r].x;
-                    x[1] += v[r].y;
-                    x[2] += v[r].z;
-                    x[3] += v[r].w;
-                }
-            const int64_t left = N - n;
-            epilogue_row4<T>(p.e, p.vec != 0, m, n, left < 4 ? int(left) : 4, x);
+        const int cols = int(min(int64_t(SWAP ? p.bp : p.bn), N - n0));
+        const int rows = int(min(int64_t(lines), M - m0));
+        switch (p.split) {
+            case 1: join_lines<T, 1>(p, part, pitch, rank, rows, cols, m0, n0); break;
+            case 2: join_lines<T, 2>(p, part, pitch, rank, rows, cols, m0, n0); break;
+            case 4: join_lines<T, 4>(p, part, pitch, rank, rows, cols, m0, n0); break;
+            default: join_lines<T, 8>(p, part, pitch, rank, rows, cols, m0, n0); break;
         }
     }
     if (*s.abort && warp == 0 && lane == 0)
@@ -892,7 +951,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
             if (issued_any & (1u << i))
                 wait_bounded(&s.full[i], (issued_parity >> i) & 1u, s.abort, tmo, true);
     __syncwarp();
-    cluster_sync();  // peers have read this CTA's partial sums
+    if (p.split > 1) cluster_sync();  // peers have read this CTA's partial sums
     if (warp == 1) {
         tc_fence_after_sync();
         tmem_dealloc<1>(tmem, uint32_t(p.tmem_cols));
@@ -942,7 +1001,7 @@ cudaError_t launch_tc_linear(const TcLinearMaps& maps, const TcLinear& p, int gr
     const size_t ring = size_t(p.stages) * (p.p_bytes + p.q_bytes);
     if (p.stages < 2 || p.stages > 32 || cluster < 1 || cluster > 8 || grid % cluster != 0 ||
         p.bn % 16 != 0 || p.bn > 256 || (p.pair && (p.bn % 32 != 0 || p.group < 1)) ||
-        (!p.pair && (p.bp > 128 || p.bp % 16 != 0 || p.split > p.k_blocks || ring > p.ring_bytes ||
+        (!p.pair && (p.bp > 128 || p.bp % 16 != 0 || p.split > p.k_blocks || (p.split & (p.split - 1)) || ring > p.ring_bytes ||
                      split_partial_bytes(p) > p.ring_bytes ||
                      p.ring_bytes + 8 * (2 * size_t(p.stages) + 1) + 16 > tc_linear_smem(p))))
         return cudaErrorInvalidValue;

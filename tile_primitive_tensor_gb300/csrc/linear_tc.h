@@ -21,6 +21,7 @@ struct TcLinear {
     int tmem_cols;         // split kernel
     int split;             // split kernel: CTAs of a cluster, each a share of K
     int group;             // tile kernel: P tiles in a raster run
+    int k_rotate;          // tile kernel: tiles start at different places of K
     int half_sm;           // split kernel: half of an SM's shared memory, two blocks to an SM
     int tma_out;           // tile kernel: Y, Z and R move by TMA (rows on 16-byte boundaries)
     int swap;              // P holds the output's columns
