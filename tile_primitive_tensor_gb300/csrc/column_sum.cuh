@@ -2,6 +2,8 @@
 #pragma once
 
 #include "elem.cuh"
+#include "launch.cuh"
+#include "ptx.cuh"
 
 namespace tpg {
 namespace {
@@ -12,8 +14,11 @@ __global__ void __launch_bounds__(256) column_sum_kernel(const float* partial, i
     __shared__ float s[8][33];
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int64_t n = int64_t(blockIdx.x) * 32 + lane;
+    grid_launch_dependents();
+    grid_dependency_wait();
     float v = 0.f;
     if (n < cols)
+#pragma unroll 4
         for (int i = w; i < strips; i += 8) v += partial[int64_t(i) * cols + n];
     s[w][lane] = v;
     __syncthreads();
@@ -29,15 +34,15 @@ inline cudaError_t launch_column_sum(const float* partial, int strips, int64_t c
                                      int elem, cudaStream_t stream) {
     const int64_t blocks = (cols + 31) / 32;
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-    const unsigned g = unsigned(blocks);
+    const dim3 g{unsigned(blocks)}, b{256};
     if (elem == TPGEMM_ELEM_F16)
-        column_sum_kernel<<<g, 256, 0, stream>>>(partial, strips, cols, static_cast<__half*>(out));
-    else if (elem == TPGEMM_ELEM_BF16)
-        column_sum_kernel<<<g, 256, 0, stream>>>(partial, strips, cols,
-                                                 static_cast<__nv_bfloat16*>(out));
-    else
-        column_sum_kernel<<<g, 256, 0, stream>>>(partial, strips, cols, static_cast<float*>(out));
-    return cudaGetLastError();
+        return launch_dependent(column_sum_kernel<__half>, g, b, 0, stream, partial, strips, cols,
+                                static_cast<__half*>(out));
+    if (elem == TPGEMM_ELEM_BF16)
+        return launch_dependent(column_sum_kernel<__nv_bfloat16>, g, b, 0, stream, partial, strips, cols,
+                                static_cast<__nv_bfloat16*>(out));
+    return launch_dependent(column_sum_kernel<float>, g, b, 0, stream, partial, strips, cols,
+                            static_cast<float*>(out));
 }
 
 }  // namespace

@@ -87,7 +87,9 @@ __global__ void __launch_bounds__(32 * kWarps) linear_few_kernel(const __grid_co
     constexpr int E = 16 / sizeof(T);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
     const int rank = int(cluster_ctarank());
-    const int64_t n0 = int64_t(blockIdx.x / split) * kRows;
+    // (More than 16 rows of A, 16 to a group of blocks, only come with K = 0.)
+    const int64_t tiles = (op.N + kRows - 1) / kRows, tile = blockIdx.x / split;
+    const int64_t n0 = tile % tiles * kRows, m0 = tile / tiles * kFewTokens;
     const T* W = static_cast<const T*>(op.b.p);
     const T* A = static_cast<const T*>(op.a.p);
     const bool live_lo = n0 + g < op.N, live_hi = n0 + g + 8 < op.N;
@@ -108,8 +110,8 @@ __global__ void __launch_bounds__(32 * kWarps) linear_few_kernel(const __grid_co
         }
 #pragma unroll
         for (int u = 0; u < TT; ++u) {
-            const bool live = 8 * u + g < op.M;
-            const T* row = A + (live ? 8 * u + g : 0) * op.a.ld;
+            const bool live = m0 + 8 * u + g < op.M;
+            const T* row = A + (live ? m0 + 8 * u + g : 0) * op.a.ld;
 #pragma unroll
             for (int i = 0; i < kRun; ++i) x[u][i] = load16<T, VEC>(row, live, k0 + (4 * i + t4) * E, op.K);
         }
@@ -143,9 +145,9 @@ __global__ void __launch_bounds__(32 * kWarps) linear_few_kernel(const __grid_co
             }
         }
     }
-    if (token < op.M && token % split == rank && n0 + row < op.N)
+    if (m0 + token < op.M && token % split == rank && n0 + row < op.N)
         with_act(op.e.act, [&](auto act) {
-            epilogue_one<O, decltype(act)::value>(op.e, token, n0 + row, v);
+            epilogue_one<O, decltype(act)::value>(op.e, m0 + token, n0 + row, v);
         });
     if (split > 1) {
         __syncwarp();
@@ -157,7 +159,7 @@ template <typename T, typename O, int TT>
 cudaError_t launch_few(const LinearOp& op, int split, cudaStream_t stream) {
     const bool vec = tma_rows(op.a, op.M, op.K, op.dtype) && tma_rows(op.b, op.N, op.K, op.dtype);
     auto fn = vec ? linear_few_kernel<T, O, TT, true> : linear_few_kernel<T, O, TT, false>;
-    const int64_t blocks = (op.N + kRows - 1) / kRows * split;
+    const int64_t blocks = (op.N + kRows - 1) / kRows * ((op.M + kFewTokens - 1) / kFewTokens) * split;
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(blocks));
@@ -190,6 +192,14 @@ cudaError_t launch_typed(const LinearOp& op, int split, cudaStream_t stream) {
 }  // namespace
 
 bool linear_few_takes(const LinearOp& op) { return op.M <= kFewTokens && !op.a.mn && !op.b.mn; }
+
+// Against the tcgen05 kernels, which stream large weights faster and do not
+// widen 8-bit ones, but take 4.3 us at the least.
+bool linear_few_wins(const LinearOp& op) {
+    if (!tma_rows(op.a, op.M, op.K, op.dtype) || !tma_rows(op.b, op.N, op.K, op.dtype)) return true;
+    const int64_t weights = op.N * op.K * elem_size(op.dtype);
+    return weights <= (elem_size(op.dtype) == 1 ? int64_t(8) << 20 : int64_t(24) << 20);
+}
 
 cudaError_t launch_linear_few(const LinearOp& op, int sms, cudaStream_t stream) {
     // Clusters share a block's rows of K while that leaves every warp a run of

@@ -130,15 +130,56 @@ tpgemm_status check_act(int act) {
         if (s_ != TPGEMM_OK) return s_;     \
     } while (0)
 
-// One product on the kernel that suits it.
-tpgemm_status run_product(const tpg::LinearOp& op, int sms, cudaStream_t st) {
+// Aligned copies of a product's operands in a workspace. An operand whose rows
+// do not start on 16-byte boundaries cannot be read by TMA: it is copied to
+// rows that do, which moves its bytes twice more, against a product on scalar
+// loads (37 x 1000 x 1001 f16: ALIGN_NOTE).
+struct Aligned {
+    size_t at = 0;      // byte offset in the workspace
+    int64_t ld = 0;     // row stride of the copy, elements
+    bool copy = false;
+};
+
+Aligned plan_aligned(const tpg::Operand& o, int64_t rows, int64_t K, int dtype, size_t* total) {
+    Aligned a;
+    a.copy = !tpg::tma_rows(o, rows, K, dtype);
+    if (!a.copy) return a;
+    const int64_t lines = o.mn ? K : rows, len = o.mn ? rows : K;
+    const size_t es = size_t(elem_size(dtype));
+    a.ld = int64_t(align_up(size_t(len) * es, 16) / es);
+    a.at = *total;
+    *total = align_up(*total + size_t(lines) * size_t(a.ld) * es, 256);
+    return a;
+}
+
+// The operand itself or, copied there first, its place in the workspace.
+tpgemm_status use_aligned(const Aligned& a, tpg::Operand* o, int64_t rows, int64_t K, int dtype,
+                          uint8_t* ws, cudaStream_t st) {
+    if (!a.copy) return TPGEMM_OK;
+    const int64_t lines = o->mn ? K : rows, len = o->mn ? rows : K;
+    const int64_t es = elem_size(dtype);
+    TPG_TRY(launched(tpg::launch_align_rows(o->p, lines, len * es, o->ld * es, ws + a.at, a.ld * es, st),
+                     "operand copy launch"));
+    o->p = ws + a.at;
+    o->ld = a.ld;
+    return TPGEMM_OK;
+}
+
+// Which product kernel takes it: the few-token one, or the tcgen05 ones. Few
+// tokens on aligned rows run faster on tcgen05 once the weights are large.
+bool takes_few(const tpg::LinearOp& op) {
+    if (op.K == 0) return true;
+    if (!tpg::linear_few_takes(op)) return false;
     const int path = tpg::linear_tuning().path;
-    if (tpg::linear_few_takes(op) && (path < 0 || path == tpg::kLinearFew || op.K == 0))
+    if (path >= 0) return path == tpg::kLinearFew;
+    return tpg::linear_few_wins(op);
+}
+
+// One product; its operands are aligned unless the few-token kernel takes it.
+tpgemm_status run_product(const tpg::LinearOp& op, int sms, cudaStream_t st) {
+    if (takes_few(op))
         return launched(tpg::launch_linear_few(op, sms, st), "linear kernel launch");
-    if (op.K > 0 && tpg::tma_rows(op.a, op.M, op.K, op.dtype) &&
-        tpg::tma_rows(op.b, op.N, op.K, op.dtype))
-        return tpg::run_linear_tc(op, sms, st);
-    return launched(tpg::launch_linear_simple(op, st), "linear kernel launch");
+    return tpg::run_linear_tc(op, sms, st);
 }
 
 tpgemm_status check_linear_desc(const tpgemm_linear_desc* d) {
@@ -155,28 +196,58 @@ tpgemm_status check_linear_desc(const tpgemm_linear_desc* d) {
     return check_act(d->act);
 }
 
+tpg::LinearOp linear_op(const void* A, const void* W, const tpgemm_linear_desc& d) {
+    tpg::LinearOp op{};
+    op.M = d.M;
+    op.N = d.N;
+    op.K = d.K;
+    op.dtype = d.dtype;
+    op.a = {A, dense(d.lda, d.K), 0};
+    op.b = {W, dense(d.ldw, d.K), 0};
+    op.e.act = d.act;
+    op.e.out = d.out;
+    return op;
+}
+
+struct LinearLayout {
+    size_t total = 0;
+    Aligned a, w;
+};
+
+LinearLayout linear_layout(const tpg::LinearOp& op) {
+    LinearLayout L;
+    if (takes_few(op)) return L;
+    L.a = plan_aligned(op.a, op.M, op.K, op.dtype, &L.total);
+    L.w = plan_aligned(op.b, op.N, op.K, op.dtype, &L.total);
+    return L;
+}
+
 // ----------------------------------------------------- linear layer, backward
 struct GradLayout {
     size_t dz = 0, partial = 0, total = 0;
     int64_t lddz = 0;
     int strips = 0;
+    Aligned dy, a, w;  // copies (dY's only where it is dZ itself)
 };
 
 GradLayout grad_layout(const void* dY, const void* A, const void* W,
                        const tpgemm_linear_grad_desc& d) {
-    (void)dY;
-    (void)A;
-    (void)W;
     GradLayout L;
     if (d.M == 0 || d.N == 0) return L;
     if (d.act != TPGEMM_ACT_NONE) {
         L.lddz = int64_t(align_up(size_t(d.N), 8));
         L.dz = L.total;
         L.total = align_up(L.total + size_t(d.M) * size_t(L.lddz) * 2, 256);
+    } else if (d.K > 0) {
+        L.dy = plan_aligned({dY, dense(d.lddy, d.N), 0}, d.M, d.N, d.dtype, &L.total);
     }
     L.strips = tpg::act_grad_strips(d.M, d.N);
     L.partial = L.total;
     L.total = align_up(L.total + size_t(L.strips) * size_t(d.N) * 4, 256);
+    if (d.K > 0) {
+        L.a = plan_aligned({A, dense(d.lda, d.K), 0}, d.M, d.K, d.dtype, &L.total);
+        L.w = plan_aligned({W, dense(d.ldw, d.K), 0}, d.N, d.K, d.dtype, &L.total);
+    }
     return L;
 }
 
@@ -203,10 +274,9 @@ size_t rmsnorm_grad_ws(int64_t rows, int64_t cols) {
 extern "C" {
 
 size_t tpgemm_linear_workspace_bytes(const void* A, const void* W, const tpgemm_linear_desc* d) {
-    (void)A;
-    (void)W;
-    (void)d;
-    return 0;
+    tpg::set_error_detail("");
+    if (check_linear_desc(d) != TPGEMM_OK || d->M == 0 || d->N == 0) return 0;
+    return linear_layout(linear_op(A, W, *d)).total;
 }
 
 tpgemm_status tpgemm_linear(void* Y, void* Z, const void* A, const void* W, const float* scale_a,
@@ -231,15 +301,19 @@ tpgemm_status tpgemm_linear(void* Y, void* Z, const void* A, const void* W, cons
     for (int i = 0; i < 6; ++i) TPG_TRY(check_mat(in[i], i < 2));
     const Pair y_is_r[1] = {{0, 2}};
     TPG_TRY(check_overlap(out, 2, in, 6, y_is_r, 1));
-    const size_t need = tpgemm_linear_workspace_bytes(A, W, d);
+    tpg::LinearOp op = linear_op(A, W, *d);
+    op.e = {Y, Z, R, bias, scale_a, scale_w, out[0].ld, out[1].ld, in[2].ld, d->act, d->out};
+    const LinearLayout L = linear_layout(op);
+    const size_t need = L.total;
     const Mat all[8] = {out[0], out[1], in[0], in[1], in[2], in[3], in[4], in[5]};
     TPG_TRY(check_workspace(workspace, workspace_bytes, need, all, 8));
     int sms = 0;
     TPG_TRY(tpg::require_device(&sms));
-    tpg::LinearOp op{M, N, K, d->dtype, {A, in[0].ld, 0}, {W, in[1].ld, 0},
-                     {Y, Z, R, bias, scale_a, scale_w, out[0].ld, out[1].ld, in[2].ld, d->act,
-                      d->out}};
-    return run_product(op, sms, static_cast<cudaStream_t>(stream));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    TPG_TRY(use_aligned(L.a, &op.a, M, K, d->dtype, ws, st));
+    TPG_TRY(use_aligned(L.w, &op.b, N, K, d->dtype, ws, st));
+    return run_product(op, sms, st);
 }
 
 size_t tpgemm_linear_backward_workspace_bytes(const void* dY, const void* A, const void* W,
@@ -308,14 +382,19 @@ tpgemm_status tpgemm_linear_backward(void* dA, void* dW, void* dbias, const void
         lddz = L.lddz;
     }
     if (K == 0) return TPGEMM_OK;
+    if (!dA && !dW) return TPGEMM_OK;
+    tpg::Operand oz{dz, lddz, 0}, oa{A, in[1].ld, 0}, ow{W, in[2].ld, 0};
+    TPG_TRY(use_aligned(L.dy, &oz, M, N, d->dtype, ws, st));
     if (dA) {  // [M, K] = dZ [M, N] . W: the reduction runs along W's rows
-        tpg::LinearOp op{M, K, N, d->dtype, {dz, lddz, 0}, {W, in[2].ld, 1},
+        TPG_TRY(use_aligned(L.w, &ow, N, K, d->dtype, ws, st));
+        tpg::LinearOp op{M, K, N, d->dtype, oz, {ow.p, ow.ld, 1},
                          {dA, nullptr, nullptr, nullptr, nullptr, nullptr, out[0].ld, 0, 0,
                           TPGEMM_ACT_NONE, d->dtype}};
         TPG_TRY(run_product(op, sms, st));
     }
     if (dW) {  // [N, K] = dZ^T . A: along the rows of both
-        tpg::LinearOp op{N, K, M, d->dtype, {dz, lddz, 1}, {A, in[1].ld, 1},
+        TPG_TRY(use_aligned(L.a, &oa, M, K, d->dtype, ws, st));
+        tpg::LinearOp op{N, K, M, d->dtype, {oz.p, oz.ld, 1}, {oa.p, oa.ld, 1},
                          {dW, nullptr, nullptr, nullptr, nullptr, nullptr, out[1].ld, 0, 0,
                           TPGEMM_ACT_NONE, d->grad}};
         TPG_TRY(run_product(op, sms, st));

@@ -64,8 +64,6 @@ struct LinearOp {
     Epilogue e;
 };
 
-cudaError_t launch_linear_simple(const LinearOp& op, cudaStream_t stream);
-
 // The product on the tcgen05 kernels (linear_plan.cu); its operands' rows start
 // on 16-byte boundaries (tma_rows). K >= 1.
 tpgemm_status run_linear_tc(const LinearOp& op, int sms, cudaStream_t stream);
@@ -74,6 +72,7 @@ tpgemm_status run_linear_tc(const LinearOp& op, int sms, cudaStream_t stream);
 // alignment, any K.
 constexpr int kFewTokens = 16;
 bool linear_few_takes(const LinearOp& op);
+bool linear_few_wins(const LinearOp& op);
 cudaError_t launch_linear_few(const LinearOp& op, int sms, cudaStream_t stream);
 
 bool tma_rows(const Operand& o, int64_t rows, int64_t K, int dtype);
@@ -94,6 +93,11 @@ struct ActGradOp {
 };
 int act_grad_strips(int64_t M, int64_t N);
 cudaError_t launch_act_grad(const ActGradOp& op, cudaStream_t stream);
+
+// Copies rows of `bytes` bytes, `pitch` bytes apart, to rows dst_pitch apart
+// (dst and dst_pitch multiples of 16, dst_pitch >= bytes rounded up to 16).
+cudaError_t launch_align_rows(const void* src, int64_t rows, int64_t bytes, int64_t pitch, void* dst,
+                              int64_t dst_pitch, cudaStream_t stream);
 
 // ---- root-mean-square norm ----
 struct RmsNormOp {
