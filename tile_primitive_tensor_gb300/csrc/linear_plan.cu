@@ -38,9 +38,26 @@ tpgemm_status max_clusters(const TcLinear& p, int* clusters) {
 // Times in ns at the clocks that products run at here (1.85 GHz): an SM takes
 // in 64 bytes a clock, and a 128-row MMA of 16 x 16-bit K takes bn / 2 clocks,
 // at least 45 (its P operand; measured in isolation). Memory delivers about
-// 6 kB a ns to all SMs together.
+// 6 kB a ns to all SMs together, L2 about 9.5 to CTAs that each read a P tile
+// of their own. A stage asked for comes back after about 1.5 us under load.
 constexpr double kClock = 1.85;
 constexpr double kMemory = 6000;
+constexpr double kL2 = 9500;
+constexpr double kLatency = 1500;
+
+// Shared bytes of one split stage. P tiles of fewer than 128 rows leave the MMA
+// to read on into the bytes behind them: their lanes' results are not used.
+uint32_t split_p_bytes(int bp, bool mn) { return mn ? uint32_t((bp + 63) / 64) * 8192u : uint32_t(bp) * 128u; }
+uint32_t split_q_bytes(int bn, bool mn) { return mn ? uint32_t((bn + 63) / 64) * 8192u : uint32_t(bn) * 128u; }
+
+// Stages of a split CTA in `have` bytes of shared memory (16 KB behind the last
+// P tile's start are read at most).
+int split_stages(size_t have, uint32_t p_bytes, uint32_t q_bytes) {
+    const size_t over = 16384 > p_bytes + q_bytes ? 16384 - (p_bytes + q_bytes) : 0;
+    return int(std::min<size_t>(12, (have - over) / (p_bytes + q_bytes)));
+}
+
+constexpr size_t kBarrierBytes = 512;
 
 struct Choice {
     double ns = 1e30;
@@ -114,11 +131,13 @@ bool tma_outputs(const Epilogue& e, int64_t M) {
 // at bn = 256 is the tensor rate too; and the last epilogue.
 Choice plan_tile(const LinearOp& op, int64_t kb, int sms, const LinearTuning& t) {
     Choice best;
+    const double memory = double((op.M + op.N) * op.K * elem_size(op.dtype) + 2 * op.M * op.N) / kMemory;
     for (int bn = 256; bn >= 32; bn -= 32) {
         if (t.bn > 0 && bn != t.bn) continue;
         const int64_t tiles = ceil_div(op.M, 256) * ceil_div(op.N, bn);
         const double stage = (256 + bn) * (bn == 256 ? 1.01 : 1.07) / kClock;
-        const double ns = 3500 + bn * 12 + double(ceil_div(tiles, sms / 2)) * (double(kb) * stage + 200);
+        const double loop = std::max(double(ceil_div(tiles, sms / 2)) * (double(kb) * stage + 200), memory);
+        const double ns = 3500 + bn * 12 + loop;
         if (ns < best.ns) {
             best.ns = ns;
             best.pair = 1;
@@ -134,7 +153,7 @@ tpgemm_status plan_split(const LinearOp& op, int64_t kb, int sms, const LinearTu
     // The output's longer side along the lanes.
     const bool swap = op.N >= op.M;
     const int64_t Mp = swap ? op.N : op.M, Nq = swap ? op.M : op.N;
-    const bool p_mn = swap ? op.b.mn : op.a.mn;
+    const bool p_mn = swap ? op.b.mn : op.a.mn, q_mn = swap ? op.a.mn : op.b.mn;
     const int64_t es = elem_size(op.dtype);
     const double memory = double((op.M + op.N) * op.K * es + 2 * op.M * op.N) / kMemory;
     // Q in tiles of equal width, 256 at most.
@@ -147,8 +166,10 @@ tpgemm_status plan_split(const LinearOp& op, int64_t kb, int sms, const LinearTu
         if (p_mn && p.bp % 64) continue;
         if (t.bp > 0 && p.bp != t.bp) continue;
         // Two blocks to an SM where the partial sums and three stages fit half of it.
-        const size_t stage = size_t(p.bp + p.bn) * 128 + 16384;  // (atoms and unused rows)
-        p.half_sm = std::max(split_partial_bytes(p), 3 * stage) + 512 <= kSplitHalfSmem;
+        const uint32_t p_bytes = split_p_bytes(p.bp, p_mn), q_bytes = split_q_bytes(p.bn, q_mn);
+        const size_t half = kSplitHalfSmem - kBarrierBytes;
+        p.half_sm = split_partial_bytes(p) <= half && split_stages(half, p_bytes, q_bytes) >= 3;
+        const int stages = split_stages(p.half_sm ? half : size_t(kTcMaxSmem) - kBarrierBytes, p_bytes, q_bytes);
         // Clusters of other sizes than these leave SMs of a group without a place.
         const int forced = t.split == 2 || t.split == 4 || t.split == 8 || t.split == 1 ? t.split : 0;
         for (p.split = 1; p.split <= 8 && p.split <= kb; p.split *= 2) {
@@ -158,16 +179,18 @@ tpgemm_status plan_split(const LinearOp& op, int64_t kb, int sms, const LinearTu
             int fit = 0;
             const tpgemm_status s = max_clusters(p, &fit);
             if (s != TPGEMM_OK) return s;
-            const int64_t rounds = ceil_div(ctas, int64_t(fit) * p.split);
-            const int64_t each = rounds > 1 ? rounds * (p.half_sm ? 2 : 1) : ceil_div(ctas, sms);
+            // (The query counts one block of a tensor-memory kernel to an SM;
+            // two of half its shared memory do run there side by side.)
+            const int64_t per_sm = p.half_sm ? 2 : 1;
+            const int64_t rounds = ceil_div(ctas, (int64_t(fit) * per_sm + per_sm) * p.split);
+            const int64_t each = std::max(ceil_div(ctas, sms), rounds > 1 ? rounds * per_sm : 1);
             const double clocks = std::max(2.0 * (p.bp + p.bn), 4.0 * std::max(45, p.bn / 2));
             const double share = double(ceil_div(kb, p.split));
-            // A CTA's stages in flight come back after about 1.5 us under load.
-            const double alone = double(rounds) * share * (p.bp + p.bn) * 128 * 1500 /
-                                 double(p.half_sm ? kSplitHalfSmem : size_t(kTcMaxSmem));
+            const double alone = double(rounds) * share * kLatency / stages;
             const double busy = double(each) * share * clocks / kClock;
-            const double join = (p.split > 1 ? 900 + 60 * p.split : 0) + p.bp * p.bn * 4 / 40 / kClock;
-            const double ns = 3000 + std::max(std::max(busy, alone), memory) +
+            const double l2 = double(ctas) * share * (p.bp + p.bn) * 128 / kL2;
+            const double join = (p.split > 1 ? 600 + 60 * p.split : 0) + p.bp * p.bn * 4 / 40 / kClock;
+            const double ns = 3000 + std::max(std::max(busy, alone), std::max(memory, l2)) +
                               double(rounds) * join;
             if (ns < best->ns) {
                 best->ns = ns;
@@ -218,8 +241,8 @@ tpgemm_status run_linear_tc(const LinearOp& op, int sms, cudaStream_t stream) {
     p.idesc = idesc_f16_f32(op.dtype == TPGEMM_ELEM_BF16 || op.dtype == TPGEMM_ELEM_E5M2, P.mn != 0,
                             Q.mn != 0, p.pair ? 256 : 128, p.bn);
     const int q_rows = p.pair ? p.bn / 2 : p.bn;
-    p.p_bytes = 16384;
-    p.q_bytes = p.q_mn ? uint32_t((q_rows + 63) / 64) * 8192u : uint32_t(q_rows) * 128u;
+    p.p_bytes = p.pair ? 16384u : split_p_bytes(p.bp, P.mn != 0);
+    p.q_bytes = split_q_bytes(q_rows, Q.mn != 0);
     const int64_t tiles_p = ceil_div(p.Mp, p.pair ? 256 : p.bp);
     const int64_t tiles_q = ceil_div(p.Nq, p.bn);
     if (tiles_p * tiles_q * p.split > 0x1fffffff)
@@ -227,7 +250,7 @@ tpgemm_status run_linear_tc(const LinearOp& op, int sms, cudaStream_t stream) {
     p.tiles_p = int(tiles_p);
     p.tiles_q = int(tiles_q);
     p.tiles = int(tiles_p * tiles_q);
-    const size_t budget = size_t(kTcMaxSmem) - 512;  // (barriers)
+    const size_t budget = size_t(kTcMaxSmem) - kBarrierBytes;
     int grid;
     if (p.pair) {
         p.stages = int(std::min<size_t>(8, (budget - kTileStagingBytes) / (p.p_bytes + p.q_bytes)));
@@ -239,10 +262,10 @@ tpgemm_status run_linear_tc(const LinearOp& op, int sms, cudaStream_t stream) {
         if (s != TPGEMM_OK) return s;
         grid = 2 * std::min(p.tiles, clusters);
     } else {
-        const size_t have = p.half_sm ? kSplitHalfSmem - 512 : budget;
-        p.stages = int(std::min<size_t>(12, have / (p.p_bytes + p.q_bytes)));
+        p.stages = split_stages(p.half_sm ? kSplitHalfSmem - kBarrierBytes : budget, p.p_bytes, p.q_bytes);
         p.ring_bytes = std::max(uint32_t(p.stages) * (p.p_bytes + p.q_bytes),
                                 uint32_t((split_partial_bytes(p) + 1023) / 1024 * 1024));
+        p.ring_bytes = std::max(p.ring_bytes, uint32_t(p.stages - 1) * (p.p_bytes + p.q_bytes) + 16384u);
         p.tmem_cols = 32;
         while (p.tmem_cols < 32 * ((p.bn + 31) / 32)) p.tmem_cols *= 2;
         grid = p.tiles * p.split;

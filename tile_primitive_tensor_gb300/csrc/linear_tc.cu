@@ -996,6 +996,17 @@ size_t tc_linear_smem(const TcLinear& p) {
     return p.half_sm ? kSplitHalfSmem : size_t(kTcMaxSmem);
 }
 
+namespace {
+// Lets a kernel use, and the occupancy query count with, all shared memory.
+cudaError_t allow_smem(const void* fn) {
+    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcMaxSmem);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(fn, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                 cudaSharedmemCarveoutMaxShared);
+    return e;
+}
+}  // namespace
+
 cudaError_t launch_tc_linear(const TcLinearMaps& maps, const TcLinear& p, int grid, cudaStream_t stream) {
     const int cluster = cluster_of(p);
     const size_t ring = size_t(p.stages) * (p.p_bytes + p.q_bytes);
@@ -1009,8 +1020,7 @@ cudaError_t launch_tc_linear(const TcLinearMaps& maps, const TcLinear& p, int gr
     if (smem > size_t(kTcMaxSmem)) return cudaErrorInvalidConfiguration;
     const TileFn tile = pick_tile(p);
     const SplitFn split = pick_split(p);
-    cudaError_t e = p.pair ? cudaFuncSetAttribute(tile, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcMaxSmem)
-                           : cudaFuncSetAttribute(split, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcMaxSmem);
+    cudaError_t e = allow_smem(p.pair ? reinterpret_cast<const void*>(tile) : reinterpret_cast<const void*>(split));
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(grid));
@@ -1030,7 +1040,7 @@ cudaError_t launch_tc_linear(const TcLinearMaps& maps, const TcLinear& p, int gr
 cudaError_t tc_linear_max_clusters(const TcLinear& p, int* clusters) {
     const void* fn = p.pair ? reinterpret_cast<const void*>(pick_tile(p))
                             : reinterpret_cast<const void*>(pick_split(p));
-    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcMaxSmem);
+    cudaError_t e = allow_smem(fn);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(cluster_of(p)));
