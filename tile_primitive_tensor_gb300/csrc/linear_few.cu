@@ -194,11 +194,13 @@ cudaError_t launch_typed(const LinearOp& op, int split, cudaStream_t stream) {
 bool linear_few_takes(const LinearOp& op) { return op.M <= kFewTokens && !op.a.mn && !op.b.mn; }
 
 // Against the tcgen05 kernels, which stream large weights faster and do not
-// widen 8-bit ones, but take 4.3 us at the least.
+// widen 8-bit ones, but take 4.3 us at the least (one token, this / tcgen05:
+// 1024 x 1024 bf16 2.5 / 4.4 us, 4096 x 4096 8.7 / 8.2, 4096 x 16384 28.1 / 21.3;
+// 16384 x 4096 e4m3 19.8 / 12.4).
 bool linear_few_wins(const LinearOp& op) {
     if (!tma_rows(op.a, op.M, op.K, op.dtype) || !tma_rows(op.b, op.N, op.K, op.dtype)) return true;
     const int64_t weights = op.N * op.K * elem_size(op.dtype);
-    return weights <= (elem_size(op.dtype) == 1 ? int64_t(8) << 20 : int64_t(24) << 20);
+    return weights <= (elem_size(op.dtype) == 1 ? int64_t(12) << 20 : int64_t(40) << 20);
 }
 
 cudaError_t launch_linear_few(const LinearOp& op, int sms, cudaStream_t stream) {

@@ -12,38 +12,34 @@ namespace {
 
 constexpr int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Clusters of the kernel that fit the device at once, asked once per device,
-// cluster size and shared-memory size (clusters are placed within groups of
-// SMs, so they can be fewer than the SMs divided by their size).
-tpgemm_status max_clusters(const TcLinear& p, int* clusters) {
+// CTA pairs of the tile kernel that fit the device at once, asked once per
+// device (all variants hold the same threads and nearly all shared memory).
+tpgemm_status max_pairs(const TcLinear& p, int* pairs) {
     static std::mutex m;
-    static int cache[64][3][9] = {};
+    static int cache[64] = {};
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev < 0 || dev >= 64) return fail_with(TPGEMM_ERR_ARCH, "device index %d unsupported", dev);
     std::lock_guard<std::mutex> lock(m);
-    int& n = cache[dev][p.pair ? 0 : p.half_sm ? 1 : 2][p.pair ? 2 : p.split];
+    int& n = cache[dev];
     if (!n) {
-        const cudaError_t e = tc_linear_max_clusters(p, &n);
+        const cudaError_t e = tc_linear_max_pairs(p, &n);
         if (e != cudaSuccess || n <= 0) {
             n = 0;
             return fail_with(TPGEMM_ERR_LAUNCH, "cluster occupancy query failed: %s",
                              cudaGetErrorString(e));
         }
     }
-    *clusters = n;
+    *pairs = n;
     return TPGEMM_OK;
 }
 
-// Times in ns at the clocks that products run at here (1.85 GHz): an SM takes
-// in 64 bytes a clock, and a 128-row MMA of 16 x 16-bit K takes bn / 2 clocks,
-// at least 45 (its P operand; measured in isolation). Memory delivers about
-// 6 kB a ns to all SMs together, L2 about 9.5 to CTAs that each read a P tile
-// of their own. A stage asked for comes back after about 1.5 us under load.
+// The models below are in ns at the clocks that products run at here (1.85
+// GHz): an SM takes in 64 bytes a clock; memory delivers about 5.5 kB a ns to
+// all SMs together, L2 about 11 to CTAs that each read a P tile of their own.
 constexpr double kClock = 1.85;
-constexpr double kMemory = 6000;
-constexpr double kL2 = 9500;
-constexpr double kLatency = 1500;
+constexpr double kMemory = 5500;
+constexpr double kL2 = 11000;
 
 // Shared bytes of one split stage. P tiles of fewer than 128 rows leave the MMA
 // to read on into the bytes behind them: their lanes' results are not used.
@@ -126,16 +122,21 @@ bool tma_outputs(const Epilogue& e, int64_t M) {
     return rows16(e.Y, e.ldy) && rows16(e.Z, e.ldz) && rows16(e.R, e.ldr);
 }
 
-// Time of the tile kernel: waves of 256 x bn tiles, each K stage bound by what
-// an SM takes in (128 + bn / 2 rows of 128 bytes; 7 % over that measured), which
-// at bn = 256 is the tensor rate too; and the last epilogue.
+double memory_ns(const LinearOp& op) {
+    return double((op.M + op.N) * op.K * elem_size(op.dtype) + 2 * op.M * op.N) / kMemory;
+}
+
+// The tile kernel: waves of 256 x bn tiles. A K stage is bound by what an SM
+// takes in (128 + bn / 2 rows of 128 bytes; 7 % over that measured), which at
+// bn = 256 is the tensor rate too, and takes 225 ns at the least (512 x 4096 x
+// 4096 bf16: 20.3 us at bn = 128, 24.0 at 256; 4096^3: 74.8 at 224, 78.8 at 256).
 Choice plan_tile(const LinearOp& op, int64_t kb, int sms, const LinearTuning& t) {
     Choice best;
-    const double memory = double((op.M + op.N) * op.K * elem_size(op.dtype) + 2 * op.M * op.N) / kMemory;
+    const double memory = memory_ns(op);
     for (int bn = 256; bn >= 32; bn -= 32) {
         if (t.bn > 0 && bn != t.bn) continue;
         const int64_t tiles = ceil_div(op.M, 256) * ceil_div(op.N, bn);
-        const double stage = (256 + bn) * (bn == 256 ? 1.01 : 1.07) / kClock;
+        const double stage = std::max(225.0, (256 + bn) * (bn == 256 ? 1.01 : 1.07) / kClock);
         const double loop = std::max(double(ceil_div(tiles, sms / 2)) * (double(kb) * stage + 200), memory);
         const double ns = 3500 + bn * 12 + loop;
         if (ns < best.ns) {
@@ -147,62 +148,58 @@ Choice plan_tile(const LinearOp& op, int64_t kb, int sms, const LinearTuning& t)
     return best;
 }
 
-// Time of the split kernel: tiles x split CTAs, each taking in its share of the
-// operands, no faster than memory delivers them; then the join.
-tpgemm_status plan_split(const LinearOp& op, int64_t kb, int sms, const LinearTuning& t, Choice* best) {
-    // The output's longer side along the lanes.
+// Blocks that run at once in clusters of `split` (placed within groups of SMs:
+// 76 of 2, 36 of 4 and 15 of 8 blocks that have an SM each).
+int64_t places(int split, bool half_sm) {
+    return (split <= 2 ? 152 : split == 4 ? 144 : 120) * (half_sm ? 2 : 1);
+}
+
+// The split kernel. Blocks take half of an SM's shared memory while that holds
+// five stages, and are then two to an SM; the tile's height and the split are
+// those that fill the most of those places, 128 rows counting a fifth more, since shorter
+// boxes stream more slowly (17 x 4096 x 4096 bf16, split / rows: 8 / 128 8.1 us,
+// 4 / 128 8.5, 2 / 64 13.9; 144 rows: 4 / 128 12.3, 2 / 64 15.4).
+Choice plan_split(const LinearOp& op, int64_t kb, const LinearTuning& t) {
+    Choice best;
+    // The output's longer side along the lanes; Q in tiles of equal width.
     const bool swap = op.N >= op.M;
     const int64_t Mp = swap ? op.N : op.M, Nq = swap ? op.M : op.N;
     const bool p_mn = swap ? op.b.mn : op.a.mn, q_mn = swap ? op.a.mn : op.b.mn;
-    const int64_t es = elem_size(op.dtype);
-    const double memory = double((op.M + op.N) * op.K * es + 2 * op.M * op.N) / kMemory;
-    // Q in tiles of equal width, 256 at most.
     const int64_t tiles_q = ceil_div(Nq, 256);
     TcLinear p{};
     p.swap = swap;
     p.bn = int(ceil_div(ceil_div(Nq, tiles_q), 16) * 16);
-    p.e.out = op.e.out;
-    for (p.bp = 128; p.bp >= 64; p.bp -= 16) {
-        if (p_mn && p.bp % 64) continue;
-        if (t.bp > 0 && p.bp != t.bp) continue;
-        // Two blocks to an SM where the partial sums and three stages fit half of it.
-        const uint32_t p_bytes = split_p_bytes(p.bp, p_mn), q_bytes = split_q_bytes(p.bn, q_mn);
+    double most = -1;
+    for (int bp = 128; bp >= 64; bp -= 16) {
+        if (t.bp > 0 ? bp != t.bp : bp == 80) continue;
+        if (p_mn && bp % 64) continue;
+        p.bp = bp;
+        const uint32_t p_bytes = split_p_bytes(bp, p_mn), q_bytes = split_q_bytes(p.bn, q_mn);
         const size_t half = kSplitHalfSmem - kBarrierBytes;
-        p.half_sm = split_partial_bytes(p) <= half && split_stages(half, p_bytes, q_bytes) >= 3;
-        const int stages = split_stages(p.half_sm ? half : size_t(kTcMaxSmem) - kBarrierBytes, p_bytes, q_bytes);
-        // Clusters of other sizes than these leave SMs of a group without a place.
-        const int forced = t.split == 2 || t.split == 4 || t.split == 8 || t.split == 1 ? t.split : 0;
-        for (p.split = 1; p.split <= 8 && p.split <= kb; p.split *= 2) {
-            if (forced && p.split != forced && p.split * 2 <= kb && p.split < forced) continue;
-            if (forced && p.split > forced) break;
-            const int64_t ctas = ceil_div(Mp, p.bp) * tiles_q * p.split;
-            int fit = 0;
-            const tpgemm_status s = max_clusters(p, &fit);
-            if (s != TPGEMM_OK) return s;
-            // (The query counts one block of a tensor-memory kernel to an SM;
-            // two of half its shared memory do run there side by side.)
-            const int64_t per_sm = p.half_sm ? 2 : 1;
-            const int64_t rounds = ceil_div(ctas, (int64_t(fit) * per_sm + per_sm) * p.split);
-            const int64_t each = std::max(ceil_div(ctas, sms), rounds > 1 ? rounds * per_sm : 1);
-            const double clocks = std::max(2.0 * (p.bp + p.bn), 4.0 * std::max(45, p.bn / 2));
-            const double share = double(ceil_div(kb, p.split));
-            const double alone = double(rounds) * share * kLatency / stages;
-            const double busy = double(each) * share * clocks / kClock;
-            const double l2 = double(ctas) * share * (p.bp + p.bn) * 128 / kL2;
-            const double join = (p.split > 1 ? 600 + 60 * p.split : 0) + p.bp * p.bn * 4 / 40 / kClock;
-            const double ns = 3000 + std::max(std::max(busy, alone), std::max(memory, l2)) +
-                              double(rounds) * join;
-            if (ns < best->ns) {
-                best->ns = ns;
-                best->swap = swap;
-                best->bn = p.bn;
-                best->bp = p.bp;
-                best->split = p.split;
-                best->half_sm = p.half_sm;
+        const int half_sm = split_partial_bytes(p) <= half && split_stages(half, p_bytes, q_bytes) >= 5;
+        const int64_t tiles = ceil_div(Mp, bp) * tiles_q;
+        int split = 1;
+        while (split < 8 && tiles * split * 2 <= places(split * 2, half_sm) && split * 4 <= kb) split *= 2;
+        if (t.split == 1 || t.split == 2 || t.split == 4 || t.split == 8)
+            for (split = t.split; split > kb; split /= 2) {
             }
-        }
+        const int64_t ctas = tiles * split;
+        const int64_t fit = places(split, half_sm);
+        const double filled = double(std::min(ctas, fit)) / double(places(1, half_sm)) * (bp == 128 ? 1.2 : 1.0);
+        if (filled <= most) continue;
+        most = filled;
+        best.swap = swap;
+        best.bn = p.bn;
+        best.bp = bp;
+        best.split = split;
+        best.half_sm = half_sm;
+        const double share = double(ceil_div(kb, split));
+        const double busy = double(ceil_div(ctas, 148)) * share * 2.0 * (bp + p.bn) / kClock;
+        const double l2 = double(ctas) * share * (bp + p.bn) * 128 / kL2;
+        best.ns = 3900 + (split > 1 ? 700 : 0) + double(ceil_div(ctas, fit)) * bp * p.bn * 4 / 32 +
+                  std::max(busy, std::max(memory_ns(op), l2));
     }
-    return TPGEMM_OK;
+    return best;
 }
 
 }  // namespace
@@ -218,9 +215,7 @@ tpgemm_status run_linear_tc(const LinearOp& op, int sms, cudaStream_t stream) {
     p.bk = p.fp8 ? 128 : 64;
     p.k_blocks = int(ceil_div(op.K, p.bk));
     p.timeout_ns = wait_timeout_ns();
-    Choice split;
-    s = plan_split(op, p.k_blocks, sms, t, &split);
-    if (s != TPGEMM_OK) return s;
+    const Choice split = plan_split(op, p.k_blocks, t);
     Choice c = plan_tile(op, p.k_blocks, sms, t);
     if (t.path == kLinearSplit || (t.path != kLinearTile && split.ns < c.ns)) c = split;
     if (c.bn == 0) return fail_with(TPGEMM_ERR_PATH, "the planner overrides leave no plan");
@@ -257,10 +252,10 @@ tpgemm_status run_linear_tc(const LinearOp& op, int sms, cudaStream_t stream) {
         p.group = 8;
         // Few tiles along one side: the CTAs at work all read the same panels.
         p.k_rotate = p.tiles_p == 1 || p.tiles_q == 1;
-        int clusters = 0;
-        s = max_clusters(p, &clusters);
+        int pairs = 0;
+        s = max_pairs(p, &pairs);
         if (s != TPGEMM_OK) return s;
-        grid = 2 * std::min(p.tiles, clusters);
+        grid = 2 * std::min(p.tiles, pairs);
     } else {
         p.stages = split_stages(p.half_sm ? kSplitHalfSmem - kBarrierBytes : budget, p.p_bytes, p.q_bytes);
         p.ring_bytes = std::max(uint32_t(p.stages) * (p.p_bytes + p.q_bytes),

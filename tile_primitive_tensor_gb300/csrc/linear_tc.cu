@@ -997,7 +997,7 @@ size_t tc_linear_smem(const TcLinear& p) {
 }
 
 namespace {
-// Lets a kernel use, and the occupancy query count with, all shared memory.
+// Lets a kernel use all shared memory.
 cudaError_t allow_smem(const void* fn) {
     cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcMaxSmem);
     if (e == cudaSuccess)
@@ -1037,20 +1037,19 @@ cudaError_t launch_tc_linear(const TcLinearMaps& maps, const TcLinear& p, int gr
     return cudaLaunchKernelEx(&cfg, split, maps.P, maps.Q, p);
 }
 
-cudaError_t tc_linear_max_clusters(const TcLinear& p, int* clusters) {
-    const void* fn = p.pair ? reinterpret_cast<const void*>(pick_tile(p))
-                            : reinterpret_cast<const void*>(pick_split(p));
-    cudaError_t e = allow_smem(fn);
+cudaError_t tc_linear_max_pairs(const TcLinear& p, int* pairs) {
+    const TileFn fn = pick_tile(p);
+    cudaError_t e = allow_smem(reinterpret_cast<const void*>(fn));
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(cluster_of(p)));
-    cfg.blockDim = dim3(p.pair ? kTileThreads : kSplitThreads);
+    cfg.gridDim = dim3(2);
+    cfg.blockDim = dim3(kTileThreads);
     cfg.dynamicSmemBytes = tc_linear_smem(p);
     cudaLaunchAttribute attr[1];
-    set_cluster(attr[0], cluster_of(p));
+    set_cluster(attr[0], 2);
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaOccupancyMaxActiveClusters(clusters, fn, &cfg);
+    return cudaOccupancyMaxActiveClusters(pairs, fn, &cfg);
 }
 
 cudaError_t linear_read_and_clear_status(int* status) {

@@ -37,8 +37,8 @@ struct TcLinearMaps {
 
 size_t tc_linear_smem(const TcLinear& p);
 cudaError_t launch_tc_linear(const TcLinearMaps& maps, const TcLinear& p, int grid, cudaStream_t stream);
-// Clusters of the kernel that fit the device at once.
-cudaError_t tc_linear_max_clusters(const TcLinear& p, int* clusters);
+// CTA pairs of the tile kernel that fit the device at once.
+cudaError_t tc_linear_max_pairs(const TcLinear& p, int* pairs);
 // Shared memory of a split block that leaves room for another on its SM.
 constexpr size_t kSplitHalfSmem = 112 * 1024;
 // Shared bytes of a split tile's partial sums.
