@@ -604,12 +604,12 @@ def _act_code(act) -> int:
     raise ValueError(f"act must be one of {', '.join(_ACTS)}, got {act!r}")
 
 
-def _matrix(name, t, rows, cols, dtype, device) -> int:
+def _matrix(name, t, rows, cols, dtype, index) -> int:
     """Checks a [rows, cols] argument of unit column stride; returns its row stride."""
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not {device}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, not cuda:{index}")
     if t.shape != (rows, cols):
         raise ValueError(f"{name} must be [{rows}, {cols}], got {list(t.shape)}")
     s0, s1 = t.stride()
@@ -622,45 +622,61 @@ def _matrix(name, t, rows, cols, dtype, device) -> int:
     return s0
 
 
-def _vector(name, t, n, dtype, device) -> None:
+def _vector(name, t, n, dtype, index) -> int:
+    """Checks a dense vector argument; returns its address."""
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not {device}")
-    if t.shape != (n,) or (n > 1 and t.stride(0) != 1):
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, not cuda:{index}")
+    if t.shape != (n,) or (n > 1 and t.stride()[0] != 1):
         raise ValueError(f"{name} must be a dense vector of {n}")
+    return t.data_ptr()
 
 
-def _scratch(torch, workspace, need, device):
-    """(workspace, its bytes): the caller's, or one from torch (None when none is needed)."""
+_torch = None
+
+
+def _import_torch():
+    global _torch
+    import torch
+    _torch = torch
+    return torch
+
+
+def _scratch(torch, workspace, need, device, index):
+    """(workspace, its address, its bytes): the caller's, or one from torch."""
     if workspace is None:
-        if need == 0:
-            return None, 0
         workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    elif workspace.device != device:
+    elif workspace.get_device() != index:
         raise ValueError(f"workspace is on {workspace.device}, not {device}")
-    return workspace, workspace.numel() * workspace.element_size()
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
-def _cuda(name, t):
-    if t.dim() != 2:
+def _sizes(name, t):
+    """Rows, columns, device index and device of the 2-D CUDA tensor that leads a call."""
+    shape = t.shape
+    if len(shape) != 2:
         raise ValueError(f"{name} must be 2-D")
-    if not t.is_cuda:
+    index = t.get_device()
+    if index < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
-    return t.device
+    return shape[0], shape[1], index, t.device
 
 
-def _enqueue(torch, device, stream, call):
-    """Runs call(stream) with `device` current and raises if it is refused. The default stream
-    is the device's current one, read through its raw handle: building torch's stream object
-    costs 2.9 us of a 10 us call."""
-    index = device.index
-    if index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            check(call(_stream(stream)))
+def _call(torch, index, stream, function, *args) -> None:
+    """function(*args, stream) with device `index` current; raises if it is refused. The default
+    stream is the device's current one, read as its raw handle: building torch's stream object
+    costs 2.9 us of a call that takes 9."""
+    cuda = torch._C
+    if index != cuda._cuda_getDevice():
+        with torch.cuda.device(index):
+            status = function(*args, cuda._cuda_getCurrentRawStream(index) if stream is None
+                              else _stream(stream))
     else:
-        check(call(torch._C._cuda_getCurrentRawStream(index) if stream is None
-                   else _stream(stream)))
+        status = function(*args, cuda._cuda_getCurrentRawStream(index) if stream is None
+                          else _stream(stream))
+    if status:
+        raise TpgemmError(status, tpgemm_last_error_detail())
 
 
 def linear(A, W, bias=None, residual=None, *, act="none", scale_a=None, scale_w=None,
@@ -673,42 +689,43 @@ def linear(A, W, bias=None, residual=None, *, act="none", scale_a=None, scale_w=
     scales, per row of A and of W, are for the 8-bit types. act: none, relu, silu, gelu or
     gelu_tanh. Matrices may be row-strided; ``out`` may be the residual itself. The workspace, if
     one is needed (tpgemm_linear_workspace_bytes), is allocated here with torch unless given."""
-    import torch
+    torch = _torch or _import_torch()
     lib = _lib or _load()
-    dev = _cuda("A", A)
-    M, K = A.shape
+    M, K, index, device = _sizes("A", A)
     N = W.shape[0]
     dt = A.dtype
-    lda = _matrix("A", A, M, K, dt, dev)
-    ldw = _matrix("W", W, N, K, dt, dev)
+    lda = _matrix("A", A, M, K, dt, index)
+    ldw = _matrix("W", W, N, K, dt, index)
     if out_dtype is None:
         out_dtype = out.dtype if out is not None else (dt if dt.itemsize == 2 else torch.bfloat16)
+    act = _act_code(act)
+    codes = elem_code(dt), elem_code(out_dtype), act
     if out is None:
-        out, ldy = torch.empty((M, N), dtype=out_dtype, device=dev), N
+        out, ldy = torch.empty((M, N), dtype=out_dtype, device=device), N
     else:
-        ldy = _matrix("out", out, M, N, out_dtype, dev)
+        ldy = _matrix("out", out, M, N, out_dtype, index)
     ldr = ldz = 0
+    pr = pz = pb = psa = psw = pws = None
     if residual is not None:
-        ldr = _matrix("residual", residual, M, N, out_dtype, dev)
+        ldr, pr = _matrix("residual", residual, M, N, out_dtype, index), residual.data_ptr()
     if pre is not None:
-        ldz = _matrix("pre", pre, M, N, out_dtype, dev)
+        ldz, pz = _matrix("pre", pre, M, N, out_dtype, index), pre.data_ptr()
     if bias is not None:
-        _vector("bias", bias, N, out_dtype, dev)
+        pb = _vector("bias", bias, N, out_dtype, index)
     if scale_a is not None:
-        _vector("scale_a", scale_a, M, torch.float32, dev)
+        psa = _vector("scale_a", scale_a, M, torch.float32, index)
     if scale_w is not None:
-        _vector("scale_w", scale_w, N, torch.float32, dev)
-    desc = LinearDesc(M, N, K, lda, ldw, ldr, ldy, ldz, elem_code(dt), elem_code(out_dtype),
-                      _act_code(act))
-    ref = ctypes.byref(desc)
+        psw = _vector("scale_w", scale_w, N, torch.float32, index)
+    desc = ctypes.byref(LinearDesc(M, N, K, lda, ldw, ldr, ldy, ldz, *codes))
     pa, pw = A.data_ptr(), W.data_ptr()
-    need = 0
-    if workspace is None:
-        need = lib.tpgemm_linear_workspace_bytes(pa, pw, ref)
-    workspace, size = _scratch(torch, workspace, need, dev)
-    _enqueue(torch, dev, stream, lambda st: lib.tpgemm_linear(
-        out.data_ptr(), _ptr(pre), pa, pw, _ptr(scale_a), _ptr(scale_w), _ptr(bias),
-        _ptr(residual), ref, _ptr(workspace), size, st))
+    size = 0
+    # (Operands on 16-byte boundaries need no workspace.)
+    if workspace is not None or (pa | pw | (lda | ldw) * dt.itemsize) & 15:
+        need = lib.tpgemm_linear_workspace_bytes(pa, pw, desc)
+        if need:
+            workspace, pws, size = _scratch(torch, workspace, need, device, index)
+    _call(torch, index, stream, lib.tpgemm_linear, out.data_ptr(), pz, pa, pw, psa, psw, pb, pr,
+          desc, pws, size)
     return out
 
 
@@ -720,35 +737,37 @@ def linear_backward(dY, A, W, pre=None, *, act="none", grad_dtype=None, need=(Tr
     dY, A, W, pre and dA are all float16 or all bfloat16; dW and dbias are of grad_dtype (float32,
     float16 or bfloat16; by default A's type). ``need`` says which of the three are wanted; the
     others are None."""
-    import torch
+    torch = _torch or _import_torch()
     lib = _lib or _load()
-    dev = _cuda("A", A)
-    M, K = A.shape
+    M, K, index, device = _sizes("A", A)
     N = W.shape[0]
     dt = A.dtype
     grad_dtype = dt if grad_dtype is None else grad_dtype
     code = _act_code(act)
-    ldz = 0
+    ldz, pz = 0, None
     if code != TPGEMM_ACT_NONE:
         if pre is None:
             raise ValueError(f"act={act!r} needs pre, the value before the activation")
-        ldz = _matrix("pre", pre, M, N, dt, dev)
-    else:
-        pre = None
-    desc = LinearGradDesc(M, N, K, _matrix("dY", dY, M, N, dt, dev), ldz,
-                          _matrix("A", A, M, K, dt, dev), _matrix("W", W, N, K, dt, dev), K, K,
-                          elem_code(dt), elem_code(grad_dtype), code)
-    dA = torch.empty((M, K), dtype=dt, device=dev) if need[0] else None
-    dW = torch.empty((N, K), dtype=grad_dtype, device=dev) if need[1] else None
-    dbias = torch.empty(N, dtype=grad_dtype, device=dev) if need[2] else None
-    ref = ctypes.byref(desc)
+        ldz, pz = _matrix("pre", pre, M, N, dt, index), pre.data_ptr()
+    desc = ctypes.byref(LinearGradDesc(
+        M, N, K, _matrix("dY", dY, M, N, dt, index), ldz, _matrix("A", A, M, K, dt, index),
+        _matrix("W", W, N, K, dt, index), K, K, elem_code(dt), elem_code(grad_dtype), code))
+    dA = dW = dbias = pda = pdw = pdb = None
+    if need[0]:
+        dA = torch.empty((M, K), dtype=dt, device=device)
+        pda = dA.data_ptr()
+    if need[1]:
+        dW = torch.empty((N, K), dtype=grad_dtype, device=device)
+        pdw = dW.data_ptr()
+    if need[2]:
+        dbias = torch.empty(N, dtype=grad_dtype, device=device)
+        pdb = dbias.data_ptr()
     py, pa, pw = dY.data_ptr(), A.data_ptr(), W.data_ptr()
-    size = 0
-    if workspace is None:
-        size = lib.tpgemm_linear_backward_workspace_bytes(py, pa, pw, ref)
-    workspace, size = _scratch(torch, workspace, size, dev)
-    _enqueue(torch, dev, stream, lambda st: lib.tpgemm_linear_backward(
-        _ptr(dA), _ptr(dW), _ptr(dbias), py, pa, pw, _ptr(pre), ref, _ptr(workspace), size, st))
+    size, pws = lib.tpgemm_linear_backward_workspace_bytes(py, pa, pw, desc), None
+    if size:
+        workspace, pws, size = _scratch(torch, workspace, size, device, index)
+    _call(torch, index, stream, lib.tpgemm_linear_backward, pda, pdw, pdb, py, pa, pw, pz, desc,
+          pws, size)
     return dA, dW, dbias
 
 
@@ -769,44 +788,47 @@ def rmsnorm(x, weight, residual=None, *, eps=1e-6, quant=None, out_dtype=None, n
     scale per row, linear's scale_a) or quant="mx" (one E8M0 scale per 32 columns, gemm_mx's SFA)
     float8_e4m3fn (the default) or float8_e5m2, holding y / scale. h is returned with a residual
     only; it may be written in place (out_h = x or residual)."""
-    import torch
+    torch = _torch or _import_torch()
     lib = _lib or _load()
-    dev = _cuda("x", x)
-    rows, cols = x.shape
+    rows, cols, index, device = _sizes("x", x)
     dt = x.dtype
     if quant not in _SCALES:
         raise ValueError(f"quant must be None, 'row' or 'mx', got {quant!r}")
     if out_dtype is None:
         out_dtype = out.dtype if out is not None else (dt if quant is None else torch.float8_e4m3fn)
-    if weight.dtype is not dt and weight.dtype is not torch.float32:
-        raise TypeError(f"weight must be {dt} or float32, got {weight.dtype}")
-    _vector("weight", weight, cols, weight.dtype, dev)
-    ldx = _matrix("x", x, rows, cols, dt, dev)
+    wt = weight.dtype
+    if wt is not dt and wt is not torch.float32:
+        raise TypeError(f"weight must be {dt} or float32, got {wt}")
+    pg = _vector("weight", weight, cols, wt, index)
+    ldx = _matrix("x", x, rows, cols, dt, index)
+    codes = elem_code(dt), elem_code(wt), elem_code(out_dtype), _SCALES[quant]
     if out is None:
-        out, ldy = torch.empty((rows, cols), dtype=out_dtype, device=dev), cols
+        out, ldy = torch.empty((rows, cols), dtype=out_dtype, device=device), cols
     else:
-        ldy = _matrix("out", out, rows, cols, out_dtype, dev)
-    h = scale = rstd = None
+        ldy = _matrix("out", out, rows, cols, out_dtype, index)
+    h = scale = rstd = pr = ph = ps = prstd = None
     ldr = ldh = 0
     if residual is not None:
-        ldr = _matrix("residual", residual, rows, cols, dt, dev)
+        ldr, pr = _matrix("residual", residual, rows, cols, dt, index), residual.data_ptr()
         if out_h is None:
-            h, ldh = torch.empty((rows, cols), dtype=dt, device=dev), cols
+            h, ldh = torch.empty((rows, cols), dtype=dt, device=device), cols
         else:
-            h, ldh = out_h, _matrix("out_h", out_h, rows, cols, dt, dev)
+            h, ldh = out_h, _matrix("out_h", out_h, rows, cols, dt, index)
+        ph = h.data_ptr()
     elif out_h is not None:
         raise ValueError("out_h needs a residual (h is x without one)")
     if quant == "row":
-        scale = torch.empty(rows, dtype=torch.float32, device=dev)
+        scale = torch.empty(rows, dtype=torch.float32, device=device)
+        ps = scale.data_ptr()
     elif quant == "mx":
-        scale = torch.empty((rows, (cols + 31) // 32), dtype=torch.uint8, device=dev)
+        scale = torch.empty((rows, (cols + 31) // 32), dtype=torch.uint8, device=device)
+        ps = scale.data_ptr()
     if need_rstd:
-        rstd = torch.empty(rows, dtype=torch.float32, device=dev)
-    desc = RmsNormDesc(rows, cols, ldx, ldr, ldh, ldy, elem_code(dt), elem_code(weight.dtype),
-                       elem_code(out_dtype), _SCALES[quant], eps)
-    _enqueue(torch, dev, stream, lambda st: lib.tpgemm_rmsnorm(
-        out.data_ptr(), _ptr(h), _ptr(scale), _ptr(rstd), x.data_ptr(), _ptr(residual),
-        weight.data_ptr(), ctypes.byref(desc), st))
+        rstd = torch.empty(rows, dtype=torch.float32, device=device)
+        prstd = rstd.data_ptr()
+    desc = RmsNormDesc(rows, cols, ldx, ldr, ldh, ldy, *codes, eps)
+    _call(torch, index, stream, lib.tpgemm_rmsnorm, out.data_ptr(), ph, ps, prstd, x.data_ptr(),
+          pr, pg, ctypes.byref(desc))
     return RmsNorm(out, h, scale, rstd)
 
 
@@ -817,33 +839,34 @@ def rmsnorm_backward(dy, h, rstd, weight, dh=None, *, grad_dtype=None, need=(Tru
 
     dy, h, dh and dx [rows, cols] are of one type (float16, bfloat16 or float32), dweight of
     grad_dtype (by default weight's). ``need`` says which are wanted; ``out`` may be dy, h or dh."""
-    import torch
+    torch = _torch or _import_torch()
     lib = _lib or _load()
-    dev = _cuda("dy", dy)
-    rows, cols = dy.shape
-    dt = dy.dtype
-    grad_dtype = weight.dtype if grad_dtype is None else grad_dtype
-    if weight.dtype is not dt and weight.dtype is not torch.float32:
-        raise TypeError(f"weight must be {dt} or float32, got {weight.dtype}")
-    _vector("weight", weight, cols, weight.dtype, dev)
-    _vector("rstd", rstd, rows, torch.float32, dev)
-    lddh = 0 if dh is None else _matrix("dh", dh, rows, cols, dt, dev)
-    dx = dweight = None
-    lddx = size = 0
+    rows, cols, index, device = _sizes("dy", dy)
+    dt, wt = dy.dtype, weight.dtype
+    grad_dtype = wt if grad_dtype is None else grad_dtype
+    if wt is not dt and wt is not torch.float32:
+        raise TypeError(f"weight must be {dt} or float32, got {wt}")
+    pg = _vector("weight", weight, cols, wt, index)
+    prstd = _vector("rstd", rstd, rows, torch.float32, index)
+    dx = dweight = pdx = pdw = pdh = pws = None
+    lddh = lddx = size = 0
+    if dh is not None:
+        lddh, pdh = _matrix("dh", dh, rows, cols, dt, index), dh.data_ptr()
     if need[0]:
         if out is None:
-            dx, lddx = torch.empty((rows, cols), dtype=dt, device=dev), cols
+            dx, lddx = torch.empty((rows, cols), dtype=dt, device=device), cols
         else:
-            dx, lddx = out, _matrix("out", out, rows, cols, dt, dev)
-    desc = RmsNormGradDesc(rows, cols, _matrix("dy", dy, rows, cols, dt, dev),
-                           _matrix("h", h, rows, cols, dt, dev), lddh, lddx, elem_code(dt),
-                           elem_code(weight.dtype), elem_code(grad_dtype))
+            dx, lddx = out, _matrix("out", out, rows, cols, dt, index)
+        pdx = dx.data_ptr()
+    desc = RmsNormGradDesc(rows, cols, _matrix("dy", dy, rows, cols, dt, index),
+                           _matrix("h", h, rows, cols, dt, index), lddh, lddx, elem_code(dt),
+                           elem_code(wt), elem_code(grad_dtype))
     if need[1]:
-        dweight = torch.empty(cols, dtype=grad_dtype, device=dev)
-        if workspace is None:
-            size = lib.tpgemm_rmsnorm_backward_workspace_bytes(rows, cols)
-    workspace, size = _scratch(torch, workspace, size, dev)
-    _enqueue(torch, dev, stream, lambda st: lib.tpgemm_rmsnorm_backward(
-        _ptr(dx), _ptr(dweight), dy.data_ptr(), h.data_ptr(), rstd.data_ptr(), weight.data_ptr(),
-        _ptr(dh), ctypes.byref(desc), _ptr(workspace), size, st))
+        dweight = torch.empty(cols, dtype=grad_dtype, device=device)
+        pdw = dweight.data_ptr()
+        size = lib.tpgemm_rmsnorm_backward_workspace_bytes(rows, cols)
+        if size:
+            workspace, pws, size = _scratch(torch, workspace, size, device, index)
+    _call(torch, index, stream, lib.tpgemm_rmsnorm_backward, pdx, pdw, dy.data_ptr(), h.data_ptr(),
+          prstd, pg, pdh, ctypes.byref(desc), pws, size)
     return dx, dweight
