@@ -1,4 +1,5 @@
-// out[n] = sum over strips s of partial[s][n], in the strips' order, rounded once.
+// out[n] = sum over strips s of partial[s][n], always in the same order, rounded
+// once.
 #pragma once
 
 #include "elem.cuh"
@@ -8,10 +9,11 @@
 namespace tpg {
 namespace {
 
+// 32 columns to a block, its 32 warps taking every 32nd strip.
 template <typename O>
-__global__ void __launch_bounds__(256) column_sum_kernel(const float* partial, int strips,
-                                                         int64_t cols, O* out) {
-    __shared__ float s[8][33];
+__global__ void __launch_bounds__(1024) column_sum_kernel(const float* partial, int strips,
+                                                          int64_t cols, O* out) {
+    __shared__ float s[32][33];
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int64_t n = int64_t(blockIdx.x) * 32 + lane;
     grid_launch_dependents();
@@ -19,22 +21,22 @@ __global__ void __launch_bounds__(256) column_sum_kernel(const float* partial, i
     float v = 0.f;
     if (n < cols)
 #pragma unroll 4
-        for (int i = w; i < strips; i += 8) v += partial[int64_t(i) * cols + n];
+        for (int i = w; i < strips; i += 32) v += partial[int64_t(i) * cols + n];
     s[w][lane] = v;
     __syncthreads();
-    if (w == 0 && n < cols) {
-        float t = 0.f;
+    // Warp w adds column w's sums.
+    v = s[lane][w];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) t += s[i][lane];
-        out[n] = from_f32<O>(t);
-    }
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    const int64_t c = int64_t(blockIdx.x) * 32 + w;
+    if (lane == 0 && c < cols) out[c] = from_f32<O>(v);
 }
 
 inline cudaError_t launch_column_sum(const float* partial, int strips, int64_t cols, void* out,
                                      int elem, cudaStream_t stream) {
     const int64_t blocks = (cols + 31) / 32;
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-    const dim3 g{unsigned(blocks)}, b{256};
+    const dim3 g{unsigned(blocks)}, b{1024};
     if (elem == TPGEMM_ELEM_F16)
         return launch_dependent(column_sum_kernel<__half>, g, b, 0, stream, partial, strips, cols,
                                 static_cast<__half*>(out));

@@ -88,6 +88,30 @@ __device__ __forceinline__ void load_cols(const void* base, int64_t row, const C
     }
 }
 
+// A group as it is loaded ahead of its use: 16-bit elements stay packed.
+template <typename T, bool VEC>
+struct Ahead {
+    static constexpr bool kPacked = VEC && sizeof(T) == 2;
+    uint4 raw;
+    float f[kPacked ? 1 : 8];
+    __device__ __forceinline__ void load(const void* base, int64_t row, const Cols<VEC>& c) {
+        if constexpr (kPacked) {
+            raw = make_uint4(0, 0, 0, 0);
+            if (c.n == 8) raw = *reinterpret_cast<const uint4*>(static_cast<const T*>(base) + row + c.first);
+        } else {
+            load_cols<T, VEC>(base, row, c, f);
+        }
+    }
+    __device__ __forceinline__ void get(float (&out)[8]) const {
+        if constexpr (kPacked) {
+            unpack8<T>(raw, out);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) out[j] = f[j];
+        }
+    }
+};
+
 template <typename T, bool VEC>
 __device__ __forceinline__ void store_cols(void* base, int64_t row, const Cols<VEC>& c,
                                            const float (&f)[8]) {
@@ -262,64 +286,77 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : kMaxTeam) rmsnorm_kern
 // ---------------------------------------------------------------- gradients
 // Blocks walk the rows grid-stride, a team (a warp or the block) to a row, and
 // keep the columns' sums of dgamma in registers; partial[block] gets the
-// block's. Rows wider than a team's registers take the two kernels after this.
+// block's. A row's reduction is a wait for all of it, so the next row's loads
+// are issued before it (without: 55 % of memory's rate at 8192 x 4096 bf16).
+// Rows wider than a team's registers take the two kernels after this.
 template <typename XT, int V, bool VEC, bool WARP, int MAXT = 512>
 __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : MAXT) rmsnorm_grad_kernel(const __grid_constant__ RmsNormGradOp op) {
     __shared__ float2 s[2][32];
     __shared__ float sum[WARP ? 8 * 32 * 8 * V : 1];
+    // (Unpacked groups, or more threads, leave no registers for it.)
+    constexpr bool kAhead = VEC && (WARP || MAXT <= 512);
     const int team = WARP ? 32 : int(blockDim.x);
     const int t = WARP ? int(threadIdx.x & 31) : int(threadIdx.x);
     const int64_t teams = WARP ? kWarpRows : 1;
+    const int64_t stride = int64_t(gridDim.x) * teams;
     grid_launch_dependents();
     grid_dependency_wait();
-    float g[V][8], acc[V][8];
+    float acc[V][8];
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const Cols<VEC> c(i, t, team, op.cols);
-        if (op.dX) load_gamma<XT, VEC>(op.gamma, op.g, c, g[i]);
+    for (int i = 0; i < V; ++i)
 #pragma unroll
         for (int j = 0; j < 8; ++j) acc[i][j] = 0.f;
-    }
-    int turn = 0;
-    for (int64_t row = int64_t(blockIdx.x) * teams + (WARP ? threadIdx.x >> 5 : 0); row < op.rows;
-         row += int64_t(gridDim.x) * teams, turn ^= 1) {
-        float dy[V][8], n[V][8];
+    int64_t row = int64_t(blockIdx.x) * teams + (WARP ? threadIdx.x >> 5 : 0);
+    Ahead<XT, VEC> a_dy[V], a_h[V], a_dh[V];
+    float a_rstd = 0.f;
+    auto fetch = [&](int64_t r) {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const Cols<VEC> c(i, t, team, op.cols);
-            load_cols<XT, VEC>(op.dY, row * op.lddy, c, dy[i]);
-            load_cols<XT, VEC>(op.H, row * op.ldh, c, n[i]);
+            a_dy[i].load(op.dY, r * op.lddy, c);
+            a_h[i].load(op.H, r * op.ldh, c);
+            if (op.dX && op.dH) a_dh[i].load(op.dH, r * op.lddh, c);
         }
-        const float rstd = op.rstd[row];
+        a_rstd = op.rstd[r];
+    };
+    if (kAhead && row < op.rows) fetch(row);
+    for (int turn = 0; row < op.rows; row += stride, turn ^= 1) {
+        if (!kAhead) fetch(row);
+        float dy[V][8], n[V][8], d[V][8];
+        const float rstd = a_rstd;
         float dot = 0.f;
         uint32_t unused = 0;
 #pragma unroll
-        for (int i = 0; i < V; ++i)
+        for (int i = 0; i < V; ++i) {
+            a_dy[i].get(dy[i]);
+            a_h[i].get(n[i]);
+            if (op.dX && op.dH) {
+                a_dh[i].get(d[i]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) d[i][j] = 0.f;
+            }
+            float g[8];
+            if (op.dX) load_gamma<XT, VEC>(op.gamma, op.g, Cols<VEC>(i, t, team, op.cols), g);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 n[i][j] *= rstd;
                 acc[i][j] += dy[i][j] * n[i][j];
                 if (op.dX) {
-                    dy[i][j] *= g[i][j];
+                    dy[i][j] *= g[j];
                     dot += dy[i][j] * n[i][j];
                 }
             }
+        }
+        if (kAhead && row + stride < op.rows) fetch(row + stride);
         if (!op.dX) continue;
         team_sum_max<WARP>(dot, unused, s[turn]);
         dot /= float(op.cols);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const Cols<VEC> c(i, t, team, op.cols);
-            float d[8];
-            if (op.dH) {
-                load_cols<XT, VEC>(op.dH, row * op.lddh, c, d);
-            } else {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) d[j] = 0.f;
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) d[j] += rstd * (dy[i][j] - n[i][j] * dot);
-            store_cols<XT, VEC>(op.dX, row * op.lddx, c, d);
+            for (int j = 0; j < 8; ++j) d[i][j] += rstd * (dy[i][j] - n[i][j] * dot);
+            store_cols<XT, VEC>(op.dX, row * op.lddx, Cols<VEC>(i, t, team, op.cols), d[i]);
         }
     }
     if (!op.dgamma) return;
@@ -396,13 +433,15 @@ struct Spread {
     int rows() const { return warp ? kWarpRows : 1; }
 };
 
-// Up to 512 columns a warp holds the row. Wider rows take one group to a thread
-// while that leaves the team at 512 threads or fewer, then two.
+// Up to 512 columns a warp holds the row (1024 with four groups to a thread).
+// Wider rows are a block's: for many rows two groups to a thread, which keeps
+// more bytes on their way (8192 x 4096 bf16: NORM_V1 us with one); for few rows one
+// group, for the shortest time to the end of a row.
 Spread spread_of(int64_t rows, int64_t cols) {
     const int64_t groups = (cols + 7) / 8;
     if (groups <= 64) return {32, groups <= 32 ? 1 : 2, true};
     if (cols > kMaxHeld) return {kMaxTeam, 0, false};
-    const bool one = groups <= 512 || (groups <= kMaxTeam && rows <= 152);
+    const bool one = groups <= kMaxTeam && rows <= 304;
     const int64_t per = one ? groups : (groups + 1) / 2;
     return {int((per + 31) / 32 * 32), one ? 1 : 2, false};
 }
@@ -435,11 +474,12 @@ cudaError_t launch_norm_typed(const RmsNormOp& op, cudaStream_t stream) {
     return vec ? launch_norm<XT, true>(op, stream) : launch_norm<XT, false>(op, stream);
 }
 
-// Blocks of the register kernel: enough to fill the GPU's threads, at most one
-// to a team's worth of rows.
+// Blocks of the register kernel: 512 threads to an SM, which is what its
+// registers leave room for, and two rows to a team at the least, since each
+// block's sums are written and read once more.
 int grad_blocks(int64_t rows, const Spread& s) {
-    const int64_t most = (rows + s.rows() - 1) / s.rows();
-    const int64_t fill = 152 * (s.threads() <= 256 ? 4 : s.threads() <= 512 ? 2 : 1);
+    const int64_t most = (rows + 2 * s.rows() - 1) / (2 * s.rows());
+    const int64_t fill = 152 * (s.threads() >= 512 ? 1 : 512 / s.threads());
     return int(most < fill ? (most < 1 ? 1 : most) : fill);
 }
 
