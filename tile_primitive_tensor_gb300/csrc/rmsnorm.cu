@@ -20,6 +20,8 @@
 // a thread at a time so that each load moves 16 bytes, reduced, and written
 // from the registers. Rows wider than a team's registers (16384 columns) are
 // read twice, the second time from L2.
+#include <algorithm>
+
 #include "column_sum.cuh"
 #include "launch.cuh"
 #include "ptx.cuh"
@@ -211,48 +213,22 @@ __device__ __forceinline__ void load_h(const RmsNormOp& op, int64_t row, const C
     }
 }
 
-// V groups of eight columns to a thread; WARP: a row to a warp, else to a
-// block; V == 0: rows of any width, read twice by a block.
+// What follows a row's loads: reduction, scale, and the stores of h and y.
 template <typename XT, int V, bool VEC, bool WARP>
-__global__ void __launch_bounds__(WARP ? 32 * kWarpRows : kMaxTeam) rmsnorm_kernel(const __grid_constant__ RmsNormOp op) {
-    __shared__ float2 s[32];
-    constexpr bool kWide = V == 0;
-    constexpr int kHeld = kWide ? 1 : V;
-    const int team = WARP ? 32 : int(blockDim.x);
-    const int t = WARP ? int(threadIdx.x & 31) : int(threadIdx.x);
-    const int64_t row = WARP ? int64_t(blockIdx.x) * kWarpRows + (threadIdx.x >> 5) : int64_t(blockIdx.x);
-    grid_launch_dependents();
-    grid_dependency_wait();
-    if (WARP && row >= op.rows) return;
+__device__ __forceinline__ void finish_row(const RmsNormOp& op, int64_t row, int t, int team,
+                                           const float (&h)[V][8], float2* s) {
     const bool row_mode = op.mode == TPGEMM_SCALE_ROW;
-    const int64_t groups = kWide ? (op.cols + 8 * team - 1) / (8 * team) : V;
-    float h[kHeld][8], g[kHeld][8];
+    float g[V][8];
     float ss = 0.f;
     uint32_t amax = 0;
-    if constexpr (!kWide) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) load_h<XT, VEC>(op, row, Cols<VEC>(i, t, team, op.cols), h[i]);
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            load_gamma<XT, VEC>(op.gamma, op.g, Cols<VEC>(i, t, team, op.cols), g[i]);
-    }
-    auto add = [&](const float (&hv)[8], const float (&gv)[8]) {
+    for (int i = 0; i < V; ++i) {
+        load_gamma<XT, VEC>(op.gamma, op.g, Cols<VEC>(i, t, team, op.cols), g[i]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            ss += hv[j] * hv[j];
-            if (row_mode) amax = max(amax, abs_bits(hv[j] * gv[j]));
+            ss += h[i][j] * h[i][j];
+            if (row_mode) amax = max(amax, abs_bits(h[i][j] * g[i][j]));
         }
-    };
-    if constexpr (kWide) {
-        for (int64_t i = 0; i < groups; ++i) {
-            const Cols<VEC> c(i, t, team, op.cols);
-            load_h<XT, VEC>(op, row, c, h[0]);
-            if (row_mode) load_gamma<XT, VEC>(op.gamma, op.g, c, g[0]);
-            add(h[0], g[0]);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) add(h[i], g[i]);
     }
     team_sum_max<WARP>(ss, amax, s);
     const float rstd = 1.f / sqrtf(ss / float(op.cols) + op.eps);
@@ -263,23 +239,104 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : kMaxTeam) rmsnorm_kern
         if (t == 0) static_cast<float*>(op.scale)[row] = scale;
         inv = 1.f / scale;
     }
-    auto finish = [&](const Cols<VEC>& c, const float (&hv)[8], const float (&gv)[8]) {
-        if (op.H) store_cols<XT, VEC>(op.H, row * op.ldh, c, hv);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const Cols<VEC> c(i, t, team, op.cols);
+        if (op.H) store_cols<XT, VEC>(op.H, row * op.ldh, c, h[i]);
         float y[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = hv[j] * rstd * gv[j];
+        for (int j = 0; j < 8; ++j) y[j] = h[i][j] * rstd * g[i][j];
         store_y<VEC>(op, row, c, y, inv);
-    };
-    if constexpr (kWide) {
-        for (int64_t i = 0; i < groups; ++i) {
-            const Cols<VEC> c(i, t, team, op.cols);
-            load_h<XT, VEC>(op, row, c, h[0]);
-            load_gamma<XT, VEC>(op.gamma, op.g, c, g[0]);
-            finish(c, h[0], g[0]);
-        }
-    } else {
+    }
+}
+
+// Rows held in registers: V groups of eight columns to a thread; WARP: a row to
+// a warp, else to a block. AHEAD: blocks stay and walk the rows grid-stride, and
+// load the next row before the reduction of this one, which waits for all of
+// it; else a team ends with its row and the blocks beside it keep memory busy.
+template <typename XT, int V, bool VEC, bool WARP, bool AHEAD = false>
+__global__ void __launch_bounds__(WARP ? 32 * kWarpRows : kMaxTeam) rmsnorm_kernel(const __grid_constant__ RmsNormOp op) {
+    __shared__ float2 s[2][32];
+    const int team = WARP ? 32 : int(blockDim.x);
+    const int t = WARP ? int(threadIdx.x & 31) : int(threadIdx.x);
+    int64_t row = WARP ? int64_t(blockIdx.x) * kWarpRows + (threadIdx.x >> 5) : int64_t(blockIdx.x);
+    grid_launch_dependents();
+    grid_dependency_wait();
+    if (WARP && row >= op.rows) return;
+    float h[V][8];
+    if constexpr (!AHEAD) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) finish(Cols<VEC>(i, t, team, op.cols), h[i], g[i]);
+        for (int i = 0; i < V; ++i) load_h<XT, VEC>(op, row, Cols<VEC>(i, t, team, op.cols), h[i]);
+        finish_row<XT, V, VEC, WARP>(op, row, t, team, h, s[0]);
+    } else {
+        Ahead<XT, VEC> x[V], r[V];
+        auto fetch = [&](int64_t at) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const Cols<VEC> c(i, t, team, op.cols);
+                x[i].load(op.X, at * op.ldx, c);
+                if (op.R) r[i].load(op.R, at * op.ldr, c);
+            }
+        };
+        fetch(row);
+        for (int turn = 0; row < op.rows; row += gridDim.x, turn ^= 1) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                x[i].get(h[i]);
+                if (op.R) {
+                    float q[8];
+                    r[i].get(q);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) h[i][j] += q[j];
+                }
+            }
+            if (row + gridDim.x < op.rows) fetch(row + gridDim.x);
+            finish_row<XT, V, VEC, WARP>(op, row, t, team, h, s[turn]);
+        }
+    }
+}
+
+// Rows of any width, a block to a row, read twice.
+template <typename XT, bool VEC>
+__global__ void __launch_bounds__(kMaxTeam) rmsnorm_wide_kernel(const __grid_constant__ RmsNormOp op) {
+    __shared__ float2 s[32];
+    const int team = int(blockDim.x), t = int(threadIdx.x);
+    const int64_t row = blockIdx.x;
+    const bool row_mode = op.mode == TPGEMM_SCALE_ROW;
+    const int64_t groups = (op.cols + 8 * team - 1) / (8 * team);
+    float h[8], g[8];
+    float ss = 0.f;
+    uint32_t amax = 0;
+    grid_launch_dependents();
+    grid_dependency_wait();
+    for (int64_t i = 0; i < groups; ++i) {
+        const Cols<VEC> c(i, t, team, op.cols);
+        load_h<XT, VEC>(op, row, c, h);
+        if (row_mode) load_gamma<XT, VEC>(op.gamma, op.g, c, g);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            ss += h[j] * h[j];
+            if (row_mode) amax = max(amax, abs_bits(h[j] * g[j]));
+        }
+    }
+    team_sum_max<false>(ss, amax, s);
+    const float rstd = 1.f / sqrtf(ss / float(op.cols) + op.eps);
+    if (t == 0 && op.rstd) op.rstd[row] = rstd;
+    float inv = 1.f;
+    if (row_mode) {
+        const float scale = row_scale(abs_bits(rstd * __uint_as_float(amax)), op.y);
+        if (t == 0) static_cast<float*>(op.scale)[row] = scale;
+        inv = 1.f / scale;
+    }
+    for (int64_t i = 0; i < groups; ++i) {
+        const Cols<VEC> c(i, t, team, op.cols);
+        load_h<XT, VEC>(op, row, c, h);
+        load_gamma<XT, VEC>(op.gamma, op.g, c, g);
+        if (op.H) store_cols<XT, VEC>(op.H, row * op.ldh, c, h);
+        float y[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] = h[j] * rstd * g[j];
+        store_y<VEC>(op, row, c, y, inv);
     }
 }
 
@@ -294,7 +351,7 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : MAXT) rmsnorm_grad_ker
     __shared__ float2 s[2][32];
     __shared__ float sum[WARP ? 8 * 32 * 8 * V : 1];
     // (Unpacked groups, or more threads, leave no registers for it.)
-    constexpr bool kAhead = VEC && (WARP || MAXT <= 512);
+    constexpr bool kAhead = (VEC || V == 1) && (WARP || MAXT <= 512);
     const int team = WARP ? 32 : int(blockDim.x);
     const int t = WARP ? int(threadIdx.x & 31) : int(threadIdx.x);
     const int64_t teams = WARP ? kWarpRows : 1;
@@ -433,15 +490,16 @@ struct Spread {
     int rows() const { return warp ? kWarpRows : 1; }
 };
 
-// Up to 512 columns a warp holds the row (1024 with four groups to a thread).
-// Wider rows are a block's: for many rows two groups to a thread, which keeps
-// more bytes on their way (8192 x 4096 bf16: NORM_V1 us with one); for few rows one
-// group, for the shortest time to the end of a row.
+// Up to 512 columns a warp holds the row. Wider rows are a block's: for many
+// rows two groups to a thread, which keeps more bytes on their way (8192 x 4096
+// bf16 with residual: 44 us, 52 with one); for few rows, and for widths that are
+// no multiple of eight, whose loads are narrow, one group, for the shortest time
+// to the end of a row.
 Spread spread_of(int64_t rows, int64_t cols) {
     const int64_t groups = (cols + 7) / 8;
     if (groups <= 64) return {32, groups <= 32 ? 1 : 2, true};
     if (cols > kMaxHeld) return {kMaxTeam, 0, false};
-    const bool one = groups <= kMaxTeam && rows <= 304;
+    const bool one = groups <= kMaxTeam && (rows <= 304 || (cols % 8 != 0 && groups <= 512));
     const int64_t per = one ? groups : (groups + 1) / 2;
     return {int((per + 31) / 32 * 32), one ? 1 : 2, false};
 }
@@ -454,14 +512,28 @@ bool rows_aligned(const void* p, int64_t ld, int64_t rows, int elem, int bytes) 
 template <typename XT, bool VEC>
 cudaError_t launch_norm(const RmsNormOp& op, cudaStream_t stream) {
     const Spread s = spread_of(op.rows, op.cols);
-    const int64_t blocks = (op.rows + s.rows() - 1) / s.rows();
+    if (s.v == 0) {
+        if (op.rows > 0x7fffffff) return cudaErrorInvalidValue;
+        return launch_dependent(rmsnorm_wide_kernel<XT, VEC>, dim3(unsigned(op.rows)),
+                                dim3(unsigned(s.threads())), 0, stream, op);
+    }
+    int64_t blocks = (op.rows + s.rows() - 1) / s.rows();
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-    const dim3 grid{unsigned(blocks)}, block{unsigned(s.threads())};
     auto fn = s.warp ? (s.v == 1 ? rmsnorm_kernel<XT, 1, VEC, true> : rmsnorm_kernel<XT, 2, VEC, true>)
-              : s.v == 0 ? rmsnorm_kernel<XT, 0, VEC, false>
               : s.v == 1 ? rmsnorm_kernel<XT, 1, VEC, false>
                          : rmsnorm_kernel<XT, 2, VEC, false>;
-    return launch_dependent(fn, grid, block, 0, stream, op);
+    if constexpr (VEC) {
+        // Teams of 512 threads and more leave an SM two rows or one, too few to
+        // hide each other's reductions: such rows are loaded ahead (bf16 with
+        // residual, MX scales: 8192 x 8192 92.6 -> 86.5 us; no scales: 2048 x
+        // 16384 55.3 -> 46.2 us). Not with row scales, whose maxima take the
+        // registers (89.1 -> 91.6), nor narrower rows (8192 x 4096 44.0 -> 46.4).
+        if (s.v == 2 && s.team >= 512 && op.mode != TPGEMM_SCALE_ROW) {
+            fn = rmsnorm_kernel<XT, 2, VEC, false, true>;
+            blocks = std::min(blocks, int64_t(152) * (kMaxTeam / s.team));
+        }
+    }
+    return launch_dependent(fn, dim3(unsigned(blocks)), dim3(unsigned(s.threads())), 0, stream, op);
 }
 
 template <typename XT>
