@@ -643,15 +643,6 @@ def _import_torch():
     return torch
 
 
-def _scratch(torch, workspace, need, device, index):
-    """(workspace, its address, its bytes): the caller's, or one from torch."""
-    if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    elif workspace.get_device() != index:
-        raise ValueError(f"workspace is on {workspace.device}, not {device}")
-    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
-
-
 def _sizes(name, t):
     """Rows, columns, device index and device of the 2-D CUDA tensor that leads a call."""
     shape = t.shape
@@ -663,18 +654,33 @@ def _sizes(name, t):
     return shape[0], shape[1], index, t.device
 
 
-def _call(torch, index, stream, function, *args) -> None:
-    """function(*args, stream) with device `index` current; raises if it is refused. The default
-    stream is the device's current one, read as its raw handle: building torch's stream object
-    costs 2.9 us of a call that takes 9."""
-    cuda = torch._C
-    if index != cuda._cuda_getDevice():
+def _call(torch, index, stream, function, args, workspace=None, need=None) -> None:
+    """function(*args, stream) with device `index` current; raises if it is refused. A function
+    that takes a workspace before the stream has ``need``, the bytes it asks for: the caller's
+    workspace or, for the length of the call, torch's allocator's on the very stream.
+
+    The stream is by default the device's current one, read as its raw handle, and the allocator
+    is called directly: a stream object costs 2.9 us of a call that takes 9, a tensor 7."""
+    c = torch._C
+    if index != c._cuda_getDevice():
         with torch.cuda.device(index):
-            status = function(*args, cuda._cuda_getCurrentRawStream(index) if stream is None
-                              else _stream(stream))
+            return _call(torch, index, stream, function, args, workspace, need)
+    handle = c._cuda_getCurrentRawStream(index) if stream is None else _stream(stream)
+    if need is None:
+        status = function(*args, handle)
+    elif workspace is not None:
+        if workspace.get_device() != index:
+            raise ValueError(f"workspace is on {workspace.device}, not cuda:{index}")
+        status = function(*args, workspace.data_ptr(),
+                          workspace.numel() * workspace.element_size(), handle)
+    elif need == 0:
+        status = function(*args, None, 0, handle)
     else:
-        status = function(*args, cuda._cuda_getCurrentRawStream(index) if stream is None
-                          else _stream(stream))
+        scratch = c._cuda_cudaCachingAllocator_raw_alloc(need, handle)
+        try:
+            status = function(*args, scratch, need, handle)
+        finally:
+            c._cuda_cudaCachingAllocator_raw_delete(scratch)
     if status:
         raise TpgemmError(status, tpgemm_last_error_detail())
 
@@ -705,7 +711,7 @@ def linear(A, W, bias=None, residual=None, *, act="none", scale_a=None, scale_w=
     else:
         ldy = _matrix("out", out, M, N, out_dtype, index)
     ldr = ldz = 0
-    pr = pz = pb = psa = psw = pws = None
+    pr = pz = pb = psa = psw = None
     if residual is not None:
         ldr, pr = _matrix("residual", residual, M, N, out_dtype, index), residual.data_ptr()
     if pre is not None:
@@ -718,14 +724,12 @@ def linear(A, W, bias=None, residual=None, *, act="none", scale_a=None, scale_w=
         psw = _vector("scale_w", scale_w, N, torch.float32, index)
     desc = ctypes.byref(LinearDesc(M, N, K, lda, ldw, ldr, ldy, ldz, *codes))
     pa, pw = A.data_ptr(), W.data_ptr()
-    size = 0
+    need = 0
     # (Operands on 16-byte boundaries need no workspace.)
-    if workspace is not None or (pa | pw | (lda | ldw) * dt.itemsize) & 15:
+    if (pa | pw | (lda | ldw) * dt.itemsize) & 15:
         need = lib.tpgemm_linear_workspace_bytes(pa, pw, desc)
-        if need:
-            workspace, pws, size = _scratch(torch, workspace, need, device, index)
-    _call(torch, index, stream, lib.tpgemm_linear, out.data_ptr(), pz, pa, pw, psa, psw, pb, pr,
-          desc, pws, size)
+    _call(torch, index, stream, lib.tpgemm_linear,
+          (out.data_ptr(), pz, pa, pw, psa, psw, pb, pr, desc), workspace, need)
     return out
 
 
@@ -763,11 +767,8 @@ def linear_backward(dY, A, W, pre=None, *, act="none", grad_dtype=None, need=(Tr
         dbias = torch.empty(N, dtype=grad_dtype, device=device)
         pdb = dbias.data_ptr()
     py, pa, pw = dY.data_ptr(), A.data_ptr(), W.data_ptr()
-    size, pws = lib.tpgemm_linear_backward_workspace_bytes(py, pa, pw, desc), None
-    if size:
-        workspace, pws, size = _scratch(torch, workspace, size, device, index)
-    _call(torch, index, stream, lib.tpgemm_linear_backward, pda, pdw, pdb, py, pa, pw, pz, desc,
-          pws, size)
+    _call(torch, index, stream, lib.tpgemm_linear_backward, (pda, pdw, pdb, py, pa, pw, pz, desc),
+          workspace, lib.tpgemm_linear_backward_workspace_bytes(py, pa, pw, desc))
     return dA, dW, dbias
 
 
@@ -827,8 +828,8 @@ def rmsnorm(x, weight, residual=None, *, eps=1e-6, quant=None, out_dtype=None, n
         rstd = torch.empty(rows, dtype=torch.float32, device=device)
         prstd = rstd.data_ptr()
     desc = RmsNormDesc(rows, cols, ldx, ldr, ldh, ldy, *codes, eps)
-    _call(torch, index, stream, lib.tpgemm_rmsnorm, out.data_ptr(), ph, ps, prstd, x.data_ptr(),
-          pr, pg, ctypes.byref(desc))
+    _call(torch, index, stream, lib.tpgemm_rmsnorm,
+          (out.data_ptr(), ph, ps, prstd, x.data_ptr(), pr, pg, ctypes.byref(desc)))
     return RmsNorm(out, h, scale, rstd)
 
 
@@ -848,8 +849,8 @@ def rmsnorm_backward(dy, h, rstd, weight, dh=None, *, grad_dtype=None, need=(Tru
         raise TypeError(f"weight must be {dt} or float32, got {wt}")
     pg = _vector("weight", weight, cols, wt, index)
     prstd = _vector("rstd", rstd, rows, torch.float32, index)
-    dx = dweight = pdx = pdw = pdh = pws = None
-    lddh = lddx = size = 0
+    dx = dweight = pdx = pdw = pdh = None
+    lddh = lddx = scratch = 0
     if dh is not None:
         lddh, pdh = _matrix("dh", dh, rows, cols, dt, index), dh.data_ptr()
     if need[0]:
@@ -864,9 +865,8 @@ def rmsnorm_backward(dy, h, rstd, weight, dh=None, *, grad_dtype=None, need=(Tru
     if need[1]:
         dweight = torch.empty(cols, dtype=grad_dtype, device=device)
         pdw = dweight.data_ptr()
-        size = lib.tpgemm_rmsnorm_backward_workspace_bytes(rows, cols)
-        if size:
-            workspace, pws, size = _scratch(torch, workspace, size, device, index)
-    _call(torch, index, stream, lib.tpgemm_rmsnorm_backward, pdx, pdw, dy.data_ptr(), h.data_ptr(),
-          prstd, pg, pdh, ctypes.byref(desc), pws, size)
+        scratch = lib.tpgemm_rmsnorm_backward_workspace_bytes(rows, cols)
+    _call(torch, index, stream, lib.tpgemm_rmsnorm_backward,
+          (pdx, pdw, dy.data_ptr(), h.data_ptr(), prstd, pg, pdh, ctypes.byref(desc)), workspace,
+          scratch)
     return dx, dweight

@@ -152,17 +152,16 @@ Aligned plan_aligned(const tpg::Operand& o, int64_t rows, int64_t K, int dtype, 
     return a;
 }
 
-// The operand itself or, copied there first, its place in the workspace.
-tpgemm_status use_aligned(const Aligned& a, tpg::Operand* o, int64_t rows, int64_t K, int dtype,
-                          uint8_t* ws, cudaStream_t st) {
-    if (!a.copy) return TPGEMM_OK;
+// Points the operand at its place in the workspace and adds the copy to jobs.
+void use_aligned(const Aligned& a, tpg::Operand* o, int64_t rows, int64_t K, int dtype, uint8_t* ws,
+                 tpg::AlignJobs* jobs) {
+    if (!a.copy) return;
     const int64_t lines = o->mn ? K : rows, len = o->mn ? rows : K;
     const int64_t es = elem_size(dtype);
-    TPG_TRY(launched(tpg::launch_align_rows(o->p, lines, len * es, o->ld * es, ws + a.at, a.ld * es, st),
-                     "operand copy launch"));
+    jobs->j[jobs->n++] = {static_cast<const uint8_t*>(o->p), lines, len * es, o->ld * es,
+                          ws + a.at, a.ld * es};
     o->p = ws + a.at;
     o->ld = a.ld;
-    return TPGEMM_OK;
 }
 
 // Which product kernel takes it: the few-token one, or the tcgen05 ones. Few
@@ -226,7 +225,6 @@ LinearLayout linear_layout(const tpg::LinearOp& op) {
 struct GradLayout {
     size_t dz = 0, partial = 0, total = 0;
     int64_t lddz = 0;
-    int strips = 0;
     Aligned dy, a, w;  // copies (dY's only where it is dZ itself)
 };
 
@@ -241,9 +239,9 @@ GradLayout grad_layout(const void* dY, const void* A, const void* W,
     } else if (d.K > 0) {
         L.dy = plan_aligned({dY, dense(d.lddy, d.N), 0}, d.M, d.N, d.dtype, &L.total);
     }
-    L.strips = tpg::act_grad_strips(d.M, d.N);
+    const int strips = tpg::act_grad_strips(d.M, d.N);
     L.partial = L.total;
-    L.total = align_up(L.total + size_t(L.strips) * size_t(d.N) * 4, 256);
+    if (strips > 1) L.total = align_up(L.total + size_t(strips) * size_t(d.N) * 4, 256);
     if (d.K > 0) {
         L.a = plan_aligned({A, dense(d.lda, d.K), 0}, d.M, d.K, d.dtype, &L.total);
         L.w = plan_aligned({W, dense(d.ldw, d.K), 0}, d.N, d.K, d.dtype, &L.total);
@@ -311,8 +309,10 @@ tpgemm_status tpgemm_linear(void* Y, void* Z, const void* A, const void* W, cons
     TPG_TRY(tpg::require_device(&sms));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    TPG_TRY(use_aligned(L.a, &op.a, M, K, d->dtype, ws, st));
-    TPG_TRY(use_aligned(L.w, &op.b, N, K, d->dtype, ws, st));
+    tpg::AlignJobs copies{};
+    use_aligned(L.a, &op.a, M, K, d->dtype, ws, &copies);
+    use_aligned(L.w, &op.b, N, K, d->dtype, ws, &copies);
+    TPG_TRY(launched(tpg::launch_align_rows(copies, st), "operand copy launch"));
     return run_product(op, sms, st);
 }
 
@@ -373,7 +373,7 @@ tpgemm_status tpgemm_linear_backward(void* dA, void* dW, void* dbias, const void
     if (dbias || (act && (dA || dW))) {
         tpg::ActGradOp g{M, N, dY, in[3].p, in[0].ld, in[3].ld,
                          (act && (dA || dW)) ? ws + L.dz : nullptr, L.lddz,
-                         dbias ? reinterpret_cast<float*>(ws + L.partial) : nullptr, dbias,
+                         reinterpret_cast<float*>(ws + L.partial), dbias,
                          d->dtype, d->act, d->grad};
         TPG_TRY(launched(tpg::launch_act_grad(g, st), "activation gradient launch"));
     }
@@ -384,16 +384,18 @@ tpgemm_status tpgemm_linear_backward(void* dA, void* dW, void* dbias, const void
     if (K == 0) return TPGEMM_OK;
     if (!dA && !dW) return TPGEMM_OK;
     tpg::Operand oz{dz, lddz, 0}, oa{A, in[1].ld, 0}, ow{W, in[2].ld, 0};
-    TPG_TRY(use_aligned(L.dy, &oz, M, N, d->dtype, ws, st));
+    tpg::AlignJobs copies{};
+    use_aligned(L.dy, &oz, M, N, d->dtype, ws, &copies);
+    if (dA) use_aligned(L.w, &ow, N, K, d->dtype, ws, &copies);
+    if (dW) use_aligned(L.a, &oa, M, K, d->dtype, ws, &copies);
+    TPG_TRY(launched(tpg::launch_align_rows(copies, st), "operand copy launch"));
     if (dA) {  // [M, K] = dZ [M, N] . W: the reduction runs along W's rows
-        TPG_TRY(use_aligned(L.w, &ow, N, K, d->dtype, ws, st));
         tpg::LinearOp op{M, K, N, d->dtype, oz, {ow.p, ow.ld, 1},
                          {dA, nullptr, nullptr, nullptr, nullptr, nullptr, out[0].ld, 0, 0,
                           TPGEMM_ACT_NONE, d->dtype}};
         TPG_TRY(run_product(op, sms, st));
     }
     if (dW) {  // [N, K] = dZ^T . A: along the rows of both
-        TPG_TRY(use_aligned(L.a, &oa, M, K, d->dtype, ws, st));
         tpg::LinearOp op{N, K, M, d->dtype, {oz.p, oz.ld, 1}, {oa.p, oa.ld, 1},
                          {dW, nullptr, nullptr, nullptr, nullptr, nullptr, out[1].ld, 0, 0,
                           TPGEMM_ACT_NONE, d->grad}};

@@ -87,17 +87,27 @@ struct ActGradOp {
     int64_t lddy, ldz;
     void* dZ;         // [M][lddz], or null
     int64_t lddz;
-    float* partial;   // [strips][N], or null when dbias is not wanted
-    void* dbias;
+    float* partial;   // [strips][N] for dbias of more than one strip
+    void* dbias;      // or null
     int dtype, act, grad;
 };
 int act_grad_strips(int64_t M, int64_t N);
 cudaError_t launch_act_grad(const ActGradOp& op, cudaStream_t stream);
 
-// Copies rows of `bytes` bytes, `pitch` bytes apart, to rows dst_pitch apart
-// (dst and dst_pitch multiples of 16, dst_pitch >= bytes rounded up to 16).
-cudaError_t launch_align_rows(const void* src, int64_t rows, int64_t bytes, int64_t pitch, void* dst,
-                              int64_t dst_pitch, cudaStream_t stream);
+// Copies of matrices, each of rows of `bytes` bytes, `pitch` bytes apart, to rows
+// dst_pitch apart (dst and dst_pitch multiples of 16, dst_pitch >= bytes rounded
+// up to 16); one launch for all of them, none for none.
+struct AlignJob {
+    const uint8_t* src;
+    int64_t rows, bytes, pitch;
+    uint8_t* dst;
+    int64_t dst_pitch;
+};
+struct AlignJobs {
+    AlignJob j[3];
+    int n;
+};
+cudaError_t launch_align_rows(const AlignJobs& jobs, cudaStream_t stream);
 
 // ---- root-mean-square norm ----
 struct RmsNormOp {
