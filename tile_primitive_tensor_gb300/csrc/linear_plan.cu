@@ -35,11 +35,13 @@ tpgemm_status max_pairs(const TcLinear& p, int* pairs) {
 }
 
 // The models below are in ns at the clocks that products run at here (1.85
-// GHz): an SM takes in 64 bytes a clock; memory delivers about 5.5 kB a ns to
-// all SMs together, L2 about 11 to CTAs that each read a P tile of their own.
+// GHz): an SM takes in 64 bytes a clock from memory or L2, and 17 from other
+// SMs; memory delivers about 5.5 kB a ns to all SMs together, L2 about 13 to
+// CTAs that each read a P tile of their own.
 constexpr double kClock = 1.85;
 constexpr double kMemory = 5500;
-constexpr double kL2 = 11000;
+constexpr double kL2 = 13000;
+constexpr double kPeer = 17;
 
 // Shared bytes of one split stage. P tiles of fewer than 128 rows leave the MMA
 // to read on into the bytes behind them: their lanes' results are not used.
@@ -138,7 +140,7 @@ Choice plan_tile(const LinearOp& op, int64_t kb, int sms, const LinearTuning& t)
         const int64_t tiles = ceil_div(op.M, 256) * ceil_div(op.N, bn);
         const double stage = std::max(225.0, (256 + bn) * (bn == 256 ? 1.01 : 1.07) / kClock);
         const double loop = std::max(double(ceil_div(tiles, sms / 2)) * (double(kb) * stage + 200), memory);
-        const double ns = 3500 + bn * 12 + loop;
+        const double ns = 3500 + bn * 18 + loop;
         if (ns < best.ns) {
             best.ns = ns;
             best.pair = 1;
@@ -154,21 +156,30 @@ int64_t places(int split, bool half_sm) {
     return (split <= 2 ? 152 : split == 4 ? 144 : 120) * (half_sm ? 2 : 1);
 }
 
-// The split kernel. Blocks take half of an SM's shared memory while that holds
-// five stages, and are then two to an SM; the tile's height and the split are
-// those that fill the most of those places, 128 rows counting a fifth more, since shorter
-// boxes stream more slowly (17 x 4096 x 4096 bf16, split / rows: 8 / 128 8.1 us,
-// 4 / 128 8.5, 2 / 64 13.9; 144 rows: 4 / 128 12.3, 2 / 64 15.4).
-Choice plan_split(const LinearOp& op, int64_t kb, const LinearTuning& t) {
+// What reading costs more when a row's stages do not start on 128-byte lines
+// and take two of them (144 rows of f16, split 1: 40.7 us at 16392 x 4104, 27.6
+// at 16384 x 4096).
+double straddle(const LinearOp& op) {
+    auto odd = [&](const Operand& o) { return (o.ld * elem_size(op.dtype)) % 128 != 0; };
+    return odd(op.a) || odd(op.b) ? 1.5 : 1.0;
+}
+
+// The split kernel with Q in tiles_q tiles. Blocks take half of an SM's shared
+// memory while that holds five stages, and are then two to an SM; the tile's
+// height and the split are those that fill the most of those places, 128 rows
+// counting a fifth more, since shorter boxes stream more slowly (17 x 4096 x
+// 4096 bf16, split / rows: 8 / 128 8.1 us, 4 / 128 8.5, 2 / 64 13.9; 144 rows:
+// 4 / 128 12.3, 2 / 64 15.4).
+Choice plan_split(const LinearOp& op, int64_t kb, const LinearTuning& t, int64_t tiles_q) {
     Choice best;
     // The output's longer side along the lanes; Q in tiles of equal width.
     const bool swap = op.N >= op.M;
     const int64_t Mp = swap ? op.N : op.M, Nq = swap ? op.M : op.N;
     const bool p_mn = swap ? op.b.mn : op.a.mn, q_mn = swap ? op.a.mn : op.b.mn;
-    const int64_t tiles_q = ceil_div(Nq, 256);
     TcLinear p{};
     p.swap = swap;
     p.bn = int(ceil_div(ceil_div(Nq, tiles_q), 16) * 16);
+    tiles_q = ceil_div(Nq, p.bn);
     double most = -1;
     for (int bp = 128; bp >= 64; bp -= 16) {
         if (t.bp > 0 ? bp != t.bp : bp == 80) continue;
@@ -193,11 +204,26 @@ Choice plan_split(const LinearOp& op, int64_t kb, const LinearTuning& t) {
         best.bp = bp;
         best.split = split;
         best.half_sm = half_sm;
-        const double share = double(ceil_div(kb, split));
-        const double busy = double(ceil_div(ctas, 148)) * share * 2.0 * (bp + p.bn) / kClock;
-        const double l2 = double(ctas) * share * (bp + p.bn) * 128 / kL2;
-        best.ns = 3900 + (split > 1 ? 700 : 0) + double(ceil_div(ctas, fit)) * bp * p.bn * 4 / 32 +
-                  std::max(busy, std::max(memory_ns(op), l2));
+        const double share = double(ceil_div(kb, split)), resident = double(ceil_div(ctas, 148));
+        const double busy = resident * share * 2.0 * (bp + p.bn) / kClock;
+        const double l2 = double(ctas) * share * (bp + p.bn) * 128 * straddle(op) / kL2;
+        const double sums = resident * bp * p.bn * 4;  // bytes an SM joins
+        const double join = split > 1 ? 1000 + sums * (split - 1) / split / kPeer / kClock : sums / 128;
+        best.ns = 4300 + join + std::max(busy, std::max(memory_ns(op), l2));
+    }
+    return best;
+}
+
+// The number of Q tiles: one more of them makes the tiles narrower and the
+// split shallower, so that less passes between SMs but P is read more often
+// (512 x 1024 x 4096 bf16, tiles of Q / split: 2 / 4 15.3 us, 3 / 4 12.4, 4 / 4
+// 11.5; 144 x 4096 x 4096: 1 / 4 12.5, 2 / 2 14.8).
+Choice plan_split(const LinearOp& op, int64_t kb, const LinearTuning& t) {
+    const int64_t Nq = std::min(op.M, op.N), least = ceil_div(Nq, 256);
+    Choice best;
+    for (int64_t q = least; q < least + 4 && q * 32 <= std::max(Nq, least * 32); ++q) {
+        const Choice c = plan_split(op, kb, t, q);
+        if (c.ns < best.ns) best = c;
     }
     return best;
 }
@@ -257,10 +283,19 @@ tpgemm_status run_linear_tc(const LinearOp& op, int sms, cudaStream_t stream) {
         if (s != TPGEMM_OK) return s;
         grid = 2 * std::min(p.tiles, pairs);
     } else {
-        p.stages = split_stages(p.half_sm ? kSplitHalfSmem - kBarrierBytes : budget, p.p_bytes, p.q_bytes);
-        p.ring_bytes = std::max(uint32_t(p.stages) * (p.p_bytes + p.q_bytes),
-                                uint32_t((split_partial_bytes(p) + 1023) / 1024 * 1024));
-        p.ring_bytes = std::max(p.ring_bytes, uint32_t(p.stages - 1) * (p.p_bytes + p.q_bytes) + 16384u);
+        const size_t have = p.half_sm ? kSplitHalfSmem - kBarrierBytes : budget;
+        const uint32_t stage = p.p_bytes + p.q_bytes, sums = uint32_t((split_partial_bytes(p) + 1023) / 1024 * 1024);
+        p.stages = split_stages(have, p.p_bytes, p.q_bytes);
+        // A split that needs few stages leaves room for the sums beside them.
+        const int few = std::max(2, int(ceil_div(p.k_blocks, p.split)));
+        const uint32_t few_bytes = std::max(uint32_t(few) * stage, uint32_t(few - 1) * stage + 16384u);
+        if (p.split > 1 && few <= p.stages && few_bytes + sums <= have) {
+            p.stages = few;
+            p.sums_at = (few_bytes + 1023u) / 1024u * 1024u;
+            p.ring_bytes = p.sums_at + sums;
+        } else {
+            p.ring_bytes = std::max(std::max(uint32_t(p.stages) * stage, sums), uint32_t(p.stages - 1) * stage + 16384u);
+        }
         p.tmem_cols = 32;
         while (p.tmem_cols < 32 * ((p.bn + 31) / 32)) p.tmem_cols *= 2;
         grid = p.tiles * p.split;

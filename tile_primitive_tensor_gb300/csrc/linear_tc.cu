@@ -662,10 +662,15 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 // shared memory shares the SM with another one, whose fills run under this
 // one's set-up and joining.
 //
-// Each CTA leaves its partial sums in shared memory (in the stages, which are
-// idle by then), lines along the output's contiguous direction; after a cluster
-// barrier every CTA adds up and writes its share of the lines, 16 bytes of
-// partial sums of each rank at a time, always in rank order.
+// The tile's lines along the output's contiguous direction are dealt out to the
+// cluster's CTAs in turn. Each CTA stores its partial sums of a line straight
+// from tensor memory into the shared memory of the line's owner, over the
+// stages once all CTAs' MMAs are done, or at once into room left beside them;
+// after a cluster barrier the owners add up and write their lines, in rank
+// order, so results repeat. What passes
+// between SMs moves at 17 bytes a clock into each, by loads, stores or bulk
+// copies alike (96 KB in a cluster of 4: 6860, 5730, 6030 clocks); stores need
+// no round trip (JOIN_NOTE).
 constexpr int kSplitThreads = 256;
 
 struct SplitSmem {
@@ -687,13 +692,31 @@ __device__ __forceinline__ SplitSmem carve_split(uint8_t* raw, const TcLinear& p
     return s;
 }
 
-__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(addr)
-                 : "memory");
-    return v;
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, uint32_t v) {
+    asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+// The two halves of cluster_sync().
+__device__ __forceinline__ void cluster_arrive() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// x[i] of lane j and x[j] of lane i change places.
+__device__ __forceinline__ void transpose32(int lane, uint32_t (&x)[32]) {
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) {
+        const bool high = (lane & s) != 0;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            if (i & s) continue;
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, high ? x[i] : x[i + s], s);
+            if (high) x[i] = got;
+            else x[i + s] = got;
+        }
+    }
 }
 
 // Four neighbouring outputs n.. of row m (cnt of them in the matrix; vec: all
@@ -736,16 +759,56 @@ __device__ __forceinline__ void store4(void* base, int64_t at, bool vec, int cnt
     }
 }
 
-// This CTA's share of the tile's `rows` lines of `cols` values: a line to a warp
-// at a time, four values to a lane, kAhead lines' sums in flight. Bias and
-// column scales are the same for all lines and loaded once.
+// Line l of a tile is rank l % SPLIT's, the l / SPLIT-th of its lines; an owner
+// holds `per` lines of every rank's partial sums, a rank's one after the other.
+// This stores the accumulators of the first `rows` lines there.
+template <int SPLIT, bool SWAP>
+__device__ __forceinline__ void deal_lines(const TcLinear& p, uint32_t tmem, float* part, int per, int pitch,
+                                           int rank, int rows) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int quad = warp & 3, pl = quad * 32 + lane;
+    const uint32_t mine = smem_u32(part) + uint32_t(rank * per * pitch) * 4u;
+    for (int c = warp >> 2; 32 * c < p.bn; c += 2) {
+        uint32_t r[32];
+        tmem_ld_32x32b_x32(tmem + (uint32_t(quad * 32) << 16) + uint32_t(32 * c), r);
+        tmem_ld_wait(r);
+        if (!SWAP && SPLIT == 1) {  // a lane is a line
+            if (pl < rows)
+#pragma unroll
+                for (int i = 0; i < 32; i += 4)
+                    if (32 * c + i < p.bn)
+                        *reinterpret_cast<uint4*>(part + pl * pitch + 32 * c + i) =
+                            make_uint4(r[i], r[i + 1], r[i + 2], r[i + 3]);
+        } else {  // a lane is a place in each of 32 lines, so that stores are contiguous
+            if (!SWAP) transpose32(lane, r);
+            const int place = SWAP ? pl : 32 * c + lane;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                const int l = (SWAP ? 32 * c : 32 * quad) + i;
+                if (l < rows && (SWAP || place < p.bn)) {
+                    if (SPLIT == 1)
+                        part[l * pitch + place] = __uint_as_float(r[i]);
+                    else
+                        st_cluster_f32(mapa_shared(mine + uint32_t(l / SPLIT * pitch + place) * 4u,
+                                                   uint32_t(i % SPLIT)), r[i]);
+                }
+            }
+        }
+        __syncwarp();
+    }
+}
+
+// Adds up and writes this CTA's lines, of `cols` values: a line to a warp at a
+// time, four values to a lane, kAhead lines' sums in flight. Bias and column
+// scales are the same for all lines and loaded once.
 template <typename T, int SPLIT>
-__device__ __forceinline__ void join_lines(const TcLinear& p, const float* part, int pitch, int rank,
+__device__ __forceinline__ void join_lines(const TcLinear& p, const float* part, int per, int pitch, int rank,
                                            int rows, int cols, int64_t m0, int64_t n0) {
     constexpr int kAhead = SPLIT == 8 ? 2 : 4;
-    constexpr int kWarps = kSplitThreads / 32 * SPLIT;  // of the cluster
+    constexpr int kWarps = kSplitThreads / 32;
     const Epilogue& e = p.e;
-    const int first = rank * (kSplitThreads / 32) + int(threadIdx.x >> 5);
+    const int owned = (rows - rank + SPLIT - 1) / SPLIT;
+    const int first = int(threadIdx.x >> 5);
     for (int at = 4 * int(threadIdx.x & 31); at < cols; at += 128) {
         const int cnt = min(4, cols - at);
         const bool vec = p.vec && cnt == 4;
@@ -753,17 +816,15 @@ __device__ __forceinline__ void join_lines(const TcLinear& p, const float* part,
         float bias[4] = {}, sw[4] = {1.f, 1.f, 1.f, 1.f};
         if (e.bias) load4<T>(e.bias, n, vec, cnt, bias);
         if (e.sw) load4<float>(e.sw, n, vec, cnt, sw);
-        for (int line = first; line < rows; line += kWarps * kAhead) {
+        for (int line = first; line < owned; line += kWarps * kAhead) {
             float x[kAhead][4];
 #pragma unroll
             for (int j = 0; j < kAhead; ++j) {
                 // (Past the last line: the last one again, not written.)
-                const float* own = part + min(line + j * kWarps, rows - 1) * pitch + at;
+                const float* own = part + min(line + j * kWarps, owned - 1) * pitch + at;
                 float4 v[SPLIT];
 #pragma unroll
-                for (int r = 0; r < SPLIT; ++r)
-                    v[r] = SPLIT == 1 ? *reinterpret_cast<const float4*>(own)
-                                      : ld_cluster_f32x4(mapa_shared(smem_u32(own), uint32_t(r)));
+                for (int r = 0; r < SPLIT; ++r) v[r] = *reinterpret_cast<const float4*>(own + r * per * pitch);
                 x[j][0] = v[0].x;
                 x[j][1] = v[0].y;
                 x[j][2] = v[0].z;
@@ -780,14 +841,14 @@ __device__ __forceinline__ void join_lines(const TcLinear& p, const float* part,
             if (e.R) {
 #pragma unroll
                 for (int j = 0; j < kAhead; ++j) {
-                    const int64_t m = m0 + min(line + j * kWarps, rows - 1);
+                    const int64_t m = m0 + min(line + j * kWarps, owned - 1) * SPLIT + rank;
                     load4<T>(e.R, m * e.ldr + n, vec, cnt, res[j]);
                 }
             }
 #pragma unroll
             for (int j = 0; j < kAhead; ++j) {
-                if (line + j * kWarps >= rows) break;
-                const int64_t m = m0 + line + j * kWarps;
+                if (line + j * kWarps >= owned) break;
+                const int64_t m = m0 + (line + j * kWarps) * SPLIT + rank;
                 const float sa = e.sa ? e.sa[m] : 1.f;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) x[j][i] = fmaf(x[j][i], sa * sw[i], bias[i]);
@@ -836,6 +897,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
     }
     tc_fence_before_sync();
     __syncthreads();
+    if (p.split > 1 && p.sums_at != 0) cluster_arrive();
     tc_fence_after_sync();
     grid_launch_dependents();
     const uint32_t tmem = *s.tmem_base;
@@ -904,54 +966,40 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
     bool ok = wait_bounded(s.acc_full, 0, s.abort, tmo, true);
     ok = __all_sync(0xffffffffu, ok);
     tc_fence_after_sync();
-    float* part = reinterpret_cast<float*>(s.stages);
-    // Lines of the output's contiguous direction: of bp (swapped) or bn values,
-    // four words more apart.
-    const int len = SWAP ? 128 : p.bn, lines = SWAP ? p.bn : p.bp, pitch = len + 4;
-    if (ok && !*s.abort) {
-        const int quad = warp & 3, pl = quad * 32 + lane;
-        for (int c = warp >> 2; 32 * c < p.bn; c += 2) {
-            uint32_t r[32];
-            tmem_ld_32x32b_x32(tmem + (uint32_t(quad * 32) << 16) + uint32_t(32 * c), r);
-            tmem_ld_wait(r);
-            if constexpr (SWAP) {  // a lane is a place in each of 32 lines
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    if (32 * c + i < p.bn) part[(32 * c + i) * pitch + pl] = __uint_as_float(r[i]);
-            } else if (pl < p.bp) {  // a lane is a line
-#pragma unroll
-                for (int i = 0; i < 32; i += 4)
-                    if (32 * c + i < p.bn)
-                        *reinterpret_cast<float4*>(part + pl * pitch + 32 * c + i) =
-                            make_float4(__uint_as_float(r[i]), __uint_as_float(r[i + 1]),
-                                        __uint_as_float(r[i + 2]), __uint_as_float(r[i + 3]));
-            }
-            __syncwarp();
+    float* part = reinterpret_cast<float*>(s.stages + p.sums_at);
+    // Lines of bp (swapped) or bn values, four words more apart.
+    const int pitch = (SWAP ? 128 : p.bn) + 4;
+    const int64_t M = SWAP ? p.Nq : p.Mp, N = SWAP ? p.Mp : p.Nq;
+    const int64_t m0 = SWAP ? q0 : p0, n0 = SWAP ? p0 : q0;
+    const int cols = int(min(int64_t(SWAP ? p.bp : p.bn), N - n0));
+    const int rows = int(min(int64_t(SWAP ? p.bn : p.bp), M - m0));
+    const auto deal_and_join = [&](auto n) {
+        constexpr int kSplit = decltype(n)::value;
+        const int per = (SWAP ? p.bn : p.bp) / kSplit;
+        if (kSplit > 1) {
+            // Peers have begun; without sums_at, their stages are idle too.
+            if (p.sums_at == 0) cluster_arrive();
+            cluster_wait();
         }
-    }
-    tc_fence_before_sync();
-    __syncwarp();
-    if (p.split > 1) cluster_sync();
-    else __syncthreads();
-    grid_dependency_wait();
-    if (!*s.abort) {
-        const int64_t M = SWAP ? p.Nq : p.Mp, N = SWAP ? p.Mp : p.Nq;
-        const int64_t m0 = SWAP ? q0 : p0, n0 = SWAP ? p0 : q0;
-        const int cols = int(min(int64_t(SWAP ? p.bp : p.bn), N - n0));
-        const int rows = int(min(int64_t(lines), M - m0));
-        switch (p.split) {
-            case 1: join_lines<T, 1>(p, part, pitch, rank, rows, cols, m0, n0); break;
-            case 2: join_lines<T, 2>(p, part, pitch, rank, rows, cols, m0, n0); break;
-            case 4: join_lines<T, 4>(p, part, pitch, rank, rows, cols, m0, n0); break;
-            default: join_lines<T, 8>(p, part, pitch, rank, rows, cols, m0, n0); break;
-        }
+        if (ok && !*s.abort) deal_lines<kSplit, SWAP>(p, tmem, part, per, pitch, rank, rows);
+        tc_fence_before_sync();
+        __syncwarp();
+        if (kSplit > 1) cluster_sync();
+        else __syncthreads();
+        grid_dependency_wait();
+        if (!*s.abort) join_lines<T, kSplit>(p, part, per, pitch, rank, rows, cols, m0, n0);
+    };
+    switch (p.split) {
+        case 1: deal_and_join(std::integral_constant<int, 1>()); break;
+        case 2: deal_and_join(std::integral_constant<int, 2>()); break;
+        case 4: deal_and_join(std::integral_constant<int, 4>()); break;
+        default: deal_and_join(std::integral_constant<int, 8>()); break;
     }
     if (*s.abort && warp == 0 && lane == 0)
         for (int i = 0; i < p.stages; ++i)
             if (issued_any & (1u << i))
                 wait_bounded(&s.full[i], (issued_parity >> i) & 1u, s.abort, tmo, true);
     __syncwarp();
-    if (p.split > 1) cluster_sync();  // peers have read this CTA's partial sums
     if (warp == 1) {
         tc_fence_after_sync();
         tmem_dealloc<1>(tmem, uint32_t(p.tmem_cols));
@@ -1012,8 +1060,9 @@ cudaError_t launch_tc_linear(const TcLinearMaps& maps, const TcLinear& p, int gr
     const size_t ring = size_t(p.stages) * (p.p_bytes + p.q_bytes);
     if (p.stages < 2 || p.stages > 32 || cluster < 1 || cluster > 8 || grid % cluster != 0 ||
         p.bn % 16 != 0 || p.bn > 256 || (p.pair && (p.bn % 32 != 0 || p.group < 1)) ||
-        (!p.pair && (p.bp > 128 || p.bp % 16 != 0 || p.split > p.k_blocks || (p.split & (p.split - 1)) || ring > p.ring_bytes ||
-                     split_partial_bytes(p) > p.ring_bytes ||
+        (!p.pair && (p.bp > 128 || p.bp % 16 != 0 || p.split > p.k_blocks || (p.split & (p.split - 1)) ||
+                     ring > (p.sums_at ? p.sums_at : p.ring_bytes) ||
+                     split_partial_bytes(p) + p.sums_at > p.ring_bytes ||
                      p.ring_bytes + 8 * (2 * size_t(p.stages) + 1) + 16 > tc_linear_smem(p))))
         return cudaErrorInvalidValue;
     const size_t smem = tc_linear_smem(p);

@@ -17,6 +17,7 @@ struct TcLinear {
     int stages;            // depth of the TMA ring
     uint32_t p_bytes, q_bytes;  // shared bytes of one stage's operands (of one CTA)
     uint32_t ring_bytes;   // split kernel: shared bytes of ring and partial sums
+    uint32_t sums_at;      // split kernel: their place; 0: over the stages
     uint32_t idesc;
     int tmem_cols;         // split kernel
     int split;             // split kernel: CTAs of a cluster, each a share of K
