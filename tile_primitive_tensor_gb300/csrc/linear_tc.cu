@@ -379,7 +379,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 
     const int prod = warp == 0 ? 0 : (warp == 2 ? 1 : -1);
     if (prod >= 0) {
-        grid_dependency_wait();
         const uint64_t pol = l2_policy(2);  // panels are read again by later tiles
         const int q_rows = p.bn / 2;        // of this CTA's half
         const int q_atoms = (q_rows + 63) / 64;
@@ -396,6 +395,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             const int p0 = (2 * tp + rank) * 128;
             const int q0 = tq * p.bn + rank * q_rows;
             int kb = p.k_rotate ? int(int64_t(t) * nk / p.tiles) : 0;
+            if (t == cid) grid_dependency_wait();
             for (int i = 0; i < nk; ++i, turn ^= 1, kb = kb + 1 == nk ? 0 : kb + 1) {
                 if (turn == prod) {
                     if (!__all_sync(0xffffffffu, wait_bounded(&s.empty[stage], phase ^ 1u, s.abort, tmo))) {
@@ -670,7 +670,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 // order, so results repeat. What passes
 // between SMs moves at 17 bytes a clock into each, by loads, stores or bulk
 // copies alike (96 KB in a cluster of 4: 6860, 5730, 6030 clocks); stores need
-// no round trip (JOIN_NOTE).
+// no round trip (144 x 4096 x 4096: 12.5 us against 13.4 with loads).
 constexpr int kSplitThreads = 256;
 
 struct SplitSmem {

