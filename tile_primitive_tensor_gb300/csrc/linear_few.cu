@@ -33,7 +33,7 @@ __device__ __forceinline__ uint4 load16(const T* r, bool live, int64_t k, int64_
     uint4 v = make_uint4(0, 0, 0, 0);
     if (!live || k >= K) return v;
     if (VEC && k + E <= K) {
-        asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+        asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                      : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                      : "l"(r + k));
         return v;
