@@ -405,3 +405,34 @@ def test_few_tokens_splits(split, M, N, K, tune):
     for dtype in (F16, BF16, E4M3, E5M2):
         check_linear(M, N, K, dtype, act="silu", pre=True, seed=split)
     tune.delenv("TPGEMM_LINEAR_SPLIT")
+
+
+@pytest.mark.parametrize("split", [1, 2, 4, 8])
+@pytest.mark.parametrize("M,N,K", [(200, 264, 8200), (264, 40, 8192), (24, 1000, 4104), (1000, 136, 9000)])
+def test_splits_of_long_sums(split, M, N, K, tune):
+    # Partial sums over the stages (long shares of K) and beside them, lines either way round.
+    tune.setenv("TPGEMM_LINEAR_PATH", "split")
+    tune.setenv("TPGEMM_LINEAR_SPLIT", str(split))
+    check_linear(M, N, K, BF16, act="silu", pre=True, seed=split)
+    check_linear(M, N, K // 16, F16, act="gelu", out=F32, seed=split)
+    for name in ("PATH", "SPLIT"):
+        tune.delenv("TPGEMM_LINEAR_" + name)
+
+
+def test_scratch_belongs_to_the_stream_it_is_used_on():
+    # Memory freed on the current stream is handed out again at once: what a call on another
+    # stream still uses must not be among it.
+    g = gen(31)
+    dY, Z = normal(g, 2000, 1000, dtype=F16), normal(g, 2000, 1000, dtype=F16)
+    A, W = normal(g, 2000, 1001, dtype=F16), normal(g, 1000, 1001, std=0.1, dtype=F16)
+    want = tp.linear_backward(dY, A, W, Z, act="silu")
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for _ in range(20):
+        got = tp.linear_backward(dY, A, W, Z, act="silu", stream=s)
+        junk = [torch.full((n * 1000,), 255, dtype=torch.uint8, device="cuda") for n in (2000, 4000, 8000)]
+        s.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+        torch.cuda.synchronize()
+        del junk

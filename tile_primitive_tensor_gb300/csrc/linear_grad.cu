@@ -7,8 +7,11 @@
 // 512 columns and its sums go to partial[strip]. A second launch adds the
 // strips in order, so the result does not depend on the order in which blocks
 // run. Few rows are one strip, of blocks of 64 columns and 32 rows at a time,
-// and end in dbias itself. Bound by memory: dY and Z are read once and dZ is
-// written once.
+// and end in dbias itself. dY and Z are read once and dZ is written once; with
+// an activation the bound is between memory and the instructions of its
+// derivative (about 24 an element): dbias of 8192 x 8192 bf16 34 us without one
+// (58 % of memory's rate), 65 with gelu. 64 registers, so that an SM has 32
+// warps, against 74 and 24: 90 us with gelu.
 #include <algorithm>
 
 #include "column_sum.cuh"
@@ -30,26 +33,56 @@ __device__ __forceinline__ void act_grad_strip(const ActGradOp& op, int strips, 
     if (n >= op.N) return;
     const int cnt = op.N - n < kPer ? int(op.N - n) : kPer;
     vec = vec && cnt == kPer;
-#pragma unroll 2
-    for (int64_t m = m_begin + lane_row; m < m_end; m += kThreads / SIDE) {
-        float d[8];
-        load8<T>(op.dY, m * op.lddy + n, vec, cnt, d);
-        if constexpr (ACT != TPGEMM_ACT_NONE) {
-            float z[8];
-            load8<T>(op.Z, m * op.ldz + n, vec, cnt, z);
+    constexpr bool kAct = ACT != TPGEMM_ACT_NONE;
+    constexpr int kStep = kThreads / SIDE;
+    const auto row = [&](int64_t m, float (&dd)[8], const float (&z)[8]) {
+        if constexpr (kAct) {
 #pragma unroll
             for (int j = 0; j < 8; j += 2)
-                split(mul(f2(d[j], d[j + 1]), act_bwd<ACT>(f2(z[j], z[j + 1]))), d[j], d[j + 1]);
+                split(mul(f2(dd[j], dd[j + 1]), act_bwd<ACT>(f2(z[j], z[j + 1]))), dd[j], dd[j + 1]);
             // The two products read dZ in the operands' own type.
-            if (op.dZ) store8<T>(op.dZ, m * op.lddz + n, vec, cnt, d);
+            if (op.dZ) store8<T>(op.dZ, m * op.lddz + n, vec, cnt, dd);
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sum[j] += d[j];
+        for (int j = 0; j < 8; ++j) sum[j] += dd[j];
+    };
+    if (vec) {
+        // kAhead rows' loads are under way while one is computed.
+        constexpr int kAhead = kAct ? 2 : 4;
+        const T* pd = static_cast<const T*>(op.dY) + n;
+        const T* pz = static_cast<const T*>(op.Z) + n;
+        uint4 rd[kAhead], rz[kAhead];
+        const auto fetch = [&](int i, int64_t m) {
+            if (m >= m_end) return;
+            rd[i] = *reinterpret_cast<const uint4*>(pd + m * op.lddy);
+            if constexpr (kAct) rz[i] = *reinterpret_cast<const uint4*>(pz + m * op.ldz);
+        };
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) fetch(i, m_begin + lane_row + i * kStep);
+        for (int64_t m = m_begin + lane_row; m < m_end; m += kAhead * kStep) {
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                const int64_t at = m + i * kStep;
+                if (at >= m_end) break;
+                float dd[8], z[8];
+                unpack8<T>(rd[i], dd);
+                if constexpr (kAct) unpack8<T>(rz[i], z);
+                fetch(i, at + kAhead * kStep);
+                row(at, dd, z);
+            }
+        }
+        return;
+    }
+    for (int64_t m = m_begin + lane_row; m < m_end; m += kStep) {
+        float dd[8], z[8];
+        load8<T>(op.dY, m * op.lddy + n, false, cnt, dd);
+        if constexpr (kAct) load8<T>(op.Z, m * op.ldz + n, false, cnt, z);
+        row(m, dd, z);
     }
 }
 
 template <typename T, int SIDE>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 4)
     act_grad_kernel(const __grid_constant__ ActGradOp op, int strips, bool vec) {
     constexpr int kRows = kThreads / SIDE, kCols = SIDE * kPer;
     __shared__ float s[kRows][kCols];
