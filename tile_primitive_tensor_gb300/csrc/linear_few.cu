@@ -25,6 +25,7 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kRows = 16;   // rows of W in a block
 constexpr int kRun = 4;     // 16-byte loads of a row that a thread has in flight at a time
+constexpr int kPrefetch = 2;  // runs of a warp asked for ahead
 
 // The 16 bytes of row r from element k on (zero past K or for no row).
 template <typename T, bool VEC>
@@ -45,6 +46,10 @@ __device__ __forceinline__ uint4 load16(const T* r, bool live, int64_t k, int64_
     for (int i = 0; i < E; ++i)
         if (k + i < K) w[i * sizeof(T) / 4] |= uint32_t(p[k + i]) << (8 * (i * sizeof(T) % 4));
     return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
 }
 
 // Two neighbouring 8-bit elements as an f16 pair.
@@ -98,6 +103,17 @@ __global__ void __launch_bounds__(32 * kWarps) linear_few_kernel(const __grid_co
     const int64_t step = 4 * E * kRun;  // K of one run of a warp
     const int64_t stride = step * kWarps * split;
     grid_launch_dependents();
+    // Ask L2 for the first weights before waiting for the previous grid: its
+    // writes land in L2 too, so no line there is ever stale.
+    if (VEC && (t4 & 1) == 0) {
+        for (int j = 0; j < kPrefetch; ++j) {
+            const int64_t k = (int64_t(rank) * kWarps + warp) * step + j * stride + t4 * (2 * E * kRun / 2);
+            if (k < op.K) {
+                if (live_lo) prefetch_l2(lo_row + k);
+                if (live_hi) prefetch_l2(hi_row + k);
+            }
+        }
+    }
     grid_dependency_wait();
     float acc[TT][4] = {};
     for (int64_t k0 = (int64_t(rank) * kWarps + warp) * step; k0 < op.K; k0 += stride) {
