@@ -26,6 +26,7 @@ constexpr int kWarps = 8;
 constexpr int kRows = 16;   // rows of W in a block
 constexpr int kRun = 4;     // 16-byte loads of a row that a thread has in flight at a time
 constexpr int kPrefetch = 2;  // runs of a warp asked for ahead
+constexpr int64_t kManyRows = 2 * 152 * kRows;  // of W: more than two blocks to an SM
 
 // The 16 bytes of row r from element k on (zero past K or for no row).
 template <typename T, bool VEC>
@@ -210,13 +211,17 @@ cudaError_t launch_typed(const LinearOp& op, int split, cudaStream_t stream) {
 bool linear_few_takes(const LinearOp& op) { return op.M <= kFewTokens && !op.a.mn && !op.b.mn; }
 
 // Against the tcgen05 kernels, which stream large weights faster and do not
-// widen 8-bit ones, but take 4.3 us at the least (one token, this / tcgen05:
-// 1024 x 1024 bf16 2.5 / 4.4 us, 4096 x 4096 8.7 / 8.2, 4096 x 16384 28.1 / 21.3;
-// 16384 x 4096 e4m3 19.8 / 12.4).
+// widen 8-bit ones, but take 3.5 us at the least. Here a block has 16 weight
+// rows whatever their length, so many short rows cost more than few long ones;
+// there it is the other way round (one token, N x K, this / tcgen05: 512 x 1024
+// bf16 2.5 / 3.6 us, 4096 x 4096 8.5 / 9.7, 1024 x 16384 9.5 / 13.0, 8192 x 2048
+// 10.2 / 7.8, 16384 x 512 7.9 / 6.0, 4096 x 8192 15.4 / 14.4; e4m3 4096 x 1024
+// 3.8 / 5.0, 1024 x 8192 6.5 / 6.0, 4096 x 4096 8.5 / 7.2).
 bool linear_few_wins(const LinearOp& op) {
     if (!tma_rows(op.a, op.M, op.K, op.dtype) || !tma_rows(op.b, op.N, op.K, op.dtype)) return true;
     const int64_t weights = op.N * op.K * elem_size(op.dtype);
-    return weights <= (elem_size(op.dtype) == 1 ? int64_t(12) << 20 : int64_t(40) << 20);
+    if (op.N > kManyRows && weights > int64_t(4) << 20) return false;
+    return weights <= (elem_size(op.dtype) == 1 ? int64_t(6) << 20 : int64_t(40) << 20);
 }
 
 cudaError_t launch_linear_few(const LinearOp& op, int sms, cudaStream_t stream) {
