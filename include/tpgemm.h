@@ -538,10 +538,10 @@ tpgemm_status tpgemm_linear(void* Y, void* Z, const void* A, const void* W, cons
                             const tpgemm_linear_desc* d, void* workspace, size_t workspace_bytes,
                             void* stream);
 
-/* Bytes of workspace tpgemm_linear needs: 0 unless more than 16 rows of A are
- * multiplied and A's or W's rows do not start on 16-byte boundaries; those
- * operands are then copied to rows that do. The addresses matter by their
- * alignment only. 0 for a description that tpgemm_linear rejects. */
+/* Bytes of workspace tpgemm_linear needs, for copies of operands: more than 16
+ * rows of A by a W where one's rows do not start on 16-byte boundaries, or 48 to
+ * 256 rows that do not start on 128-byte ones by a large W; else 0. The
+ * addresses matter by their alignment only. 0 for a description that tpgemm_linear rejects. */
 size_t tpgemm_linear_workspace_bytes(const void* A, const void* W, const tpgemm_linear_desc* d);
 
 /*

@@ -725,8 +725,8 @@ def linear(A, W, bias=None, residual=None, *, act="none", scale_a=None, scale_w=
     desc = ctypes.byref(LinearDesc(M, N, K, lda, ldw, ldr, ldy, ldz, *codes))
     pa, pw = A.data_ptr(), W.data_ptr()
     need = 0
-    # (Operands on 16-byte boundaries need no workspace.)
-    if (pa | pw | (lda | ldw) * dt.itemsize) & 15:
+    # (Operands whose rows start on 128-byte lines need no workspace.)
+    if (pa | pw | (lda | ldw) * dt.itemsize) & 127:
         need = lib.tpgemm_linear_workspace_bytes(pa, pw, desc)
     _call(torch, index, stream, lib.tpgemm_linear,
           (out.data_ptr(), pz, pa, pw, psa, psw, pb, pr, desc), workspace, need)

@@ -70,6 +70,11 @@ bool tma_rows(const Operand& o, int64_t rows, int64_t K, int dtype) {
            (lines <= 1 || (o.ld * elem_size(dtype)) % 16 == 0);
 }
 
+bool whole_lines(const Operand& o, int64_t rows, int64_t K, int dtype) {
+    const int64_t lines = o.mn ? K : rows;
+    return reinterpret_cast<uintptr_t>(o.p) % 128 == 0 && (lines <= 1 || (o.ld * elem_size(dtype)) % 128 == 0);
+}
+
 namespace {
 
 // box_rows: rows of a K-contiguous box; K rows of a box along the operand's rows.
@@ -132,13 +137,16 @@ double memory_ns(const LinearOp& op) {
 // takes in (128 + bn / 2 rows of 128 bytes; 7 % over that measured), which at
 // bn = 256 is the tensor rate too, and takes 225 ns at the least (512 x 4096 x
 // 4096 bf16: 20.3 us at bn = 128, 24.0 at 256; 4096^3: 74.8 at 224, 78.8 at 256).
+// Q's rows off the 128-byte lines take a seventh longer (144 x 16384 x 4096 f16
+// 28.6 -> 32.5 us; P's 28.8).
 Choice plan_tile(const LinearOp& op, int64_t kb, int sms, const LinearTuning& t) {
     Choice best;
     const double memory = memory_ns(op);
+    const double off_lines = whole_lines(op.b, op.N, op.K, op.dtype) ? 1.0 : 1.15;
     for (int bn = 256; bn >= 32; bn -= 32) {
         if (t.bn > 0 && bn != t.bn) continue;
         const int64_t tiles = ceil_div(op.M, 256) * ceil_div(op.N, bn);
-        const double stage = std::max(225.0, (256 + bn) * (bn == 256 ? 1.01 : 1.07) / kClock);
+        const double stage = std::max(225.0, (256 + bn) * (bn == 256 ? 1.01 : 1.07) / kClock) * off_lines;
         const double loop = std::max(double(ceil_div(tiles, sms / 2)) * (double(kb) * stage + 200), memory);
         const double ns = 3500 + bn * 18 + loop;
         if (ns < best.ns) {
@@ -156,12 +164,14 @@ int64_t places(int split, bool half_sm) {
     return (split <= 2 ? 152 : split == 4 ? 144 : 120) * (half_sm ? 2 : 1);
 }
 
-// What reading costs more when a row's stages do not start on 128-byte lines
-// and take two of them (144 rows of f16, split 1: 40.7 us at 16392 x 4104, 27.6
-// at 16384 x 4096).
-double straddle(const LinearOp& op) {
-    auto odd = [&](const Operand& o) { return (o.ld * elem_size(op.dtype)) % 128 != 0; };
-    return odd(op.a) || odd(op.b) ? 1.5 : 1.0;
+// What L2 costs the split kernel more when a row's stages of Q, which many
+// tiles read, do not start on 128-byte lines and take two of them (144 x 16384
+// x 4096 f16, split 1: 27.6 us, 32.9 with Q off the lines, 39.6 with P too, 27.8
+// with P alone).
+double straddle(const LinearOp& op, bool swap) {
+    const bool a = whole_lines(op.a, op.M, op.K, op.dtype), b = whole_lines(op.b, op.N, op.K, op.dtype);
+    if (swap ? a : b) return 1.0;
+    return a || b ? 1.25 : 1.5;
 }
 
 // The split kernel with Q in tiles_q tiles. Blocks take half of an SM's shared
@@ -206,7 +216,7 @@ Choice plan_split(const LinearOp& op, int64_t kb, const LinearTuning& t, int64_t
         best.half_sm = half_sm;
         const double share = double(ceil_div(kb, split)), resident = double(ceil_div(ctas, 148));
         const double busy = resident * share * 2.0 * (bp + p.bn) / kClock;
-        const double l2 = double(ctas) * share * (bp + p.bn) * 128 * straddle(op) / kL2;
+        const double l2 = double(ctas) * share * (bp + p.bn) * 128 * straddle(op, swap) / kL2;
         const double sums = resident * bp * p.bn * 4;  // bytes an SM joins
         const double join = split > 1 ? 1000 + sums * (split - 1) / split / kPeer / kClock : sums / 128;
         best.ns = 4300 + join + std::max(busy, std::max(memory_ns(op), l2));

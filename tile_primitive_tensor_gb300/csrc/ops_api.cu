@@ -133,20 +133,22 @@ tpgemm_status check_act(int act) {
 // Aligned copies of a product's operands in a workspace. An operand whose rows
 // do not start on 16-byte boundaries cannot be read by TMA: it is copied to
 // rows that do, which moves its bytes twice more (37 x 1000 x 1001 f16: 7.7 us
-// with the copies, 6.0 at 40 x 1000 x 1000, which needs none).
+// with the copies, 6.0 at 40 x 1000 x 1000, which needs none). Copies start
+// their rows on 128-byte lines.
 struct Aligned {
     size_t at = 0;      // byte offset in the workspace
     int64_t ld = 0;     // row stride of the copy, elements
     bool copy = false;
 };
 
-Aligned plan_aligned(const tpg::Operand& o, int64_t rows, int64_t K, int dtype, size_t* total) {
+Aligned plan_aligned(const tpg::Operand& o, int64_t rows, int64_t K, int dtype, size_t* total,
+                     bool lines128 = false) {
     Aligned a;
-    a.copy = !tpg::tma_rows(o, rows, K, dtype);
+    a.copy = !tpg::tma_rows(o, rows, K, dtype) || (lines128 && !tpg::whole_lines(o, rows, K, dtype));
     if (!a.copy) return a;
     const int64_t lines = o.mn ? K : rows, len = o.mn ? rows : K;
     const size_t es = size_t(elem_size(dtype));
-    a.ld = int64_t(align_up(size_t(len) * es, 16) / es);
+    a.ld = int64_t(align_up(size_t(len) * es, 128) / es);
     a.at = *total;
     *total = align_up(*total + size_t(lines) * size_t(a.ld) * es, 256);
     return a;
@@ -208,6 +210,16 @@ tpg::LinearOp linear_op(const void* A, const void* W, const tpgemm_linear_desc& 
     return op;
 }
 
+// Whether the tokens' rows are worth a copy to rows that start on 128-byte
+// lines. With few tokens every tile reads all of them, from L2, and a row's
+// stage that takes two lines takes twice as long there; with large weights that
+// is more than the 2 us of a copy (f16, lines of 16 bytes off, without / with:
+// 96 x 16384 x 4096 32.5 / 27.5 us, 144 x 8192 x 8192 39.7 / 29.5; without
+// gain at 96 x 4096 x 4096, 12.2, and 32 x 16384 x 4096, 25.8).
+bool tokens_on_lines(const tpg::LinearOp& op) {
+    return op.M >= 48 && op.M <= 256 && op.N * op.K * elem_size(op.dtype) >= int64_t(64) << 20;
+}
+
 struct LinearLayout {
     size_t total = 0;
     Aligned a, w;
@@ -216,7 +228,7 @@ struct LinearLayout {
 LinearLayout linear_layout(const tpg::LinearOp& op) {
     LinearLayout L;
     if (takes_few(op)) return L;
-    L.a = plan_aligned(op.a, op.M, op.K, op.dtype, &L.total);
+    L.a = plan_aligned(op.a, op.M, op.K, op.dtype, &L.total, tokens_on_lines(op));
     L.w = plan_aligned(op.b, op.N, op.K, op.dtype, &L.total);
     return L;
 }
@@ -233,7 +245,7 @@ GradLayout grad_layout(const void* dY, const void* A, const void* W,
     GradLayout L;
     if (d.M == 0 || d.N == 0) return L;
     if (d.act != TPGEMM_ACT_NONE) {
-        L.lddz = int64_t(align_up(size_t(d.N), 8));
+        L.lddz = int64_t(align_up(size_t(d.N), 64));  // whole 128-byte lines
         L.dz = L.total;
         L.total = align_up(L.total + size_t(d.M) * size_t(L.lddz) * 2, 256);
     } else if (d.K > 0) {

@@ -73,6 +73,8 @@ tpgemm_status run_linear_tc(const LinearOp& op, int sms, cudaStream_t stream);
 constexpr int kFewTokens = 16;
 bool linear_few_takes(const LinearOp& op);
 bool linear_few_wins(const LinearOp& op);
+// Whether every line of the operand starts on a 128-byte boundary.
+bool whole_lines(const Operand& o, int64_t rows, int64_t K, int dtype);
 cudaError_t launch_linear_few(const LinearOp& op, int sms, cudaStream_t stream);
 
 bool tma_rows(const Operand& o, int64_t rows, int64_t K, int dtype);
