@@ -182,35 +182,61 @@ __device__ __forceinline__ void act_n(int act, float (&x)[N]) {
     });
 }
 
-// Up to 8 consecutive columns n.. of output row m, a row to a lane.
+// x[i] of lane j and x[j] of lane i change places.
+template <typename V>
+__device__ __forceinline__ void transpose32(int lane, V (&x)[32]) {
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) {
+        const bool high = (lane & s) != 0;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            if (i & s) continue;
+            const V got = __shfl_xor_sync(0xffffffffu, high ? x[i] : x[i + s], s);
+            if (high) x[i] = got;
+            else x[i + s] = got;
+        }
+    }
+}
+
+// A 32 x 32 chunk, a row m0 + lane to a lane with that row's scale sa, of
+// outputs whose rows start anywhere: turned, so that a warp reads and writes 32
+// neighbouring columns of a row at a time.
 template <typename T>
-__device__ __forceinline__ void epilogue_row8(const Epilogue& e, bool vec, int64_t m, int64_t n,
-                                              int64_t N, float sa, float (&x)[8]) {
-    if (n >= N) return;
-    const int cnt = int(N - n < 8 ? N - n : 8);
-    vec = vec && cnt == 8;
-    float t[8];
-    if (e.sw) {
-        load8<float>(e.sw, n, vec, cnt, t);
+__device__ __forceinline__ void epilogue_turned(const Epilogue& e, int64_t m0, int64_t n0, int64_t M, int64_t N,
+                                                int lane, float sa, float (&x)[32]) {
+    transpose32(lane, x);
+    if (e.sa) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] *= sa * t[i];
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] *= sa;
+        for (int i = 0; i < 32; ++i) x[i] *= __shfl_sync(0xffffffffu, sa, i);
     }
-    if (e.bias) {
-        load8<T>(e.bias, n, vec, cnt, t);
+    const int64_t n = n0 + lane;
+    const int rows = int(min(int64_t(32), M - m0));
+    if (n < N) {
+        const float sw = e.sw ? e.sw[n] : 1.f;
+        const float bias = e.bias ? to_f32(static_cast<const T*>(e.bias)[n]) : 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] += t[i];
-    }
-    if (e.Z) store8<T>(e.Z, m * e.ldz + n, vec, cnt, x);
-    act_n(e.act, x);
-    if (e.R) {
-        load8<T>(e.R, m * e.ldr + n, vec, cnt, t);
+        for (int i = 0; i < 32; ++i) x[i] = fmaf(x[i], sw, bias);
+        if (e.Z) {
+            T* z = static_cast<T*>(e.Z) + m0 * e.ldz + n;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] += t[i];
+            for (int i = 0; i < 32; ++i)
+                if (i < rows) z[i * e.ldz] = from_f32<T>(x[i]);
+        }
+        act_n(e.act, x);
+        if (e.R) {
+            const T* r = static_cast<const T*>(e.R) + m0 * e.ldr + n;
+            float f[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) f[i] = i < rows ? to_f32(r[i * e.ldr]) : 0.f;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[i] += f[i];
+        }
+        T* y = static_cast<T*>(e.Y) + m0 * e.ldy + n;
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (i < rows) y[i * e.ldy] = from_f32<T>(x[i]);
     }
-    store8<T>(e.Y, m * e.ldy + n, vec, cnt, x);
+    __syncwarp();
 }
 
 // 32 columns of an output row, staged for a TMA store: a lane's row of the
@@ -286,7 +312,8 @@ __device__ __forceinline__ void apply_columns(float v, float (&x)[32]) {
 // Outputs whose rows start on 16-byte boundaries leave through a staging tile
 // and TMA stores; the residual comes in the same way, ahead of its use. Stores
 // straight from registers, 16 bytes to each of 32 rows, occupy the load/store
-// path for 32 cycles an instruction; they serve the other outputs.
+// path for 32 cycles an instruction, and those of single elements as long: the
+// other outputs are turned first (TURN_NOTE).
 constexpr int kTileThreads = 384;
 constexpr int kTileEpiWarps = 8;
 constexpr int kStaging = 4096;  // staging bytes of an epilogue warp
@@ -532,16 +559,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(r[i]);
                 }
                 if (!tma) {
-                    if (live) {
-#pragma unroll
-                        for (int g = 0; g < 4; ++g) {
-                            float y[8];
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) y[i] = x[8 * g + i];
-                            epilogue_row8<T>(p.e, false, m, q0 + c + 8 * g, p.Nq, sa, y);
-                        }
-                    }
-                    __syncwarp();
+                    epilogue_turned<T>(p.e, m0, q0 + c, p.Mp, p.Nq, lane, sa, x);
                     continue;
                 }
                 const int64_t n = q0 + c;
@@ -702,21 +720,6 @@ __device__ __forceinline__ void cluster_arrive() {
 }
 __device__ __forceinline__ void cluster_wait() {
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
-// x[i] of lane j and x[j] of lane i change places.
-__device__ __forceinline__ void transpose32(int lane, uint32_t (&x)[32]) {
-#pragma unroll
-    for (int s = 16; s > 0; s >>= 1) {
-        const bool high = (lane & s) != 0;
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            if (i & s) continue;
-            const uint32_t got = __shfl_xor_sync(0xffffffffu, high ? x[i] : x[i + s], s);
-            if (high) x[i] = got;
-            else x[i + s] = got;
-        }
-    }
 }
 
 // Four neighbouring outputs n.. of row m (cnt of them in the matrix; vec: all
