@@ -29,12 +29,12 @@ constexpr int kPrefetch = 2;  // runs of a warp asked for ahead
 constexpr int64_t kManyRows = 2 * 152 * kRows;  // of W: more than two blocks to an SM
 
 // The 16 bytes of row r from element k on (zero past K or for no row).
-template <typename T, bool VEC>
+template <typename T>
 __device__ __forceinline__ uint4 load16(const T* r, bool live, int64_t k, int64_t K) {
     constexpr int E = 16 / sizeof(T);
     uint4 v = make_uint4(0, 0, 0, 0);
     if (!live || k >= K) return v;
-    if (VEC && k + E <= K) {
+    if (k + E <= K) {
         asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                      : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                      : "l"(r + k));
@@ -117,20 +117,40 @@ __global__ void __launch_bounds__(32 * kWarps) linear_few_kernel(const __grid_co
     }
     grid_dependency_wait();
     float acc[TT][4] = {};
+    // Rows that start anywhere are read as the aligned 16 bytes that each lane's
+    // start in; a row's four lanes pass them on.
+    const auto load_run = [&](const T* row, bool live, int64_t k0, uint4 (&out)[kRun]) {
+        if constexpr (VEC) {
+#pragma unroll
+            for (int i = 0; i < kRun; ++i) out[i] = load16<T>(row, live, k0 + (4 * i + t4) * E, op.K);
+        } else {
+            const uint8_t* bytes = reinterpret_cast<const uint8_t*>(row);
+            const int off = int(reinterpret_cast<uintptr_t>(bytes) & 15u);
+            const int64_t len = live ? op.K * int64_t(sizeof(T)) : 0, at = k0 * int64_t(sizeof(T)) + 16 * t4 - off;
+            Window w[kRun + 1];
+#pragma unroll
+            for (int i = 0; i < kRun; ++i) w[i] = load_window(bytes, at + 64 * i, len);
+            w[kRun] = t4 == 0 ? load_window(bytes, at + 64 * kRun, len) : make_uint4(0, 0, 0, 0);
+            const int from = (lane & ~3) | ((t4 + 1) & 3);
+            Window here = shuffle_window(w[0], from);
+#pragma unroll
+            for (int i = 0; i < kRun; ++i) {
+                const Window after = shuffle_window(w[i + 1], from);
+                const uint4 v = join_windows(w[i], t4 == 3 ? after : here, off);
+                // (Bytes past K are zero there already.)
+                out[i] = v;
+                here = after;
+            }
+        }
+    };
     for (int64_t k0 = (int64_t(rank) * kWarps + warp) * step; k0 < op.K; k0 += stride) {
         uint4 lo[kRun], hi[kRun], x[TT][kRun];
-#pragma unroll
-        for (int i = 0; i < kRun; ++i) {
-            const int64_t k = k0 + (4 * i + t4) * E;
-            lo[i] = load16<T, VEC>(lo_row, live_lo, k, op.K);
-            hi[i] = load16<T, VEC>(hi_row, live_hi, k, op.K);
-        }
+        load_run(lo_row, live_lo, k0, lo);
+        load_run(hi_row, live_hi, k0, hi);
 #pragma unroll
         for (int u = 0; u < TT; ++u) {
             const bool live = m0 + 8 * u + g < op.M;
-            const T* row = A + (live ? m0 + 8 * u + g : 0) * op.a.ld;
-#pragma unroll
-            for (int i = 0; i < kRun; ++i) x[u][i] = load16<T, VEC>(row, live, k0 + (4 * i + t4) * E, op.K);
+            load_run(A + (live ? m0 + 8 * u + g : 0) * op.a.ld, live, k0, x[u]);
         }
 #pragma unroll
         for (int i = 0; i < kRun; ++i)

@@ -126,6 +126,7 @@ __global__ void __launch_bounds__(256) align_rows_kernel(const __grid_constant__
     const int64_t u = int64_t(blockIdx.x) * 32 + (threadIdx.x & 31);
     const int64_t bytes = job.bytes;
     if (16 * u >= bytes) return;
+#pragma unroll 4
     for (int64_t r = int64_t(blockIdx.y) * 8 + (threadIdx.x >> 5); r < job.rows; r += int64_t(gridDim.y) * 8) {
         const uint8_t* p = job.src + r * job.pitch + 16 * u;
         uint32_t w[4] = {};
@@ -183,14 +184,17 @@ cudaError_t launch_act_grad(const ActGradOp& op, cudaStream_t stream) {
     return launch_column_sum(op.partial, strips, op.N, op.dbias, op.grad, stream);
 }
 
+constexpr int64_t kAlignBlocks = 8 * 152;  // eight to an SM; a warp then has several rows' loads in flight
+
 cudaError_t launch_align_rows(const AlignJobs& jobs, cudaStream_t stream) {
     if (jobs.n == 0) return cudaSuccess;
     int64_t bx = 1, by = 1;
     for (int i = 0; i < jobs.n; ++i) {
         bx = std::max(bx, (jobs.j[i].bytes + 511) / 512);
-        by = std::max(by, std::min<int64_t>((jobs.j[i].rows + 7) / 8, 4096));
+        by = std::max(by, (jobs.j[i].rows + 7) / 8);
     }
     if (bx > 0x7fffffff) return cudaErrorInvalidValue;
+    by = std::min(by, std::max<int64_t>(1, kAlignBlocks / bx));
     return launch_dependent(align_rows_kernel, dim3(unsigned(bx), unsigned(by), unsigned(jobs.n)), dim3(256),
                             0, stream, jobs);
 }

@@ -137,6 +137,8 @@ double memory_ns(const LinearOp& op) {
 // takes in (128 + bn / 2 rows of 128 bytes; 7 % over that measured), which at
 // bn = 256 is the tensor rate too, and takes 225 ns at the least (512 x 4096 x
 // 4096 bf16: 20.3 us at bn = 128, 24.0 at 256; 4096^3: 74.8 at 224, 78.8 at 256).
+// Short sums are bound by the epilogue, which has a fixed part to a tile (4096 x
+// 4096 x 64 f16: 16.5 us at 256, 19.4 at 128, 28.4 at 64).
 // Q's rows off the 128-byte lines take a seventh longer (144 x 16384 x 4096 f16
 // 28.6 -> 32.5 us; P's 28.8).
 Choice plan_tile(const LinearOp& op, int64_t kb, int sms, const LinearTuning& t) {
@@ -147,7 +149,8 @@ Choice plan_tile(const LinearOp& op, int64_t kb, int sms, const LinearTuning& t)
         if (t.bn > 0 && bn != t.bn) continue;
         const int64_t tiles = ceil_div(op.M, 256) * ceil_div(op.N, bn);
         const double stage = std::max(225.0, (256 + bn) * (bn == 256 ? 1.01 : 1.07) / kClock) * off_lines;
-        const double loop = std::max(double(ceil_div(tiles, sms / 2)) * (double(kb) * stage + 200), memory);
+        const double mmas = double(kb) * stage + 200, epilogue = 1300 + 6.7 * bn;
+        const double loop = std::max(mmas + double(ceil_div(tiles, sms / 2) - 1) * std::max(mmas, epilogue), memory);
         const double ns = 3500 + bn * 18 + loop;
         if (ns < best.ns) {
             best.ns = ns;
@@ -219,7 +222,7 @@ Choice plan_split(const LinearOp& op, int64_t kb, const LinearTuning& t, int64_t
         const double l2 = double(ctas) * share * (bp + p.bn) * 128 * straddle(op, swap) / kL2;
         const double sums = resident * bp * p.bn * 4;  // bytes an SM joins
         const double join = split > 1 ? 1000 + sums * (split - 1) / split / kPeer / kClock : sums / 128;
-        best.ns = 4300 + join + std::max(busy, std::max(memory_ns(op), l2));
+        best.ns = 4300.0 * double(ceil_div(ctas, fit)) + join + std::max(busy, std::max(memory_ns(op), l2));
     }
     return best;
 }

@@ -86,4 +86,38 @@ __device__ __forceinline__ void store8(void* base, int64_t at, bool vec, int n, 
     }
 }
 
+// Sixteen bytes at a row's byte `at`, whose address is a multiple of 16; those
+// outside of the row's `bytes` read as zero and are not touched.
+using Window = uint4;
+
+__device__ __forceinline__ Window load_window(const uint8_t* row, int64_t at, int64_t bytes) {
+    if (at >= 0 && at + 16 <= bytes) return *reinterpret_cast<const uint4*>(row + at);
+    uint32_t w[4] = {};
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        if (at + i >= 0 && at + i < bytes) w[i / 4] |= uint32_t(row[at + i]) << (8 * (i % 4));
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ Window shuffle_window(const Window& w, int lane) {
+    return make_uint4(__shfl_sync(0xffffffffu, w.x, lane), __shfl_sync(0xffffffffu, w.y, lane),
+                      __shfl_sync(0xffffffffu, w.z, lane), __shfl_sync(0xffffffffu, w.w, lane));
+}
+
+// The 16 bytes from byte `off` on of two neighbouring windows.
+__device__ __forceinline__ uint4 join_windows(const Window& a, const Window& b, int off) {
+    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    if (off & 8) {
+#pragma unroll
+        for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+    }
+    if (off & 4) {
+#pragma unroll
+        for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+    }
+    const uint32_t bits = 8u * (uint32_t(off) & 3u);
+    return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
+                      __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
+}
+
 }  // namespace tpg
