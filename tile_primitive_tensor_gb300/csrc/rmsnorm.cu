@@ -494,12 +494,13 @@ struct Spread {
 // rows two groups to a thread, which keeps more bytes on their way (8192 x 4096
 // bf16 with residual: 44 us, 52 with one); for few rows, and for widths that are
 // no multiple of eight, whose loads are narrow, one group, for the shortest time
-// to the end of a row.
+// to the end of a row (4096 x 4100 bf16: 63 us, 62 with two; gradients 95, 133;
+// 333 x 1001: 3.6, 4.8).
 Spread spread_of(int64_t rows, int64_t cols) {
     const int64_t groups = (cols + 7) / 8;
     if (groups <= 64) return {32, groups <= 32 ? 1 : 2, true};
     if (cols > kMaxHeld) return {kMaxTeam, 0, false};
-    const bool one = groups <= kMaxTeam && (rows <= 304 || (cols % 8 != 0 && groups <= 512));
+    const bool one = groups <= kMaxTeam && (rows <= 304 || cols % 8 != 0);
     const int64_t per = one ? groups : (groups + 1) / 2;
     return {int((per + 31) / 32 * 32), one ? 1 : 2, false};
 }
