@@ -584,8 +584,8 @@ size_t tpgemm_linear_backward_workspace_bytes(const void* dY, const void* A, con
  *     e - 127 = floor(log2 max |Y|) - (8 / 15) over each 32 columns, at least
  *     -127: the SFA of tpgemm_gemm_mx (dense Y). Larger values saturate.
  * A row (block) with an infinity or a NaN gets a NaN scale. Sums, H before its
- * rounding, and Y before its rounding are 32-bit (so a block whose largest |Y|
- * is within 2^-22 of a power of two may get the scale of either side).
+ * rounding, and Y before its rounding are 32-bit; the exponent of an MX scale is
+ * that of the unrounded Y, to twice as many bits where it is close.
  */
 typedef enum {
     TPGEMM_SCALE_NONE = 0,

@@ -326,3 +326,23 @@ def test_offsets_past_32_bits():
     a = tp.rmsnorm_backward(x, x, rstd, w)
     b = tp.rmsnorm_backward(x.contiguous(), x.contiguous(), rstd, w)
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("cols", [1, 32, 333, 512, 1001, 2048, 4096, 8192, 16384, 20000])
+@pytest.mark.parametrize("eps", [0.0, 1e-8, 1e-6, 1e-3])
+@pytest.mark.parametrize("rows", [3, 400])
+def test_mx_scale_at_a_power_of_two(cols, eps, rows):
+    # Rows of +-1 under a weight of 2: |y| = 2 / sqrt(1 + eps), which is 2 or less than it by as
+    # little as 5e-9 of it, less than 32-bit arithmetic tells apart. The exponent is exact.
+    g = torch.Generator(device="cuda").manual_seed(cols)
+    x = torch.where(torch.rand(rows, cols, generator=g, device="cuda") < 0.5, -1.0, 1.0).bfloat16()
+    w = torch.full((cols,), 2.0, device="cuda").bfloat16()
+    r = tp.rmsnorm(x, w, eps=eps, quant="mx")
+    code = 127 - 8 + (1 if eps == 0 else 0)
+    assert (r.scale == code).all()
+    top = 256.0 if eps == 0 else 448.0  # 2 / 2^-7; just under 2 / 2^-8, past the largest
+    assert torch.equal(r.y.float(), x.float() * top)
+    half = torch.zeros_like(x)
+    both = tp.rmsnorm(x, w, half, eps=eps, quant="mx", out_h=x)  # h in place of x
+    assert torch.equal(both.y.view(torch.uint8), r.y.view(torch.uint8))
+    assert torch.equal(both.scale, r.scale)

@@ -160,11 +160,45 @@ __device__ __forceinline__ void team_sum_max(float& a, uint32_t& b, float2* s) {
     }
 }
 
+// A block's maximum within a few units of a power of two: its scale hangs on
+// roundings of 32-bit arithmetic (one block in 10^6), so the power is compared
+// with |h rstd gamma| to twice as many bits.
+__device__ __forceinline__ bool near_power(uint32_t amax) {
+    return ((amax + 8u) & 0x7fffffu) < 16u && amax >= 0x10000000u && amax < 0x70000000u;
+}
+
+// 1 / sqrt(sum / cols + eps) as a 32-bit value and what it is short of: one
+// Newton step from the exact residual.
+struct Rstd {
+    float hi, lo;
+};
+__device__ __forceinline__ Rstd rstd_of(float sum, float cols, float eps) {
+    const float q = sum / cols, ql = fmaf(-q, cols, sum) / cols;
+    const float m = q + eps, t = m - q;
+    const float ml = (q - (m - t)) + (eps - t) + ql;
+    const float r = 1.f / sqrtf(m), rr = r * r;
+    return {r, 0.5f * r * (fmaf(-m, rr, 1.f) - fmaf(m, fmaf(r, r, -rr), ml * rr))};
+}
+__device__ __forceinline__ bool reaches(float power, float h, const Rstd& r, float g) {
+    const float p = h * r.hi, pl = fmaf(h, r.hi, -p) + h * r.lo;
+    const float y = p * g, yl = fmaf(p, g, -y) + pl * g;
+    return (fabsf(y) - power) + (y < 0.f ? -yl : yl) >= 0.f;
+}
+
+template <typename XT>
+__device__ __forceinline__ float gamma_of(const RmsNormOp& op, int64_t c) {
+    return op.g == TPGEMM_ELEM_F32 ? static_cast<const float*>(op.gamma)[c]
+                                   : to_f32(static_cast<const XT*>(op.gamma)[c]);
+}
+
 // Stores one group of y (scaled for an 8-bit output) and, for MX, its scales.
-template <bool VEC>
-__device__ __forceinline__ void store_y(const RmsNormOp& op, int64_t row, const Cols<VEC>& c,
-                                        float (&y)[8], float inv) {
-    if (op.mode == TPGEMM_SCALE_MX) {
+// True: the group's block is near a power of two, see settle_block (elements
+// that are not neighbours settle theirs here, before h is stored over X or R).
+template <typename XT, bool VEC, bool MX>
+__device__ __forceinline__ bool store_y(const RmsNormOp& op, int64_t row, const Cols<VEC>& c,
+                                        float (&y)[8], float inv, float sum) {
+    bool near = false;
+    if constexpr (MX) {
         uint8_t* scale = static_cast<uint8_t*>(op.scale) + row * ((op.cols + 31) / 32);
         if constexpr (VEC) {  // four lanes hold 32 neighbouring columns
             uint32_t amax = 0;
@@ -172,6 +206,7 @@ __device__ __forceinline__ void store_y(const RmsNormOp& op, int64_t row, const 
             for (int j = 0; j < 8; ++j) amax = max(amax, abs_bits(y[j]));
             amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
             amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+            near = near_power(amax);  // (the same in all four)
             const uint32_t code = mx_scale(amax, op.y, inv);
             if ((threadIdx.x & 3) == 0 && c.n > 0) scale[c.first / 32] = uint8_t(code);
 #pragma unroll
@@ -179,8 +214,20 @@ __device__ __forceinline__ void store_y(const RmsNormOp& op, int64_t row, const 
         } else {  // the warp holds 32 neighbouring columns of each j
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const uint32_t code =
-                    mx_scale(__reduce_max_sync(0xffffffffu, abs_bits(y[j])), op.y, inv);
+                uint32_t amax = __reduce_max_sync(0xffffffffu, abs_bits(y[j]));
+                if (near_power(amax)) {
+                    const uint32_t power = (amax + 8u) & 0x7f800000u;
+                    bool any = false;
+                    if (j < c.n) {  // (h and gamma are read again, to hold no registers)
+                        const int64_t at = c.first + int64_t(j) * c.step;
+                        float h = to_f32(static_cast<const XT*>(op.X)[row * op.ldx + at]);
+                        if (op.R) h += to_f32(static_cast<const XT*>(op.R)[row * op.ldr + at]);
+                        any = reaches(__uint_as_float(power), h, rstd_of(sum, float(op.cols), op.eps),
+                                      gamma_of<XT>(op, at));
+                    }
+                    amax = __any_sync(0xffffffffu, any) ? power : power - 1u;
+                }
+                const uint32_t code = mx_scale(amax, op.y, inv);
                 if ((threadIdx.x & 31) == 0 && j < c.n)
                     scale[(c.first + int64_t(j) * c.step) / 32] = uint8_t(code);
                 y[j] *= inv;
@@ -198,6 +245,38 @@ __device__ __forceinline__ void store_y(const RmsNormOp& op, int64_t row, const 
         case TPGEMM_ELEM_E5M2: store_cols<e5m2, VEC>(op.Y, at, c, y); break;
         default: store_cols<float, VEC>(op.Y, at, c, y); break;
     }
+    return near;
+}
+
+// Writes a block near a power of two again, by four lanes: the power in doubt is
+// compared exactly. It comes after the row's stores, when registers are free
+// (8192 x 8192 bf16: 87 us without it, 90 so, 110 in their midst).
+template <typename XT>
+__device__ __forceinline__ void settle_block(const RmsNormOp& op, int64_t row, const Cols<true>& c,
+                                             const float (&h)[8], float sum) {
+    const unsigned four = 0xfu << (threadIdx.x & 28);
+    const Rstd rstd = rstd_of(sum, float(op.cols), op.eps);
+    uint32_t amax = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        if (c.n == 8) amax = max(amax, abs_bits(h[j] * rstd.hi * gamma_of<XT>(op, c.first + j)));
+    amax = max(amax, __shfl_xor_sync(four, amax, 1));
+    amax = max(amax, __shfl_xor_sync(four, amax, 2));
+    const uint32_t power = (amax + 8u) & 0x7f800000u;
+    bool any = false;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        if (c.n == 8) any = any || reaches(__uint_as_float(power), h[j], rstd, gamma_of<XT>(op, c.first + j));
+    any = __any_sync(four, any);
+    float inv;
+    const uint32_t code = mx_scale(any ? power : power - 1u, op.y, inv);
+    if (c.n != 8) return;
+    if ((threadIdx.x & 3) == 0) static_cast<uint8_t*>(op.scale)[row * ((op.cols + 31) / 32) + c.first / 32] = uint8_t(code);
+    float y[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) y[j] = h[j] * rstd.hi * gamma_of<XT>(op, c.first + j) * inv;
+    if (op.y == TPGEMM_ELEM_E4M3) store_cols<e4m3, true>(op.Y, row * op.ldy, c, y);
+    else store_cols<e5m2, true>(op.Y, row * op.ldy, c, y);
 }
 
 // h of one group: x + r.
@@ -214,7 +293,7 @@ __device__ __forceinline__ void load_h(const RmsNormOp& op, int64_t row, const C
 }
 
 // What follows a row's loads: reduction, scale, and the stores of h and y.
-template <typename XT, int V, bool VEC, bool WARP>
+template <typename XT, int V, bool VEC, bool WARP, bool MX>
 __device__ __forceinline__ void finish_row(const RmsNormOp& op, int64_t row, int t, int team,
                                            const float (&h)[V][8], float2* s) {
     const bool row_mode = op.mode == TPGEMM_SCALE_ROW;
@@ -239,14 +318,22 @@ __device__ __forceinline__ void finish_row(const RmsNormOp& op, int64_t row, int
         if (t == 0) static_cast<float*>(op.scale)[row] = scale;
         inv = 1.f / scale;
     }
+    uint32_t near = 0;  // groups whose block is near a power of two
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const Cols<VEC> c(i, t, team, op.cols);
-        if (op.H) store_cols<XT, VEC>(op.H, row * op.ldh, c, h[i]);
         float y[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) y[j] = h[i][j] * rstd * g[i][j];
-        store_y<VEC>(op, row, c, y, inv);
+        if (store_y<XT, VEC, MX>(op, row, c, y, inv, ss)) near |= 1u << i;
+        if (op.H) store_cols<XT, VEC>(op.H, row * op.ldh, c, h[i]);
+    }
+    if constexpr (MX && VEC) {
+        if (near) {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if ((near >> i) & 1u) settle_block<XT>(op, row, Cols<VEC>(i, t, team, op.cols), h[i], ss);
+        }
     }
 }
 
@@ -254,7 +341,7 @@ __device__ __forceinline__ void finish_row(const RmsNormOp& op, int64_t row, int
 // a warp, else to a block. AHEAD: blocks stay and walk the rows grid-stride, and
 // load the next row before the reduction of this one, which waits for all of
 // it; else a team ends with its row and the blocks beside it keep memory busy.
-template <typename XT, int V, bool VEC, bool WARP, bool AHEAD = false>
+template <typename XT, int V, bool VEC, bool WARP, bool MX, bool AHEAD = false>
 __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : kMaxTeam) rmsnorm_kernel(const __grid_constant__ RmsNormOp op) {
     __shared__ float2 s[2][32];
     const int team = WARP ? 32 : int(blockDim.x);
@@ -267,7 +354,7 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : kMaxTeam) rmsnorm_kern
     if constexpr (!AHEAD) {
 #pragma unroll
         for (int i = 0; i < V; ++i) load_h<XT, VEC>(op, row, Cols<VEC>(i, t, team, op.cols), h[i]);
-        finish_row<XT, V, VEC, WARP>(op, row, t, team, h, s[0]);
+        finish_row<XT, V, VEC, WARP, MX>(op, row, t, team, h, s[0]);
     } else {
         Ahead<XT, VEC> x[V], r[V];
         auto fetch = [&](int64_t at) {
@@ -291,13 +378,13 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : kMaxTeam) rmsnorm_kern
                 }
             }
             if (row + gridDim.x < op.rows) fetch(row + gridDim.x);
-            finish_row<XT, V, VEC, WARP>(op, row, t, team, h, s[turn]);
+            finish_row<XT, V, VEC, WARP, MX>(op, row, t, team, h, s[turn]);
         }
     }
 }
 
 // Rows of any width, a block to a row, read twice.
-template <typename XT, bool VEC>
+template <typename XT, bool VEC, bool MX>
 __global__ void __launch_bounds__(kMaxTeam) rmsnorm_wide_kernel(const __grid_constant__ RmsNormOp op) {
     __shared__ float2 s[32];
     const int team = int(blockDim.x), t = int(threadIdx.x);
@@ -332,11 +419,14 @@ __global__ void __launch_bounds__(kMaxTeam) rmsnorm_wide_kernel(const __grid_con
         const Cols<VEC> c(i, t, team, op.cols);
         load_h<XT, VEC>(op, row, c, h);
         load_gamma<XT, VEC>(op.gamma, op.g, c, g);
-        if (op.H) store_cols<XT, VEC>(op.H, row * op.ldh, c, h);
         float y[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) y[j] = h[j] * rstd * g[j];
-        store_y<VEC>(op, row, c, y, inv);
+        const bool near = store_y<XT, VEC, MX>(op, row, c, y, inv, ss);
+        if constexpr (MX && VEC) {
+            if (near) settle_block<XT>(op, row, c, h, ss);
+        }
+        if (op.H) store_cols<XT, VEC>(op.H, row * op.ldh, c, h);
     }
 }
 
@@ -510,27 +600,27 @@ bool rows_aligned(const void* p, int64_t ld, int64_t rows, int elem, int bytes) 
                   (rows <= 1 || (ld * elem_size(elem)) % bytes == 0));
 }
 
-template <typename XT, bool VEC>
+template <typename XT, bool VEC, bool MX>
 cudaError_t launch_norm(const RmsNormOp& op, cudaStream_t stream) {
     const Spread s = spread_of(op.rows, op.cols);
     if (s.v == 0) {
         if (op.rows > 0x7fffffff) return cudaErrorInvalidValue;
-        return launch_dependent(rmsnorm_wide_kernel<XT, VEC>, dim3(unsigned(op.rows)),
+        return launch_dependent(rmsnorm_wide_kernel<XT, VEC, MX>, dim3(unsigned(op.rows)),
                                 dim3(unsigned(s.threads())), 0, stream, op);
     }
     int64_t blocks = (op.rows + s.rows() - 1) / s.rows();
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-    auto fn = s.warp ? (s.v == 1 ? rmsnorm_kernel<XT, 1, VEC, true> : rmsnorm_kernel<XT, 2, VEC, true>)
-              : s.v == 1 ? rmsnorm_kernel<XT, 1, VEC, false>
-                         : rmsnorm_kernel<XT, 2, VEC, false>;
+    auto fn = s.warp ? (s.v == 1 ? rmsnorm_kernel<XT, 1, VEC, true, MX> : rmsnorm_kernel<XT, 2, VEC, true, MX>)
+              : s.v == 1 ? rmsnorm_kernel<XT, 1, VEC, false, MX>
+                         : rmsnorm_kernel<XT, 2, VEC, false, MX>;
     if constexpr (VEC) {
         // Teams of 512 threads and more leave an SM two rows or one, too few to
         // hide each other's reductions: such rows are loaded ahead (bf16 with
-        // residual, MX scales: 8192 x 8192 92.6 -> 86.5 us; no scales: 2048 x
+        // residual, MX scales: 8192 x 8192 92 -> 87 us; no scales: 2048 x
         // 16384 55.3 -> 46.2 us). Not with row scales, whose maxima take the
         // registers (89.1 -> 91.6), nor narrower rows (8192 x 4096 44.0 -> 46.4).
         if (s.v == 2 && s.team >= 512 && op.mode != TPGEMM_SCALE_ROW) {
-            fn = rmsnorm_kernel<XT, 2, VEC, false, true>;
+            fn = rmsnorm_kernel<XT, 2, VEC, false, MX, true>;
             blocks = std::min(blocks, int64_t(152) * (kMaxTeam / s.team));
         }
     }
@@ -544,7 +634,9 @@ cudaError_t launch_norm_typed(const RmsNormOp& op, cudaStream_t stream) {
                      rows_aligned(op.H, op.ldh, op.rows, op.x, 16) &&
                      rows_aligned(op.Y, op.ldy, op.rows, op.y, elem_size(op.y) == 1 ? 8 : 16) &&
                      rows_aligned(op.gamma, 0, 1, op.g, 16);
-    return vec ? launch_norm<XT, true>(op, stream) : launch_norm<XT, false>(op, stream);
+    if (op.mode == TPGEMM_SCALE_MX)
+        return vec ? launch_norm<XT, true, true>(op, stream) : launch_norm<XT, false, true>(op, stream);
+    return vec ? launch_norm<XT, true, false>(op, stream) : launch_norm<XT, false, false>(op, stream);
 }
 
 // Blocks of the register kernel: 512 threads to an SM, which is what its
