@@ -12,7 +12,9 @@
 //
 // A block takes 16 rows of W, its 8 warps alternate runs of K; with few rows a
 // cluster of blocks shares them. Partial sums meet in shared memory and are
-// added in a fixed order. Bound by memory: the weights' bytes.
+// added in a fixed order. Bound by memory: the weights' bytes, and for few of
+// them by its latency (one token of 4096 x 4096 bf16: 8.5 us, of which 4.9 are
+// the bytes; unaligned rows, 12 x 4096 x 4097: 33 us, 42 element by element).
 #include <algorithm>
 
 #include "launch.cuh"
@@ -136,9 +138,7 @@ __global__ void __launch_bounds__(32 * kWarps) linear_few_kernel(const __grid_co
 #pragma unroll
             for (int i = 0; i < kRun; ++i) {
                 const Window after = shuffle_window(w[i + 1], from);
-                const uint4 v = join_windows(w[i], t4 == 3 ? after : here, off);
-                // (Bytes past K are zero there already.)
-                out[i] = v;
+                out[i] = join_windows(w[i], t4 == 3 ? after : here, off);  // (zero past K)
                 here = after;
             }
         }

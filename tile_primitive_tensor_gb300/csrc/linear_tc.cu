@@ -12,7 +12,12 @@
 //          repeat, and no global scratch or flag is needed.
 //
 // Operands are read where they lie, K-contiguous or along their rows, by TMA
-// into 128-byte-swizzled stages (K's and the rows' ends read as zero). Every
+// into 128-byte-swizzled stages (K's and the rows' ends read as zero). The tensor
+// cores add into their 32-bit accumulators with truncation: against 64 bits a
+// sum of random signs is off by 5e-7 of its size at K = 512, 2e-6 at 4096 and
+// 9e-6 at 16384 (shares of a split K are added with rounding and are each that
+// much shorter). 16-bit outputs do not see it; taking the sums out of tensor
+// memory every 1024 of K, for 32-bit ones, would halve the tile's width. Every
 // wait is bounded: on expiry the kernel records a status, lets its copies and
 // MMAs in flight finish, frees tensor memory and returns.
 #include <algorithm>
