@@ -436,3 +436,34 @@ def test_scratch_belongs_to_the_stream_it_is_used_on():
             assert torch.equal(a, b)
         torch.cuda.synchronize()
         del junk
+
+
+def ones(g, *shape, dtype):
+    """Values of -1, 0 and 1: sums of up to 256 of their products are exact in every output type."""
+    return torch.randint(-1, 2, shape, generator=g, device="cuda").to(dtype)
+
+
+@pytest.mark.parametrize("bn", [None] + list(range(32, 257, 32)))
+def test_short_sums_of_many_tiles_are_exact(bn, tune):
+    # Many tiles to a pair of CTAs, short sums and nothing but the output to store: each tile's
+    # stores follow the last one's at once, with odd numbers of chunks to a warp at most widths.
+    tune.setenv("TPGEMM_LINEAR_PATH", "tile")
+    if bn:
+        tune.setenv("TPGEMM_LINEAR_BN", str(bn))
+    g = gen(bn or 0)
+    for M, N, K in [(4096, 4096, 64), (2100, 8200, 128), (4100, 2072, 72)]:
+        for dtype, out in [(F16, F16), (BF16, BF16), (E4M3, BF16), (BF16, F32)]:
+            A, W = ones(g, M, K, dtype=dtype), ones(g, N, K, dtype=dtype)
+            want = (A.float() @ W.float().t()).to(out)
+            for _ in range(3):
+                assert torch.equal(tp.linear(A, W, out_dtype=out), want)
+    # the gradients' products, along the operands' rows
+    dY, A, W = (ones(g, *s, dtype=F16) for s in ((64, 4096), (64, 4104), (4096, 4104)))
+    want = (dY.float().t() @ A.float()).half()
+    for _ in range(3):
+        assert torch.equal(tp.linear_backward(dY, A, W, need=(False, True, False))[1], want)
+    dY, W = ones(g, 4104, 72, dtype=BF16), ones(g, 72, 4096, dtype=BF16)
+    want = (dY.float() @ W.float()).bfloat16()
+    A = torch.zeros(4104, 4096, dtype=BF16, device="cuda")
+    for _ in range(3):
+        assert torch.equal(tp.linear_backward(dY, A, W, need=(True, False, False))[0], want)

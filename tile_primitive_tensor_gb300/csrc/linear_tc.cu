@@ -503,6 +503,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const bool staged_r = tma && p.e.R && !p.e.Z;         // (with Z the buffers are taken)
         const uint64_t pol = l2_policy(1);                    // outputs pass through once
         int it = 0;
+        // The buffer of the next chunk. Without Z and R it alternates on from one
+        // tile to the next: each use waits for all stores but the latest, which
+        // an odd number of chunks would otherwise leave in the first buffer.
+        int j = 0;
         for (int t = cid; t < p.tiles; t += ncl, ++it) {
             int tp, tq;
             tile_at(t, p, tp, tq);
@@ -517,11 +521,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 tma_load_2d_hint(staging + buf * kBuf, &mapR, &rbar[buf], int(q0) + c, int(m0), pol);
             };
             if (staged_r) {
+                j = 0;
                 if (lane == 0) bulk_wait_group_read<0>();
-                for (int j = 0; j < kBufs; ++j)
-                    if (32 * half + 64 * j < limit) {
-                        if (lane == 0) fetch_r(32 * half + 64 * j, j);
-                        rpend |= 1u << j;
+                for (int i = 0; i < kBufs; ++i)
+                    if (32 * half + 64 * i < limit) {
+                        if (lane == 0) fetch_r(32 * half + 64 * i, i);
+                        rpend |= 1u << i;
                     }
                 __syncwarp();
             }
@@ -557,7 +562,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             if (!ok) break;
             tc_fence_after_sync();
             const uint32_t acc = tmem + lanes + uint32_t(b * 256);
-            int j = 0;
             for (int c = 32 * half; c < limit; c += 64, j ^= kBufs - 1) {
                 float x[32];
                 {
@@ -662,8 +666,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
         if (lane == 0) bulk_wait_group_read<0>();
         if (*s.abort)
-            for (int j = 0; j < 2; ++j)
-                if (rpend & (1u << j)) wait_bounded(&rbar[j], (rphase >> j) & 1u, s.abort, tmo, true);
+            for (int i = 0; i < 2; ++i)
+                if (rpend & (1u << i)) wait_bounded(&rbar[i], (rphase >> i) & 1u, s.abort, tmo, true);
     }
     tc_fence_before_sync();
     __syncthreads();
