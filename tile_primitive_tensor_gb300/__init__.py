@@ -11,6 +11,7 @@ Build it with ``tile_primitive_tensor_gb300.build.build()``.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import re
@@ -654,18 +655,34 @@ def _sizes(name, t):
     return shape[0], shape[1], index, t.device
 
 
-def _call(torch, index, stream, function, args, workspace=None, need=None) -> None:
-    """function(*args, stream) with device `index` current; raises if it is refused. A function
-    that takes a workspace before the stream has ``need``, the bytes it asks for: the caller's
-    workspace or, for the length of the call, torch's allocator's on the very stream.
+def _current(stream, t):
+    """A context in which `stream` (a torch.cuda.Stream or an integer cudaStream_t of the CUDA
+    tensor t's device) is torch's current stream. A call on a given stream runs in it whole, so
+    that its outputs too come from that stream's memory: taken from the stream current before,
+    they could be blocks that work there still reads, or go back to it while this stream writes."""
+    torch = _torch or _import_torch()
+    if isinstance(stream, torch.cuda.Stream):
+        return torch.cuda.stream(stream)
+    if t.get_device() < 0:
+        return contextlib.nullcontext()  # (refused by the call)
+    handle = _stream(stream)
+    # (1 is CUDA's other name of the default stream.)
+    return torch.cuda.stream(torch.cuda.ExternalStream(0 if handle == 1 else handle, device=t.device))
 
-    The stream is by default the device's current one, read as its raw handle, and the allocator
-    is called directly: a stream object costs 2.9 us of a call that takes 9, a tensor 7."""
+
+def _call(torch, index, function, args, workspace=None, need=None) -> None:
+    """function(*args, stream) with device `index` and its current stream; raises if it is
+    refused. A function that takes a workspace before the stream has ``need``, the bytes it asks
+    for: the caller's workspace or, for the length of the call, torch's allocator's on the very
+    stream.
+
+    The stream is read as its raw handle, and the allocator is called directly: a stream object
+    costs 2.9 us of a call that takes 9, a tensor 7."""
     c = torch._C
     if index != c._cuda_getDevice():
         with torch.cuda.device(index):
-            return _call(torch, index, stream, function, args, workspace, need)
-    handle = c._cuda_getCurrentRawStream(index) if stream is None else _stream(stream)
+            return _call(torch, index, function, args, workspace, need)
+    handle = c._cuda_getCurrentRawStream(index)
     if need is None:
         status = function(*args, handle)
     elif workspace is not None:
@@ -694,7 +711,12 @@ def linear(A, W, bias=None, residual=None, *, act="none", scale_a=None, scale_w=
     out_dtype (float16, bfloat16 or float32; by default A's 16-bit type, or bfloat16). The float32
     scales, per row of A and of W, are for the 8-bit types. act: none, relu, silu, gelu or
     gelu_tanh. Matrices may be row-strided; ``out`` may be the residual itself. The workspace, if
-    one is needed (tpgemm_linear_workspace_bytes), is allocated here with torch unless given."""
+    one is needed (tpgemm_linear_workspace_bytes), is allocated here with torch unless given.
+    stream (by default the current one) is current for the call: its memory holds the outputs."""
+    if stream is not None:
+        with _current(stream, A):
+            return linear(A, W, bias, residual, act=act, scale_a=scale_a, scale_w=scale_w,
+                          out_dtype=out_dtype, out=out, pre=pre, workspace=workspace)
     torch = _torch or _import_torch()
     lib = _lib or _load()
     M, K, index, device = _sizes("A", A)
@@ -728,7 +750,7 @@ def linear(A, W, bias=None, residual=None, *, act="none", scale_a=None, scale_w=
     # (Operands whose rows start on 128-byte lines need no workspace.)
     if (pa | pw | (lda | ldw) * dt.itemsize) & 127:
         need = lib.tpgemm_linear_workspace_bytes(pa, pw, desc)
-    _call(torch, index, stream, lib.tpgemm_linear,
+    _call(torch, index, lib.tpgemm_linear,
           (out.data_ptr(), pz, pa, pw, psa, psw, pb, pr, desc), workspace, need)
     return out
 
@@ -740,7 +762,11 @@ def linear_backward(dY, A, W, pre=None, *, act="none", grad_dtype=None, need=(Tr
 
     dY, A, W, pre and dA are all float16 or all bfloat16; dW and dbias are of grad_dtype (float32,
     float16 or bfloat16; by default A's type). ``need`` says which of the three are wanted; the
-    others are None."""
+    others are None. stream: as for linear."""
+    if stream is not None:
+        with _current(stream, A):
+            return linear_backward(dY, A, W, pre, act=act, grad_dtype=grad_dtype, need=need,
+                                   workspace=workspace)
     torch = _torch or _import_torch()
     lib = _lib or _load()
     M, K, index, device = _sizes("A", A)
@@ -767,7 +793,7 @@ def linear_backward(dY, A, W, pre=None, *, act="none", grad_dtype=None, need=(Tr
         dbias = torch.empty(N, dtype=grad_dtype, device=device)
         pdb = dbias.data_ptr()
     py, pa, pw = dY.data_ptr(), A.data_ptr(), W.data_ptr()
-    _call(torch, index, stream, lib.tpgemm_linear_backward, (pda, pdw, pdb, py, pa, pw, pz, desc),
+    _call(torch, index, lib.tpgemm_linear_backward, (pda, pdw, pdb, py, pa, pw, pz, desc),
           workspace, lib.tpgemm_linear_backward_workspace_bytes(py, pa, pw, desc))
     return dA, dW, dbias
 
@@ -788,7 +814,11 @@ def rmsnorm(x, weight, residual=None, *, eps=1e-6, quant=None, out_dtype=None, n
     or float32. y is of out_dtype: a float type (by default x's), or with quant="row" (one float32
     scale per row, linear's scale_a) or quant="mx" (one E8M0 scale per 32 columns, gemm_mx's SFA)
     float8_e4m3fn (the default) or float8_e5m2, holding y / scale. h is returned with a residual
-    only; it may be written in place (out_h = x or residual)."""
+    only; it may be written in place (out_h = x or residual). stream: as for linear."""
+    if stream is not None:
+        with _current(stream, x):
+            return rmsnorm(x, weight, residual, eps=eps, quant=quant, out_dtype=out_dtype,
+                           need_rstd=need_rstd, out=out, out_h=out_h)
     torch = _torch or _import_torch()
     lib = _lib or _load()
     rows, cols, index, device = _sizes("x", x)
@@ -828,7 +858,7 @@ def rmsnorm(x, weight, residual=None, *, eps=1e-6, quant=None, out_dtype=None, n
         rstd = torch.empty(rows, dtype=torch.float32, device=device)
         prstd = rstd.data_ptr()
     desc = RmsNormDesc(rows, cols, ldx, ldr, ldh, ldy, *codes, eps)
-    _call(torch, index, stream, lib.tpgemm_rmsnorm,
+    _call(torch, index, lib.tpgemm_rmsnorm,
           (out.data_ptr(), ph, ps, prstd, x.data_ptr(), pr, pg, ctypes.byref(desc)))
     return RmsNorm(out, h, scale, rstd)
 
@@ -839,7 +869,12 @@ def rmsnorm_backward(dy, h, rstd, weight, dh=None, *, grad_dtype=None, need=(Tru
     gradient dh that reaches h past the norm (or None). dx is the gradient of x and of residual.
 
     dy, h, dh and dx [rows, cols] are of one type (float16, bfloat16 or float32), dweight of
-    grad_dtype (by default weight's). ``need`` says which are wanted; ``out`` may be dy, h or dh."""
+    grad_dtype (by default weight's). ``need`` says which are wanted; ``out`` may be dy, h or dh.
+    stream: as for linear."""
+    if stream is not None:
+        with _current(stream, dy):
+            return rmsnorm_backward(dy, h, rstd, weight, dh, grad_dtype=grad_dtype, need=need,
+                                    out=out, workspace=workspace)
     torch = _torch or _import_torch()
     lib = _lib or _load()
     rows, cols, index, device = _sizes("dy", dy)
@@ -866,7 +901,7 @@ def rmsnorm_backward(dy, h, rstd, weight, dh=None, *, grad_dtype=None, need=(Tru
         dweight = torch.empty(cols, dtype=grad_dtype, device=device)
         pdw = dweight.data_ptr()
         scratch = lib.tpgemm_rmsnorm_backward_workspace_bytes(rows, cols)
-    _call(torch, index, stream, lib.tpgemm_rmsnorm_backward,
+    _call(torch, index, lib.tpgemm_rmsnorm_backward,
           (pdx, pdw, dy.data_ptr(), h.data_ptr(), prstd, pg, pdh, ctypes.byref(desc)), workspace,
           scratch)
     return dx, dweight
