@@ -22,17 +22,21 @@ def _setup():
 
 
 def calls():
-    """Name, and a call whose largest outputs are [N, N] of 16 bits."""
+    """Name, and a call whose largest outputs are [N, N] of 16 bits (32 of the multiplies)."""
     g = torch.Generator(device="cuda").manual_seed(1)
     a, b = (torch.randn(N, N, generator=g, device="cuda").half() for _ in range(2))
     w, rstd = torch.ones(N, device="cuda").half(), torch.ones(N, device="cuda")
-    return {"linear": lambda s: tp.linear(a, b, stream=s),
+    a8, b8 = a.to(torch.float8_e4m3fn), b.to(torch.float8_e4m3fn)
+    sf = torch.full((N, N // 32), 127, dtype=torch.uint8, device="cuda")
+    return {"gemm": lambda s: tp.gemm(a, b, stream=s),
+            "gemm_mx": lambda s: tp.gemm_mx(a8, b8, sf, sf, stream=s),
+            "linear": lambda s: tp.linear(a, b, stream=s),
             "linear_backward": lambda s: tp.linear_backward(a, a, b, stream=s)[1],
             "rmsnorm": lambda s: tp.rmsnorm(a, w, b, need_rstd=True, stream=s).h,
             "rmsnorm_backward": lambda s: tp.rmsnorm_backward(a, b, rstd, w, stream=s)[0]}
 
 
-NAMES = ["linear", "linear_backward", "rmsnorm", "rmsnorm_backward"]
+NAMES = ["gemm", "gemm_mx", "linear", "linear_backward", "rmsnorm", "rmsnorm_backward"]
 
 
 @pytest.mark.parametrize("kind", ["stream", "handle"])
@@ -44,7 +48,7 @@ def test_outputs_are_not_taken_from_the_current_stream(name, kind):
     want = call(None).clone()
     call(given)  # modules loaded, memory of both streams at hand
     torch.cuda.synchronize()
-    blocks = [torch.full((N, N), float(i), dtype=torch.float16, device="cuda") for i in range(8)]
+    blocks = [torch.full((N, N), float(i), dtype=want.dtype, device="cuda") for i in range(8)]
     copies = [torch.empty_like(b) for b in blocks]
     torch.cuda.synchronize()
     torch.cuda._sleep(LONG)
@@ -62,13 +66,13 @@ def test_outputs_are_not_taken_from_the_current_stream(name, kind):
 def test_dropped_outputs_do_not_come_back_to_the_current_stream(name):
     call = calls()[name]
     s = torch.cuda.Stream()
-    call(s)
+    dtype = call(s).dtype
     torch.cuda.synchronize()
     with torch.cuda.stream(s):
         torch.cuda._sleep(LONG)
     for _ in range(4):
         call(s)  # its result is dropped before it has run
-    mine = [torch.full((N, N), float(i), dtype=torch.float16, device="cuda") for i in range(16)]
+    mine = [torch.full((N, N), float(i), dtype=dtype, device="cuda") for i in range(16)]
     torch.cuda.synchronize()
     for i, m in enumerate(mine):
         assert (m == i).all()

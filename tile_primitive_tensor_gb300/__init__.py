@@ -484,7 +484,12 @@ def gemm_mx(A, B, SFA, SFB, C=None, *, beta=None, out=None, workspace=None, stre
     A is fp8 [M, K], B fp8 [N, K] (same dtype), or both fp4 as uint8 [M, K/2]
     and [N, K/2] (two codes per byte) with dtype=TPGEMM_E2M1; SFA uint8
     [M, ceil(K/32)] and SFB uint8 [N, ceil(K/32)] E8M0 scales, C float32 [M, N].
-    The scale-packing workspace is allocated here with torch unless given."""
+    The scale-packing workspace is allocated here with torch unless given.
+    stream (by default the current one) is current for the call: its memory
+    holds the output and the workspace."""
+    if stream is not None:
+        with _current(stream, A):
+            return gemm_mx(A, B, SFA, SFB, C, beta=beta, out=out, workspace=workspace, dtype=dtype)
     import torch
     if beta is None:
         beta = 0.0 if C is None else 1.0
@@ -501,7 +506,7 @@ def gemm_mx(A, B, SFA, SFB, C=None, *, beta=None, out=None, workspace=None, stre
     if workspace is None:
         workspace = torch.empty(wsb, dtype=torch.uint8, device=A.device)
     check(tpgemm_gemm_mx(out, A, B, C, SFA, SFB, M, N, K, code, beta, workspace,
-                         workspace.numel() * workspace.element_size(), stream))
+                         workspace.numel() * workspace.element_size()))
     return out
 
 
@@ -511,8 +516,12 @@ def gemm(A, B, C=None, *, beta=None, transA=False, transB=False, out=None, strea
 
     A is [M, K] (or [K, M] with transA), B is [K, N] (or [N, K] with transB),
     C is float32 [M, N]. beta defaults to 1 when C is given, else 0. ``out``
-    may be C itself for the in-place form D += A.B.
+    may be C itself for the in-place form D += A.B. stream (by default the
+    current one) is current for the call: its memory holds the output.
     """
+    if stream is not None:
+        with _current(stream, A):
+            return gemm(A, B, C, beta=beta, transA=transA, transB=transB, out=out, path=path)
     import torch
     if beta is None:
         beta = 0.0 if C is None else 1.0
@@ -530,7 +539,7 @@ def gemm(A, B, C=None, *, beta=None, transA=False, transB=False, out=None, strea
     if out is None:
         out = torch.empty((M, N), dtype=torch.float32, device=A.device)
     check(tpgemm_gemm_path(out, A, B, C if beta else C, M, N, K, transA, transB,
-                           dtype_code(A.dtype), beta, stream, path))
+                           dtype_code(A.dtype), beta, None, path))
     return out
 
 
