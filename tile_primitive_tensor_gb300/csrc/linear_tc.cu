@@ -178,12 +178,13 @@ __device__ __forceinline__ uint64_t operand_desc(int mn) {
 __device__ __forceinline__ uint64_t operand_step(int mn) { return mn ? 128u : 2u; }
 
 // ---------------------------------------------------------------- epilogues
-template <int N>
+// The activation of N values on their way to outputs of type T.
+template <typename T, int N>
 __device__ __forceinline__ void act_n(int act, float (&x)[N]) {
     with_act(act, [&](auto a) {
 #pragma unroll
         for (int i = 0; i < N; i += 2)
-            split(act_fwd<decltype(a)::value>(f2(x[i], x[i + 1])), x[i], x[i + 1]);
+            split(act_fwd<decltype(a)::value, sizeof(T) == 4>(f2(x[i], x[i + 1])), x[i], x[i + 1]);
     });
 }
 
@@ -234,7 +235,7 @@ __device__ __forceinline__ void epilogue_turned(const Epilogue& e, int64_t m0, i
             for (int i = 0; i < 32; ++i)
                 if (i < rows) z[i * e.ldz] = from_f32<T>(x[i]);
         }
-        act_n(e.act, x);
+        act_n<T>(e.act, x);
         if (e.R) {
 #pragma unroll
             for (int i = 0; i < 32; ++i)
@@ -617,7 +618,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     }
                     buf = staging + (kBufs - 1) * kBuf;
                 }
-                act_n(p.e.act, x);
+                act_n<T>(p.e.act, x);
                 if (staged_r) {
                     bool rok = wait_bounded(&rbar[j], (rphase >> j) & 1u, s.abort, tmo);
                     ok = __all_sync(0xffffffffu, rok);
@@ -869,7 +870,7 @@ __device__ __forceinline__ void join_lines(const TcLinear& p, const float* part,
 #pragma unroll
                 for (int i = 0; i < 4; ++i) x[j][i] = fmaf(x[j][i], sa * sw[i], bias[i]);
                 if (e.Z) store4<T>(e.Z, m * e.ldz + n, vec, cnt, x[j]);
-                act_n(e.act, x[j]);
+                act_n<T>(e.act, x[j]);
                 if (e.R) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) x[j][i] += res[j][i];
