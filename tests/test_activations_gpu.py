@@ -109,3 +109,23 @@ def test_small_derivatives(act):
     floor = (1 + d.abs() * (1 + 6 * d * d * (act == "gelu_tanh"))) * 2.0 ** -126
     ok, why = ref.within(got, terms[0] + terms[1], rel * size + floor)
     assert ok, why
+
+
+@pytest.mark.parametrize("act", ["none", "relu", "silu", "gelu", "gelu_tanh"])
+@pytest.mark.parametrize("rows", [1, 20, 300])
+def test_infinities_follow_the_formulas(act, rows):
+    # act(+inf) is inf; act(-inf) is -inf (none), 0 (relu) or, of -inf times 0, a NaN. The largest
+    # finite values are not infinite.
+    inf, top = float("inf"), torch.finfo(BF16).max
+    low = {"none": -inf, "relu": 0.0}.get(act, float("nan"))
+    want = torch.tensor([inf, low, top, {"none": -top}.get(act, 0.0), float("nan")], device="cuda")
+    z = torch.tensor([inf, -inf, top, -top, float("nan")], device="cuda").to(BF16)
+    z = z.repeat(rows, 1)
+    one, zero = torch.ones(5, 1, dtype=BF16, device="cuda"), torch.zeros(rows, 1, dtype=BF16, device="cuda")
+    for out in (BF16, F32):
+        pre = torch.empty(rows, 5, dtype=out, device="cuda")
+        # the values come in by the bias of a product that is 0, a row at a time alike
+        y = tp.linear(zero, one, z[0].to(out), act=act, out_dtype=out, pre=pre)
+        assert torch.equal(torch.nan_to_num(pre.float(), 7.0), torch.nan_to_num(z.float(), 7.0))
+        assert torch.equal(torch.isnan(y), torch.isnan(want).expand(rows, 5))
+        assert torch.equal(torch.nan_to_num(y.float(), 7.0), torch.nan_to_num(want.to(out).float(), 7.0).expand(rows, 5))

@@ -77,11 +77,17 @@ __device__ __forceinline__ F2 recip_2(F2 p) {
     split(p, a, b);
     return f2(__fdividef(1.f, a), __fdividef(1.f, b));
 }
-// min(|x|, 16) of both.
-__device__ __forceinline__ F2 abs16_2(F2 p) {
+// max(-|x|, -16) and min(x, y) of both.
+__device__ __forceinline__ F2 minus_abs16_2(F2 p) {
     float a, b;
     split(p, a, b);
-    return f2(fminf(fabsf(a), 16.f), fminf(fabsf(b), 16.f));
+    return f2(fmaxf(-fabsf(a), -16.f), fmaxf(-fabsf(b), -16.f));
+}
+__device__ __forceinline__ F2 min_2(F2 p, F2 q) {
+    float a, b, c, d;
+    split(p, a, b);
+    split(q, c, d);
+    return f2(fminf(a, c), fminf(b, d));
 }
 __device__ __forceinline__ F2 neg_2(F2 p) { return F2{p.v ^ 0x8000000080000000ull}; }
 // max(x, 0); a NaN stays one.
@@ -99,9 +105,9 @@ __device__ __forceinline__ F2 relu_2(F2 p) {
 constexpr float kLog2e = 1.4426950408889634f;
 
 // The normal distribution's tail past a in [0, 16], erfc(a / sqrt 2) / 2, as
-// 2^P(a): log2 of the tail is smooth, and P is a polynomial over [0, 13.2] (where
-// a times the tail leaves 32 bits' normal numbers), fitted here by weighted least
-// squares to the smallest largest error of two kinds at once: of the tail, and of
+// 2^P(m), m = -a: log2 of the tail is smooth, and P is a polynomial over [-13.2,
+// 0] (past which a times the tail leaves 32 bits' normal numbers), fitted here by
+// weighted least squares to the smallest largest error of two kinds at once: of the tail, and of
 // the tail relative to itself, so that a negative z's gelu, though small, keeps
 // its size. Evaluated in 32 bits:
 //   degree 8   off by 5.3e-7, by 1e-4 of itself up to a = 4, 1.4e-4 up to 4.4 (where
@@ -110,35 +116,35 @@ constexpr float kLog2e = 1.4426950408889634f;
 //   FINE (12)  off by 5.5e-8, by 4.7e-6 of itself up to 3, 3.2e-5 up to 4, 3.5e-4
 //              anywhere: for 32-bit results. Half as much work again (4096 x 4096
 //              x 64 with gelu 25.7 us, 24.0 of degree 8).
-// P(16) is below -189, so the tail ends at 0. One branch-free exponential: erff
+// P(-16) is below -189, so the tail ends at 0. One branch-free exponential: erff
 // takes two paths that a warp has to go through both, and a rational form needs a
 // reciprocal besides, at 8 cycles of the special-function unit for a warp (gelu
 // at 32 columns: 1400 cycles so).
 template <bool FINE>
-__device__ __forceinline__ F2 normal_tail(F2 a) {
+__device__ __forceinline__ F2 normal_tail(F2 m) {
     F2 p;
     if constexpr (FINE) {
-        p = fma(a, f2(-1.77966791e-11f), f2(1.30777622e-09f));
-        p = fma(a, p, f2(-4.15794723e-08f));
-        p = fma(a, p, f2(7.47283934e-07f));
-        p = fma(a, p, f2(-8.27881195e-06f));
-        p = fma(a, p, f2(5.6687426e-05f));
-        p = fma(a, p, f2(-0.000204559736f));
-        p = fma(a, p, f2(-0.000161342788f));
-        p = fma(a, p, f2(0.00714332843f));
-        p = fma(a, p, f2(-0.0525699668f));
-        p = fma(a, p, f2(-0.459180653f));
-        p = fma(a, p, f2(-1.15110874f));
-        p = fma(a, p, f2(-0.99999994f));
+        p = fma(m, f2(-1.77966791e-11f), f2(-1.30777622e-09f));
+        p = fma(m, p, f2(-4.15794723e-08f));
+        p = fma(m, p, f2(-7.47283934e-07f));
+        p = fma(m, p, f2(-8.27881195e-06f));
+        p = fma(m, p, f2(-5.6687426e-05f));
+        p = fma(m, p, f2(-0.000204559736f));
+        p = fma(m, p, f2(0.000161342788f));
+        p = fma(m, p, f2(0.00714332843f));
+        p = fma(m, p, f2(0.0525699668f));
+        p = fma(m, p, f2(-0.459180653f));
+        p = fma(m, p, f2(1.15110874f));
+        p = fma(m, p, f2(-0.99999994f));
     } else {
-        p = fma(a, f2(3.89714749e-08f), f2(-2.379222e-06f));
-        p = fma(a, p, f2(6.1675637e-05f));
-        p = fma(a, p, f2(-0.000899372157f));
-        p = fma(a, p, f2(0.00833507441f));
-        p = fma(a, p, f2(-0.0536045954f));
-        p = fma(a, p, f2(-0.458758682f));
-        p = fma(a, p, f2(-1.15117025f));
-        p = fma(a, p, f2(-0.999998569f));
+        p = fma(m, f2(3.89714749e-08f), f2(2.379222e-06f));
+        p = fma(m, p, f2(6.1675637e-05f));
+        p = fma(m, p, f2(0.000899372157f));
+        p = fma(m, p, f2(0.00833507441f));
+        p = fma(m, p, f2(0.0536045954f));
+        p = fma(m, p, f2(-0.458758682f));
+        p = fma(m, p, f2(1.15117025f));
+        p = fma(m, p, f2(-0.999998569f));
     }
     return exp2_2(p);
 }
@@ -153,9 +159,11 @@ __device__ __forceinline__ F2 act_fwd(F2 z) {
     if constexpr (ACT == TPGEMM_ACT_SILU)
         return mul(z, recip_2(add(exp2_2(mul(z, f2(-kLog2e))), f2(1.f))));
     if constexpr (ACT == TPGEMM_ACT_GELU) {
-        // z Phi(z) = max(z, 0) - |z| tail(|z|)
-        const F2 a = abs16_2(z);
-        return fma(neg_2(a), normal_tail<FINE>(a), relu_2(z));
+        // z Phi(z) = max(z, 0) - |z| tail(|z|). A large positive z is held to 16
+        // there too, a negative one is not: -infinity meets a tail of 0, which is
+        // the formula's NaN.
+        const F2 m = minus_abs16_2(z);
+        return fma(min_2(z, m), normal_tail<FINE>(m), relu_2(z));
     }
     if constexpr (ACT == TPGEMM_ACT_GELU_TANH) {
         // (1 + tanh u) / 2 = 1 / (1 + exp(-2 u)), u = sqrt(2/pi) (z + 0.044715 z^3)
@@ -181,7 +189,7 @@ __device__ __forceinline__ F2 act_bwd(F2 z) {
     if constexpr (ACT == TPGEMM_ACT_GELU) {
         // Phi(z) + z phi(z), Phi(z) = tail or 1 - tail
         const F2 e = exp2_2(mul(mul(z, z), f2(-0.5f * kLog2e)));
-        const F2 q = normal_tail<false>(abs16_2(z));
+        const F2 q = normal_tail<false>(minus_abs16_2(z));
         float qa, qb, a, b;
         split(q, qa, qb);
         split(z, a, b);
