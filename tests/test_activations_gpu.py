@@ -129,3 +129,13 @@ def test_infinities_follow_the_formulas(act, rows):
         assert torch.equal(torch.nan_to_num(pre.float(), 7.0), torch.nan_to_num(z.float(), 7.0))
         assert torch.equal(torch.isnan(y), torch.isnan(want).expand(rows, 5))
         assert torch.equal(torch.nan_to_num(y.float(), 7.0), torch.nan_to_num(want.to(out).float(), 7.0).expand(rows, 5))
+
+
+@pytest.mark.parametrize("act", ["relu", "silu", "gelu", "gelu_tanh"])
+def test_derivatives_of_large_values_are_zero_and_one(act):
+    z = torch.tensor([[100.0, 1e4, 1e10, 1e20, 3e38]], device="cuda").to(BF16)
+    dY, W = torch.ones(1, 5, dtype=BF16, device="cuda"), torch.eye(5, dtype=BF16, device="cuda")
+    A = torch.ones(1, 5, dtype=BF16, device="cuda")
+    for pre, want in ((z, 1.0), (-z, 0.0)):
+        for g in tp.linear_backward(dY, A, W, pre, act=act, grad_dtype=F32):
+            assert (g == want).all()
