@@ -456,6 +456,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
     }
     if (warp == 1 && rank == 0) {
+        grid_dependency_wait();  // no wait's bound runs while the previous grid does
         const uint64_t dP = smem_desc_with_addr(operand_desc(p.p_mn), smem_u32(s.stages));
         const uint64_t dQ = smem_desc_with_addr(operand_desc(p.q_mn), smem_u32(s.stages) + p.p_bytes);
         const uint64_t step_p = operand_step(p.p_mn), step_q = operand_step(p.q_mn);
@@ -954,6 +955,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
             }
         }
     } else if (warp == 1) {
+        grid_dependency_wait();  // (as below)
         const uint64_t dP = smem_desc_with_addr(operand_desc(p.p_mn), smem_u32(s.stages));
         const uint64_t dQ = smem_desc_with_addr(operand_desc(p.q_mn), smem_u32(s.stages) + p.p_bytes);
         const uint64_t step_p = operand_step(p.p_mn), step_q = operand_step(p.q_mn);
@@ -976,6 +978,8 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
         }
         // Complete once every MMA issued is (also after a wait gave up).
         commit_elected(s.acc_full);
+    } else {
+        grid_dependency_wait();  // no wait's bound runs while the previous grid does
     }
     __syncwarp();
     // Every warp waits for the MMAs before it may read tensor memory, reuse the
@@ -1003,7 +1007,6 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
         __syncwarp();
         if (kSplit > 1) cluster_sync();
         else __syncthreads();
-        grid_dependency_wait();
         if (!*s.abort) join_lines<T, kSplit>(p, part, per, pitch, rank, rows, cols, m0, n0);
     };
     switch (p.split) {
