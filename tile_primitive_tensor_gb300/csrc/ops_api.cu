@@ -66,7 +66,8 @@ tpgemm_status check_mat(Mat& m, bool needed) {
     if (m.ld < m.cols || m.ld > (int64_t(1) << 40))
         return fail_with(TPGEMM_ERR_SHAPE, "%s: row stride %lld for %lld columns", m.name,
                          (long long)m.ld, (long long)m.cols);
-    if (m.rows * (m.pitch() / 16 + 1) > (int64_t(1) << 36))
+    // (Not as a product: 2^30 rows of 2^42 bytes are past 64 bits.)
+    if (m.pitch() / 16 + 1 > (int64_t(1) << 36) / m.rows)
         return fail_with(TPGEMM_ERR_SHAPE, "%s exceeds one GPU's memory", m.name);
     return TPGEMM_OK;
 }
