@@ -160,6 +160,24 @@ __device__ __forceinline__ void team_sum_max(float& a, uint32_t& b, float2* s) {
     }
 }
 
+// Row scales take the maximum of |h gamma| along with the sum of squares, and
+// rstd after it. Where 32 bits do not hold that maximum, the row's maximum is
+// taken again, of |h rstd gamma|.
+__device__ __forceinline__ bool off_scale(uint32_t amax) { return amax < 0x00800000u || amax >= 0x7f800000u; }
+
+// Maximum over a warp, or over the block through an `s` that it may still read.
+template <bool WARP>
+__device__ __forceinline__ void team_max(uint32_t& b, float2* s) {
+    b = __reduce_max_sync(0xffffffffu, b);
+    if constexpr (!WARP) {
+        const int nw = blockDim.x >> 5, lane = threadIdx.x & 31;
+        __syncthreads();
+        if (lane == 0) s[threadIdx.x >> 5].y = __uint_as_float(b);
+        __syncthreads();
+        b = __reduce_max_sync(0xffffffffu, lane < nw ? __float_as_uint(s[lane].y) : 0u);
+    }
+}
+
 // A block's maximum within a few units of a power of two: its scale hangs on
 // roundings of 32-bit arithmetic (one block in 10^6), so the power is compared
 // with |h rstd gamma| to twice as many bits.
@@ -194,11 +212,11 @@ __device__ __forceinline__ float gamma_of(const RmsNormOp& op, int64_t c) {
 // Stores one group of y (scaled for an 8-bit output) and, for MX, its scales.
 // True: the group's block is near a power of two, see settle_block (elements
 // that are not neighbours settle theirs here, before h is stored over X or R).
-template <typename XT, bool VEC, bool MX>
+template <typename XT, bool VEC, int MODE>
 __device__ __forceinline__ bool store_y(const RmsNormOp& op, int64_t row, const Cols<VEC>& c,
                                         float (&y)[8], float inv, float sum) {
     bool near = false;
-    if constexpr (MX) {
+    if constexpr (MODE == TPGEMM_SCALE_MX) {
         uint8_t* scale = static_cast<uint8_t*>(op.scale) + row * ((op.cols + 31) / 32);
         if constexpr (VEC) {  // four lanes hold 32 neighbouring columns
             uint32_t amax = 0;
@@ -233,7 +251,7 @@ __device__ __forceinline__ bool store_y(const RmsNormOp& op, int64_t row, const 
                 y[j] *= inv;
             }
         }
-    } else if (op.mode == TPGEMM_SCALE_ROW) {
+    } else if constexpr (MODE == TPGEMM_SCALE_ROW) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) y[j] *= inv;
     }
@@ -293,10 +311,10 @@ __device__ __forceinline__ void load_h(const RmsNormOp& op, int64_t row, const C
 }
 
 // What follows a row's loads: reduction, scale, and the stores of h and y.
-template <typename XT, int V, bool VEC, bool WARP, bool MX>
+template <typename XT, int V, bool VEC, bool WARP, int MODE>
 __device__ __forceinline__ void finish_row(const RmsNormOp& op, int64_t row, int t, int team,
                                            const float (&h)[V][8], float2* s) {
-    const bool row_mode = op.mode == TPGEMM_SCALE_ROW;
+    constexpr bool row_mode = MODE == TPGEMM_SCALE_ROW;
     float g[V][8];
     float ss = 0.f;
     uint32_t amax = 0;
@@ -306,15 +324,25 @@ __device__ __forceinline__ void finish_row(const RmsNormOp& op, int64_t row, int
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             ss += h[i][j] * h[i][j];
-            if (row_mode) amax = max(amax, abs_bits(h[i][j] * g[i][j]));
+            if constexpr (row_mode) amax = max(amax, abs_bits(h[i][j] * g[i][j]));
         }
     }
     team_sum_max<WARP>(ss, amax, s);
     const float rstd = 1.f / sqrtf(ss / float(op.cols) + op.eps);
     if (t == 0 && op.rstd) op.rstd[row] = rstd;
     float inv = 1.f;
-    if (row_mode) {
-        const float scale = row_scale(abs_bits(rstd * __uint_as_float(amax)), op.y);
+    if constexpr (row_mode) {
+        if (!off_scale(amax)) {
+            amax = abs_bits(rstd * __uint_as_float(amax));
+        } else {  // (the same for the whole team)
+            amax = 0;
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) amax = max(amax, abs_bits(h[i][j] * rstd * g[i][j]));
+            team_max<WARP>(amax, s);
+        }
+        const float scale = row_scale(amax, op.y);
         if (t == 0) static_cast<float*>(op.scale)[row] = scale;
         inv = 1.f / scale;
     }
@@ -325,10 +353,10 @@ __device__ __forceinline__ void finish_row(const RmsNormOp& op, int64_t row, int
         float y[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) y[j] = h[i][j] * rstd * g[i][j];
-        if (store_y<XT, VEC, MX>(op, row, c, y, inv, ss)) near |= 1u << i;
+        if (store_y<XT, VEC, MODE>(op, row, c, y, inv, ss)) near |= 1u << i;
         if (op.H) store_cols<XT, VEC>(op.H, row * op.ldh, c, h[i]);
     }
-    if constexpr (MX && VEC) {
+    if constexpr (MODE == TPGEMM_SCALE_MX && VEC) {
         if (near) {
 #pragma unroll
             for (int i = 0; i < V; ++i)
@@ -341,7 +369,7 @@ __device__ __forceinline__ void finish_row(const RmsNormOp& op, int64_t row, int
 // a warp, else to a block. AHEAD: blocks stay and walk the rows grid-stride, and
 // load the next row before the reduction of this one, which waits for all of
 // it; else a team ends with its row and the blocks beside it keep memory busy.
-template <typename XT, int V, bool VEC, bool WARP, bool MX, bool AHEAD = false>
+template <typename XT, int V, bool VEC, bool WARP, int MODE, bool AHEAD = false>
 __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : kMaxTeam) rmsnorm_kernel(const __grid_constant__ RmsNormOp op) {
     __shared__ float2 s[2][32];
     const int team = WARP ? 32 : int(blockDim.x);
@@ -354,7 +382,7 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : kMaxTeam) rmsnorm_kern
     if constexpr (!AHEAD) {
 #pragma unroll
         for (int i = 0; i < V; ++i) load_h<XT, VEC>(op, row, Cols<VEC>(i, t, team, op.cols), h[i]);
-        finish_row<XT, V, VEC, WARP, MX>(op, row, t, team, h, s[0]);
+        finish_row<XT, V, VEC, WARP, MODE>(op, row, t, team, h, s[0]);
     } else {
         Ahead<XT, VEC> x[V], r[V];
         auto fetch = [&](int64_t at) {
@@ -378,18 +406,19 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : kMaxTeam) rmsnorm_kern
                 }
             }
             if (row + gridDim.x < op.rows) fetch(row + gridDim.x);
-            finish_row<XT, V, VEC, WARP, MX>(op, row, t, team, h, s[turn]);
+            finish_row<XT, V, VEC, WARP, MODE>(op, row, t, team, h, s[turn]);
         }
     }
 }
 
-// Rows of any width, a block to a row, read twice.
-template <typename XT, bool VEC, bool MX>
-__global__ void __launch_bounds__(kMaxTeam) rmsnorm_wide_kernel(const __grid_constant__ RmsNormOp op) {
+// Rows of any width, a block to a row, read twice. Two blocks to an SM where 32
+// registers do (2048 x 20480 bf16 with row scales 79 us, 112 with one).
+template <typename XT, bool VEC, int MODE>
+__global__ void __launch_bounds__(kMaxTeam, VEC && MODE != TPGEMM_SCALE_MX ? 2 : 1) rmsnorm_wide_kernel(const __grid_constant__ RmsNormOp op) {
     __shared__ float2 s[32];
     const int team = int(blockDim.x), t = int(threadIdx.x);
     const int64_t row = blockIdx.x;
-    const bool row_mode = op.mode == TPGEMM_SCALE_ROW;
+    constexpr bool row_mode = MODE == TPGEMM_SCALE_ROW;
     const int64_t groups = (op.cols + 8 * team - 1) / (8 * team);
     float h[8], g[8];
     float ss = 0.f;
@@ -399,19 +428,33 @@ __global__ void __launch_bounds__(kMaxTeam) rmsnorm_wide_kernel(const __grid_con
     for (int64_t i = 0; i < groups; ++i) {
         const Cols<VEC> c(i, t, team, op.cols);
         load_h<XT, VEC>(op, row, c, h);
-        if (row_mode) load_gamma<XT, VEC>(op.gamma, op.g, c, g);
+        if constexpr (row_mode) load_gamma<XT, VEC>(op.gamma, op.g, c, g);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             ss += h[j] * h[j];
-            if (row_mode) amax = max(amax, abs_bits(h[j] * g[j]));
+            if constexpr (row_mode) amax = max(amax, abs_bits(h[j] * g[j]));
         }
     }
     team_sum_max<false>(ss, amax, s);
     const float rstd = 1.f / sqrtf(ss / float(op.cols) + op.eps);
     if (t == 0 && op.rstd) op.rstd[row] = rstd;
     float inv = 1.f;
-    if (row_mode) {
-        const float scale = row_scale(abs_bits(rstd * __uint_as_float(amax)), op.y);
+    if constexpr (row_mode) {
+        if (!off_scale(amax)) {
+            amax = abs_bits(rstd * __uint_as_float(amax));
+        } else {  // (the same for the whole block)
+            amax = 0;
+#pragma unroll 1
+            for (int64_t i = 0; i < groups; ++i) {
+                const Cols<VEC> c(i, t, team, op.cols);
+                load_h<XT, VEC>(op, row, c, h);
+                load_gamma<XT, VEC>(op.gamma, op.g, c, g);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) amax = max(amax, abs_bits(h[j] * rstd * g[j]));
+            }
+            team_max<false>(amax, s);
+        }
+        const float scale = row_scale(amax, op.y);
         if (t == 0) static_cast<float*>(op.scale)[row] = scale;
         inv = 1.f / scale;
     }
@@ -422,8 +465,8 @@ __global__ void __launch_bounds__(kMaxTeam) rmsnorm_wide_kernel(const __grid_con
         float y[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) y[j] = h[j] * rstd * g[j];
-        const bool near = store_y<XT, VEC, MX>(op, row, c, y, inv, ss);
-        if constexpr (MX && VEC) {
+        const bool near = store_y<XT, VEC, MODE>(op, row, c, y, inv, ss);
+        if constexpr (MODE == TPGEMM_SCALE_MX && VEC) {
             if (near) settle_block<XT>(op, row, c, h, ss);
         }
         if (op.H) store_cols<XT, VEC>(op.H, row * op.ldh, c, h);
@@ -600,27 +643,27 @@ bool rows_aligned(const void* p, int64_t ld, int64_t rows, int elem, int bytes) 
                   (rows <= 1 || (ld * elem_size(elem)) % bytes == 0));
 }
 
-template <typename XT, bool VEC, bool MX>
+template <typename XT, bool VEC, int MODE>
 cudaError_t launch_norm(const RmsNormOp& op, cudaStream_t stream) {
     const Spread s = spread_of(op.rows, op.cols);
     if (s.v == 0) {
         if (op.rows > 0x7fffffff) return cudaErrorInvalidValue;
-        return launch_dependent(rmsnorm_wide_kernel<XT, VEC, MX>, dim3(unsigned(op.rows)),
+        return launch_dependent(rmsnorm_wide_kernel<XT, VEC, MODE>, dim3(unsigned(op.rows)),
                                 dim3(unsigned(s.threads())), 0, stream, op);
     }
     int64_t blocks = (op.rows + s.rows() - 1) / s.rows();
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-    auto fn = s.warp ? (s.v == 1 ? rmsnorm_kernel<XT, 1, VEC, true, MX> : rmsnorm_kernel<XT, 2, VEC, true, MX>)
-              : s.v == 1 ? rmsnorm_kernel<XT, 1, VEC, false, MX>
-                         : rmsnorm_kernel<XT, 2, VEC, false, MX>;
-    if constexpr (VEC) {
+    auto fn = s.warp ? (s.v == 1 ? rmsnorm_kernel<XT, 1, VEC, true, MODE> : rmsnorm_kernel<XT, 2, VEC, true, MODE>)
+              : s.v == 1 ? rmsnorm_kernel<XT, 1, VEC, false, MODE>
+                         : rmsnorm_kernel<XT, 2, VEC, false, MODE>;
+    if constexpr (VEC && MODE != TPGEMM_SCALE_ROW) {
         // Teams of 512 threads and more leave an SM two rows or one, too few to
         // hide each other's reductions: such rows are loaded ahead (bf16 with
         // residual, MX scales: 8192 x 8192 92 -> 87 us; no scales: 2048 x
         // 16384 55.3 -> 46.2 us). Not with row scales, whose maxima take the
         // registers (89.1 -> 91.6), nor narrower rows (8192 x 4096 44.0 -> 46.4).
-        if (s.v == 2 && s.team >= 512 && op.mode != TPGEMM_SCALE_ROW) {
-            fn = rmsnorm_kernel<XT, 2, VEC, false, MX, true>;
+        if (s.v == 2 && s.team >= 512) {
+            fn = rmsnorm_kernel<XT, 2, VEC, false, MODE, true>;
             blocks = std::min(blocks, int64_t(152) * (kMaxTeam / s.team));
         }
     }
@@ -634,9 +677,13 @@ cudaError_t launch_norm_typed(const RmsNormOp& op, cudaStream_t stream) {
                      rows_aligned(op.H, op.ldh, op.rows, op.x, 16) &&
                      rows_aligned(op.Y, op.ldy, op.rows, op.y, elem_size(op.y) == 1 ? 8 : 16) &&
                      rows_aligned(op.gamma, 0, 1, op.g, 16);
-    if (op.mode == TPGEMM_SCALE_MX)
-        return vec ? launch_norm<XT, true, true>(op, stream) : launch_norm<XT, false, true>(op, stream);
-    return vec ? launch_norm<XT, true, false>(op, stream) : launch_norm<XT, false, false>(op, stream);
+    const auto launch = [&](auto mode) {
+        constexpr int kMode = decltype(mode)::value;
+        return vec ? launch_norm<XT, true, kMode>(op, stream) : launch_norm<XT, false, kMode>(op, stream);
+    };
+    if (op.mode == TPGEMM_SCALE_MX) return launch(std::integral_constant<int, TPGEMM_SCALE_MX>());
+    if (op.mode == TPGEMM_SCALE_ROW) return launch(std::integral_constant<int, TPGEMM_SCALE_ROW>());
+    return launch(std::integral_constant<int, TPGEMM_SCALE_NONE>());
 }
 
 // Blocks of the register kernel: 512 threads to an SM, which is what its
