@@ -118,7 +118,8 @@ __global__ void __launch_bounds__(kThreads, 4)
 // Rows of `bytes` bytes, `pitch` apart and anywhere in memory, to rows of whole
 // 16-byte units; a thread to a unit, blockIdx.z to a matrix. A unit with another
 // one behind it in its row is read as five aligned words and shifted into place,
-// the last one or two byte by byte.
+// the last one or two byte by byte, and so the matrix's first one where its first
+// word begins before it.
 __global__ void __launch_bounds__(256) align_rows_kernel(const __grid_constant__ AlignJobs jobs) {
     grid_launch_dependents();
     grid_dependency_wait();
@@ -130,8 +131,8 @@ __global__ void __launch_bounds__(256) align_rows_kernel(const __grid_constant__
     for (int64_t r = int64_t(blockIdx.y) * 8 + (threadIdx.x >> 5); r < job.rows; r += int64_t(gridDim.y) * 8) {
         const uint8_t* p = job.src + r * job.pitch + 16 * u;
         uint32_t w[4] = {};
-        if (16 * u + 32 <= bytes) {
-            const uint32_t off = uint32_t(reinterpret_cast<uintptr_t>(p) & 3u);
+        const uint32_t off = uint32_t(reinterpret_cast<uintptr_t>(p) & 3u);
+        if (16 * u + 32 <= bytes && p - off >= job.src) {
             const uint32_t* q = reinterpret_cast<const uint32_t*>(p - off);
             uint32_t x[5];
 #pragma unroll
