@@ -48,3 +48,53 @@ def test_no_bound_runs_while_the_previous_grid_does(path, M, N, tune):
     assert tp.tpgemm_last_device_error() == tp.TPGEMM_OK
     assert begin.elapsed_time(end) > 4.0  # (else nothing was shown)
     assert torch.equal(got, want)
+
+
+def gives_up(A, W, residual, pre):
+    """Whether the product ends with the waits' status, read once, and the context goes on."""
+    tp.linear(A, W, None, residual, pre=pre)
+    status = tp.tpgemm_last_device_error()
+    assert status in (tp.TPGEMM_OK, tp.TPGEMM_ERR_TIMEOUT), tp.tpgemm_last_error_detail()
+    assert tp.tpgemm_last_device_error() == tp.TPGEMM_OK
+    return status == tp.TPGEMM_ERR_TIMEOUT
+
+
+# Sums so long that the epilogue's wait for one runs out on a healthy product, with fills and MMAs
+# under way in both CTAs of each pair: all roles stop, what is in flight lands, tensor memory is
+# freed, and the next call on the same SMs is right.
+@pytest.mark.parametrize("M,N,more", [(256, 256, False), (250, 250, True), (512, 512, True)])
+def test_a_tile_product_that_gives_up(M, N, more, tune):
+    g = torch.Generator(device="cuda").manual_seed(N)
+    K = 1 << (21 if M <= 256 else 20)
+    A, W = torch.zeros(M, K, dtype=torch.bfloat16, device="cuda"), torch.zeros(N, K, dtype=torch.bfloat16, device="cuda")
+    r = torch.zeros(M, N, dtype=torch.bfloat16, device="cuda") if more else None
+    z = torch.zeros(M, N, dtype=torch.bfloat16, device="cuda") if more and M == 512 else None
+    a, w = ones(g, 1000, 192), ones(g, 1200, 192)
+    want = (a.float() @ w.float().t()).bfloat16()
+    tune.setenv("TPGEMM_LINEAR_PATH", "tile")
+    for i in range(6):
+        tune.setenv("TPGEMM_WAIT_TIMEOUT_MS", "1")
+        assert gives_up(A, W, r, z)
+        tune.delenv("TPGEMM_WAIT_TIMEOUT_MS")
+        for _ in range(3):
+            assert torch.equal(tp.linear(a, w), want)
+    assert not gives_up(A, W, r, z)
+
+
+@pytest.mark.parametrize("split", [1, 2])
+@pytest.mark.parametrize("M,N", [(40, 128), (128, 40)])
+def test_a_split_product_that_gives_up(M, N, split, tune):
+    g = torch.Generator(device="cuda").manual_seed(split)
+    K = 1 << 22
+    A, W = torch.zeros(M, K, dtype=torch.bfloat16, device="cuda"), torch.zeros(N, K, dtype=torch.bfloat16, device="cuda")
+    a, w = ones(g, 100, 192), ones(g, 1200, 192)
+    want = (a.float() @ w.float().t()).bfloat16()
+    tune.setenv("TPGEMM_LINEAR_PATH", "split")
+    tune.setenv("TPGEMM_LINEAR_SPLIT", str(split))
+    for i in range(6):
+        tune.setenv("TPGEMM_WAIT_TIMEOUT_MS", "1")
+        assert gives_up(A, W, None, None)
+        tune.delenv("TPGEMM_WAIT_TIMEOUT_MS")
+        for _ in range(3):
+            assert torch.equal(tp.linear(a, w), want)
+    assert not gives_up(A, W, None, None)

@@ -31,6 +31,8 @@ constexpr int kPrefetch = 2;  // runs of a warp asked for ahead
 constexpr int64_t kManyRows = 2 * 152 * kRows;  // of W: more than two blocks to an SM
 
 // The 16 bytes of row r from element k on (zero past K or for no row).
+// (A coherent load: the weights may be what the previous grid, which this one
+// starts beside, still writes until the dependency is waited for.)
 template <typename T>
 __device__ __forceinline__ uint4 load16(const T* r, bool live, int64_t k, int64_t K) {
     constexpr int E = 16 / sizeof(T);

@@ -152,6 +152,10 @@ __device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* ma
     }
 }
 
+__device__ __forceinline__ void st_cluster_b32(uint32_t addr, uint32_t v) {
+    asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
 // Commits of the elected thread's MMAs (the whole warp, convergent).
 __device__ __forceinline__ void commit_elected(uint64_t* bar) {
     asm volatile(
@@ -336,6 +340,8 @@ struct TileSmem {
     uint64_t *full, *empty, *acc_full, *acc_empty, *drain, *rbar;
     uint32_t* tmem_base;
     volatile int* abort;
+    volatile int* fills;  // after a timeout: the two producers' fills,
+    volatile int* peer;   // and the other CTA's, [2] set once it has given up too
 };
 
 __device__ __forceinline__ TileSmem carve_tile(uint8_t* raw, const TcLinear& p) {
@@ -353,6 +359,8 @@ __device__ __forceinline__ TileSmem carve_tile(uint8_t* raw, const TcLinear& p) 
     s.rbar = s.drain + 1;  // [epilogue warps][2] residual fills
     s.tmem_base = reinterpret_cast<uint32_t*>(s.rbar + 2 * kTileEpiWarps);
     s.abort = reinterpret_cast<volatile int*>(s.tmem_base + 1);
+    s.fills = s.abort + 1;
+    s.peer = s.fills + 2;
     return s;
 }
 
@@ -367,6 +375,30 @@ __device__ __forceinline__ void tile_at(int T, const TcLinear& p, int& tp, int& 
     tp = first + r % n;
     tq = r / n;
     if (g & 1) tq = p.tiles_q - 1 - tq;
+}
+
+// Lets the fills of a pair that gave up land, by a thread of the even CTA, on
+// whose barriers they complete. Fill g (of stage g % stages, by producer g & 1) is
+// both CTAs' boxes, but one CTA may have stopped a fill before the other: the
+// half that does not come is left out of the count.
+__device__ __forceinline__ void drain_fills(const TileSmem& s, const TcLinear& p, uint32_t half, uint64_t tmo) {
+    const int own0 = s.fills[0], own1 = s.fills[1], peer0 = s.peer[0], peer1 = s.peer[1];
+    const int end = max(2 * max(own0, peer0) - 1, 2 * max(own1, peer1));  // past the last fill
+    // A stage's last fill is among the last 2 stages + 2: producers stay within
+    // the ring of each other.
+    uint32_t seen = 0;
+    for (int g = end - 1; g >= 0 && g >= end - 2 * p.stages - 2; --g) {
+        const int i = g % p.stages;
+        const bool ours = (g >> 1) < ((g & 1) ? own1 : own0), theirs = (g >> 1) < ((g & 1) ? peer1 : peer0);
+        if (((seen >> i) & 1u) || !(ours || theirs)) continue;
+        seen |= 1u << i;
+        if (!ours) mbar_arrive_expect_tx(&s.full[i], half);
+        if (!theirs)
+            asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(&s.full[i])),
+                         "r"(half)
+                         : "memory");
+        wait_bounded(&s.full[i], uint32_t(g / p.stages) & 1u, s.abort, tmo, true);
+    }
 }
 
 template <typename T>
@@ -400,6 +432,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         mbar_init(s.drain, 1);
         for (int i = 0; i < 2 * kTileEpiWarps; ++i) mbar_init(&s.rbar[i], 1);
         *s.abort = 0;
+        s.peer[2] = 0;
         fence_mbarrier_init();
     }
     if (warp == 1) {
@@ -411,7 +444,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     tc_fence_after_sync();
     grid_launch_dependents();
     const uint32_t tmem = *s.tmem_base;
-    uint32_t issued_any = 0, issued_parity = 0;  // a producer's last fill of each stage
+    int fills = 0;  // a producer's
     uint32_t rphase = 0, rpend = 0;  // residual fills: next parity, and in flight (bit: buffer)
 
     const int prod = warp == 0 ? 0 : (warp == 2 ? 1 : -1);
@@ -445,8 +478,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     if (rank == 0) expect_elected(full0 + 8u * uint32_t(stage), tx);
                     load_operand<true>(sp, &mapP, lead, p.p_mn, 2, p0, k0, pol);
                     load_operand<true>(sp + p.p_bytes, &mapQ, lead, p.q_mn, q_atoms, q0, k0, pol);
-                    issued_any |= 1u << stage;
-                    issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
+                    ++fills;
                 }
                 if (++stage == nstages) {
                     stage = 0;
@@ -673,15 +705,23 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
     tc_fence_before_sync();
     __syncthreads();
-    if (*s.abort) {
-        // Both CTAs' fills complete on the even CTA's barriers.
-        if (prod >= 0 && lane == 0 && rank == 0)
-            for (int i = 0; i < p.stages; ++i)
-                if (issued_any & (1u << i))
-                    wait_bounded(&s.full[i], (issued_parity >> i) & 1u, s.abort, tmo, true);
-        __syncthreads();
+    const bool gave_up = *s.abort != 0;
+    if (gave_up && prod >= 0 && lane == 0) {
+        s.fills[prod] = fills;
+        const uint32_t peer = mapa_shared(smem_u32(const_cast<int*>(s.peer)), uint32_t(rank ^ 1));
+        st_cluster_b32(peer + 4u * uint32_t(prod), uint32_t(fills));
+        if (prod == 0) st_cluster_b32(peer + 8u, 1u);
     }
     cluster_sync();  // no CTA leaves while a peer may still reach its barriers
+    // (Where only one gave up, the other has seen all MMAs through and with them
+    // all fills.)
+    if (gave_up && s.peer[2]) {
+        if (rank == 0 && threadIdx.x == 0) {
+            const int q_rows = p.bn / 2;
+            drain_fills(s, p, p.p_bytes + (p.q_mn ? uint32_t((q_rows + 63) / 64) * kAtom : uint32_t(q_rows) * 128u), tmo);
+        }
+        cluster_sync();
+    }
     if (warp == 1) {
         __syncwarp();
         tc_fence_after_sync();
@@ -723,10 +763,6 @@ __device__ __forceinline__ SplitSmem carve_split(uint8_t* raw, const TcLinear& p
     s.tmem_base = reinterpret_cast<uint32_t*>(s.acc_full + 1);
     s.abort = reinterpret_cast<volatile int*>(s.tmem_base + 1);
     return s;
-}
-
-__device__ __forceinline__ void st_cluster_f32(uint32_t addr, uint32_t v) {
-    asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
 // The two halves of cluster_sync().
@@ -807,7 +843,7 @@ __device__ __forceinline__ void deal_lines(const TcLinear& p, uint32_t tmem, flo
                     if (SPLIT == 1)
                         part[l * pitch + place] = __uint_as_float(r[i]);
                     else
-                        st_cluster_f32(mapa_shared(mine + uint32_t(l / SPLIT * pitch + place) * 4u,
+                        st_cluster_b32(mapa_shared(mine + uint32_t(l / SPLIT * pitch + place) * 4u,
                                                    uint32_t(i % SPLIT)), r[i]);
                 }
             }
@@ -1002,7 +1038,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
             if (p.sums_at == 0) cluster_arrive();
             cluster_wait();
         }
-        if (ok && !*s.abort) deal_lines<kSplit, SWAP>(p, tmem, part, per, pitch, rank, rows);
+        if (__all_sync(0xffffffffu, ok && !*s.abort)) deal_lines<kSplit, SWAP>(p, tmem, part, per, pitch, rank, rows);
         tc_fence_before_sync();
         __syncwarp();
         if (kSplit > 1) cluster_sync();
@@ -1060,7 +1096,7 @@ void set_cluster(cudaLaunchAttribute& a, int n) {
 size_t tc_linear_smem(const TcLinear& p) {
     if (p.pair)
         return size_t(p.stages) * (p.p_bytes + p.q_bytes) + kTileEpiWarps * (kStaging + kBiasBytes) +
-               8 * (2 * size_t(p.stages) + 5 + 2 * kTileEpiWarps) + 16;
+               8 * (2 * size_t(p.stages) + 5 + 2 * kTileEpiWarps) + 32;
     return p.half_sm ? kSplitHalfSmem : size_t(kTcMaxSmem);
 }
 
