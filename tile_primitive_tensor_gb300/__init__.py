@@ -729,6 +729,8 @@ def linear(A, W, bias=None, residual=None, *, act="none", scale_a=None, scale_w=
     torch = _torch or _import_torch()
     lib = _lib or _load()
     M, K, index, device = _sizes("A", A)
+    if W.dim() != 2:
+        raise ValueError("W must be 2-D")
     N = W.shape[0]
     dt = A.dtype
     lda = _matrix("A", A, M, K, dt, index)
@@ -779,6 +781,8 @@ def linear_backward(dY, A, W, pre=None, *, act="none", grad_dtype=None, need=(Tr
     torch = _torch or _import_torch()
     lib = _lib or _load()
     M, K, index, device = _sizes("A", A)
+    if W.dim() != 2:
+        raise ValueError("W must be 2-D")
     N = W.shape[0]
     dt = A.dtype
     grad_dtype = dt if grad_dtype is None else grad_dtype
