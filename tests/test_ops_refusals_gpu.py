@@ -18,7 +18,7 @@ def _setup():
 
 
 def half(*shape):
-    return torch.ones(*shape, device="cuda").half()
+    return torch.ones(shape, device="cuda").half()
 
 
 @pytest.mark.parametrize("shape", [(), (16,), (1, 8, 16)])
