@@ -27,3 +27,18 @@ def test_weights_that_are_no_matrix(shape):
                  lambda: tp.linear_backward(half(4, 8), half(4, 16), half(*shape))):
         with pytest.raises(ValueError, match="W must be 2-D"):
             call()
+
+
+def test_a_workspace_with_gaps():
+    # Its elements' bytes from its start on would be used, which are not all its own.
+    A, W, dY, w = half(40, 41), half(24, 41), half(40, 24), half(41)
+    whole = torch.zeros(1 << 20, dtype=torch.uint8, device="cuda")
+    ok = tp.linear(A, W, workspace=whole)
+    assert torch.equal(ok, tp.linear(A, W))
+    whole.zero_()
+    for call in (lambda ws: tp.linear(A, W, workspace=ws), lambda ws: tp.linear_backward(dY, A, W, workspace=ws),
+                 lambda ws: tp.rmsnorm_backward(A, A, torch.ones(40, device="cuda"), w, workspace=ws)):
+        with pytest.raises(ValueError, match="contiguous"):
+            call(whole[::2])
+    torch.cuda.synchronize()
+    assert (whole == 0).all()

@@ -697,6 +697,8 @@ def _call(torch, index, function, args, workspace=None, need=None) -> None:
     elif workspace is not None:
         if workspace.get_device() != index:
             raise ValueError(f"workspace is on {workspace.device}, not cuda:{index}")
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
         status = function(*args, workspace.data_ptr(),
                           workspace.numel() * workspace.element_size(), handle)
     elif need == 0:
