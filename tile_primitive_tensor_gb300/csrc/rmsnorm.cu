@@ -656,12 +656,14 @@ cudaError_t launch_norm(const RmsNormOp& op, cudaStream_t stream) {
     auto fn = s.warp ? (s.v == 1 ? rmsnorm_kernel<XT, 1, VEC, true, MODE> : rmsnorm_kernel<XT, 2, VEC, true, MODE>)
               : s.v == 1 ? rmsnorm_kernel<XT, 1, VEC, false, MODE>
                          : rmsnorm_kernel<XT, 2, VEC, false, MODE>;
-    if constexpr (VEC && MODE != TPGEMM_SCALE_ROW) {
+    if constexpr (VEC && (MODE == TPGEMM_SCALE_NONE || (MODE == TPGEMM_SCALE_MX && sizeof(XT) == 2))) {
         // Teams of 512 threads and more leave an SM two rows or one, too few to
         // hide each other's reductions: such rows are loaded ahead (bf16 with
         // residual, MX scales: 8192 x 8192 92 -> 87 us; no scales: 2048 x
-        // 16384 55.3 -> 46.2 us). Not with row scales, whose maxima take the
-        // registers (89.1 -> 91.6), nor narrower rows (8192 x 4096 44.0 -> 46.4).
+        // 16384 55.3 -> 46.2 us; f32 8192 x 8192 179 -> 182, 98 -> 94 without
+        // residual, 2048 x 16384 61 -> 55 so). Not with row scales, whose maxima
+        // take the registers (bf16 89.1 -> 91.6), nor f32 rows with MX scales, which
+        // would spill (140 -> 186), nor narrower rows (8192 x 4096 44.0 -> 46.4).
         if (s.v == 2 && s.team >= 512) {
             fn = rmsnorm_kernel<XT, 2, VEC, false, MODE, true>;
             blocks = std::min(blocks, int64_t(152) * (kMaxTeam / s.team));
