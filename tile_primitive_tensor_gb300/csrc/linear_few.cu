@@ -28,7 +28,7 @@ constexpr int kWarps = 8;
 constexpr int kRows = 16;   // rows of W in a block
 constexpr int kRun = 4;     // 16-byte loads of a row that a thread has in flight at a time
 constexpr int kPrefetch = 2;  // runs of a warp asked for ahead
-constexpr int64_t kManyRows = 2 * 152 * kRows;  // of W: more than two blocks to an SM
+constexpr int64_t kManyRows = 2 * kSms * kRows;  // of W: more than two blocks to an SM
 
 // The 16 bytes of row r from element k on (zero past K or for no row).
 // (A coherent load: the weights may be what the previous grid, which this one

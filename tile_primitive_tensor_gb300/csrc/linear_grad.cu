@@ -161,7 +161,7 @@ constexpr int64_t kFewRows = 256;
 int act_grad_strips(int64_t M, int64_t N) {
     if (M <= kFewRows) return 1;
     const int64_t cb = (N + kWide * kPer - 1) / (kWide * kPer);
-    const int64_t want = cb > 0 ? (608 + cb - 1) / cb : 1;
+    const int64_t want = cb > 0 ? (4 * kSms + cb - 1) / cb : 1;
     const int64_t most = (M + 15) / 16;
     return int(want < most ? want : most);
 }
@@ -185,7 +185,7 @@ cudaError_t launch_act_grad(const ActGradOp& op, cudaStream_t stream) {
     return launch_column_sum(op.partial, strips, op.N, op.dbias, op.grad, stream);
 }
 
-constexpr int64_t kAlignBlocks = 8 * 152;  // eight to an SM; a warp then has several rows' loads in flight
+constexpr int64_t kAlignBlocks = 8 * kSms;  // eight to an SM; a warp then has several rows' loads in flight
 
 cudaError_t launch_align_rows(const AlignJobs& jobs, cudaStream_t stream) {
     if (jobs.n == 0) return cudaSuccess;

@@ -161,10 +161,12 @@ Choice plan_tile(const LinearOp& op, int64_t kb, int sms, const LinearTuning& t)
     return best;
 }
 
-// Blocks that run at once in clusters of `split` (placed within groups of SMs:
-// 76 of 2, 36 of 4 and 15 of 8 blocks that have an SM each).
+// Blocks that run at once in clusters of `split`, placed within groups of SMs: 76
+// of 2, 36 of 4 and 15 of 8 blocks that have an SM each, as the occupancy query
+// counted them. Chips differ in which SMs a group has, by a cluster or two; a plan
+// that counts on too many runs a few of its clusters late, with the same result.
 int64_t places(int split, bool half_sm) {
-    return (split <= 2 ? 152 : split == 4 ? 144 : 120) * (half_sm ? 2 : 1);
+    return (split <= 2 ? kSms : split == 4 ? 144 : 120) * (half_sm ? 2 : 1);
 }
 
 // What L2 costs the split kernel more when a row's stages of Q, which many
@@ -217,7 +219,7 @@ Choice plan_split(const LinearOp& op, int64_t kb, const LinearTuning& t, int64_t
         best.bp = bp;
         best.split = split;
         best.half_sm = half_sm;
-        const double share = double(ceil_div(kb, split)), resident = double(ceil_div(ctas, 148));
+        const double share = double(ceil_div(kb, split)), resident = double(ceil_div(ctas, kSms));
         const double busy = resident * share * 2.0 * (bp + p.bn) / kClock;
         const double l2 = double(ctas) * share * (bp + p.bn) * 128 * straddle(op, swap) / kL2;
         const double sums = resident * bp * p.bn * 4;  // bytes an SM joins

@@ -28,6 +28,11 @@ struct LinearTuning {
 };
 LinearTuning linear_tuning();
 
+// Streaming multiprocessors of a GB300. Grids and plans of these operators are
+// sized by it. It is a constant, not the device's count, since the strips of
+// column sums go by it too: results and workspaces are then the same everywhere.
+constexpr int kSms = 152;
+
 inline int elem_size(int elem) {
     return elem == TPGEMM_ELEM_F32 ? 4 : (elem == TPGEMM_ELEM_F16 || elem == TPGEMM_ELEM_BF16) ? 2 : 1;
 }

@@ -633,7 +633,7 @@ Spread spread_of(int64_t rows, int64_t cols) {
     const int64_t groups = (cols + 7) / 8;
     if (groups <= 64) return {32, groups <= 32 ? 1 : 2, true};
     if (cols > kMaxHeld) return {kMaxTeam, 0, false};
-    const bool one = groups <= kMaxTeam && (rows <= 304 || cols % 8 != 0);
+    const bool one = groups <= kMaxTeam && (rows <= 2 * kSms || cols % 8 != 0);
     const int64_t per = one ? groups : (groups + 1) / 2;
     return {int((per + 31) / 32 * 32), one ? 1 : 2, false};
 }
@@ -666,7 +666,7 @@ cudaError_t launch_norm(const RmsNormOp& op, cudaStream_t stream) {
         // would spill (140 -> 186), nor narrower rows (8192 x 4096 44.0 -> 46.4).
         if (s.v == 2 && s.team >= 512) {
             fn = rmsnorm_kernel<XT, 2, VEC, false, MODE, true>;
-            blocks = std::min(blocks, int64_t(152) * (kMaxTeam / s.team));
+            blocks = std::min(blocks, int64_t(kSms) * (kMaxTeam / s.team));
         }
     }
     return launch_dependent(fn, dim3(unsigned(blocks)), dim3(unsigned(s.threads())), 0, stream, op);
@@ -693,7 +693,7 @@ cudaError_t launch_norm_typed(const RmsNormOp& op, cudaStream_t stream) {
 // block's sums are written and read once more.
 int grad_blocks(int64_t rows, const Spread& s) {
     const int64_t most = (rows + 2 * s.rows() - 1) / (2 * s.rows());
-    const int64_t fill = 152 * (s.threads() >= 512 ? 1 : 512 / s.threads());
+    const int64_t fill = kSms * (s.threads() >= 512 ? 1 : 512 / s.threads());
     return int(most < fill ? (most < 1 ? 1 : most) : fill);
 }
 
