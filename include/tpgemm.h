@@ -544,8 +544,9 @@ tpgemm_status tpgemm_linear(void* Y, void* Z, const void* A, const void* W, cons
 
 /* Bytes of workspace tpgemm_linear needs, for copies of operands: more than 16
  * rows of A by a W where one's rows do not start on 16-byte boundaries, or 48 to
- * 256 rows that do not start on 128-byte ones by a large W; else 0. The
- * addresses matter by their alignment only. 0 for a description that tpgemm_linear rejects. */
+ * 256 rows that do not start on 128-byte ones by a large W; else 0, and so
+ * always where both operands' rows start on 128-byte lines. The addresses matter
+ * by their alignment only. 0 for a description that tpgemm_linear rejects. */
 size_t tpgemm_linear_workspace_bytes(const void* A, const void* W, const tpgemm_linear_desc* d);
 
 /*
@@ -632,8 +633,8 @@ tpgemm_status tpgemm_rmsnorm_backward(void* dX, void* dgamma, const void* dY, co
                                       const tpgemm_rmsnorm_grad_desc* d, void* workspace,
                                       size_t workspace_bytes, void* stream);
 
-/* Bytes of workspace tpgemm_rmsnorm_backward needs for dgamma's partial sums
- * (0 when dgamma is not wanted), 256-byte aligned. */
+/* Bytes of workspace tpgemm_rmsnorm_backward needs, where dgamma is wanted, for
+ * its partial sums, 256-byte aligned. (None is read where dgamma is NULL.) */
 size_t tpgemm_rmsnorm_backward_workspace_bytes(int64_t rows, int64_t cols);
 
 /* Static English name of a status. Never NULL. */

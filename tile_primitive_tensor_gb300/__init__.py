@@ -760,7 +760,7 @@ def linear(A, W, bias=None, residual=None, *, act="none", scale_a=None, scale_w=
     desc = ctypes.byref(LinearDesc(M, N, K, lda, ldw, ldr, ldy, ldz, *codes))
     pa, pw = A.data_ptr(), W.data_ptr()
     need = 0
-    # (Operands whose rows start on 128-byte lines need no workspace.)
+    # (Operands whose rows start on 128-byte lines need no workspace: the library's promise.)
     if (pa | pw | (lda | ldw) * dt.itemsize) & 127:
         need = lib.tpgemm_linear_workspace_bytes(pa, pw, desc)
     _call(torch, index, lib.tpgemm_linear,
