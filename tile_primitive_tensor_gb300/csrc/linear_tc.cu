@@ -37,14 +37,23 @@ namespace {
 
 constexpr uint32_t kAtom = 8192;  // an operand stored along its rows: 64 K x 64 rows of 16 bits
 
+// Waits for a phase of `bar` for at most timeout_ns from when the previous grid has
+// ended: abort[1] is set once a thread of this CTA has passed the dependency. (The
+// check costs a wait nothing until it expires. With the dependency in every warp
+// before its first wait, a norm and its product took 15.0 us for 14.7: the MMA
+// warp's instructions came that much later.)
 __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, volatile int* abort,
                                              uint64_t timeout_ns, bool drain = false) {
     if (mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = globaltimer_ns();
+    uint64_t t0 = globaltimer_ns();
     while (true) {
         if (mbar_try_wait(bar, parity)) return true;
         if (!drain && *abort) return false;
         if (globaltimer_ns() - t0 > timeout_ns) {
+            if (!abort[1]) {
+                t0 = globaltimer_ns();
+                continue;
+            }
             *abort = 1;
             atomicExch(&g_linear_status, kStatusTimeout);
             return false;
@@ -339,7 +348,7 @@ struct TileSmem {
     uint8_t* bias;  // [epilogue warps][128] 16-bit bias of the warp's columns
     uint64_t *full, *empty, *acc_full, *acc_empty, *drain, *rbar;
     uint32_t* tmem_base;
-    volatile int* abort;
+    volatile int* abort;  // and [1], see wait_bounded
     volatile int* fills;  // after a timeout: the two producers' fills,
     volatile int* peer;   // and the other CTA's, [2] set once it has given up too
 };
@@ -359,7 +368,7 @@ __device__ __forceinline__ TileSmem carve_tile(uint8_t* raw, const TcLinear& p) 
     s.rbar = s.drain + 1;  // [epilogue warps][2] residual fills
     s.tmem_base = reinterpret_cast<uint32_t*>(s.rbar + 2 * kTileEpiWarps);
     s.abort = reinterpret_cast<volatile int*>(s.tmem_base + 1);
-    s.fills = s.abort + 1;
+    s.fills = s.abort + 2;
     s.peer = s.fills + 2;
     return s;
 }
@@ -431,7 +440,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
         mbar_init(s.drain, 1);
         for (int i = 0; i < 2 * kTileEpiWarps; ++i) mbar_init(&s.rbar[i], 1);
-        *s.abort = 0;
+        s.abort[0] = s.abort[1] = 0;
         s.peer[2] = 0;
         fence_mbarrier_init();
     }
@@ -465,7 +474,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             const int p0 = (2 * tp + rank) * 128;
             const int q0 = tq * p.bn + rank * q_rows;
             int kb = p.k_rotate ? int(int64_t(t) * nk / p.tiles) : 0;
-            if (t == cid) grid_dependency_wait();
+            if (t == cid) {
+                grid_dependency_wait();
+                s.abort[1] = 1;
+            }
             for (int i = 0; i < nk; ++i, turn ^= 1, kb = kb + 1 == nk ? 0 : kb + 1) {
                 if (turn == prod) {
                     if (!__all_sync(0xffffffffu, wait_bounded(&s.empty[stage], phase ^ 1u, s.abort, tmo))) {
@@ -488,7 +500,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
     }
     if (warp == 1 && rank == 0) {
-        grid_dependency_wait();  // no wait's bound runs while the previous grid does
         const uint64_t dP = smem_desc_with_addr(operand_desc(p.p_mn), smem_u32(s.stages));
         const uint64_t dQ = smem_desc_with_addr(operand_desc(p.q_mn), smem_u32(s.stages) + p.p_bytes);
         const uint64_t step_p = operand_step(p.p_mn), step_q = operand_step(p.q_mn);
@@ -750,7 +761,7 @@ struct SplitSmem {
     uint8_t* stages;  // then the partial sums
     uint64_t *full, *empty, *acc_full;
     uint32_t* tmem_base;
-    volatile int* abort;
+    volatile int* abort;  // and [1], see wait_bounded
 };
 
 __device__ __forceinline__ SplitSmem carve_split(uint8_t* raw, const TcLinear& p) {
@@ -942,7 +953,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
             mbar_init(&s.empty[i], 1);
         }
         mbar_init(s.acc_full, 1);
-        *s.abort = 0;
+        s.abort[0] = s.abort[1] = 0;
         fence_mbarrier_init();
     }
     if (warp == 1) {
@@ -974,6 +985,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
             }
         }
         grid_dependency_wait();
+        s.abort[1] = 1;
         int stage = 0;
         uint32_t phase = 0;
         for (int kb = kb0; kb < kb1; ++kb) {
@@ -991,7 +1003,6 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
             }
         }
     } else if (warp == 1) {
-        grid_dependency_wait();  // (as below)
         const uint64_t dP = smem_desc_with_addr(operand_desc(p.p_mn), smem_u32(s.stages));
         const uint64_t dQ = smem_desc_with_addr(operand_desc(p.q_mn), smem_u32(s.stages) + p.p_bytes);
         const uint64_t step_p = operand_step(p.p_mn), step_q = operand_step(p.q_mn);
@@ -1014,8 +1025,6 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
         }
         // Complete once every MMA issued is (also after a wait gave up).
         commit_elected(s.acc_full);
-    } else {
-        grid_dependency_wait();  // no wait's bound runs while the previous grid does
     }
     __syncwarp();
     // Every warp waits for the MMAs before it may read tensor memory, reuse the
@@ -1043,6 +1052,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
         __syncwarp();
         if (kSplit > 1) cluster_sync();
         else __syncthreads();
+        grid_dependency_wait();
         if (!*s.abort) join_lines<T, kSplit>(p, part, per, pitch, rank, rows, cols, m0, n0);
     };
     switch (p.split) {
