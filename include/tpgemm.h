@@ -521,9 +521,10 @@ typedef enum {
  * and bias are of `out` (f16, bf16 or f32). Sums are 32-bit (a sum over K of
  * random signs is within some 6e-10 K of its size; 16384: 9e-6) and each output
  * is rounded once; Y is computed from the unrounded Z. Activations are within half
- * of a 16-bit output's rounding; for 32-bit outputs silu and gelu_tanh are within
- * 2^-20 of themselves (negative z: |log2| of the small factor 2^-22 more, and 0 where
- * that factor is below 2^-126), gelu within 6e-8 and 4e-4 of itself, 5e-6 down to -3.
+ * of a 16-bit output's rounding. For 32-bit outputs silu and gelu_tanh are within
+ * 2^-20 of themselves (for negative z within 2^-22 |log2 f| more, f the factor of z,
+ * and 0 where f is below 2^-126), gelu within 6e-8 and within 4e-4 of itself (5e-6
+ * down to z = -3).
  */
 typedef struct {
     int64_t M, N, K;                 /* each below 2^30 */
@@ -590,7 +591,8 @@ size_t tpgemm_linear_backward_workspace_bytes(const void* dY, const void* A, con
  *     -127: the SFA of tpgemm_gemm_mx (dense Y). Larger values saturate.
  * A row (block) with an infinity or a NaN gets a NaN scale. Sums, H before its
  * rounding, and Y before its rounding are 32-bit; the exponent of an MX scale is
- * that of the unrounded Y, to twice as many bits where it is close.
+ * that of the exact product of H, gamma and the rstd that the 32-bit sum of squares
+ * gives (a maximum within some 1e-7 of a power of two may fall on either side).
  */
 typedef enum {
     TPGEMM_SCALE_NONE = 0,

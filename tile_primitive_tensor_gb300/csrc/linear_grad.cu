@@ -10,8 +10,9 @@
 // and end in dbias itself. dY and Z are read once and dZ is written once; with
 // an activation the bound is between memory and the instructions of its
 // derivative (about 24 an element): dbias of 8192 x 8192 bf16 34 us without one
-// (58 % of memory's rate), 65 with gelu. 64 registers, so that an SM has 32
-// warps, against 74 and 24: 90 us with gelu.
+// (58 % of memory's rate), 60 with silu, 64 with gelu, 67 with gelu_tanh. 64
+// registers, so that an SM has 32 warps, against 74 and 24: 90 us with gelu, though
+// bf16 spills 48 bytes a thread so (f16 none).
 #include <algorithm>
 
 #include "column_sum.cuh"

@@ -336,7 +336,10 @@ __device__ __forceinline__ void apply_columns(float v, float (&x)[32]) {
 // and TMA stores; the residual comes in the same way, ahead of its use. Stores
 // straight from registers, 16 bytes to each of 32 rows, occupy the load/store
 // path for 32 cycles an instruction, and those of single elements as long: the
-// other outputs are turned first (2048 x 4099 x 2048 bf16: 86 -> 28 us).
+// other outputs are turned first (2048 x 4099 x 2048 bf16: 86 -> 28 us). With Z and a
+// residual the buffers hold Z and Y, and the residual is read that way, 16 bytes to
+// each of 32 rows (4096^3 bf16 with gelu: plain 78.2 us, Z 80.1, residual 80.4, both
+// 84.2).
 constexpr int kTileThreads = 384;
 constexpr int kTileEpiWarps = 8;
 constexpr int kStaging = 4096;  // staging bytes of an epilogue warp

@@ -178,9 +178,11 @@ __device__ __forceinline__ void team_max(uint32_t& b, float2* s) {
     }
 }
 
-// A block's maximum within a few units of a power of two: its scale hangs on
-// roundings of 32-bit arithmetic (one block in 10^6), so the power is compared
-// with |h rstd gamma| to twice as many bits.
+// A block's maximum within a few units of a power of two: its scale hangs on the
+// roundings of rstd and of two products (one block in 10^6), so the power is
+// compared with |h rstd gamma| to twice as many bits, rstd that of the 32-bit sum of
+// squares. What that sum is off by (some 1e-7 of it) still decides one block in
+// 2 x 10^7.
 __device__ __forceinline__ bool near_power(uint32_t amax) {
     return ((amax + 8u) & 0x7fffffu) < 16u && amax >= 0x10000000u && amax < 0x70000000u;
 }
@@ -268,7 +270,7 @@ __device__ __forceinline__ bool store_y(const RmsNormOp& op, int64_t row, const 
 
 // Writes a block near a power of two again, by four lanes: the power in doubt is
 // compared exactly. It comes after the row's stores, when registers are free
-// (8192 x 8192 bf16: 87 us without it, 90 so, 110 in their midst).
+// (8192 x 8192 bf16: 88 us so, 89 without it, 110 in their midst).
 template <typename XT>
 __device__ __forceinline__ void settle_block(const RmsNormOp& op, int64_t row, const Cols<true>& c,
                                              const float (&h)[8], float sum) {
@@ -659,11 +661,12 @@ cudaError_t launch_norm(const RmsNormOp& op, cudaStream_t stream) {
     if constexpr (VEC && (MODE == TPGEMM_SCALE_NONE || (MODE == TPGEMM_SCALE_MX && sizeof(XT) == 2))) {
         // Teams of 512 threads and more leave an SM two rows or one, too few to
         // hide each other's reductions: such rows are loaded ahead (bf16 with
-        // residual, MX scales: 8192 x 8192 92 -> 87 us; no scales: 2048 x
-        // 16384 55.3 -> 46.2 us; f32 8192 x 8192 179 -> 182, 98 -> 94 without
-        // residual, 2048 x 16384 61 -> 55 so). Not with row scales, whose maxima
-        // take the registers (bf16 89.1 -> 91.6), nor f32 rows with MX scales, which
-        // would spill (140 -> 186), nor narrower rows (8192 x 4096 44.0 -> 46.4).
+        // residual, MX scales: 8192 x 8192 97 -> 88 us; no scales: 2048 x
+        // 16384 55.9 -> 46.3 us; f32 8192 x 8192 179 -> 182, 98 -> 94 without
+        // residual, 2048 x 16384 61 -> 55 so). Not with row scales, where it gains
+        // nothing (bf16 90.5 either way, 2048 x 16384 55.3), nor f32 rows with MX
+        // scales, which would spill (140 -> 186), nor narrower rows (8192 x 4096
+        // 44.0 -> 46.4).
         if (s.v == 2 && s.team >= 512) {
             fn = rmsnorm_kernel<XT, 2, VEC, false, MODE, true>;
             blocks = std::min(blocks, int64_t(kSms) * (kMaxTeam / s.team));
