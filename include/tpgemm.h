@@ -484,9 +484,10 @@ tpgemm_status tpgemm_vcopy_roundtrip(void* dst, const void* src, size_t buffer_b
 
 /*
  * ------------------------------------------------------------------------
- * The operators around the multiply: the linear layer with its epilogue, its
- * gradients, the root-mean-square norm and its gradients. (Not on the pages:
- * what a network computes right before and right after the multiply.)
+ * The operators around the multiply: the linear layer with its epilogue and its
+ * gated form, the root-mean-square norm, the layer norm, dropout, and their
+ * gradients. (Not on the pages: what a network computes right before and right
+ * after the multiply.)
  *
  * Matrices here are row-major with unit column stride and a row stride in
  * elements (0 = dense, else at least the columns), so slices of wider buffers
@@ -638,6 +639,88 @@ tpgemm_status tpgemm_rmsnorm_backward(void* dX, void* dgamma, const void* dY, co
 /* Bytes of workspace tpgemm_rmsnorm_backward needs, where dgamma is wanted, for
  * its partial sums, 256-byte aligned. (None is read where dgamma is NULL.) */
 size_t tpgemm_rmsnorm_backward_workspace_bytes(int64_t rows, int64_t cols);
+
+/*
+ * Dropout: an element x becomes x / (1 - p) (in 32 bits) or, with probability p,
+ * 0 whatever it was. Which one depends on the seed, the offset and the element's
+ * row i and column j alone: word j % 4 of Philox4x32-10 with the counter
+ * (j / 4, i, offset low, offset high) and the key (seed low, seed high), each of 32
+ * bits, is compared with round(p 2^32); at least that keeps the element. So no mask
+ * is stored, and a backward pass with the same numbers draws the same one.
+ */
+typedef struct {
+    double p;                /* in [0, 1); 0 keeps everything */
+    uint64_t seed, offset;
+    const uint64_t* counter; /* one number in device memory, 8-byte aligned, added to offset
+                                when the work runs (so that a captured graph can draw anew);
+                                or NULL */
+} tpgemm_drop;
+
+typedef struct {
+    int64_t rows, cols;    /* each below 2^30 */
+    int64_t ldx, ldr, ldy; /* row strides */
+    tpgemm_elem x;
+    tpgemm_drop drop;
+} tpgemm_dropout_desc;
+
+/* Y = drop(X) + R, all of `x` (f16, bf16 or f32). R may be NULL (zero); Y may be X
+ * or R itself (same address and row stride). The gradient of X is drop(dY) with the
+ * same numbers, that of R is dY. */
+tpgemm_status tpgemm_dropout(void* Y, const void* X, const void* R, const tpgemm_dropout_desc* d,
+                             void* stream);
+
+/*
+ * Layer norm of each row, after dropout and the residual's addition:
+ *   H = drop(X) + R,  mean[i] = mean_j H[i, j],
+ *   rstd[i] = 1 / sqrt(mean_j (H[i, j] - mean[i])^2 + eps),
+ *   Y[i, j] = (H[i, j] - mean[i]) rstd[i] gamma[j] + beta[j].
+ * X, R and H are of `x` (f16, bf16 or f32), gamma and beta [cols] of `gamma` (`x` or
+ * f32). Y is of `y`: f16, bf16 or f32 with TPGEMM_SCALE_NONE, or e4m3 / e5m2 as
+ * Y / scale with TPGEMM_SCALE_ROW, scale as for tpgemm_rmsnorm. (TPGEMM_SCALE_MX
+ * is not taken.) Sums, H before its rounding, and Y before its rounding are 32-bit.
+ */
+typedef struct {
+    int64_t rows, cols;          /* rows >= 0, cols >= 1, each below 2^30 */
+    int64_t ldx, ldr, ldh, ldy;  /* row strides */
+    tpgemm_elem x, gamma, y;
+    tpgemm_scale_mode scale;
+    float eps;
+    tpgemm_drop drop;            /* of X; p = 0: none */
+} tpgemm_layernorm_desc;
+
+/* R and beta may be NULL (zero); H, mean [rows] and rstd [rows] may be NULL (not
+ * stored). H may be X or R itself (same address and row stride), and Y may be X or R
+ * itself when they have one type and H is NULL. */
+tpgemm_status tpgemm_layernorm(void* Y, void* H, float* scale, float* mean, float* rstd,
+                               const void* X, const void* R, const void* gamma, const void* beta,
+                               const tpgemm_layernorm_desc* d, void* stream);
+
+/*
+ * Gradients of the layer norm, n = (H - mean) rstd, w = dY gamma:
+ *   dR[i, j] = rstd[i] (w[i, j] - mean_j(w) - n[i, j] mean_j(w n)) + dH[i, j]
+ *   dX = drop(dR)
+ *   dgamma[j] = sum_i dY[i, j] n[i, j],  dbeta[j] = sum_i dY[i, j].
+ * dY, H, dH, dX and dR are of `x`; dgamma and dbeta [cols] of `grad` (f16, bf16 or
+ * f32). dH (the gradient that reaches H past the norm) may be NULL; each output may
+ * be NULL when not wanted. dX and dR may each be dY, H or dH itself (same address
+ * and row stride).
+ */
+typedef struct {
+    int64_t rows, cols;
+    int64_t lddy, ldh, lddh, lddx, lddr; /* row strides */
+    tpgemm_elem x, gamma, grad;
+    tpgemm_drop drop;
+} tpgemm_layernorm_grad_desc;
+
+tpgemm_status tpgemm_layernorm_backward(void* dX, void* dR, void* dgamma, void* dbeta,
+                                        const void* dY, const void* H, const float* mean,
+                                        const float* rstd, const void* gamma, const void* dH,
+                                        const tpgemm_layernorm_grad_desc* d, void* workspace,
+                                        size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace tpgemm_layernorm_backward needs, where dgamma or dbeta is
+ * wanted, for its partial sums, 256-byte aligned. (Else none is read.) */
+size_t tpgemm_layernorm_backward_workspace_bytes(int64_t rows, int64_t cols);
 
 /* Static English name of a status. Never NULL. */
 const char* tpgemm_status_string(tpgemm_status s);

@@ -116,6 +116,30 @@ class RmsNormGradDesc(ctypes.Structure):
         [(n, ctypes.c_int) for n in ("x", "gamma", "grad")]
 
 
+class Drop(ctypes.Structure):
+    """tpgemm_drop: probability, seed, offset and the device address of a counter (or None)."""
+    _fields_ = [("p", ctypes.c_double), ("seed", ctypes.c_uint64), ("offset", ctypes.c_uint64),
+                ("counter", ctypes.c_void_p)]
+
+
+class DropoutDesc(ctypes.Structure):
+    """tpgemm_dropout_desc: sizes, row strides, type and random numbers of a dropout."""
+    _fields_ = [(n, ctypes.c_int64) for n in ("rows", "cols", "ldx", "ldr", "ldy")] + \
+        [("x", ctypes.c_int), ("drop", Drop)]
+
+
+class LayerNormDesc(ctypes.Structure):
+    """tpgemm_layernorm_desc: as RmsNormDesc, and the dropout before the norm."""
+    _fields_ = RmsNormDesc._fields_ + [("drop", Drop)]
+
+
+class LayerNormGradDesc(ctypes.Structure):
+    """tpgemm_layernorm_grad_desc: as LayerNormDesc, for the gradients."""
+    _fields_ = [(n, ctypes.c_int64)
+                for n in ("rows", "cols", "lddy", "ldh", "lddh", "lddx", "lddr")] + \
+        [(n, ctypes.c_int) for n in ("x", "gamma", "grad")] + [("drop", Drop)]
+
+
 class CpDesc(ctypes.Structure):
     """tpgemm_cp_desc: a shared-memory region and where its rows go in tensor memory."""
     _fields_ = [("rows", ctypes.c_int), ("row_bits", ctypes.c_int), ("swizzle", ctypes.c_int),
@@ -197,6 +221,14 @@ def _open(path):
     lib.tpgemm_rmsnorm_backward.restype = ci
     lib.tpgemm_rmsnorm_backward_workspace_bytes.argtypes = [i64, i64]
     lib.tpgemm_rmsnorm_backward_workspace_bytes.restype = sz
+    lib.tpgemm_dropout.argtypes = [vp] * 3 + [ctypes.POINTER(DropoutDesc), vp]
+    lib.tpgemm_dropout.restype = ci
+    lib.tpgemm_layernorm.argtypes = [vp] * 9 + [ctypes.POINTER(LayerNormDesc), vp]
+    lib.tpgemm_layernorm.restype = ci
+    lib.tpgemm_layernorm_backward.argtypes = [vp] * 10 + [ctypes.POINTER(LayerNormGradDesc), vp, sz, vp]
+    lib.tpgemm_layernorm_backward.restype = ci
+    lib.tpgemm_layernorm_backward_workspace_bytes.argtypes = [i64, i64]
+    lib.tpgemm_layernorm_backward_workspace_bytes.restype = sz
     lib.tpgemm_version.argtypes = []
     lib.tpgemm_version.restype = ctypes.c_char_p
     lib.tpgemm_cp_parse_shape.argtypes = [ctypes.c_char_p, ctypes.POINTER(ci)]
@@ -589,6 +621,35 @@ def tpgemm_rmsnorm_backward_workspace_bytes(rows, cols) -> int:
     return int(_load().tpgemm_rmsnorm_backward_workspace_bytes(int(rows), int(cols)))
 
 
+def tpgemm_dropout(Y, X, R, desc: DropoutDesc, stream=None) -> int:
+    """Enqueue Y = drop(X) + R; returns the tpgemm_status code."""
+    return int(_load().tpgemm_dropout(_ptr(Y), _ptr(X), _ptr(R), ctypes.byref(desc),
+                                      _stream(stream)))
+
+
+def tpgemm_layernorm(Y, H, scale, mean, rstd, X, R, gamma, beta, desc: LayerNormDesc,
+                     stream=None) -> int:
+    """Enqueue a layer norm; returns the tpgemm_status code."""
+    return int(_load().tpgemm_layernorm(_ptr(Y), _ptr(H), _ptr(scale), _ptr(mean), _ptr(rstd),
+                                        _ptr(X), _ptr(R), _ptr(gamma), _ptr(beta),
+                                        ctypes.byref(desc), _stream(stream)))
+
+
+def tpgemm_layernorm_backward(dX, dR, dgamma, dbeta, dY, H, mean, rstd, gamma, dH,
+                              desc: LayerNormGradDesc, workspace=None, workspace_bytes=0,
+                              stream=None) -> int:
+    """Enqueue the gradients of a layer norm; returns the tpgemm_status code."""
+    return int(_load().tpgemm_layernorm_backward(_ptr(dX), _ptr(dR), _ptr(dgamma), _ptr(dbeta),
+                                                 _ptr(dY), _ptr(H), _ptr(mean), _ptr(rstd),
+                                                 _ptr(gamma), _ptr(dH), ctypes.byref(desc),
+                                                 _ptr(workspace), int(workspace_bytes),
+                                                 _stream(stream)))
+
+
+def tpgemm_layernorm_backward_workspace_bytes(rows, cols) -> int:
+    return int(_load().tpgemm_layernorm_backward_workspace_bytes(int(rows), int(cols)))
+
+
 _ACTS = {"none": TPGEMM_ACT_NONE, "relu": TPGEMM_ACT_RELU, "silu": TPGEMM_ACT_SILU,
          "gelu": TPGEMM_ACT_GELU, "gelu_tanh": TPGEMM_ACT_GELU_TANH}
 _SCALES = {None: TPGEMM_SCALE_NONE, "row": TPGEMM_SCALE_ROW, "mx": TPGEMM_SCALE_MX}
@@ -920,3 +981,195 @@ def rmsnorm_backward(dy, h, rstd, weight, dh=None, *, grad_dtype=None, need=(Tru
           (pdx, pdw, dy.data_ptr(), h.data_ptr(), prstd, pg, pdh, ctypes.byref(desc)), workspace,
           scratch)
     return dx, dweight
+
+
+class Dropout(typing.NamedTuple):
+    """A dropout's numbers. The mask is a function of these and of each element's row and column
+    (Philox4x32-10, see include/tpgemm.h), so the backward pass is given the same ones."""
+    p: float          # probability to drop an element, in [0, 1)
+    seed: int         # below 2^64
+    offset: object = 0  # below 2^64, or a CUDA int64 tensor of one element, read when the work runs
+
+
+def _drop(d, index) -> Drop:
+    """The tpgemm_drop of a Dropout (or of None: nothing is dropped)."""
+    if d is None:
+        return Drop()
+    p, seed, offset = d
+    counter = None
+    if not isinstance(offset, int):
+        torch = _torch or _import_torch()
+        if not isinstance(offset, torch.Tensor):
+            raise TypeError(f"offset must be an int or a tensor, got {type(offset).__name__}")
+        if offset.dtype is not torch.int64 or offset.numel() != 1 or offset.get_device() != index:
+            raise ValueError(f"offset must be an int64 tensor of one element on cuda:{index}")
+        offset, counter = 0, offset.data_ptr()
+    if not 0 <= seed < 1 << 64 or not 0 <= offset < 1 << 64:
+        raise ValueError("seed and offset must be at least 0 and below 2^64")
+    return Drop(p, seed, offset, counter)
+
+
+def dropout(x, drop, residual=None, *, out=None, stream=None):
+    """y = x / (1 - p) where it is kept and 0 where it is dropped, plus residual; returns y.
+
+    x, residual and y [rows, cols] are float16, bfloat16 or float32; drop is a Dropout. ``out`` may
+    be x or residual itself. stream: as for linear."""
+    if stream is not None:
+        with _current(stream, x):
+            return dropout(x, drop, residual, out=out)
+    torch = _torch or _import_torch()
+    lib = _lib or _load()
+    rows, cols, index, device = _sizes("x", x)
+    dt = x.dtype
+    ldx = _matrix("x", x, rows, cols, dt, index)
+    code = elem_code(dt)
+    pr, ldr = None, 0
+    if residual is not None:
+        ldr, pr = _matrix("residual", residual, rows, cols, dt, index), residual.data_ptr()
+    if out is None:
+        out, ldy = torch.empty((rows, cols), dtype=dt, device=device), cols
+    else:
+        ldy = _matrix("out", out, rows, cols, dt, index)
+    desc = DropoutDesc(rows, cols, ldx, ldr, ldy, code, _drop(drop, index))
+    _call(torch, index, lib.tpgemm_dropout,
+          (out.data_ptr(), x.data_ptr(), pr, ctypes.byref(desc)))
+    return out
+
+
+def dropout_backward(dy, drop, *, out=None, stream=None):
+    """The gradient of dropout's x, given that of y and the same Dropout (the residual's is dy).
+    ``out`` may be dy itself. stream: as for linear."""
+    return dropout(dy, drop, out=out, stream=stream)
+
+
+class LayerNorm(typing.NamedTuple):
+    """What layernorm returns; what was not asked for is None."""
+    y: object
+    h: object      # dropout(x) + residual
+    scale: object  # float32 [rows] ("row")
+    mean: object   # float32 [rows]
+    rstd: object   # float32 [rows]
+
+
+def layernorm(x, weight, bias=None, residual=None, *, eps=1e-5, dropout=None, quant=None,
+              out_dtype=None, need_stats=False, out=None, out_h=None, stream=None):
+    """Layer norm of the rows of h = dropout(x) + residual:
+    y = (h - mean(h)) / sqrt(var(h) + eps) weight + bias.
+
+    x, residual and h [rows, cols] are float16, bfloat16 or float32; weight and bias [cols] are of
+    x's type or both float32; dropout is a Dropout or None. y is of out_dtype: a float type (by
+    default x's), or with quant="row" (one float32 scale per row, linear's scale_a) float8_e4m3fn
+    (the default) or float8_e5m2, holding y / scale. h is returned with a residual or a dropout
+    only; it may be written in place (out_h = x or residual). need_stats: mean and rstd are
+    returned, for layernorm_backward. stream: as for linear."""
+    if stream is not None:
+        with _current(stream, x):
+            return layernorm(x, weight, bias, residual, eps=eps, dropout=dropout, quant=quant,
+                             out_dtype=out_dtype, need_stats=need_stats, out=out, out_h=out_h)
+    torch = _torch or _import_torch()
+    lib = _lib or _load()
+    rows, cols, index, device = _sizes("x", x)
+    dt = x.dtype
+    if quant not in (None, "row"):
+        raise ValueError(f"quant must be None or 'row', got {quant!r}")
+    if out_dtype is None:
+        out_dtype = out.dtype if out is not None else (dt if quant is None else torch.float8_e4m3fn)
+    wt = weight.dtype
+    if wt is not dt and wt is not torch.float32:
+        raise TypeError(f"weight must be {dt} or float32, got {wt}")
+    pg = _vector("weight", weight, cols, wt, index)
+    pb = None if bias is None else _vector("bias", bias, cols, wt, index)
+    ldx = _matrix("x", x, rows, cols, dt, index)
+    codes = elem_code(dt), elem_code(wt), elem_code(out_dtype), _SCALES[quant]
+    if out is None:
+        out, ldy = torch.empty((rows, cols), dtype=out_dtype, device=device), cols
+    else:
+        ldy = _matrix("out", out, rows, cols, out_dtype, index)
+    h = scale = mean = rstd = pr = ph = ps = pm = prstd = None
+    ldr = ldh = 0
+    if residual is not None:
+        ldr, pr = _matrix("residual", residual, rows, cols, dt, index), residual.data_ptr()
+    if residual is not None or dropout is not None:
+        if out_h is None:
+            h, ldh = torch.empty((rows, cols), dtype=dt, device=device), cols
+        else:
+            h, ldh = out_h, _matrix("out_h", out_h, rows, cols, dt, index)
+        ph = h.data_ptr()
+    elif out_h is not None:
+        raise ValueError("out_h needs a residual or a dropout (h is x without them)")
+    if quant == "row":
+        scale = torch.empty(rows, dtype=torch.float32, device=device)
+        ps = scale.data_ptr()
+    if need_stats:
+        mean, rstd = torch.empty((2, rows), dtype=torch.float32, device=device)
+        pm, prstd = mean.data_ptr(), rstd.data_ptr()
+    desc = LayerNormDesc(rows, cols, ldx, ldr, ldh, ldy, *codes, eps, _drop(dropout, index))
+    _call(torch, index, lib.tpgemm_layernorm,
+          (out.data_ptr(), ph, ps, pm, prstd, x.data_ptr(), pr, pg, pb, ctypes.byref(desc)))
+    return LayerNorm(out, h, scale, mean, rstd)
+
+
+class LayerNormGrad(typing.NamedTuple):
+    """What layernorm_backward returns; what was not asked for is None."""
+    dx: object
+    dresidual: object  # dx itself without a dropout
+    dweight: object
+    dbias: object
+
+
+def layernorm_backward(dy, h, mean, rstd, weight, dh=None, *, dropout=None, grad_dtype=None,
+                       need=(True, True, True, True), out=None, workspace=None, stream=None):
+    """The gradients of a layer norm, given dy, the normalised rows' h, mean and rstd, the gradient
+    dh that reaches h past the norm (or None), and the Dropout of the forward pass.
+
+    dy, h, dh, dx and dresidual [rows, cols] are of one type (float16, bfloat16 or float32),
+    dweight and dbias of grad_dtype (by default weight's). ``need`` says which of dx, dresidual,
+    dweight and dbias are wanted; ``out`` (of dx, or of both without a dropout) may be dy, h or dh.
+    stream: as for linear."""
+    if stream is not None:
+        with _current(stream, dy):
+            return layernorm_backward(dy, h, mean, rstd, weight, dh, dropout=dropout,
+                                      grad_dtype=grad_dtype, need=need, out=out,
+                                      workspace=workspace)
+    torch = _torch or _import_torch()
+    lib = _lib or _load()
+    rows, cols, index, device = _sizes("dy", dy)
+    dt, wt = dy.dtype, weight.dtype
+    grad_dtype = wt if grad_dtype is None else grad_dtype
+    if wt is not dt and wt is not torch.float32:
+        raise TypeError(f"weight must be {dt} or float32, got {wt}")
+    pg = _vector("weight", weight, cols, wt, index)
+    pm = _vector("mean", mean, rows, torch.float32, index)
+    prstd = _vector("rstd", rstd, rows, torch.float32, index)
+    dx = dr = pdh = pdx = pdr = pdw = pdb = dweight = dbias = None
+    lddh = lddx = lddr = scratch = 0
+    if dh is not None:
+        lddh, pdh = _matrix("dh", dh, rows, cols, dt, index), dh.data_ptr()
+    apart = dropout is not None
+    if need[0] or (need[1] and not apart):
+        if out is None:
+            dx, lddx = torch.empty((rows, cols), dtype=dt, device=device), cols
+        else:
+            dx, lddx = out, _matrix("out", out, rows, cols, dt, index)
+        pdx = dx.data_ptr()
+    if need[1] and apart:
+        dr, lddr = torch.empty((rows, cols), dtype=dt, device=device), cols
+        pdr = dr.data_ptr()
+    if need[2]:
+        dweight = torch.empty(cols, dtype=grad_dtype, device=device)
+        pdw = dweight.data_ptr()
+    if need[3]:
+        dbias = torch.empty(cols, dtype=grad_dtype, device=device)
+        pdb = dbias.data_ptr()
+    if need[2] or need[3]:
+        scratch = lib.tpgemm_layernorm_backward_workspace_bytes(rows, cols)
+    desc = LayerNormGradDesc(rows, cols, _matrix("dy", dy, rows, cols, dt, index),
+                             _matrix("h", h, rows, cols, dt, index), lddh, lddx, lddr, elem_code(dt),
+                             elem_code(wt), elem_code(grad_dtype), _drop(dropout, index))
+    _call(torch, index, lib.tpgemm_layernorm_backward,
+          (pdx, pdr, pdw, pdb, dy.data_ptr(), h.data_ptr(), pm, prstd, pg, pdh, ctypes.byref(desc)),
+          workspace, scratch)
+    if not apart:
+        dr = dx if need[1] else None
+        dx = dx if need[0] else None
+    return LayerNormGrad(dx, dr, dweight, dbias)

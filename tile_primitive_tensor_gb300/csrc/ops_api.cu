@@ -1,6 +1,7 @@
 // C-ABI entry points of the operators around the multiply: argument checks,
 // the choice of kernels, and their launches on the caller's stream.
 #include <algorithm>
+#include <cmath>
 
 #include "ops_internal.h"
 #include "tpgemm_internal.h"
@@ -276,6 +277,27 @@ tpgemm_status check_linear_grad_desc(const tpgemm_linear_grad_desc* d) {
     return check_act(d->act);
 }
 
+// Dropout's numbers; `in` gets the counter's place, for the overlap check.
+tpgemm_status check_drop(const tpgemm_drop& d, tpg::Drop* drop, Mat* in) {
+    *in = {"counter", nullptr, 1, 8, 8, TPGEMM_ELEM_E4M3};
+    *drop = {};
+    if (!(d.p >= 0.0 && d.p < 1.0))
+        return fail_with(TPGEMM_ERR_SHAPE, "p=%g must be at least 0 and below 1", d.p);
+    if (d.p == 0.0) return TPGEMM_OK;
+    if (reinterpret_cast<uintptr_t>(d.counter) % 8)
+        return fail_with(TPGEMM_ERR_ALIGN, "counter=%p is not 8-byte aligned",
+                         static_cast<const void*>(d.counter));
+    in->p = d.counter;
+    const double t = std::nearbyint(d.p * 4294967296.0);
+    *drop = {d.seed, d.offset, d.counter, t < 4294967295.0 ? uint32_t(t) : 0xffffffffu,
+             float(1.0 / (1.0 - d.p)), 1};
+    return TPGEMM_OK;
+}
+
+size_t layernorm_grad_ws(int64_t rows, int64_t cols) {
+    return align_up(size_t(tpg::layernorm_grad_strips(rows, cols)) * size_t(cols) * 8, 256);
+}
+
 size_t rmsnorm_grad_ws(int64_t rows, int64_t cols) {
     return align_up(size_t(tpg::rmsnorm_grad_strips(rows, cols)) * size_t(cols) * 4, 256);
 }
@@ -511,6 +533,137 @@ tpgemm_status tpgemm_rmsnorm_backward(void* dX, void* dgamma, const void* dY, co
                           static_cast<float*>(workspace), in[0].ld, in[1].ld, in[2].ld, out[0].ld,
                           d->x, d->gamma, d->grad};
     return launched(tpg::launch_rmsnorm_grad(op, st), "norm gradient launch");
+}
+
+tpgemm_status tpgemm_dropout(void* Y, const void* X, const void* R, const tpgemm_dropout_desc* d,
+                             void* stream) {
+    tpg::set_error_detail("");
+    if (!d) return fail_with(TPGEMM_ERR_NULL, "the description is NULL");
+    TPG_TRY(check_dim("rows", d->rows, 0));
+    TPG_TRY(check_dim("cols", d->cols, 0));
+    if (!is_float(d->x)) return fail_with(TPGEMM_ERR_DTYPE, "X must be f16, bf16 or f32 (%d)", int(d->x));
+    tpg::Drop drop;
+    Mat counter;
+    TPG_TRY(check_drop(d->drop, &drop, &counter));
+    const int64_t rows = d->rows, cols = d->cols;
+    if (rows == 0 || cols == 0) return TPGEMM_OK;
+    Mat out[1] = {{"Y", Y, rows, cols, dense(d->ldy, cols), d->x}};
+    Mat in[3] = {{"X", X, rows, cols, dense(d->ldx, cols), d->x},
+                 {"R", R, rows, cols, dense(d->ldr, cols), d->x},
+                 counter};
+    TPG_TRY(check_mat(out[0], true));
+    TPG_TRY(check_mat(in[0], true));
+    TPG_TRY(check_mat(in[1], false));
+    const Pair pairs[2] = {{0, 0}, {0, 1}};
+    TPG_TRY(check_overlap(out, 1, in, 3, pairs, 2));
+    int sms = 0;
+    TPG_TRY(tpg::require_device(&sms));
+    const tpg::DropoutOp op{rows, cols, X, R, Y, in[0].ld, in[1].ld, out[0].ld, d->x, drop};
+    return launched(tpg::launch_dropout(op, static_cast<cudaStream_t>(stream)), "dropout launch");
+}
+
+tpgemm_status tpgemm_layernorm(void* Y, void* H, float* scale, float* mean, float* rstd,
+                               const void* X, const void* R, const void* gamma, const void* beta,
+                               const tpgemm_layernorm_desc* d, void* stream) {
+    tpg::set_error_detail("");
+    if (!d) return fail_with(TPGEMM_ERR_NULL, "the description is NULL");
+    TPG_TRY(check_dim("rows", d->rows, 0));
+    TPG_TRY(check_dim("cols", d->cols, 1));
+    if (!is_float(d->x)) return fail_with(TPGEMM_ERR_DTYPE, "X must be f16, bf16 or f32 (%d)", int(d->x));
+    if (d->gamma != d->x && d->gamma != TPGEMM_ELEM_F32)
+        return fail_with(TPGEMM_ERR_DTYPE, "gamma and beta must be of X's type or f32 (%d)", int(d->gamma));
+    if (d->scale != TPGEMM_SCALE_NONE && d->scale != TPGEMM_SCALE_ROW)
+        return fail_with(TPGEMM_ERR_DTYPE, "scale mode %d must be none or row", int(d->scale));
+    const bool row = d->scale == TPGEMM_SCALE_ROW;
+    if (row ? !is_fp8(d->y) : !is_float(d->y))
+        return fail_with(TPGEMM_ERR_DTYPE,
+                         "Y must be f16, bf16 or f32 without scales and e4m3 or e5m2 with them (%d)",
+                         int(d->y));
+    if (!(d->eps >= 0.f))
+        return fail_with(TPGEMM_ERR_SHAPE, "eps=%g must not be negative", double(d->eps));
+    tpg::Drop drop;
+    Mat counter;
+    TPG_TRY(check_drop(d->drop, &drop, &counter));
+    const int64_t rows = d->rows, cols = d->cols;
+    if (rows == 0) return TPGEMM_OK;
+    Mat out[5] = {{"Y", Y, rows, cols, dense(d->ldy, cols), d->y},
+                  {"H", H, rows, cols, dense(d->ldh, cols), d->x},
+                  vec("scale", row ? scale : nullptr, rows, TPGEMM_ELEM_F32),
+                  vec("mean", mean, rows, TPGEMM_ELEM_F32),
+                  vec("rstd", rstd, rows, TPGEMM_ELEM_F32)};
+    Mat in[5] = {{"X", X, rows, cols, dense(d->ldx, cols), d->x},
+                 {"R", R, rows, cols, dense(d->ldr, cols), d->x},
+                 vec("gamma", gamma, cols, d->gamma),
+                 vec("beta", beta, cols, d->gamma),
+                 counter};
+    for (int i = 0; i < 5; ++i) TPG_TRY(check_mat(out[i], i == 0 || (i == 2 && row)));
+    for (int i = 0; i < 5; ++i) TPG_TRY(check_mat(in[i], i == 0 || i == 2));
+    const Pair pairs[4] = {{1, 0}, {1, 1}, {0, 0}, {0, 1}};
+    TPG_TRY(check_overlap(out, 5, in, 5, pairs, H ? 2 : 4));
+    int sms = 0;
+    TPG_TRY(tpg::require_device(&sms));
+    const tpg::LayerNormOp op{rows, cols, X, R, gamma, beta, H, Y, scale, mean, rstd, in[0].ld, in[1].ld,
+                              out[1].ld, out[0].ld, d->x, d->gamma, d->y, d->scale, d->eps, drop};
+    return launched(tpg::launch_layernorm(op, static_cast<cudaStream_t>(stream)), "layer norm launch");
+}
+
+size_t tpgemm_layernorm_backward_workspace_bytes(int64_t rows, int64_t cols) {
+    if (rows <= 0 || cols <= 0 || rows >= kMaxDim || cols >= kMaxDim) return 0;
+    return layernorm_grad_ws(rows, cols);
+}
+
+tpgemm_status tpgemm_layernorm_backward(void* dX, void* dR, void* dgamma, void* dbeta,
+                                        const void* dY, const void* H, const float* mean,
+                                        const float* rstd, const void* gamma, const void* dH,
+                                        const tpgemm_layernorm_grad_desc* d, void* workspace,
+                                        size_t workspace_bytes, void* stream) {
+    tpg::set_error_detail("");
+    if (!d) return fail_with(TPGEMM_ERR_NULL, "the description is NULL");
+    TPG_TRY(check_dim("rows", d->rows, 0));
+    TPG_TRY(check_dim("cols", d->cols, 1));
+    if (!is_float(d->x)) return fail_with(TPGEMM_ERR_DTYPE, "dY must be f16, bf16 or f32 (%d)", int(d->x));
+    if (d->gamma != d->x && d->gamma != TPGEMM_ELEM_F32)
+        return fail_with(TPGEMM_ERR_DTYPE, "gamma must be of dY's type or f32 (%d)", int(d->gamma));
+    if (!is_float(d->grad))
+        return fail_with(TPGEMM_ERR_DTYPE, "dgamma and dbeta must be f16, bf16 or f32 (%d)", int(d->grad));
+    tpg::Drop drop;
+    Mat counter;
+    TPG_TRY(check_drop(d->drop, &drop, &counter));
+    const int64_t rows = d->rows, cols = d->cols;
+    const bool by_row = dX || dR, by_col = dgamma || dbeta;
+    Mat out[4] = {{"dX", dX, rows, cols, dense(d->lddx, cols), d->x},
+                  {"dR", dR, rows, cols, dense(d->lddr, cols), d->x},
+                  vec("dgamma", dgamma, cols, d->grad),
+                  vec("dbeta", dbeta, cols, d->grad)};
+    Mat in[7] = {{"dY", dY, rows, cols, dense(d->lddy, cols), d->x},
+                 {"H", H, rows, cols, dense(d->ldh, cols), d->x},
+                 {"dH", dH, rows, cols, dense(d->lddh, cols), d->x},
+                 vec("mean", mean, rows, TPGEMM_ELEM_F32),
+                 vec("rstd", rstd, rows, TPGEMM_ELEM_F32),
+                 vec("gamma", gamma, cols, d->gamma),
+                 counter};
+    for (Mat& m : out) TPG_TRY(check_mat(m, false));
+    for (int i = 0; i < 7; ++i)
+        TPG_TRY(check_mat(in[i], (by_row || by_col) && rows > 0 && i != 2 && i != 6 && (i != 5 || by_row)));
+    const Pair pairs[6] = {{0, 0}, {0, 1}, {0, 2}, {1, 0}, {1, 1}, {1, 2}};
+    TPG_TRY(check_overlap(out, 4, in, 7, pairs, 6));
+    const Mat all[11] = {out[0], out[1], out[2], out[3], in[0], in[1], in[2], in[3], in[4], in[5], in[6]};
+    if (by_col && rows > 0)
+        TPG_TRY(check_workspace(workspace, workspace_bytes, layernorm_grad_ws(rows, cols), all, 11));
+    int sms = 0;
+    TPG_TRY(tpg::require_device(&sms));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (rows == 0) {
+        const size_t bytes = size_t(cols) * size_t(elem_size(d->grad));
+        if (dgamma) TPG_TRY(launched(cudaMemsetAsync(dgamma, 0, bytes, st), "zero dgamma"));
+        if (dbeta) TPG_TRY(launched(cudaMemsetAsync(dbeta, 0, bytes, st), "zero dbeta"));
+        return TPGEMM_OK;
+    }
+    if (!by_row && !by_col) return TPGEMM_OK;
+    const tpg::LayerNormGradOp op{rows, cols, dY, H, mean, rstd, gamma, dH, dX, dR, dgamma, dbeta,
+                                  by_col ? static_cast<float*>(workspace) : nullptr, in[0].ld, in[1].ld,
+                                  in[2].ld, out[0].ld, out[1].ld, d->x, d->gamma, d->grad, drop};
+    return launched(tpg::launch_layernorm_grad(op, st), "layer norm gradient launch");
 }
 
 }  // extern "C"

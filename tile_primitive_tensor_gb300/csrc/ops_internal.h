@@ -1,6 +1,6 @@
 // Host-side interfaces of the operators around the multiply (linear layer, its
-// gradients, root-mean-square norm and its gradients) between their entry
-// points (ops_api.cu) and their kernels. Not part of the public ABI.
+// gradients, norms and their gradients, dropout) between their entry points
+// (ops_api.cu) and their kernels. Not part of the public ABI.
 #pragma once
 
 #include <cstddef>
@@ -148,5 +148,67 @@ struct RmsNormGradOp {
 };
 int rmsnorm_grad_strips(int64_t rows, int64_t cols);
 cudaError_t launch_rmsnorm_grad(const RmsNormGradOp& op, cudaStream_t stream);
+
+// ---- dropout ----
+// Element (i, j) is kept when its random word is at least `threshold` (the
+// probability to drop it times 2^32), and multiplied by `scale`.
+struct Drop {
+    uint64_t seed, offset;
+    const uint64_t* counter;  // in device memory, added to offset; or null
+    uint32_t threshold;
+    float scale;
+    int on;  // 0: nothing is dropped, and nothing above is read
+};
+
+struct DropoutOp {
+    int64_t rows, cols;
+    const void* X;
+    const void* R;  // or null
+    void* Y;
+    int64_t ldx, ldr, ldy;
+    int elem;
+    Drop drop;
+};
+cudaError_t launch_dropout(const DropoutOp& op, cudaStream_t stream);
+
+// ---- layer norm ----
+struct LayerNormOp {
+    int64_t rows, cols;
+    const void* X;
+    const void* R;      // or null
+    const void* gamma;
+    const void* beta;   // or null
+    void* H;            // or null
+    void* Y;
+    float* scale;       // [rows] with TPGEMM_SCALE_ROW
+    float* mean;        // or null
+    float* rstd;        // or null
+    int64_t ldx, ldr, ldh, ldy;
+    int x, g, y;        // element types
+    int mode;           // TPGEMM_SCALE_NONE or _ROW
+    float eps;
+    Drop drop;
+};
+cudaError_t launch_layernorm(const LayerNormOp& op, cudaStream_t stream);
+
+struct LayerNormGradOp {
+    int64_t rows, cols;
+    const void* dY;
+    const void* H;
+    const float* mean;
+    const float* rstd;
+    const void* gamma;
+    const void* dH;     // or null
+    void* dX;           // or null
+    void* dR;           // or null
+    void* dgamma;       // or null
+    void* dbeta;        // or null
+    float* partial;     // [strips][2][cols], or null when neither is wanted
+    int64_t lddy, ldh, lddh, lddx, lddr;
+    int x, g, grad;
+    Drop drop;
+};
+int layernorm_grad_strips(int64_t rows, int64_t cols);
+cudaError_t launch_layernorm_grad(const LayerNormGradOp& op, cudaStream_t stream);
 
 }  // namespace tpg
