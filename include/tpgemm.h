@@ -579,6 +579,38 @@ size_t tpgemm_linear_backward_workspace_bytes(const void* dY, const void* A, con
                                               const tpgemm_linear_grad_desc* d);
 
 /*
+ * The gated linear layer: W holds two projections, N rows of the gate's and then N
+ * rows of the factor's, and
+ *   Z[m, j] = scale_a[m] scale_w[j] sum_k A[m, k] W[j, k] + bias[j],  j < 2 N,
+ *   Y[m, n] = act(Z[m, n]) Z[m, N + n],
+ * from the unrounded Z, rounded once. The description is tpgemm_linear's, where N is
+ * Y's columns (2 N below 2^30) and ldr is not read; W is [2 N, K], bias and scale_w
+ * [2 N] and Z [M, 2 N]. Types, NULLs, precision of sums and activations and the
+ * workspace are as for tpgemm_linear.
+ */
+tpgemm_status tpgemm_gated_linear(void* Y, void* Z, const void* A, const void* W,
+                                  const float* scale_a, const float* scale_w, const void* bias,
+                                  const tpgemm_linear_desc* d, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+size_t tpgemm_gated_linear_workspace_bytes(const void* A, const void* W,
+                                           const tpgemm_linear_desc* d);
+
+/*
+ * Gradients of the gated linear layer without scales:
+ *   dZ[m, n] = dY[m, n] Z[m, N + n] act'(Z[m, n]),  dZ[m, N + n] = dY[m, n] act(Z[m, n]),
+ *   dA = dZ W,  dW = dZ^T A,  dbias[j] = sum_m dZ[m, j].
+ * The description is tpgemm_linear_backward's, where N is dY's columns; W and dW are
+ * [2 N, K], Z [M, 2 N] (read for every activation) and dbias [2 N]. The rest is as
+ * for tpgemm_linear_backward.
+ */
+tpgemm_status tpgemm_gated_linear_backward(void* dA, void* dW, void* dbias, const void* dY,
+                                           const void* A, const void* W, const void* Z,
+                                           const tpgemm_linear_grad_desc* d, void* workspace,
+                                           size_t workspace_bytes, void* stream);
+size_t tpgemm_gated_linear_backward_workspace_bytes(const void* dY, const void* A, const void* W,
+                                                    const tpgemm_linear_grad_desc* d);
+
+/*
  * Root-mean-square norm of each row, after the residual's addition:
  *   H = X + R,  rstd[i] = 1 / sqrt(mean_j H[i, j]^2 + eps),
  *   Y[i, j] = H[i, j] rstd[i] gamma[j].

@@ -152,3 +152,86 @@ def test_layernorm_backward_refuses(kw, status, frag):
 def test_layernorm_backward_accepts(kw):
     st, why = norm_backward(**kw)
     assert st == tp.TPGEMM_ERR_ARCH, (st, why)
+
+
+def gated(M=24, N=40, K=64, lda=0, ldw=0, ldy=0, ldz=0, dtype=tp.TPGEMM_ELEM_F16, out=tp.TPGEMM_ELEM_F16, act=2,
+          Y=addr(0), Z=addr(1), A=addr(2), W=addr(3), sa=None, sw=None, bias=addr(4), ws=None, wsb=0):
+    d = tp.LinearDesc(M, N, K, lda, ldw, 0, ldy, ldz, dtype, out, act)
+    st = tp.tpgemm_gated_linear(Y, Z, A, W, sa, sw, bias, d, ws, wsb, 0)
+    return st, tp.tpgemm_last_error_detail()
+
+
+@pytest.mark.parametrize("kw,status,frag", [
+    (dict(M=-1), tp.TPGEMM_ERR_SHAPE, "M=-1"),
+    (dict(N=1 << 29), tp.TPGEMM_ERR_SHAPE, "2 N=1073741824"),
+    (dict(ldw=63), tp.TPGEMM_ERR_SHAPE, "W: row stride 63"),
+    (dict(ldz=79), tp.TPGEMM_ERR_SHAPE, "Z: row stride 79"),
+    (dict(dtype=tp.TPGEMM_ELEM_F32), tp.TPGEMM_ERR_DTYPE, "dtype 8"),
+    (dict(out=tp.TPGEMM_ELEM_E4M3), tp.TPGEMM_ERR_DTYPE, "out 2"),
+    (dict(act=5), tp.TPGEMM_ERR_DTYPE, "activation 5"),
+    (dict(sw=addr(6)), tp.TPGEMM_ERR_DTYPE, "e4m3 or e5m2"),
+    (dict(Y=None), tp.TPGEMM_ERR_NULL, "Y is NULL"),
+    (dict(W=None), tp.TPGEMM_ERR_NULL, "W is NULL"),
+    (dict(bias=addr(4, 1)), tp.TPGEMM_ERR_ALIGN, "bias="),
+    # the second half of what has 2 N rows or columns counts
+    (dict(Y=addr(3, 2 * 79 * 64)), tp.TPGEMM_ERR_ALIAS, "Y overlaps W"),
+    (dict(Z=addr(0, -2 * (24 * 80 - 1))), tp.TPGEMM_ERR_ALIAS, "Y overlaps Z"),
+    (dict(Y=addr(4, 2 * 79)), tp.TPGEMM_ERR_ALIAS, "Y overlaps bias"),
+    (dict(A=addr(2, 2)), tp.TPGEMM_ERR_NULL, "workspace is NULL"),
+])
+def test_gated_linear_refuses(kw, status, frag):
+    st, why = gated(**kw)
+    assert st == status and frag in why, (st, why)
+
+
+@needs_no_gpu
+@pytest.mark.parametrize("kw", [dict(), dict(Z=None, bias=None), dict(K=0, A=None, W=None), dict(A=addr(2, 2)),
+                                dict(dtype=tp.TPGEMM_ELEM_E5M2, sa=addr(6), sw=addr(7), out=8)])
+def test_gated_linear_accepts(kw):
+    need = tp.tpgemm_gated_linear_workspace_bytes(
+        kw.get("A", addr(2)), addr(3), tp.LinearDesc(24, 40, kw.get("K", 64), 0, 0, 0, 0, 0, kw.get("dtype", 0), 0, 0))
+    st, why = gated(**kw, ws=addr(9) if need else None, wsb=need)
+    assert st == tp.TPGEMM_ERR_ARCH, (st, why)
+
+
+def gated_backward(M=24, N=40, K=64, dtype=0, grad=8, act=2, dA=addr(0), dW=addr(1), db=addr(2), dY=addr(3),
+                   A=addr(4), W=addr(5), Z=addr(6), ws=addr(9), wsb=None, **lds):
+    d = tp.LinearGradDesc(M, N, K, *[lds.get(n, 0) for n in ("lddy", "ldz", "lda", "ldw", "ldda", "lddw")],
+                          dtype, grad, act)
+    if wsb is None:
+        wsb = tp.tpgemm_gated_linear_backward_workspace_bytes(dY, A, W, d)
+    st = tp.tpgemm_gated_linear_backward(dA, dW, db, dY, A, W, Z, d, ws, wsb, 0)
+    return st, tp.tpgemm_last_error_detail()
+
+
+@pytest.mark.parametrize("kw,status,frag", [
+    (dict(N=1 << 29), tp.TPGEMM_ERR_SHAPE, "2 N="),
+    (dict(dtype=tp.TPGEMM_ELEM_E4M3), tp.TPGEMM_ERR_DTYPE, "f16 or bf16"),
+    (dict(Z=None), tp.TPGEMM_ERR_NULL, "Z is NULL"),
+    (dict(Z=None, act=0), tp.TPGEMM_ERR_NULL, "Z is NULL"),
+    (dict(ldz=79), tp.TPGEMM_ERR_SHAPE, "Z: row stride 79"),
+    (dict(dW=addr(5, 2 * 64 * 80 - 2)), tp.TPGEMM_ERR_ALIGN, "dW="),
+    (dict(dW=addr(5, 2 * 64 * 80 - 4)), tp.TPGEMM_ERR_ALIAS, "dW overlaps W"),
+    (dict(db=addr(1, 4 * 64 * 80 - 4)), tp.TPGEMM_ERR_ALIAS, "dW overlaps dbias"),
+    (dict(ws=None), tp.TPGEMM_ERR_NULL, "workspace is NULL"),
+    (dict(wsb=512), tp.TPGEMM_ERR_NULL, "workspace of 512 bytes"),
+    (dict(ws=addr(6)), tp.TPGEMM_ERR_ALIAS, "workspace overlaps Z"),
+])
+def test_gated_linear_backward_refuses(kw, status, frag):
+    st, why = gated_backward(**kw)
+    assert st == status and frag in why, (st, why)
+
+
+@needs_no_gpu
+@pytest.mark.parametrize("kw", [dict(), dict(act=0), dict(dA=None, W=None), dict(dW=None, A=None)])
+def test_gated_linear_backward_accepts(kw):
+    st, why = gated_backward(**kw)
+    assert st == tp.TPGEMM_ERR_ARCH, (st, why)
+
+
+def test_python_refuses_before_the_library():
+    a = torch.zeros(4, 8)
+    for call in (lambda: tp.gated_linear(a, torch.zeros(6, 8)), lambda: tp.layernorm(a, torch.zeros(8)),
+                 lambda: tp.dropout(a, tp.Dropout(0.1, 1))):
+        with pytest.raises(ValueError, match="CUDA tensor"):
+            call()

@@ -215,6 +215,15 @@ def _open(path):
     lib.tpgemm_linear_backward_workspace_bytes.argtypes = [vp, vp, vp,
                                                            ctypes.POINTER(LinearGradDesc)]
     lib.tpgemm_linear_backward_workspace_bytes.restype = sz
+    lib.tpgemm_gated_linear.argtypes = [vp] * 7 + [ctypes.POINTER(LinearDesc), vp, sz, vp]
+    lib.tpgemm_gated_linear.restype = ci
+    lib.tpgemm_gated_linear_workspace_bytes.argtypes = [vp, vp, ctypes.POINTER(LinearDesc)]
+    lib.tpgemm_gated_linear_workspace_bytes.restype = sz
+    lib.tpgemm_gated_linear_backward.argtypes = [vp] * 7 + [ctypes.POINTER(LinearGradDesc), vp, sz, vp]
+    lib.tpgemm_gated_linear_backward.restype = ci
+    lib.tpgemm_gated_linear_backward_workspace_bytes.argtypes = [vp, vp, vp,
+                                                                 ctypes.POINTER(LinearGradDesc)]
+    lib.tpgemm_gated_linear_backward_workspace_bytes.restype = sz
     lib.tpgemm_rmsnorm.argtypes = [vp] * 7 + [ctypes.POINTER(RmsNormDesc), vp]
     lib.tpgemm_rmsnorm.restype = ci
     lib.tpgemm_rmsnorm_backward.argtypes = [vp] * 7 + [ctypes.POINTER(RmsNormGradDesc), vp, sz, vp]
@@ -602,6 +611,32 @@ def tpgemm_linear_backward_workspace_bytes(dY, A, W, desc: LinearGradDesc) -> in
                                                               ctypes.byref(desc)))
 
 
+def tpgemm_gated_linear(Y, Z, A, W, scale_a, scale_w, bias, desc: LinearDesc, workspace=None,
+                        workspace_bytes=0, stream=None) -> int:
+    """Enqueue a gated linear layer; returns the tpgemm_status code."""
+    return int(_load().tpgemm_gated_linear(_ptr(Y), _ptr(Z), _ptr(A), _ptr(W), _ptr(scale_a),
+                                           _ptr(scale_w), _ptr(bias), ctypes.byref(desc),
+                                           _ptr(workspace), int(workspace_bytes),
+                                           _stream(stream)))
+
+
+def tpgemm_gated_linear_workspace_bytes(A, W, desc: LinearDesc) -> int:
+    return int(_load().tpgemm_gated_linear_workspace_bytes(_ptr(A), _ptr(W), ctypes.byref(desc)))
+
+
+def tpgemm_gated_linear_backward(dA, dW, dbias, dY, A, W, Z, desc: LinearGradDesc, workspace=None,
+                                 workspace_bytes=0, stream=None) -> int:
+    """Enqueue the gradients of a gated linear layer; returns the tpgemm_status code."""
+    return int(_load().tpgemm_gated_linear_backward(
+        _ptr(dA), _ptr(dW), _ptr(dbias), _ptr(dY), _ptr(A), _ptr(W), _ptr(Z), ctypes.byref(desc),
+        _ptr(workspace), int(workspace_bytes), _stream(stream)))
+
+
+def tpgemm_gated_linear_backward_workspace_bytes(dY, A, W, desc: LinearGradDesc) -> int:
+    return int(_load().tpgemm_gated_linear_backward_workspace_bytes(_ptr(dY), _ptr(A), _ptr(W),
+                                                                    ctypes.byref(desc)))
+
+
 def tpgemm_rmsnorm(Y, H, scale, rstd, X, R, gamma, desc: RmsNormDesc, stream=None) -> int:
     """Enqueue a root-mean-square norm; returns the tpgemm_status code."""
     return int(_load().tpgemm_rmsnorm(_ptr(Y), _ptr(H), _ptr(scale), _ptr(rstd), _ptr(X), _ptr(R),
@@ -871,6 +906,95 @@ def linear_backward(dY, A, W, pre=None, *, act="none", grad_dtype=None, need=(Tr
     py, pa, pw = dY.data_ptr(), A.data_ptr(), W.data_ptr()
     _call(torch, index, lib.tpgemm_linear_backward, (pda, pdw, pdb, py, pa, pw, pz, desc),
           workspace, lib.tpgemm_linear_backward_workspace_bytes(py, pa, pw, desc))
+    return dA, dW, dbias
+
+
+def _gated_sizes(A, W):
+    M, K, index, device = _sizes("A", A)
+    if W.dim() != 2:
+        raise ValueError("W must be 2-D")
+    if W.shape[0] % 2:
+        raise ValueError(f"W must hold two projections of as many rows, got {W.shape[0]}")
+    return M, K, W.shape[0] // 2, index, device
+
+
+def gated_linear(A, W, bias=None, *, act="silu", scale_a=None, scale_w=None, out_dtype=None, out=None,
+                 pre=None, workspace=None, stream=None):
+    """Y = act(G) U, [G | U] = scale_a[m] scale_w[n] A.W^T + bias on CUDA tensors; returns Y.
+
+    A is [M, K] and W [2N, K]: the gate's N rows, then those of the factor U. Y is [M, N], bias and
+    scale_w [2N], and ``pre`` [M, 2N] is given to receive [G | U], which gated_linear_backward
+    needs. Types, scales, activations, strides, workspace (tpgemm_gated_linear_workspace_bytes) and
+    stream are as for linear."""
+    if stream is not None:
+        with _current(stream, A):
+            return gated_linear(A, W, bias, act=act, scale_a=scale_a, scale_w=scale_w,
+                                out_dtype=out_dtype, out=out, pre=pre, workspace=workspace)
+    torch = _torch or _import_torch()
+    lib = _lib or _load()
+    M, K, N, index, device = _gated_sizes(A, W)
+    dt = A.dtype
+    lda = _matrix("A", A, M, K, dt, index)
+    ldw = _matrix("W", W, 2 * N, K, dt, index)
+    if out_dtype is None:
+        out_dtype = out.dtype if out is not None else (dt if dt.itemsize == 2 else torch.bfloat16)
+    codes = elem_code(dt), elem_code(out_dtype), _act_code(act)
+    if out is None:
+        out, ldy = torch.empty((M, N), dtype=out_dtype, device=device), N
+    else:
+        ldy = _matrix("out", out, M, N, out_dtype, index)
+    ldz = 0
+    pz = pb = psa = psw = None
+    if pre is not None:
+        ldz, pz = _matrix("pre", pre, M, 2 * N, out_dtype, index), pre.data_ptr()
+    if bias is not None:
+        pb = _vector("bias", bias, 2 * N, out_dtype, index)
+    if scale_a is not None:
+        psa = _vector("scale_a", scale_a, M, torch.float32, index)
+    if scale_w is not None:
+        psw = _vector("scale_w", scale_w, 2 * N, torch.float32, index)
+    desc = ctypes.byref(LinearDesc(M, N, K, lda, ldw, 0, ldy, ldz, *codes))
+    pa, pw = A.data_ptr(), W.data_ptr()
+    need = 0
+    # (Operands whose rows start on 128-byte lines need no workspace: the library's promise.)
+    if (pa | pw | (lda | ldw) * dt.itemsize) & 127:
+        need = lib.tpgemm_gated_linear_workspace_bytes(pa, pw, desc)
+    _call(torch, index, lib.tpgemm_gated_linear,
+          (out.data_ptr(), pz, pa, pw, psa, psw, pb, desc), workspace, need)
+    return out
+
+
+def gated_linear_backward(dY, A, W, pre, *, act="silu", grad_dtype=None, need=(True, True, True),
+                          workspace=None, stream=None):
+    """(dA, dW, dbias) of Y = act(G) U, [G | U] = A.W^T + bias, given dY [M, N] and ``pre`` [M, 2N],
+    which holds [G | U]. W and dW are [2N, K], dbias [2N]; the rest is as for linear_backward."""
+    if stream is not None:
+        with _current(stream, A):
+            return gated_linear_backward(dY, A, W, pre, act=act, grad_dtype=grad_dtype, need=need,
+                                         workspace=workspace)
+    torch = _torch or _import_torch()
+    lib = _lib or _load()
+    M, K, N, index, device = _gated_sizes(A, W)
+    dt = A.dtype
+    grad_dtype = dt if grad_dtype is None else grad_dtype
+    desc = ctypes.byref(LinearGradDesc(
+        M, N, K, _matrix("dY", dY, M, N, dt, index), _matrix("pre", pre, M, 2 * N, dt, index),
+        _matrix("A", A, M, K, dt, index), _matrix("W", W, 2 * N, K, dt, index), K, K,
+        elem_code(dt), elem_code(grad_dtype), _act_code(act)))
+    dA = dW = dbias = pda = pdw = pdb = None
+    if need[0]:
+        dA = torch.empty((M, K), dtype=dt, device=device)
+        pda = dA.data_ptr()
+    if need[1]:
+        dW = torch.empty((2 * N, K), dtype=grad_dtype, device=device)
+        pdw = dW.data_ptr()
+    if need[2]:
+        dbias = torch.empty(2 * N, dtype=grad_dtype, device=device)
+        pdb = dbias.data_ptr()
+    py, pa, pw = dY.data_ptr(), A.data_ptr(), W.data_ptr()
+    _call(torch, index, lib.tpgemm_gated_linear_backward,
+          (pda, pdw, pdb, py, pa, pw, pre.data_ptr(), desc), workspace,
+          lib.tpgemm_gated_linear_backward_workspace_bytes(py, pa, pw, desc))
     return dA, dW, dbias
 
 

@@ -240,4 +240,27 @@ __device__ __forceinline__ void epilogue_one(const Epilogue& e, int64_t m, int64
     static_cast<T*>(e.Y)[m * e.ldy + n] = from_f32<T>(x);
 }
 
+// The gated epilogue of output (m, n) of N, from its gate's and its factor's sums.
+template <typename T, int ACT>
+__device__ __forceinline__ void epilogue_gated(const Epilogue& e, int64_t N, int64_t m, int64_t n, float x,
+                                               float u) {
+    if (e.sa) {
+        x *= e.sa[m];
+        u *= e.sa[m];
+    }
+    if (e.sw) {
+        x *= e.sw[n];
+        u *= e.sw[N + n];
+    }
+    if (e.bias) {
+        x += to_f32(static_cast<const T*>(e.bias)[n]);
+        u += to_f32(static_cast<const T*>(e.bias)[N + n]);
+    }
+    if (e.Z) {
+        static_cast<T*>(e.Z)[m * e.ldz + n] = from_f32<T>(x);
+        static_cast<T*>(e.Z)[m * e.ldz + N + n] = from_f32<T>(u);
+    }
+    static_cast<T*>(e.Y)[m * e.ldy + n] = from_f32<T>(act_fwd<ACT, sizeof(T) == 4>(x) * u);
+}
+
 }  // namespace tpg

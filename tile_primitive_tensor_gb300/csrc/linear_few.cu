@@ -25,7 +25,7 @@ namespace tpg {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kRows = 16;   // rows of W in a block
+constexpr int kRows = 16;   // rows of W in a block (gated: 8 of each half)
 constexpr int kRun = 4;     // 16-byte loads of a row that a thread has in flight at a time
 constexpr int kPrefetch = 2;  // runs of a warp asked for ahead
 constexpr int64_t kManyRows = 2 * kSms * kRows;  // of W: more than two blocks to an SM
@@ -98,13 +98,14 @@ __global__ void __launch_bounds__(32 * kWarps) linear_few_kernel(const __grid_co
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
     const int rank = int(cluster_ctarank());
     // (More than 16 rows of A, 16 to a group of blocks, only come with K = 0.)
-    const int64_t tiles = (op.N + kRows - 1) / kRows, tile = blockIdx.x / split;
-    const int64_t n0 = tile % tiles * kRows, m0 = tile / tiles * kFewTokens;
+    const int per = op.gated ? kRows / 2 : kRows;  // outputs of a token
+    const int64_t tiles = (op.N + per - 1) / per, tile = blockIdx.x / split;
+    const int64_t n0 = tile % tiles * per, m0 = tile / tiles * kFewTokens;
     const T* W = static_cast<const T*>(op.b.p);
     const T* A = static_cast<const T*>(op.a.p);
-    const bool live_lo = n0 + g < op.N, live_hi = n0 + g + 8 < op.N;
+    const bool live_lo = n0 + g < op.N, live_hi = op.gated ? live_lo : n0 + g + 8 < op.N;
     const T* lo_row = W + (live_lo ? n0 + g : 0) * op.b.ld;
-    const T* hi_row = W + (live_hi ? n0 + g + 8 : 0) * op.b.ld;
+    const T* hi_row = W + (live_hi ? n0 + g + (op.gated ? op.N : 8) : 0) * op.b.ld;
     const int64_t step = 4 * E * kRun;  // K of one run of a warp
     const int64_t stride = step * kWarps * split;
     grid_launch_dependents();
@@ -184,7 +185,13 @@ __global__ void __launch_bounds__(32 * kWarps) linear_few_kernel(const __grid_co
             }
         }
     }
-    if (m0 + token < op.M && token % split == rank && n0 + row < op.N)
+    if (op.gated) {  // lanes 8 apart hold an output's gate and factor
+        const float u = __shfl_xor_sync(0xffffffffu, v, kRows / 2);
+        if (row < kRows / 2 && m0 + token < op.M && token % split == rank && n0 + row < op.N)
+            with_act(op.e.act, [&](auto act) {
+                epilogue_gated<O, decltype(act)::value>(op.e, op.N, m0 + token, n0 + row, v, u);
+            });
+    } else if (m0 + token < op.M && token % split == rank && n0 + row < op.N)
         with_act(op.e.act, [&](auto act) {
             epilogue_one<O, decltype(act)::value>(op.e, m0 + token, n0 + row, v);
         });
@@ -196,9 +203,10 @@ __global__ void __launch_bounds__(32 * kWarps) linear_few_kernel(const __grid_co
 
 template <typename T, typename O, int TT>
 cudaError_t launch_few(const LinearOp& op, int split, cudaStream_t stream) {
-    const bool vec = tma_rows(op.a, op.M, op.K, op.dtype) && tma_rows(op.b, op.N, op.K, op.dtype);
+    const bool vec = tma_rows(op.a, op.M, op.K, op.dtype) &&
+                     tma_rows(op.b, weight_rows(op), op.K, op.dtype);
     auto fn = vec ? linear_few_kernel<T, O, TT, true> : linear_few_kernel<T, O, TT, false>;
-    const int64_t blocks = (op.N + kRows - 1) / kRows * ((op.M + kFewTokens - 1) / kFewTokens) * split;
+    const int64_t blocks = (weight_rows(op) + kRows - 1) / kRows * ((op.M + kFewTokens - 1) / kFewTokens) * split;
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(blocks));
@@ -240,16 +248,17 @@ bool linear_few_takes(const LinearOp& op) { return op.M <= kFewTokens && !op.a.m
 // 10.2 / 7.8, 16384 x 512 7.9 / 6.0, 4096 x 8192 15.4 / 14.4; e4m3 4096 x 1024
 // 3.8 / 5.0, 1024 x 8192 6.5 / 6.0, 4096 x 4096 8.5 / 7.2).
 bool linear_few_wins(const LinearOp& op) {
-    if (!tma_rows(op.a, op.M, op.K, op.dtype) || !tma_rows(op.b, op.N, op.K, op.dtype)) return true;
-    const int64_t weights = op.N * op.K * elem_size(op.dtype);
-    if (op.N > kManyRows && weights > int64_t(4) << 20) return false;
+    const int64_t rows = weight_rows(op);
+    if (!tma_rows(op.a, op.M, op.K, op.dtype) || !tma_rows(op.b, rows, op.K, op.dtype)) return true;
+    const int64_t weights = rows * op.K * elem_size(op.dtype);
+    if (rows > kManyRows && weights > int64_t(4) << 20) return false;
     return weights <= (elem_size(op.dtype) == 1 ? int64_t(6) << 20 : int64_t(40) << 20);
 }
 
 cudaError_t launch_linear_few(const LinearOp& op, int sms, cudaStream_t stream) {
     // Clusters share a block's rows of K while that leaves every warp a run of
     // its own and the GPU is not full: 4 blocks of 8 warps to an SM.
-    const int64_t tiles = (op.N + kRows - 1) / kRows;
+    const int64_t tiles = (weight_rows(op) + kRows - 1) / kRows;
     const int64_t run = 4 * (16 / elem_size(op.dtype)) * kRun * kWarps;
     int split = 1;
     while (split < 8 && tiles * split * 2 <= 2 * sms && run * split * 2 <= op.K) split *= 2;

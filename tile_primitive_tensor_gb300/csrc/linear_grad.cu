@@ -116,6 +116,108 @@ __global__ void __launch_bounds__(kThreads, 4)
     }
 }
 
+// The gated layer's: Z holds gates g and factors u, N columns of each, and
+//   dZ[m, n] = dY u act'(g),  dZ[m, N + n] = dY act(g),
+// with the sums of both. A thread takes eight outputs, from dY and both halves of
+// Z, and loads the next row while it computes one.
+template <typename T, int ACT, int SIDE>
+__device__ __forceinline__ void gated_grad_strip(const ActGradOp& op, int strips, bool vec, float (&sg)[kPer],
+                                                 float (&su)[kPer]) {
+    const int t = threadIdx.x % SIDE, lane_row = threadIdx.x / SIDE;
+    const int64_t n = (int64_t(blockIdx.x) * SIDE + t) * kPer;
+    const int64_t m_begin = op.M * blockIdx.y / strips, m_end = op.M * (blockIdx.y + 1) / strips;
+    if (n >= op.N) return;
+    const int cnt = op.N - n < kPer ? int(op.N - n) : kPer;
+    vec = vec && cnt == kPer;
+    constexpr int kStep = kThreads / SIDE;
+    const auto row = [&](int64_t m, const float (&dy)[8], const float (&g)[8], const float (&u)[8]) {
+        float dg[8], du[8];
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+            const F2 z = f2(g[j], g[j + 1]), d = f2(dy[j], dy[j + 1]);
+            split(mul(mul(d, f2(u[j], u[j + 1])), act_bwd<ACT>(z)), dg[j], dg[j + 1]);
+            split(mul(d, act_fwd<ACT, false>(z)), du[j], du[j + 1]);
+        }
+        // The two products read dZ in the operands' own type.
+        if (op.dZ) {
+            store8<T>(op.dZ, m * op.lddz + n, vec, cnt, dg);
+            store8<T>(op.dZ, m * op.lddz + op.N + n, vec, cnt, du);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            sg[j] += dg[j];
+            su[j] += du[j];
+        }
+    };
+    if (vec) {
+        const T* pd = static_cast<const T*>(op.dY) + n;
+        const T* pz = static_cast<const T*>(op.Z) + n;
+        uint4 rd, rg, ru;
+        const auto fetch = [&](int64_t m) {
+            if (m >= m_end) return;
+            rd = *reinterpret_cast<const uint4*>(pd + m * op.lddy);
+            rg = *reinterpret_cast<const uint4*>(pz + m * op.ldz);
+            ru = *reinterpret_cast<const uint4*>(pz + m * op.ldz + op.N);
+        };
+        fetch(m_begin + lane_row);
+        for (int64_t m = m_begin + lane_row; m < m_end; m += kStep) {
+            float dy[8], g[8], u[8];
+            unpack8<T>(rd, dy);
+            unpack8<T>(rg, g);
+            unpack8<T>(ru, u);
+            fetch(m + kStep);
+            row(m, dy, g, u);
+        }
+        return;
+    }
+    for (int64_t m = m_begin + lane_row; m < m_end; m += kStep) {
+        float dy[8], g[8], u[8];
+        load8<T>(op.dY, m * op.lddy + n, false, cnt, dy);
+        load8<T>(op.Z, m * op.ldz + n, false, cnt, g);
+        load8<T>(op.Z, m * op.ldz + op.N + n, false, cnt, u);
+        row(m, dy, g, u);
+    }
+}
+
+template <typename T, int SIDE>
+__global__ void __launch_bounds__(kThreads, 3)
+    gated_grad_kernel(const __grid_constant__ ActGradOp op, int strips, bool vec) {
+    constexpr int kRows = kThreads / SIDE, kCols = SIDE * kPer;
+    __shared__ float s[kRows][2][kCols];
+    grid_launch_dependents();
+    grid_dependency_wait();
+    float sg[kPer] = {}, su[kPer] = {};
+    with_act(op.act, [&](auto act) {
+        gated_grad_strip<T, decltype(act)::value, SIDE>(op, strips, vec, sg, su);
+    });
+    if (!op.dbias) return;
+    const int t = threadIdx.x % SIDE, lane_row = threadIdx.x / SIDE;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+        s[lane_row][0][j * SIDE + t] = sg[j];
+        s[lane_row][1][j * SIDE + t] = su[j];
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < 2 * kCols; i += kThreads) {
+        const int h = i / kCols, c = i % kCols;
+        int64_t n = int64_t(blockIdx.x) * kCols + c;
+        if (n >= op.N) continue;
+        n += h * op.N;
+        const int at = (c % kPer) * SIDE + c / kPer;
+        float v = 0.f;
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) v += s[r][h][at];
+        if (SIDE == kWide)
+            op.partial[int64_t(blockIdx.y) * 2 * op.N + n] = v;
+        else if (op.grad == TPGEMM_ELEM_F32)
+            static_cast<float*>(op.dbias)[n] = v;
+        else if (op.grad == TPGEMM_ELEM_BF16)
+            static_cast<__nv_bfloat16*>(op.dbias)[n] = from_f32<__nv_bfloat16>(v);
+        else
+            static_cast<__half*>(op.dbias)[n] = from_f32<__half>(v);
+    }
+}
+
 // Rows of `bytes` bytes, `pitch` apart and anywhere in memory, to rows of whole
 // 16-byte units; a thread to a unit, blockIdx.z to a matrix. A unit with another
 // one behind it in its row is read as five aligned words and shifted into place,
@@ -184,6 +286,27 @@ cudaError_t launch_act_grad(const ActGradOp& op, cudaStream_t stream) {
     const cudaError_t e = launch_dependent(fn, grid, dim3(kThreads), 0, stream, op, strips, vec);
     if (e != cudaSuccess || !op.dbias || few) return e;
     return launch_column_sum(op.partial, strips, op.N, op.dbias, op.grad, stream);
+}
+
+int gated_grad_strips(int64_t M, int64_t N) { return act_grad_strips(M, N); }
+
+cudaError_t launch_gated_grad(const ActGradOp& op, cudaStream_t stream) {
+    const int strips = gated_grad_strips(op.M, op.N);
+    const bool few = strips == 1;
+    const int cols = (few ? kNarrow : kWide) * kPer;
+    const int64_t cb = (op.N + cols - 1) / cols;
+    if (cb > 0x7fffffff || strips > 65535) return cudaErrorInvalidValue;
+    auto rows16 = [&](const void* p, int64_t ld) {
+        return !p || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && (op.M <= 1 || ld % 8 == 0));
+    };
+    const bool vec = op.N % 8 == 0 && rows16(op.dY, op.lddy) && rows16(op.Z, op.ldz) && rows16(op.dZ, op.lddz);
+    const bool f16 = op.dtype == TPGEMM_ELEM_F16;
+    auto fn = few ? (f16 ? gated_grad_kernel<__half, kNarrow> : gated_grad_kernel<__nv_bfloat16, kNarrow>)
+                  : (f16 ? gated_grad_kernel<__half, kWide> : gated_grad_kernel<__nv_bfloat16, kWide>);
+    const cudaError_t e = launch_dependent(fn, dim3(unsigned(cb), unsigned(strips)), dim3(kThreads), 0, stream, op,
+                                           strips, vec);
+    if (e != cudaSuccess || !op.dbias || few) return e;
+    return launch_column_sum(op.partial, strips, 2 * op.N, op.dbias, op.grad, stream);
 }
 
 constexpr int64_t kAlignBlocks = 8 * kSms;  // eight to an SM; a warp then has several rows' loads in flight

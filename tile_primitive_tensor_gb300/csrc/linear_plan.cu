@@ -129,6 +129,8 @@ bool tma_outputs(const Epilogue& e, int64_t M) {
     return rows16(e.Y, e.ldy) && rows16(e.Z, e.ldz) && rows16(e.R, e.ldr);
 }
 
+// Costs and plans are of the accumulators: of a gated product's op N is taken as
+// twice its own, which is also how many tiles of bn / 2 (bp / 2) outputs it has.
 double memory_ns(const LinearOp& op) {
     return double((op.M + op.N) * op.K * elem_size(op.dtype) + 2 * op.M * op.N) / kMemory;
 }
@@ -147,6 +149,7 @@ Choice plan_tile(const LinearOp& op, int64_t kb, int sms, const LinearTuning& t)
     const double off_lines = whole_lines(op.b, op.N, op.K, op.dtype) ? 1.0 : 1.15;
     for (int bn = 256; bn >= 32; bn -= 32) {
         if (t.bn > 0 && bn != t.bn) continue;
+        if (op.gated && bn % 64) continue;  // halves of whole 32-column chunks
         const int64_t tiles = ceil_div(op.M, 256) * ceil_div(op.N, bn);
         const double stage = std::max(225.0, (256 + bn) * (bn == 256 ? 1.01 : 1.07) / kClock) * off_lines;
         const double mmas = double(kb) * stage + 200, epilogue = 1300 + 6.7 * bn;
@@ -256,8 +259,10 @@ tpgemm_status run_linear_tc(const LinearOp& op, int sms, cudaStream_t stream) {
     p.bk = p.fp8 ? 128 : 64;
     p.k_blocks = int(ceil_div(op.K, p.bk));
     p.timeout_ns = wait_timeout_ns();
-    const Choice split = plan_split(op, p.k_blocks, t);
-    Choice c = plan_tile(op, p.k_blocks, sms, t);
+    LinearOp wide = op;  // (see memory_ns)
+    wide.N = weight_rows(op);
+    const Choice split = plan_split(wide, p.k_blocks, t);
+    Choice c = plan_tile(wide, p.k_blocks, sms, t);
     if (t.path == kLinearSplit || (t.path != kLinearTile && split.ns < c.ns)) c = split;
     if (c.bn == 0) return fail_with(TPGEMM_ERR_PATH, "the planner overrides leave no plan");
     p.pair = c.pair;
@@ -266,8 +271,11 @@ tpgemm_status run_linear_tc(const LinearOp& op, int sms, cudaStream_t stream) {
     p.bp = c.bp;
     p.split = c.split;
     p.half_sm = c.half_sm;
-    p.tma_out = p.pair && tma_outputs(op.e, op.M);
-    p.vec = !p.pair && tma_outputs(op.e, op.M) && aligned16(op.e.bias) && aligned16(op.e.sw);
+    p.gated = op.gated;
+    // (The gated layer's second halves of Z, bias and scales start N elements on.)
+    const bool halves = !op.gated || op.N * elem_size(op.e.out) % 16 == 0;
+    p.tma_out = p.pair && tma_outputs(op.e, op.M) && (halves || !op.e.Z);
+    p.vec = !p.pair && tma_outputs(op.e, op.M) && aligned16(op.e.bias) && aligned16(op.e.sw) && halves;
     const Operand& P = p.swap ? op.b : op.a;
     const Operand& Q = p.swap ? op.a : op.b;
     p.Mp = p.swap ? op.N : op.M;
@@ -279,8 +287,9 @@ tpgemm_status run_linear_tc(const LinearOp& op, int sms, cudaStream_t stream) {
     const int q_rows = p.pair ? p.bn / 2 : p.bn;
     p.p_bytes = p.pair ? 16384u : split_p_bytes(p.bp, P.mn != 0);
     p.q_bytes = split_q_bytes(q_rows, Q.mn != 0);
-    const int64_t tiles_p = ceil_div(p.Mp, p.pair ? 256 : p.bp);
-    const int64_t tiles_q = ceil_div(p.Nq, p.bn);
+    const int64_t rows_p = p.swap ? wide.N : p.Mp, rows_q = p.swap ? p.Nq : wide.N;
+    const int64_t tiles_p = ceil_div(rows_p, p.pair ? 256 : p.bp);
+    const int64_t tiles_q = ceil_div(rows_q, p.bn);
     if (tiles_p * tiles_q * p.split > 0x1fffffff)
         return fail_with(TPGEMM_ERR_SHAPE, "too many tiles");
     p.tiles_p = int(tiles_p);
@@ -316,17 +325,21 @@ tpgemm_status run_linear_tc(const LinearOp& op, int sms, cudaStream_t stream) {
         grid = p.tiles * p.split;
     }
     TcLinearMaps maps;
-    s = encode(enc, &maps.P, P, p.Mp, op.K, op.dtype,
-               P.mn ? 64 : p.pair ? 128 : p.bp);
+    // (Gated weights come as two boxes, but to the pairs, whose CTAs load half each.)
+    s = encode(enc, &maps.P, P, rows_p, op.K, op.dtype,
+               P.mn ? 64 : p.pair ? 128 : op.gated && p.swap ? p.bp / 2 : p.bp);
     if (s != TPGEMM_OK) return s;
-    s = encode(enc, &maps.Q, Q, p.Nq, op.K, op.dtype,
-               Q.mn ? 64 : q_rows);
+    s = encode(enc, &maps.Q, Q, rows_q, op.K, op.dtype,
+               Q.mn ? 64 : op.gated && !p.pair && !p.swap ? q_rows / 2 : q_rows);
     if (s != TPGEMM_OK) return s;
     maps.Y = maps.Z = maps.R = maps.P;
     if (p.tma_out) {
         const Epilogue& o = op.e;
         s = encode_out(enc, &maps.Y, o.Y, op.M, op.N, o.ldy, o.out);
         if (s == TPGEMM_OK && o.Z) s = encode_out(enc, &maps.Z, o.Z, op.M, op.N, o.ldz, o.out);
+        if (s == TPGEMM_OK && o.Z && op.gated)
+            s = encode_out(enc, &maps.R, static_cast<const uint8_t*>(o.Z) + op.N * elem_size(o.out), op.M, op.N,
+                           o.ldz, o.out);
         if (s == TPGEMM_OK && o.R) s = encode_out(enc, &maps.R, o.R, op.M, op.N, o.ldr, o.out);
         if (s != TPGEMM_OK) return s;
     }

@@ -11,6 +11,11 @@
 //          joined through distributed shared memory in rank order, so results
 //          repeat, and no global scratch or flag is needed.
 //
+// The gated layer's products take half of a tile's weight rows from W's first
+// half and half from its second, so that an output's gate and factor meet in one
+// tile: in a pair each CTA loads one half's rows as its share of Q, and elsewhere
+// the weights' box comes as two.
+//
 // Operands are read where they lie, K-contiguous or along their rows, by TMA
 // into 128-byte-swizzled stages (K's and the rows' ends read as zero). The tensor
 // cores add into their 32-bit accumulators with truncation: against 64 bits a
@@ -262,6 +267,50 @@ __device__ __forceinline__ void epilogue_turned(const Epilogue& e, int64_t m0, i
     __syncwarp();
 }
 
+// The same of the gated layer: x the gates' sums, u the factors'.
+template <typename T>
+__device__ __forceinline__ void epilogue_turned_gated(const Epilogue& e, int64_t m0, int64_t n0, int64_t M,
+                                                      int64_t N, int lane, float sa, float (&x)[32],
+                                                      float (&u)[32]) {
+    const int64_t n = n0 + lane;
+    const int rows = int(min(int64_t(32), M - m0));
+    transpose32(lane, x);
+    transpose32(lane, u);
+    if (e.sa) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            const float f = __shfl_sync(0xffffffffu, sa, i);
+            x[i] *= f;
+            u[i] *= f;
+        }
+    }
+    if (n < N) {
+        const float swx = e.sw ? e.sw[n] : 1.f, swu = e.sw ? e.sw[N + n] : 1.f;
+        const float bx = e.bias ? to_f32(static_cast<const T*>(e.bias)[n]) : 0.f;
+        const float bu = e.bias ? to_f32(static_cast<const T*>(e.bias)[N + n]) : 0.f;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            x[i] = fmaf(x[i], swx, bx);
+            u[i] = fmaf(u[i], swu, bu);
+        }
+        if (e.Z) {
+            T* z = static_cast<T*>(e.Z) + m0 * e.ldz + n;
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                if (i < rows) {
+                    z[i * e.ldz] = from_f32<T>(x[i]);
+                    z[i * e.ldz + N] = from_f32<T>(u[i]);
+                }
+        }
+        act_n<T>(e.act, x);
+        T* y = static_cast<T*>(e.Y) + m0 * e.ldy + n;
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (i < rows) y[i * e.ldy] = from_f32<T>(x[i] * u[i]);
+    }
+    __syncwarp();
+}
+
 // 32 columns of an output row, staged for a TMA store: a lane's row of the
 // warp's 32 x 32 tile, its 16-byte units placed by the store's swizzle (64
 // bytes to a row of 16-bit outputs, 128 to one of 32-bit ones).
@@ -413,7 +462,139 @@ __device__ __forceinline__ void drain_fills(const TileSmem& s, const TcLinear& p
     }
 }
 
+// The epilogue warps of a gated product. A tile's columns [0, bn / 2) hold gates
+// and the others their factors; a warp takes 32 of both at a time and stores the
+// 32 products, and ahead of them, when Z is kept, the two 32 that they come from.
 template <typename T>
+__device__ __forceinline__ void gated_epilogue(const TcLinear& p, const TileSmem& s, const CUtensorMap& mapY,
+                                               const CUtensorMap& mapZ, const CUtensorMap& mapZu, uint32_t tmem,
+                                               int warp, int lane, int rank, int cid, int ncl) {
+    const Epilogue& e = p.e;
+    const int ew = warp - 4, quad = warp & 3, half = ew >> 2, width = p.bn / 2;
+    const uint32_t lanes = uint32_t(quad * 32) << 16;
+    uint8_t* const staging = s.staging + ew * kStaging;
+    constexpr int kBuf = 1024 * int(sizeof(T));  // one 32 x 32 tile
+    constexpr int kBufs = kStaging / kBuf;       // 2, or 1 of 32-bit outputs
+    const bool tma = p.tma_out != 0;
+    const uint64_t pol = l2_policy(1);  // outputs pass through once
+    int j = 0;                          // the buffer of the next store
+    const auto emit = [&](const CUtensorMap& map, const float (&v)[32], int64_t n, int64_t m) {
+        if (lane == 0) bulk_wait_group_read<kBufs - 1>();  // the buffer's last store has been read
+        __syncwarp();
+        stage_row32<T>(staging + j * kBuf, lane, v);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            tma_store_2d_hint(&map, staging + j * kBuf, int(n), int(m), pol);
+            bulk_commit_group();
+        }
+        j ^= kBufs - 1;
+    };
+    for (int t = cid, it = 0; t < p.tiles; t += ncl, ++it) {
+        int tp, tq;
+        tile_at(t, p, tp, tq);
+        const int64_t m0 = int64_t(2 * tp + rank) * 128 + quad * 32, m = m0 + lane;
+        const int64_t n0 = int64_t(tq) * width;
+        const int b = it & 1;
+        // This warp's chunks: columns c = 32 half, + 64, ... below limit.
+        const int limit = m0 < p.Mp ? int(max(int64_t(0), min(int64_t(width), p.Nq - n0))) : 0;
+        const float sa = m < p.Mp && e.sa ? e.sa[m] : 1.f;
+        // As of the plain epilogue: a 16-bit bias in shared memory, a 32-bit one and
+        // the columns' scales in registers, a chunk ahead.
+        constexpr bool kBiasSmem = sizeof(T) == 2;
+        T* const bias_s = reinterpret_cast<T*>(s.bias + ew * kBiasBytes);  // [chunk][half of W][32]
+        float bias_c[2] = {0.f, 0.f}, sw_c[2] = {1.f, 1.f};
+        const auto fetch_columns = [&](int c) {
+            const int64_t n = n0 + c + lane;
+            if (c >= limit || n >= p.Nq) return;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if (!kBiasSmem && e.bias) bias_c[h] = to_f32(static_cast<const T*>(e.bias)[n + h * p.Nq]);
+                if (e.sw) sw_c[h] = e.sw[n + h * p.Nq];
+            }
+        };
+        if (tma) {
+            if (kBiasSmem && e.bias) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int c = 32 * half + 64 * (i >> 1);
+                    const int64_t n = n0 + c + lane;
+                    if (c < limit && n < p.Nq)
+                        bias_s[32 * i + lane] = static_cast<const T*>(e.bias)[n + (i & 1) * p.Nq];
+                }
+                __syncwarp();
+            }
+            fetch_columns(32 * half);
+        }
+        bool ok = wait_bounded(&s.acc_full[b], (it >> 1) & 1, s.abort, p.timeout_ns);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after_sync();
+        const uint32_t acc = tmem + lanes + uint32_t(b * 256);
+        for (int c = 32 * half; c < limit; c += 64) {
+            float x[2][32];  // gates, factors
+            {
+                uint32_t r[32], q[32];
+                tmem_ld_32x32b_x32(acc + uint32_t(c), r);
+                tmem_ld_32x32b_x32(acc + uint32_t(width + c), q);
+                tmem_ld_wait(r);
+                tmem_ld_wait(q);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    x[0][i] = __uint_as_float(r[i]);
+                    x[1][i] = __uint_as_float(q[i]);
+                }
+            }
+            if (!tma) {
+                epilogue_turned_gated<T>(e, m0, n0 + c, p.Mp, p.Nq, lane, sa, x[0], x[1]);
+                continue;
+            }
+            const float bias_n[2] = {bias_c[0], bias_c[1]}, sw_n[2] = {sw_c[0], sw_c[1]};
+            fetch_columns(c + 64);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if (e.sa) {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2)
+                        split(mul(f2(x[h][i], x[h][i + 1]), f2(sa)), x[h][i], x[h][i + 1]);
+                }
+                if (e.sw) apply_columns<true>(sw_n[h], x[h]);
+                if (e.bias) {
+                    if constexpr (kBiasSmem) {
+                        const uint4* v = reinterpret_cast<const uint4*>(bias_s + (c / 64 * 2 + h) * 32);
+#pragma unroll
+                        for (int g = 0; g < 4; ++g) {
+                            float f[8];
+                            unpack8<T>(v[g], f);
+#pragma unroll
+                            for (int i = 0; i < 8; i += 2)
+                                split(add(f2(x[h][8 * g + i], x[h][8 * g + i + 1]), f2(f[i], f[i + 1])),
+                                      x[h][8 * g + i], x[h][8 * g + i + 1]);
+                        }
+                    } else {
+                        apply_columns<false>(bias_n[h], x[h]);
+                    }
+                }
+            }
+            if (e.Z) {
+                emit(mapZ, x[0], n0 + c, m0);
+                emit(mapZu, x[1], n0 + c, m0);
+            }
+            act_n<T>(e.act, x[0]);
+#pragma unroll
+            for (int i = 0; i < 32; i += 2)
+                split(mul(f2(x[0][i], x[0][i + 1]), f2(x[1][i], x[1][i + 1])), x[0][i], x[0][i + 1]);
+            emit(mapY, x[0], n0 + c, m0);
+            __syncwarp();
+        }
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&s.acc_empty[b]), 0u));
+    }
+    if (lane == 0) bulk_wait_group_read<0>();
+}
+
+template <typename T, bool GATED>
 __global__ void __launch_bounds__(kTileThreads, 1)
     linear_tile_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_constant__ CUtensorMap mapQ,
                        const __grid_constant__ CUtensorMap mapY, const __grid_constant__ CUtensorMap mapZ,
@@ -431,7 +612,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         if (p.tma_out) {
             prefetch_tensormap(&mapY);
             if (p.e.Z) prefetch_tensormap(&mapZ);
-            if (p.e.R) prefetch_tensormap(&mapR);
+            if (GATED ? p.e.Z != nullptr : p.e.R != nullptr) prefetch_tensormap(&mapR);
         }
         for (int i = 0; i < p.stages; ++i) {
             mbar_init(&s.full[i], 1);
@@ -475,7 +656,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             int tp, tq;
             tile_at(t, p, tp, tq);
             const int p0 = (2 * tp + rank) * 128;
-            const int q0 = tq * p.bn + rank * q_rows;
+            const int q0 = GATED ? tq * q_rows + rank * int(p.Nq) : tq * p.bn + rank * q_rows;
             int kb = p.k_rotate ? int(int64_t(t) * nk / p.tiles) : 0;
             if (t == cid) {
                 grid_dependency_wait();
@@ -538,7 +719,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         commit_elected_pair(s.drain, 1);
         wait_bounded(s.drain, 0, s.abort, tmo, true);
     }
-    if (warp >= 4) {
+    if (GATED && warp >= 4) {
+        grid_dependency_wait();
+        gated_epilogue<T>(p, s, mapY, mapZ, mapR, tmem, warp, lane, rank, cid, ncl);
+    }
+    if (!GATED && warp >= 4) {
         grid_dependency_wait();
         const int ew = warp - 4, quad = warp & 3, half = ew >> 2;
         const uint32_t lanes = uint32_t(quad * 32) << 16;
@@ -932,7 +1117,62 @@ __device__ __forceinline__ void join_lines(const TcLinear& p, const float* part,
     }
 }
 
-template <typename T, bool SWAP>
+// The same of the gated layer: a line's values are `half` gates and as many
+// factors, `cols` of each in the matrix. Lines are short, so a warp takes several
+// at a time, 16 or 32 lanes to each.
+template <typename T, int SPLIT>
+__device__ __forceinline__ void join_gated(const TcLinear& p, const float* part, int per, int pitch, int rank,
+                                           int rows, int cols, int half, int64_t N, int64_t m0, int64_t n0) {
+    const Epilogue& e = p.e;
+    const int owned = (rows - rank + SPLIT - 1) / SPLIT;
+    const int side = half <= 64 ? 16 : 32;  // lanes to a line
+    for (int at = 4 * int(threadIdx.x % side); at < cols; at += 4 * side) {
+        const int cnt = min(4, cols - at);
+        const bool vec = p.vec && cnt == 4;
+        const int64_t n = n0 + at;
+        float bias[2][4] = {}, sw[2][4] = {{1.f, 1.f, 1.f, 1.f}, {1.f, 1.f, 1.f, 1.f}};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if (e.bias) load4<T>(e.bias, n + h * N, vec, cnt, bias[h]);
+            if (e.sw) load4<float>(e.sw, n + h * N, vec, cnt, sw[h]);
+        }
+        for (int line = int(threadIdx.x) / side; line < owned; line += kSplitThreads / side) {
+            const float* own = part + line * pitch + at;
+            const int64_t m = m0 + line * SPLIT + rank;
+            float4 v[2][SPLIT];
+#pragma unroll
+            for (int r = 0; r < SPLIT; ++r)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    v[h][r] = *reinterpret_cast<const float4*>(own + r * per * pitch + h * half);
+            const float sa = e.sa ? e.sa[m] : 1.f;
+            float x[2][4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                x[h][0] = v[h][0].x;
+                x[h][1] = v[h][0].y;
+                x[h][2] = v[h][0].z;
+                x[h][3] = v[h][0].w;
+#pragma unroll
+                for (int r = 1; r < SPLIT; ++r) {
+                    x[h][0] += v[h][r].x;
+                    x[h][1] += v[h][r].y;
+                    x[h][2] += v[h][r].z;
+                    x[h][3] += v[h][r].w;
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[h][i] = fmaf(x[h][i], sa * sw[h][i], bias[h][i]);
+                if (e.Z) store4<T>(e.Z, m * e.ldz + n + h * N, vec, cnt, x[h]);
+            }
+            act_n<T>(e.act, x[0]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[0][i] *= x[1][i];
+            store4<T>(e.Y, m * e.ldy + n, vec, cnt, x[0]);
+        }
+    }
+}
+
+template <typename T, bool SWAP, bool GATED>
 __global__ void __launch_bounds__(kSplitThreads, 2)
     linear_split_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_constant__ CUtensorMap mapQ,
                         const __grid_constant__ TcLinear p) {
@@ -942,7 +1182,10 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
     const int rank = int(cluster_ctarank());
     const int tile = blockIdx.x / p.split;
     const int tp = tile % p.tiles_p, tq = tile / p.tiles_p;
-    const int p0 = tp * p.bp, q0 = tq * p.bn;
+    // (Gated weights come as two boxes, each of half the rows, the second one's
+    // `up` rows after the first's.)
+    const int p0 = GATED && SWAP ? tp * (p.bp / 2) : tp * p.bp, q0 = GATED && !SWAP ? tq * (p.bn / 2) : tq * p.bn;
+    const int up = GATED ? int(SWAP ? p.Mp : p.Nq) : 0;
     const int kb0 = int(int64_t(p.k_blocks) * rank / p.split);
     const int kb1 = int(int64_t(p.k_blocks) * (rank + 1) / p.split);
     const int nk = kb1 - kb0;
@@ -985,6 +1228,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
                 for (int a = 0; a < p_atoms; ++a) prefetch_elected(&mapP, p0 + 64 * a, k0);
             } else {
                 prefetch_elected(&mapP, k0, p0);
+                if (GATED && SWAP) prefetch_elected(&mapP, k0, p0 + up);
             }
         }
         grid_dependency_wait();
@@ -998,6 +1242,9 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
             expect_elected(bar, tx);
             load_operand<false>(sp, &mapP, bar, p.p_mn, p_atoms, p0, k0, pol_p);
             load_operand<false>(sp + p.p_bytes, &mapQ, bar, p.q_mn, q_atoms, q0, k0, pol_q);
+            if (GATED && SWAP) load_elected<false>(sp + uint32_t(p.bp) * 64u, &mapP, bar, k0, p0 + up, pol_p);
+            if (GATED && !SWAP)
+                load_elected<false>(sp + p.p_bytes + uint32_t(p.bn) * 64u, &mapQ, bar, k0, q0 + up, pol_q);
             issued_any |= 1u << stage;
             issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
             if (++stage == nstages) {
@@ -1040,7 +1287,8 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
     const int pitch = (SWAP ? 128 : p.bn) + 4;
     const int64_t M = SWAP ? p.Nq : p.Mp, N = SWAP ? p.Mp : p.Nq;
     const int64_t m0 = SWAP ? q0 : p0, n0 = SWAP ? p0 : q0;
-    const int cols = int(min(int64_t(SWAP ? p.bp : p.bn), N - n0));
+    const int width = (SWAP ? p.bp : p.bn) / (GATED ? 2 : 1);
+    const int cols = int(min(int64_t(width), N - n0));
     const int rows = int(min(int64_t(SWAP ? p.bn : p.bp), M - m0));
     const auto deal_and_join = [&](auto n) {
         constexpr int kSplit = decltype(n)::value;
@@ -1056,7 +1304,10 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
         if (kSplit > 1) cluster_sync();
         else __syncthreads();
         grid_dependency_wait();
-        if (!*s.abort) join_lines<T, kSplit>(p, part, per, pitch, rank, rows, cols, m0, n0);
+        if (!*s.abort) {
+            if constexpr (GATED) join_gated<T, kSplit>(p, part, per, pitch, rank, rows, cols, width, N, m0, n0);
+            else join_lines<T, kSplit>(p, part, per, pitch, rank, rows, cols, m0, n0);
+        }
     };
     switch (p.split) {
         case 1: deal_and_join(std::integral_constant<int, 1>()); break;
@@ -1078,15 +1329,21 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
 using TileFn = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, TcLinear);
 using SplitFn = void (*)(CUtensorMap, CUtensorMap, TcLinear);
 
+template <typename T>
+TileFn pick_tile_typed(const TcLinear& p) {
+    return p.gated ? linear_tile_kernel<T, true> : linear_tile_kernel<T, false>;
+}
+
 TileFn pick_tile(const TcLinear& p) {
-    return p.e.out == TPGEMM_ELEM_F16    ? linear_tile_kernel<__half>
-           : p.e.out == TPGEMM_ELEM_BF16 ? linear_tile_kernel<__nv_bfloat16>
-                                         : linear_tile_kernel<float>;
+    return p.e.out == TPGEMM_ELEM_F16    ? pick_tile_typed<__half>(p)
+           : p.e.out == TPGEMM_ELEM_BF16 ? pick_tile_typed<__nv_bfloat16>(p)
+                                         : pick_tile_typed<float>(p);
 }
 
 template <typename T>
 SplitFn pick_split_typed(const TcLinear& p) {
-    return p.swap ? linear_split_kernel<T, true> : linear_split_kernel<T, false>;
+    if (p.gated) return p.swap ? linear_split_kernel<T, true, true> : linear_split_kernel<T, false, true>;
+    return p.swap ? linear_split_kernel<T, true, false> : linear_split_kernel<T, false, false>;
 }
 
 SplitFn pick_split(const TcLinear& p) {
@@ -1129,6 +1386,7 @@ cudaError_t launch_tc_linear(const TcLinearMaps& maps, const TcLinear& p, int gr
     const size_t ring = size_t(p.stages) * (p.p_bytes + p.q_bytes);
     if (p.stages < 2 || p.stages > 32 || cluster < 1 || cluster > 8 || grid % cluster != 0 ||
         p.bn % 16 != 0 || p.bn > 256 || (p.pair && (p.bn % 32 != 0 || p.group < 1)) ||
+        (p.gated && (p.pair ? p.bn % 64 != 0 : (p.swap ? p.p_mn : p.q_mn) != 0)) ||
         (!p.pair && (p.bp > 128 || p.bp % 16 != 0 || p.split > p.k_blocks || (p.split & (p.split - 1)) ||
                      ring > (p.sums_at ? p.sums_at : p.ring_bytes) ||
                      split_partial_bytes(p) + p.sums_at > p.ring_bytes ||

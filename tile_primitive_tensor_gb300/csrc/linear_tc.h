@@ -7,7 +7,8 @@ namespace tpg {
 
 struct TcLinear {
     Epilogue e;
-    int64_t Mp, Nq;        // rows of P and of Q
+    int64_t Mp, Nq;        // rows of P and of Q (gated: half of the weights')
+    int gated;             // see LinearOp: a tile's weight rows are of both halves
     uint64_t timeout_ns;   // bound of every wait
     int tiles_p, tiles_q;  // a cluster's tiles along P and Q
     int tiles;             // tile kernel: their number
@@ -33,7 +34,7 @@ struct TcLinear {
 
 struct TcLinearMaps {
     CUtensorMap P, Q;     // operands
-    CUtensorMap Y, Z, R;  // tile kernel with tma_out: 32 x 32 boxes
+    CUtensorMap Y, Z, R;  // tile kernel with tma_out: 32 x 32 boxes (gated: Z's halves)
 };
 
 size_t tc_linear_smem(const TcLinear& p);

@@ -185,11 +185,13 @@ tpgemm_status run_product(const tpg::LinearOp& op, int sms, cudaStream_t st) {
     return tpg::run_linear_tc(op, sms, st);
 }
 
-tpgemm_status check_linear_desc(const tpgemm_linear_desc* d) {
+// (The gated layer's 2 N rows of W are within the bound of sizes too.)
+tpgemm_status check_linear_desc(const tpgemm_linear_desc* d, bool gated = false) {
     if (!d) return fail_with(TPGEMM_ERR_NULL, "the description is NULL");
     TPG_TRY(check_dim("M", d->M, 0));
     TPG_TRY(check_dim("N", d->N, 0));
     TPG_TRY(check_dim("K", d->K, 0));
+    if (gated) TPG_TRY(check_dim("2 N", 2 * d->N, 0));
     if (!is_16bit(d->dtype) && !is_fp8(d->dtype))
         return fail_with(TPGEMM_ERR_DTYPE, "A and W must be f16, bf16, e4m3 or e5m2 (dtype %d)",
                          int(d->dtype));
@@ -199,7 +201,7 @@ tpgemm_status check_linear_desc(const tpgemm_linear_desc* d) {
     return check_act(d->act);
 }
 
-tpg::LinearOp linear_op(const void* A, const void* W, const tpgemm_linear_desc& d) {
+tpg::LinearOp linear_op(const void* A, const void* W, const tpgemm_linear_desc& d, bool gated = false) {
     tpg::LinearOp op{};
     op.M = d.M;
     op.N = d.N;
@@ -209,6 +211,7 @@ tpg::LinearOp linear_op(const void* A, const void* W, const tpgemm_linear_desc& 
     op.b = {W, dense(d.ldw, d.K), 0};
     op.e.act = d.act;
     op.e.out = d.out;
+    op.gated = gated;
     return op;
 }
 
@@ -219,7 +222,7 @@ tpg::LinearOp linear_op(const void* A, const void* W, const tpgemm_linear_desc& 
 // 96 x 16384 x 4096 32.5 / 27.5 us, 144 x 8192 x 8192 39.7 / 29.5; without
 // gain at 96 x 4096 x 4096, 12.2, and 32 x 16384 x 4096, 25.8).
 bool tokens_on_lines(const tpg::LinearOp& op) {
-    return op.M >= 48 && op.M <= 256 && op.N * op.K * elem_size(op.dtype) >= int64_t(64) << 20;
+    return op.M >= 48 && op.M <= 256 && weight_rows(op) * op.K * elem_size(op.dtype) >= int64_t(64) << 20;
 }
 
 struct LinearLayout {
@@ -231,7 +234,7 @@ LinearLayout linear_layout(const tpg::LinearOp& op) {
     LinearLayout L;
     if (takes_few(op)) return L;
     L.a = plan_aligned(op.a, op.M, op.K, op.dtype, &L.total, tokens_on_lines(op));
-    L.w = plan_aligned(op.b, op.N, op.K, op.dtype, &L.total);
+    L.w = plan_aligned(op.b, weight_rows(op), op.K, op.dtype, &L.total);
     return L;
 }
 
@@ -243,31 +246,33 @@ struct GradLayout {
 };
 
 GradLayout grad_layout(const void* dY, const void* A, const void* W,
-                       const tpgemm_linear_grad_desc& d) {
+                       const tpgemm_linear_grad_desc& d, bool gated = false) {
     GradLayout L;
     if (d.M == 0 || d.N == 0) return L;
-    if (d.act != TPGEMM_ACT_NONE) {
-        L.lddz = int64_t(align_up(size_t(d.N), 64));  // whole 128-byte lines
+    const int64_t rows = gated ? 2 * d.N : d.N;
+    if (gated || d.act != TPGEMM_ACT_NONE) {
+        L.lddz = int64_t(align_up(size_t(rows), 64));  // whole 128-byte lines
         L.dz = L.total;
         L.total = align_up(L.total + size_t(d.M) * size_t(L.lddz) * 2, 256);
     } else if (d.K > 0) {
         L.dy = plan_aligned({dY, dense(d.lddy, d.N), 0}, d.M, d.N, d.dtype, &L.total);
     }
-    const int strips = tpg::act_grad_strips(d.M, d.N);
+    const int strips = gated ? tpg::gated_grad_strips(d.M, d.N) : tpg::act_grad_strips(d.M, d.N);
     L.partial = L.total;
-    if (strips > 1) L.total = align_up(L.total + size_t(strips) * size_t(d.N) * 4, 256);
+    if (strips > 1) L.total = align_up(L.total + size_t(strips) * size_t(rows) * 4, 256);
     if (d.K > 0) {
         L.a = plan_aligned({A, dense(d.lda, d.K), 0}, d.M, d.K, d.dtype, &L.total);
-        L.w = plan_aligned({W, dense(d.ldw, d.K), 0}, d.N, d.K, d.dtype, &L.total);
+        L.w = plan_aligned({W, dense(d.ldw, d.K), 0}, rows, d.K, d.dtype, &L.total);
     }
     return L;
 }
 
-tpgemm_status check_linear_grad_desc(const tpgemm_linear_grad_desc* d) {
+tpgemm_status check_linear_grad_desc(const tpgemm_linear_grad_desc* d, bool gated = false) {
     if (!d) return fail_with(TPGEMM_ERR_NULL, "the description is NULL");
     TPG_TRY(check_dim("M", d->M, 0));
     TPG_TRY(check_dim("N", d->N, 0));
     TPG_TRY(check_dim("K", d->K, 0));
+    if (gated) TPG_TRY(check_dim("2 N", 2 * d->N, 0));
     if (!is_16bit(d->dtype))
         return fail_with(TPGEMM_ERR_DTYPE, "the operands must be f16 or bf16 (dtype %d)",
                          int(d->dtype));
@@ -275,6 +280,126 @@ tpgemm_status check_linear_grad_desc(const tpgemm_linear_grad_desc* d) {
         return fail_with(TPGEMM_ERR_DTYPE, "the gradients must be f16, bf16 or f32 (grad %d)",
                          int(d->grad));
     return check_act(d->act);
+}
+
+// The linear layer and, gated, its form with two halves of weights (see LinearOp).
+tpgemm_status linear_forward(bool gated, void* Y, void* Z, const void* A, const void* W, const float* scale_a,
+                             const float* scale_w, const void* bias, const void* R, const tpgemm_linear_desc* d,
+                             void* workspace, size_t workspace_bytes, void* stream) {
+    TPG_TRY(check_linear_desc(d, gated));
+    const int64_t M = d->M, N = d->N, K = d->K, rows = gated ? 2 * N : N;
+    if ((scale_a || scale_w) && !is_fp8(d->dtype))
+        return fail_with(TPGEMM_ERR_DTYPE, "scale_a and scale_w need e4m3 or e5m2 operands");
+    Mat out[2] = {{"Y", Y, M, N, dense(d->ldy, N), d->out}, {"Z", Z, M, rows, dense(d->ldz, rows), d->out}};
+    Mat in[6] = {{"A", A, M, K, dense(d->lda, K), d->dtype},
+                 {"W", W, rows, K, dense(d->ldw, K), d->dtype},
+                 {"R", R, M, N, dense(d->ldr, N), d->out},
+                 vec("bias", bias, rows, d->out),
+                 vec("scale_a", scale_a, M, TPGEMM_ELEM_F32),
+                 vec("scale_w", scale_w, rows, TPGEMM_ELEM_F32)};
+    if (M == 0 || N == 0) return TPGEMM_OK;
+    TPG_TRY(check_mat(out[0], true));
+    TPG_TRY(check_mat(out[1], false));
+    for (int i = 0; i < 6; ++i) TPG_TRY(check_mat(in[i], i < 2));
+    const Pair y_is_r[1] = {{0, 2}};
+    TPG_TRY(check_overlap(out, 2, in, 6, y_is_r, 1));
+    tpg::LinearOp op = linear_op(A, W, *d, gated);
+    op.e = {Y, Z, R, bias, scale_a, scale_w, out[0].ld, out[1].ld, in[2].ld, d->act, d->out};
+    const LinearLayout L = linear_layout(op);
+    const size_t need = L.total;
+    const Mat all[8] = {out[0], out[1], in[0], in[1], in[2], in[3], in[4], in[5]};
+    TPG_TRY(check_workspace(workspace, workspace_bytes, need, all, 8));
+    int sms = 0;
+    TPG_TRY(tpg::require_device(&sms));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    tpg::AlignJobs copies{};
+    use_aligned(L.a, &op.a, M, K, d->dtype, ws, &copies);
+    use_aligned(L.w, &op.b, rows, K, d->dtype, ws, &copies);
+    TPG_TRY(launched(tpg::launch_align_rows(copies, st), "operand copy launch"));
+    return run_product(op, sms, st);
+}
+
+// Gradients of both.
+tpgemm_status linear_gradients(bool gated, void* dA, void* dW, void* dbias, const void* dY, const void* A,
+                               const void* W, const void* Z, const tpgemm_linear_grad_desc* d, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+    TPG_TRY(check_linear_grad_desc(d, gated));
+    // (Of the gated layer dZ has 2 N columns: `rows` of W.)
+    const int64_t M = d->M, N = d->N, K = d->K, rows = gated ? 2 * N : N;
+    const bool act = gated || d->act != TPGEMM_ACT_NONE;
+    Mat out[3] = {{"dA", dA, M, K, dense(d->ldda, K), d->dtype},
+                  {"dW", dW, rows, K, dense(d->lddw, K), d->grad},
+                  vec("dbias", dbias, rows, d->grad)};
+    Mat in[4] = {{"dY", dY, M, N, dense(d->lddy, N), d->dtype},
+                 {"A", A, M, K, dense(d->lda, K), d->dtype},
+                 {"W", W, rows, K, dense(d->ldw, K), d->dtype},
+                 {"Z", act ? Z : nullptr, M, rows, dense(d->ldz, rows), d->dtype}};
+    for (int i = 0; i < 3; ++i) TPG_TRY(check_mat(out[i], false));
+    TPG_TRY(check_mat(in[0], dA || dW || dbias));
+    TPG_TRY(check_mat(in[1], dW != nullptr));
+    TPG_TRY(check_mat(in[2], dA != nullptr));
+    TPG_TRY(check_mat(in[3], act));
+    TPG_TRY(check_overlap(out, 3, in, 4, nullptr, 0));
+    const GradLayout L = grad_layout(dY, A, W, *d, gated);
+    const Mat all[7] = {out[0], out[1], out[2], in[0], in[1], in[2], in[3]};
+    if (dA || dW || dbias)
+        TPG_TRY(check_workspace(workspace, workspace_bytes, L.total, all, 7));
+    int sms = 0;
+    TPG_TRY(tpg::require_device(&sms));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    const size_t gs = size_t(elem_size(d->grad));
+    // Sums over nothing are zero.
+    if (M == 0) {
+        if (dW && N > 0 && K > 0)
+            TPG_TRY(launched(cudaMemset2DAsync(dW, size_t(out[1].ld) * gs, 0, size_t(K) * gs,
+                                               size_t(rows), st), "zero dW"));
+        if (dbias && N > 0)
+            TPG_TRY(launched(cudaMemsetAsync(dbias, 0, size_t(rows) * gs, st), "zero dbias"));
+        return TPGEMM_OK;
+    }
+    if (N == 0) {
+        if (dA && K > 0)
+            TPG_TRY(launched(cudaMemset2DAsync(dA, size_t(out[0].ld) * 2, 0, size_t(K) * 2,
+                                               size_t(M), st), "zero dA"));
+        return TPGEMM_OK;
+    }
+    const void* dz = dY;
+    int64_t lddz = in[0].ld;
+    if (dbias || (act && (dA || dW))) {
+        tpg::ActGradOp g{M, N, dY, in[3].p, in[0].ld, in[3].ld,
+                         (act && (dA || dW)) ? ws + L.dz : nullptr, L.lddz,
+                         reinterpret_cast<float*>(ws + L.partial), dbias,
+                         d->dtype, d->act, d->grad};
+        TPG_TRY(launched(gated ? tpg::launch_gated_grad(g, st) : tpg::launch_act_grad(g, st),
+                         "activation gradient launch"));
+    }
+    if (act) {
+        dz = ws + L.dz;
+        lddz = L.lddz;
+    }
+    if (K == 0) return TPGEMM_OK;
+    if (!dA && !dW) return TPGEMM_OK;
+    tpg::Operand oz{dz, lddz, 0}, oa{A, in[1].ld, 0}, ow{W, in[2].ld, 0};
+    tpg::AlignJobs copies{};
+    use_aligned(L.dy, &oz, M, rows, d->dtype, ws, &copies);
+    if (dA) use_aligned(L.w, &ow, rows, K, d->dtype, ws, &copies);
+    if (dW) use_aligned(L.a, &oa, M, K, d->dtype, ws, &copies);
+    TPG_TRY(launched(tpg::launch_align_rows(copies, st), "operand copy launch"));
+    if (dA) {  // [M, K] = dZ [M, rows] . W: the reduction runs along W's rows
+        tpg::LinearOp op{M, K, rows, d->dtype, oz, {ow.p, ow.ld, 1},
+                         {dA, nullptr, nullptr, nullptr, nullptr, nullptr, out[0].ld, 0, 0,
+                          TPGEMM_ACT_NONE, d->dtype}};
+        TPG_TRY(run_product(op, sms, st));
+    }
+    if (dW) {  // [rows, K] = dZ^T . A: along the rows of both
+        tpg::LinearOp op{rows, K, M, d->dtype, {oz.p, oz.ld, 1}, {oa.p, oa.ld, 1},
+                         {dW, nullptr, nullptr, nullptr, nullptr, nullptr, out[1].ld, 0, 0,
+                          TPGEMM_ACT_NONE, d->grad}};
+        TPG_TRY(run_product(op, sms, st));
+    }
+    return TPGEMM_OK;
 }
 
 // Dropout's numbers; `in` gets the counter's place, for the overlap check.
@@ -317,38 +442,7 @@ tpgemm_status tpgemm_linear(void* Y, void* Z, const void* A, const void* W, cons
                             const tpgemm_linear_desc* d, void* workspace, size_t workspace_bytes,
                             void* stream) {
     tpg::set_error_detail("");
-    TPG_TRY(check_linear_desc(d));
-    const int64_t M = d->M, N = d->N, K = d->K;
-    if ((scale_a || scale_w) && !is_fp8(d->dtype))
-        return fail_with(TPGEMM_ERR_DTYPE, "scale_a and scale_w need e4m3 or e5m2 operands");
-    Mat out[2] = {{"Y", Y, M, N, dense(d->ldy, N), d->out}, {"Z", Z, M, N, dense(d->ldz, N), d->out}};
-    Mat in[6] = {{"A", A, M, K, dense(d->lda, K), d->dtype},
-                 {"W", W, N, K, dense(d->ldw, K), d->dtype},
-                 {"R", R, M, N, dense(d->ldr, N), d->out},
-                 vec("bias", bias, N, d->out),
-                 vec("scale_a", scale_a, M, TPGEMM_ELEM_F32),
-                 vec("scale_w", scale_w, N, TPGEMM_ELEM_F32)};
-    if (M == 0 || N == 0) return TPGEMM_OK;
-    TPG_TRY(check_mat(out[0], true));
-    TPG_TRY(check_mat(out[1], false));
-    for (int i = 0; i < 6; ++i) TPG_TRY(check_mat(in[i], i < 2));
-    const Pair y_is_r[1] = {{0, 2}};
-    TPG_TRY(check_overlap(out, 2, in, 6, y_is_r, 1));
-    tpg::LinearOp op = linear_op(A, W, *d);
-    op.e = {Y, Z, R, bias, scale_a, scale_w, out[0].ld, out[1].ld, in[2].ld, d->act, d->out};
-    const LinearLayout L = linear_layout(op);
-    const size_t need = L.total;
-    const Mat all[8] = {out[0], out[1], in[0], in[1], in[2], in[3], in[4], in[5]};
-    TPG_TRY(check_workspace(workspace, workspace_bytes, need, all, 8));
-    int sms = 0;
-    TPG_TRY(tpg::require_device(&sms));
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
-    uint8_t* ws = static_cast<uint8_t*>(workspace);
-    tpg::AlignJobs copies{};
-    use_aligned(L.a, &op.a, M, K, d->dtype, ws, &copies);
-    use_aligned(L.w, &op.b, N, K, d->dtype, ws, &copies);
-    TPG_TRY(launched(tpg::launch_align_rows(copies, st), "operand copy launch"));
-    return run_product(op, sms, st);
+    return linear_forward(false, Y, Z, A, W, scale_a, scale_w, bias, R, d, workspace, workspace_bytes, stream);
 }
 
 size_t tpgemm_linear_backward_workspace_bytes(const void* dY, const void* A, const void* W,
@@ -363,80 +457,34 @@ tpgemm_status tpgemm_linear_backward(void* dA, void* dW, void* dbias, const void
                                      const tpgemm_linear_grad_desc* d, void* workspace,
                                      size_t workspace_bytes, void* stream) {
     tpg::set_error_detail("");
-    TPG_TRY(check_linear_grad_desc(d));
-    const int64_t M = d->M, N = d->N, K = d->K;
-    const bool act = d->act != TPGEMM_ACT_NONE;
-    Mat out[3] = {{"dA", dA, M, K, dense(d->ldda, K), d->dtype},
-                  {"dW", dW, N, K, dense(d->lddw, K), d->grad},
-                  vec("dbias", dbias, N, d->grad)};
-    Mat in[4] = {{"dY", dY, M, N, dense(d->lddy, N), d->dtype},
-                 {"A", A, M, K, dense(d->lda, K), d->dtype},
-                 {"W", W, N, K, dense(d->ldw, K), d->dtype},
-                 {"Z", act ? Z : nullptr, M, N, dense(d->ldz, N), d->dtype}};
-    for (int i = 0; i < 3; ++i) TPG_TRY(check_mat(out[i], false));
-    TPG_TRY(check_mat(in[0], dA || dW || dbias));
-    TPG_TRY(check_mat(in[1], dW != nullptr));
-    TPG_TRY(check_mat(in[2], dA != nullptr));
-    TPG_TRY(check_mat(in[3], act));
-    TPG_TRY(check_overlap(out, 3, in, 4, nullptr, 0));
-    const GradLayout L = grad_layout(dY, A, W, *d);
-    const Mat all[7] = {out[0], out[1], out[2], in[0], in[1], in[2], in[3]};
-    if (dA || dW || dbias)
-        TPG_TRY(check_workspace(workspace, workspace_bytes, L.total, all, 7));
-    int sms = 0;
-    TPG_TRY(tpg::require_device(&sms));
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
-    uint8_t* ws = static_cast<uint8_t*>(workspace);
-    const size_t gs = size_t(elem_size(d->grad));
-    // Sums over nothing are zero.
-    if (M == 0) {
-        if (dW && N > 0 && K > 0)
-            TPG_TRY(launched(cudaMemset2DAsync(dW, size_t(out[1].ld) * gs, 0, size_t(K) * gs,
-                                               size_t(N), st), "zero dW"));
-        if (dbias && N > 0)
-            TPG_TRY(launched(cudaMemsetAsync(dbias, 0, size_t(N) * gs, st), "zero dbias"));
-        return TPGEMM_OK;
-    }
-    if (N == 0) {
-        if (dA && K > 0)
-            TPG_TRY(launched(cudaMemset2DAsync(dA, size_t(out[0].ld) * 2, 0, size_t(K) * 2,
-                                               size_t(M), st), "zero dA"));
-        return TPGEMM_OK;
-    }
-    const void* dz = dY;
-    int64_t lddz = in[0].ld;
-    if (dbias || (act && (dA || dW))) {
-        tpg::ActGradOp g{M, N, dY, in[3].p, in[0].ld, in[3].ld,
-                         (act && (dA || dW)) ? ws + L.dz : nullptr, L.lddz,
-                         reinterpret_cast<float*>(ws + L.partial), dbias,
-                         d->dtype, d->act, d->grad};
-        TPG_TRY(launched(tpg::launch_act_grad(g, st), "activation gradient launch"));
-    }
-    if (act) {
-        dz = ws + L.dz;
-        lddz = L.lddz;
-    }
-    if (K == 0) return TPGEMM_OK;
-    if (!dA && !dW) return TPGEMM_OK;
-    tpg::Operand oz{dz, lddz, 0}, oa{A, in[1].ld, 0}, ow{W, in[2].ld, 0};
-    tpg::AlignJobs copies{};
-    use_aligned(L.dy, &oz, M, N, d->dtype, ws, &copies);
-    if (dA) use_aligned(L.w, &ow, N, K, d->dtype, ws, &copies);
-    if (dW) use_aligned(L.a, &oa, M, K, d->dtype, ws, &copies);
-    TPG_TRY(launched(tpg::launch_align_rows(copies, st), "operand copy launch"));
-    if (dA) {  // [M, K] = dZ [M, N] . W: the reduction runs along W's rows
-        tpg::LinearOp op{M, K, N, d->dtype, oz, {ow.p, ow.ld, 1},
-                         {dA, nullptr, nullptr, nullptr, nullptr, nullptr, out[0].ld, 0, 0,
-                          TPGEMM_ACT_NONE, d->dtype}};
-        TPG_TRY(run_product(op, sms, st));
-    }
-    if (dW) {  // [N, K] = dZ^T . A: along the rows of both
-        tpg::LinearOp op{N, K, M, d->dtype, {oz.p, oz.ld, 1}, {oa.p, oa.ld, 1},
-                         {dW, nullptr, nullptr, nullptr, nullptr, nullptr, out[1].ld, 0, 0,
-                          TPGEMM_ACT_NONE, d->grad}};
-        TPG_TRY(run_product(op, sms, st));
-    }
-    return TPGEMM_OK;
+    return linear_gradients(false, dA, dW, dbias, dY, A, W, Z, d, workspace, workspace_bytes, stream);
+}
+
+size_t tpgemm_gated_linear_workspace_bytes(const void* A, const void* W, const tpgemm_linear_desc* d) {
+    tpg::set_error_detail("");
+    if (check_linear_desc(d, true) != TPGEMM_OK || d->M == 0 || d->N == 0) return 0;
+    return linear_layout(linear_op(A, W, *d, true)).total;
+}
+
+tpgemm_status tpgemm_gated_linear(void* Y, void* Z, const void* A, const void* W, const float* scale_a,
+                                  const float* scale_w, const void* bias, const tpgemm_linear_desc* d,
+                                  void* workspace, size_t workspace_bytes, void* stream) {
+    tpg::set_error_detail("");
+    return linear_forward(true, Y, Z, A, W, scale_a, scale_w, bias, nullptr, d, workspace, workspace_bytes, stream);
+}
+
+size_t tpgemm_gated_linear_backward_workspace_bytes(const void* dY, const void* A, const void* W,
+                                                    const tpgemm_linear_grad_desc* d) {
+    tpg::set_error_detail("");
+    if (check_linear_grad_desc(d, true) != TPGEMM_OK) return 0;
+    return grad_layout(dY, A, W, *d, true).total;
+}
+
+tpgemm_status tpgemm_gated_linear_backward(void* dA, void* dW, void* dbias, const void* dY, const void* A,
+                                           const void* W, const void* Z, const tpgemm_linear_grad_desc* d,
+                                           void* workspace, size_t workspace_bytes, void* stream) {
+    tpg::set_error_detail("");
+    return linear_gradients(true, dA, dW, dbias, dY, A, W, Z, d, workspace, workspace_bytes, stream);
 }
 
 tpgemm_status tpgemm_rmsnorm(void* Y, void* H, void* scale, float* rstd, const void* X,

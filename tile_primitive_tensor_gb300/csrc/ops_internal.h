@@ -62,12 +62,18 @@ struct Epilogue {
 };
 
 // Y = epilogue(A B^T): A has M rows, B has N rows, both K columns of `dtype`.
+// Gated: B has 2 N rows, sw, bias and Z as many columns; of an output's two
+// accumulators the first gives the gate z (B's row n), the second the factor u
+// (row N + n), both stored to Z, and Y[m, n] = act(z) u. R is null then.
 struct LinearOp {
     int64_t M, N, K;
     int dtype;
     Operand a, b;
     Epilogue e;
+    int gated = 0;
 };
+// Rows of B.
+inline int64_t weight_rows(const LinearOp& op) { return op.gated ? 2 * op.N : op.N; }
 
 // The product on the tcgen05 kernels (linear_plan.cu); its operands' rows start
 // on 16-byte boundaries (tma_rows). K >= 1.
@@ -100,6 +106,11 @@ struct ActGradOp {
 };
 int act_grad_strips(int64_t M, int64_t N);
 cudaError_t launch_act_grad(const ActGradOp& op, cudaStream_t stream);
+
+// The gated layer's: dZ [M][2 N] from dY [M][N] and Z [M][2 N], dbias [2 N],
+// partial [strips][2 N].
+int gated_grad_strips(int64_t M, int64_t N);
+cudaError_t launch_gated_grad(const ActGradOp& op, cudaStream_t stream);
 
 // Copies of matrices, each of rows of `bytes` bytes, `pitch` bytes apart, to rows
 // dst_pitch apart (dst and dst_pitch multiples of 16, dst_pitch >= bytes rounded
