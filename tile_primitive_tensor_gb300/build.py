@@ -26,10 +26,12 @@ BUILD_DIR_DEBUG = os.path.join(HERE, "_build_debug")
 LIB_PATH_DEBUG = os.path.join(LIB_DIR, "libtpgemm_debug.so")
 SOURCES = ["tpgemm_api.cu", "tc_gemm.cu", "mma_sync_gemm.cu", "tmem_copy.cu", "vec_copy.cu",
            "mx_scales.cu", "ops_api.cu", "linear_tc.cu",
-           "linear_plan.cu", "linear_few.cu", "linear_grad.cu", "rmsnorm.cu", "layernorm.cu",
+           "linear_plan.cu", "linear_few.cu", "linear_grad.cu", "rmsnorm.cu", "layernorm.cu", "layernorm_f16.cu",
+           "layernorm_bf16.cu", "layernorm_f32.cu",
            "dropout.cu"]
 HEADERS = ["ptx.cuh", "tpgemm_internal.h", "ops_internal.h", "elem.cuh", "column_sum.cuh",
-           "linear_tc.h", "vec8.cuh", "launch.cuh", "norm_rows.cuh", "philox.cuh"]
+           "linear_tc.h", "vec8.cuh", "launch.cuh", "norm_rows.cuh", "philox.cuh",
+           "layernorm_rows.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -25,7 +25,8 @@ __global__ void __launch_bounds__(kDropThreads) dropout_kernel(const __grid_cons
     int64_t row = int64_t(at / uint64_t(groups)), g = int64_t(at % uint64_t(groups));
     grid_launch_dependents();
     grid_dependency_wait();
-    const DropKey k = drop_key(op.drop);
+    const DropOffset offset = drop_offset(op.drop);
+    const float scale = op.drop.on ? op.drop.scale : 1.f;
     for (; row < op.rows; row += step_rows, g += step_groups) {
         if (g >= groups) {
             g -= groups;
@@ -37,12 +38,16 @@ __global__ void __launch_bounds__(kDropThreads) dropout_kernel(const __grid_cons
         load8<T>(op.X, row * op.ldx + c, VEC, n, x);
         if (op.R) load8<T>(op.R, row * op.ldr + c, VEC, n, r);
         if (op.drop.on) {
-            drop4(k, uint32_t(row), uint32_t(2 * g), x);
-            drop4(k, uint32_t(row), uint32_t(2 * g + 1), x + 4);
+            const DropRow w = drop_row(op.drop, offset, uint32_t(row));
+            keep4(op.drop, w, uint32_t(2 * g), x);
+            keep4(op.drop, w, uint32_t(2 * g + 1), x + 4);
         }
         if (op.R) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] += r[j];
+            for (int j = 0; j < 8; ++j) x[j] = fmaf(x[j], scale, r[j]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] *= scale;
         }
         store8<T>(op.Y, row * op.ldy + c, VEC, n, x);
     }

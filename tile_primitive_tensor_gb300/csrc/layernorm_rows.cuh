@@ -1,0 +1,1119 @@
+// Layer norm over rows, with dropout and the residual's addition before it and an
+// optional 8-bit output with row scales; and its gradients.
+//
+//   h = r + drop(x),  mean and var of h's row,  rstd = 1 / sqrt(var + eps),
+//   y = (h - mean) rstd gamma + beta,
+//
+// all in 32 bits from the sum x + r on; the stored h, y, mean and rstd are its
+// roundings. var is the mean of (h - mean)^2, taken after the mean from the row
+// in registers, so that it loses nothing to a large mean; what the 32-bit mean is
+// off by comes out of the same pass, as the mean of h - mean, and is taken off.
+// 8-bit rows: y / scale, scale = max(max|y| / top, 2^-126), as of the
+// root-mean-square norm.
+//
+// Gradients, with n = (h - mean) rstd and w = dy gamma:
+//   dt = rstd (w - mean(w) - n mean(w n)) + dh,  dr = dt,  dx = drop(dt),
+//   dgamma = sum over rows of dy n,  dbeta = sum over rows of dy.
+//
+// Bound by memory. A row is read once, by a team of threads (a warp for narrow
+// rows, else a block), eight neighbouring columns to a thread at a time. Blocks
+// stay and walk the rows; each thread copies its own columns of the rows to come to
+// its own places in shared memory (cp.async), where they wait without holding
+// registers and without a barrier, so that memory is kept busy through a row's
+// reductions. Rows that do not start on 16-byte boundaries, or of a width that is
+// no multiple of eight, are read element by element, a team to a row; rows wider
+// than a team's registers (16384 columns) are read again from L2 for each pass.
+#pragma once
+
+#include <algorithm>
+
+#include "column_sum.cuh"
+#include "launch.cuh"
+#include "norm_rows.cuh"
+#include "philox.cuh"
+
+namespace tpg {
+namespace {
+
+// Sums of a and b over a warp, or over the block through `s`. (Reductions that
+// follow one another take different `s`; the one before last may be used again.)
+template <bool WARP>
+__device__ __forceinline__ void team_sum2(float& a, float& b, float2* s) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        a += __shfl_xor_sync(0xffffffffu, a, o);
+        b += __shfl_xor_sync(0xffffffffu, b, o);
+    }
+    if constexpr (!WARP) {
+        const int nw = blockDim.x >> 5, lane = threadIdx.x & 31;
+        if (lane == 0) s[threadIdx.x >> 5] = make_float2(a, b);
+        __syncthreads();
+        const float2 v = lane < nw ? s[lane] : make_float2(0.f, 0.f);
+        a = v.x;
+        b = v.y;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            a += __shfl_xor_sync(0xffffffffu, a, o);
+            b += __shfl_xor_sync(0xffffffffu, b, o);
+        }
+    }
+}
+
+template <bool WARP>
+__device__ __forceinline__ float team_sum1(float a, float2* s) {
+    uint32_t unused = 0;
+    team_sum_max<WARP>(a, unused, s);
+    return a;
+}
+
+// Dropout of a thread's group but for the factor; the whole warp calls it.
+template <bool VEC>
+__device__ __forceinline__ void keep_cols(const Drop& d, const DropRow& w, const Cols<VEC>& c, float (&x)[8]) {
+    if constexpr (VEC) {
+        if (c.n == 8) {
+            keep4(d, w, uint32_t(c.first / 4), x);
+            keep4(d, w, uint32_t(c.first / 4 + 1), x + 4);
+        }
+    } else {
+        keep8_apart(d, w, c.first, c.step, x);
+    }
+}
+
+template <typename XT, bool VEC, bool DROP>
+__device__ __forceinline__ void load_sum(const LayerNormOp& op, const DropRow& w, int64_t row, const Cols<VEC>& c,
+                                         float (&h)[8]) {
+    load_cols<XT, VEC>(op.X, row * op.ldx, c, h);
+    if constexpr (DROP) keep_cols<VEC>(op.drop, w, c, h);
+    const float scale = DROP ? op.drop.scale : 1.f;
+    if (op.R) {
+        float r[8];
+        load_cols<XT, VEC>(op.R, row * op.ldr, c, r);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) h[j] = fmaf(h[j], scale, r[j]);
+    } else if constexpr (DROP) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) h[j] *= scale;
+    }
+}
+
+template <bool VEC>
+__device__ __forceinline__ void store_y(const LayerNormOp& op, int64_t row, const Cols<VEC>& c, const float (&y)[8]) {
+    const int64_t at = row * op.ldy;
+    switch (op.y) {
+        case TPGEMM_ELEM_F16: store_cols<__half, VEC>(op.Y, at, c, y); break;
+        case TPGEMM_ELEM_BF16: store_cols<__nv_bfloat16, VEC>(op.Y, at, c, y); break;
+        case TPGEMM_ELEM_E4M3: store_cols<e4m3, VEC>(op.Y, at, c, y); break;
+        case TPGEMM_ELEM_E5M2: store_cols<e5m2, VEC>(op.Y, at, c, y); break;
+        default: store_cols<float, VEC>(op.Y, at, c, y); break;
+    }
+}
+
+// A row's mean as two 32-bit values (what the first is off by in the second),
+// and rstd.
+struct Stats {
+    float mean, off, rstd;
+};
+
+// From the sums of h - mean and of its square.
+__device__ __forceinline__ Stats stats_of(float mean, float d, float dd, float inv_n, float eps) {
+    const float off = d * inv_n;
+    float var = fmaf(dd, inv_n, -off * off);
+    var = var < 0.f ? 0.f : var;  // (a NaN stays one)
+    return {mean, off, 1.f / sqrtf(var + eps)};
+}
+
+// y of one group.
+template <typename XT, bool VEC>
+__device__ __forceinline__ void normalise(const LayerNormOp& op, const Stats& st, const Cols<VEC>& c,
+                                          const float (&h)[8], float (&y)[8]) {
+    float g[8], b[8];
+    load_gamma<XT, VEC>(op.gamma, op.g, c, g);
+    if (op.beta) {
+        load_gamma<XT, VEC>(op.beta, op.g, c, b);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) b[j] = 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) y[j] = fmaf((h[j] - st.mean - st.off) * st.rstd, g[j], b[j]);
+}
+
+// ------------------------------------------------------------ aligned rows
+// A thread's places for rows to come: `depth` rows of `inputs` matrices, V groups of
+// eight columns each. Only the thread itself writes and reads them, so no barrier is
+// needed, and a warp's accesses are contiguous.
+template <typename T, int V, int STEP>  // STEP: 16-byte units between a thread's places
+struct Ring {
+    uint4* mine;     // the thread's first place
+    int row_units;   // from one row to the next
+    int depth;
+    __device__ __forceinline__ Ring(void* smem, int depth, int inputs)
+        : mine(static_cast<uint4*>(smem) + threadIdx.x), row_units(inputs * V * kUnits<T> * STEP), depth(depth) {}
+    // The place of a row, and from there those of its groups.
+    __device__ __forceinline__ uint4* row(int slot) const { return mine + slot * row_units; }
+    __device__ __forceinline__ static constexpr int place(int input, int group, int unit) {
+        return ((input * V + group) * kUnits<T> + unit) * STEP;
+    }
+    __device__ __forceinline__ void fetch(uint4* row, int input, int group, const T* p) const {
+#pragma unroll
+        for (int u = 0; u < kUnits<T>; ++u)
+            cp_async_16(smem_u32(row + place(input, group, u)), reinterpret_cast<const uint4*>(p) + u, 16);
+    }
+    __device__ __forceinline__ void get(const uint4* row, int input, int group, F2 (&f)[4]) const {
+        uint4 v[kUnits<T>];
+#pragma unroll
+        for (int u = 0; u < kUnits<T>; ++u) v[u] = row[place(input, group, u)];
+        unpack_pairs<T>(v, f);
+    }
+    // The oldest of `depth` rows in flight (a group of copies each) has arrived.
+    __device__ __forceinline__ void wait() const {
+        switch (depth) {
+            case 1: cp_async_wait<0>(); break;
+            case 2: cp_async_wait<1>(); break;
+            case 3: cp_async_wait<2>(); break;
+            default: cp_async_wait<3>(); break;
+        }
+    }
+};
+constexpr int kMaxDepth = 4;
+
+// A spread of aligned rows: V groups of eight columns to a thread of a team of T
+// threads (T = 0: any team), all of them in the row (WHOLE) or not. T is a constant
+// since places and addresses then are: 8192 x 4096 bf16 with dropout takes 55 us so,
+// 62 otherwise. Threads of a block at most, and blocks to an SM at least, by the
+// registers that a thread then has: the norm does with 64, the gradients, which hold
+// 16 sums for each group, with 128.
+template <int V, int T, bool GRAD>
+struct RowKernel {
+    static constexpr int kThreads = T == 0 && !GRAD ? kMaxTeam : GRAD && T != 0 && T <= 256 ? 256 : 512;
+    static constexpr int kBlocks = T == 0 ? 1 : GRAD && T == 512 ? 1 : 2;
+};
+
+// How the rows of a call are spread (ring_plan): threads of a team, rows that a
+// thread copies ahead, and where behind them the weights lie (0: they are not held).
+struct RingPlan {
+    int team, depth, weights_at;
+};
+
+// Gamma and beta: held in shared memory behind the ring, for all teams of a block
+// (from L2 they would come in the midst of every row), or, of rows too wide for
+// that, read from memory.
+template <typename XT, int V>
+struct Weights {
+    const uint4* mine;  // the thread's first place; null: not held
+    int elem, step;     // their type, and 16-byte units between a thread's places
+    template <typename T>
+    __device__ __forceinline__ void get_as(int which, int group, const void* p, int c, F2 (&f)[4]) const {
+        uint4 v[kUnits<T>];
+#pragma unroll
+        for (int u = 0; u < kUnits<T>; ++u)
+            v[u] = mine ? mine[((which * V + group) * kUnits<T> + u) * step]
+                        : reinterpret_cast<const uint4*>(static_cast<const T*>(p) + c)[u];
+        unpack_pairs<T>(v, f);
+    }
+    __device__ __forceinline__ void get(int which, int group, const void* p, int c, F2 (&f)[4]) const {
+        if (elem == TPGEMM_ELEM_F32) get_as<float>(which, group, p, c, f);
+        else get_as<XT>(which, group, p, c, f);
+    }
+    // By one team, a group of copies.
+    __device__ __forceinline__ void fetch(int which, int group, const void* p, int c) const {
+        if (elem == TPGEMM_ELEM_F32) fetch_as<float>(which, group, p, c);
+        else fetch_as<XT>(which, group, p, c);
+    }
+    template <typename T>
+    __device__ __forceinline__ void fetch_as(int which, int group, const void* p, int c) const {
+#pragma unroll
+        for (int u = 0; u < kUnits<T>; ++u)
+            cp_async_16(smem_u32(mine + ((which * V + group) * kUnits<T> + u) * step),
+                        reinterpret_cast<const uint4*>(static_cast<const T*>(p) + c) + u, 16);
+    }
+};
+
+// The threads that share a row: T of them, or `any` (a multiple of 32); `first` is the
+// block's number of the team's first warp, t a thread's place.
+template <int T>
+struct Team {
+    int any, first, index, t;
+    __device__ __forceinline__ explicit Team(int any) : any(any) {
+        index = int(threadIdx.x) / threads();
+        first = index * warps();
+        t = int(threadIdx.x) - index * threads();
+    }
+    __device__ __forceinline__ int threads() const { return T ? T : any; }
+    __device__ __forceinline__ int warps() const { return threads() / 32; }
+    // (Barriers 1 and up; 0 is the block's.)
+    __device__ __forceinline__ void sync() const {
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + index), "r"(threads()) : "memory");
+    }
+    __device__ __forceinline__ int halves() const {  // the largest power of two below warps()
+        return T ? T / 64 : 1 << (31 - __clz(warps() - 1));
+    }
+    // Sums of N values over the team, through `s`, a place of the block's warps that
+    // the reduction before last may have used.
+    template <int N>
+    __device__ __forceinline__ void sum(float (&a)[N], float2* s) const {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+            for (int i = 0; i < N; ++i) a[i] += __shfl_xor_sync(0xffffffffu, a[i], o);
+        if (warps() == 1) return;
+        const int lane = threadIdx.x & 31;
+        if (lane == 0) s[threadIdx.x >> 5] = make_float2(a[0], a[N - 1]);
+        sync();
+        const float2 v = lane < warps() ? s[first + lane] : make_float2(0.f, 0.f);
+        a[0] = v.x;
+        a[N - 1] = N > 1 ? v.y : v.x;
+#pragma unroll
+        for (int o = halves(); o > 0; o >>= 1)
+#pragma unroll
+            for (int i = 0; i < N; ++i) a[i] += __shfl_xor_sync(0xffffffffu, a[i], o);
+#pragma unroll
+        for (int i = 0; i < N; ++i) a[i] = __shfl_sync(0xffffffffu, a[i], 0);
+    }
+    __device__ __forceinline__ uint32_t max(uint32_t v, float2* s) const {
+        v = __reduce_max_sync(0xffffffffu, v);
+        if (warps() == 1) return v;
+        const int lane = threadIdx.x & 31;
+        if (lane == 0) s[threadIdx.x >> 5].x = __uint_as_float(v);
+        sync();
+        return __reduce_max_sync(0xffffffffu, lane < warps() ? __float_as_uint(s[first + lane].x) : 0u);
+    }
+};
+
+// The sum of four pairs' two sums.
+__device__ __forceinline__ float sum_of(const F2 (&f)[4]) {
+    float a, b;
+    split(add(add(f[0], f[1]), add(f[2], f[3])), a, b);
+    return a + b;
+}
+
+// Dropout of eight neighbouring elements from column c on, but for the factor.
+__device__ __forceinline__ void keep8(const Drop& d, const DropRow& w, int c, F2 (&f)[4]) {
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) split(f[i], x[2 * i], x[2 * i + 1]);
+    keep4(d, w, uint32_t(c) / 4, x);
+    keep4(d, w, uint32_t(c) / 4 + 1, x + 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = f2(x[2 * i], x[2 * i + 1]);
+}
+
+template <typename XT, int V, int T, bool WHOLE, bool DROP>
+__global__ void __launch_bounds__(RowKernel<V, T, false>::kThreads, RowKernel<V, T, false>::kBlocks)
+    layernorm_rows_kernel(const __grid_constant__ LayerNormOp op, const RingPlan plan) {
+    extern __shared__ __align__(16) uint8_t ring_smem[];
+    __shared__ float2 s[3][32];
+    const Team<T> team(plan.team);
+    const int64_t teams = blockDim.x / unsigned(team.threads()), stride = gridDim.x * teams;
+    int64_t row = blockIdx.x * teams + team.index;
+    const int cols = int(op.cols), depth = plan.depth;
+    const Ring<XT, V, RowKernel<V, T, false>::kThreads> ring(ring_smem, depth, op.R ? 2 : 1);
+    const Weights<XT, V> weights{
+        plan.weights_at ? reinterpret_cast<const uint4*>(ring_smem + plan.weights_at) + team.t : nullptr, op.g, team.threads()};
+    const auto column = [&](int i) { return 8 * (i * team.threads() + team.t); };
+    const auto has = [&](int i) { return WHOLE || column(i) < cols; };  // group i is in the row
+    const auto fetch = [&](int64_t r, uint4* place) {
+        if (r < op.rows) {
+            const XT* x = static_cast<const XT*>(op.X) + r * op.ldx;
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (has(i)) ring.fetch(place, 0, i, x + column(i));
+            if (op.R) {
+                const XT* q = static_cast<const XT*>(op.R) + r * op.ldr;
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    if (has(i)) ring.fetch(place, 1, i, q + column(i));
+            }
+        }
+        cp_async_commit();
+    };
+    grid_launch_dependents();
+    grid_dependency_wait();
+    for (int i = 0; i < depth; ++i) fetch(row + i * stride, ring.row(i));
+    if (weights.mine) {
+        if (team.index == 0)
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (has(i)) {
+                    weights.fetch(0, i, op.gamma, column(i));
+                    if (op.beta) weights.fetch(1, i, op.beta, column(i));
+                }
+        cp_async_commit();
+        cp_async_wait<0>();
+        __syncthreads();
+    }
+    DropOffset offset{};
+    if constexpr (DROP) offset = drop_offset(op.drop);
+    const float inv_n = 1.f / float(op.cols);
+    const F2 scale = f2(DROP ? op.drop.scale : 1.f);
+    for (int slot = 0; row < op.rows; row += stride, slot = slot + 1 == depth ? 0 : slot + 1) {
+        DropRow w{};
+        if constexpr (DROP) w = drop_row(op.drop, offset, uint32_t(row));
+        ring.wait();
+        uint4* const place = ring.row(slot);
+        F2 h[V][4];
+        F2 part[4] = {f2(0.f), f2(0.f), f2(0.f), f2(0.f)};
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            if (!has(i)) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) h[i][j] = f2(0.f);
+                continue;
+            }
+            ring.get(place, 0, i, h[i]);
+            if constexpr (DROP) keep8(op.drop, w, column(i), h[i]);
+            F2 r[4] = {f2(0.f), f2(0.f), f2(0.f), f2(0.f)};
+            if (op.R) ring.get(place, 1, i, r);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                h[i][j] = fma(h[i][j], scale, r[j]);
+                part[j] = add(part[j], h[i][j]);
+            }
+        }
+        fetch(row + depth * stride, place);
+        float sum[1] = {sum_of(part)};
+        team.sum(sum, s[0]);
+        const float mean = sum[0] * inv_n;
+        if (op.H) {
+            XT* p = static_cast<XT*>(op.H) + row * op.ldh;
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (has(i)) store_pairs<XT>(p + column(i), h[i]);
+        }
+        F2 d[4] = {f2(0.f), f2(0.f), f2(0.f), f2(0.f)}, dd[4] = {f2(0.f), f2(0.f), f2(0.f), f2(0.f)};
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (has(i))
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    h[i][j] = add(h[i][j], f2(-mean));
+                    d[j] = add(d[j], h[i][j]);
+                    dd[j] = fma(h[i][j], h[i][j], dd[j]);
+                }
+        float both[2] = {sum_of(d), sum_of(dd)};
+        team.sum(both, s[1]);
+        const Stats st = stats_of(mean, both[0], both[1], inv_n, op.eps);
+        if (team.t == 0) {
+            if (op.mean) op.mean[row] = st.mean + st.off;
+            if (op.rstd) op.rstd[row] = st.rstd;
+        }
+        // y takes h's place.
+        uint32_t amax = 0;
+        const F2 rstd = f2(st.rstd), shift = f2(-st.off * st.rstd);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            if (!has(i)) continue;
+            F2 g[4], b[4] = {f2(0.f), f2(0.f), f2(0.f), f2(0.f)};
+            weights.get(0, i, op.gamma, column(i), g);
+            if (op.beta) weights.get(1, i, op.beta, column(i), b);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) h[i][j] = fma(fma(h[i][j], rstd, shift), g[j], b[j]);
+            if (op.mode == TPGEMM_SCALE_ROW) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    float lo, hi;
+                    split(h[i][j], lo, hi);
+                    amax = max(amax, max(abs_bits(lo), abs_bits(hi)));
+                }
+            }
+        }
+        if (op.mode == TPGEMM_SCALE_ROW) {
+            const float to = row_scale(team.max(amax, s[2]), op.y);
+            if (team.t == 0) op.scale[row] = to;
+            const F2 inv = f2(1.f / to);
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) h[i][j] = mul(h[i][j], inv);
+        }
+        const auto store = [&](auto* y) {
+            y += row * op.ldy;
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (has(i)) store_pairs(y + column(i), h[i]);
+        };
+        switch (op.y) {
+            case TPGEMM_ELEM_F16: store(static_cast<__half*>(op.Y)); break;
+            case TPGEMM_ELEM_BF16: store(static_cast<__nv_bfloat16*>(op.Y)); break;
+            case TPGEMM_ELEM_E4M3: store(static_cast<e4m3*>(op.Y)); break;
+            case TPGEMM_ELEM_E5M2: store(static_cast<e5m2*>(op.Y)); break;
+            default: store(static_cast<float*>(op.Y)); break;
+        }
+    }
+    cp_async_wait<0>();
+}
+
+// --------------------------------------------------------- rows as they come
+// Unaligned rows held in registers: V groups of eight columns to a thread; WARP: a
+// row to a warp, else to a block.
+template <typename XT, int V, bool WARP, bool DROP>
+__global__ void __launch_bounds__(WARP ? 32 * kWarpRows : kMaxTeam)
+    layernorm_kernel(const __grid_constant__ LayerNormOp op) {
+    constexpr bool VEC = false;
+    __shared__ float2 s[3][32];
+    const int team = WARP ? 32 : int(blockDim.x);
+    const int t = WARP ? int(threadIdx.x & 31) : int(threadIdx.x);
+    const int64_t row = WARP ? int64_t(blockIdx.x) * kWarpRows + (threadIdx.x >> 5) : int64_t(blockIdx.x);
+    grid_launch_dependents();
+    grid_dependency_wait();
+    if (WARP && row >= op.rows) return;
+    DropRow k{};
+    if constexpr (DROP) k = drop_row(op.drop, drop_offset(op.drop), uint32_t(row));
+    float h[V][8];
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        load_sum<XT, VEC, DROP>(op, k, row, Cols<VEC>(i, t, team, op.cols), h[i]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum += h[i][j];
+    }
+    const float mean = team_sum1<WARP>(sum, s[0]) / float(op.cols);
+    float d = 0.f, dd = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const Cols<VEC> c(i, t, team, op.cols);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float e = j < c.n ? h[i][j] - mean : 0.f;
+            d += e;
+            dd += e * e;
+        }
+    }
+    team_sum2<WARP>(d, dd, s[1]);
+    const Stats st = stats_of(mean, d, dd, 1.f / float(op.cols), op.eps);
+    if (t == 0) {
+        if (op.mean) op.mean[row] = st.mean + st.off;
+        if (op.rstd) op.rstd[row] = st.rstd;
+    }
+    float inv = 1.f;
+    if (op.mode == TPGEMM_SCALE_ROW) {
+        float none = 0.f;
+        uint32_t amax = 0;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const Cols<VEC> c(i, t, team, op.cols);
+            float y[8];
+            normalise<XT, VEC>(op, st, c, h[i], y);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (j < c.n) amax = max(amax, abs_bits(y[j]));
+        }
+        team_sum_max<WARP>(none, amax, s[2]);
+        const float scale = row_scale(amax, op.y);
+        if (t == 0) op.scale[row] = scale;
+        inv = 1.f / scale;
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const Cols<VEC> c(i, t, team, op.cols);
+        float y[8];
+        normalise<XT, VEC>(op, st, c, h[i], y);
+        if (op.mode == TPGEMM_SCALE_ROW) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[j] *= inv;
+        }
+        store_y<VEC>(op, row, c, y);
+        if (op.H) store_cols<XT, VEC>(op.H, row * op.ldh, c, h[i]);
+    }
+}
+
+// Rows of any width, a block to a row, read once for each pass.
+template <typename XT, bool VEC, bool DROP>
+__global__ void __launch_bounds__(kMaxTeam) layernorm_wide_kernel(const __grid_constant__ LayerNormOp op) {
+    __shared__ float2 s[3][32];
+    const int team = int(blockDim.x), t = int(threadIdx.x);
+    const int64_t row = blockIdx.x;
+    const int64_t groups = (op.cols + 8 * team - 1) / (8 * team);
+    grid_launch_dependents();
+    grid_dependency_wait();
+    DropRow k{};
+    if constexpr (DROP) k = drop_row(op.drop, drop_offset(op.drop), uint32_t(row));
+    float h[8], y[8];
+    float sum = 0.f;
+    for (int64_t i = 0; i < groups; ++i) {
+        load_sum<XT, VEC, DROP>(op, k, row, Cols<VEC>(i, t, team, op.cols), h);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum += h[j];
+    }
+    const float mean = team_sum1<false>(sum, s[0]) / float(op.cols);
+    float d = 0.f, dd = 0.f;
+    for (int64_t i = 0; i < groups; ++i) {
+        const Cols<VEC> c(i, t, team, op.cols);
+        load_sum<XT, VEC, DROP>(op, k, row, c, h);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float e = j < c.n ? h[j] - mean : 0.f;
+            d += e;
+            dd += e * e;
+        }
+    }
+    team_sum2<false>(d, dd, s[1]);
+    const Stats st = stats_of(mean, d, dd, 1.f / float(op.cols), op.eps);
+    if (t == 0) {
+        if (op.mean) op.mean[row] = st.mean + st.off;
+        if (op.rstd) op.rstd[row] = st.rstd;
+    }
+    float inv = 1.f;
+    if (op.mode == TPGEMM_SCALE_ROW) {
+        float none = 0.f;
+        uint32_t amax = 0;
+        for (int64_t i = 0; i < groups; ++i) {
+            const Cols<VEC> c(i, t, team, op.cols);
+            load_sum<XT, VEC, DROP>(op, k, row, c, h);
+            normalise<XT, VEC>(op, st, c, h, y);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (j < c.n) amax = max(amax, abs_bits(y[j]));
+        }
+        team_sum_max<false>(none, amax, s[2]);
+        const float scale = row_scale(amax, op.y);
+        if (t == 0) op.scale[row] = scale;
+        inv = 1.f / scale;
+    }
+    for (int64_t i = 0; i < groups; ++i) {
+        const Cols<VEC> c(i, t, team, op.cols);
+        load_sum<XT, VEC, DROP>(op, k, row, c, h);
+        normalise<XT, VEC>(op, st, c, h, y);
+        if (op.mode == TPGEMM_SCALE_ROW) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[j] *= inv;
+        }
+        store_y<VEC>(op, row, c, y);
+        if (op.H) store_cols<XT, VEC>(op.H, row * op.ldh, c, h);
+    }
+}
+
+// ---------------------------------------------------------------- gradients
+// Blocks walk the rows grid-stride, a team to a row, with the columns' sums of
+// dgamma and dbeta in registers; partial[block] gets the block's, dgamma's
+// columns and then dbeta's.
+//
+// Aligned rows, read ahead as by the norm. With more than two groups to a thread
+// what a reduction leaves to be used, w and n, is computed a second time from shared
+// memory in place of held in registers, which the columns' sums take. A block's
+// teams add up their sums in order at the end.
+template <typename XT, int V, int T, bool WHOLE, bool DROP>
+__global__ void __launch_bounds__(RowKernel<V, T, true>::kThreads, RowKernel<V, T, true>::kBlocks)
+    layernorm_grad_rows_kernel(const __grid_constant__ LayerNormGradOp op, const RingPlan plan) {
+    extern __shared__ __align__(16) uint8_t ring_smem[];
+    __shared__ float2 s[2][32];
+    __shared__ float stats[kMaxDepth][16][2];  // mean and rstd of the rows ahead, for each warp
+    constexpr bool kAgain = V > 2;
+    const Team<T> team(plan.team);
+    const int teams = int(blockDim.x) / team.threads();
+    const int64_t stride = int64_t(gridDim.x) * teams;
+    int64_t row = int64_t(blockIdx.x) * teams + team.index;
+    const int cols = int(op.cols), depth = plan.depth;
+    const bool rows_wanted = op.dX || op.dR, add_dh = rows_wanted && op.dH;
+    const Ring<XT, V, RowKernel<V, T, true>::kThreads> ring(ring_smem, depth, add_dh ? 3 : 2);
+    const Weights<XT, V> weights{
+        plan.weights_at ? reinterpret_cast<const uint4*>(ring_smem + plan.weights_at) + team.t : nullptr, op.g, team.threads()};
+    const auto column = [&](int i) { return 8 * (i * team.threads() + team.t); };
+    const auto has = [&](int i) { return WHOLE || column(i) < cols; };  // group i is in the row
+    const auto fetch = [&](int64_t r, int slot) {
+        uint4* const place = ring.row(slot);
+        if (r < op.rows) {
+            // (A load that the next row waits for would take as long as that row.)
+            const int lane = threadIdx.x & 31;
+            if (lane < 2)
+                cp_async_4(smem_u32(&stats[slot][threadIdx.x >> 5][lane]), (lane ? op.rstd : op.mean) + r);
+            const XT* dy = static_cast<const XT*>(op.dY) + r * op.lddy;
+            const XT* h = static_cast<const XT*>(op.H) + r * op.ldh;
+            const XT* dh = static_cast<const XT*>(op.dH) + (add_dh ? r * op.lddh : 0);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                if (!has(i)) continue;
+                ring.fetch(place, 0, i, dy + column(i));
+                ring.fetch(place, 1, i, h + column(i));
+                if (add_dh) ring.fetch(place, 2, i, dh + column(i));
+            }
+        }
+        cp_async_commit();
+    };
+    grid_launch_dependents();
+    grid_dependency_wait();
+    for (int i = 0; i < depth; ++i) fetch(row + i * stride, i);
+    if (rows_wanted && weights.mine) {
+        if (team.index == 0)
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (has(i)) weights.fetch(0, i, op.gamma, column(i));
+        cp_async_commit();
+        cp_async_wait<0>();
+        __syncthreads();
+    }
+    DropOffset offset{};
+    if constexpr (DROP) offset = drop_offset(op.drop);
+    const float inv_n = 1.f / float(op.cols);
+    F2 ag[V][4], ab[V][4];
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) ag[i][j] = ab[i][j] = f2(0.f);
+    for (int slot = 0, turn = 0; row < op.rows; row += stride, turn ^= 1, slot = slot + 1 == depth ? 0 : slot + 1) {
+        ring.wait();
+        __syncwarp();
+        const float mean = stats[slot][threadIdx.x >> 5][0], rstd = stats[slot][threadIdx.x >> 5][1];
+        uint4* const place = ring.row(slot);
+        F2 kept_w[kAgain ? 1 : V][4], kept_n[kAgain ? 1 : V][4];
+        // dY and (H - mean) rstd of group i.
+        const auto load = [&](int i, F2 (&w)[4], F2 (&n)[4]) {
+            ring.get(place, 0, i, w);
+            ring.get(place, 1, i, n);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) n[j] = mul(add(n[j], f2(-mean)), f2(rstd));
+        };
+        const auto times_gamma = [&](int i, F2 (&w)[4]) {
+            F2 g[4];
+            weights.get(0, i, op.gamma, column(i), g);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[j] = mul(w[j], g[j]);
+        };
+        F2 pw[4] = {f2(0.f), f2(0.f), f2(0.f), f2(0.f)}, pn[4] = {f2(0.f), f2(0.f), f2(0.f), f2(0.f)};
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            if (!has(i)) continue;
+            F2 (&w)[4] = kept_w[kAgain ? 0 : i], (&n)[4] = kept_n[kAgain ? 0 : i];
+            load(i, w, n);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                ag[i][j] = fma(w[j], n[j], ag[i][j]);
+                ab[i][j] = add(ab[i][j], w[j]);
+            }
+            if (rows_wanted) {
+                times_gamma(i, w);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    pw[j] = add(pw[j], w[j]);
+                    pn[j] = fma(w[j], n[j], pn[j]);
+                }
+            }
+        }
+        if (rows_wanted) {
+            float both[2] = {sum_of(pw), sum_of(pn)};
+            team.sum(both, s[turn]);
+            const F2 sw = f2(-both[0] * inv_n), swn = f2(-both[1] * inv_n);
+            DropRow words{};
+            if constexpr (DROP) words = drop_row(op.drop, offset, uint32_t(row));
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                if (!has(i)) continue;
+                F2 (&w)[4] = kept_w[kAgain ? 0 : i], (&n)[4] = kept_n[kAgain ? 0 : i];
+                if constexpr (kAgain) {
+                    load(i, w, n);
+                    times_gamma(i, w);
+                }
+                F2 dt[4] = {f2(0.f), f2(0.f), f2(0.f), f2(0.f)};
+                if (add_dh) ring.get(place, 2, i, dt);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) dt[j] = fma(fma(n[j], swn, add(w[j], sw)), f2(rstd), dt[j]);
+                if (op.dR) store_pairs<XT>(static_cast<XT*>(op.dR) + row * op.lddr + column(i), dt);
+                if (op.dX) {
+                    if constexpr (DROP) {
+                        keep8(op.drop, words, column(i), dt);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) dt[j] = mul(dt[j], f2(op.drop.scale));
+                    }
+                    store_pairs<XT>(static_cast<XT*>(op.dX) + row * op.lddx + column(i), dt);
+                }
+            }
+        }
+        __syncwarp();  // (the warp has read its statistics)
+        fetch(row + depth * stride, slot);
+    }
+    cp_async_wait<0>();
+    if (!op.partial) return;
+    float* out = op.partial + int64_t(blockIdx.x) * 2 * op.cols;
+    if (teams == 1) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (has(i)) {
+                store_pairs<float>(out + column(i), ag[i]);
+                store_pairs<float>(out + op.cols + column(i), ab[i]);
+            }
+        return;
+    }
+    // Through the ring's place, where nothing is on its way: gamma's sums, then beta's.
+    float* const sums = reinterpret_cast<float*>(ring_smem);  // [teams][padded columns]
+    const int pitch = 8 * V * team.threads();
+    const auto join = [&](const F2 (&a)[V][4], float* to) {
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < V; ++i) store_pairs<float>(sums + team.index * pitch + column(i), a[i]);
+        __syncthreads();
+        for (int c = int(threadIdx.x); c < cols; c += int(blockDim.x)) {
+            float v = 0.f;
+            for (int r = 0; r < teams; ++r) v += sums[r * pitch + c];
+            to[c] = v;
+        }
+    };
+    join(ag, out);
+    join(ab, out + op.cols);
+}
+
+// Unaligned rows.
+template <typename XT, int V, bool WARP, bool DROP>
+__global__ void __launch_bounds__(WARP ? 32 * kWarpRows : kMaxTeam)
+    layernorm_grad_kernel(const __grid_constant__ LayerNormGradOp op) {
+    constexpr bool VEC = false;
+    __shared__ float2 s[2][32];
+    __shared__ float sum[WARP ? 8 * 32 * 8 * V : 1];
+    const int team = WARP ? 32 : int(blockDim.x);
+    const int t = WARP ? int(threadIdx.x & 31) : int(threadIdx.x);
+    const int64_t teams = WARP ? kWarpRows : 1;
+    const int64_t stride = int64_t(gridDim.x) * teams;
+    grid_launch_dependents();
+    grid_dependency_wait();
+    DropOffset offset{};
+    if constexpr (DROP) offset = drop_offset(op.drop);
+    const bool rows_wanted = op.dX || op.dR;
+    float ag[V][8], ab[V][8];
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) ag[i][j] = ab[i][j] = 0.f;
+    int64_t row = int64_t(blockIdx.x) * teams + (WARP ? threadIdx.x >> 5 : 0);
+    for (int turn = 0; row < op.rows; row += stride, turn ^= 1) {
+        const float rstd = op.rstd[row], mean = op.mean[row];
+        float w[V][8], n[V][8];
+        float sw = 0.f, swn = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const Cols<VEC> c(i, t, team, op.cols);
+            load_cols<XT, VEC>(op.dY, row * op.lddy, c, w[i]);
+            load_cols<XT, VEC>(op.H, row * op.ldh, c, n[i]);
+            float g[8];
+            if (rows_wanted) load_gamma<XT, VEC>(op.gamma, op.g, c, g);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                n[i][j] = (n[i][j] - mean) * rstd;
+                ag[i][j] += w[i][j] * n[i][j];
+                ab[i][j] += w[i][j];
+                if (rows_wanted) {
+                    w[i][j] *= g[j];  // (0 past the row)
+                    sw += w[i][j];
+                    swn += w[i][j] * n[i][j];
+                }
+            }
+        }
+        if (!rows_wanted) continue;
+        team_sum2<WARP>(sw, swn, s[turn]);
+        sw /= float(op.cols);
+        swn /= float(op.cols);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const Cols<VEC> c(i, t, team, op.cols);
+            float dt[8];
+            if (op.dH) {
+                load_cols<XT, VEC>(op.dH, row * op.lddh, c, dt);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) dt[j] = 0.f;
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) dt[j] += rstd * (w[i][j] - sw - n[i][j] * swn);
+            if (op.dR) store_cols<XT, VEC>(op.dR, row * op.lddr, c, dt);
+            if (op.dX) {
+                if constexpr (DROP) {
+                    keep_cols<VEC>(op.drop, drop_row(op.drop, offset, uint32_t(row)), c, dt);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) dt[j] *= op.drop.scale;
+                }
+                store_cols<XT, VEC>(op.dX, row * op.lddx, c, dt);
+            }
+        }
+    }
+    if (!op.partial) return;
+    float* out = op.partial + int64_t(blockIdx.x) * 2 * op.cols;
+    if constexpr (WARP) {
+        const int w = threadIdx.x >> 5;
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) sum[((w * V + i) * 8 + j) * 32 + t] = which ? ab[i][j] : ag[i][j];
+            __syncthreads();
+            // The warps' sums in order; warp w finishes the groups w, w + 8, ...
+            for (int q = w; q < V * 8; q += kWarpRows) {
+                float v = 0.f;
+#pragma unroll
+                for (int r = 0; r < kWarpRows; ++r) v += sum[(r * V * 8 + q) * 32 + t];
+                const Cols<VEC> c(q / 8, t, team, op.cols);
+                if (q % 8 < c.n) out[which * op.cols + c.first + int64_t(q % 8) * c.step] = v;
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const Cols<VEC> c(i, t, team, op.cols);
+            store_cols<float, VEC>(out, 0, c, ag[i]);
+            store_cols<float, VEC>(out, op.cols, c, ab[i]);
+        }
+    }
+}
+
+template <typename XT>
+__device__ __forceinline__ float gamma_at(const LayerNormGradOp& op, int64_t c) {
+    return op.g == TPGEMM_ELEM_F32 ? static_cast<const float*>(op.gamma)[c]
+                                   : to_f32(static_cast<const XT*>(op.gamma)[c]);
+}
+
+// Rows wider than a team's registers: dt a row to a block, read twice, and the
+// column sums apart.
+template <typename XT, bool DROP>
+__global__ void __launch_bounds__(kMaxTeam) layernorm_grad_wide_kernel(const __grid_constant__ LayerNormGradOp op) {
+    __shared__ float2 s[32];
+    const int64_t row = blockIdx.x;
+    grid_launch_dependents();
+    grid_dependency_wait();
+    DropRow k{};
+    if constexpr (DROP) k = drop_row(op.drop, drop_offset(op.drop), uint32_t(row));
+    const XT* dy = static_cast<const XT*>(op.dY) + row * op.lddy;
+    const XT* h = static_cast<const XT*>(op.H) + row * op.ldh;
+    const float rstd = op.rstd[row], mean = op.mean[row];
+    float sw = 0.f, swn = 0.f;
+    for (int64_t c = threadIdx.x; c < op.cols; c += kMaxTeam) {
+        const float w = to_f32(dy[c]) * gamma_at<XT>(op, c);
+        sw += w;
+        swn += w * ((to_f32(h[c]) - mean) * rstd);
+    }
+    team_sum2<false>(sw, swn, s);
+    sw /= float(op.cols);
+    swn /= float(op.cols);
+    for (int64_t c = threadIdx.x; c < op.cols; c += kMaxTeam) {
+        float d = rstd * (to_f32(dy[c]) * gamma_at<XT>(op, c) - sw - (to_f32(h[c]) - mean) * rstd * swn);
+        if (op.dH) d += to_f32(static_cast<const XT*>(op.dH)[row * op.lddh + c]);
+        if (op.dR) static_cast<XT*>(op.dR)[row * op.lddr + c] = from_f32<XT>(d);
+        if (op.dX) {
+            if constexpr (DROP) {
+                const uint4 w = philox(op.drop, k, uint32_t(c / 4));
+                const int q = int(c & 3);
+                d = keep_one(op.drop, q == 0 ? w.x : q == 1 ? w.y : q == 2 ? w.z : w.w, d) * op.drop.scale;
+            }
+            static_cast<XT*>(op.dX)[row * op.lddx + c] = from_f32<XT>(d);
+        }
+    }
+}
+
+// partial[strip] = the strip's sums of dy n, then of dy.
+template <typename XT>
+__global__ void __launch_bounds__(256) layernorm_columns_kernel(const __grid_constant__ LayerNormGradOp op, int strips) {
+    const int64_t c = int64_t(blockIdx.x) * 256 + threadIdx.x;
+    const int64_t begin = op.rows * blockIdx.y / strips, end = op.rows * (blockIdx.y + 1) / strips;
+    grid_launch_dependents();
+    grid_dependency_wait();
+    if (c >= op.cols) return;
+    float g = 0.f, b = 0.f;
+    for (int64_t r = begin; r < end; ++r) {
+        const float dy = to_f32(static_cast<const XT*>(op.dY)[r * op.lddy + c]);
+        g += dy * ((to_f32(static_cast<const XT*>(op.H)[r * op.ldh + c]) - op.mean[r]) * op.rstd[r]);
+        b += dy;
+    }
+    float* out = op.partial + int64_t(blockIdx.y) * 2 * op.cols + c;
+    out[0] = g;
+    out[op.cols] = b;
+}
+
+// Unaligned rows: up to 512 columns a warp holds the row, wider rows are a block's.
+Spread spread_of(int64_t cols) {
+    const int64_t groups = (cols + 7) / 8;
+    if (groups <= 64) return {32, groups <= 32 ? 1 : 2, true};
+    if (cols > kMaxHeld) return {kMaxTeam, 0, false};
+    const bool one = groups <= kMaxTeam;
+    const int64_t per = one ? groups : (groups + 1) / 2;
+    return {int((per + 31) / 32 * 32), one ? 1 : 2, false};
+}
+
+// Aligned rows of up to kMaxHeld columns. A reduction costs each warp that takes
+// part as many instructions as two groups of columns, so the norm of 16-bit rows has
+// four groups to a thread; two where the rows' bytes or the columns' sums are twice
+// as many; one or two of rows that a warp then holds whole; and of few rows one, for
+// the shortest time to the end.
+struct RowSpread {
+    int v, t;         // the kernel's V and T
+    bool whole;       // and WHOLE
+    int team, teams;  // threads of a team, teams of a block
+    int blocks;       // to an SM
+    int threads() const { return team * teams; }
+};
+RowSpread row_spread(int64_t rows, int64_t cols, int elem, bool grad) {
+    const int groups = int((cols + 7) / 8);
+    const int most = elem == TPGEMM_ELEM_F32 || grad ? 2 : 4;
+    if (rows <= kSms && groups <= (grad ? 512 : kMaxTeam))
+        return {1, 0, false, (groups + 31) / 32 * 32, 1, 1};
+    int v = groups <= 32 ? 1 : groups <= 64 ? 2 : groups <= 512 * most ? most : 4, t = 32;
+    while (t * v < groups) t *= 2;
+    if (v == 4 && most == 2) t = 512;
+    const int threads = grad && t <= 256 ? 256 : 512;
+    const int teams = int(std::max<int64_t>(1, std::min<int64_t>(threads / t, rows / kSms)));
+    return {v, t, t * v == groups, t, teams, std::min((grad ? 512 : 1024) / (t * teams), 8)};
+}
+
+constexpr int kRingBytes = 216 * 1024;  // of an SM, for its blocks
+RingPlan ring_plan(RowSpread* s, int step, int inputs, int elem, int vectors, int vector_elem, size_t* bytes) {
+    const size_t row = size_t(inputs) * s->v * step * 8 * elem_size(elem);  // of all teams
+    size_t held = size_t(vectors) * s->v * s->team * 8 * elem_size(vector_elem);
+    while (s->blocks > 1 && held + row > size_t(kRingBytes / s->blocks)) --s->blocks;
+    const size_t have = size_t(kRingBytes / s->blocks);
+    if (held + row > have) held = 0;
+    const int depth = std::max(1, std::min(kMaxDepth, int((have - held) / row)));
+    *bytes = depth * row + held;
+    return {s->team, depth, held ? int(depth * row) : 0};
+}
+
+// f(V, T, WHOLE) of the spread's kernel, as integral constants; MOST as in row_spread.
+template <int MOST, typename F>
+cudaError_t with_spread(const RowSpread& s, F&& f) {
+    using std::integral_constant;
+    const auto call = [&](auto v, auto t) {
+        return s.whole ? f(v, t, std::true_type()) : f(v, t, std::false_type());
+    };
+    constexpr integral_constant<int, MOST> most{};
+    if (s.t == 0) return f(integral_constant<int, 1>(), integral_constant<int, 0>(), std::false_type());
+    if (s.v == 1) return call(integral_constant<int, 1>(), integral_constant<int, 32>());
+    if (s.v == MOST) {
+        switch (s.t) {
+            case 32: return call(most, integral_constant<int, 32>());
+            case 64: return call(most, integral_constant<int, 64>());
+            case 128: return call(most, integral_constant<int, 128>());
+            case 256: return call(most, integral_constant<int, 256>());
+            default: return call(most, integral_constant<int, 512>());
+        }
+    }
+    if constexpr (MOST == 2) return call(integral_constant<int, 4>(), integral_constant<int, 512>());
+    else return call(integral_constant<int, 2>(), integral_constant<int, 32>());
+}
+
+template <typename F, typename Op>
+cudaError_t launch_ring(F fn, int64_t blocks, int threads, size_t bytes, const RingPlan& plan, cudaStream_t stream,
+                        const Op& op) {
+    const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(fn),
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
+    if (e != cudaSuccess) return e;
+    return launch_dependent(fn, dim3(unsigned(blocks)), dim3(unsigned(threads)), bytes, stream, op, plan);
+}
+
+template <typename XT, bool DROP>
+cudaError_t launch_rows(const LayerNormOp& op, cudaStream_t stream) {
+    RowSpread s = row_spread(op.rows, op.cols, op.x, false);
+    return with_spread<sizeof(XT) == 4 ? 2 : 4>(s, [&](auto v, auto t, auto whole) {
+        constexpr int V = decltype(v)::value, T = decltype(t)::value;
+        size_t bytes;
+        const RingPlan plan = ring_plan(&s, RowKernel<V, T, false>::kThreads, op.R ? 2 : 1, op.x, op.beta ? 2 : 1,
+                                        op.g, &bytes);
+        const int64_t blocks = std::min<int64_t>((op.rows + s.teams - 1) / s.teams, int64_t(kSms) * s.blocks);
+        return launch_ring(layernorm_rows_kernel<XT, V, T, decltype(whole)::value, DROP>, blocks, s.threads(), bytes,
+                           plan, stream, op);
+    });
+}
+
+template <typename XT, bool VEC, bool DROP>
+cudaError_t launch_norm(const LayerNormOp& op, cudaStream_t stream) {
+    const Spread s = spread_of(op.cols);
+    const int64_t blocks = s.v == 0 ? op.rows : (op.rows + s.rows() - 1) / s.rows();
+    if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+    if (s.v == 0)
+        return launch_dependent(layernorm_wide_kernel<XT, VEC, DROP>, dim3(unsigned(blocks)),
+                                dim3(unsigned(s.threads())), 0, stream, op);
+    if constexpr (VEC) {
+        return launch_rows<XT, DROP>(op, stream);
+    } else {
+        auto fn = s.warp ? (s.v == 1 ? layernorm_kernel<XT, 1, true, DROP> : layernorm_kernel<XT, 2, true, DROP>)
+                         : (s.v == 1 ? layernorm_kernel<XT, 1, false, DROP> : layernorm_kernel<XT, 2, false, DROP>);
+        return launch_dependent(fn, dim3(unsigned(blocks)), dim3(unsigned(s.threads())), 0, stream, op);
+    }
+}
+
+template <typename XT>
+cudaError_t launch_norm_typed(const LayerNormOp& op, cudaStream_t stream) {
+    const bool vec = op.cols % 8 == 0 && rows_aligned(op.X, op.ldx, op.rows, op.x, 16) &&
+                     rows_aligned(op.R, op.ldr, op.rows, op.x, 16) &&
+                     rows_aligned(op.H, op.ldh, op.rows, op.x, 16) &&
+                     rows_aligned(op.Y, op.ldy, op.rows, op.y, elem_size(op.y) == 1 ? 8 : 16) &&
+                     rows_aligned(op.gamma, 0, 1, op.g, 16) && rows_aligned(op.beta, 0, 1, op.g, 16);
+    if (op.drop.on)
+        return vec ? launch_norm<XT, true, true>(op, stream) : launch_norm<XT, false, true>(op, stream);
+    return vec ? launch_norm<XT, true, false>(op, stream) : launch_norm<XT, false, false>(op, stream);
+}
+
+// Two rows to a team at the least, since each block's sums are written and read
+// once more; else what the SMs hold.
+int grad_blocks(int64_t rows, const Spread& s) {
+    const int64_t most = (rows + 2 * s.rows() - 1) / (2 * s.rows());
+    const int64_t fill = int64_t(kSms) * std::max(1, 512 / s.threads());
+    return int(most < fill ? (most < 1 ? 1 : most) : fill);
+}
+int grad_row_blocks(int64_t rows, const RowSpread& s) {
+    const int64_t most = (rows + 2 * s.teams - 1) / (2 * s.teams);
+    return int(std::max<int64_t>(1, std::min<int64_t>(most, int64_t(kSms) * s.blocks)));
+}
+
+int wide_strips(int64_t rows) {
+    const int64_t most = (rows + 15) / 16;
+    return int(most < 1 ? 1 : (most < 64 ? most : 64));
+}
+
+template <typename XT, bool DROP>
+cudaError_t launch_grad(const LayerNormGradOp& op, const Spread& u, bool vec, int* strips, cudaStream_t stream) {
+    if (vec) {
+        RowSpread s = row_spread(op.rows, op.cols, op.x, true);
+        return with_spread<2>(s, [&](auto v, auto t, auto whole) {
+            constexpr int V = decltype(v)::value, T = decltype(t)::value;
+            size_t bytes;
+            const RingPlan plan = ring_plan(&s, RowKernel<V, T, true>::kThreads, op.dH && (op.dX || op.dR) ? 3 : 2, op.x,
+                                            1, op.g, &bytes);
+            if (s.teams > 1) bytes = std::max(bytes, size_t(V) * s.threads() * 8 * 4);  // (the teams' sums)
+            *strips = grad_row_blocks(op.rows, s);
+            return launch_ring(layernorm_grad_rows_kernel<XT, V, T, decltype(whole)::value, DROP>, *strips, s.threads(),
+                               bytes, plan, stream, op);
+        });
+    }
+    *strips = grad_blocks(op.rows, u);
+    auto fn = u.warp ? (u.v == 1 ? layernorm_grad_kernel<XT, 1, true, DROP> : layernorm_grad_kernel<XT, 2, true, DROP>)
+                     : (u.v == 1 ? layernorm_grad_kernel<XT, 1, false, DROP> : layernorm_grad_kernel<XT, 2, false, DROP>);
+    return launch_dependent(fn, dim3(unsigned(*strips)), dim3(unsigned(u.threads())), 0, stream, op);
+}
+
+template <typename XT>
+cudaError_t launch_grad_typed(const LayerNormGradOp& op, cudaStream_t stream) {
+    const Spread s = spread_of(op.cols);
+    int strips = wide_strips(op.rows);
+    const bool drop = op.drop.on != 0;
+    cudaError_t e = cudaSuccess;
+    if (s.v == 0) {
+        // The columns first: dX or dR may be written over dY or H.
+        if (op.partial) {
+            const dim3 grid(unsigned((op.cols + 255) / 256), static_cast<unsigned>(strips));
+            e = launch_dependent(layernorm_columns_kernel<XT>, grid, dim3(256), 0, stream, op, strips);
+        }
+        if (e == cudaSuccess && (op.dX || op.dR))
+            e = launch_dependent(drop ? layernorm_grad_wide_kernel<XT, true> : layernorm_grad_wide_kernel<XT, false>,
+                                 dim3(unsigned(op.rows)), dim3(kMaxTeam), 0, stream, op);
+    } else {
+        const bool vec = op.cols % 8 == 0 && rows_aligned(op.dY, op.lddy, op.rows, op.x, 16) &&
+                         rows_aligned(op.H, op.ldh, op.rows, op.x, 16) &&
+                         rows_aligned(op.dH, op.lddh, op.rows, op.x, 16) &&
+                         rows_aligned(op.dX, op.lddx, op.rows, op.x, 16) &&
+                         rows_aligned(op.dR, op.lddr, op.rows, op.x, 16) &&
+                         rows_aligned(op.gamma, 0, 1, op.g, 16);
+        e = drop ? launch_grad<XT, true>(op, s, vec, &strips, stream) : launch_grad<XT, false>(op, s, vec, &strips, stream);
+    }
+    if (e != cudaSuccess || !op.partial) return e;
+    return launch_column_sums(op.partial, strips, op.cols, op.dgamma, op.dbeta, op.grad, stream);
+}
+
+}  // namespace
+
+template <typename XT>
+cudaError_t layernorm_of(const LayerNormOp& op, cudaStream_t stream) {
+    return launch_norm_typed<XT>(op, stream);
+}
+
+template <typename XT>
+cudaError_t layernorm_grad_of(const LayerNormGradOp& op, cudaStream_t stream) {
+    return launch_grad_typed<XT>(op, stream);
+}
+
+}  // namespace tpg

@@ -414,8 +414,12 @@ tpgemm_status check_drop(const tpgemm_drop& d, tpg::Drop* drop, Mat* in) {
                          static_cast<const void*>(d.counter));
     in->p = d.counter;
     const double t = std::nearbyint(d.p * 4294967296.0);
-    *drop = {d.seed, d.offset, d.counter, t < 4294967295.0 ? uint32_t(t) : 0xffffffffu,
-             float(1.0 / (1.0 - d.p)), 1};
+    tpg::drop_keys(drop, d.seed);
+    drop->offset = d.offset;
+    drop->counter = d.counter;
+    drop->threshold = t < 4294967295.0 ? uint32_t(t) : 0xffffffffu;
+    drop->scale = float(1.0 / (1.0 - d.p));
+    drop->on = 1;
     return TPGEMM_OK;
 }
 

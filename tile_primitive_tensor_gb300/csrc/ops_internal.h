@@ -164,12 +164,20 @@ cudaError_t launch_rmsnorm_grad(const RmsNormGradOp& op, cudaStream_t stream);
 // Element (i, j) is kept when its random word is at least `threshold` (the
 // probability to drop it times 2^32), and multiplied by `scale`.
 struct Drop {
-    uint64_t seed, offset;
+    uint32_t key[10][2];      // of each round, from the seed (drop_keys)
+    uint64_t offset;
     const uint64_t* counter;  // in device memory, added to offset; or null
     uint32_t threshold;
     float scale;
     int on;  // 0: nothing is dropped, and nothing above is read
 };
+
+inline void drop_keys(Drop* d, uint64_t seed) {
+    for (uint32_t i = 0; i < 10; ++i) {
+        d->key[i][0] = uint32_t(seed) + i * 0x9E3779B9u;
+        d->key[i][1] = uint32_t(seed >> 32) + i * 0xBB67AE85u;
+    }
+}
 
 struct DropoutOp {
     int64_t rows, cols;
@@ -219,7 +227,7 @@ struct LayerNormGradOp {
     int x, g, grad;
     Drop drop;
 };
-int layernorm_grad_strips(int64_t rows, int64_t cols);
+int layernorm_grad_strips(int64_t rows, int64_t cols);  // (at most)
 cudaError_t launch_layernorm_grad(const LayerNormGradOp& op, cudaStream_t stream);
 
 }  // namespace tpg

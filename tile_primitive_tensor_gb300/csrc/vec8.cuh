@@ -86,6 +86,38 @@ __device__ __forceinline__ void store8(void* base, int64_t at, bool vec, int n, 
     }
 }
 
+// Eight elements as pairs of 32-bit values, from and to their 16-byte units (one of
+// 16-bit elements, two of 32-bit ones).
+template <typename T>
+constexpr int kUnits = int(sizeof(T)) / 2;
+
+template <typename T>
+__device__ __forceinline__ void unpack_pairs(const uint4 (&u)[kUnits<T>], F2 (&f)[4]) {
+    if constexpr (sizeof(T) == 4) {
+        f[0] = f2(__uint_as_float(u[0].x), __uint_as_float(u[0].y));
+        f[1] = f2(__uint_as_float(u[0].z), __uint_as_float(u[0].w));
+        f[2] = f2(__uint_as_float(u[1].x), __uint_as_float(u[1].y));
+        f[3] = f2(__uint_as_float(u[1].z), __uint_as_float(u[1].w));
+    } else {
+        float x[8];
+        unpack8<T>(u[0], x);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = f2(x[2 * i], x[2 * i + 1]);
+    }
+}
+
+// Stores eight pairs' values to 16-byte (8-bit types: 8-byte) aligned memory.
+template <typename T>
+__device__ __forceinline__ void store_pairs(T* p, const F2 (&f)[4]) {
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) split(f[i], x[2 * i], x[2 * i + 1]);
+    if constexpr (sizeof(T) == 1)
+        *reinterpret_cast<uint2*>(p) = pack8_fp8(x, std::is_same<T, e4m3>::value ? __NV_E4M3 : __NV_E5M2);
+    else
+        store8<T>(p, 0, true, 8, x);
+}
+
 // Sixteen bytes at a row's byte `at`, whose address is a multiple of 16; those
 // outside of the row's `bytes` read as zero and are not touched.
 using Window = uint4;
