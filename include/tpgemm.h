@@ -600,8 +600,10 @@ size_t tpgemm_gated_linear_workspace_bytes(const void* A, const void* W,
  *   dZ[m, n] = dY[m, n] Z[m, N + n] act'(Z[m, n]),  dZ[m, N + n] = dY[m, n] act(Z[m, n]),
  *   dA = dZ W,  dW = dZ^T A,  dbias[j] = sum_m dZ[m, j].
  * The description is tpgemm_linear_backward's, where N is dY's columns; W and dW are
- * [2 N, K], Z [M, 2 N] (read for every activation) and dbias [2 N]. The rest is as
- * for tpgemm_linear_backward.
+ * [2 N, K], Z [M, 2 N] (read for every activation) and dbias [2 N]. dA and a 16-bit
+ * dW are products of dZ rounded to `dtype`; a 32-bit dW is one of dZ as two 16-bit
+ * values, its rounding and the rest (within 2^-17 of each term in all), two products
+ * one after the other. The rest is as for tpgemm_linear_backward.
  */
 tpgemm_status tpgemm_gated_linear_backward(void* dA, void* dW, void* dbias, const void* dY,
                                            const void* A, const void* W, const void* Z,

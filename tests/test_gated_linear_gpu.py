@@ -222,6 +222,34 @@ def test_backward_types(dtype, act, grad):
         check_backward(M, N, K, dtype, act, grad, seed=M)
 
 
+@pytest.mark.parametrize("dtype,std", [(BF16, 1.0), (F16, 1.0), (F16, 1e-6), (BF16, 1e-20)])
+@pytest.mark.parametrize("M,N,K", [(100, 72, 264), (700, 264, 136)])
+def test_32_bit_weight_gradients_see_all_of_dz(dtype, std, M, N, K):
+    # dz as a rounding and its rest: within 2^-18 of bf16's and 2^-24 of f16's terms (whose rest is
+    # kept away from f16's subnormal numbers), with a few roundings of its own, and two sums over M
+    g = torch.Generator(device="cuda").manual_seed(M)
+    pre, A, W = view(g, M, 2 * N, dtype), view(g, M, K, dtype), view(g, 2 * N, K, dtype)
+    dY = view(g, M, N, dtype, std=std)
+    _, dW, db = tp.gated_linear_backward(dY, A, W, pre, act="none", grad_dtype=F32)
+    dz = torch.cat([dY.double() * pre[:, N:].double(), dY.double() * pre[:, :N].double()], 1)
+    terms = dz.abs().t() @ A.double().abs()
+    want = dz.t() @ A.double()
+    ok, why = ref.within(dW, want, (2.0 ** -17 + 2 * ref.acc(M)) * terms + 2.0 ** -22 * want.abs() + 1e-44)
+    assert ok, why
+    assert float((dW.double() - want).norm() / want.norm()) <= 1e-5
+
+
+@pytest.mark.parametrize("M,N,K", [(40, 200, 9000), (300, 264, 16384)])
+def test_long_sums_of_32_bit_outputs(M, N, K):
+    # two sums of random signs in each output, in pieces: off by less than 1e-5 of the outputs' size
+    g = torch.Generator(device="cuda").manual_seed(K)
+    A, W = view(g, M, K, BF16), view(g, 2 * N, K, BF16, std=K ** -0.5)
+    y = tp.gated_linear(A, W, act="none", out_dtype=F32)
+    z = A.double() @ W.double().t()
+    want = z[:, :N] * z[:, N:]
+    assert float((y.double() - want).norm() / want.norm()) <= 1e-5
+
+
 @pytest.mark.parametrize("pad,offset", [(8, 0), (16, 8), (1, 0), (0, 1), (8, 4)])
 def test_backward_strides(pad, offset):
     for M, N, K in ((3, 72, 256), (60, 100, 264), (300, 264, 96)):

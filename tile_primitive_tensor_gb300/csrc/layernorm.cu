@@ -19,7 +19,11 @@ cudaError_t launch_layernorm(const LayerNormOp& op, cudaStream_t stream) {
 int layernorm_grad_strips(int64_t rows, int64_t cols) {
     const Spread s = spread_of(cols);
     if (s.v == 0) return wide_strips(rows);
-    return std::max(grad_blocks(rows, s), grad_row_blocks(rows, row_spread(rows, cols, TPGEMM_ELEM_F16, true)));
+    // (The workspace does not hang on the rows' type.)
+    int most = grad_blocks(rows, s);
+    for (const int elem : {TPGEMM_ELEM_F16, TPGEMM_ELEM_F32})
+        most = std::max(most, grad_row_blocks(rows, row_spread(rows, cols, elem, true)));
+    return most;
 }
 
 cudaError_t launch_layernorm_grad(const LayerNormGradOp& op, cudaStream_t stream) {

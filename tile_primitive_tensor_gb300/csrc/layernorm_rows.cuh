@@ -139,31 +139,27 @@ __device__ __forceinline__ void normalise(const LayerNormOp& op, const Stats& st
 }
 
 // ------------------------------------------------------------ aligned rows
-// A thread's places for rows to come: `depth` rows of `inputs` matrices, V groups of
-// eight columns each. Only the thread itself writes and reads them, so no barrier is
-// needed, and a warp's accesses are contiguous.
-template <typename T, int V, int STEP>  // STEP: 16-byte units between a thread's places
+// A team takes a row in pieces of 16 bytes: piece i of thread t holds the columns from
+// kCols (i threads + t) on, so that a warp's accesses are contiguous.
+template <typename T>
+constexpr int kCols = 16 / int(sizeof(T));
+
+// A thread's places for rows to come: `depth` rows of `inputs` matrices, P pieces
+// each. Only the thread itself writes and reads them, so no barrier is needed.
+template <typename T, int P, int STEP>  // STEP: 16-byte units between a thread's places
 struct Ring {
-    uint4* mine;     // the thread's first place
-    int row_units;   // from one row to the next
+    uint4* mine;    // the thread's first place
+    int row_units;  // from one row to the next
     int depth;
     __device__ __forceinline__ Ring(void* smem, int depth, int inputs)
-        : mine(static_cast<uint4*>(smem) + threadIdx.x), row_units(inputs * V * kUnits<T> * STEP), depth(depth) {}
-    // The place of a row, and from there those of its groups.
+        : mine(static_cast<uint4*>(smem) + threadIdx.x), row_units(inputs * P * STEP), depth(depth) {}
+    // The place of a row, and from there those of its pieces.
     __device__ __forceinline__ uint4* row(int slot) const { return mine + slot * row_units; }
-    __device__ __forceinline__ static constexpr int place(int input, int group, int unit) {
-        return ((input * V + group) * kUnits<T> + unit) * STEP;
+    __device__ __forceinline__ void fetch(uint4* row, int input, int piece, const T* p) const {
+        cp_async_16(smem_u32(row + (input * P + piece) * STEP), p, 16);
     }
-    __device__ __forceinline__ void fetch(uint4* row, int input, int group, const T* p) const {
-#pragma unroll
-        for (int u = 0; u < kUnits<T>; ++u)
-            cp_async_16(smem_u32(row + place(input, group, u)), reinterpret_cast<const uint4*>(p) + u, 16);
-    }
-    __device__ __forceinline__ void get(const uint4* row, int input, int group, F2 (&f)[4]) const {
-        uint4 v[kUnits<T>];
-#pragma unroll
-        for (int u = 0; u < kUnits<T>; ++u) v[u] = row[place(input, group, u)];
-        unpack_pairs<T>(v, f);
+    __device__ __forceinline__ void get(const uint4* row, int input, int piece, F2 (&f)[kPairs<T>]) const {
+        unpack_pairs<T>(row[(input * P + piece) * STEP], f);
     }
     // The oldest of `depth` rows in flight (a group of copies each) has arrived.
     __device__ __forceinline__ void wait() const {
@@ -177,13 +173,13 @@ struct Ring {
 };
 constexpr int kMaxDepth = 4;
 
-// A spread of aligned rows: V groups of eight columns to a thread of a team of T
-// threads (T = 0: any team), all of them in the row (WHOLE) or not. T is a constant
-// since places and addresses then are: 8192 x 4096 bf16 with dropout takes 55 us so,
-// 62 otherwise. Threads of a block at most, and blocks to an SM at least, by the
-// registers that a thread then has: the norm does with 64, the gradients, which hold
-// 16 sums for each group, with 128.
-template <int V, int T, bool GRAD>
+// A spread of aligned rows: P pieces to a thread of a team of T threads (T = 0: any
+// team), all of them in the row (WHOLE) or not. T is a constant since places and
+// addresses then are: 8192 x 4096 bf16 with dropout takes 55 us so, 62 otherwise.
+// Threads of a block at most, and blocks to an SM at least, by the registers that a
+// thread then has: the norm does with 64, the gradients, which hold two sums for
+// each column, with 128.
+template <int T, bool GRAD>
 struct RowKernel {
     static constexpr int kThreads = T == 0 && !GRAD ? kMaxTeam : GRAD && T != 0 && T <= 256 ? 256 : 512;
     static constexpr int kBlocks = T == 0 ? 1 : GRAD && T == 512 ? 1 : 2;
@@ -195,37 +191,43 @@ struct RingPlan {
     int team, depth, weights_at;
 };
 
-// Gamma and beta: held in shared memory behind the ring, for all teams of a block
-// (from L2 they would come in the midst of every row), or, of rows too wide for
-// that, read from memory.
-template <typename XT, int V>
+// Gamma and beta, of XT or 32-bit: held in shared memory behind the ring, for all
+// teams of a block (from L2 they would come in the midst of every row), or, of rows
+// too wide for that, read from memory.
+template <typename XT, int P>
 struct Weights {
     const uint4* mine;  // the thread's first place; null: not held
     int elem, step;     // their type, and 16-byte units between a thread's places
+    // Units of a piece's columns.
     template <typename T>
-    __device__ __forceinline__ void get_as(int which, int group, const void* p, int c, F2 (&f)[4]) const {
-        uint4 v[kUnits<T>];
+    static constexpr int kUnits = kCols<XT> / kCols<T>;
+    template <typename T>
+    __device__ __forceinline__ void get_as(int which, int piece, const void* p, int c, F2 (&f)[kPairs<XT>]) const {
+#pragma unroll
+        for (int u = 0; u < kUnits<T>; ++u) {
+            const uint4 v = mine ? mine[((which * P + piece) * kUnits<T> + u) * step]
+                                 : reinterpret_cast<const uint4*>(static_cast<const T*>(p) + c)[u];
+            F2 part[kPairs<T>];
+            unpack_pairs<T>(v, part);
+#pragma unroll
+            for (int j = 0; j < kPairs<T>; ++j) f[u * kPairs<T> + j] = part[j];
+        }
+    }
+    __device__ __forceinline__ void get(int which, int piece, const void* p, int c, F2 (&f)[kPairs<XT>]) const {
+        if (elem == TPGEMM_ELEM_F32) get_as<float>(which, piece, p, c, f);
+        else get_as<XT>(which, piece, p, c, f);
+    }
+    template <typename T>
+    __device__ __forceinline__ void fetch_as(int which, int piece, const void* p, int c) const {
 #pragma unroll
         for (int u = 0; u < kUnits<T>; ++u)
-            v[u] = mine ? mine[((which * V + group) * kUnits<T> + u) * step]
-                        : reinterpret_cast<const uint4*>(static_cast<const T*>(p) + c)[u];
-        unpack_pairs<T>(v, f);
-    }
-    __device__ __forceinline__ void get(int which, int group, const void* p, int c, F2 (&f)[4]) const {
-        if (elem == TPGEMM_ELEM_F32) get_as<float>(which, group, p, c, f);
-        else get_as<XT>(which, group, p, c, f);
-    }
-    // By one team, a group of copies.
-    __device__ __forceinline__ void fetch(int which, int group, const void* p, int c) const {
-        if (elem == TPGEMM_ELEM_F32) fetch_as<float>(which, group, p, c);
-        else fetch_as<XT>(which, group, p, c);
-    }
-    template <typename T>
-    __device__ __forceinline__ void fetch_as(int which, int group, const void* p, int c) const {
-#pragma unroll
-        for (int u = 0; u < kUnits<T>; ++u)
-            cp_async_16(smem_u32(mine + ((which * V + group) * kUnits<T> + u) * step),
+            cp_async_16(smem_u32(mine + ((which * P + piece) * kUnits<T> + u) * step),
                         reinterpret_cast<const uint4*>(static_cast<const T*>(p) + c) + u, 16);
+    }
+    // By one team.
+    __device__ __forceinline__ void fetch(int which, int piece, const void* p, int c) const {
+        if (elem == TPGEMM_ELEM_F32) fetch_as<float>(which, piece, p, c);
+        else fetch_as<XT>(which, piece, p, c);
     }
 };
 
@@ -280,48 +282,58 @@ struct Team {
     }
 };
 
-// The sum of four pairs' two sums.
-__device__ __forceinline__ float sum_of(const F2 (&f)[4]) {
+template <int N>
+__device__ __forceinline__ void zero(F2 (&f)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = f2(0.f);
+}
+
+template <int N>
+__device__ __forceinline__ float sum_of(const F2 (&f)[N]) {
+    F2 v = add(f[0], f[1]);
+    if constexpr (N == 4) v = add(v, add(f[2], f[3]));
     float a, b;
-    split(add(add(f[0], f[1]), add(f[2], f[3])), a, b);
+    split(v, a, b);
     return a + b;
 }
 
-// Dropout of eight neighbouring elements from column c on, but for the factor.
-__device__ __forceinline__ void keep8(const Drop& d, const DropRow& w, int c, F2 (&f)[4]) {
-    float x[8];
+// Dropout of 2 N neighbouring elements from column c on, but for the factor.
+template <int N>
+__device__ __forceinline__ void keep_pairs(const Drop& d, const DropRow& w, int c, F2 (&f)[N]) {
+    float x[2 * N];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) split(f[i], x[2 * i], x[2 * i + 1]);
-    keep4(d, w, uint32_t(c) / 4, x);
-    keep4(d, w, uint32_t(c) / 4 + 1, x + 4);
+    for (int i = 0; i < N; ++i) split(f[i], x[2 * i], x[2 * i + 1]);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = f2(x[2 * i], x[2 * i + 1]);
+    for (int i = 0; i < N / 2; ++i) keep4(d, w, uint32_t(c) / 4 + i, x + 4 * i);
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = f2(x[2 * i], x[2 * i + 1]);
 }
 
-template <typename XT, int V, int T, bool WHOLE, bool DROP>
-__global__ void __launch_bounds__(RowKernel<V, T, false>::kThreads, RowKernel<V, T, false>::kBlocks)
+template <typename XT, int P, int T, bool WHOLE, bool DROP>
+__global__ void __launch_bounds__(RowKernel<T, false>::kThreads, RowKernel<T, false>::kBlocks)
     layernorm_rows_kernel(const __grid_constant__ LayerNormOp op, const RingPlan plan) {
+    constexpr int N = kPairs<XT>;
     extern __shared__ __align__(16) uint8_t ring_smem[];
     __shared__ float2 s[3][32];
     const Team<T> team(plan.team);
     const int64_t teams = blockDim.x / unsigned(team.threads()), stride = gridDim.x * teams;
     int64_t row = blockIdx.x * teams + team.index;
     const int cols = int(op.cols), depth = plan.depth;
-    const Ring<XT, V, RowKernel<V, T, false>::kThreads> ring(ring_smem, depth, op.R ? 2 : 1);
-    const Weights<XT, V> weights{
+    const Ring<XT, P, RowKernel<T, false>::kThreads> ring(ring_smem, depth, op.R ? 2 : 1);
+    const Weights<XT, P> weights{
         plan.weights_at ? reinterpret_cast<const uint4*>(ring_smem + plan.weights_at) + team.t : nullptr, op.g, team.threads()};
-    const auto column = [&](int i) { return 8 * (i * team.threads() + team.t); };
-    const auto has = [&](int i) { return WHOLE || column(i) < cols; };  // group i is in the row
+    const auto column = [&](int i) { return kCols<XT> * (i * team.threads() + team.t); };
+    const auto has = [&](int i) { return WHOLE || column(i) < cols; };  // piece i is in the row
     const auto fetch = [&](int64_t r, uint4* place) {
         if (r < op.rows) {
             const XT* x = static_cast<const XT*>(op.X) + r * op.ldx;
 #pragma unroll
-            for (int i = 0; i < V; ++i)
+            for (int i = 0; i < P; ++i)
                 if (has(i)) ring.fetch(place, 0, i, x + column(i));
             if (op.R) {
                 const XT* q = static_cast<const XT*>(op.R) + r * op.ldr;
 #pragma unroll
-                for (int i = 0; i < V; ++i)
+                for (int i = 0; i < P; ++i)
                     if (has(i)) ring.fetch(place, 1, i, q + column(i));
             }
         }
@@ -333,7 +345,7 @@ __global__ void __launch_bounds__(RowKernel<V, T, false>::kThreads, RowKernel<V,
     if (weights.mine) {
         if (team.index == 0)
 #pragma unroll
-            for (int i = 0; i < V; ++i)
+            for (int i = 0; i < P; ++i)
                 if (has(i)) {
                     weights.fetch(0, i, op.gamma, column(i));
                     if (op.beta) weights.fetch(1, i, op.beta, column(i));
@@ -351,21 +363,22 @@ __global__ void __launch_bounds__(RowKernel<V, T, false>::kThreads, RowKernel<V,
         if constexpr (DROP) w = drop_row(op.drop, offset, uint32_t(row));
         ring.wait();
         uint4* const place = ring.row(slot);
-        F2 h[V][4];
-        F2 part[4] = {f2(0.f), f2(0.f), f2(0.f), f2(0.f)};
+        F2 h[P][N];
+        F2 part[N];
+        zero(part);
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
+        for (int i = 0; i < P; ++i) {
             if (!has(i)) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) h[i][j] = f2(0.f);
+                zero(h[i]);
                 continue;
             }
             ring.get(place, 0, i, h[i]);
-            if constexpr (DROP) keep8(op.drop, w, column(i), h[i]);
-            F2 r[4] = {f2(0.f), f2(0.f), f2(0.f), f2(0.f)};
+            if constexpr (DROP) keep_pairs(op.drop, w, column(i), h[i]);
+            F2 r[N];
+            zero(r);
             if (op.R) ring.get(place, 1, i, r);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < N; ++j) {
                 h[i][j] = fma(h[i][j], scale, r[j]);
                 part[j] = add(part[j], h[i][j]);
             }
@@ -377,15 +390,17 @@ __global__ void __launch_bounds__(RowKernel<V, T, false>::kThreads, RowKernel<V,
         if (op.H) {
             XT* p = static_cast<XT*>(op.H) + row * op.ldh;
 #pragma unroll
-            for (int i = 0; i < V; ++i)
+            for (int i = 0; i < P; ++i)
                 if (has(i)) store_pairs<XT>(p + column(i), h[i]);
         }
-        F2 d[4] = {f2(0.f), f2(0.f), f2(0.f), f2(0.f)}, dd[4] = {f2(0.f), f2(0.f), f2(0.f), f2(0.f)};
+        F2 d[N], dd[N];
+        zero(d);
+        zero(dd);
 #pragma unroll
-        for (int i = 0; i < V; ++i)
+        for (int i = 0; i < P; ++i)
             if (has(i))
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
+                for (int j = 0; j < N; ++j) {
                     h[i][j] = add(h[i][j], f2(-mean));
                     d[j] = add(d[j], h[i][j]);
                     dd[j] = fma(h[i][j], h[i][j], dd[j]);
@@ -401,16 +416,17 @@ __global__ void __launch_bounds__(RowKernel<V, T, false>::kThreads, RowKernel<V,
         uint32_t amax = 0;
         const F2 rstd = f2(st.rstd), shift = f2(-st.off * st.rstd);
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
+        for (int i = 0; i < P; ++i) {
             if (!has(i)) continue;
-            F2 g[4], b[4] = {f2(0.f), f2(0.f), f2(0.f), f2(0.f)};
+            F2 g[N], b[N];
+            zero(b);
             weights.get(0, i, op.gamma, column(i), g);
             if (op.beta) weights.get(1, i, op.beta, column(i), b);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) h[i][j] = fma(fma(h[i][j], rstd, shift), g[j], b[j]);
+            for (int j = 0; j < N; ++j) h[i][j] = fma(fma(h[i][j], rstd, shift), g[j], b[j]);
             if (op.mode == TPGEMM_SCALE_ROW) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
+                for (int j = 0; j < N; ++j) {
                     float lo, hi;
                     split(h[i][j], lo, hi);
                     amax = max(amax, max(abs_bits(lo), abs_bits(hi)));
@@ -422,14 +438,14 @@ __global__ void __launch_bounds__(RowKernel<V, T, false>::kThreads, RowKernel<V,
             if (team.t == 0) op.scale[row] = to;
             const F2 inv = f2(1.f / to);
 #pragma unroll
-            for (int i = 0; i < V; ++i)
+            for (int i = 0; i < P; ++i)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) h[i][j] = mul(h[i][j], inv);
+                for (int j = 0; j < N; ++j) h[i][j] = mul(h[i][j], inv);
         }
         const auto store = [&](auto* y) {
             y += row * op.ldy;
 #pragma unroll
-            for (int i = 0; i < V; ++i)
+            for (int i = 0; i < P; ++i)
                 if (has(i)) store_pairs(y + column(i), h[i]);
         };
         switch (op.y) {
@@ -588,28 +604,29 @@ __global__ void __launch_bounds__(kMaxTeam) layernorm_wide_kernel(const __grid_c
 // dgamma and dbeta in registers; partial[block] gets the block's, dgamma's
 // columns and then dbeta's.
 //
-// Aligned rows, read ahead as by the norm. With more than two groups to a thread
+// Aligned rows, read ahead as by the norm. With more than 16 columns to a thread
 // what a reduction leaves to be used, w and n, is computed a second time from shared
 // memory in place of held in registers, which the columns' sums take. A block's
 // teams add up their sums in order at the end.
-template <typename XT, int V, int T, bool WHOLE, bool DROP>
-__global__ void __launch_bounds__(RowKernel<V, T, true>::kThreads, RowKernel<V, T, true>::kBlocks)
+template <typename XT, int P, int T, bool WHOLE, bool DROP>
+__global__ void __launch_bounds__(RowKernel<T, true>::kThreads, RowKernel<T, true>::kBlocks)
     layernorm_grad_rows_kernel(const __grid_constant__ LayerNormGradOp op, const RingPlan plan) {
+    constexpr int N = kPairs<XT>;
     extern __shared__ __align__(16) uint8_t ring_smem[];
     __shared__ float2 s[2][32];
     __shared__ float stats[kMaxDepth][16][2];  // mean and rstd of the rows ahead, for each warp
-    constexpr bool kAgain = V > 2;
+    constexpr bool kAgain = P * N > 8;
     const Team<T> team(plan.team);
     const int teams = int(blockDim.x) / team.threads();
     const int64_t stride = int64_t(gridDim.x) * teams;
     int64_t row = int64_t(blockIdx.x) * teams + team.index;
     const int cols = int(op.cols), depth = plan.depth;
     const bool rows_wanted = op.dX || op.dR, add_dh = rows_wanted && op.dH;
-    const Ring<XT, V, RowKernel<V, T, true>::kThreads> ring(ring_smem, depth, add_dh ? 3 : 2);
-    const Weights<XT, V> weights{
+    const Ring<XT, P, RowKernel<T, true>::kThreads> ring(ring_smem, depth, add_dh ? 3 : 2);
+    const Weights<XT, P> weights{
         plan.weights_at ? reinterpret_cast<const uint4*>(ring_smem + plan.weights_at) + team.t : nullptr, op.g, team.threads()};
-    const auto column = [&](int i) { return 8 * (i * team.threads() + team.t); };
-    const auto has = [&](int i) { return WHOLE || column(i) < cols; };  // group i is in the row
+    const auto column = [&](int i) { return kCols<XT> * (i * team.threads() + team.t); };
+    const auto has = [&](int i) { return WHOLE || column(i) < cols; };  // piece i is in the row
     const auto fetch = [&](int64_t r, int slot) {
         uint4* const place = ring.row(slot);
         if (r < op.rows) {
@@ -621,7 +638,7 @@ __global__ void __launch_bounds__(RowKernel<V, T, true>::kThreads, RowKernel<V, 
             const XT* h = static_cast<const XT*>(op.H) + r * op.ldh;
             const XT* dh = static_cast<const XT*>(op.dH) + (add_dh ? r * op.lddh : 0);
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
+            for (int i = 0; i < P; ++i) {
                 if (!has(i)) continue;
                 ring.fetch(place, 0, i, dy + column(i));
                 ring.fetch(place, 1, i, h + column(i));
@@ -636,7 +653,7 @@ __global__ void __launch_bounds__(RowKernel<V, T, true>::kThreads, RowKernel<V, 
     if (rows_wanted && weights.mine) {
         if (team.index == 0)
 #pragma unroll
-            for (int i = 0; i < V; ++i)
+            for (int i = 0; i < P; ++i)
                 if (has(i)) weights.fetch(0, i, op.gamma, column(i));
         cp_async_commit();
         cp_async_wait<0>();
@@ -645,45 +662,47 @@ __global__ void __launch_bounds__(RowKernel<V, T, true>::kThreads, RowKernel<V, 
     DropOffset offset{};
     if constexpr (DROP) offset = drop_offset(op.drop);
     const float inv_n = 1.f / float(op.cols);
-    F2 ag[V][4], ab[V][4];
+    F2 ag[P][N], ab[P][N];
 #pragma unroll
-    for (int i = 0; i < V; ++i)
+    for (int i = 0; i < P; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) ag[i][j] = ab[i][j] = f2(0.f);
+        for (int j = 0; j < N; ++j) ag[i][j] = ab[i][j] = f2(0.f);
     for (int slot = 0, turn = 0; row < op.rows; row += stride, turn ^= 1, slot = slot + 1 == depth ? 0 : slot + 1) {
         ring.wait();
         __syncwarp();
         const float mean = stats[slot][threadIdx.x >> 5][0], rstd = stats[slot][threadIdx.x >> 5][1];
         uint4* const place = ring.row(slot);
-        F2 kept_w[kAgain ? 1 : V][4], kept_n[kAgain ? 1 : V][4];
-        // dY and (H - mean) rstd of group i.
-        const auto load = [&](int i, F2 (&w)[4], F2 (&n)[4]) {
+        F2 kept_w[kAgain ? 1 : P][N], kept_n[kAgain ? 1 : P][N];
+        // dY and (H - mean) rstd of piece i.
+        const auto load = [&](int i, F2 (&w)[N], F2 (&n)[N]) {
             ring.get(place, 0, i, w);
             ring.get(place, 1, i, n);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) n[j] = mul(add(n[j], f2(-mean)), f2(rstd));
+            for (int j = 0; j < N; ++j) n[j] = mul(add(n[j], f2(-mean)), f2(rstd));
         };
-        const auto times_gamma = [&](int i, F2 (&w)[4]) {
-            F2 g[4];
+        const auto times_gamma = [&](int i, F2 (&w)[N]) {
+            F2 g[N];
             weights.get(0, i, op.gamma, column(i), g);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) w[j] = mul(w[j], g[j]);
+            for (int j = 0; j < N; ++j) w[j] = mul(w[j], g[j]);
         };
-        F2 pw[4] = {f2(0.f), f2(0.f), f2(0.f), f2(0.f)}, pn[4] = {f2(0.f), f2(0.f), f2(0.f), f2(0.f)};
+        F2 pw[N], pn[N];
+        zero(pw);
+        zero(pn);
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
+        for (int i = 0; i < P; ++i) {
             if (!has(i)) continue;
-            F2 (&w)[4] = kept_w[kAgain ? 0 : i], (&n)[4] = kept_n[kAgain ? 0 : i];
+            F2 (&w)[N] = kept_w[kAgain ? 0 : i], (&n)[N] = kept_n[kAgain ? 0 : i];
             load(i, w, n);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < N; ++j) {
                 ag[i][j] = fma(w[j], n[j], ag[i][j]);
                 ab[i][j] = add(ab[i][j], w[j]);
             }
             if (rows_wanted) {
                 times_gamma(i, w);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
+                for (int j = 0; j < N; ++j) {
                     pw[j] = add(pw[j], w[j]);
                     pn[j] = fma(w[j], n[j], pn[j]);
                 }
@@ -696,23 +715,24 @@ __global__ void __launch_bounds__(RowKernel<V, T, true>::kThreads, RowKernel<V, 
             DropRow words{};
             if constexpr (DROP) words = drop_row(op.drop, offset, uint32_t(row));
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
+            for (int i = 0; i < P; ++i) {
                 if (!has(i)) continue;
-                F2 (&w)[4] = kept_w[kAgain ? 0 : i], (&n)[4] = kept_n[kAgain ? 0 : i];
+                F2 (&w)[N] = kept_w[kAgain ? 0 : i], (&n)[N] = kept_n[kAgain ? 0 : i];
                 if constexpr (kAgain) {
                     load(i, w, n);
                     times_gamma(i, w);
                 }
-                F2 dt[4] = {f2(0.f), f2(0.f), f2(0.f), f2(0.f)};
+                F2 dt[N];
+                zero(dt);
                 if (add_dh) ring.get(place, 2, i, dt);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) dt[j] = fma(fma(n[j], swn, add(w[j], sw)), f2(rstd), dt[j]);
+                for (int j = 0; j < N; ++j) dt[j] = fma(fma(n[j], swn, add(w[j], sw)), f2(rstd), dt[j]);
                 if (op.dR) store_pairs<XT>(static_cast<XT*>(op.dR) + row * op.lddr + column(i), dt);
                 if (op.dX) {
                     if constexpr (DROP) {
-                        keep8(op.drop, words, column(i), dt);
+                        keep_pairs(op.drop, words, column(i), dt);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) dt[j] = mul(dt[j], f2(op.drop.scale));
+                        for (int j = 0; j < N; ++j) dt[j] = mul(dt[j], f2(op.drop.scale));
                     }
                     store_pairs<XT>(static_cast<XT*>(op.dX) + row * op.lddx + column(i), dt);
                 }
@@ -726,7 +746,7 @@ __global__ void __launch_bounds__(RowKernel<V, T, true>::kThreads, RowKernel<V, 
     float* out = op.partial + int64_t(blockIdx.x) * 2 * op.cols;
     if (teams == 1) {
 #pragma unroll
-        for (int i = 0; i < V; ++i)
+        for (int i = 0; i < P; ++i)
             if (has(i)) {
                 store_pairs<float>(out + column(i), ag[i]);
                 store_pairs<float>(out + op.cols + column(i), ab[i]);
@@ -735,11 +755,11 @@ __global__ void __launch_bounds__(RowKernel<V, T, true>::kThreads, RowKernel<V, 
     }
     // Through the ring's place, where nothing is on its way: gamma's sums, then beta's.
     float* const sums = reinterpret_cast<float*>(ring_smem);  // [teams][padded columns]
-    const int pitch = 8 * V * team.threads();
-    const auto join = [&](const F2 (&a)[V][4], float* to) {
+    const int pitch = kCols<XT> * P * team.threads();
+    const auto join = [&](const F2 (&a)[P][N], float* to) {
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < V; ++i) store_pairs<float>(sums + team.index * pitch + column(i), a[i]);
+        for (int i = 0; i < P; ++i) store_pairs<float>(sums + team.index * pitch + column(i), a[i]);
         __syncthreads();
         for (int c = int(threadIdx.x); c < cols; c += int(blockDim.x)) {
             float v = 0.f;
@@ -927,34 +947,37 @@ Spread spread_of(int64_t cols) {
 }
 
 // Aligned rows of up to kMaxHeld columns. A reduction costs each warp that takes
-// part as many instructions as two groups of columns, so the norm of 16-bit rows has
-// four groups to a thread; two where the rows' bytes or the columns' sums are twice
-// as many; one or two of rows that a warp then holds whole; and of few rows one, for
-// the shortest time to the end.
+// part as many instructions as 16 columns, so the norm has four pieces to a thread,
+// its gradients 16 columns; fewer of rows that a warp then holds whole; twice as many
+// of rows wider than 512 such threads; and of few rows one, for the shortest time to
+// the end.
+constexpr int most_pieces(int elem, bool grad) { return grad && elem != TPGEMM_ELEM_F32 ? 2 : 4; }
+
 struct RowSpread {
-    int v, t;         // the kernel's V and T
+    int p, t;         // the kernel's P and T
     bool whole;       // and WHOLE
     int team, teams;  // threads of a team, teams of a block
     int blocks;       // to an SM
     int threads() const { return team * teams; }
 };
 RowSpread row_spread(int64_t rows, int64_t cols, int elem, bool grad) {
-    const int groups = int((cols + 7) / 8);
-    const int most = elem == TPGEMM_ELEM_F32 || grad ? 2 : 4;
-    if (rows <= kSms && groups <= (grad ? 512 : kMaxTeam))
-        return {1, 0, false, (groups + 31) / 32 * 32, 1, 1};
-    int v = groups <= 32 ? 1 : groups <= 64 ? 2 : groups <= 512 * most ? most : 4, t = 32;
-    while (t * v < groups) t *= 2;
-    if (v == 4 && most == 2) t = 512;
+    const int pieces = int((cols * elem_size(elem) + 15) / 16), most = most_pieces(elem, grad);
+    if (rows <= kSms && pieces <= (grad ? 512 : kMaxTeam))
+        return {1, 0, false, (pieces + 31) / 32 * 32, 1, 1};
+    int p = 1, t = 32;
+    while (p < most && t * p < pieces) p *= 2;
+    while (t < 512 && t * p < pieces) t *= 2;
+    if (t * p < pieces) p *= 2;
     const int threads = grad && t <= 256 ? 256 : 512;
     const int teams = int(std::max<int64_t>(1, std::min<int64_t>(threads / t, rows / kSms)));
-    return {v, t, t * v == groups, t, teams, std::min((grad ? 512 : 1024) / (t * teams), 8)};
+    return {p, t, t * p == pieces, t, teams, std::min((grad ? 512 : 1024) / (t * teams), 8)};
 }
 
 constexpr int kRingBytes = 216 * 1024;  // of an SM, for its blocks
+// `step`: threads that a block's places are laid out for.
 RingPlan ring_plan(RowSpread* s, int step, int inputs, int elem, int vectors, int vector_elem, size_t* bytes) {
-    const size_t row = size_t(inputs) * s->v * step * 8 * elem_size(elem);  // of all teams
-    size_t held = size_t(vectors) * s->v * s->team * 8 * elem_size(vector_elem);
+    const size_t row = size_t(inputs) * s->p * step * 16;  // of all teams
+    size_t held = size_t(vectors) * s->p * s->team * 16 * elem_size(vector_elem) / elem_size(elem);
     while (s->blocks > 1 && held + row > size_t(kRingBytes / s->blocks)) --s->blocks;
     const size_t have = size_t(kRingBytes / s->blocks);
     if (held + row > have) held = 0;
@@ -963,27 +986,31 @@ RingPlan ring_plan(RowSpread* s, int step, int inputs, int elem, int vectors, in
     return {s->team, depth, held ? int(depth * row) : 0};
 }
 
-// f(V, T, WHOLE) of the spread's kernel, as integral constants; MOST as in row_spread.
-template <int MOST, typename F>
+// f(P, T, WHOLE) of the spread's kernel, as integral constants. TWICE: whether rows
+// of up to kMaxHeld columns come to more than MOST pieces.
+template <int MOST, bool TWICE, typename F>
 cudaError_t with_spread(const RowSpread& s, F&& f) {
-    using std::integral_constant;
-    const auto call = [&](auto v, auto t) {
-        return s.whole ? f(v, t, std::true_type()) : f(v, t, std::false_type());
+    const auto call = [&](auto p, auto t) {
+        return s.whole ? f(p, t, std::true_type()) : f(p, t, std::false_type());
     };
-    constexpr integral_constant<int, MOST> most{};
-    if (s.t == 0) return f(integral_constant<int, 1>(), integral_constant<int, 0>(), std::false_type());
-    if (s.v == 1) return call(integral_constant<int, 1>(), integral_constant<int, 32>());
-    if (s.v == MOST) {
+    constexpr std::integral_constant<int, 1> one{};
+    constexpr std::integral_constant<int, 2> two{};
+    constexpr std::integral_constant<int, MOST> most{};
+    constexpr std::integral_constant<int, 32> t32{};
+    constexpr std::integral_constant<int, 512> t512{};
+    if (s.t == 0) return f(one, std::integral_constant<int, 0>(), std::false_type());
+    if constexpr (TWICE)
+        if (s.p > MOST) return call(std::integral_constant<int, 2 * MOST>(), t512);
+    if (s.p == MOST) {
         switch (s.t) {
-            case 32: return call(most, integral_constant<int, 32>());
-            case 64: return call(most, integral_constant<int, 64>());
-            case 128: return call(most, integral_constant<int, 128>());
-            case 256: return call(most, integral_constant<int, 256>());
-            default: return call(most, integral_constant<int, 512>());
+            case 32: return call(most, t32);
+            case 64: return call(most, std::integral_constant<int, 64>());
+            case 128: return call(most, std::integral_constant<int, 128>());
+            case 256: return call(most, std::integral_constant<int, 256>());
+            default: return call(most, t512);
         }
     }
-    if constexpr (MOST == 2) return call(integral_constant<int, 4>(), integral_constant<int, 512>());
-    else return call(integral_constant<int, 2>(), integral_constant<int, 32>());
+    return MOST > 2 && s.p == 2 ? call(two, t32) : call(one, t32);
 }
 
 template <typename F, typename Op>
@@ -998,13 +1025,13 @@ cudaError_t launch_ring(F fn, int64_t blocks, int threads, size_t bytes, const R
 template <typename XT, bool DROP>
 cudaError_t launch_rows(const LayerNormOp& op, cudaStream_t stream) {
     RowSpread s = row_spread(op.rows, op.cols, op.x, false);
-    return with_spread<sizeof(XT) == 4 ? 2 : 4>(s, [&](auto v, auto t, auto whole) {
-        constexpr int V = decltype(v)::value, T = decltype(t)::value;
+    return with_spread<4, sizeof(XT) == 4>(s, [&](auto p, auto t, auto whole) {
+        constexpr int P = decltype(p)::value, T = decltype(t)::value;
         size_t bytes;
-        const RingPlan plan = ring_plan(&s, RowKernel<V, T, false>::kThreads, op.R ? 2 : 1, op.x, op.beta ? 2 : 1,
+        const RingPlan plan = ring_plan(&s, RowKernel<T, false>::kThreads, op.R ? 2 : 1, op.x, op.beta ? 2 : 1,
                                         op.g, &bytes);
         const int64_t blocks = std::min<int64_t>((op.rows + s.teams - 1) / s.teams, int64_t(kSms) * s.blocks);
-        return launch_ring(layernorm_rows_kernel<XT, V, T, decltype(whole)::value, DROP>, blocks, s.threads(), bytes,
+        return launch_ring(layernorm_rows_kernel<XT, P, T, decltype(whole)::value, DROP>, blocks, s.threads(), bytes,
                            plan, stream, op);
     });
 }
@@ -1059,14 +1086,14 @@ template <typename XT, bool DROP>
 cudaError_t launch_grad(const LayerNormGradOp& op, const Spread& u, bool vec, int* strips, cudaStream_t stream) {
     if (vec) {
         RowSpread s = row_spread(op.rows, op.cols, op.x, true);
-        return with_spread<2>(s, [&](auto v, auto t, auto whole) {
-            constexpr int V = decltype(v)::value, T = decltype(t)::value;
+        return with_spread<sizeof(XT) == 4 ? 4 : 2, true>(s, [&](auto p, auto t, auto whole) {
+            constexpr int P = decltype(p)::value, T = decltype(t)::value;
             size_t bytes;
-            const RingPlan plan = ring_plan(&s, RowKernel<V, T, true>::kThreads, op.dH && (op.dX || op.dR) ? 3 : 2, op.x,
+            const RingPlan plan = ring_plan(&s, RowKernel<T, true>::kThreads, op.dH && (op.dX || op.dR) ? 3 : 2, op.x,
                                             1, op.g, &bytes);
-            if (s.teams > 1) bytes = std::max(bytes, size_t(V) * s.threads() * 8 * 4);  // (the teams' sums)
+            if (s.teams > 1) bytes = std::max(bytes, size_t(P) * kCols<XT> * s.threads() * 4);  // (the teams' sums)
             *strips = grad_row_blocks(op.rows, s);
-            return launch_ring(layernorm_grad_rows_kernel<XT, V, T, decltype(whole)::value, DROP>, *strips, s.threads(),
+            return launch_ring(layernorm_grad_rows_kernel<XT, P, T, decltype(whole)::value, DROP>, *strips, s.threads(),
                                bytes, plan, stream, op);
         });
     }

@@ -120,9 +120,26 @@ __global__ void __launch_bounds__(kThreads, 4)
 //   dZ[m, n] = dY u act'(g),  dZ[m, N + n] = dY act(g),
 // with the sums of both. A thread takes eight outputs, from dY and both halves of
 // Z, and loads the next row while it computes one.
-template <typename T, int ACT, int SIDE>
-__device__ __forceinline__ void gated_grad_strip(const ActGradOp& op, int strips, bool vec, float (&sg)[kPer],
-                                                 float (&su)[kPer]) {
+//
+// A 32-bit dW takes dZ as two 16-bit values, its rounding and what that left (REST):
+// from the rounding alone it would be off by 2^-9 (bf16) or 2^-12 (f16) of its
+// terms. The rest of an f16 value may lie below f16's normal numbers, so it is kept
+// 2^11 times as large, which fits f16 for every rounding that does.
+template <typename T>
+constexpr float kRestScale = std::is_same<T, __half>::value ? 1.f / 2048.f : 1.f;
+
+template <typename T>
+__device__ __forceinline__ void rest_of(const float (&x)[8], float (&low)[8]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float high = to_f32(from_f32<T>(x[j]));
+        low[j] = isinf(high) ? 0.f : (x[j] - high) * (1.f / kRestScale<T>);  // (a NaN stays one)
+    }
+}
+
+template <typename T, int ACT, int SIDE, bool REST>
+__device__ __forceinline__ void gated_grad_strip(const ActGradOp& op, void* rest, int strips, bool vec,
+                                                 float (&sg)[kPer], float (&su)[kPer]) {
     const int t = threadIdx.x % SIDE, lane_row = threadIdx.x / SIDE;
     const int64_t n = (int64_t(blockIdx.x) * SIDE + t) * kPer;
     const int64_t m_begin = op.M * blockIdx.y / strips, m_end = op.M * (blockIdx.y + 1) / strips;
@@ -142,6 +159,13 @@ __device__ __forceinline__ void gated_grad_strip(const ActGradOp& op, int strips
         if (op.dZ) {
             store8<T>(op.dZ, m * op.lddz + n, vec, cnt, dg);
             store8<T>(op.dZ, m * op.lddz + op.N + n, vec, cnt, du);
+        }
+        if constexpr (REST) {
+            float low[8];
+            rest_of<T>(dg, low);
+            store8<T>(rest, m * op.lddz + n, vec, cnt, low);
+            rest_of<T>(du, low);
+            store8<T>(rest, m * op.lddz + op.N + n, vec, cnt, low);
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -179,17 +203,24 @@ __device__ __forceinline__ void gated_grad_strip(const ActGradOp& op, int strips
     }
 }
 
-template <typename T, int SIDE>
+template <typename T, int SIDE, bool REST>
 __global__ void __launch_bounds__(kThreads, 3)
-    gated_grad_kernel(const __grid_constant__ ActGradOp op, int strips, bool vec) {
+    gated_grad_kernel(const __grid_constant__ ActGradOp op, const DzRest rest, int strips, bool vec) {
     constexpr int kRows = kThreads / SIDE, kCols = SIDE * kPer;
     __shared__ float s[kRows][2][kCols];
     grid_launch_dependents();
     grid_dependency_wait();
     float sg[kPer] = {}, su[kPer] = {};
     with_act(op.act, [&](auto act) {
-        gated_grad_strip<T, decltype(act)::value, SIDE>(op, strips, vec, sg, su);
+        gated_grad_strip<T, decltype(act)::value, SIDE, REST>(op, rest.low, strips, vec, sg, su);
     });
+    if constexpr (REST) {
+        if (blockIdx.y == 0)
+            for (int i = threadIdx.x; i < 2 * kCols; i += kThreads) {
+                const int64_t n = int64_t(blockIdx.x) * kCols + i % kCols;
+                if (n < op.N) rest.scale[n + (i / kCols) * op.N] = kRestScale<T>;
+            }
+    }
     if (!op.dbias) return;
     const int t = threadIdx.x % SIDE, lane_row = threadIdx.x / SIDE;
 #pragma unroll
@@ -290,7 +321,8 @@ cudaError_t launch_act_grad(const ActGradOp& op, cudaStream_t stream) {
 
 int gated_grad_strips(int64_t M, int64_t N) { return act_grad_strips(M, N); }
 
-cudaError_t launch_gated_grad(const ActGradOp& op, cudaStream_t stream) {
+template <typename T, bool REST>
+static cudaError_t launch_gated_typed(const ActGradOp& op, const DzRest& rest, cudaStream_t stream) {
     const int strips = gated_grad_strips(op.M, op.N);
     const bool few = strips == 1;
     const int cols = (few ? kNarrow : kWide) * kPer;
@@ -300,13 +332,19 @@ cudaError_t launch_gated_grad(const ActGradOp& op, cudaStream_t stream) {
         return !p || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && (op.M <= 1 || ld % 8 == 0));
     };
     const bool vec = op.N % 8 == 0 && rows16(op.dY, op.lddy) && rows16(op.Z, op.ldz) && rows16(op.dZ, op.lddz);
-    const bool f16 = op.dtype == TPGEMM_ELEM_F16;
-    auto fn = few ? (f16 ? gated_grad_kernel<__half, kNarrow> : gated_grad_kernel<__nv_bfloat16, kNarrow>)
-                  : (f16 ? gated_grad_kernel<__half, kWide> : gated_grad_kernel<__nv_bfloat16, kWide>);
+    auto fn = few ? gated_grad_kernel<T, kNarrow, REST> : gated_grad_kernel<T, kWide, REST>;
     const cudaError_t e = launch_dependent(fn, dim3(unsigned(cb), unsigned(strips)), dim3(kThreads), 0, stream, op,
-                                           strips, vec);
+                                           rest, strips, vec);
     if (e != cudaSuccess || !op.dbias || few) return e;
     return launch_column_sum(op.partial, strips, 2 * op.N, op.dbias, op.grad, stream);
+}
+
+cudaError_t launch_gated_grad(const ActGradOp& op, const DzRest& rest, cudaStream_t stream) {
+    if (op.dtype == TPGEMM_ELEM_F16)
+        return rest.low ? launch_gated_typed<__half, true>(op, rest, stream)
+                        : launch_gated_typed<__half, false>(op, rest, stream);
+    return rest.low ? launch_gated_typed<__nv_bfloat16, true>(op, rest, stream)
+                    : launch_gated_typed<__nv_bfloat16, false>(op, rest, stream);
 }
 
 constexpr int64_t kAlignBlocks = 8 * kSms;  // eight to an SM; a warp then has several rows' loads in flight

@@ -188,7 +188,7 @@ double straddle(const LinearOp& op, bool swap) {
 // counting a fifth more, since shorter boxes stream more slowly (17 x 4096 x
 // 4096 bf16, split / rows: 8 / 128 8.1 us, 4 / 128 8.5, 2 / 64 13.9; 144 rows:
 // 4 / 128 12.3, 2 / 64 15.4).
-Choice plan_split(const LinearOp& op, int64_t kb, const LinearTuning& t, int64_t tiles_q) {
+Choice plan_split(const LinearOp& op, int64_t kb, const LinearTuning& t, int64_t tiles_q, int least) {
     Choice best;
     // The output's longer side along the lanes; Q in tiles of equal width.
     const bool swap = op.N >= op.M;
@@ -212,6 +212,7 @@ Choice plan_split(const LinearOp& op, int64_t kb, const LinearTuning& t, int64_t
         if (t.split == 1 || t.split == 2 || t.split == 4 || t.split == 8)
             for (split = t.split; split > kb; split /= 2) {
             }
+        split = std::max(split, least);
         const int64_t ctas = tiles * split;
         const int64_t fit = places(split, half_sm);
         const double filled = double(std::min(ctas, fit)) / double(places(1, half_sm)) * (bp == 128 ? 1.2 : 1.0);
@@ -236,14 +237,25 @@ Choice plan_split(const LinearOp& op, int64_t kb, const LinearTuning& t, int64_t
 // split shallower, so that less passes between SMs but P is read more often
 // (512 x 1024 x 4096 bf16, tiles of Q / split: 2 / 4 15.3 us, 3 / 4 12.4, 4 / 4
 // 11.5; 144 x 4096 x 4096: 1 / 4 12.5, 2 / 2 14.8).
-Choice plan_split(const LinearOp& op, int64_t kb, const LinearTuning& t) {
+Choice plan_split(const LinearOp& op, int64_t kb, const LinearTuning& t, int least_split) {
     const int64_t Nq = std::min(op.M, op.N), least = ceil_div(Nq, 256);
     Choice best;
     for (int64_t q = least; q < least + 4 && q * 32 <= std::max(Nq, least * 32); ++q) {
-        const Choice c = plan_split(op, kb, t, q);
+        const Choice c = plan_split(op, kb, t, q, least_split);
         if (c.ns < best.ns) best = c;
     }
     return best;
+}
+
+// A gated 32-bit output is a product of two sums, and off by both of theirs: sums
+// of more than kLongSum terms are shared out to CTAs, whose shorter ones are added
+// with rounding (2048 x 2048 outputs of random signs, K = 16384 in four shares:
+// 8.2e-6 of their size).
+int least_split(const LinearOp& op) {
+    int split = 1;
+    if (op.gated && op.e.out == TPGEMM_ELEM_F32)
+        while (split < 8 && op.K > split * kLongSum) split *= 2;
+    return split;
 }
 
 }  // namespace
@@ -261,9 +273,10 @@ tpgemm_status run_linear_tc(const LinearOp& op, int sms, cudaStream_t stream) {
     p.timeout_ns = wait_timeout_ns();
     LinearOp wide = op;  // (see memory_ns)
     wide.N = weight_rows(op);
-    const Choice split = plan_split(wide, p.k_blocks, t);
+    const int least = least_split(op);
+    const Choice split = plan_split(wide, p.k_blocks, t, least);
     Choice c = plan_tile(wide, p.k_blocks, sms, t);
-    if (t.path == kLinearSplit || (t.path != kLinearTile && split.ns < c.ns)) c = split;
+    if (t.path == kLinearSplit || least > 1 || (t.path != kLinearTile && split.ns < c.ns)) c = split;
     if (c.bn == 0) return fail_with(TPGEMM_ERR_PATH, "the planner overrides leave no plan");
     p.pair = c.pair;
     p.swap = c.swap;

@@ -241,6 +241,7 @@ LinearLayout linear_layout(const tpg::LinearOp& op) {
 // ----------------------------------------------------- linear layer, backward
 struct GradLayout {
     size_t dz = 0, partial = 0, total = 0;
+    size_t rest = 0, rest_scale = 0;  // of dZ, for a 32-bit dW of the gated layer
     int64_t lddz = 0;
     Aligned dy, a, w;  // copies (dY's only where it is dZ itself)
 };
@@ -254,6 +255,11 @@ GradLayout grad_layout(const void* dY, const void* A, const void* W,
         L.lddz = int64_t(align_up(size_t(rows), 64));  // whole 128-byte lines
         L.dz = L.total;
         L.total = align_up(L.total + size_t(d.M) * size_t(L.lddz) * 2, 256);
+        if (gated && d.grad == TPGEMM_ELEM_F32) {
+            L.rest = L.total;
+            L.rest_scale = align_up(L.rest + size_t(d.M) * size_t(L.lddz) * 2, 256);
+            L.total = align_up(L.rest_scale + size_t(rows) * 4, 256);
+        }
     } else if (d.K > 0) {
         L.dy = plan_aligned({dY, dense(d.lddy, d.N), 0}, d.M, d.N, d.dtype, &L.total);
     }
@@ -372,7 +378,9 @@ tpgemm_status linear_gradients(bool gated, void* dA, void* dW, void* dbias, cons
                          (act && (dA || dW)) ? ws + L.dz : nullptr, L.lddz,
                          reinterpret_cast<float*>(ws + L.partial), dbias,
                          d->dtype, d->act, d->grad};
-        TPG_TRY(launched(gated ? tpg::launch_gated_grad(g, st) : tpg::launch_act_grad(g, st),
+        tpg::DzRest rest{};
+        if (L.rest && dW) rest = {ws + L.rest, reinterpret_cast<float*>(ws + L.rest_scale)};
+        TPG_TRY(launched(gated ? tpg::launch_gated_grad(g, rest, st) : tpg::launch_act_grad(g, st),
                          "activation gradient launch"));
     }
     if (act) {
@@ -397,7 +405,26 @@ tpgemm_status linear_gradients(bool gated, void* dA, void* dW, void* dbias, cons
         tpg::LinearOp op{rows, K, M, d->dtype, {oz.p, oz.ld, 1}, {oa.p, oa.ld, 1},
                          {dW, nullptr, nullptr, nullptr, nullptr, nullptr, out[1].ld, 0, 0,
                           TPGEMM_ACT_NONE, d->grad}};
-        TPG_TRY(run_product(op, sms, st));
+        // (A 32-bit dW of the gated layer: some tokens after the others, dW += ..., and
+        // then scale rest^T . A.)
+        const int64_t parts = L.rest ? (M + tpg::kLongSum - 1) / tpg::kLongSum : 1;
+        for (int64_t i = 0; i < parts; ++i) {
+            const int64_t begin = M * i / parts / 64 * 64, end = i + 1 == parts ? M : M * (i + 1) / parts / 64 * 64;
+            op.K = end - begin;
+            op.a.p = static_cast<const uint8_t*>(oz.p) + begin * oz.ld * 2;
+            op.b.p = static_cast<const uint8_t*>(oa.p) + begin * oa.ld * 2;
+            op.e.R = i > 0 ? dW : nullptr;
+            op.e.ldr = out[1].ld;
+            TPG_TRY(run_product(op, sms, st));
+        }
+        if (L.rest) {
+            op.K = M;
+            op.a.p = ws + L.rest;
+            op.b.p = oa.p;
+            op.e.R = dW;
+            op.e.sa = reinterpret_cast<const float*>(ws + L.rest_scale);
+            TPG_TRY(run_product(op, sms, st));
+        }
     }
     return TPGEMM_OK;
 }

@@ -33,6 +33,10 @@ LinearTuning linear_tuning();
 // column sums go by it too: results and workspaces are then the same everywhere.
 constexpr int kSms = 152;
 
+// Terms that tensor memory adds up in one go for a 32-bit result of the gated layer:
+// its additions truncate, so a sum is off by some 1.2e-9 of its size for each term.
+constexpr int64_t kLongSum = 4096;
+
 inline int elem_size(int elem) {
     return elem == TPGEMM_ELEM_F32 ? 4 : (elem == TPGEMM_ELEM_F16 || elem == TPGEMM_ELEM_BF16) ? 2 : 1;
 }
@@ -110,7 +114,13 @@ cudaError_t launch_act_grad(const ActGradOp& op, cudaStream_t stream);
 // The gated layer's: dZ [M][2 N] from dY [M][N] and Z [M][2 N], dbias [2 N],
 // partial [strips][2 N].
 int gated_grad_strips(int64_t M, int64_t N);
-cudaError_t launch_gated_grad(const ActGradOp& op, cudaStream_t stream);
+// What dZ lost to its rounding: low [M][lddz] = (dZ - its rounding) / scale[n], with
+// scale [2 N] a power of two; or null.
+struct DzRest {
+    void* low;
+    float* scale;
+};
+cudaError_t launch_gated_grad(const ActGradOp& op, const DzRest& rest, cudaStream_t stream);
 
 // Copies of matrices, each of rows of `bytes` bytes, `pitch` bytes apart, to rows
 // dst_pitch apart (dst and dst_pitch multiples of 16, dst_pitch >= bytes rounded

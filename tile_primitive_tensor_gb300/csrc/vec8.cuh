@@ -86,36 +86,49 @@ __device__ __forceinline__ void store8(void* base, int64_t at, bool vec, int n, 
     }
 }
 
-// Eight elements as pairs of 32-bit values, from and to their 16-byte units (one of
-// 16-bit elements, two of 32-bit ones).
+// Sixteen bytes of a type as pairs of 32-bit values: four pairs of 16-bit elements,
+// two of 32-bit ones.
 template <typename T>
-constexpr int kUnits = int(sizeof(T)) / 2;
+constexpr int kPairs = 8 / int(sizeof(T));
 
 template <typename T>
-__device__ __forceinline__ void unpack_pairs(const uint4 (&u)[kUnits<T>], F2 (&f)[4]) {
+__device__ __forceinline__ void unpack_pairs(const uint4& u, F2 (&f)[kPairs<T>]) {
     if constexpr (sizeof(T) == 4) {
-        f[0] = f2(__uint_as_float(u[0].x), __uint_as_float(u[0].y));
-        f[1] = f2(__uint_as_float(u[0].z), __uint_as_float(u[0].w));
-        f[2] = f2(__uint_as_float(u[1].x), __uint_as_float(u[1].y));
-        f[3] = f2(__uint_as_float(u[1].z), __uint_as_float(u[1].w));
+        f[0] = f2(__uint_as_float(u.x), __uint_as_float(u.y));
+        f[1] = f2(__uint_as_float(u.z), __uint_as_float(u.w));
     } else {
         float x[8];
-        unpack8<T>(u[0], x);
+        unpack8<T>(u, x);
 #pragma unroll
         for (int i = 0; i < 4; ++i) f[i] = f2(x[2 * i], x[2 * i + 1]);
     }
 }
 
-// Stores eight pairs' values to 16-byte (8-bit types: 8-byte) aligned memory.
-template <typename T>
-__device__ __forceinline__ void store_pairs(T* p, const F2 (&f)[4]) {
-    float x[8];
+// Stores N pairs as 2 N elements of T, aligned to all of them (to 16 bytes at most).
+template <typename T, int N>
+__device__ __forceinline__ void store_pairs(T* p, const F2 (&f)[N]) {
+    static_assert(N == 2 || N == 4, "four or eight elements");
+    float x[2 * N];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) split(f[i], x[2 * i], x[2 * i + 1]);
-    if constexpr (sizeof(T) == 1)
-        *reinterpret_cast<uint2*>(p) = pack8_fp8(x, std::is_same<T, e4m3>::value ? __NV_E4M3 : __NV_E5M2);
-    else
-        store8<T>(p, 0, true, 8, x);
+    for (int i = 0; i < N; ++i) split(f[i], x[2 * i], x[2 * i + 1]);
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < 2 * N; i += 4)
+            *reinterpret_cast<float4*>(p + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+    } else {
+        float y[8] = {};
+#pragma unroll
+        for (int i = 0; i < 2 * N; ++i) y[i] = x[i];
+        if constexpr (sizeof(T) == 1) {
+            const uint2 v = pack8_fp8(y, std::is_same<T, e4m3>::value ? __NV_E4M3 : __NV_E5M2);
+            if constexpr (N == 4) *reinterpret_cast<uint2*>(p) = v;
+            else *reinterpret_cast<uint32_t*>(p) = v.x;
+        } else {
+            const uint4 v = pack8<T>(y);
+            if constexpr (N == 4) *reinterpret_cast<uint4*>(p) = v;
+            else *reinterpret_cast<uint2*>(p) = make_uint2(v.x, v.y);
+        }
+    }
 }
 
 // Sixteen bytes at a row's byte `at`, whose address is a multiple of 16; those
