@@ -1225,7 +1225,8 @@ def layernorm(x, weight, bias=None, residual=None, *, eps=1e-5, dropout=None, qu
         scale = torch.empty(rows, dtype=torch.float32, device=device)
         ps = scale.data_ptr()
     if need_stats:
-        mean, rstd = torch.empty((2, rows), dtype=torch.float32, device=device)
+        mean = torch.empty(rows, dtype=torch.float32, device=device)
+        rstd = torch.empty(rows, dtype=torch.float32, device=device)
         pm, prstd = mean.data_ptr(), rstd.data_ptr()
     desc = LayerNormDesc(rows, cols, ldx, ldr, ldh, ldy, *codes, eps, _drop(dropout, index))
     _call(torch, index, lib.tpgemm_layernorm,

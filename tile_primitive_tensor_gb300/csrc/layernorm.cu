@@ -17,12 +17,12 @@ cudaError_t launch_layernorm(const LayerNormOp& op, cudaStream_t stream) {
 }
 
 int layernorm_grad_strips(int64_t rows, int64_t cols) {
-    const Spread s = spread_of(cols);
-    if (s.v == 0) return wide_strips(rows);
-    // (The workspace does not hang on the rows' type.)
-    int most = grad_blocks(rows, s);
+    if (cols > kMaxHeld) return wide_strips(rows);
+    // (The workspace does not hang on the rows' type and place.)
+    int most = 1;
     for (const int elem : {TPGEMM_ELEM_F16, TPGEMM_ELEM_F32})
-        most = std::max(most, grad_row_blocks(rows, row_spread(rows, cols, elem, true)));
+        for (const bool aligned : {false, true})
+            most = std::max(most, grad_row_blocks(rows, row_spread(rows, cols, elem, true, aligned)));
     return most;
 }
 

@@ -144,22 +144,53 @@ __device__ __forceinline__ void normalise(const LayerNormOp& op, const Stats& st
 template <typename T>
 constexpr int kCols = 16 / int(sizeof(T));
 
-// A thread's places for rows to come: `depth` rows of `inputs` matrices, P pieces
-// each. Only the thread itself writes and reads them, so no barrier is needed.
-template <typename T, int P, int STEP>  // STEP: 16-byte units between a thread's places
+// Where rows lie: anywhere; on 16-byte boundaries, in whole pieces; and then with
+// all of a team's pieces in the row.
+enum Rows { kAnywhere, kAligned, kWhole };
+
+__device__ __forceinline__ int off16(const void* p) { return int(reinterpret_cast<uintptr_t>(p) & 15u); }
+
+// Places for rows to come: `depth` rows of `inputs` matrices, P pieces each. Of
+// aligned rows only the thread itself writes and reads its places, so no barrier is
+// needed. Of others a piece's place holds the aligned 16 bytes that it starts in, and
+// the piece is joined from there and the next lane's place; a place more for each warp
+// holds the bytes behind its last lane's. (Bytes before a row's start are read with
+// those of its 16, not those behind its end.)
+template <typename T, int P, int STEP, int ROWS>  // STEP: threads that places are laid out for
 struct Ring {
-    uint4* mine;    // the thread's first place
-    int row_units;  // from one row to the next
-    int depth;
+    uint4* base;
+    int inputs, depth;
     __device__ __forceinline__ Ring(void* smem, int depth, int inputs)
-        : mine(static_cast<uint4*>(smem) + threadIdx.x), row_units(inputs * P * STEP), depth(depth) {}
-    // The place of a row, and from there those of its pieces.
-    __device__ __forceinline__ uint4* row(int slot) const { return mine + slot * row_units; }
-    __device__ __forceinline__ void fetch(uint4* row, int input, int piece, const T* p) const {
-        cp_async_16(smem_u32(row + (input * P + piece) * STEP), p, 16);
+        : base(static_cast<uint4*>(smem)), inputs(inputs), depth(depth) {}
+    static constexpr int kSpare = ROWS == kAnywhere ? STEP / 32 : 0;
+    __device__ __forceinline__ uint4* row(int slot) const { return base + slot * inputs * P * (STEP + kSpare) + threadIdx.x; }
+    __device__ __forceinline__ static int place(int input, int piece) { return (input * P + piece) * (STEP + kSpare); }
+    // The warp's spare place.
+    __device__ __forceinline__ static int spare(int input, int piece) {
+        return place(input, piece) + STEP + int(threadIdx.x >> 5) - int(threadIdx.x);
     }
-    __device__ __forceinline__ void get(const uint4* row, int input, int piece, F2 (&f)[kPairs<T>]) const {
-        unpack_pairs<T>(row[(input * P + piece) * STEP], f);
+    // The piece at column c of the row of `cols` columns at p; the whole warp calls it.
+    __device__ __forceinline__ void fetch(uint4* row, int input, int piece, const T* p, int c, int cols) const {
+        if constexpr (ROWS != kAnywhere) {
+            cp_async_16(smem_u32(row + place(input, piece)), p + c, 16);
+        } else {
+            const uintptr_t end = reinterpret_cast<uintptr_t>(p + cols), start = reinterpret_cast<uintptr_t>(p) & ~uintptr_t(15);
+            uintptr_t at = start + uintptr_t(c) * sizeof(T);
+            cp_async_16(smem_u32(row + place(input, piece)), reinterpret_cast<const void*>(at < end ? at : start),
+                        at < end ? uint32_t(min(uintptr_t(16), end - at)) : 0u);
+            if ((threadIdx.x & 31) == 31) {
+                at += 16;
+                cp_async_16(smem_u32(row + spare(input, piece)), reinterpret_cast<const void*>(at < end ? at : start),
+                            at < end ? uint32_t(min(uintptr_t(16), end - at)) : 0u);
+            }
+        }
+    }
+    // off: off16 of the row. Columns past the row are zero.
+    __device__ __forceinline__ void get(const uint4* row, int input, int piece, int off, F2 (&f)[kPairs<T>]) const {
+        uint4 v = row[place(input, piece)];
+        if constexpr (ROWS == kAnywhere)
+            v = join_windows(v, row[(threadIdx.x & 31) == 31 ? spare(input, piece) : place(input, piece) + 1], off);
+        unpack_pairs<T>(v, f);
     }
     // The oldest of `depth` rows in flight (a group of copies each) has arrived.
     __device__ __forceinline__ void wait() const {
@@ -169,20 +200,24 @@ struct Ring {
             case 3: cp_async_wait<2>(); break;
             default: cp_async_wait<3>(); break;
         }
+        pass_on();
+    }
+    // Before a lane reads what others copied, and before it copies over what they read.
+    __device__ __forceinline__ void pass_on() const {
+        if constexpr (ROWS == kAnywhere) __syncwarp();
     }
 };
 constexpr int kMaxDepth = 4;
 
-// A spread of aligned rows: P pieces to a thread of a team of T threads (T = 0: any
-// team), all of them in the row (WHOLE) or not. T is a constant since places and
-// addresses then are: 8192 x 4096 bf16 with dropout takes 55 us so, 62 otherwise.
-// Threads of a block at most, and blocks to an SM at least, by the registers that a
-// thread then has: the norm does with 64, the gradients, which hold two sums for
-// each column, with 128.
+// A spread of rows: P pieces to a thread of a team of T threads (T = 0: any team). T
+// is a constant where the row is whole and T a power of two, since places and
+// addresses then are: 8192 x 4096 bf16 with dropout takes 55 us so, 62 otherwise. Threads of a block at most, and
+// blocks to an SM at least, by the registers that a thread then has: the norm does
+// with 64, the gradients, which hold two sums for each column, with 128.
 template <int T, bool GRAD>
 struct RowKernel {
-    static constexpr int kThreads = T == 0 && !GRAD ? kMaxTeam : GRAD && T != 0 && T <= 256 ? 256 : 512;
-    static constexpr int kBlocks = T == 0 ? 1 : GRAD && T == 512 ? 1 : 2;
+    static constexpr int kThreads = GRAD && T != 0 && T <= 256 ? 256 : 512;
+    static constexpr int kBlocks = T == 0 || (GRAD && T == 512) ? 1 : 2;
 };
 
 // How the rows of a call are spread (ring_plan): threads of a team, rows that a
@@ -194,19 +229,33 @@ struct RingPlan {
 // Gamma and beta, of XT or 32-bit: held in shared memory behind the ring, for all
 // teams of a block (from L2 they would come in the midst of every row), or, of rows
 // too wide for that, read from memory.
-template <typename XT, int P>
+template <typename XT, int P, int ROWS>
 struct Weights {
-    const uint4* mine;  // the thread's first place; null: not held
-    int elem, step;     // their type, and 16-byte units between a thread's places
+    uint4* mine;     // the thread's first place; null: not held
+    int elem, step;  // their type, and 16-byte units between a thread's places
+    int cols;
     // Units of a piece's columns.
     template <typename T>
     static constexpr int kUnits = kCols<XT> / kCols<T>;
+    // 16 bytes from column c on, zero past the last column.
+    template <typename T>
+    __device__ __forceinline__ uint4 load(const T* p, int c) const {
+        if constexpr (ROWS != kAnywhere) return *reinterpret_cast<const uint4*>(p + c);
+        uint32_t w[4] = {};
+#pragma unroll
+        for (int i = 0; i < kCols<T>; ++i) {
+            if (c + i >= cols) break;
+            if constexpr (sizeof(T) == 4) w[i] = __float_as_uint(p[c + i]);
+            else w[i / 2] |= uint32_t(reinterpret_cast<const uint16_t*>(p)[c + i]) << (16 * (i & 1));
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
     template <typename T>
     __device__ __forceinline__ void get_as(int which, int piece, const void* p, int c, F2 (&f)[kPairs<XT>]) const {
 #pragma unroll
         for (int u = 0; u < kUnits<T>; ++u) {
             const uint4 v = mine ? mine[((which * P + piece) * kUnits<T> + u) * step]
-                                 : reinterpret_cast<const uint4*>(static_cast<const T*>(p) + c)[u];
+                                 : load(static_cast<const T*>(p), c + u * kCols<T>);
             F2 part[kPairs<T>];
             unpack_pairs<T>(v, part);
 #pragma unroll
@@ -218,16 +267,15 @@ struct Weights {
         else get_as<XT>(which, piece, p, c, f);
     }
     template <typename T>
-    __device__ __forceinline__ void fetch_as(int which, int piece, const void* p, int c) const {
+    __device__ __forceinline__ void hold_as(int which, int piece, const void* p, int c) const {
 #pragma unroll
         for (int u = 0; u < kUnits<T>; ++u)
-            cp_async_16(smem_u32(mine + ((which * P + piece) * kUnits<T> + u) * step),
-                        reinterpret_cast<const uint4*>(static_cast<const T*>(p) + c) + u, 16);
+            mine[((which * P + piece) * kUnits<T> + u) * step] = load(static_cast<const T*>(p), c + u * kCols<T>);
     }
     // By one team.
-    __device__ __forceinline__ void fetch(int which, int piece, const void* p, int c) const {
-        if (elem == TPGEMM_ELEM_F32) fetch_as<float>(which, piece, p, c);
-        else fetch_as<XT>(which, piece, p, c);
+    __device__ __forceinline__ void hold(int which, int piece, const void* p, int c) const {
+        if (elem == TPGEMM_ELEM_F32) hold_as<float>(which, piece, p, c);
+        else hold_as<XT>(which, piece, p, c);
     }
 };
 
@@ -309,7 +357,82 @@ __device__ __forceinline__ void keep_pairs(const Drop& d, const DropRow& w, int 
     for (int i = 0; i < N; ++i) f[i] = f2(x[2 * i], x[2 * i + 1]);
 }
 
-template <typename XT, int P, int T, bool WHOLE, bool DROP>
+// Zeroes all but the first n of 2 N values.
+template <int N>
+__device__ __forceinline__ void keep_first(int n, F2 (&f)[N]) {
+    if (n >= 2 * N) return;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        float a, b;
+        split(f[i], a, b);
+        f[i] = f2(2 * i < n ? a : 0.f, 2 * i + 1 < n ? b : 0.f);
+    }
+}
+
+template <typename U>
+__device__ __forceinline__ U part_of(const uint4& v, int i) {  // (i a constant)
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    if constexpr (sizeof(U) == 4) return w[i];
+    else return U(w[i / 2] >> (16 * (i & 1)));
+}
+
+// Stores 16 bytes of neighbouring elements from each lane, the first n of a lane's, to
+// rows that start anywhere: each lane the aligned 16 bytes that its own begin in, with
+// the end of the lane's before it, and the warp's two ends element by element. The
+// whole warp calls it; all lanes before one that has elements are full.
+template <typename O, int N>
+__device__ __forceinline__ void store_anywhere(O* p, int n, const F2 (&f)[N]) {
+    if constexpr (2 * N * sizeof(O) != 16) {
+        float x[2 * N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) split(f[i], x[2 * i], x[2 * i + 1]);
+#pragma unroll
+        for (int i = 0; i < 2 * N; ++i)
+            if (i < n) p[i] = from_f32<O>(x[i]);
+    } else {
+        using U = typename std::conditional<sizeof(O) == 4, uint32_t, uint16_t>::type;
+        constexpr int kSize = int(sizeof(O));
+        uint4 v;
+        store_pairs(reinterpret_cast<O*>(&v), f);
+        const int lane = threadIdx.x & 31, off = off16(p);
+        const Window before = make_uint4(__shfl_up_sync(0xffffffffu, v.x, 1), __shfl_up_sync(0xffffffffu, v.y, 1),
+                                         __shfl_up_sync(0xffffffffu, v.z, 1), __shfl_up_sync(0xffffffffu, v.w, 1));
+        const int n_before = __shfl_up_sync(0xffffffffu, n, 1);
+        const uint4 w = off ? join_windows(before, v, 16 - off) : v;
+        // This lane's window of 16 bytes holds elements [lo, hi) of the row.
+        const int skip = off / kSize;
+        int lo = lane == 0 ? skip : 0;
+        int hi = n > 0 ? min(2 * N, skip + n) : lane > 0 ? n_before - (2 * N - skip) : 0;
+        U* q = reinterpret_cast<U*>(reinterpret_cast<uint8_t*>(p) - off);
+        if (lo == 0 && hi == 2 * N) {
+            *reinterpret_cast<uint4*>(q) = w;
+            lo = hi = 0;
+        }
+        // What is left: parts of windows, and the start of the window behind the last
+        // lane's, whose own is then a whole one.
+        uint4 rest = w;
+        if (lane == 31 && skip && n > 2 * N - skip) {
+            lo = 2 * N - skip;
+            hi = n;
+            q = reinterpret_cast<U*>(p);
+            rest = v;
+        }
+        if (lo < hi) {
+            const uint32_t mask = ((1u << hi) - 1u) & ~((1u << lo) - 1u);
+#pragma unroll
+            for (int i = 0; i < 2 * N; ++i)
+                if ((mask >> i) & 1u) q[i] = part_of<U>(rest, i);
+        }
+    }
+}
+
+template <int ROWS, typename O, int N>
+__device__ __forceinline__ void store_piece(O* p, int n, const F2 (&f)[N]) {
+    if constexpr (ROWS == kAnywhere) store_anywhere(p, n, f);
+    else store_pairs(p, f);
+}
+
+template <typename XT, int P, int T, int ROWS, bool DROP>
 __global__ void __launch_bounds__(RowKernel<T, false>::kThreads, RowKernel<T, false>::kBlocks)
     layernorm_rows_kernel(const __grid_constant__ LayerNormOp op, const RingPlan plan) {
     constexpr int N = kPairs<XT>;
@@ -319,22 +442,26 @@ __global__ void __launch_bounds__(RowKernel<T, false>::kThreads, RowKernel<T, fa
     const int64_t teams = blockDim.x / unsigned(team.threads()), stride = gridDim.x * teams;
     int64_t row = blockIdx.x * teams + team.index;
     const int cols = int(op.cols), depth = plan.depth;
-    const Ring<XT, P, RowKernel<T, false>::kThreads> ring(ring_smem, depth, op.R ? 2 : 1);
-    const Weights<XT, P> weights{
-        plan.weights_at ? reinterpret_cast<const uint4*>(ring_smem + plan.weights_at) + team.t : nullptr, op.g, team.threads()};
+    const Ring<XT, P, RowKernel<T, false>::kThreads, ROWS> ring(ring_smem, depth, op.R ? 2 : 1);
+    const Weights<XT, P, ROWS> weights{
+        plan.weights_at ? reinterpret_cast<uint4*>(ring_smem + plan.weights_at) + team.t : nullptr, op.g, team.threads(), cols};
     const auto column = [&](int i) { return kCols<XT> * (i * team.threads() + team.t); };
-    const auto has = [&](int i) { return WHOLE || column(i) < cols; };  // piece i is in the row
+    // Whether piece i is in the row (of rows anywhere: the warp's first lane's is), and its columns there.
+    const auto has = [&](int i) {
+        return ROWS == kWhole || column(i) - (ROWS == kAnywhere ? kCols<XT> * int(threadIdx.x & 31) : 0) < cols;
+    };
+    const auto count = [&](int i) { return ROWS == kAnywhere ? max(0, min(kCols<XT>, cols - column(i))) : kCols<XT>; };
     const auto fetch = [&](int64_t r, uint4* place) {
         if (r < op.rows) {
             const XT* x = static_cast<const XT*>(op.X) + r * op.ldx;
 #pragma unroll
             for (int i = 0; i < P; ++i)
-                if (has(i)) ring.fetch(place, 0, i, x + column(i));
+                if (has(i)) ring.fetch(place, 0, i, x, column(i), cols);
             if (op.R) {
                 const XT* q = static_cast<const XT*>(op.R) + r * op.ldr;
 #pragma unroll
                 for (int i = 0; i < P; ++i)
-                    if (has(i)) ring.fetch(place, 1, i, q + column(i));
+                    if (has(i)) ring.fetch(place, 1, i, q, column(i), cols);
             }
         }
         cp_async_commit();
@@ -347,11 +474,9 @@ __global__ void __launch_bounds__(RowKernel<T, false>::kThreads, RowKernel<T, fa
 #pragma unroll
             for (int i = 0; i < P; ++i)
                 if (has(i)) {
-                    weights.fetch(0, i, op.gamma, column(i));
-                    if (op.beta) weights.fetch(1, i, op.beta, column(i));
+                    weights.hold(0, i, op.gamma, column(i));
+                    if (op.beta) weights.hold(1, i, op.beta, column(i));
                 }
-        cp_async_commit();
-        cp_async_wait<0>();
         __syncthreads();
     }
     DropOffset offset{};
@@ -363,6 +488,8 @@ __global__ void __launch_bounds__(RowKernel<T, false>::kThreads, RowKernel<T, fa
         if constexpr (DROP) w = drop_row(op.drop, offset, uint32_t(row));
         ring.wait();
         uint4* const place = ring.row(slot);
+        const int off_x = off16(static_cast<const XT*>(op.X) + row * op.ldx);
+        const int off_r = off16(static_cast<const XT*>(op.R) + row * op.ldr);
         F2 h[P][N];
         F2 part[N];
         zero(part);
@@ -372,17 +499,18 @@ __global__ void __launch_bounds__(RowKernel<T, false>::kThreads, RowKernel<T, fa
                 zero(h[i]);
                 continue;
             }
-            ring.get(place, 0, i, h[i]);
+            ring.get(place, 0, i, off_x, h[i]);
             if constexpr (DROP) keep_pairs(op.drop, w, column(i), h[i]);
             F2 r[N];
             zero(r);
-            if (op.R) ring.get(place, 1, i, r);
+            if (op.R) ring.get(place, 1, i, off_r, r);
 #pragma unroll
             for (int j = 0; j < N; ++j) {
                 h[i][j] = fma(h[i][j], scale, r[j]);
                 part[j] = add(part[j], h[i][j]);
             }
         }
+        ring.pass_on();
         fetch(row + depth * stride, place);
         float sum[1] = {sum_of(part)};
         team.sum(sum, s[0]);
@@ -391,20 +519,23 @@ __global__ void __launch_bounds__(RowKernel<T, false>::kThreads, RowKernel<T, fa
             XT* p = static_cast<XT*>(op.H) + row * op.ldh;
 #pragma unroll
             for (int i = 0; i < P; ++i)
-                if (has(i)) store_pairs<XT>(p + column(i), h[i]);
+                if (has(i)) store_piece<ROWS>(p + column(i), count(i), h[i]);
         }
         F2 d[N], dd[N];
         zero(d);
         zero(dd);
 #pragma unroll
         for (int i = 0; i < P; ++i)
-            if (has(i))
+            if (has(i)) {
+#pragma unroll
+                for (int j = 0; j < N; ++j) h[i][j] = add(h[i][j], f2(-mean));
+                keep_first(count(i), h[i]);
 #pragma unroll
                 for (int j = 0; j < N; ++j) {
-                    h[i][j] = add(h[i][j], f2(-mean));
                     d[j] = add(d[j], h[i][j]);
                     dd[j] = fma(h[i][j], h[i][j], dd[j]);
                 }
+            }
         float both[2] = {sum_of(d), sum_of(dd)};
         team.sum(both, s[1]);
         const Stats st = stats_of(mean, both[0], both[1], inv_n, op.eps);
@@ -446,7 +577,7 @@ __global__ void __launch_bounds__(RowKernel<T, false>::kThreads, RowKernel<T, fa
             y += row * op.ldy;
 #pragma unroll
             for (int i = 0; i < P; ++i)
-                if (has(i)) store_pairs(y + column(i), h[i]);
+                if (has(i)) store_piece<ROWS>(y + column(i), count(i), h[i]);
         };
         switch (op.y) {
             case TPGEMM_ELEM_F16: store(static_cast<__half*>(op.Y)); break;
@@ -459,80 +590,7 @@ __global__ void __launch_bounds__(RowKernel<T, false>::kThreads, RowKernel<T, fa
     cp_async_wait<0>();
 }
 
-// --------------------------------------------------------- rows as they come
-// Unaligned rows held in registers: V groups of eight columns to a thread; WARP: a
-// row to a warp, else to a block.
-template <typename XT, int V, bool WARP, bool DROP>
-__global__ void __launch_bounds__(WARP ? 32 * kWarpRows : kMaxTeam)
-    layernorm_kernel(const __grid_constant__ LayerNormOp op) {
-    constexpr bool VEC = false;
-    __shared__ float2 s[3][32];
-    const int team = WARP ? 32 : int(blockDim.x);
-    const int t = WARP ? int(threadIdx.x & 31) : int(threadIdx.x);
-    const int64_t row = WARP ? int64_t(blockIdx.x) * kWarpRows + (threadIdx.x >> 5) : int64_t(blockIdx.x);
-    grid_launch_dependents();
-    grid_dependency_wait();
-    if (WARP && row >= op.rows) return;
-    DropRow k{};
-    if constexpr (DROP) k = drop_row(op.drop, drop_offset(op.drop), uint32_t(row));
-    float h[V][8];
-    float sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        load_sum<XT, VEC, DROP>(op, k, row, Cols<VEC>(i, t, team, op.cols), h[i]);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) sum += h[i][j];
-    }
-    const float mean = team_sum1<WARP>(sum, s[0]) / float(op.cols);
-    float d = 0.f, dd = 0.f;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const Cols<VEC> c(i, t, team, op.cols);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float e = j < c.n ? h[i][j] - mean : 0.f;
-            d += e;
-            dd += e * e;
-        }
-    }
-    team_sum2<WARP>(d, dd, s[1]);
-    const Stats st = stats_of(mean, d, dd, 1.f / float(op.cols), op.eps);
-    if (t == 0) {
-        if (op.mean) op.mean[row] = st.mean + st.off;
-        if (op.rstd) op.rstd[row] = st.rstd;
-    }
-    float inv = 1.f;
-    if (op.mode == TPGEMM_SCALE_ROW) {
-        float none = 0.f;
-        uint32_t amax = 0;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const Cols<VEC> c(i, t, team, op.cols);
-            float y[8];
-            normalise<XT, VEC>(op, st, c, h[i], y);
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (j < c.n) amax = max(amax, abs_bits(y[j]));
-        }
-        team_sum_max<WARP>(none, amax, s[2]);
-        const float scale = row_scale(amax, op.y);
-        if (t == 0) op.scale[row] = scale;
-        inv = 1.f / scale;
-    }
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const Cols<VEC> c(i, t, team, op.cols);
-        float y[8];
-        normalise<XT, VEC>(op, st, c, h[i], y);
-        if (op.mode == TPGEMM_SCALE_ROW) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] *= inv;
-        }
-        store_y<VEC>(op, row, c, y);
-        if (op.H) store_cols<XT, VEC>(op.H, row * op.ldh, c, h[i]);
-    }
-}
-
+// ---------------------------------------------------------------- wider rows
 // Rows of any width, a block to a row, read once for each pass.
 template <typename XT, bool VEC, bool DROP>
 __global__ void __launch_bounds__(kMaxTeam) layernorm_wide_kernel(const __grid_constant__ LayerNormOp op) {
@@ -608,7 +666,7 @@ __global__ void __launch_bounds__(kMaxTeam) layernorm_wide_kernel(const __grid_c
 // what a reduction leaves to be used, w and n, is computed a second time from shared
 // memory in place of held in registers, which the columns' sums take. A block's
 // teams add up their sums in order at the end.
-template <typename XT, int P, int T, bool WHOLE, bool DROP>
+template <typename XT, int P, int T, int ROWS, bool DROP>
 __global__ void __launch_bounds__(RowKernel<T, true>::kThreads, RowKernel<T, true>::kBlocks)
     layernorm_grad_rows_kernel(const __grid_constant__ LayerNormGradOp op, const RingPlan plan) {
     constexpr int N = kPairs<XT>;
@@ -622,11 +680,15 @@ __global__ void __launch_bounds__(RowKernel<T, true>::kThreads, RowKernel<T, tru
     int64_t row = int64_t(blockIdx.x) * teams + team.index;
     const int cols = int(op.cols), depth = plan.depth;
     const bool rows_wanted = op.dX || op.dR, add_dh = rows_wanted && op.dH;
-    const Ring<XT, P, RowKernel<T, true>::kThreads> ring(ring_smem, depth, add_dh ? 3 : 2);
-    const Weights<XT, P> weights{
-        plan.weights_at ? reinterpret_cast<const uint4*>(ring_smem + plan.weights_at) + team.t : nullptr, op.g, team.threads()};
+    const Ring<XT, P, RowKernel<T, true>::kThreads, ROWS> ring(ring_smem, depth, add_dh ? 3 : 2);
+    const Weights<XT, P, ROWS> weights{
+        plan.weights_at ? reinterpret_cast<uint4*>(ring_smem + plan.weights_at) + team.t : nullptr, op.g, team.threads(), cols};
     const auto column = [&](int i) { return kCols<XT> * (i * team.threads() + team.t); };
-    const auto has = [&](int i) { return WHOLE || column(i) < cols; };  // piece i is in the row
+    // Whether piece i is in the row (of rows anywhere: the warp's first lane's is), and its columns there.
+    const auto has = [&](int i) {
+        return ROWS == kWhole || column(i) - (ROWS == kAnywhere ? kCols<XT> * int(threadIdx.x & 31) : 0) < cols;
+    };
+    const auto count = [&](int i) { return ROWS == kAnywhere ? max(0, min(kCols<XT>, cols - column(i))) : kCols<XT>; };
     const auto fetch = [&](int64_t r, int slot) {
         uint4* const place = ring.row(slot);
         if (r < op.rows) {
@@ -640,9 +702,9 @@ __global__ void __launch_bounds__(RowKernel<T, true>::kThreads, RowKernel<T, tru
 #pragma unroll
             for (int i = 0; i < P; ++i) {
                 if (!has(i)) continue;
-                ring.fetch(place, 0, i, dy + column(i));
-                ring.fetch(place, 1, i, h + column(i));
-                if (add_dh) ring.fetch(place, 2, i, dh + column(i));
+                ring.fetch(place, 0, i, dy, column(i), cols);
+                ring.fetch(place, 1, i, h, column(i), cols);
+                if (add_dh) ring.fetch(place, 2, i, dh, column(i), cols);
             }
         }
         cp_async_commit();
@@ -654,9 +716,7 @@ __global__ void __launch_bounds__(RowKernel<T, true>::kThreads, RowKernel<T, tru
         if (team.index == 0)
 #pragma unroll
             for (int i = 0; i < P; ++i)
-                if (has(i)) weights.fetch(0, i, op.gamma, column(i));
-        cp_async_commit();
-        cp_async_wait<0>();
+                if (has(i)) weights.hold(0, i, op.gamma, column(i));
         __syncthreads();
     }
     DropOffset offset{};
@@ -673,10 +733,13 @@ __global__ void __launch_bounds__(RowKernel<T, true>::kThreads, RowKernel<T, tru
         const float mean = stats[slot][threadIdx.x >> 5][0], rstd = stats[slot][threadIdx.x >> 5][1];
         uint4* const place = ring.row(slot);
         F2 kept_w[kAgain ? 1 : P][N], kept_n[kAgain ? 1 : P][N];
+        const int off_dy = off16(static_cast<const XT*>(op.dY) + row * op.lddy);
+        const int off_h = off16(static_cast<const XT*>(op.H) + row * op.ldh);
+        const int off_dh = add_dh ? off16(static_cast<const XT*>(op.dH) + row * op.lddh) : 0;
         // dY and (H - mean) rstd of piece i.
         const auto load = [&](int i, F2 (&w)[N], F2 (&n)[N]) {
-            ring.get(place, 0, i, w);
-            ring.get(place, 1, i, n);
+            ring.get(place, 0, i, off_dy, w);
+            ring.get(place, 1, i, off_h, n);
 #pragma unroll
             for (int j = 0; j < N; ++j) n[j] = mul(add(n[j], f2(-mean)), f2(rstd));
         };
@@ -724,17 +787,17 @@ __global__ void __launch_bounds__(RowKernel<T, true>::kThreads, RowKernel<T, tru
                 }
                 F2 dt[N];
                 zero(dt);
-                if (add_dh) ring.get(place, 2, i, dt);
+                if (add_dh) ring.get(place, 2, i, off_dh, dt);
 #pragma unroll
                 for (int j = 0; j < N; ++j) dt[j] = fma(fma(n[j], swn, add(w[j], sw)), f2(rstd), dt[j]);
-                if (op.dR) store_pairs<XT>(static_cast<XT*>(op.dR) + row * op.lddr + column(i), dt);
+                if (op.dR) store_piece<ROWS>(static_cast<XT*>(op.dR) + row * op.lddr + column(i), count(i), dt);
                 if (op.dX) {
                     if constexpr (DROP) {
                         keep_pairs(op.drop, words, column(i), dt);
 #pragma unroll
                         for (int j = 0; j < N; ++j) dt[j] = mul(dt[j], f2(op.drop.scale));
                     }
-                    store_pairs<XT>(static_cast<XT*>(op.dX) + row * op.lddx + column(i), dt);
+                    store_piece<ROWS>(static_cast<XT*>(op.dX) + row * op.lddx + column(i), count(i), dt);
                 }
             }
         }
@@ -748,8 +811,8 @@ __global__ void __launch_bounds__(RowKernel<T, true>::kThreads, RowKernel<T, tru
 #pragma unroll
         for (int i = 0; i < P; ++i)
             if (has(i)) {
-                store_pairs<float>(out + column(i), ag[i]);
-                store_pairs<float>(out + op.cols + column(i), ab[i]);
+                store_piece<ROWS>(out + column(i), count(i), ag[i]);
+                store_piece<ROWS>(out + op.cols + column(i), count(i), ab[i]);
             }
         return;
     }
@@ -759,7 +822,7 @@ __global__ void __launch_bounds__(RowKernel<T, true>::kThreads, RowKernel<T, tru
     const auto join = [&](const F2 (&a)[P][N], float* to) {
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < P; ++i) store_pairs<float>(sums + team.index * pitch + column(i), a[i]);
+        for (int i = 0; i < P; ++i) store_pairs(sums + team.index * pitch + column(i), a[i]);
         __syncthreads();
         for (int c = int(threadIdx.x); c < cols; c += int(blockDim.x)) {
             float v = 0.f;
@@ -769,109 +832,6 @@ __global__ void __launch_bounds__(RowKernel<T, true>::kThreads, RowKernel<T, tru
     };
     join(ag, out);
     join(ab, out + op.cols);
-}
-
-// Unaligned rows.
-template <typename XT, int V, bool WARP, bool DROP>
-__global__ void __launch_bounds__(WARP ? 32 * kWarpRows : kMaxTeam)
-    layernorm_grad_kernel(const __grid_constant__ LayerNormGradOp op) {
-    constexpr bool VEC = false;
-    __shared__ float2 s[2][32];
-    __shared__ float sum[WARP ? 8 * 32 * 8 * V : 1];
-    const int team = WARP ? 32 : int(blockDim.x);
-    const int t = WARP ? int(threadIdx.x & 31) : int(threadIdx.x);
-    const int64_t teams = WARP ? kWarpRows : 1;
-    const int64_t stride = int64_t(gridDim.x) * teams;
-    grid_launch_dependents();
-    grid_dependency_wait();
-    DropOffset offset{};
-    if constexpr (DROP) offset = drop_offset(op.drop);
-    const bool rows_wanted = op.dX || op.dR;
-    float ag[V][8], ab[V][8];
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) ag[i][j] = ab[i][j] = 0.f;
-    int64_t row = int64_t(blockIdx.x) * teams + (WARP ? threadIdx.x >> 5 : 0);
-    for (int turn = 0; row < op.rows; row += stride, turn ^= 1) {
-        const float rstd = op.rstd[row], mean = op.mean[row];
-        float w[V][8], n[V][8];
-        float sw = 0.f, swn = 0.f;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const Cols<VEC> c(i, t, team, op.cols);
-            load_cols<XT, VEC>(op.dY, row * op.lddy, c, w[i]);
-            load_cols<XT, VEC>(op.H, row * op.ldh, c, n[i]);
-            float g[8];
-            if (rows_wanted) load_gamma<XT, VEC>(op.gamma, op.g, c, g);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                n[i][j] = (n[i][j] - mean) * rstd;
-                ag[i][j] += w[i][j] * n[i][j];
-                ab[i][j] += w[i][j];
-                if (rows_wanted) {
-                    w[i][j] *= g[j];  // (0 past the row)
-                    sw += w[i][j];
-                    swn += w[i][j] * n[i][j];
-                }
-            }
-        }
-        if (!rows_wanted) continue;
-        team_sum2<WARP>(sw, swn, s[turn]);
-        sw /= float(op.cols);
-        swn /= float(op.cols);
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const Cols<VEC> c(i, t, team, op.cols);
-            float dt[8];
-            if (op.dH) {
-                load_cols<XT, VEC>(op.dH, row * op.lddh, c, dt);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) dt[j] = 0.f;
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) dt[j] += rstd * (w[i][j] - sw - n[i][j] * swn);
-            if (op.dR) store_cols<XT, VEC>(op.dR, row * op.lddr, c, dt);
-            if (op.dX) {
-                if constexpr (DROP) {
-                    keep_cols<VEC>(op.drop, drop_row(op.drop, offset, uint32_t(row)), c, dt);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) dt[j] *= op.drop.scale;
-                }
-                store_cols<XT, VEC>(op.dX, row * op.lddx, c, dt);
-            }
-        }
-    }
-    if (!op.partial) return;
-    float* out = op.partial + int64_t(blockIdx.x) * 2 * op.cols;
-    if constexpr (WARP) {
-        const int w = threadIdx.x >> 5;
-#pragma unroll
-        for (int which = 0; which < 2; ++which) {
-            __syncthreads();
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) sum[((w * V + i) * 8 + j) * 32 + t] = which ? ab[i][j] : ag[i][j];
-            __syncthreads();
-            // The warps' sums in order; warp w finishes the groups w, w + 8, ...
-            for (int q = w; q < V * 8; q += kWarpRows) {
-                float v = 0.f;
-#pragma unroll
-                for (int r = 0; r < kWarpRows; ++r) v += sum[(r * V * 8 + q) * 32 + t];
-                const Cols<VEC> c(q / 8, t, team, op.cols);
-                if (q % 8 < c.n) out[which * op.cols + c.first + int64_t(q % 8) * c.step] = v;
-            }
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const Cols<VEC> c(i, t, team, op.cols);
-            store_cols<float, VEC>(out, 0, c, ag[i]);
-            store_cols<float, VEC>(out, op.cols, c, ab[i]);
-        }
-    }
 }
 
 template <typename XT>
@@ -936,17 +896,7 @@ __global__ void __launch_bounds__(256) layernorm_columns_kernel(const __grid_con
     out[op.cols] = b;
 }
 
-// Unaligned rows: up to 512 columns a warp holds the row, wider rows are a block's.
-Spread spread_of(int64_t cols) {
-    const int64_t groups = (cols + 7) / 8;
-    if (groups <= 64) return {32, groups <= 32 ? 1 : 2, true};
-    if (cols > kMaxHeld) return {kMaxTeam, 0, false};
-    const bool one = groups <= kMaxTeam;
-    const int64_t per = one ? groups : (groups + 1) / 2;
-    return {int((per + 31) / 32 * 32), one ? 1 : 2, false};
-}
-
-// Aligned rows of up to kMaxHeld columns. A reduction costs each warp that takes
+// Rows of up to kMaxHeld columns. A reduction costs each warp that takes
 // part as many instructions as 16 columns, so the norm has four pieces to a thread,
 // its gradients 16 columns; fewer of rows that a warp then holds whole; twice as many
 // of rows wider than 512 such threads; and of few rows one, for the shortest time to
@@ -955,123 +905,124 @@ constexpr int most_pieces(int elem, bool grad) { return grad && elem != TPGEMM_E
 
 struct RowSpread {
     int p, t;         // the kernel's P and T
-    bool whole;       // and WHOLE
+    bool whole;       // all of the team's pieces are in the row
     int team, teams;  // threads of a team, teams of a block
     int blocks;       // to an SM
     int threads() const { return team * teams; }
 };
-RowSpread row_spread(int64_t rows, int64_t cols, int elem, bool grad) {
-    const int pieces = int((cols * elem_size(elem) + 15) / 16), most = most_pieces(elem, grad);
-    if (rows <= kSms && pieces <= (grad ? 512 : kMaxTeam))
-        return {1, 0, false, (pieces + 31) / 32 * 32, 1, 1};
-    int p = 1, t = 32;
-    while (p < most && t * p < pieces) p *= 2;
-    while (t < 512 && t * p < pieces) t *= 2;
-    if (t * p < pieces) p *= 2;
-    const int threads = grad && t <= 256 ? 256 : 512;
-    const int teams = int(std::max<int64_t>(1, std::min<int64_t>(threads / t, rows / kSms)));
-    return {p, t, t * p == pieces, t, teams, std::min((grad ? 512 : 1024) / (t * teams), 8)};
+RowSpread row_spread(int64_t rows, int64_t cols, int elem, bool grad, bool aligned) {
+    const int pieces = int((cols * elem_size(elem) + 15) / 16);
+    const int most = rows <= kSms ? 1 : most_pieces(elem, grad);
+    int p = 1;
+    while (p < most && 32 * p < pieces) p *= 2;
+    while (512 * p < pieces) p *= 2;
+    const int team = (pieces + 32 * p - 1) / (32 * p) * 32;
+    const bool whole = aligned && most > 1 && team * p == pieces;
+    const int t = whole && (team & (team - 1)) == 0 ? team : 0;
+    const int threads = grad && t != 0 && t <= 256 ? 256 : 512;
+    const int teams = int(std::max<int64_t>(1, std::min<int64_t>(threads / team, rows / kSms)));
+    return {p, t, whole, team, teams, std::max(1, std::min((grad || t == 0 ? 512 : 1024) / (team * teams), 8))};
 }
 
 constexpr int kRingBytes = 216 * 1024;  // of an SM, for its blocks
-// `step`: threads that a block's places are laid out for.
-RingPlan ring_plan(RowSpread* s, int step, int inputs, int elem, int vectors, int vector_elem, size_t* bytes) {
-    const size_t row = size_t(inputs) * s->p * step * 16;  // of all teams
-    size_t held = size_t(vectors) * s->p * s->team * 16 * elem_size(vector_elem) / elem_size(elem);
+// `step`: threads that a block's places are laid out for. A team's only row is copied
+// alone, and the weights that it reads once are not held.
+RingPlan ring_plan(RowSpread* s, bool anywhere, int64_t rows, int step, int inputs, int elem, int vectors, int vector_elem,
+                   size_t* bytes) {
+    const size_t row = size_t(inputs) * s->p * (step + (anywhere ? step / 32 : 0)) * 16;  // of all teams
+    const int64_t turns = (rows + int64_t(kSms) * s->blocks * s->teams - 1) / (int64_t(kSms) * s->blocks * s->teams);
+    size_t held = turns == 1 ? 0 : size_t(vectors) * s->p * s->team * 16 * elem_size(vector_elem) / elem_size(elem);
     while (s->blocks > 1 && held + row > size_t(kRingBytes / s->blocks)) --s->blocks;
     const size_t have = size_t(kRingBytes / s->blocks);
     if (held + row > have) held = 0;
-    const int depth = std::max(1, std::min(kMaxDepth, int((have - held) / row)));
+    const int fit = int((have - held) / row);
+    const int depth = int(std::max<int64_t>(1, std::min<int64_t>(turns, std::min(kMaxDepth, fit))));
     *bytes = depth * row + held;
     return {s->team, depth, held ? int(depth * row) : 0};
 }
 
-// f(P, T, WHOLE) of the spread's kernel, as integral constants. TWICE: whether rows
-// of up to kMaxHeld columns come to more than MOST pieces.
+// f(P, T, ROWS) of the spread's kernel, as integral constants. MOST: most_pieces;
+// TWICE: whether rows of up to kMaxHeld columns come to more than MOST.
 template <int MOST, bool TWICE, typename F>
-cudaError_t with_spread(const RowSpread& s, F&& f) {
-    const auto call = [&](auto p, auto t) {
-        return s.whole ? f(p, t, std::true_type()) : f(p, t, std::false_type());
+cudaError_t with_spread(const RowSpread& s, bool aligned, F&& f) {
+    using std::integral_constant;
+    const auto pieces = [&](auto g) {
+        if constexpr (TWICE)
+            if (s.p == 2 * MOST) return g(integral_constant<int, 2 * MOST>());
+        if constexpr (MOST == 4)
+            if (s.p == 4) return g(integral_constant<int, 4>());
+        return s.p == 2 ? g(integral_constant<int, 2>()) : g(integral_constant<int, 1>());
     };
-    constexpr std::integral_constant<int, 1> one{};
-    constexpr std::integral_constant<int, 2> two{};
-    constexpr std::integral_constant<int, MOST> most{};
-    constexpr std::integral_constant<int, 32> t32{};
-    constexpr std::integral_constant<int, 512> t512{};
-    if (s.t == 0) return f(one, std::integral_constant<int, 0>(), std::false_type());
-    if constexpr (TWICE)
-        if (s.p > MOST) return call(std::integral_constant<int, 2 * MOST>(), t512);
-    if (s.p == MOST) {
-        switch (s.t) {
-            case 32: return call(most, t32);
-            case 64: return call(most, std::integral_constant<int, 64>());
-            case 128: return call(most, std::integral_constant<int, 128>());
-            case 256: return call(most, std::integral_constant<int, 256>());
-            default: return call(most, t512);
-        }
+    if (s.t == 0)
+        return pieces([&](auto p) {
+            constexpr integral_constant<int, 0> any{};
+            return s.whole   ? f(p, any, integral_constant<int, kWhole>())
+                   : aligned ? f(p, any, integral_constant<int, kAligned>())
+                             : f(p, any, integral_constant<int, kAnywhere>());
+        });
+    constexpr integral_constant<int, kWhole> whole{};
+    constexpr integral_constant<int, 512> t512{};
+    if (s.t == 32) {  // (as many pieces as MOST at the most)
+        constexpr integral_constant<int, 32> t32{};
+        if constexpr (MOST == 4)
+            if (s.p == 4) return f(integral_constant<int, 4>(), t32, whole);
+        return s.p == 2 ? f(integral_constant<int, 2>(), t32, whole) : f(integral_constant<int, 1>(), t32, whole);
     }
-    return MOST > 2 && s.p == 2 ? call(two, t32) : call(one, t32);
+    if constexpr (TWICE)
+        if (s.p > MOST) return f(integral_constant<int, 2 * MOST>(), t512, whole);
+    constexpr integral_constant<int, MOST> most{};
+    switch (s.t) {
+        case 64: return f(most, integral_constant<int, 64>(), whole);
+        case 128: return f(most, integral_constant<int, 128>(), whole);
+        case 256: return f(most, integral_constant<int, 256>(), whole);
+        default: return f(most, t512, whole);
+    }
 }
 
 template <typename F, typename Op>
 cudaError_t launch_ring(F fn, int64_t blocks, int threads, size_t bytes, const RingPlan& plan, cudaStream_t stream,
                         const Op& op) {
-    const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(fn),
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
-    if (e != cudaSuccess) return e;
+    if (bytes > 40 * 1024) {  // (with the kernel's own, more than a block has without asking)
+        const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(fn),
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
+        if (e != cudaSuccess) return e;
+    }
     return launch_dependent(fn, dim3(unsigned(blocks)), dim3(unsigned(threads)), bytes, stream, op, plan);
 }
 
 template <typename XT, bool DROP>
-cudaError_t launch_rows(const LayerNormOp& op, cudaStream_t stream) {
-    RowSpread s = row_spread(op.rows, op.cols, op.x, false);
-    return with_spread<4, sizeof(XT) == 4>(s, [&](auto p, auto t, auto whole) {
+cudaError_t launch_norm(const LayerNormOp& op, bool aligned, cudaStream_t stream) {
+    if (op.rows > 0x7fffffff) return cudaErrorInvalidValue;
+    if (op.cols > kMaxHeld)
+        return launch_dependent(aligned && op.cols % 8 == 0 ? layernorm_wide_kernel<XT, true, DROP>
+                                                            : layernorm_wide_kernel<XT, false, DROP>,
+                                dim3(unsigned(op.rows)), dim3(kMaxTeam), 0, stream, op);
+    RowSpread s = row_spread(op.rows, op.cols, op.x, false, aligned);
+    return with_spread<4, sizeof(XT) == 4>(s, aligned, [&](auto p, auto t, auto where) {
         constexpr int P = decltype(p)::value, T = decltype(t)::value;
         size_t bytes;
-        const RingPlan plan = ring_plan(&s, RowKernel<T, false>::kThreads, op.R ? 2 : 1, op.x, op.beta ? 2 : 1,
-                                        op.g, &bytes);
+        const RingPlan plan = ring_plan(&s, !aligned, op.rows, RowKernel<T, false>::kThreads, op.R ? 2 : 1, op.x,
+                                        op.beta ? 2 : 1, op.g, &bytes);
         const int64_t blocks = std::min<int64_t>((op.rows + s.teams - 1) / s.teams, int64_t(kSms) * s.blocks);
-        return launch_ring(layernorm_rows_kernel<XT, P, T, decltype(whole)::value, DROP>, blocks, s.threads(), bytes,
+        return launch_ring(layernorm_rows_kernel<XT, P, T, decltype(where)::value, DROP>, blocks, s.threads(), bytes,
                            plan, stream, op);
     });
 }
 
-template <typename XT, bool VEC, bool DROP>
-cudaError_t launch_norm(const LayerNormOp& op, cudaStream_t stream) {
-    const Spread s = spread_of(op.cols);
-    const int64_t blocks = s.v == 0 ? op.rows : (op.rows + s.rows() - 1) / s.rows();
-    if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-    if (s.v == 0)
-        return launch_dependent(layernorm_wide_kernel<XT, VEC, DROP>, dim3(unsigned(blocks)),
-                                dim3(unsigned(s.threads())), 0, stream, op);
-    if constexpr (VEC) {
-        return launch_rows<XT, DROP>(op, stream);
-    } else {
-        auto fn = s.warp ? (s.v == 1 ? layernorm_kernel<XT, 1, true, DROP> : layernorm_kernel<XT, 2, true, DROP>)
-                         : (s.v == 1 ? layernorm_kernel<XT, 1, false, DROP> : layernorm_kernel<XT, 2, false, DROP>);
-        return launch_dependent(fn, dim3(unsigned(blocks)), dim3(unsigned(s.threads())), 0, stream, op);
-    }
-}
-
 template <typename XT>
 cudaError_t launch_norm_typed(const LayerNormOp& op, cudaStream_t stream) {
-    const bool vec = op.cols % 8 == 0 && rows_aligned(op.X, op.ldx, op.rows, op.x, 16) &&
-                     rows_aligned(op.R, op.ldr, op.rows, op.x, 16) &&
-                     rows_aligned(op.H, op.ldh, op.rows, op.x, 16) &&
-                     rows_aligned(op.Y, op.ldy, op.rows, op.y, elem_size(op.y) == 1 ? 8 : 16) &&
-                     rows_aligned(op.gamma, 0, 1, op.g, 16) && rows_aligned(op.beta, 0, 1, op.g, 16);
-    if (op.drop.on)
-        return vec ? launch_norm<XT, true, true>(op, stream) : launch_norm<XT, false, true>(op, stream);
-    return vec ? launch_norm<XT, true, false>(op, stream) : launch_norm<XT, false, false>(op, stream);
+    // (The kernel of wider rows stores eight columns at a time.)
+    const int y_bytes = (op.cols > kMaxHeld ? 8 : kCols<XT>) * elem_size(op.y);
+    const bool aligned = op.cols % kCols<XT> == 0 && rows_aligned(op.X, op.ldx, op.rows, op.x, 16) &&
+                         rows_aligned(op.R, op.ldr, op.rows, op.x, 16) &&
+                         rows_aligned(op.H, op.ldh, op.rows, op.x, 16) &&
+                         rows_aligned(op.Y, op.ldy, op.rows, op.y, std::min(16, y_bytes)) &&
+                         rows_aligned(op.gamma, 0, 1, op.g, 16) && rows_aligned(op.beta, 0, 1, op.g, 16);
+    return op.drop.on ? launch_norm<XT, true>(op, aligned, stream) : launch_norm<XT, false>(op, aligned, stream);
 }
 
 // Two rows to a team at the least, since each block's sums are written and read
 // once more; else what the SMs hold.
-int grad_blocks(int64_t rows, const Spread& s) {
-    const int64_t most = (rows + 2 * s.rows() - 1) / (2 * s.rows());
-    const int64_t fill = int64_t(kSms) * std::max(1, 512 / s.threads());
-    return int(most < fill ? (most < 1 ? 1 : most) : fill);
-}
 int grad_row_blocks(int64_t rows, const RowSpread& s) {
     const int64_t most = (rows + 2 * s.teams - 1) / (2 * s.teams);
     return int(std::max<int64_t>(1, std::min<int64_t>(most, int64_t(kSms) * s.blocks)));
@@ -1083,33 +1034,26 @@ int wide_strips(int64_t rows) {
 }
 
 template <typename XT, bool DROP>
-cudaError_t launch_grad(const LayerNormGradOp& op, const Spread& u, bool vec, int* strips, cudaStream_t stream) {
-    if (vec) {
-        RowSpread s = row_spread(op.rows, op.cols, op.x, true);
-        return with_spread<sizeof(XT) == 4 ? 4 : 2, true>(s, [&](auto p, auto t, auto whole) {
-            constexpr int P = decltype(p)::value, T = decltype(t)::value;
-            size_t bytes;
-            const RingPlan plan = ring_plan(&s, RowKernel<T, true>::kThreads, op.dH && (op.dX || op.dR) ? 3 : 2, op.x,
-                                            1, op.g, &bytes);
-            if (s.teams > 1) bytes = std::max(bytes, size_t(P) * kCols<XT> * s.threads() * 4);  // (the teams' sums)
-            *strips = grad_row_blocks(op.rows, s);
-            return launch_ring(layernorm_grad_rows_kernel<XT, P, T, decltype(whole)::value, DROP>, *strips, s.threads(),
-                               bytes, plan, stream, op);
-        });
-    }
-    *strips = grad_blocks(op.rows, u);
-    auto fn = u.warp ? (u.v == 1 ? layernorm_grad_kernel<XT, 1, true, DROP> : layernorm_grad_kernel<XT, 2, true, DROP>)
-                     : (u.v == 1 ? layernorm_grad_kernel<XT, 1, false, DROP> : layernorm_grad_kernel<XT, 2, false, DROP>);
-    return launch_dependent(fn, dim3(unsigned(*strips)), dim3(unsigned(u.threads())), 0, stream, op);
+cudaError_t launch_grad(const LayerNormGradOp& op, bool aligned, int* strips, cudaStream_t stream) {
+    RowSpread s = row_spread(op.rows, op.cols, op.x, true, aligned);
+    return with_spread<sizeof(XT) == 4 ? 4 : 2, true>(s, aligned, [&](auto p, auto t, auto where) {
+        constexpr int P = decltype(p)::value, T = decltype(t)::value;
+        size_t bytes;
+        const RingPlan plan = ring_plan(&s, !aligned, op.rows, RowKernel<T, true>::kThreads,
+                                        op.dH && (op.dX || op.dR) ? 3 : 2, op.x, 1, op.g, &bytes);
+        if (s.teams > 1) bytes = std::max(bytes, size_t(P) * kCols<XT> * s.threads() * 4);  // (the teams' sums)
+        *strips = grad_row_blocks(op.rows, s);
+        return launch_ring(layernorm_grad_rows_kernel<XT, P, T, decltype(where)::value, DROP>, *strips, s.threads(),
+                           bytes, plan, stream, op);
+    });
 }
 
 template <typename XT>
 cudaError_t launch_grad_typed(const LayerNormGradOp& op, cudaStream_t stream) {
-    const Spread s = spread_of(op.cols);
     int strips = wide_strips(op.rows);
     const bool drop = op.drop.on != 0;
     cudaError_t e = cudaSuccess;
-    if (s.v == 0) {
+    if (op.cols > kMaxHeld) {
         // The columns first: dX or dR may be written over dY or H.
         if (op.partial) {
             const dim3 grid(unsigned((op.cols + 255) / 256), static_cast<unsigned>(strips));
@@ -1119,13 +1063,13 @@ cudaError_t launch_grad_typed(const LayerNormGradOp& op, cudaStream_t stream) {
             e = launch_dependent(drop ? layernorm_grad_wide_kernel<XT, true> : layernorm_grad_wide_kernel<XT, false>,
                                  dim3(unsigned(op.rows)), dim3(kMaxTeam), 0, stream, op);
     } else {
-        const bool vec = op.cols % 8 == 0 && rows_aligned(op.dY, op.lddy, op.rows, op.x, 16) &&
-                         rows_aligned(op.H, op.ldh, op.rows, op.x, 16) &&
-                         rows_aligned(op.dH, op.lddh, op.rows, op.x, 16) &&
-                         rows_aligned(op.dX, op.lddx, op.rows, op.x, 16) &&
-                         rows_aligned(op.dR, op.lddr, op.rows, op.x, 16) &&
-                         rows_aligned(op.gamma, 0, 1, op.g, 16);
-        e = drop ? launch_grad<XT, true>(op, s, vec, &strips, stream) : launch_grad<XT, false>(op, s, vec, &strips, stream);
+        const bool aligned = op.cols % kCols<XT> == 0 && rows_aligned(op.dY, op.lddy, op.rows, op.x, 16) &&
+                             rows_aligned(op.H, op.ldh, op.rows, op.x, 16) &&
+                             rows_aligned(op.dH, op.lddh, op.rows, op.x, 16) &&
+                             rows_aligned(op.dX, op.lddx, op.rows, op.x, 16) &&
+                             rows_aligned(op.dR, op.lddr, op.rows, op.x, 16) &&
+                             rows_aligned(op.gamma, 0, 1, op.g, 16);
+        e = drop ? launch_grad<XT, true>(op, aligned, &strips, stream) : launch_grad<XT, false>(op, aligned, &strips, stream);
     }
     if (e != cudaSuccess || !op.partial) return e;
     return launch_column_sums(op.partial, strips, op.cols, op.dgamma, op.dbeta, op.grad, stream);
