@@ -119,12 +119,16 @@ __global__ void __launch_bounds__(kThreads, 4)
 // The gated layer's: Z holds gates g and factors u, N columns of each, and
 //   dZ[m, n] = dY u act'(g),  dZ[m, N + n] = dY act(g),
 // with the sums of both. A thread takes eight outputs, from dY and both halves of
-// Z, and loads the next row while it computes one.
+// Z, which it copies kGatedAhead rows ahead to its own places in shared memory (silu
+// of 4096 x 4096 bf16, dbias alone: 24 us so, 35 with one row ahead in registers).
 //
 // A 32-bit dW takes dZ as two 16-bit values, its rounding and what that left (REST):
 // from the rounding alone it would be off by 2^-9 (bf16) or 2^-12 (f16) of its
 // terms. The rest of an f16 value may lie below f16's normal numbers, so it is kept
 // 2^11 times as large, which fits f16 for every rounding that does.
+constexpr int kGatedAhead = 3;
+using GatedRing = uint4[kGatedAhead][3][kThreads];
+
 template <typename T>
 constexpr float kRestScale = std::is_same<T, __half>::value ? 1.f / 2048.f : 1.f;
 
@@ -139,7 +143,7 @@ __device__ __forceinline__ void rest_of(const float (&x)[8], float (&low)[8]) {
 
 template <typename T, int ACT, int SIDE, bool REST>
 __device__ __forceinline__ void gated_grad_strip(const ActGradOp& op, void* rest, int strips, bool vec,
-                                                 float (&sg)[kPer], float (&su)[kPer]) {
+                                                 GatedRing& ring, float (&sg)[kPer], float (&su)[kPer]) {
     const int t = threadIdx.x % SIDE, lane_row = threadIdx.x / SIDE;
     const int64_t n = (int64_t(blockIdx.x) * SIDE + t) * kPer;
     const int64_t m_begin = op.M * blockIdx.y / strips, m_end = op.M * (blockIdx.y + 1) / strips;
@@ -176,22 +180,27 @@ __device__ __forceinline__ void gated_grad_strip(const ActGradOp& op, void* rest
     if (vec) {
         const T* pd = static_cast<const T*>(op.dY) + n;
         const T* pz = static_cast<const T*>(op.Z) + n;
-        uint4 rd, rg, ru;
-        const auto fetch = [&](int64_t m) {
-            if (m >= m_end) return;
-            rd = *reinterpret_cast<const uint4*>(pd + m * op.lddy);
-            rg = *reinterpret_cast<const uint4*>(pz + m * op.ldz);
-            ru = *reinterpret_cast<const uint4*>(pz + m * op.ldz + op.N);
+        const auto fetch = [&](int slot, int64_t m) {
+            if (m < m_end) {
+                cp_async_16(smem_u32(&ring[slot][0][threadIdx.x]), pd + m * op.lddy, 16);
+                cp_async_16(smem_u32(&ring[slot][1][threadIdx.x]), pz + m * op.ldz, 16);
+                cp_async_16(smem_u32(&ring[slot][2][threadIdx.x]), pz + m * op.ldz + op.N, 16);
+            }
+            cp_async_commit();
         };
-        fetch(m_begin + lane_row);
-        for (int64_t m = m_begin + lane_row; m < m_end; m += kStep) {
+        int64_t m = m_begin + lane_row;
+#pragma unroll
+        for (int i = 0; i < kGatedAhead; ++i) fetch(i, m + i * kStep);
+        for (int slot = 0; m < m_end; m += kStep, slot = slot + 1 == kGatedAhead ? 0 : slot + 1) {
+            cp_async_wait<kGatedAhead - 1>();
             float dy[8], g[8], u[8];
-            unpack8<T>(rd, dy);
-            unpack8<T>(rg, g);
-            unpack8<T>(ru, u);
-            fetch(m + kStep);
+            unpack8<T>(ring[slot][0][threadIdx.x], dy);
+            unpack8<T>(ring[slot][1][threadIdx.x], g);
+            unpack8<T>(ring[slot][2][threadIdx.x], u);
+            fetch(slot, m + kGatedAhead * kStep);
             row(m, dy, g, u);
         }
+        cp_async_wait<0>();
         return;
     }
     for (int64_t m = m_begin + lane_row; m < m_end; m += kStep) {
@@ -207,12 +216,16 @@ template <typename T, int SIDE, bool REST>
 __global__ void __launch_bounds__(kThreads, 3)
     gated_grad_kernel(const __grid_constant__ ActGradOp op, const DzRest rest, int strips, bool vec) {
     constexpr int kRows = kThreads / SIDE, kCols = SIDE * kPer;
-    __shared__ float s[kRows][2][kCols];
+    __shared__ union {
+        GatedRing ring;
+        float s[kRows][2][kCols];
+    } shared;
+    auto& s = shared.s;
     grid_launch_dependents();
     grid_dependency_wait();
     float sg[kPer] = {}, su[kPer] = {};
     with_act(op.act, [&](auto act) {
-        gated_grad_strip<T, decltype(act)::value, SIDE, REST>(op, rest.low, strips, vec, sg, su);
+        gated_grad_strip<T, decltype(act)::value, SIDE, REST>(op, rest.low, strips, vec, shared.ring, sg, su);
     });
     if constexpr (REST) {
         if (blockIdx.y == 0)
@@ -222,6 +235,7 @@ __global__ void __launch_bounds__(kThreads, 3)
             }
     }
     if (!op.dbias) return;
+    __syncthreads();  // (the ring's place)
     const int t = threadIdx.x % SIDE, lane_row = threadIdx.x / SIDE;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
