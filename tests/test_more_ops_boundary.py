@@ -38,7 +38,7 @@ def test_known_words(counter, key, words):
 
 
 def dropout(rows=6, cols=100, ldx=0, ldr=0, ldy=0, x=0, p=0.1, counter=None, Y=addr(0), X=addr(1), R=addr(2)):
-    d = tp.DropoutDesc(rows, cols, ldx, ldr, ldy, x, tp.Drop(p, 1, 2, counter))
+    d = tp.DropoutDesc(rows, cols, ldx, ldr, ldy, x, p, 1, 2, counter)
     return tp.tpgemm_dropout(Y, X, R, d, 0), tp.tpgemm_last_error_detail()
 
 
@@ -73,7 +73,7 @@ def test_dropout_accepts(kw):
 
 def norm(rows=6, cols=100, ldx=0, ldr=0, ldh=0, ldy=0, x=0, g=0, y=0, scale=0, eps=1e-5, p=0.0, counter=None,
          Y=addr(0), H=addr(1), S=addr(2), mean=addr(3), rstd=addr(4), X=addr(5), R=addr(6), G=addr(7), B=addr(8)):
-    d = tp.LayerNormDesc(rows, cols, ldx, ldr, ldh, ldy, x, g, y, scale, eps, tp.Drop(p, 1, 2, counter))
+    d = tp.LayerNormDesc(rows, cols, ldx, ldr, ldh, ldy, x, g, y, scale, eps, p, 1, 2, counter)
     return tp.tpgemm_layernorm(Y, H, S, mean, rstd, X, R, G, B, d, 0), tp.tpgemm_last_error_detail()
 
 
@@ -117,7 +117,7 @@ def norm_backward(rows=6, cols=100, x=0, g=0, grad=8, p=0.0, dX=addr(0), dR=addr
                   dY=addr(4), H=addr(5), mean=addr(6), rstd=addr(7), G=addr(8), dH=addr(9), ws=addr(10), wsb=None,
                   **lds):
     d = tp.LayerNormGradDesc(rows, cols, *[lds.get(n, 0) for n in ("lddy", "ldh", "lddh", "lddx", "lddr")], x, g,
-                             grad, tp.Drop(p, 1, 2, None))
+                             grad, p, 1, 2, None)
     if wsb is None:
         wsb = tp.tpgemm_layernorm_backward_workspace_bytes(rows, cols)
     st = tp.tpgemm_layernorm_backward(dX, dR, dG, dB, dY, H, mean, rstd, G, dH, d, ws, wsb, 0)
