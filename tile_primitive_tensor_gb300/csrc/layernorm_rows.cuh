@@ -1021,11 +1021,10 @@ cudaError_t launch_norm_typed(const LayerNormOp& op, cudaStream_t stream) {
     return op.drop.on ? launch_norm<XT, true>(op, aligned, stream) : launch_norm<XT, false>(op, aligned, stream);
 }
 
-// Two rows to a team at the least, since each block's sums are written and read
-// once more; else what the SMs hold.
+// What the SMs hold, and no more than there are rows.
 int grad_row_blocks(int64_t rows, const RowSpread& s) {
-    const int64_t most = (rows + 2 * s.teams - 1) / (2 * s.teams);
-    return int(std::max<int64_t>(1, std::min<int64_t>(most, int64_t(kSms) * s.blocks)));
+    const int64_t most = (rows + s.teams - 1) / s.teams;
+    return int(std::min<int64_t>(most, int64_t(kSms) * s.blocks));
 }
 
 int wide_strips(int64_t rows) {
