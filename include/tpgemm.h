@@ -679,8 +679,8 @@ size_t tpgemm_rmsnorm_backward_workspace_bytes(int64_t rows, int64_t cols);
  * 0 whatever it was. Which one depends on the seed, the offset and the element's
  * row i and column j alone: word j % 4 of Philox4x32-10 with the counter
  * (j / 4, i, offset low, offset high) and the key (seed low, seed high), each of 32
- * bits, is compared with round(p 2^32); at least that keeps the element. So no mask
- * is stored, and a backward pass with the same numbers draws the same one.
+ * bits, is compared with round(p 2^32) (2^32 - 1 at most); at least that keeps the
+ * element. So no mask is stored, and a backward pass with the same numbers draws the same one.
  */
 typedef struct {
     double p;                /* in [0, 1); 0 keeps everything */
