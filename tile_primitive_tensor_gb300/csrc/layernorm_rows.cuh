@@ -470,7 +470,7 @@ __global__ void __launch_bounds__(RowKernel<T, false>::kThreads, RowKernel<T, fa
                     weights.hold(0, i, op.gamma, column(i));
                     if (op.beta) weights.hold(1, i, op.beta, column(i));
                 }
-        __syncthreads();
+        if (teams > 1) __syncthreads();  // (else each thread reads its own)
     }
     DropOffset offset{};
     if constexpr (DROP) offset = drop_offset(op.drop);
@@ -712,7 +712,7 @@ __global__ void __launch_bounds__(RowKernel<T, true>::kThreads, RowKernel<T, tru
 #pragma unroll
             for (int i = 0; i < P; ++i)
                 if (has(i)) weights.hold(0, i, op.gamma, column(i));
-        __syncthreads();
+        if (teams > 1) __syncthreads();  // (else each thread reads its own)
     }
     DropOffset offset{};
     if constexpr (DROP) offset = drop_offset(op.drop);
@@ -920,13 +920,14 @@ RowSpread row_spread(int64_t rows, int64_t cols, int elem, bool grad, bool align
 }
 
 constexpr int kRingBytes = 216 * 1024;  // of an SM, for its blocks
-// `step`: threads that a block's places are laid out for. A team's only row is copied
-// alone, and the weights that it reads once are not held.
+// `step`: threads that a block's places are laid out for. Of a team's only row no other
+// is copied ahead, and the weights, which it reads once, are held where it is the
+// block's only team: they come beside the row and not after its reductions.
 RingPlan ring_plan(RowSpread* s, bool anywhere, int64_t rows, int step, int inputs, int elem, int vectors, int vector_elem,
                    size_t* bytes) {
     const size_t row = size_t(inputs) * s->p * (step + (anywhere ? step / 32 : 0)) * 16;  // of all teams
     const int64_t turns = (rows + int64_t(kSms) * s->blocks * s->teams - 1) / (int64_t(kSms) * s->blocks * s->teams);
-    size_t held = turns == 1 ? 0 : size_t(vectors) * s->p * s->team * 16 * elem_size(vector_elem) / elem_size(elem);
+    size_t held = turns == 1 && s->teams > 1 ? 0 : size_t(vectors) * s->p * s->team * 16 * elem_size(vector_elem) / elem_size(elem);
     while (s->blocks > 1 && held + row > size_t(kRingBytes / s->blocks)) --s->blocks;
     const size_t have = size_t(kRingBytes / s->blocks);
     if (held + row > have) held = 0;
