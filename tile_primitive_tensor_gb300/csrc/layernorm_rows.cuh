@@ -21,7 +21,7 @@
 // where they wait without holding registers and without a barrier, so that memory is
 // kept busy through a row's reductions. Rows that start anywhere are copied in
 // aligned 16 bytes and joined; rows wider than a team's registers (16384 columns) are
-// read again from L2 for each pass.
+// kept in shared memory as far as it goes, the rest read again for each pass.
 //
 // 8192 x 4096 bf16 with residual 48 us (83 % of memory's rate), with dropout 54
 // (74 %); gradients with dh 50 (80 %) and 65 (77 %), where instructions bound them:
@@ -584,31 +584,62 @@ __global__ void __launch_bounds__(RowKernel<T, false>::kThreads, RowKernel<T, fa
 }
 
 // ---------------------------------------------------------------- wider rows
-// Rows of any width, a block to a row, read once for each pass.
+// Rows of any width, a block to a row, eight columns to a thread at a time. The first
+// `held` such groups keep h in the thread's places in shared memory (49152 columns in
+// all); the others are read again for each pass (2048 x 20480 bf16 with residual 130
+// us, 212 with all read again).
+struct Held {
+    float4* mine;
+    int groups;
+    __device__ __forceinline__ Held(void* smem, int groups) : mine(static_cast<float4*>(smem) + threadIdx.x), groups(groups) {}
+    __device__ __forceinline__ void put(int64_t i, const float (&f)[8]) const {
+        if (i >= groups) return;
+        float4* p = mine + i * 2 * kMaxTeam;
+        p[0] = make_float4(f[0], f[1], f[2], f[3]);
+        p[kMaxTeam] = make_float4(f[4], f[5], f[6], f[7]);
+    }
+    __device__ __forceinline__ bool get(int64_t i, float (&f)[8]) const {
+        if (i >= groups) return false;
+        const float4 *p = mine + i * 2 * kMaxTeam, a = p[0], b = p[kMaxTeam];
+        f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+        f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+        return true;
+    }
+};
+constexpr size_t kHeldGroup = kMaxTeam * 8 * 4;  // bytes of a block's group
+
 template <typename XT, bool VEC, bool DROP>
-__global__ void __launch_bounds__(kMaxTeam) layernorm_wide_kernel(const __grid_constant__ LayerNormOp op) {
+__global__ void __launch_bounds__(kMaxTeam) layernorm_wide_kernel(const __grid_constant__ LayerNormOp op, int held_groups) {
+    extern __shared__ __align__(16) uint8_t ring_smem[];
     __shared__ float2 s[3][32];
-    const int team = int(blockDim.x), t = int(threadIdx.x);
+    constexpr int team = kMaxTeam;
+    const int t = int(threadIdx.x);
     const int64_t row = blockIdx.x;
     const int64_t groups = (op.cols + 8 * team - 1) / (8 * team);
+    const Held held(ring_smem, held_groups);
     grid_launch_dependents();
     grid_dependency_wait();
     DropRow k{};
     if constexpr (DROP) k = drop_row(op.drop, drop_offset(op.drop), uint32_t(row));
     float h[8], y[8];
-    float sum = 0.f;
+    // h of group i (zero past the row).
+    const auto load = [&](int64_t i) {
+        if (!held.get(i, h)) load_sum<XT, VEC, DROP>(op, k, row, Cols<VEC>(i, t, team, op.cols), h);
+    };
+    float sum = 0.f, unused = 0.f;
+#pragma unroll 2
     for (int64_t i = 0; i < groups; ++i) {
         load_sum<XT, VEC, DROP>(op, k, row, Cols<VEC>(i, t, team, op.cols), h);
+        held.put(i, h);
 #pragma unroll
         for (int j = 0; j < 8; ++j) sum += h[j];
     }
-    float unused = 0.f;
     block_sum(sum, unused, s[0]);
     const float mean = sum / float(op.cols);
     float d = 0.f, dd = 0.f;
     for (int64_t i = 0; i < groups; ++i) {
         const Cols<VEC> c(i, t, team, op.cols);
-        load_sum<XT, VEC, DROP>(op, k, row, c, h);
+        load(i);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const float e = j < c.n ? h[j] - mean : 0.f;
@@ -624,24 +655,23 @@ __global__ void __launch_bounds__(kMaxTeam) layernorm_wide_kernel(const __grid_c
     }
     float inv = 1.f;
     if (op.mode == TPGEMM_SCALE_ROW) {
-        float none = 0.f;
         uint32_t amax = 0;
         for (int64_t i = 0; i < groups; ++i) {
             const Cols<VEC> c(i, t, team, op.cols);
-            load_sum<XT, VEC, DROP>(op, k, row, c, h);
+            load(i);
             normalise<XT, VEC>(op, st, c, h, y);
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 if (j < c.n) amax = max(amax, abs_bits(y[j]));
         }
-        team_sum_max<false>(none, amax, s[2]);
+        team_sum_max<false>(unused, amax, s[2]);
         const float scale = row_scale(amax, op.y);
         if (t == 0) op.scale[row] = scale;
         inv = 1.f / scale;
     }
     for (int64_t i = 0; i < groups; ++i) {
         const Cols<VEC> c(i, t, team, op.cols);
-        load_sum<XT, VEC, DROP>(op, k, row, c, h);
+        load(i);
         normalise<XT, VEC>(op, st, c, h, y);
         if (op.mode == TPGEMM_SCALE_ROW) {
 #pragma unroll
@@ -829,45 +859,71 @@ __global__ void __launch_bounds__(RowKernel<T, true>::kThreads, RowKernel<T, tru
     join(ab, out + op.cols);
 }
 
-template <typename XT>
-__device__ __forceinline__ float gamma_at(const LayerNormGradOp& op, int64_t c) {
-    return op.g == TPGEMM_ELEM_F32 ? static_cast<const float*>(op.gamma)[c]
-                                   : to_f32(static_cast<const XT*>(op.gamma)[c]);
-}
-
-// Rows wider than a team's registers: dt a row to a block, read twice, and the
-// column sums apart.
-template <typename XT, bool DROP>
-__global__ void __launch_bounds__(kMaxTeam) layernorm_grad_wide_kernel(const __grid_constant__ LayerNormGradOp op) {
+// Wider rows: dt a row to a block, w and n of the first `held` groups (24576 columns)
+// kept in shared memory, and the column sums apart (2048 x 20480 bf16 with dropout and
+// dh 191 us, 344 with all read again, element by element).
+template <typename XT, bool VEC, bool DROP>
+__global__ void __launch_bounds__(kMaxTeam) layernorm_grad_wide_kernel(const __grid_constant__ LayerNormGradOp op,
+                                                                       int held_groups) {
+    extern __shared__ __align__(16) uint8_t ring_smem[];
     __shared__ float2 s[32];
+    constexpr int team = kMaxTeam;
+    const int t = int(threadIdx.x);
     const int64_t row = blockIdx.x;
+    const int64_t groups = (op.cols + 8 * team - 1) / (8 * team);
+    const Held held(ring_smem, 2 * held_groups);
     grid_launch_dependents();
     grid_dependency_wait();
     DropRow k{};
     if constexpr (DROP) k = drop_row(op.drop, drop_offset(op.drop), uint32_t(row));
-    const XT* dy = static_cast<const XT*>(op.dY) + row * op.lddy;
-    const XT* h = static_cast<const XT*>(op.H) + row * op.ldh;
     const float rstd = op.rstd[row], mean = op.mean[row];
+    float w[8], n[8];
+    const auto load = [&](int64_t i, const Cols<VEC>& c) {
+        float g[8];
+        load_cols<XT, VEC>(op.dY, row * op.lddy, c, w);
+        load_cols<XT, VEC>(op.H, row * op.ldh, c, n);
+        load_gamma<XT, VEC>(op.gamma, op.g, c, g);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            w[j] *= g[j];  // (0 past the row)
+            n[j] = (n[j] - mean) * rstd;
+        }
+    };
     float sw = 0.f, swn = 0.f;
-    for (int64_t c = threadIdx.x; c < op.cols; c += kMaxTeam) {
-        const float w = to_f32(dy[c]) * gamma_at<XT>(op, c);
-        sw += w;
-        swn += w * ((to_f32(h[c]) - mean) * rstd);
+    for (int64_t i = 0; i < groups; ++i) {
+        load(i, Cols<VEC>(i, t, team, op.cols));
+        held.put(2 * i, w);
+        held.put(2 * i + 1, n);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            sw += w[j];
+            swn += w[j] * n[j];
+        }
     }
     block_sum(sw, swn, s);
     sw /= float(op.cols);
     swn /= float(op.cols);
-    for (int64_t c = threadIdx.x; c < op.cols; c += kMaxTeam) {
-        float d = rstd * (to_f32(dy[c]) * gamma_at<XT>(op, c) - sw - (to_f32(h[c]) - mean) * rstd * swn);
-        if (op.dH) d += to_f32(static_cast<const XT*>(op.dH)[row * op.lddh + c]);
-        if (op.dR) static_cast<XT*>(op.dR)[row * op.lddr + c] = from_f32<XT>(d);
+    for (int64_t i = 0; i < groups; ++i) {
+        const Cols<VEC> c(i, t, team, op.cols);
+        float dt[8];
+        if (op.dH) {
+            load_cols<XT, VEC>(op.dH, row * op.lddh, c, dt);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) dt[j] = 0.f;
+        }
+        if (held.get(2 * i, w)) held.get(2 * i + 1, n);
+        else load(i, c);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) dt[j] += rstd * (w[j] - sw - n[j] * swn);
+        if (op.dR) store_cols<XT, VEC>(op.dR, row * op.lddr, c, dt);
         if (op.dX) {
             if constexpr (DROP) {
-                const uint4 w = philox(op.drop, k, uint32_t(c / 4));
-                const int q = int(c & 3);
-                d = keep_one(op.drop, q == 0 ? w.x : q == 1 ? w.y : q == 2 ? w.z : w.w, d) * op.drop.scale;
+                keep_cols<VEC>(op.drop, k, c, dt);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) dt[j] *= op.drop.scale;
             }
-            static_cast<XT*>(op.dX)[row * op.lddx + c] = from_f32<XT>(d);
+            store_cols<XT, VEC>(op.dX, row * op.lddx, c, dt);
         }
     }
 }
@@ -881,6 +937,7 @@ __global__ void __launch_bounds__(256) layernorm_columns_kernel(const __grid_con
     grid_dependency_wait();
     if (c >= op.cols) return;
     float g = 0.f, b = 0.f;
+#pragma unroll 8
     for (int64_t r = begin; r < end; ++r) {
         const float dy = to_f32(static_cast<const XT*>(op.dY)[r * op.lddy + c]);
         g += dy * ((to_f32(static_cast<const XT*>(op.H)[r * op.ldh + c]) - op.mean[r]) * op.rstd[r]);
@@ -986,13 +1043,24 @@ cudaError_t launch_ring(F fn, int64_t blocks, int threads, size_t bytes, const R
     return launch_dependent(fn, dim3(unsigned(blocks)), dim3(unsigned(threads)), bytes, stream, op, plan);
 }
 
+// A block to a row, with room for `values` values of as many columns as fit.
+template <typename F, typename Op>
+cudaError_t launch_wide(F fn, const Op& op, int values, cudaStream_t stream) {
+    const int64_t groups = (op.cols + 8 * kMaxTeam - 1) / (8 * kMaxTeam);
+    const int held = int(std::min<int64_t>(groups, int64_t(kRingBytes / kHeldGroup) / values));
+    const size_t bytes = size_t(held) * values * kHeldGroup;
+    const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(fn),
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
+    if (e != cudaSuccess) return e;
+    return launch_dependent(fn, dim3(unsigned(op.rows)), dim3(kMaxTeam), bytes, stream, op, held);
+}
+
 template <typename XT, bool DROP>
 cudaError_t launch_norm(const LayerNormOp& op, bool aligned, cudaStream_t stream) {
     if (op.rows > 0x7fffffff) return cudaErrorInvalidValue;
     if (op.cols > kMaxHeld)
-        return launch_dependent(aligned && op.cols % 8 == 0 ? layernorm_wide_kernel<XT, true, DROP>
-                                                            : layernorm_wide_kernel<XT, false, DROP>,
-                                dim3(unsigned(op.rows)), dim3(kMaxTeam), 0, stream, op);
+        return launch_wide(aligned && op.cols % 8 == 0 ? layernorm_wide_kernel<XT, true, DROP>
+                                                       : layernorm_wide_kernel<XT, false, DROP>, op, 1, stream);
     RowSpread s = row_spread(op.rows, op.cols, op.x, false, aligned);
     return with_spread<4, sizeof(XT) == 4>(s, aligned, [&](auto p, auto t, auto where) {
         constexpr int P = decltype(p)::value, T = decltype(t)::value;
@@ -1047,6 +1115,12 @@ template <typename XT>
 cudaError_t launch_grad_typed(const LayerNormGradOp& op, cudaStream_t stream) {
     int strips = wide_strips(op.rows);
     const bool drop = op.drop.on != 0;
+    const bool aligned = op.cols % kCols<XT> == 0 && rows_aligned(op.dY, op.lddy, op.rows, op.x, 16) &&
+                         rows_aligned(op.H, op.ldh, op.rows, op.x, 16) &&
+                         rows_aligned(op.dH, op.lddh, op.rows, op.x, 16) &&
+                         rows_aligned(op.dX, op.lddx, op.rows, op.x, 16) &&
+                         rows_aligned(op.dR, op.lddr, op.rows, op.x, 16) &&
+                         rows_aligned(op.gamma, 0, 1, op.g, 16);
     cudaError_t e = cudaSuccess;
     if (op.cols > kMaxHeld) {
         // The columns first: dX or dR may be written over dY or H.
@@ -1054,16 +1128,13 @@ cudaError_t launch_grad_typed(const LayerNormGradOp& op, cudaStream_t stream) {
             const dim3 grid(unsigned((op.cols + 255) / 256), static_cast<unsigned>(strips));
             e = launch_dependent(layernorm_columns_kernel<XT>, grid, dim3(256), 0, stream, op, strips);
         }
-        if (e == cudaSuccess && (op.dX || op.dR))
-            e = launch_dependent(drop ? layernorm_grad_wide_kernel<XT, true> : layernorm_grad_wide_kernel<XT, false>,
-                                 dim3(unsigned(op.rows)), dim3(kMaxTeam), 0, stream, op);
+        if (e == cudaSuccess && (op.dX || op.dR)) {
+            auto fn = aligned && op.cols % 8 == 0
+                          ? (drop ? layernorm_grad_wide_kernel<XT, true, true> : layernorm_grad_wide_kernel<XT, true, false>)
+                          : (drop ? layernorm_grad_wide_kernel<XT, false, true> : layernorm_grad_wide_kernel<XT, false, false>);
+            e = launch_wide(fn, op, 2, stream);
+        }
     } else {
-        const bool aligned = op.cols % kCols<XT> == 0 && rows_aligned(op.dY, op.lddy, op.rows, op.x, 16) &&
-                             rows_aligned(op.H, op.ldh, op.rows, op.x, 16) &&
-                             rows_aligned(op.dH, op.lddh, op.rows, op.x, 16) &&
-                             rows_aligned(op.dX, op.lddx, op.rows, op.x, 16) &&
-                             rows_aligned(op.dR, op.lddr, op.rows, op.x, 16) &&
-                             rows_aligned(op.gamma, 0, 1, op.g, 16);
         e = drop ? launch_grad<XT, true>(op, aligned, &strips, stream) : launch_grad<XT, false>(op, aligned, &strips, stream);
     }
     if (e != cudaSuccess || !op.partial) return e;
