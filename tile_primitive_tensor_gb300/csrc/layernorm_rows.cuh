@@ -24,7 +24,7 @@
 // kept in shared memory as far as it goes, the rest read again for each pass.
 //
 // 8192 x 4096 bf16 with residual 48 us (83 % of memory's rate), with dropout 54
-// (74 %); gradients with dh 50 (80 %) and 65 (77 %), where instructions bound them:
+// (74 %); gradients with dh 46 (87 %) and 65 (77 %), where instructions bound them:
 // 180 and 290 to eight columns, 300 and 320.
 #pragma once
 
@@ -221,11 +221,11 @@ struct RingPlan {
 
 // Gamma and beta, of XT or 32-bit: held in shared memory behind the ring, for all
 // teams of a block (from L2 they would come in the midst of every row), or, of rows
-// too wide for that, read from memory.
-template <typename XT, int P, int ROWS>
+// too wide for that, read from memory. WIDE: held as 32-bit values.
+template <typename XT, int P, int ROWS, bool WIDE>
 struct Weights {
     uint4* mine;     // the thread's first place; null: not held
-    int elem, step;  // their type, and 16-byte units between a thread's places
+    int elem, step;  // their type in memory, and 16-byte units between a thread's places
     int cols;
     // Units of a piece's columns.
     template <typename T>
@@ -245,9 +245,10 @@ struct Weights {
     }
     template <typename T>
     __device__ __forceinline__ void get_as(int which, int piece, const void* p, int c, F2 (&f)[kPairs<XT>]) const {
+        const bool here = mine && (!WIDE || sizeof(T) == 4);
 #pragma unroll
         for (int u = 0; u < kUnits<T>; ++u) {
-            const uint4 v = mine ? mine[((which * P + piece) * kUnits<T> + u) * step]
+            const uint4 v = here ? mine[((which * P + piece) * kUnits<T> + u) * step]
                                  : load(static_cast<const T*>(p), c + u * kCols<T>);
             F2 part[kPairs<T>];
             unpack_pairs<T>(v, part);
@@ -256,14 +257,24 @@ struct Weights {
         }
     }
     __device__ __forceinline__ void get(int which, int piece, const void* p, int c, F2 (&f)[kPairs<XT>]) const {
-        if (elem == TPGEMM_ELEM_F32) get_as<float>(which, piece, p, c, f);
+        if (elem == TPGEMM_ELEM_F32 || (WIDE && mine)) get_as<float>(which, piece, p, c, f);
         else get_as<XT>(which, piece, p, c, f);
     }
     template <typename T>
     __device__ __forceinline__ void hold_as(int which, int piece, const void* p, int c) const {
+        if constexpr (WIDE && sizeof(T) == 2) {
+            F2 f[kPairs<T>];
+            unpack_pairs<T>(load(static_cast<const T*>(p), c), f);
 #pragma unroll
-        for (int u = 0; u < kUnits<T>; ++u)
-            mine[((which * P + piece) * kUnits<T> + u) * step] = load(static_cast<const T*>(p), c + u * kCols<T>);
+            for (int u = 0; u < 2; ++u) {
+                const F2 two[2] = {f[2 * u], f[2 * u + 1]};
+                store_pairs(reinterpret_cast<float*>(mine + ((which * P + piece) * 2 + u) * step), two);
+            }
+        } else {
+#pragma unroll
+            for (int u = 0; u < kUnits<T>; ++u)
+                mine[((which * P + piece) * kUnits<T> + u) * step] = load(static_cast<const T*>(p), c + u * kCols<T>);
+        }
     }
     // By one team.
     __device__ __forceinline__ void hold(int which, int piece, const void* p, int c) const {
@@ -436,7 +447,7 @@ __global__ void __launch_bounds__(RowKernel<T, false>::kThreads, RowKernel<T, fa
     int64_t row = blockIdx.x * teams + team.index;
     const int cols = int(op.cols), depth = plan.depth;
     const Ring<XT, P, RowKernel<T, false>::kThreads, ROWS> ring(ring_smem, depth, op.R ? 2 : 1);
-    const Weights<XT, P, ROWS> weights{
+    const Weights<XT, P, ROWS, false> weights{
         plan.weights_at ? reinterpret_cast<uint4*>(ring_smem + plan.weights_at) + team.t : nullptr, op.g, team.threads(), cols};
     const auto column = [&](int i) { return kCols<XT> * (i * team.threads() + team.t); };
     // Whether piece i is in the row (of rows anywhere: the warp's first lane's is), and its columns there.
@@ -691,6 +702,14 @@ __global__ void __launch_bounds__(kMaxTeam) layernorm_wide_kernel(const __grid_c
 // what a reduction leaves to be used, w and n, is computed a second time from shared
 // memory in place of held in registers, which the columns' sums take. A block's
 // teams add up their sums in order at the end.
+// Whole rows of at most 16 columns to a thread hold gamma as 32-bit values, which saves
+// taking it apart in every row: 8192 x 4096 bf16 with dh 46 us, 50 held as bf16; 8192 x
+// 8192 120 and 121, 65536 x 512 60 and 59. With more columns or an index computed in the
+// row it takes registers that the rows need: 2048 x 16384 100 and 94, 4096 x 4099 122
+// and 108.
+template <typename XT, int P, int T, int ROWS>
+constexpr bool kWideGamma = ROWS == kWhole && T != 0 && P * kPairs<XT> <= 8;
+
 template <typename XT, int P, int T, int ROWS, bool DROP>
 __global__ void __launch_bounds__(RowKernel<T, true>::kThreads, RowKernel<T, true>::kBlocks)
     layernorm_grad_rows_kernel(const __grid_constant__ LayerNormGradOp op, const RingPlan plan) {
@@ -706,7 +725,7 @@ __global__ void __launch_bounds__(RowKernel<T, true>::kThreads, RowKernel<T, tru
     const int cols = int(op.cols), depth = plan.depth;
     const bool rows_wanted = op.dX || op.dR, add_dh = rows_wanted && op.dH;
     const Ring<XT, P, RowKernel<T, true>::kThreads, ROWS> ring(ring_smem, depth, add_dh ? 3 : 2);
-    const Weights<XT, P, ROWS> weights{
+    const Weights<XT, P, ROWS, kWideGamma<XT, P, T, ROWS>> weights{
         plan.weights_at ? reinterpret_cast<uint4*>(ring_smem + plan.weights_at) + team.t : nullptr, op.g, team.threads(), cols};
     const auto column = [&](int i) { return kCols<XT> * (i * team.threads() + team.t); };
     // Whether piece i is in the row (of rows anywhere: the warp's first lane's is), and its columns there.
@@ -1103,7 +1122,8 @@ cudaError_t launch_grad(const LayerNormGradOp& op, bool aligned, int* strips, cu
         constexpr int P = decltype(p)::value, T = decltype(t)::value;
         size_t bytes;
         const RingPlan plan = ring_plan(&s, !aligned, op.rows, RowKernel<T, true>::kThreads,
-                                        op.dH && (op.dX || op.dR) ? 3 : 2, op.x, 1, op.g, &bytes);
+                                        op.dH && (op.dX || op.dR) ? 3 : 2, op.x, 1,
+                                        kWideGamma<XT, P, T, decltype(where)::value> ? TPGEMM_ELEM_F32 : int(op.g), &bytes);
         if (s.teams > 1) bytes = std::max(bytes, size_t(P) * kCols<XT> * s.threads() * 4);  // (the teams' sums)
         *strips = grad_row_blocks(op.rows, s);
         return launch_ring(layernorm_grad_rows_kernel<XT, P, T, decltype(where)::value, DROP>, *strips, s.threads(),
