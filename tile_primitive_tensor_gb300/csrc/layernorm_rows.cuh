@@ -202,14 +202,22 @@ struct Ring {
 };
 constexpr int kMaxDepth = 4;
 
+// Threads of a block of teams of any size: 640 of the norm's, which have 96 registers
+// each then, take more of the teams that do not fill 512 (bf16 4096 x 4099 57 us, 63
+// with 512 threads; 8192 x 2560 31 and 37, 4096 x 6144 34 and 38, f32 4096 x 4099 107
+// and 151), at the price of rows of which as many fit 512 (4096 x 7168 with dropout 62
+// and 58). Eight pieces to a thread want more registers (f32 2048 x 12301 217 and 207),
+// and the gradients do (4096 x 5120 70 and 57).
+constexpr int any_threads(int pieces, bool grad) { return grad || pieces > 4 ? 512 : 640; }
+
 // A spread of rows: P pieces to a thread of a team of T threads (T = 0: any team). T
 // is a constant where the row is whole and T a power of two, since places and
 // addresses then are: 8192 x 4096 bf16 with dropout takes 55 us so, 62 otherwise. Threads of a block at most, and
 // blocks to an SM at least, by the registers that a thread then has: the norm does
 // with 64, the gradients, which hold two sums for each column, with 128.
-template <int T, bool GRAD>
+template <int P, int T, bool GRAD>
 struct RowKernel {
-    static constexpr int kThreads = GRAD && T != 0 && T <= 256 ? 256 : 512;
+    static constexpr int kThreads = T == 0 ? any_threads(P, GRAD) : GRAD && T <= 256 ? 256 : 512;
     static constexpr int kBlocks = T == 0 || (GRAD && T == 512) ? 1 : 2;
 };
 
@@ -437,7 +445,7 @@ __device__ __forceinline__ void store_piece(O* p, int n, const F2 (&f)[N]) {
 }
 
 template <typename XT, int P, int T, int ROWS, bool DROP>
-__global__ void __launch_bounds__(RowKernel<T, false>::kThreads, RowKernel<T, false>::kBlocks)
+__global__ void __launch_bounds__(RowKernel<P, T, false>::kThreads, RowKernel<P, T, false>::kBlocks)
     layernorm_rows_kernel(const __grid_constant__ LayerNormOp op, const RingPlan plan) {
     constexpr int N = kPairs<XT>;
     extern __shared__ __align__(16) uint8_t ring_smem[];
@@ -446,7 +454,7 @@ __global__ void __launch_bounds__(RowKernel<T, false>::kThreads, RowKernel<T, fa
     const int64_t teams = blockDim.x / unsigned(team.threads()), stride = gridDim.x * teams;
     int64_t row = blockIdx.x * teams + team.index;
     const int cols = int(op.cols), depth = plan.depth;
-    const Ring<XT, P, RowKernel<T, false>::kThreads, ROWS> ring(ring_smem, depth, op.R ? 2 : 1);
+    const Ring<XT, P, RowKernel<P, T, false>::kThreads, ROWS> ring(ring_smem, depth, op.R ? 2 : 1);
     const Weights<XT, P, ROWS, false> weights{
         plan.weights_at ? reinterpret_cast<uint4*>(ring_smem + plan.weights_at) + team.t : nullptr, op.g, team.threads(), cols};
     const auto column = [&](int i) { return kCols<XT> * (i * team.threads() + team.t); };
@@ -711,7 +719,7 @@ template <typename XT, int P, int T, int ROWS>
 constexpr bool kWideGamma = ROWS == kWhole && T != 0 && P * kPairs<XT> <= 8;
 
 template <typename XT, int P, int T, int ROWS, bool DROP>
-__global__ void __launch_bounds__(RowKernel<T, true>::kThreads, RowKernel<T, true>::kBlocks)
+__global__ void __launch_bounds__(RowKernel<P, T, true>::kThreads, RowKernel<P, T, true>::kBlocks)
     layernorm_grad_rows_kernel(const __grid_constant__ LayerNormGradOp op, const RingPlan plan) {
     constexpr int N = kPairs<XT>;
     extern __shared__ __align__(16) uint8_t ring_smem[];
@@ -724,7 +732,7 @@ __global__ void __launch_bounds__(RowKernel<T, true>::kThreads, RowKernel<T, tru
     int64_t row = int64_t(blockIdx.x) * teams + team.index;
     const int cols = int(op.cols), depth = plan.depth;
     const bool rows_wanted = op.dX || op.dR, add_dh = rows_wanted && op.dH;
-    const Ring<XT, P, RowKernel<T, true>::kThreads, ROWS> ring(ring_smem, depth, add_dh ? 3 : 2);
+    const Ring<XT, P, RowKernel<P, T, true>::kThreads, ROWS> ring(ring_smem, depth, add_dh ? 3 : 2);
     const Weights<XT, P, ROWS, kWideGamma<XT, P, T, ROWS>> weights{
         plan.weights_at ? reinterpret_cast<uint4*>(ring_smem + plan.weights_at) + team.t : nullptr, op.g, team.threads(), cols};
     const auto column = [&](int i) { return kCols<XT> * (i * team.threads() + team.t); };
@@ -990,9 +998,9 @@ RowSpread row_spread(int64_t rows, int64_t cols, int elem, bool grad, bool align
     const int team = (pieces + 32 * p - 1) / (32 * p) * 32;
     const bool whole = aligned && most > 1 && team * p == pieces;
     const int t = whole && (team & (team - 1)) == 0 ? team : 0;
-    const int threads = grad && t != 0 && t <= 256 ? 256 : 512;
+    const int threads = t == 0 ? any_threads(p, grad) : grad && t <= 256 ? 256 : 512;
     const int teams = int(std::max<int64_t>(1, std::min<int64_t>(threads / team, rows / kSms)));
-    return {p, t, whole, team, teams, std::max(1, std::min((grad || t == 0 ? 512 : 1024) / (team * teams), 8))};
+    return {p, t, whole, team, teams, std::max(1, std::min((t == 0 ? threads : grad ? 512 : 1024) / (team * teams), 8))};
 }
 
 constexpr int kRingBytes = 216 * 1024;  // of an SM, for its blocks
@@ -1084,7 +1092,7 @@ cudaError_t launch_norm(const LayerNormOp& op, bool aligned, cudaStream_t stream
     return with_spread<4, sizeof(XT) == 4>(s, aligned, [&](auto p, auto t, auto where) {
         constexpr int P = decltype(p)::value, T = decltype(t)::value;
         size_t bytes;
-        const RingPlan plan = ring_plan(&s, !aligned, op.rows, RowKernel<T, false>::kThreads, op.R ? 2 : 1, op.x,
+        const RingPlan plan = ring_plan(&s, !aligned, op.rows, RowKernel<P, T, false>::kThreads, op.R ? 2 : 1, op.x,
                                         op.beta ? 2 : 1, op.g, &bytes);
         const int64_t blocks = std::min<int64_t>((op.rows + s.teams - 1) / s.teams, int64_t(kSms) * s.blocks);
         return launch_ring(layernorm_rows_kernel<XT, P, T, decltype(where)::value, DROP>, blocks, s.threads(), bytes,
@@ -1121,7 +1129,7 @@ cudaError_t launch_grad(const LayerNormGradOp& op, bool aligned, int* strips, cu
     return with_spread<sizeof(XT) == 4 ? 4 : 2, true>(s, aligned, [&](auto p, auto t, auto where) {
         constexpr int P = decltype(p)::value, T = decltype(t)::value;
         size_t bytes;
-        const RingPlan plan = ring_plan(&s, !aligned, op.rows, RowKernel<T, true>::kThreads,
+        const RingPlan plan = ring_plan(&s, !aligned, op.rows, RowKernel<P, T, true>::kThreads,
                                         op.dH && (op.dX || op.dR) ? 3 : 2, op.x, 1,
                                         kWideGamma<XT, P, T, decltype(where)::value> ? TPGEMM_ELEM_F32 : int(op.g), &bytes);
         if (s.teams > 1) bytes = std::max(bytes, size_t(P) * kCols<XT> * s.threads() * 4);  // (the teams' sums)
