@@ -30,7 +30,7 @@ SOURCES = ["tpgemm_api.cu", "tc_gemm.cu", "mma_sync_gemm.cu", "tmem_copy.cu", "v
            "layernorm_bf16.cu", "layernorm_f32.cu",
            "dropout.cu"]
 HEADERS = ["ptx.cuh", "tpgemm_internal.h", "ops_internal.h", "elem.cuh", "column_sum.cuh",
-           "linear_tc.h", "vec8.cuh", "launch.cuh", "norm_rows.cuh", "philox.cuh",
+           "linear_tc.h", "vec8.cuh", "windows.h", "launch.cuh", "norm_rows.cuh", "philox.cuh",
            "layernorm_rows.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

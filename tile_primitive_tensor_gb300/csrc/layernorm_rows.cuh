@@ -34,6 +34,7 @@
 #include "launch.cuh"
 #include "norm_rows.cuh"
 #include "philox.cuh"
+#include "windows.h"
 
 namespace tpg {
 namespace {
@@ -148,7 +149,7 @@ __device__ __forceinline__ int off16(const void* p) { return int(reinterpret_cas
 // needed. Of others a piece's place holds the aligned 16 bytes that it starts in, and
 // the piece is joined from there and the next lane's place; a place more for each warp
 // holds the bytes behind its last lane's. (Bytes before a row's start are read with
-// those of its 16, not those behind its end.)
+// those of its 16, but not those before the matrix or behind a row's end.)
 template <typename T, int P, int STEP, int ROWS>  // STEP: threads that places are laid out for
 struct Ring {
     uint4* base;
@@ -162,19 +163,25 @@ struct Ring {
     __device__ __forceinline__ static int spare(int input, int piece) {
         return place(input, piece) + STEP + int(threadIdx.x >> 5) - int(threadIdx.x);
     }
-    // The piece at column c of the row of `cols` columns at p; the whole warp calls it.
-    __device__ __forceinline__ void fetch(uint4* row, int input, int piece, const T* p, int c, int cols) const {
+    // The piece at column c of the row of `cols` columns at p, of the matrix at `base`; the
+    // whole warp calls it. FIRST: p may be one of the matrix's first eight rows, of which
+    // short ones may all start in the 16 bytes that the matrix does.
+    template <bool FIRST>
+    __device__ __forceinline__ void fetch(uint4* row, int input, int piece, const void* base, const T* p, int c,
+                                          int cols) const {
         if constexpr (ROWS != kAnywhere) {
             cp_async_16(smem_u32(row + place(input, piece)), p + c, 16);
         } else {
-            const uintptr_t end = reinterpret_cast<uintptr_t>(p + cols), start = reinterpret_cast<uintptr_t>(p) & ~uintptr_t(15);
-            uintptr_t at = start + uintptr_t(c) * sizeof(T);
-            cp_async_16(smem_u32(row + place(input, piece)), reinterpret_cast<const void*>(at < end ? at : start),
-                        at < end ? uint32_t(min(uintptr_t(16), end - at)) : 0u);
+            const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+            const uint64_t bytes = uint64_t(cols) * sizeof(T), offset = uint64_t(c) * sizeof(T);
+            const CopyWindow w = copy_window(at, bytes, offset);
+            if (FIRST && piece == 0 && begins_apart(at, reinterpret_cast<uintptr_t>(base), offset))
+                row[place(input, 0)] = load_window(reinterpret_cast<const uint8_t*>(p), -int64_t(at & 15), int64_t(bytes));
+            else
+                cp_async_16(smem_u32(row + place(input, piece)), reinterpret_cast<const void*>(w.at), w.bytes);
             if ((threadIdx.x & 31) == 31) {
-                at += 16;
-                cp_async_16(smem_u32(row + spare(input, piece)), reinterpret_cast<const void*>(at < end ? at : start),
-                            at < end ? uint32_t(min(uintptr_t(16), end - at)) : 0u);
+                const CopyWindow v = copy_window(at, bytes, offset + 16);
+                cp_async_16(smem_u32(row + spare(input, piece)), reinterpret_cast<const void*>(v.at), v.bytes);
             }
         }
     }
@@ -463,24 +470,28 @@ __global__ void __launch_bounds__(RowKernel<P, T, false>::kThreads, RowKernel<P,
         return ROWS == kWhole || column(i) - (ROWS == kAnywhere ? kCols<XT> * int(threadIdx.x & 31) : 0) < cols;
     };
     const auto count = [&](int i) { return ROWS == kAnywhere ? max(0, min(kCols<XT>, cols - column(i))) : kCols<XT>; };
-    const auto fetch = [&](int64_t r, uint4* place) {
+    // (first: whether r may be one of the first eight rows, a constant. Blocks' later rows
+    // are not: a turn of the grid takes all rows, or 152 and more.)
+    const auto fetch = [&](int64_t r, uint4* place, auto first) {
+        constexpr bool kFirst = decltype(first)::value;
         if (r < op.rows) {
             const XT* x = static_cast<const XT*>(op.X) + r * op.ldx;
 #pragma unroll
             for (int i = 0; i < P; ++i)
-                if (has(i)) ring.fetch(place, 0, i, x, column(i), cols);
+                if (has(i)) ring.template fetch<kFirst>(place, 0, i, op.X, x, column(i), cols);
             if (op.R) {
                 const XT* q = static_cast<const XT*>(op.R) + r * op.ldr;
 #pragma unroll
                 for (int i = 0; i < P; ++i)
-                    if (has(i)) ring.fetch(place, 1, i, q, column(i), cols);
+                    if (has(i)) ring.template fetch<kFirst>(place, 1, i, op.R, q, column(i), cols);
             }
         }
         cp_async_commit();
     };
     grid_launch_dependents();
     grid_dependency_wait();
-    for (int i = 0; i < depth; ++i) fetch(row + i * stride, ring.row(i));
+    if (ROWS == kAnywhere) fetch(row, ring.row(0), std::true_type());
+    for (int i = ROWS == kAnywhere; i < depth; ++i) fetch(row + i * stride, ring.row(i), std::false_type());
     if (weights.mine) {
         if (team.index == 0)
 #pragma unroll
@@ -523,7 +534,7 @@ __global__ void __launch_bounds__(RowKernel<P, T, false>::kThreads, RowKernel<P,
             }
         }
         ring.pass_on();
-        fetch(row + depth * stride, place);
+        fetch(row + depth * stride, place, std::false_type());
         float sum[1] = {sum_of(part)};
         team.sum(sum, s[0]);
         const float mean = sum[0] * inv_n;
@@ -741,7 +752,10 @@ __global__ void __launch_bounds__(RowKernel<P, T, true>::kThreads, RowKernel<P, 
         return ROWS == kWhole || column(i) - (ROWS == kAnywhere ? kCols<XT> * int(threadIdx.x & 31) : 0) < cols;
     };
     const auto count = [&](int i) { return ROWS == kAnywhere ? max(0, min(kCols<XT>, cols - column(i))) : kCols<XT>; };
-    const auto fetch = [&](int64_t r, int slot) {
+    // (first: whether r may be one of the first eight rows, a constant. Blocks' later rows
+    // are not: a turn of the grid takes all rows, or 152 and more.)
+    const auto fetch = [&](int64_t r, int slot, auto first) {
+        constexpr bool kFirst = decltype(first)::value;
         uint4* const place = ring.row(slot);
         if (r < op.rows) {
             // (A load that the next row waits for would take as long as that row.)
@@ -754,16 +768,17 @@ __global__ void __launch_bounds__(RowKernel<P, T, true>::kThreads, RowKernel<P, 
 #pragma unroll
             for (int i = 0; i < P; ++i) {
                 if (!has(i)) continue;
-                ring.fetch(place, 0, i, dy, column(i), cols);
-                ring.fetch(place, 1, i, h, column(i), cols);
-                if (add_dh) ring.fetch(place, 2, i, dh, column(i), cols);
+                ring.template fetch<kFirst>(place, 0, i, op.dY, dy, column(i), cols);
+                ring.template fetch<kFirst>(place, 1, i, op.H, h, column(i), cols);
+                if (add_dh) ring.template fetch<kFirst>(place, 2, i, op.dH, dh, column(i), cols);
             }
         }
         cp_async_commit();
     };
     grid_launch_dependents();
     grid_dependency_wait();
-    for (int i = 0; i < depth; ++i) fetch(row + i * stride, i);
+    if (ROWS == kAnywhere) fetch(row, 0, std::true_type());
+    for (int i = ROWS == kAnywhere; i < depth; ++i) fetch(row + i * stride, i, std::false_type());
     if (rows_wanted && weights.mine) {
         if (team.index == 0)
 #pragma unroll
@@ -854,7 +869,7 @@ __global__ void __launch_bounds__(RowKernel<P, T, true>::kThreads, RowKernel<P, 
             }
         }
         __syncwarp();  // (the warp has read its statistics)
-        fetch(row + depth * stride, slot);
+        fetch(row + depth * stride, slot, std::false_type());
     }
     cp_async_wait<0>();
     if (!op.partial) return;
