@@ -1074,12 +1074,18 @@ cudaError_t with_spread(const RowSpread& s, bool aligned, F&& f) {
     }
 }
 
+// Lets a kernel use all of kRingBytes: the most that any call of it wants, and not this
+// call's, since the limit is the kernel's and another thread may be about to launch it.
+template <typename F>
+cudaError_t allow_ring(F fn) {
+    return cudaFuncSetAttribute(reinterpret_cast<const void*>(fn), cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+}
+
 template <typename F, typename Op>
 cudaError_t launch_ring(F fn, int64_t blocks, int threads, size_t bytes, const RingPlan& plan, cudaStream_t stream,
                         const Op& op) {
     if (bytes > 40 * 1024) {  // (with the kernel's own, more than a block has without asking)
-        const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(fn),
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
+        const cudaError_t e = allow_ring(fn);
         if (e != cudaSuccess) return e;
     }
     return launch_dependent(fn, dim3(unsigned(blocks)), dim3(unsigned(threads)), bytes, stream, op, plan);
@@ -1091,8 +1097,7 @@ cudaError_t launch_wide(F fn, const Op& op, int values, cudaStream_t stream) {
     const int64_t groups = (op.cols + 8 * kMaxTeam - 1) / (8 * kMaxTeam);
     const int held = int(std::min<int64_t>(groups, int64_t(kRingBytes / kHeldGroup) / values));
     const size_t bytes = size_t(held) * values * kHeldGroup;
-    const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(fn),
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
+    const cudaError_t e = allow_ring(fn);
     if (e != cudaSuccess) return e;
     return launch_dependent(fn, dim3(unsigned(op.rows)), dim3(kMaxTeam), bytes, stream, op, held);
 }
