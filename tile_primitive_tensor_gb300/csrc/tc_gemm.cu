@@ -1105,8 +1105,9 @@ cudaError_t launch_tc(const TcMaps& maps, const TcParams& p, int grid, cudaStrea
     const size_t smem = tc_smem_bytes(p.stages, p.p_bytes + p.q_bytes + p.sf_bytes, p.epi_bufs);
     if (smem > size_t(kTcMaxSmem)) return cudaErrorInvalidConfiguration;
     auto kernel = pick_kernel(p);
+    // (The limit is the kernel's, which another thread may be about to launch with more.)
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         int(smem));
+                                         kTcMaxSmem);
     if (e != cudaSuccess) return e;
     // Programmatic dependent launch: this grid's set-up may overlap the tail of
     // the previous kernel in the stream; the kernel waits (griddepcontrol.wait)
@@ -1133,7 +1134,7 @@ cudaError_t tc_max_active_clusters(const TcParams& p, int* clusters) {
     const size_t smem = tc_smem_bytes(p.stages, p.p_bytes + p.q_bytes + p.sf_bytes, p.epi_bufs);
     auto kernel = pick_kernel(p);
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         int(smem));
+                                         kTcMaxSmem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(p.mc));

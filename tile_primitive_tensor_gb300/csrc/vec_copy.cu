@@ -313,8 +313,9 @@ tpgemm_status tpgemm_vcopy_roundtrip(void* dst, const void* src, size_t buffer_b
     auto* i = static_cast<const uint8_t*>(src);
     cudaError_t e = cudaSuccess;
     auto launch = [&](auto kernel) {
+        // (The limit is the kernel's, which another thread may be about to launch with more.)
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 p.smem_bytes);
+                                 kMaxSmemBytes);
         if (e == cudaSuccess) {
             kernel<<<ctas, d->threads, p.smem_bytes, st>>>(o, i, so, kp);
             e = cudaGetLastError();
