@@ -174,8 +174,10 @@ __device__ __forceinline__ F2 act_fwd(F2 z) {
     return z;
 }
 
-// act'(z) of a pair, as exactly as a 16-bit dZ needs it.
-template <int ACT>
+// act'(z) of a pair, as exactly as a 16-bit dZ needs it, or FINE: gelu's, a sum of a
+// tail and of a product below a quarter, then within 2^-21 in place of 2^-20. (The
+// others have one form.)
+template <int ACT, bool FINE = false>
 __device__ __forceinline__ F2 act_bwd(F2 z) {
     if constexpr (ACT == TPGEMM_ACT_RELU) {
         float a, b;
@@ -189,7 +191,7 @@ __device__ __forceinline__ F2 act_bwd(F2 z) {
     if constexpr (ACT == TPGEMM_ACT_GELU) {
         // Phi(z) + z phi(z), Phi(z) = tail or 1 - tail
         const F2 e = exp2_2(mul(mul(z, z), f2(-0.5f * kLog2e)));
-        const F2 q = normal_tail<false>(minus_abs16_2(z));
+        const F2 q = normal_tail<FINE>(minus_abs16_2(z));
         float qa, qb, a, b;
         split(q, qa, qb);
         split(z, a, b);

@@ -125,7 +125,10 @@ __global__ void __launch_bounds__(kThreads, 4)
 // A 32-bit dW takes dZ as two 16-bit values, its rounding and what that left (REST):
 // from the rounding alone it would be off by 2^-9 (bf16) or 2^-12 (f16) of its
 // terms. The rest of an f16 value may lie below f16's normal numbers, so it is kept
-// 2^11 times as large, which fits f16 for every rounding that does.
+// 2^11 times as large, which fits f16 for every rounding that does. Activations are
+// then those of 32-bit results (FINE), and so for a 32-bit dbias: gelu's other form is
+// off by up to 1e-4 of itself, ten times what the two values of dZ lose (dbias alone of
+// 4096 x 4096 with gelu 31 us, 29 with that form).
 constexpr int kGatedAhead = 3;
 using GatedRing = uint4[kGatedAhead][3][kThreads];
 
@@ -141,7 +144,7 @@ __device__ __forceinline__ void rest_of(const float (&x)[8], float (&low)[8]) {
     }
 }
 
-template <typename T, int ACT, int SIDE, bool REST>
+template <typename T, int ACT, int SIDE, bool REST, bool FINE>
 __device__ __forceinline__ void gated_grad_strip(const ActGradOp& op, void* rest, int strips, bool vec,
                                                  GatedRing& ring, float (&sg)[kPer], float (&su)[kPer]) {
     const int t = threadIdx.x % SIDE, lane_row = threadIdx.x / SIDE;
@@ -156,8 +159,8 @@ __device__ __forceinline__ void gated_grad_strip(const ActGradOp& op, void* rest
 #pragma unroll
         for (int j = 0; j < 8; j += 2) {
             const F2 z = f2(g[j], g[j + 1]), d = f2(dy[j], dy[j + 1]);
-            split(mul(mul(d, f2(u[j], u[j + 1])), act_bwd<ACT>(z)), dg[j], dg[j + 1]);
-            split(mul(d, act_fwd<ACT, false>(z)), du[j], du[j + 1]);
+            split(mul(mul(d, f2(u[j], u[j + 1])), act_bwd<ACT, FINE>(z)), dg[j], dg[j + 1]);
+            split(mul(d, act_fwd<ACT, FINE>(z)), du[j], du[j + 1]);
         }
         // The two products read dZ in the operands' own type.
         if (op.dZ) {
@@ -212,7 +215,7 @@ __device__ __forceinline__ void gated_grad_strip(const ActGradOp& op, void* rest
     }
 }
 
-template <typename T, int SIDE, bool REST>
+template <typename T, int SIDE, bool REST, bool FINE>
 __global__ void __launch_bounds__(kThreads, 3)
     gated_grad_kernel(const __grid_constant__ ActGradOp op, const DzRest rest, int strips, bool vec) {
     constexpr int kRows = kThreads / SIDE, kCols = SIDE * kPer;
@@ -225,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, 3)
     grid_dependency_wait();
     float sg[kPer] = {}, su[kPer] = {};
     with_act(op.act, [&](auto act) {
-        gated_grad_strip<T, decltype(act)::value, SIDE, REST>(op, rest.low, strips, vec, shared.ring, sg, su);
+        gated_grad_strip<T, decltype(act)::value, SIDE, REST, FINE>(op, rest.low, strips, vec, shared.ring, sg, su);
     });
     if constexpr (REST) {
         if (blockIdx.y == 0)
@@ -335,7 +338,7 @@ cudaError_t launch_act_grad(const ActGradOp& op, cudaStream_t stream) {
 
 int gated_grad_strips(int64_t M, int64_t N) { return act_grad_strips(M, N); }
 
-template <typename T, bool REST>
+template <typename T, bool REST, bool FINE>
 static cudaError_t launch_gated_typed(const ActGradOp& op, const DzRest& rest, cudaStream_t stream) {
     const int strips = gated_grad_strips(op.M, op.N);
     const bool few = strips == 1;
@@ -346,19 +349,23 @@ static cudaError_t launch_gated_typed(const ActGradOp& op, const DzRest& rest, c
         return !p || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && (op.M <= 1 || ld % 8 == 0));
     };
     const bool vec = op.N % 8 == 0 && rows16(op.dY, op.lddy) && rows16(op.Z, op.ldz) && rows16(op.dZ, op.lddz);
-    auto fn = few ? gated_grad_kernel<T, kNarrow, REST> : gated_grad_kernel<T, kWide, REST>;
+    auto fn = few ? gated_grad_kernel<T, kNarrow, REST, FINE> : gated_grad_kernel<T, kWide, REST, FINE>;
     const cudaError_t e = launch_dependent(fn, dim3(unsigned(cb), unsigned(strips)), dim3(kThreads), 0, stream, op,
                                            rest, strips, vec);
     if (e != cudaSuccess || !op.dbias || few) return e;
     return launch_column_sum(op.partial, strips, 2 * op.N, op.dbias, op.grad, stream);
 }
 
+template <typename T>
+static cudaError_t launch_gated_of(const ActGradOp& op, const DzRest& rest, cudaStream_t stream) {
+    if (op.grad != TPGEMM_ELEM_F32) return launch_gated_typed<T, false, false>(op, rest, stream);
+    return rest.low ? launch_gated_typed<T, true, true>(op, rest, stream)
+                    : launch_gated_typed<T, false, true>(op, rest, stream);
+}
+
 cudaError_t launch_gated_grad(const ActGradOp& op, const DzRest& rest, cudaStream_t stream) {
-    if (op.dtype == TPGEMM_ELEM_F16)
-        return rest.low ? launch_gated_typed<__half, true>(op, rest, stream)
-                        : launch_gated_typed<__half, false>(op, rest, stream);
-    return rest.low ? launch_gated_typed<__nv_bfloat16, true>(op, rest, stream)
-                    : launch_gated_typed<__nv_bfloat16, false>(op, rest, stream);
+    return op.dtype == TPGEMM_ELEM_F16 ? launch_gated_of<__half>(op, rest, stream)
+                                       : launch_gated_of<__nv_bfloat16>(op, rest, stream);
 }
 
 constexpr int64_t kAlignBlocks = 8 * kSms;  // eight to an SM; a warp then has several rows' loads in flight
