@@ -1,6 +1,6 @@
 """32-bit gradients of the gated linear layer against 64 bits, by bounds that leave no room for a dZ of
-16 bits or an activation made for 16-bit results (GPU only): every activation, and more tokens than
-one sum takes."""
+16 bits or an activation made for 16-bit results (GPU only): every activation, more tokens than one
+sum takes, and infinities."""
 import pytest
 import torch
 
@@ -99,3 +99,29 @@ def test_negative_gates(M, dtype, act):
     pre = torch.cat([gates.expand(M, 64), 0.5 + torch.rand(M, 64, generator=g, device="cuda").to(dtype)], 1)
     dY, A = ((0.5 + torch.rand(M, n, generator=g, device="cuda")).to(dtype) for n in (64, 72))
     check(dY, A, gl.view(g, 128, 72, dtype), pre, act)
+
+
+@pytest.mark.parametrize("path", ["tile", "split"])
+@pytest.mark.parametrize("M,N,K", [(100, 40, 264), (300, 40, 265), (5000, 72, 136)])
+@pytest.mark.parametrize("whole", [True, False])
+def test_infinities_of_the_input(M, N, K, whole, path, tune):
+    # An infinite A[m, k] makes column k of dW infinite with dZ[m]'s signs, whether dZ is a 16-bit value
+    # (whole numbers) or not, and a second one of the other sign a NaN where those signs agree.
+    tune.setenv("TPGEMM_LINEAR_PATH", path)
+    for dtype in (F16, BF16):
+        dY, A, W, pre = args(M, N, K, dtype, 3)
+        if whole:
+            dY, pre = dY.sign() + (dY == 0), (pre * 4).round() + (pre.abs() <= 0.125)
+        A[7, 5], A[M - 1, 5], A[M - 2, 9] = float("inf"), float("-inf"), float("-inf")
+        _, dW, _ = tp.gated_linear_backward(dY, A, W, pre, act="none", grad_dtype=F32)
+        dz, _ = dz_of(dY, pre, "none")
+        assert (dz[[7, M - 1, M - 2]] != 0).all()
+        assert torch.equal(dW[:, 9].double(), dz[M - 2].sign() * float("-inf"))
+        meet = dz[7].sign() * float("inf") + dz[M - 1].sign() * float("-inf")
+        assert torch.equal(torch.isnan(dW[:, 5]), torch.isnan(meet))
+        assert torch.equal(dW[:, 5].double()[~torch.isnan(meet)], meet[~torch.isnan(meet)])
+        rest = [k for k in range(K) if k not in (5, 9)]
+        clean = A.clone()
+        clean[:, [5, 9]] = 0
+        _, want, _ = tp.gated_linear_backward(dY, clean, W, pre, act="none", grad_dtype=F32)
+        assert torch.equal(dW[:, rest], want[:, rest])

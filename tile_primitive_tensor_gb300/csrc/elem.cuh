@@ -230,6 +230,18 @@ __device__ __forceinline__ void with_act(int act, F&& f) {
     }
 }
 
+// x[i] += r[i], the residual; as the rest of it (see Epilogue), where that is finite.
+template <typename T, int N>
+__device__ __forceinline__ void add_residual(int rest, const float (&r)[N], float* x) {
+    if (sizeof(T) == 4 && rest) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) x[i] = isfinite(r[i]) ? x[i] + r[i] : r[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) x[i] += r[i];
+    }
+}
+
 // The epilogue of output (m, n), in 32 bits until the one rounding of each store.
 template <typename T, int ACT>
 __device__ __forceinline__ void epilogue_one(const Epilogue& e, int64_t m, int64_t n, float x) {
@@ -238,7 +250,10 @@ __device__ __forceinline__ void epilogue_one(const Epilogue& e, int64_t m, int64
     if (e.bias) x += to_f32(static_cast<const T*>(e.bias)[n]);
     if (e.Z) static_cast<T*>(e.Z)[m * e.ldz + n] = from_f32<T>(x);
     x = act_fwd<ACT, sizeof(T) == 4>(x);
-    if (e.R) x += to_f32(static_cast<const T*>(e.R)[m * e.ldr + n]);
+    if (e.R) {
+        const float r[1] = {to_f32(static_cast<const T*>(e.R)[m * e.ldr + n])};
+        add_residual<T>(e.rest, r, &x);
+    }
     static_cast<T*>(e.Y)[m * e.ldy + n] = from_f32<T>(x);
 }
 

@@ -255,9 +255,10 @@ __device__ __forceinline__ void epilogue_turned(const Epilogue& e, int64_t m0, i
         }
         act_n<T>(e.act, x);
         if (e.R) {
+            float r[32];
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-                if (i < rows) x[i] += to_f32(res[i]);
+            for (int i = 0; i < 32; ++i) r[i] = i < rows ? to_f32(res[i]) : 0.f;
+            add_residual<T>(e.rest, r, x);
         }
         T* y = static_cast<T*>(e.Y) + m0 * e.ldy + n;
 #pragma unroll
@@ -341,7 +342,7 @@ __device__ __forceinline__ void stage_row32(uint8_t* buf, int lane, const float 
 }
 
 template <typename T>
-__device__ __forceinline__ void add_staged32(uint8_t* buf, int lane, float (&x)[32]) {
+__device__ __forceinline__ void add_staged32(uint8_t* buf, int lane, int rest, float (&x)[32]) {
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
         float f[8];
@@ -354,8 +355,7 @@ __device__ __forceinline__ void add_staged32(uint8_t* buf, int lane, float (&x)[
         } else {
             unpack8<T>(*staged_unit<T>(buf, lane, g), f);
         }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[8 * g + i] += f[i];
+        add_residual<T>(rest, f, x + 8 * g);
     }
 }
 
@@ -857,7 +857,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     if (!ok) break;
                     rphase ^= 1u << j;
                     rpend &= ~(1u << j);
-                    add_staged32<T>(buf, lane, x);
+                    add_staged32<T>(buf, lane, p.e.rest, x);
                 } else {
                     if (p.e.R && live) {
 #pragma unroll
@@ -865,8 +865,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                             float f[8];
                             const int64_t left = p.Nq - (n + 8 * g);
                             load8<T>(p.e.R, m * p.e.ldr + n + 8 * g, left >= 8, left < 8 ? int(left) : 8, f);
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) x[8 * g + i] += f[i];
+                            add_residual<T>(p.e.rest, f, x + 8 * g);
                         }
                     }
                     // The buffer's last store has been read (with Z: all but Z's).
@@ -1107,10 +1106,7 @@ __device__ __forceinline__ void join_lines(const TcLinear& p, const float* part,
                 for (int i = 0; i < 4; ++i) x[j][i] = fmaf(x[j][i], sa * sw[i], bias[i]);
                 if (e.Z) store4<T>(e.Z, m * e.ldz + n, vec, cnt, x[j]);
                 act_n<T>(e.act, x[j]);
-                if (e.R) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) x[j][i] += res[j][i];
-                }
+                if (e.R) add_residual<T>(e.rest, res[j], x[j]);
                 store4<T>(e.Y, m * e.ldy + n, vec, cnt, x[j]);
             }
         }

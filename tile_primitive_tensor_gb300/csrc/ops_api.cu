@@ -422,6 +422,7 @@ tpgemm_status linear_gradients(bool gated, void* dA, void* dW, void* dbias, cons
             op.a.p = ws + L.rest;
             op.b.p = oa.p;
             op.e.R = dW;
+            op.e.rest = 1;
             op.e.sa = reinterpret_cast<const float*>(ws + L.rest_scale);
             TPG_TRY(run_product(op, sms, st));
         }

@@ -53,7 +53,10 @@ struct Operand {
 // What happens to an accumulator x of output (m, n):
 //   z = sa[m] sw[n] x + bias[n]  (z is stored to Z when given),
 //   Y[m, n] = act(z) + R[m, n].
-// Y, Z, R and bias are of type `out`; every pointer but Y may be null.
+// Y, Z, R and bias are of type `out`; every pointer but Y may be null. rest: z is what
+// R, a 32-bit sum of the same terms' larger parts, lacks, and is left out where R is not
+// finite (an infinity times the parts may be a NaN where it is an infinity times the
+// whole).
 struct Epilogue {
     void* Y;
     void* Z;
@@ -63,6 +66,7 @@ struct Epilogue {
     const float* sw;
     int64_t ldy, ldz, ldr;
     int act, out;
+    int rest = 0;
 };
 
 // Y = epilogue(A B^T): A has M rows, B has N rows, both K columns of `dtype`.
