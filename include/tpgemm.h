@@ -603,11 +603,10 @@ size_t tpgemm_gated_linear_workspace_bytes(const void* A, const void* W,
  * [2 N, K], Z [M, 2 N] (read for every activation) and dbias [2 N]. dA and a 16-bit
  * dW are products of dZ rounded to `dtype`; a 32-bit dW is one of dZ as two 16-bit
  * values, its rounding and the rest (they are within 2^-17 of dZ, and in f16, whose
- * steps end, within 2^-36 where that is more; past f16's range they are an infinity), two
- * products one after the other. With
- * 32-bit gradients dZ's act is as precise as of tpgemm_linear's 32-bit outputs, and its
- * act', whose terms cancel, within 2^-18, gelu's within 2^-21. The rest is as for
- * tpgemm_linear_backward.
+ * steps end, within 2^-36 where that is more; past f16's range they are an infinity),
+ * two products one after the other. With 32-bit gradients dZ's act is as precise as of
+ * tpgemm_linear's 32-bit outputs, and its act', whose terms cancel, within 2^-18, gelu's
+ * within 2^-21. The rest is as for tpgemm_linear_backward.
  */
 tpgemm_status tpgemm_gated_linear_backward(void* dA, void* dW, void* dbias, const void* dY,
                                            const void* A, const void* W, const void* Z,

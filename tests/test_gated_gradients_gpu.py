@@ -1,6 +1,6 @@
 """32-bit gradients of the gated linear layer against 64 bits, by bounds that leave no room for a dZ of
 16 bits or an activation made for 16-bit results (GPU only): every activation, more tokens than one
-sum takes, and infinities."""
+sum takes, infinities, and sums of 32-bit outputs that are longer than their pieces."""
 import pytest
 import torch
 
@@ -125,3 +125,16 @@ def test_infinities_of_the_input(M, N, K, whole, path, tune):
         clean[:, [5, 9]] = 0
         _, want, _ = tp.gated_linear_backward(dY, clean, W, pre, act="none", grad_dtype=F32)
         assert torch.equal(dW[:, rest], want[:, rest])
+
+
+@pytest.mark.parametrize("M,K,share", [(1100, 5000, 2560), (40, 32768, 4096), (40, 65536, 8192)])
+def test_long_sums_of_32_bit_outputs(M, K, share):
+    # Sums come in at most eight pieces. A term of a piece costs its sum up to 1.2e-9 of its size, and
+    # an output is a product of two sums.
+    g = torch.Generator(device="cuda").manual_seed(K)
+    A, W = gl.view(g, M, K, BF16), gl.view(g, 200, K, BF16, std=K ** -0.5)
+    y = tp.gated_linear(A, W, act="none", out_dtype=F32)
+    z = A.double() @ W.double().t()
+    want = z[:, :100] * z[:, 100:]
+    # (two sums, and a rounding of each and of the product)
+    assert float((y.double() - want).norm() / want.norm()) <= 2 * 1.2e-9 * share + 3 * E32

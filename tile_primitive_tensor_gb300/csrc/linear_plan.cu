@@ -250,7 +250,9 @@ Choice plan_split(const LinearOp& op, int64_t kb, const LinearTuning& t, int lea
 // A gated 32-bit output is a product of two sums, and off by both of theirs: sums
 // of more than kLongSum terms are shared out to CTAs, whose shorter ones are added
 // with rounding (2048 x 2048 outputs of random signs, K = 16384 in four shares:
-// 8.2e-6 of their size).
+// 8.2e-6 of their size). Eight shares are the most: they keep to kLongSum up to K =
+// 32768, and past it grow with K. The tile kernel, whatever its cost or the override of
+// the path, does not take these products: it adds all of K in one piece.
 int least_split(const LinearOp& op) {
     int split = 1;
     if (op.gated && op.e.out == TPGEMM_ELEM_F32)
