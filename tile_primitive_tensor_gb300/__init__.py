@@ -1253,8 +1253,12 @@ def layernorm_backward(dy, h, mean, rstd, weight, dh=None, *, dropout=None, grad
 
     dy, h, dh, dx and dresidual [rows, cols] are of one type (float16, bfloat16 or float32),
     dweight and dbias of grad_dtype (by default weight's). ``need`` says which of dx, dresidual,
-    dweight and dbias are wanted; ``out`` (of dx, or of both without a dropout) may be dy, h or dh.
-    stream: as for linear."""
+    dweight and dbias are wanted; ``out`` (of dx, or of both without a dropout) may be dy, h or dh, and
+    is refused where it would not be written. stream: as for linear."""
+    apart = dropout is not None
+    dx_wanted = need[0] or (need[1] and not apart)
+    if out is not None and not dx_wanted:
+        raise ValueError("out is dx's, which need leaves out")
     if stream is not None:
         with _current(stream, dy):
             return layernorm_backward(dy, h, mean, rstd, weight, dh, dropout=dropout,
@@ -1275,8 +1279,7 @@ def layernorm_backward(dy, h, mean, rstd, weight, dh=None, *, dropout=None, grad
     if dh is not None:
         lddh, pdh = _matrix("dh", dh, rows, cols, dt, index), dh.data_ptr()
     lddy = _matrix("dy", dy, rows, cols, dt, index)
-    apart = dropout is not None
-    if need[0] or (need[1] and not apart):
+    if dx_wanted:
         if out is None:
             dx, lddx = torch.empty_like(dy) if lddy == cols else torch.empty((rows, cols), dtype=dt, device=device), cols
         else:
