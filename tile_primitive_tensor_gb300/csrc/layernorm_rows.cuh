@@ -1048,15 +1048,19 @@ cudaError_t with_spread(const RowSpread& s, bool aligned, F&& f) {
             if (s.p == 4) return g(integral_constant<int, 4>());
         return s.p == 2 ? g(integral_constant<int, 2>()) : g(integral_constant<int, 1>());
     };
-    if (s.t == 0)
+    constexpr integral_constant<int, 0> any{};
+    constexpr integral_constant<int, MOST> most{};
+    if (s.t == 0 && !s.whole)
         return pieces([&](auto p) {
-            constexpr integral_constant<int, 0> any{};
-            return s.whole   ? f(p, any, integral_constant<int, kWhole>())
-                   : aligned ? f(p, any, integral_constant<int, kAligned>())
-                             : f(p, any, integral_constant<int, kAnywhere>());
+            return aligned ? f(p, any, integral_constant<int, kAligned>()) : f(p, any, integral_constant<int, kAnywhere>());
         });
     constexpr integral_constant<int, kWhole> whole{};
     constexpr integral_constant<int, 512> t512{};
+    if (s.t == 0) {  // (a team of 96 threads or more, with as many pieces as MOST at least)
+        if constexpr (TWICE)
+            if (s.p > MOST) return f(integral_constant<int, 2 * MOST>(), any, whole);
+        return f(most, any, whole);
+    }
     if (s.t == 32) {  // (as many pieces as MOST at the most)
         constexpr integral_constant<int, 32> t32{};
         if constexpr (MOST == 4)
@@ -1065,7 +1069,6 @@ cudaError_t with_spread(const RowSpread& s, bool aligned, F&& f) {
     }
     if constexpr (TWICE)
         if (s.p > MOST) return f(integral_constant<int, 2 * MOST>(), t512, whole);
-    constexpr integral_constant<int, MOST> most{};
     switch (s.t) {
         case 64: return f(most, integral_constant<int, 64>(), whole);
         case 128: return f(most, integral_constant<int, 128>(), whole);
