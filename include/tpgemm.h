@@ -492,9 +492,10 @@ tpgemm_status tpgemm_vcopy_roundtrip(void* dst, const void* src, size_t buffer_b
  * Matrices here are row-major with unit column stride and a row stride in
  * elements (0 = dense, else at least the columns), so slices of wider buffers
  * can be given. Pointers are aligned to their element; rows that start on
- * 16-byte boundaries run fastest. Sizes may be any, zero included. All calls are asynchronous on
- * `stream`, allocate nothing, keep no pointer, and may be captured into a
- * CUDA graph. An output may not share bytes with an input or another output,
+ * 16-byte boundaries, and output rows that end on them too, run fastest. Nothing
+ * outside of an output's rows is written. Sizes may be any, zero included. All calls
+ * are asynchronous on `stream`, allocate nothing, keep no pointer, and may be captured
+ * into a CUDA graph. An output may not share bytes with an input or another output,
  * except where in-place use is named below. Inputs' infinities and NaN
  * propagate as in the formulas.
  */

@@ -25,7 +25,7 @@ struct TcLinear {
     int group;             // tile kernel: P tiles in a raster run
     int k_rotate;          // tile kernel: tiles start at different places of K
     int half_sm;           // split kernel: half of an SM's shared memory, two blocks to an SM
-    int tma_out;           // tile kernel: Y, Z and R move by TMA (rows on 16-byte boundaries)
+    int tma_out;           // tile kernel: Y, Z and R move by TMA (rows of whole units on 16-byte boundaries)
     int swap;              // P holds the output's columns
     int pair;              // tile kernel (1) or split kernel (0)
     int fp8;
