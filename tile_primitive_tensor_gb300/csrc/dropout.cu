@@ -4,8 +4,10 @@
 // A thread takes eight neighbouring columns, 16 bytes of each matrix of 16-bit
 // elements, and walks the matrix grid-stride. Rows that do not start on 16-byte
 // boundaries, or widths that are no multiple of eight, move element by element.
-// 8192 x 8192 bf16 with residual 64 us (94 % of memory's rate), where the random words
-// take as long; 8192 x 4099 79 us (aligned 16 bytes joined and turned: 84). Two groups
+// 8192 x 8192 bf16 with residual 65 us (93 % of memory's rate), without 62 (65 %): there
+// the words' products keep their pipe busy for 70 % of the time and a third of the warps'
+// waiting is for loads, which a thread asks for after the words of the group before; the
+// two add up in part. 8192 x 4099 79 us (aligned 16 bytes joined and turned: 84). Two groups
 // of columns to a thread at a time gained nothing (79 us at 8192 x 8192), nor did four
 // of one row (78): warps, which have the registers then, are what hides memory here.
 #include <algorithm>

@@ -24,8 +24,12 @@
 // kept in shared memory as far as it goes, the rest read again for each pass.
 //
 // 8192 x 4096 bf16 with residual 48 us (83 % of memory's rate), with dropout 54
-// (74 %); gradients with dh 46 (87 %) and 65 (77 %), where instructions bound them:
-// 180 and 290 to eight columns, 300 and 320.
+// (74 %); gradients with dh 47 (85 %) and 65 (77 %). 172 and 287 instructions to eight
+// columns, gradients 192 and 318. With dropout it is not issue that bounds them (55 % of
+// the slots are used) but the random words' products, whose pipe is busy for 60 % of the
+// time, and the waits for it, for shared memory and at barriers between, which 27 warps
+// to an SM (gradients 15) do not hide. Rows that start anywhere take some 610 to eight
+// columns: 4096 x 4099 55 us, gradients 82.
 #pragma once
 
 #include <algorithm>
