@@ -1,6 +1,8 @@
 """32-bit gradients of the gated linear layer against 64 bits, by bounds that leave no room for a dZ of
 16 bits or an activation made for 16-bit results (GPU only): every activation, more tokens than one
 sum takes, infinities, and sums of 32-bit outputs that are longer than their pieces."""
+import math
+
 import pytest
 import torch
 
@@ -33,6 +35,8 @@ def dz_of(dY, pre, act):
     dy = dY.double()
     g, u = pre.double().chunk(2, 1)
     f, df = ref.act(g, act), ref.act_grad(g, act)
+    if act == "gelu_tanh":  # (1 + tanh v as it stands loses its digits where it is small, in 64 bits too)
+        f = g * torch.sigmoid(2 * math.sqrt(2 / math.pi) * (g + 0.044715 * g ** 3))
     zero = torch.zeros_like(g)
     if act == "gelu":
         ef = torch.minimum(torch.full_like(g, 6e-8), torch.where(g >= -3, 5e-6, 4e-4) * f.abs())
