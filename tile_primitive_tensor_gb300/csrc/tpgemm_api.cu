@@ -71,6 +71,24 @@ tpgemm_status device_info(DeviceInfo* out) {
     return TPGEMM_OK;
 }
 
+// The driver's encoder wants a current context, which a host thread that has made no
+// runtime call yet does not have: the device's own is made current then.
+CUresult CUDAAPI encode_in_context(CUtensorMap* map, CUtensorMapDataType type, cuuint32_t rank, void* base,
+                                   const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box,
+                                   const cuuint32_t* step, CUtensorMapInterleave interleave,
+                                   CUtensorMapSwizzle swizzle, CUtensorMapL2promotion promotion,
+                                   CUtensorMapFloatOOBfill fill) {
+    const auto encode = [&] {
+        return g_encode(map, type, rank, base, dims, strides, box, step, interleave, swizzle, promotion, fill);
+    };
+    const CUresult r = encode();
+    int dev = 0;
+    if (r != CUDA_ERROR_INVALID_CONTEXT || cudaGetDevice(&dev) != cudaSuccess ||
+        cudaSetDevice(dev) != cudaSuccess)
+        return r;
+    return encode();
+}
+
 tpgemm_status get_encoder(PFN_cuTensorMapEncodeTiled_v12000* fn) {
     std::lock_guard<std::mutex> lock(g_mutex);
     if (!g_encode) {
@@ -82,7 +100,7 @@ tpgemm_status get_encoder(PFN_cuTensorMapEncodeTiled_v12000* fn) {
             return fail(TPGEMM_ERR_LAUNCH, "cuTensorMapEncodeTiled not available from the driver");
         g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
     }
-    *fn = g_encode;
+    *fn = encode_in_context;
     return TPGEMM_OK;
 }
 
